@@ -6,6 +6,7 @@ C ABI; every step of the path runs in the library's HIP kernels.  There is no
 fallback: if the library is missing or fails to load, importing the ops raises.
 
   pregate(x, Wr)                  -> (idx [T][2] int32, g [T][2] fp32)
+  route(logits, k, ...)           -> (idx [T][k] int32, g [T][k] fp32); route_backward
   Layers([(W, A, B), ...], E, r, scale).switch(old, new)   # in place, one launch
   sgmm(x, idx, g, A, B, y, scale)                          # y updated in place
   SgmmGroup([(x, A, B, y), ...], E, r, scale).run(idx, g)
@@ -25,6 +26,7 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "dlm.h")
 DLM_OK, DLM_EINVAL, DLM_ESHAPE, DLM_EDTYPE, DLM_EALIGN = 0, -1, -2, -3, -4
 DLM_EWORKSPACE, DLM_EHIP, DLM_EDEVICE, DLM_ENOMEM = -5, -6, -7, -8
 DLM_F32, DLM_BF16 = 0, 1
+DLM_SOFTMAX, DLM_SIGMOID = 0, 1
 STATUS_NAMES = {0: "DLM_OK", -1: "DLM_EINVAL", -2: "DLM_ESHAPE", -3: "DLM_EDTYPE",
                 -4: "DLM_EALIGN", -5: "DLM_EWORKSPACE", -6: "DLM_EHIP", -7: "DLM_EDEVICE",
                 -8: "DLM_ENOMEM"}
@@ -46,6 +48,11 @@ class dlm_sgmm_problem(C.Structure):
                 ("d_in", C.c_int64), ("d_out", C.c_int64)]
 
 
+class dlm_route_cfg(C.Structure):
+    _fields_ = [("k", C.c_int32), ("score", C.c_int32), ("n_groups", C.c_int32), ("keep_groups", C.c_int32),
+                ("group_top", C.c_int32), ("renorm", C.c_int32), ("scale", C.c_float)]
+
+
 _lib = None
 
 
@@ -63,6 +70,8 @@ def load(path: str = LIB_PATH):
         "dlm_version": ([], C.c_char_p),
         "dlm_pregate": ([P, P, I64, I64, I32, I32, P, P, P], C.c_int),
         "dlm_pregate_centroid": ([P, P, I64, I64, I32, I32, I32, P, P, P], C.c_int),
+        "dlm_route": ([P, I64, P, I64, I32, I32, P, P, P, P, P], C.c_int),
+        "dlm_route_backward": ([P, I64, P, P, I64, I32, I32, P, P, I64, P], C.c_int),
         "dlm_layers_create": ([P, I32, I32, I32, F, I32, P], C.c_int),
         "dlm_layers_destroy": ([P], C.c_int),
         "dlm_switch": ([P, P, P, P, P, P], C.c_int),
@@ -180,6 +189,95 @@ def pregate_centroid(x: torch.Tensor, C: torch.Tensor, idx=None, g=None, stream=
     _check(load().dlm_pregate_centroid(_p(x), _p(C), T, d, E, J, _dt(x), _p(idx), _p(g), _stream(stream)),
            "dlm_pregate_centroid")
     return idx, g
+
+
+_SCORES = {"softmax": DLM_SOFTMAX, "sigmoid": DLM_SIGMOID}
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(T, E, row pitch) of a device matrix whose rows are contiguous, its pitch any."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    T, E = t.shape
+    ld = t.stride(0) if T > 1 else max(E, 1)
+    if ld < E:
+        raise ValueError(f"{name} has overlapping rows (pitch {ld} of {E})")
+    return T, E, ld
+
+
+def _here(t: torch.Tensor, stream, name: str):
+    """The library launches on the current device: tensors and stream belong to it."""
+    dev = torch.cuda.current_device()
+    if t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, but the current device is cuda:{dev}")
+
+
+def _fresh(stream, *tensors):
+    """Tensors made here on the current stream and used on `stream`: the
+    allocator keeps them until that work has ended."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _route_cfg(k, score, n_groups, keep_groups, group_top, renorm, scale):
+    if score not in _SCORES:
+        raise ValueError(f"score is one of {sorted(_SCORES)}, got {score!r}")
+    return dlm_route_cfg(k, _SCORES[score], n_groups, keep_groups, group_top, 1 if renorm else 0, scale)
+
+
+def route(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, n_groups: int = 1, keep_groups: int = 1,
+          group_top: int = 1, renorm: bool = True, scale: float = 1.0, counts=None, idx=None, g=None, stream=None):
+    """Routing from logits [T][E] (any row pitch): softmax or sigmoid scores, a
+    selection bias [E] fp32, the best keep_groups of n_groups groups (by their
+    best key or the sum of their best two), the top k, weights renormalised over
+    the chosen or not -> idx [T][k] int32, g [T][k] fp32 (device).  -inf marks an
+    expert the row may not use; counts [E] int32 is added to."""
+    T, E, ld = _rows(logits, "logits")
+    _here(logits, stream, "logits")
+    if bias is not None:
+        _like(bias, "bias", (E,), torch.float32, logits.device)
+    if counts is not None:
+        _like(counts, "counts", (E,), torch.int32, logits.device)
+    if idx is None:
+        idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    if g is None:
+        g = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _like(idx, "route idx", (T, k), torch.int32, logits.device)
+    _like(g, "route g", (T, k), torch.float32, logits.device)
+    cfg = _route_cfg(k, score, n_groups, keep_groups, group_top, renorm, scale)
+    _check(load().dlm_route(_p(logits), ld, _p(bias), T, E, _dt(logits), C.byref(cfg), _p(idx), _p(g), _p(counts),
+                            _stream(stream)), "dlm_route")
+    _fresh(stream, idx, g)
+    return idx, g
+
+
+def route_backward(logits: torch.Tensor, idx: torch.Tensor, dg: torch.Tensor, score: str = "softmax",
+                   renorm: bool = True, scale: float = 1.0, dlogits=None, stream=None):
+    """dLoss/dlogits [T][E] (logits' dtype; returned) from dg [T][k] = dLoss/dg of
+    route()'s weights for its choice idx [T][k]."""
+    T, E, ld = _rows(logits, "logits")
+    _here(logits, stream, "logits")
+    if idx.dim() != 2:
+        raise ValueError("idx must be [T][k]")
+    k = idx.shape[1]
+    _like(idx, "idx", (T, k), torch.int32, logits.device)
+    _like(dg, "dg", (T, k), torch.float32, logits.device)
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    Td, Ed, ldd = _rows(dlogits, "dlogits")
+    if (Td, Ed) != (T, E) or dlogits.dtype != logits.dtype or dlogits.device != logits.device:
+        raise ValueError("dlogits must have logits' shape, dtype and device")
+    cfg = _route_cfg(k, score, 1, 1, 1, renorm, scale)
+    _check(load().dlm_route_backward(_p(logits), ld, _p(idx), _p(dg), T, E, _dt(logits), C.byref(cfg), _p(dlogits), ldd,
+                                     _stream(stream)), "dlm_route_backward")
+    _fresh(stream, dlogits)
+    return dlogits
 
 
 # ---- fused switch ---------------------------------------------------------------

@@ -11,7 +11,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdlm.so")
-SOURCES = ["api.hip", "pregate.hip", "switch.hip", "sgmm.hip"]
+SOURCES = ["api.hip", "pregate.hip", "route.hip", "switch.hip", "sgmm.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -15,6 +15,7 @@
 
 #include "dlm.h"
 #include "internal.hpp"
+#include "route.hpp"
 #include "sgmm.hpp"
 
 using namespace dlm;
@@ -205,6 +206,102 @@ int dlm_pregate_centroid(const void* x, const void* C, int64_t T, int64_t d, int
     if (!x || !C || !idx || !g) return fail(DLM_EINVAL, "pregate_centroid: null pointer");
     hipError_t e = launch_pregate_centroid(x, C, T, d, E, J, dtype, idx, g, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "pregate_centroid launch");
+    return ok();
+}
+
+// Checks and arguments shared by dlm_route and dlm_route_backward.
+static int route_args(const char* call, const void* logits, int64_t ld, int64_t T, int32_t E, int32_t dtype,
+                      const dlm_route_cfg* c, RouteArgs* a) {
+    static_assert(kRouteMaxExperts == DLM_MAX_ROUTE_EXPERTS && kRouteMaxK == DLM_MAX_ROUTE_K, "route limits");
+    static_assert(kRouteSoftmax == DLM_SOFTMAX && kRouteSigmoid == DLM_SIGMOID, "score codes");
+    if (!c) return fail(DLM_EINVAL, "%s: cfg is null", call);
+    if (T < 0 || T >= ((int64_t)1 << 31)) return fail(DLM_ESHAPE, "%s: T=%lld out of range", call, (long long)T);
+    if (E < 1 || E > DLM_MAX_ROUTE_EXPERTS)
+        return fail(DLM_ESHAPE, "%s: E=%d not in [1, %d]", call, E, DLM_MAX_ROUTE_EXPERTS);
+    if (!valid_dtype(dtype)) return fail(DLM_EDTYPE, "%s: unknown dtype %d", call, dtype);
+    if (ld < E || ld > kMaxDim) return fail(DLM_ESHAPE, "%s: row pitch %lld of rows of %d", call, (long long)ld, E);
+    if (c->score != DLM_SOFTMAX && c->score != DLM_SIGMOID) return fail(DLM_EINVAL, "%s: unknown score %d", call, c->score);
+    if (!std::isfinite(c->scale)) return fail(DLM_EINVAL, "%s: scale is not finite", call);
+    if (c->n_groups < 1 || c->n_groups > DLM_MAX_ROUTE_GROUPS || E % c->n_groups != 0)
+        return fail(DLM_ESHAPE, "%s: %d groups of %d experts (at most %d groups, of equal size)", call, c->n_groups, E,
+                    DLM_MAX_ROUTE_GROUPS);
+    if (c->keep_groups < 1 || c->keep_groups > c->n_groups)
+        return fail(DLM_ESHAPE, "%s: keep_groups=%d not in [1, %d]", call, c->keep_groups, c->n_groups);
+    if (c->group_top != 1 && c->group_top != 2) return fail(DLM_EINVAL, "%s: group_top=%d is not 1 or 2", call, c->group_top);
+    const int gs = E / c->n_groups;
+    if (c->k < 1 || c->k > DLM_MAX_ROUTE_K || c->k > c->keep_groups * gs)
+        return fail(DLM_ESHAPE, "%s: k=%d of %d experts in the kept groups (at most %d)", call, c->k, c->keep_groups * gs,
+                    DLM_MAX_ROUTE_K);
+    *a = RouteArgs{};
+    a->logits = logits;
+    a->ld = ld;
+    a->T = T;
+    a->E = E;
+    a->k = c->k;
+    a->score = c->score;
+    a->renorm = c->renorm ? 1 : 0;
+    a->scale = c->scale;
+    a->n_groups = c->n_groups;
+    a->group_size = gs;
+    a->keep_groups = c->keep_groups;
+    a->group_top = c->group_top;
+    a->gs_magic = (uint32_t)((1u << 20) / gs + 1);
+    const int64_t w = 16 / (int64_t)esize(dtype);
+    a->vec = aligned16(logits) && ld % w == 0 && E % w == 0;
+    return DLM_OK;
+}
+
+// Bytes from the first to behind the last element of T rows of n, ld apart.
+static size_t rows_bytes(int64_t T, int64_t ld, int64_t n, size_t es) { return ((size_t)(T - 1) * ld + n) * es; }
+
+int dlm_route(const void* logits, int64_t ld, const float* bias, int64_t T, int32_t E, int32_t dtype,
+              const dlm_route_cfg* cfg, int32_t* idx, float* g, int32_t* counts, void* stream) {
+    RouteArgs a;
+    const int rc = route_args("route", logits, ld, T, E, dtype, cfg, &a);
+    if (rc != DLM_OK) return rc;
+    if (T == 0) return ok();
+    if (!logits || !idx || !g) return fail(DLM_EINVAL, "route: null pointer");
+    std::vector<Span> v = {span(logits, rows_bytes(T, ld, E, esize(dtype)), false, "logits", 0),
+                           span(idx, (size_t)T * a.k * 4, true, "idx", 0), span(g, (size_t)T * a.k * 4, true, "g", 0)};
+    if (bias) v.push_back(span(bias, (size_t)E * 4, false, "bias", 0));
+    if (counts) v.push_back(span(counts, (size_t)E * 4, true, "counts", 0));
+    Span p, q;
+    if (write_conflict(std::move(v), &p, &q)) return conflict_fail("route", p, q);
+    a.bias = bias;
+    a.scores_order = bias || (a.n_groups > 1 && a.group_top == 2) ? 1 : 0;
+    a.need_scores = a.scores_order || (a.score == kRouteSoftmax && !a.renorm) ? 1 : 0;
+    a.idx = idx;
+    a.g = g;
+    a.counts = counts;
+    const hipError_t e = launch_route(a, dtype, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "route launch");
+    return ok();
+}
+
+int dlm_route_backward(const void* logits, int64_t ld, const int32_t* idx, const float* dg, int64_t T, int32_t E,
+                       int32_t dtype, const dlm_route_cfg* cfg, void* dlogits, int64_t ldd, void* stream) {
+    RouteArgs a;
+    const int rc = route_args("route_backward", logits, ld, T, E, dtype, cfg, &a);
+    if (rc != DLM_OK) return rc;
+    if (ldd < E || ldd > kMaxDim)
+        return fail(DLM_ESHAPE, "route_backward: row pitch %lld of dlogits rows of %d", (long long)ldd, E);
+    if (T == 0) return ok();
+    if (!logits || !idx || !dg || !dlogits) return fail(DLM_EINVAL, "route_backward: null pointer");
+    const size_t es = esize(dtype);
+    Span p, q;
+    if (write_conflict({span(logits, rows_bytes(T, ld, E, es), false, "logits", 0),
+                        span(dlogits, rows_bytes(T, ldd, E, es), true, "dlogits", 0),
+                        span(idx, (size_t)T * a.k * 4, false, "idx", 0), span(dg, (size_t)T * a.k * 4, false, "dg", 0)},
+                       &p, &q))
+        return conflict_fail("route_backward", p, q);
+    a.in_idx = idx;
+    a.dg = dg;
+    a.dlogits = dlogits;
+    a.ldd = ldd;
+    const int64_t w = 16 / (int64_t)es;
+    a.vec_out = aligned16(dlogits) && ldd % w == 0 && E % w == 0;
+    const hipError_t e = launch_route_grad(a, dtype, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "route_backward launch");
     return ok();
 }
 

@@ -115,6 +115,61 @@ int dlm_pregate(const void* x, const void* Wr, int64_t T, int64_t d, int32_t E,
 int dlm_pregate_centroid(const void* x, const void* C, int64_t T, int64_t d, int32_t E,
                          int32_t J, int32_t dtype, int32_t* idx, float* g, void* stream);
 
+/*
+ * Routing from router logits for any number of experts (the top-2 pre-gate's
+ * general form, for routers whose product is computed elsewhere and for
+ * training; k = 2 with E <= DLM_MAX_EXPERTS gives sets that dlm_switch and
+ * dlm_sgmm take as they are):
+ *   s      softmax(l) over the available experts of the row, or sigmoid(l)
+ *   key    s + bias (bias [E] fp32 or NULL: it steers the choice, for balance,
+ *          and is not part of the weights)
+ *   groups n_groups runs of E / n_groups experts, each ranked by its best key
+ *          (group_top 1) or the sum of its best two (group_top 2); the best
+ *          keep_groups of them stay (n_groups = 1: all experts)
+ *   idx    [T][k] the k largest keys of the kept groups, descending
+ *   g      [T][k] scale * s_i, or with renorm scale * s_i / sum_j s_j over the
+ *          chosen (0 where that sum is 0)
+ * Equal keys go to the lower index.  Without a bias (and with group_top 1) the
+ * logits themselves are compared, exactly; otherwise keys are binary64 values
+ * and two within 2^-43 of their size may count as equal.  Scores and sums are
+ * binary64; g is rounded to fp32 once.
+ * A logit of -inf or NaN marks an expert that is not available to the row: its
+ * score is 0 and it is never chosen; +inf counts as the largest fp32 value.  A
+ * row with fewer than k available experts in its kept groups ends in empty
+ * slots (idx -1, g 0); a padding row of -inf has only those.
+ *   logits [T] rows of E (dtype), ld elements apart (ld >= E)
+ *   counts [E] int32 or NULL: the number of rows that chose each expert is
+ *          ADDED to it (the load a balance bias is steered by)
+ * One launch on `stream`, no allocation.  T = 0 enqueues nothing.
+ */
+#define DLM_MAX_ROUTE_EXPERTS 512
+#define DLM_MAX_ROUTE_K 16
+#define DLM_MAX_ROUTE_GROUPS 32
+typedef enum { DLM_SOFTMAX = 0, DLM_SIGMOID = 1 } dlm_score;
+typedef struct {
+    int32_t k;            /* 1 .. min(DLM_MAX_ROUTE_K, keep_groups * E / n_groups) */
+    int32_t score;        /* dlm_score */
+    int32_t n_groups;     /* 1 .. DLM_MAX_ROUTE_GROUPS, dividing E */
+    int32_t keep_groups;  /* 1 .. n_groups */
+    int32_t group_top;    /* 1 or 2 */
+    int32_t renorm;       /* 0 or 1 */
+    float scale;
+} dlm_route_cfg;
+int dlm_route(const void* logits, int64_t ld, const float* bias, int64_t T, int32_t E, int32_t dtype,
+              const dlm_route_cfg* cfg, int32_t* idx, float* g, int32_t* counts, void* stream);
+
+/*
+ * The gradient of dlm_route's weights: given dg [T][k] = dLoss/dg for the
+ * choice idx [T][k], dlogits [T] rows of E (dtype, ldd elements apart) =
+ * dLoss/dlogits, every element of the rows written.  The choice itself has no
+ * gradient.  Entries of idx outside [0, E) are empty slots, and so are those
+ * that name an expert that is not available; an expert named twice
+ * counts twice.  binary64 inside, rounded once.  cfg as for dlm_route (its
+ * groups only bound k).  One launch on `stream`, no allocation.
+ */
+int dlm_route_backward(const void* logits, int64_t ld, const int32_t* idx, const float* dg, int64_t T, int32_t E,
+                       int32_t dtype, const dlm_route_cfg* cfg, void* dlogits, int64_t ldd, void* stream);
+
 /* ------------------------------------------------------------ fused switch */
 
 /* One adapted weight and its expert bank. */

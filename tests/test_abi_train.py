@@ -1,0 +1,94 @@
+"""Refusals of the training operators' entry points, on the host before any HIP
+call (no GPU: every call below fails validation or has nothing to do), and the
+plain forms of the tests against each other."""
+import ctypes as C
+import os
+
+import numpy as np
+import pytest
+
+import dynamic_lora_moe_amd as dlm
+import route_ref
+
+P = C.c_void_p
+FAKE = 0x100000
+MB = 1 << 20
+
+built = pytest.mark.skipif(not os.path.exists(dlm.LIB_PATH), reason="libdlm.so not built")
+
+
+def _cfg(**kw):
+    c = dict(k=2, score=dlm.DLM_SOFTMAX, n_groups=1, keep_groups=1, group_top=1, renorm=1, scale=1.0)
+    c.update(kw)
+    return C.byref(dlm.dlm_route_cfg(*[c[f] for f, _ in dlm.dlm_route_cfg._fields_]))
+
+
+@built
+def test_route_validation():
+    lib = dlm.load()
+    out = P(FAKE + 64 * MB), P(FAKE + 65 * MB)
+
+    def route(logits=P(FAKE), ld=8, bias=None, T=4, E=8, dt=0, cfg=None, idx=out[0], g=out[1], counts=None):
+        return lib.dlm_route(logits, ld, bias, T, E, dt, cfg or _cfg(), idx, g, counts, None)
+
+    def back(logits=P(FAKE), ld=8, idx=out[0], dg=out[1], T=4, E=8, dt=0, cfg=None, dl=P(FAKE + 66 * MB), ldd=8):
+        return lib.dlm_route_backward(logits, ld, idx, dg, T, E, dt, cfg or _cfg(), dl, ldd, None)
+
+    for f in (route, back):
+        assert f(T=-1) == dlm.DLM_ESHAPE and f(T=1 << 31) == dlm.DLM_ESHAPE
+        assert f(E=0) == dlm.DLM_ESHAPE and f(E=513, ld=513) == dlm.DLM_ESHAPE
+        assert f(ld=7) == dlm.DLM_ESHAPE
+        assert f(dt=2) == dlm.DLM_EDTYPE
+        assert f(logits=None) == dlm.DLM_EINVAL and f(idx=None) == dlm.DLM_EINVAL
+        assert f(cfg=_cfg(score=2)) == dlm.DLM_EINVAL
+        assert f(cfg=_cfg(scale=float("inf"))) == dlm.DLM_EINVAL
+        assert f(cfg=_cfg(k=0)) == dlm.DLM_ESHAPE and f(cfg=_cfg(k=9)) == dlm.DLM_ESHAPE
+        assert f(E=64, ld=64, cfg=_cfg(k=17)) == dlm.DLM_ESHAPE
+        assert f(cfg=_cfg(n_groups=3)) == dlm.DLM_ESHAPE and f(cfg=_cfg(n_groups=0)) == dlm.DLM_ESHAPE
+        assert f(E=66, ld=66, cfg=_cfg(n_groups=33)) == dlm.DLM_ESHAPE
+        assert f(cfg=_cfg(n_groups=4, keep_groups=5)) == dlm.DLM_ESHAPE
+        assert f(cfg=_cfg(n_groups=4, keep_groups=0)) == dlm.DLM_ESHAPE
+        assert f(cfg=_cfg(k=3, n_groups=4, keep_groups=1)) == dlm.DLM_ESHAPE
+        assert f(cfg=_cfg(group_top=0)) == dlm.DLM_EINVAL and f(cfg=_cfg(group_top=3)) == dlm.DLM_EINVAL
+        assert f(T=0, logits=None, idx=None) == dlm.DLM_OK
+    assert route(g=None) == dlm.DLM_EINVAL
+    assert back(dg=None) == dlm.DLM_EINVAL and back(dl=None) == dlm.DLM_EINVAL and back(ldd=7) == dlm.DLM_ESHAPE
+    # written buffers overlap nothing
+    assert route(idx=P(FAKE)) == dlm.DLM_EINVAL and route(g=out[0]) == dlm.DLM_EINVAL
+    assert route(counts=out[0]) == dlm.DLM_EINVAL and route(bias=out[1]) == dlm.DLM_EINVAL
+    assert back(dl=P(FAKE)) == dlm.DLM_EINVAL and back(dl=out[1]) == dlm.DLM_EINVAL
+    assert lib.dlm_route(P(FAKE), 8, None, 4, 8, 0, None, out[0], out[1], None, None) == dlm.DLM_EINVAL
+
+
+def test_route_gradient_is_the_weights_derivative():
+    """The plain gradient against central differences of the plain weights, in binary64."""
+    rng = np.random.default_rng(1)
+    l = rng.standard_normal((4, 9))
+    l[1, 2] = -np.inf
+    dg = rng.standard_normal((4, 3))
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            idx, g = route_ref.route(l, 3, score=score, renorm=renorm, scale=1.5, n_groups=3, keep_groups=2, group_top=2)
+            assert np.allclose(g, route_ref.weights(l, idx, score, renorm, 1.5), rtol=1e-13)
+            got = route_ref.route_backward(l, idx, dg, score, renorm, 1.5)
+            h = 1e-6
+            for e in range(9):
+                up, dn = l.copy(), l.copy()
+                up[:, e] += h
+                dn[:, e] -= h
+                want = ((route_ref.weights(up, idx, score, renorm, 1.5)
+                         - route_ref.weights(dn, idx, score, renorm, 1.5)) * dg).sum(1) / (2 * h)
+                # differences: h^2 of truncation, 2^-52 / h of rounding
+                assert np.abs(got[:, e] - want).max() < 1e-8
+
+
+def test_route_plain_form_by_hand():
+    l = np.log(np.array([[1.0, 2.0, 4.0, 1.0]]))
+    idx, g = route_ref.route(l, 2)
+    assert idx.tolist() == [[2, 1]] and np.allclose(g, [[4 / 6, 2 / 6]])
+    idx, g = route_ref.route(l, 2, renorm=False)
+    assert np.allclose(g, [[0.5, 0.25]])
+    idx, g = route_ref.route(l, 2, bias=np.array([1.0, 0, 0, 1.0]))
+    assert idx.tolist() == [[0, 3]] and np.allclose(g, [[0.5, 0.5]])
+    idx, g = route_ref.route(l, 1, n_groups=2, keep_groups=1, group_top=2)
+    assert idx.tolist() == [[2]]
