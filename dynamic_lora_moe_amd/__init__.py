@@ -9,6 +9,7 @@ fallback: if the library is missing or fails to load, importing the ops raises.
   route(logits, k, ...)           -> (idx [T][k] int32, g [T][k] fp32); route_backward
   Layers([(W, A, B), ...], E, r, scale).switch(old, new)   # in place, one launch
   sgmm(x, idx, g, A, B, y, scale)                          # y updated in place
+  AdamW(params, grads, ...).step(lr)                       # many tensors at once
   SgmmGroup([(x, A, B, y), ...], E, r, scale).run(idx, g)
 """
 from __future__ import annotations
@@ -53,6 +54,15 @@ class dlm_route_cfg(C.Structure):
                 ("group_top", C.c_int32), ("renorm", C.c_int32), ("scale", C.c_float)]
 
 
+class dlm_adamw_param(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("master", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("m_scale", C.c_void_p), ("v_scale", C.c_void_p), ("n", C.c_int64), ("weight_decay", C.c_float)]
+
+
+class dlm_adamw_cfg(C.Structure):
+    _fields_ = [("lr", C.c_float), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_float)]
+
+
 _lib = None
 
 
@@ -72,6 +82,11 @@ def load(path: str = LIB_PATH):
         "dlm_pregate_centroid": ([P, P, I64, I64, I32, I32, I32, P, P, P], C.c_int),
         "dlm_route": ([P, I64, P, I64, I32, I32, P, P, P, P, P], C.c_int),
         "dlm_route_backward": ([P, I64, P, P, I64, I32, I32, P, P, I64, P], C.c_int),
+        "dlm_adamw_create": ([P, I32, I32, I32, I32, I64, C.c_uint32, P], C.c_int),
+        "dlm_adamw_destroy": ([P], C.c_int),
+        "dlm_adamw_step": ([P, P, P, P, P], C.c_int),
+        "dlm_adamw_status": ([P, P, P, P], C.c_int),
+        "dlm_adamw_read_state": ([P, P, P, P, I64, P, P, P], C.c_int),
         "dlm_layers_create": ([P, I32, I32, I32, F, I32, P], C.c_int),
         "dlm_layers_destroy": ([P], C.c_int),
         "dlm_switch": ([P, P, P, P, P, P], C.c_int),
@@ -544,3 +559,126 @@ class SgmmGroup:
             self.close()
         except Exception:  # noqa: BLE001
             pass
+
+
+# ---- AdamW -------------------------------------------------------------------------
+
+ADAMW_BLOCK = 256  # elements that share a scale of the 8-bit moments
+
+
+class AdamW:
+    """AdamW over many tensors at once (params updated in place).
+
+    params / grads: device tensors of one dtype each (fp32 or bf16), any shapes.
+    masters: per parameter an fp32 copy that the step updates (a bf16 parameter
+    then becomes its rounding), or None.  state_bits 32: moments fp32; 8: codes
+    with a scale per 256 elements.  states: per parameter (m, v), or with 8 bits
+    (m int8, v uint8, m_scale, v_scale), flat; zeros are made when None.
+    weight_decay: one value, or one per parameter.  step: steps already taken."""
+
+    def __init__(self, params, grads, masters=None, state_bits: int = 32, states=None, beta1: float = 0.9,
+                 beta2: float = 0.999, eps: float = 1e-8, weight_decay=0.01, step: int = 0, seed: int = 0):
+        self.params, self.grads = list(params), list(grads)
+        n = len(self.params)
+        if not n or len(self.grads) != n:
+            raise ValueError("one gradient per parameter, at least one parameter")
+        self.masters = [None] * n if masters is None else list(masters)
+        wd = [float(w) for w in weight_decay] if isinstance(weight_decay, (list, tuple)) else [float(weight_decay)] * n
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits is 32 or 8")
+        if states is None:
+            states = [self._zeros(p, state_bits) for p in self.params]
+        self.states = [tuple(st) for st in states]
+        if not len(self.masters) == len(wd) == len(self.states) == n:
+            raise ValueError("one master (or None), weight decay and state per parameter")
+        p0, g0 = self.params[0], self.grads[0]
+        arr = (dlm_adamw_param * n)()
+        for k, (p, g, w, st) in enumerate(zip(self.params, self.grads, self.masters, self.states)):
+            _like(p, f"parameter {k}", p.shape, p0.dtype, p0.device)
+            _like(g, f"gradient {k}", p.shape, g0.dtype, p0.device)
+            if w is not None:
+                _like(w, f"master {k}", p.shape, torch.float32, p0.device)
+            ne = p.numel()
+            nb = -(-ne // ADAMW_BLOCK)
+            want = [torch.float32, torch.float32] if state_bits == 32 else \
+                [torch.int8, torch.uint8, torch.float32, torch.float32]
+            if len(st) != len(want):
+                raise ValueError(f"state {k} has {len(st)} tensors, expected {len(want)}")
+            for t, dt, m, name in zip(st, want, (ne, ne, nb, nb), ("m", "v", "m_scale", "v_scale")):
+                if t.numel() != m:
+                    raise ValueError(f"state {k} {name} has {t.numel()} elements, expected {m}")
+                _like(t, f"state {k} {name}", t.shape, dt, p0.device)
+            ptr = [t.data_ptr() for t in st] + [None, None]
+            arr[k] = dlm_adamw_param(p.data_ptr(), g.data_ptr(), None if w is None else w.data_ptr(), ptr[0], ptr[1],
+                                     ptr[2], ptr[3], ne, wd[k])
+        _here(p0, None, "parameter 0")
+        h = C.c_void_p()
+        _check(load().dlm_adamw_create(arr, n, _dt(p0), _dt(g0), state_bits, int(step), seed & 0xFFFFFFFF, C.byref(h)),
+               "dlm_adamw_create")
+        self._h = h
+        self.state_bits, self.device = state_bits, p0.device
+        self.beta1, self.beta2, self.eps = float(beta1), float(beta2), float(eps)
+
+    @staticmethod
+    def _zeros(p, bits):
+        z = lambda n, dt: torch.zeros(n, dtype=dt, device=p.device)  # noqa: E731
+        n = p.numel()
+        if bits == 32:
+            return z(n, torch.float32), z(n, torch.float32)
+        nb = -(-n // ADAMW_BLOCK)
+        return z(n, torch.int8), z(n, torch.uint8), z(nb, torch.float32), z(nb, torch.float32)
+
+    def step(self, lr: float, lr_scale=None, grad_scale=None, stream=None):
+        """One step.  lr_scale / grad_scale: optional fp32 [1] device tensors that
+        multiply lr / the gradients, read when the step runs."""
+        _here(self.params[0], stream, "parameter 0")
+        for t, name in ((lr_scale, "lr_scale"), (grad_scale, "grad_scale")):
+            if t is not None:
+                _like(t, name, (1,), torch.float32, self.device)
+        cfg = dlm_adamw_cfg(float(lr), self.beta1, self.beta2, self.eps)
+        _check(load().dlm_adamw_step(self._h, C.byref(cfg), _p(lr_scale), _p(grad_scale), _stream(stream)),
+               "dlm_adamw_step")
+
+    def status(self, stream=None):
+        """(steps taken, DLM_OK or DLM_EDEVICE: some gradient was not finite); clears the error."""
+        step, code = C.c_int64(0), C.c_int32(0)
+        _check(load().dlm_adamw_status(self._h, C.byref(step), C.byref(code), _stream(stream)), "dlm_adamw_status")
+        return step.value, code.value
+
+    def read_state(self, k: int, stream=None):
+        """(m, v) of parameter k as fp32 tensors of its shape."""
+        st, shape = self.states[k], self.params[k].shape
+        if self.state_bits == 32:
+            return st[0].view(shape), st[1].view(shape)
+        m, v = adamw_read_state(*st, stream=stream)
+        return m.view(shape), v.view(shape)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            _check(load().dlm_adamw_destroy(self._h), "dlm_adamw_destroy")
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001
+            pass
+
+
+def adamw_read_state(m, v, m_scale, v_scale, m_out=None, v_out=None, stream=None):
+    """The fp32 values (m, v) that 8-bit moments stand for: flat codes and one scale per 256 elements."""
+    n = m.numel()
+    nb = -(-n // ADAMW_BLOCK)
+    _like(m, "m", (n,), torch.int8, m.device)
+    _like(v, "v", (n,), torch.uint8, m.device)
+    _like(m_scale, "m_scale", (nb,), torch.float32, m.device)
+    _like(v_scale, "v_scale", (nb,), torch.float32, m.device)
+    _here(m, stream, "m")
+    m_out = torch.empty(n, device=m.device) if m_out is None else m_out
+    v_out = torch.empty(n, device=m.device) if v_out is None else v_out
+    _like(m_out, "m_out", (n,), torch.float32, m.device)
+    _like(v_out, "v_out", (n,), torch.float32, m.device)
+    _check(load().dlm_adamw_read_state(_p(m), _p(v), _p(m_scale), _p(v_scale), n, _p(m_out), _p(v_out), _stream(stream)),
+           "dlm_adamw_read_state")
+    _fresh(stream, m_out, v_out)
+    return m_out, v_out

@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "dlm.h"
+#include "adamw.hpp"
 #include "internal.hpp"
 #include "route.hpp"
 #include "sgmm.hpp"
@@ -162,6 +163,15 @@ struct dlm_sgmm_group {
     };
     std::vector<Pack> packs;
     int64_t checked_T = 0;  // largest row count whose buffers were checked for overlaps
+};
+
+struct dlm_adamw {
+    AdDesc* d_descs = nullptr;  // device block: descriptors, then the tensor of every chunk
+    const int32_t* d_chunk_tensor = nullptr;
+    AdWords* d_words = nullptr;
+    int64_t n_chunks = 0;
+    int32_t p_dtype = 0, g_dtype = 0, bits = 32;
+    uint32_t seed = 0;
 };
 
 // Scratch memory of dlm_sgmm_noalloc: one file-scope device array, which each
@@ -971,6 +981,164 @@ int dlm_sgmm_launches(int64_t T, int64_t d_in_max, int32_t r, int32_t n_problems
         return seg + 1;  // one launch after the segmentation
     if (T <= kSgmmInlineRows && !vsum) return 2;  // the rows ordered inside the shrink and expand
     return seg + 2 + vsum;
+}
+
+// ----------------------------------------------------------------- AdamW ----
+
+int dlm_adamw_create(const dlm_adamw_param* params, int32_t n, int32_t p_dtype, int32_t g_dtype, int32_t state_bits,
+                     int64_t step, uint32_t seed, dlm_adamw** out) {
+    if (!out) return fail(DLM_EINVAL, "adamw_create: out is null");
+    *out = nullptr;
+    if (!params || n < 1 || n > (1 << 20)) return fail(DLM_EINVAL, "adamw_create: bad tensor list (n=%d)", n);
+    if (!valid_dtype(p_dtype) || !valid_dtype(g_dtype))
+        return fail(DLM_EDTYPE, "adamw_create: unknown dtype (p %d, g %d)", p_dtype, g_dtype);
+    if (state_bits != 32 && state_bits != 8) return fail(DLM_EINVAL, "adamw_create: state_bits=%d is not 32 or 8", state_bits);
+    if (step < 0 || step >= ((int64_t)1 << 31)) return fail(DLM_EINVAL, "adamw_create: step=%lld", (long long)step);
+    const size_t ps = esize(p_dtype), gs = esize(g_dtype), ss = state_bits == 32 ? 4 : 1;
+    std::vector<AdDesc> descs;
+    std::vector<Span> v;
+    std::vector<char> blob;
+    dlm_adamw* h = nullptr;
+    int64_t chunks = 0;
+    size_t desc_bytes = 0;
+    try {
+        descs.resize(n);
+        for (int i = 0; i < n; ++i) {
+            const dlm_adamw_param& q = params[i];
+            AdDesc& d = descs[i];
+            if (q.n < 0 || q.n > ((int64_t)1 << 40)) return fail(DLM_ESHAPE, "adamw_create: tensor %d: n=%lld", i, (long long)q.n);
+            if (q.n > 0 && (!q.p || !q.g || !q.m || !q.v || (state_bits == 8 && (!q.m_scale || !q.v_scale))))
+                return fail(DLM_EINVAL, "adamw_create: tensor %d: null pointer", i);
+            if (q.master && p_dtype == DLM_F32)
+                return fail(DLM_EINVAL, "adamw_create: tensor %d: an fp32 parameter has no master", i);
+            if (!std::isfinite(q.weight_decay)) return fail(DLM_EINVAL, "adamw_create: tensor %d: weight_decay is not finite", i);
+            if ((uintptr_t)q.p % ps || (uintptr_t)q.g % gs || (uintptr_t)q.m % ss || (uintptr_t)q.v % ss ||
+                (uintptr_t)q.master % 4 || (uintptr_t)q.m_scale % 4 || (uintptr_t)q.v_scale % 4)
+                return fail(DLM_EALIGN, "adamw_create: tensor %d: a pointer is not a multiple of its element's size", i);
+            d = AdDesc{};
+            d.p = q.p;
+            d.g = q.g;
+            d.master = q.master;
+            d.m = q.m;
+            d.v = q.v;
+            d.ms = q.m_scale;
+            d.vs = q.v_scale;
+            d.n = q.n;
+            d.wd = q.weight_decay;
+            d.vec = (uintptr_t)q.p % (4 * ps) == 0 && (uintptr_t)q.g % (4 * gs) == 0 && (uintptr_t)q.m % (4 * ss) == 0 &&
+                    (uintptr_t)q.v % (4 * ss) == 0 && (uintptr_t)q.master % 16 == 0;
+            d.chunk0 = chunks;
+            chunks += (q.n + kAdamChunk - 1) / kAdamChunk;
+            const size_t nb = (size_t)(q.n + kAdamBlock - 1) / kAdamBlock * 4;
+            v.push_back(span(q.p, q.n * ps, true, "p", i));
+            v.push_back(span(q.g, q.n * gs, false, "g", i));
+            v.push_back(span(q.m, q.n * ss, true, "m", i));
+            v.push_back(span(q.v, q.n * ss, true, "v", i));
+            if (q.master) v.push_back(span(q.master, (size_t)q.n * 4, true, "master", i));
+            if (state_bits == 8) {
+                v.push_back(span(q.m_scale, nb, true, "m_scale", i));
+                v.push_back(span(q.v_scale, nb, true, "v_scale", i));
+            }
+        }
+        if (!grid_fits(chunks, 256)) return fail(DLM_ESHAPE, "adamw_create: the sizes need a launch grid of more than 2^32 - 1 work-items");
+        Span a, b;
+        if (write_conflict(std::move(v), &a, &b)) return conflict_fail("adamw_create", a, b);
+        desc_bytes = (sizeof(AdDesc) * n + 255) & ~(size_t)255;
+        blob.resize(desc_bytes + sizeof(int32_t) * (size_t)chunks + 256);
+        std::memcpy(blob.data(), descs.data(), sizeof(AdDesc) * n);
+        int32_t* map = (int32_t*)(blob.data() + desc_bytes);
+        for (int i = 0; i < n; ++i) {
+            const int64_t end = i + 1 < n ? descs[i + 1].chunk0 : chunks;
+            for (int64_t c = descs[i].chunk0; c < end; ++c) map[c] = i;
+        }
+        h = new dlm_adamw();
+    } catch (const std::bad_alloc&) {
+        return fail(DLM_ENOMEM, "adamw_create: host allocation failed");
+    }
+    AdWords w{};
+    w.t = step;
+    hipError_t e = hipMalloc((void**)&h->d_descs, blob.size());
+    if (e == hipSuccess) e = hipMemcpy(h->d_descs, blob.data(), blob.size(), hipMemcpyHostToDevice);
+    if (e == hipSuccess) e = hipMalloc((void**)&h->d_words, 256);
+    if (e == hipSuccess) e = hipMemcpy(h->d_words, &w, sizeof w, hipMemcpyHostToDevice);
+    if (e != hipSuccess) {
+        if (h->d_descs) (void)hipFree(h->d_descs);
+        if (h->d_words) (void)hipFree(h->d_words);
+        delete h;
+        return hip_fail(e, "adamw_create");
+    }
+    h->d_chunk_tensor = (const int32_t*)((const char*)h->d_descs + desc_bytes);
+    h->n_chunks = chunks;
+    h->p_dtype = p_dtype;
+    h->g_dtype = g_dtype;
+    h->bits = state_bits;
+    h->seed = seed;
+    *out = h;
+    return ok();
+}
+
+int dlm_adamw_destroy(dlm_adamw* h) {
+    if (!h) return fail(DLM_EINVAL, "adamw_destroy: null handle");
+    const hipError_t e = hipDeviceSynchronize();
+    (void)hipFree(h->d_descs);
+    (void)hipFree(h->d_words);
+    delete h;
+    if (e != hipSuccess) return hip_fail(e, "adamw_destroy");
+    return ok();
+}
+
+int dlm_adamw_step(dlm_adamw* h, const dlm_adamw_cfg* c, const float* lr_scale, const float* grad_scale, void* stream) {
+    if (!h || !c) return fail(DLM_EINVAL, "adamw_step: null argument");
+    if (!std::isfinite(c->lr)) return fail(DLM_EINVAL, "adamw_step: lr is not finite");
+    if (!(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0))
+        return fail(DLM_EINVAL, "adamw_step: beta1=%g, beta2=%g not in [0, 1)", c->beta1, c->beta2);
+    if (!(c->eps > 0.f) || !std::isfinite(c->eps)) return fail(DLM_EINVAL, "adamw_step: eps=%g is not positive", c->eps);
+    if (h->n_chunks == 0) return ok();
+    AdamArgs a{};
+    a.descs = h->d_descs;
+    a.chunk_tensor = h->d_chunk_tensor;
+    a.words = h->d_words;
+    a.n_chunks = h->n_chunks;
+    a.beta1 = c->beta1;
+    a.beta2 = c->beta2;
+    a.lb1 = std::log(c->beta1);
+    a.lb2 = std::log(c->beta2);
+    a.lr = c->lr;
+    a.eps = c->eps;
+    a.seed = h->seed;
+    a.lr_scale = lr_scale;
+    a.grad_scale = grad_scale;
+    const hipError_t e = launch_adamw(a, h->p_dtype, h->g_dtype, h->bits, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "adamw_step launch");
+    return ok();
+}
+
+int dlm_adamw_status(dlm_adamw* h, int64_t* step, int32_t* code, void* stream) {
+    if (!h || !step || !code) return fail(DLM_EINVAL, "adamw_status: null argument");
+    AdWords w{};
+    hipError_t e = hipStreamSynchronize((hipStream_t)stream);
+    if (e == hipSuccess) e = hipMemcpy(&w, h->d_words, sizeof w, hipMemcpyDeviceToHost);
+    if (e == hipSuccess && w.err) e = hipMemset(&h->d_words->err, 0, sizeof w.err);
+    if (e != hipSuccess) return hip_fail(e, "adamw_status");
+    *step = w.t;
+    *code = w.err ? DLM_EDEVICE : DLM_OK;
+    return ok();
+}
+
+int dlm_adamw_read_state(const int8_t* m, const uint8_t* v, const float* m_scale, const float* v_scale, int64_t n,
+                         float* m_out, float* v_out, void* stream) {
+    if (n < 0 || n > ((int64_t)1 << 40)) return fail(DLM_ESHAPE, "adamw_read_state: n=%lld", (long long)n);
+    if (n == 0) return ok();
+    if (!m || !v || !m_scale || !v_scale || !m_out || !v_out) return fail(DLM_EINVAL, "adamw_read_state: null pointer");
+    const size_t nb = (size_t)(n + kAdamBlock - 1) / kAdamBlock * 4;
+    Span a, b;
+    if (write_conflict({span(m, n, false, "m", 0), span(v, n, false, "v", 0), span(m_scale, nb, false, "m_scale", 0),
+                        span(v_scale, nb, false, "v_scale", 0), span(m_out, (size_t)n * 4, true, "m_out", 0),
+                        span(v_out, (size_t)n * 4, true, "v_out", 0)}, &a, &b))
+        return conflict_fail("adamw_read_state", a, b);
+    const hipError_t e = launch_adamw_read_state(m, v, m_scale, v_scale, n, m_out, v_out, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "adamw_read_state launch");
+    return ok();
 }
 
 }  // extern "C"

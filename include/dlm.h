@@ -444,6 +444,79 @@ int dlm_sgmm_status(void* workspace, int32_t* code, void* stream);
  */
 int dlm_sgmm_launches(int64_t T, int64_t d_in_max, int32_t r, int32_t n_problems, int32_t dtype);
 
+/* ------------------------------------------------------------------ AdamW */
+
+/* One tensor of an AdamW step. */
+typedef struct {
+    void* p;           /* [n] parameter (p_dtype), updated in place */
+    const void* g;     /* [n] gradient (g_dtype) */
+    float* master;     /* [n] fp32 copy of a bf16 parameter, updated in place (the
+                          parameter becomes its rounding), or NULL */
+    void* m;           /* [n] first moment: fp32, or int8 codes with 8-bit states */
+    void* v;           /* [n] second moment: fp32, or uint8 codes */
+    float* m_scale;    /* [ceil(n / 256)] one scale per block (8-bit states only) */
+    float* v_scale;
+    int64_t n;
+    float weight_decay;
+} dlm_adamw_param;
+
+typedef struct {
+    float lr;
+    double beta1, beta2; /* in [0, 1) */
+    float eps;           /* > 0 */
+} dlm_adamw_cfg;
+
+typedef struct dlm_adamw dlm_adamw;
+
+/*
+ * Register n tensors (the adapter banks of every layer, a router's weight) that
+ * one AdamW step updates together.  Copies the descriptors to a small device
+ * table; the buffers stay owned by the caller, must outlive the handle, and no
+ * written one may overlap another.  step = steps already taken (0 at the start
+ * of training): the count lives on the device from here on.  seed: of the
+ * 8-bit states' rounding noise.
+ * state_bits 32: m and v are fp32.  state_bits 8: blocks of 256 consecutive
+ * elements share a scale each,
+ *   m = m_scale sign(q) (q / 127)^2      v = v_scale (c / 255)^4
+ * rounded stochastically (the stored value's mean is the exact one), a positive
+ * v to a code of at least 1; all-zero codes and scales are zero moments.
+ * Tensors may be of any size and alignment of their element (aligned to four
+ * elements they are faster).
+ */
+int dlm_adamw_create(const dlm_adamw_param* params, int32_t n, int32_t p_dtype, int32_t g_dtype, int32_t state_bits,
+                     int64_t step, uint32_t seed, dlm_adamw** out);
+
+/* Free the handle's device memory (synchronises the device first). */
+int dlm_adamw_destroy(dlm_adamw* h);
+
+/*
+ * One step over every tensor, two launches (a one-thread count, the step), no allocation:
+ *   t <- t + 1,  g' = grad_scale g,  m <- b1 m + (1 - b1) g',  v <- b2 v + (1 - b2) g'^2
+ *   w <- w (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+ * w = the master where there is one, else the parameter; lr = cfg's times
+ * *lr_scale.  lr_scale and grad_scale are DEVICE floats or NULL (1): a captured
+ * step reads them, and t, on every replay.
+ * fp32 throughout (8-bit moments: binary64 between their codes); m and v of
+ * this step enter w before they are rounded to codes.
+ * An element whose new v is not finite in fp32 (a gradient infinite, NaN or
+ * past 1.8e19) is left unchanged, with 8-bit states its whole block of 256, and
+ * the error word is set.
+ */
+int dlm_adamw_step(dlm_adamw* h, const dlm_adamw_cfg* cfg, const float* lr_scale, const float* grad_scale, void* stream);
+
+/*
+ * Synchronise `stream`, then read the step count and read and clear the error
+ * word: *step, *code (host) = DLM_OK or DLM_EDEVICE (some gradient was not finite).
+ */
+int dlm_adamw_status(dlm_adamw* h, int64_t* step, int32_t* code, void* stream);
+
+/*
+ * The fp32 values that n 8-bit moments stand for (checkpoints, inspection):
+ * m_out [n], v_out [n].  One launch on `stream`.
+ */
+int dlm_adamw_read_state(const int8_t* m, const uint8_t* v, const float* m_scale, const float* v_scale, int64_t n,
+                         float* m_out, float* v_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

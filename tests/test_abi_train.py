@@ -92,3 +92,74 @@ def test_route_plain_form_by_hand():
     assert idx.tolist() == [[0, 3]] and np.allclose(g, [[0.5, 0.5]])
     idx, g = route_ref.route(l, 1, n_groups=2, keep_groups=1, group_top=2)
     assert idx.tolist() == [[2]]
+
+
+def _params(*ps):
+    arr = (dlm.dlm_adamw_param * len(ps))()
+    for i, p in enumerate(ps):
+        arr[i] = dlm.dlm_adamw_param(*p)
+    return arr
+
+
+@built
+def test_adamw_validation():
+    lib = dlm.load()
+    h = C.c_void_p()
+    a = [FAKE + k * MB for k in range(8)]
+    ok32 = (a[0], a[1], None, a[2], a[3], None, None, 100, 0.01)
+    ok8 = (a[0], a[1], None, a[2], a[3], a[4], a[5], 100, 0.01)
+
+    def create(ps, n=1, pd=0, gd=0, bits=32, step=0, out=True):
+        return lib.dlm_adamw_create(ps, n, pd, gd, bits, step, 0, C.byref(h) if out else None)
+
+    assert create(None) == dlm.DLM_EINVAL and create(_params(ok32), 0) == dlm.DLM_EINVAL
+    assert create(_params(ok32), out=False) == dlm.DLM_EINVAL
+    assert create(_params(ok32), pd=3) == dlm.DLM_EDTYPE and create(_params(ok32), gd=-1) == dlm.DLM_EDTYPE
+    assert create(_params(ok32), bits=16) == dlm.DLM_EINVAL
+    assert create(_params(ok32), step=-1) == dlm.DLM_EINVAL
+    assert create(_params(ok32), bits=8) == dlm.DLM_EINVAL  # no scales
+    for k in (0, 1, 3, 4):
+        bad = list(ok32)
+        bad[k] = None
+        assert create(_params(tuple(bad))) == dlm.DLM_EINVAL
+    assert create(_params(ok32[:7] + (-1, 0.0))) == dlm.DLM_ESHAPE
+    assert create(_params(ok32[:8] + (float("nan"),))) == dlm.DLM_EINVAL
+    assert create(_params((a[0], a[1], a[6]) + ok32[3:])) == dlm.DLM_EINVAL  # fp32 parameter with a master
+    assert create(_params((a[0] + 2,) + ok32[1:])) == dlm.DLM_EALIGN
+    assert create(_params((a[0] + 1,) + ok32[1:]), pd=1) == dlm.DLM_EALIGN
+    # buffers that overlap, in one tensor and between two; the second tensor is named
+    assert create(_params((a[0], a[0]) + ok32[2:])) == dlm.DLM_EINVAL
+    assert create(_params(ok8[:6] + (a[4],) + ok8[7:]), bits=8) == dlm.DLM_EINVAL
+    other = (a[6], a[1] + 1000, None, a[2] + 396, a[7], None, None, 100, 0.0)
+    assert create(_params(ok32, other), 2) == dlm.DLM_EINVAL
+    assert "1" in lib.dlm_last_error().decode()
+    assert h.value is None
+    cfg = dlm.dlm_adamw_cfg(1e-3, 0.9, 0.999, 1e-8)
+    assert lib.dlm_adamw_step(None, C.byref(cfg), None, None, None) == dlm.DLM_EINVAL
+    assert lib.dlm_adamw_destroy(None) == dlm.DLM_EINVAL
+    assert lib.dlm_adamw_status(None, None, None, None) == dlm.DLM_EINVAL
+    rd = lib.dlm_adamw_read_state
+    assert rd(a[0], a[1], a[2], a[3], -1, a[4], a[5], None) == dlm.DLM_ESHAPE
+    assert rd(None, a[1], a[2], a[3], 5, a[4], a[5], None) == dlm.DLM_EINVAL
+    assert rd(a[0], a[1], a[2], a[3], 5, a[4], a[4], None) == dlm.DLM_EINVAL
+    assert rd(None, None, None, None, 0, None, None, None) == dlm.DLM_OK
+
+
+def test_adamw_codes_round_trip():
+    """The plain codes: decoding is within one code step, its mean over the noise exact, zeros stay zeros."""
+    import adamw_ref
+
+    rng = np.random.default_rng(0)
+    m, v = rng.standard_normal(700) * 1e-3, rng.standard_normal(700) ** 2 * 1e-6
+    m[:5] = 0
+    v[3] = 0
+    acc_m, acc_v, n = 0.0, 0.0, 400
+    for t in range(n):
+        q, c, ms, vs = adamw_ref.encode(m, v, 1, t, 0)
+        dm, dv = adamw_ref.decode(q, c, ms, vs)
+        b = np.arange(700) // 256
+        assert (np.abs(dm - m) <= ms[b] * (2 * np.abs(q.astype(int)) + 1) / 127 ** 2).all()
+        assert (dm[:5] == 0).all() and dv[3] == 0 and (dv[v > 0] > 0).all()
+        acc_m, acc_v = acc_m + dm, acc_v + dv
+    step = ms[b] * (2 * 127 + 1) / 127 ** 2
+    assert (np.abs(acc_m / n - m) <= 6 * step / 2 / np.sqrt(n)).all()
