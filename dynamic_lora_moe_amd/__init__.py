@@ -10,7 +10,7 @@ fallback: if the library is missing or fails to load, importing the ops raises.
   Layers([(W, A, B), ...], E, r, scale).switch(old, new)   # in place, one launch
   sgmm(x, idx, g, A, B, y, scale)                          # y updated in place
   AdamW(params, grads, ...).step(lr)                       # many tensors at once
-  SgmmGroup([(x, A, B, y), ...], E, r, scale).run(idx, g)
+  SgmmGroup([(x, A, B, y), ...], E, r, scale).run(idx, g)  # .bind_grads(...).backward(idx, g, dg)
 """
 from __future__ import annotations
 
@@ -82,6 +82,9 @@ def load(path: str = LIB_PATH):
         "dlm_pregate_centroid": ([P, P, I64, I64, I32, I32, I32, P, P, P], C.c_int),
         "dlm_route": ([P, I64, P, I64, I32, I32, P, P, P, P, P], C.c_int),
         "dlm_route_backward": ([P, I64, P, P, I64, I32, I32, P, P, I64, P], C.c_int),
+        "dlm_sgmm_backward_workspace_size": ([I64, I64, I32, I32, I32, P], C.c_int),
+        "dlm_sgmm_group_bind_grads": ([P, P, P, P, P], C.c_int),
+        "dlm_sgmm_group_backward": ([P, P, P, P, I64, I32, P, C.c_size_t, P], C.c_int),
         "dlm_adamw_create": ([P, I32, I32, I32, I32, I64, C.c_uint32, P], C.c_int),
         "dlm_adamw_destroy": ([P], C.c_int),
         "dlm_adamw_step": ([P, P, P, P, P], C.c_int),
@@ -547,6 +550,56 @@ class SgmmGroup:
             # a workspace made here on the current stream is used on `stream`:
             # keep the allocator from handing it out again before those launches end
             workspace.record_stream(stream)
+        return workspace
+
+    def bind_grads(self, dys, dxs, dAs, dBs):
+        """Bind the buffers of backward(): per problem dy [T][d_out] and dx [T][d_in]
+        (the problems' dtype; dxs or an entry of it may be None, and problems that
+        share an x may share a dx), dA [E][r][d_in] and dB [E][d_out][r] fp32."""
+        n = self.n
+        dys, dAs, dBs = list(dys), list(dAs), list(dBs)
+        dxs = [None] * n if dxs is None else list(dxs)
+        if not len(dys) == len(dxs) == len(dAs) == len(dBs) == n:
+            raise ValueError("one dy, dx (or None), dA and dB per problem")
+        for k, ((x, A, B, y), dy, dx, dA, dB) in enumerate(zip(self._keep, dys, dxs, dAs, dBs)):
+            _like(dy, f"dy {k}", y.shape, x.dtype, x.device)
+            if dx is not None:
+                _like(dx, f"dx {k}", x.shape, x.dtype, x.device)
+            _like(dA, f"dA {k}", A.shape, torch.float32, x.device)
+            _like(dB, f"dB {k}", B.shape, torch.float32, x.device)
+        ptrs = lambda ts: (C.c_void_p * n)(*[None if t is None else t.data_ptr() for t in ts])  # noqa: E731
+        _check(load().dlm_sgmm_group_bind_grads(self._h, ptrs(dys), ptrs(dxs), ptrs(dAs), ptrs(dBs)),
+               "dlm_sgmm_group_bind_grads")
+        self._grads = (dys, dxs, dAs, dBs)
+
+    def backward_workspace(self, T: int):
+        d_max = max(max(x.shape[1], y.shape[1]) for x, _, _, y in self._keep)
+        b = C.c_size_t(0)
+        _check(load().dlm_sgmm_backward_workspace_size(T, d_max, self.E, self.r, self.n, C.byref(b)),
+               "dlm_sgmm_backward_workspace_size")
+        return torch.empty(b.value, dtype=torch.uint8, device=self.device)
+
+    def backward(self, idx, g, dg=None, accumulate: bool = False, T: int | None = None, workspace=None, stream=None):
+        """The gradients of run() for rows [0, T) of (idx, g) into the bound buffers:
+        dx is added to in place, dA and dB are written (or added to), and dg [T][2]
+        fp32, if given, is the gradient of g.  Returns the workspace, whose status
+        word sgmm_status() reads (a rejected set leaves every buffer unchanged)."""
+        _need(idx, "idx")
+        _here(idx, stream, "idx")
+        T = idx.shape[0] if T is None else T
+        if not 0 <= T <= self.rows:
+            raise ValueError(f"T={T} rows, but the group's problems hold {self.rows}")
+        _like(idx[:T], "idx", (T, 2), torch.int32, self.device)
+        _like(g[:T], "g", (T, 2), torch.float32, self.device)
+        if dg is not None:
+            _like(dg[:T], "dg", (T, 2), torch.float32, self.device)
+        own = workspace is None
+        if own:
+            workspace = self.backward_workspace(T)
+        _check(load().dlm_sgmm_group_backward(self._h, _p(idx), _p(g), _p(dg), T, 1 if accumulate else 0, _p(workspace),
+                                              _ws_bytes(workspace), _stream(stream)), "dlm_sgmm_group_backward")
+        if own:
+            _fresh(stream, workspace)
         return workspace
 
     def close(self):

@@ -11,7 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdlm.so")
-SOURCES = ["api.hip", "pregate.hip", "route.hip", "switch.hip", "sgmm.hip", "adamw.hip"]
+SOURCES = ["api.hip", "pregate.hip", "route.hip", "switch.hip", "sgmm.hip", "sgmm_grad.hip",
+           "adamw.hip"]
 ARCH = "gfx950"
 
 FLAGS = [
@@ -28,7 +29,7 @@ def hipcc() -> str:
     return p
 
 
-def build(verbose: bool = False, jobs: int = 6) -> str:
+def build(verbose: bool = False, jobs: int = 7) -> str:
     """Compile every source to an object (in parallel) and link libdlm.so."""
     bdir = os.path.join(HERE, "_build")
     os.makedirs(bdir, exist_ok=True)

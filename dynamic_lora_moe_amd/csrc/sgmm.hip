@@ -1566,8 +1566,9 @@ __global__ __launch_bounds__(256) void sgmm_pack_a_kernel(const uint16_t* __rest
 // Grid for at most max_items work items (a multiple of 8: one share per XCD).
 inline int64_t item_grid(int64_t max_items) { return 8 * ((max_items + 7) / 8); }
 
+// The shrink, and above kSgmmFoldRank the K-slice sum.
 template <int R16>
-hipError_t launch_mfma(const SgmmArgs& a, hipStream_t s) {
+hipError_t launch_shrink(const SgmmArgs& a, hipStream_t s) {
     const dim3 gs((unsigned)item_grid(a.total_ks * a.L.tiles_max));
     if (a.packed)
         hipLaunchKernelGGL((sgmm_shrink_bf16<R16, true>), gs, dim3(256), 0, s, a);
@@ -1579,8 +1580,12 @@ hipError_t launch_mfma(const SgmmArgs& a, hipStream_t s) {
         const dim3 gs((unsigned)((a.L.T_pad * 2 * a.L.r_pad / 4 + 255) / 256), (unsigned)a.n_prob);
         hipLaunchKernelGGL(sgmm_vsum_kernel, gs, dim3(256), 0, s, a);
         e = hipGetLastError();
-        if (e != hipSuccess) return e;
     }
+    return e;
+}
+
+template <int R16>
+hipError_t launch_expand(const SgmmArgs& a, hipStream_t s) {
     const int64_t per_max = (a.n_expand_units + 7) / 8;
     const dim3 ge((unsigned)(8 * (per_max + (per_max < kExpandSplit ? per_max : kExpandSplit))));
     if (a.r % 8 == 0)
@@ -1613,19 +1618,52 @@ hipError_t launch_fused_r(const SgmmArgs& a, hipStream_t s) {
     }
 }
 
-// The MFMA launches for the workspace's padded rank.
-hipError_t launch_mfma_r(const SgmmArgs& a, hipStream_t s) {
+// The MFMA launches for the workspace's padded rank: the shrink, the expand or both.
+template <int R16>
+hipError_t launch_mfma(const SgmmArgs& a, bool shrink, bool expand, hipStream_t s) {
+    hipError_t e = hipSuccess;
+    if (shrink) e = launch_shrink<R16>(a, s);
+    if (expand && e == hipSuccess) e = launch_expand<R16>(a, s);
+    return e;
+}
+hipError_t launch_mfma_r(const SgmmArgs& a, hipStream_t s, bool shrink = true, bool expand = true) {
     switch (a.L.r_pad / 16) {
-        case 1: return launch_mfma<1>(a, s);
-        case 2: return launch_mfma<2>(a, s);
-        case 3: return launch_mfma<3>(a, s);
-        case 4: return launch_mfma<4>(a, s);
-        case 5: return launch_mfma<5>(a, s);
-        case 6: return launch_mfma<6>(a, s);
-        case 7: return launch_mfma<7>(a, s);
-        case 8: return launch_mfma<8>(a, s);
+        case 1: return launch_mfma<1>(a, shrink, expand, s);
+        case 2: return launch_mfma<2>(a, shrink, expand, s);
+        case 3: return launch_mfma<3>(a, shrink, expand, s);
+        case 4: return launch_mfma<4>(a, shrink, expand, s);
+        case 5: return launch_mfma<5>(a, shrink, expand, s);
+        case 6: return launch_mfma<6>(a, shrink, expand, s);
+        case 7: return launch_mfma<7>(a, shrink, expand, s);
+        case 8: return launch_mfma<8>(a, shrink, expand, s);
         default: return hipErrorInvalidValue;
     }
+}
+
+// The segmentation (with the one-launch form's work ranges when fused).
+hipError_t launch_segment(const SgmmArgs& a, int fused, hipStream_t s) {
+    const int64_t n_chunks = a.L.n_chunks;
+    if (n_chunks > kSegFewChunks) {
+        hipLaunchKernelGGL(sgmm_seg_count, dim3((unsigned)n_chunks), dim3(kSegThreads), 0, s, a.idx, a.g, a.T, a.E,
+                           a.ws, a.L);
+        const hipError_t e0 = hipGetLastError();
+        if (e0 != hipSuccess) return e0;
+    }
+    hipLaunchKernelGGL(sgmm_seg_place, dim3((unsigned)n_chunks), dim3(kSegThreads), 0, s, a.idx, a.g, a.T, a.E,
+                       a.ws, a.L, a.status_out, a.descs, a.single, a.n_prob, a.total_ks, a.total_cb, fused);
+    return hipGetLastError();
+}
+
+// fp32: element-wise kernels, grids sized for the most rows possible.
+hipError_t launch_shrink_generic(const SgmmArgs& a, hipStream_t s) {
+    const dim3 g1((unsigned)((a.L.T_pad * 2 * a.r + 255) / 256), (unsigned)a.n_prob);
+    hipLaunchKernelGGL(sgmm_shrink_generic<float>, g1, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+hipError_t launch_expand_generic(const SgmmArgs& a, hipStream_t s) {
+    const dim3 g2((unsigned)((a.L.T_pad * a.d_out_max + 255) / 256), (unsigned)a.n_prob);
+    hipLaunchKernelGGL(sgmm_expand_generic<float>, g2, dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -1682,28 +1720,25 @@ hipError_t launch_sgmm(const SgmmArgs& a, int dtype, hipStream_t s) {
         return launch_mfma_r(b, s);
     }
     static_assert(kSegThreads == kSgmmSegRows, "segmentation chunk");
-    const int64_t n_chunks = a.L.n_chunks;
-    if (n_chunks > kSegFewChunks) {
-        hipLaunchKernelGGL(sgmm_seg_count, dim3((unsigned)n_chunks), dim3(kSegThreads), 0, s, a.idx, a.g, a.T, a.E,
-                           a.ws, a.L);
-        hipError_t e0 = hipGetLastError();
-        if (e0 != hipSuccess) return e0;
-    }
-    hipLaunchKernelGGL(sgmm_seg_place, dim3((unsigned)n_chunks), dim3(kSegThreads), 0, s, a.idx, a.g, a.T, a.E,
-                       a.ws, a.L, a.status_out, a.descs, a.single, a.n_prob, a.total_ks, a.total_cb,
-                       fused ? 1 : 0);
-    hipError_t e = hipGetLastError();
+    hipError_t e = launch_segment(a, fused ? 1 : 0, s);
     if (e != hipSuccess) return e;
     if (fused) return launch_fused_r(a, s);
     if (dtype == 1) return launch_mfma_r(a, s);
-    // fp32: element-wise kernels, grid sized for the most rows possible
-    const dim3 g1((unsigned)((a.L.T_pad * 2 * a.r + 255) / 256), (unsigned)a.n_prob);
-    hipLaunchKernelGGL(sgmm_shrink_generic<float>, g1, dim3(256), 0, s, a);
-    e = hipGetLastError();
+    e = launch_shrink_generic(a, s);
     if (e != hipSuccess) return e;
-    const dim3 g2((unsigned)((a.L.T_pad * a.d_out_max + 255) / 256), (unsigned)a.n_prob);
-    hipLaunchKernelGGL(sgmm_expand_generic<float>, g2, dim3(256), 0, s, a);
-    return hipGetLastError();
+    return launch_expand_generic(a, s);
 }
+
+hipError_t launch_sgmm_segment(const SgmmArgs& a, hipStream_t s) {
+    if (!grid_fits(a.L.n_chunks, kSegThreads)) return hipErrorInvalidConfiguration;
+    return launch_segment(a, 0, s);
+}
+hipError_t launch_sgmm_shrink(const SgmmArgs& a, int dtype, hipStream_t s) {
+    return dtype == 1 ? launch_mfma_r(a, s, true, false) : launch_shrink_generic(a, s);
+}
+hipError_t launch_sgmm_expand(const SgmmArgs& a, int dtype, hipStream_t s) {
+    return dtype == 1 ? launch_mfma_r(a, s, false, true) : launch_expand_generic(a, s);
+}
+bool sgmm_launches_fit(const SgmmArgs& a, int dtype) { return sgmm_grids_fit(a, dtype); }
 
 }  // namespace dlm

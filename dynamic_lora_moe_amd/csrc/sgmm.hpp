@@ -108,4 +108,78 @@ hipError_t launch_sgmm(const SgmmArgs& a, int dtype, hipStream_t s);
 // Ap[e][k / 8][rho][0..8) = A[e][rho][k..k+8) for k = 0, 8, ..., d_in - 8 (bf16).
 hipError_t launch_sgmm_pack_a(const void* A, void* Ap, int E, int r, int64_t d_in, hipStream_t s);
 
+// The steps of an SGMM one by one (the gradients run other work between them):
+// the segmentation into the workspace, the shrink of every problem of a
+// segmented batch (with its K-slice sum above kSgmmFoldRank), and the expand of
+// a set of problems, whose v (ks0, n_ks) a shrink has left in the workspace.
+hipError_t launch_sgmm_segment(const SgmmArgs& a, hipStream_t s);
+hipError_t launch_sgmm_shrink(const SgmmArgs& a, int dtype, hipStream_t s);
+hipError_t launch_sgmm_expand(const SgmmArgs& a, int dtype, hipStream_t s);
+bool sgmm_launches_fit(const SgmmArgs& a, int dtype);
+
+// ---- gradients ----------------------------------------------------------------
+
+// Columns of one item of the banks' gradients, slots of one list tile.
+constexpr int kGradCols = 128;
+constexpr int kGradTile = 32;
+
+// One projection and its gradients in the device table.
+struct SgGrad {
+    const void* A;   // [E][r][d_in]
+    const void* B;   // [E][d_out][r]
+    void* Ap;        // A packed for the shrink (bf16), else unused
+    void* At;        // [E][d_in][r]: A transposed, the dx expand's up matrix
+    void* Bt;        // B transposed: [E][d_out / 8][r][8] (bf16) or [E][r][d_out] (fp32)
+    int32_t d_in, d_out;
+    int64_t pk0;     // first 8-element group of this projection's banks (prefix sum over A and B)
+    int64_t ks_u, ks_w;      // first K slice of u = A x and of w = B^T dy in the workspace's v
+    int32_t n_ks_u, n_ks_w;  // and how many there are to add
+};
+// One side of a projection's bank gradients: dA from x, dB from dy.
+struct SgOuter {
+    const void* act;  // x [T][d] or dy [T][d]
+    float* out;       // dA [E][r][d] or dB [E][d][r]
+    int32_t d;
+    int32_t side;     // 0: dA, 1: dB
+    int32_t prob;
+    int32_t unit0;    // first column block (prefix sum)
+};
+
+// Workspace of a backward call: the SGMM's for twice the problems, then these.
+struct SgGradLayout {
+    SgLayout L;
+    size_t eoff;   // [E + 1] first list position of every expert (multiples of kGradTile)
+    size_t slot;   // [cap] 2 * position + k, or -1 (padding)
+    size_t srow;   // [cap] the row
+    size_t coef;   // [prob][side][hi, lo][cap / kGradTile][rc_pad][kGradTile] bf16
+    size_t dgp;    // [prob][T][2] fp32
+    size_t total;
+    int64_t cap;   // list positions at most
+    int rc_pad;    // ranks of a coefficient tile
+};
+SgGradLayout sgmm_grad_layout(int64_t T, int64_t d_max, int E, int r, int n_prob);
+
+struct SgGradArgs {
+    const SgGrad* probs;
+    const SgOuter* outers;       // 2 * n_prob
+    const int32_t* unit_outer;   // the owning entry of every column block
+    int32_t n_prob, n_units;
+    int64_t pk_total;
+    const int32_t* idx;
+    int64_t T;
+    int32_t E, r;
+    float scale;
+    char* ws;
+    SgGradLayout G;
+    float* dg;           // [T][2] or nullptr
+    int32_t accumulate;  // add to dA and dB instead of writing them
+};
+// T = 0: the gradients of no rows.
+hipError_t launch_grad_zero(const SgGradArgs& a, hipStream_t s);
+hipError_t launch_grad_pack(const SgGradArgs& a, int dtype, hipStream_t s);
+hipError_t launch_grad_lists(const SgGradArgs& a, hipStream_t s);
+hipError_t launch_grad_coefs(const SgGradArgs& a, int dtype, hipStream_t s);
+hipError_t launch_grad_outer(const SgGradArgs& a, int dtype, hipStream_t s);
+bool sgmm_grad_fits(const SgGradArgs& a, int dtype);
+
 }  // namespace dlm

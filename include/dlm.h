@@ -420,6 +420,46 @@ int dlm_sgmm_group_run(dlm_sgmm_group* h, const int32_t* idx, const float* g, in
                        void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Gradients of the group's product (training the adapters and the router that
+ * gates them).  Bind every problem's buffers once:
+ *   dy (host) [n] device pointers, dy_i [T][d_out_i] = dLoss/dy_i (dtype)
+ *   dx (host) [n] device pointers or NULL, dx_i [T][d_in_i] (dtype): the
+ *      adapters' share is ADDED to it, in place (it joins what the base product
+ *      left there); NULL entries are not wanted.  Problems that read one x may
+ *      share one dx: their shares are added in problem order, each with a
+ *      rounding of its own
+ *   dA, dB (host) [n] device pointers, dA_i [E][r][d_in_i], dB_i [E][d_out_i][r]
+ *      fp32
+ * bf16: all 16-byte aligned.  The handle allocates memory for the banks'
+ * transposes (the banks' size); the device is synchronised first.  The buffers
+ * stay owned by the caller.  Binding again replaces them.
+ */
+int dlm_sgmm_group_bind_grads(dlm_sgmm_group* h, const void* const* dy, void* const* dx, float* const* dA,
+                              float* const* dB);
+
+/*
+ * The backward pass of the group for T rows and their sets: with u = A_e x and
+ * w = B_e^T dy for the expert e of a row's slot k,
+ *   dx[t] <- round( dx[t] + sum_k s g_k A_e^T w )     (rows with a set; others untouched)
+ *   dg[t][k] = s sum_problems u . w   ([T][2] fp32 or NULL; 0 for an empty slot)
+ *   dA_e = s sum g w x[t]^T,  dB_e = s sum g dy[t] u^T   (over the slots with e;
+ *          written whole, 0 for an expert no row chose, or with accumulate != 0 added to)
+ * bf16: bf16 operands, fp32 sums; s g u and s g w enter as two bf16 terms.
+ * Reads the banks as they are (nothing is packed ahead).  Every result is
+ * bitwise reproducible.  A set the forward call would reject leaves all of
+ * them unchanged and sets the workspace status word (dlm_sgmm_status).  T = 0
+ * writes zeros to dA and dB unless accumulate, and looks at nothing else.
+ * workspace: >= dlm_sgmm_backward_workspace_size(T, the largest d_in or d_out,
+ * E, r, n_problems) bytes, 256-byte aligned.  No allocation; 7 launches (bf16
+ * up to rank 64: transposes, segmentation, shrink, lists, coefficients, expand,
+ * outer products) and one more each for dg, for T > 8192, for the K-slice sum
+ * above rank 64, and for every further problem that shares the same dx.
+ */
+int dlm_sgmm_backward_workspace_size(int64_t T, int64_t d_max, int32_t E, int32_t r, int32_t n_problems, size_t* bytes);
+int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* g, float* dg, int64_t T,
+                            int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Synchronise `stream`, then read and clear the workspace status word:
  * *code (host) = DLM_OK or DLM_EDEVICE.  Besides a rejected expert set, the
  * one-launch shrink + expand sets it if an expand work item waited about a

@@ -163,3 +163,39 @@ def test_adamw_codes_round_trip():
         acc_m, acc_v = acc_m + dm, acc_v + dv
     step = ms[b] * (2 * 127 + 1) / 127 ** 2
     assert (np.abs(acc_m / n - m) <= 6 * step / 2 / np.sqrt(n)).all()
+
+
+@built
+def test_backward_validation():
+    lib = dlm.load()
+    b = C.c_size_t(0)
+    size = lib.dlm_sgmm_backward_workspace_size
+    assert size(64, 4096, 8, 16, 7, None) == dlm.DLM_EINVAL
+    for bad in ((-1, 64, 8, 16, 1), ((1 << 29) + 1, 64, 8, 16, 1), (4, 0, 8, 16, 1), (4, 64, 0, 16, 1), (4, 64, 33, 16, 1),
+                (4, 64, 8, 0, 1), (4, 64, 8, 129, 1), (4, 64, 8, 16, 0)):
+        assert size(*bad, C.byref(b)) == dlm.DLM_ESHAPE
+    assert size(64, 4096, 8, 16, 7, C.byref(b)) == dlm.DLM_OK and b.value > 0
+    small = b.value
+    assert size(128, 4096, 8, 16, 7, C.byref(b)) == dlm.DLM_OK and b.value > small
+    # it holds the forward workspace of twice the problems
+    assert b.value > dlm.sgmm_workspace_size(128, 4096, 8, 16, 14)
+    assert lib.dlm_sgmm_group_bind_grads(None, None, None, None, None) == dlm.DLM_EINVAL
+    assert lib.dlm_sgmm_group_backward(None, P(FAKE), P(FAKE), None, 4, 0, P(FAKE), 1 << 20, None) == dlm.DLM_EINVAL
+
+
+def test_plain_gradients_against_differences():
+    """The plain gradients of the SGMM against differences of the plain product (linear in each argument)."""
+    torch = pytest.importorskip("torch")
+    import grad_ref
+
+    gen = torch.Generator().manual_seed(0)
+    T, E, r, i, o = 7, 3, 2, 5, 4
+    rnd = lambda *s: torch.randn(s, generator=gen, dtype=torch.float64)  # noqa: E731
+    x, A, B, dy, g = rnd(T, i), rnd(E, r, i), rnd(E, o, r), rnd(T, o), rnd(T, 2)
+    idx = torch.tensor([[0, 1], [2, 2], [-1, 0], [-1, -1], [1, -1], [2, 0], [0, 2]])
+    (dx, dA, dB, dg), _ = grad_ref.backward(x, idx, g, A, B, dy, 1.5)
+    for which, grad in (("x", dx), ("A", dA), ("B", dB), ("g", dg)):
+        v = rnd(*grad.shape)
+        a = dict(x=x, g=g, A=A, B=B)
+        f = lambda s: (grad_ref.forward(**{"idx": idx, "scale": 1.5, **{k: t + s * v if k == which else t for k, t in a.items()}}) * dy).sum()  # noqa: E731
+        assert abs(float(f(0.5) - f(-0.5) - (grad * v).sum())) < 1e-10

@@ -1,0 +1,375 @@
+"""The SGMM's gradients on the GPU against the plain binary64 form.
+
+Tolerances, with S the formula's sum over magnitudes and gamma_n the bound of an
+n-term fp32 sum (gpu_util): u and w are sums of d_in and d_out products, the
+coefficients s g u and s g w two more roundings, and in bf16 two bf16 terms
+(hi to 2^-8 of the value, lo to 2^-8 of the rest: 2^-16); the last sum runs over
+the rank (dx), the expert's slots twice (dA, dB: hi and lo) or rank and problems (dg):
+  dA  (gamma(d_out + 2 slots + 8) + 2^-16) S       dB the same with d_in
+  dx  (gamma(d_out + 4 r + 8) + 2^-16) S, and bf16's rounding 2^-8 of the result
+  dg  gamma(d_in + d_out + 2 r + problems + 8) S
+fp32 has no 2^-16 and no 2^-8 but fp32's own rounding.  The bounds above are the
+worst case; over random signs the split's error adds up like the values do, so
+the norms of dA and dB are also held to 2^-14 of the result's (fp32: 2^-18)."""
+import numpy as np
+import pytest
+import torch
+
+import dynamic_lora_moe_amd as dlm
+import grad_ref as ref
+from gpu_util import gamma
+
+pytestmark = pytest.mark.gpu
+SPLIT = 2.0 ** -16
+
+
+def _rnd(shape, dtype, std, gen):
+    return (torch.randn(shape, generator=gen) * std).to(dtype)
+
+
+def _sets(T, E, gen, empty=0.1, both=0.05, dup=0.0):
+    idx = torch.randint(0, E, (T, 2), generator=gen, dtype=torch.int32)
+    if E > 1:
+        same = (idx[:, 0] == idx[:, 1]) & (torch.rand(T, generator=gen) >= dup)
+        idx[same, 1] = (idx[same, 0] + 1) % E
+    idx[torch.rand(T, generator=gen) < empty, 1] = -1
+    idx[torch.rand(T, generator=gen) < empty, 0] = -1
+    idx[torch.rand(T, generator=gen) < both] = -1
+    return idx, torch.rand((T, 2), generator=gen) - 0.25
+
+
+class Case:
+    """A group of problems with their gradients' buffers, device and host."""
+
+    def __init__(self, T, shapes, E, r, dtype, seed=0, scale=1.5, rows=None, **sets):
+        gen = torch.Generator().manual_seed(seed)
+        self.T, self.E, self.r, self.dtype, self.scale = T, E, r, dtype, scale
+        n = T if rows is None else rows
+        self.idx, self.g = _sets(T, E, gen, **sets)
+        self.x = [_rnd((n, i), dtype, 1.0, gen) for o, i in shapes]
+        self.A = [_rnd((E, r, i), dtype, i ** -0.5, gen) for o, i in shapes]
+        self.B = [_rnd((E, o, r), dtype, 0.3, gen) for o, i in shapes]
+        self.dy = [_rnd((n, o), dtype, 1.0, gen) for o, i in shapes]
+        self.dx0 = [_rnd((n, i), dtype, 1.0, gen) for o, i in shapes]
+        self.shapes = shapes
+
+    def bind(self, dx=None):
+        up = lambda ts: [t.cuda() for t in ts]  # noqa: E731
+        self.dev = list(zip(up(self.x), up(self.A), up(self.B), [torch.zeros_like(t).cuda() for t in self.dy]))
+        self.ddy, self.ddx = up(self.dy), up(self.dx0) if dx is None else dx
+        self.dA = [torch.full(t.shape, 9.0, device="cuda") for t in self.A]
+        self.dB = [torch.full(t.shape, 9.0, device="cuda") for t in self.B]
+        self.dg = torch.full((self.T, 2), 9.0, device="cuda")
+        self.grp = dlm.SgmmGroup(self.dev, self.E, self.r, self.scale)
+        self.grp.bind_grads(self.ddy, self.ddx, self.dA, self.dB)
+        return self
+
+    def run(self, **kw):
+        ws = self.grp.backward(self.idx.cuda(), self.g.cuda(), self.dg, **kw)
+        torch.cuda.synchronize()
+        return ws
+
+    def refs(self):
+        T = self.T
+        return [ref.backward(x[:T], self.idx, self.g, A, B, dy[:T], self.scale)
+                for x, A, B, dy in zip(self.x, self.A, self.B, self.dy)]
+
+    def check(self, base=0.0):
+        bf = self.dtype == torch.bfloat16
+        split, u = (SPLIT, 2.0 ** -8) if bf else (0.0, 2.0 ** -24)
+        slots = max([int((self.idx == e).sum()) for e in range(self.E)])
+        dg = torch.zeros((self.T, 2), dtype=torch.float64)
+        dgm = torch.zeros_like(dg)
+        terms = 0
+        for p, ((o, i), (out, mag)) in enumerate(zip(self.shapes, self.refs())):
+            for name, got, want, m, n in (("dA", self.dA[p], out[1], mag[1], o), ("dB", self.dB[p], out[2], mag[2], i)):
+                got = got.cpu().double()
+                err = (got - base - want).abs()
+                tol = (gamma(n + 2 * slots + 8) + split) * m + 2.0 ** -23 * abs(base)
+                assert (err <= tol).all(), (name, p, float((err - tol).max()))
+                if base == 0.0 and want.norm() > 0 and want.numel() >= 256:
+                    assert err.norm() <= (2.0 ** -14 if bf else 2.0 ** -18) * want.norm(), (name, p)
+            if self.ddx[p] is not None:
+                want = self.dx0[p][:self.T].double() + out[0]
+                err = (self.ddx[p][:self.T].cpu().double() - want).abs()
+                tol = (gamma(o + 4 * self.r + 8) + split) * (mag[0] + self.dx0[p][:self.T].double().abs() * (1 - bf)) + u * want.abs()
+                assert (err <= tol + u * tol).all(), ("dx", p, float((err - tol).max()))
+                assert torch.equal(self.ddx[p][self.T:].cpu(), self.dx0[p][self.T:])
+                none = (self.idx < 0).all(1)
+                assert torch.equal(self.ddx[p][:self.T].cpu()[none], self.dx0[p][:self.T][none])
+            dg += out[3]
+            dgm += mag[3]
+            terms = max(terms, o + i)
+        err = (self.dg.cpu().double() - dg).abs()
+        assert (err <= gamma(terms + 2 * self.r + len(self.shapes) + 8) * dgm).all(), ("dg", float(err.max()))
+        assert (self.dg.cpu()[self.idx < 0] == 0).all()
+
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 31, 32, 33, 63, 64, 65, 200, 1000, 2500])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_every_length(T, dtype):
+    print(T, dtype, flush=True)
+    c = Case(T, [(136, 264)], 8, 16, dtype, seed=T).bind()
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("r", [1, 2, 3, 4, 7, 8, 12, 16, 17, 24, 31, 32, 40, 48, 63, 64, 65, 80, 96, 127, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_every_rank(r, dtype):
+    print(r, dtype, flush=True)
+    c = Case(70, [(72, 200)], 4, r, dtype, seed=r).bind()
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("E", [1, 2, 3, 16, 31, 32])
+@pytest.mark.parametrize("dup", [0.0, 1.0])
+def test_every_bank_size(E, dup):
+    """Up to 32 experts, with rows that name one expert twice."""
+    print(E, dup, flush=True)
+    c = Case(300, [(64, 128)], E, 16, BF, seed=E, dup=dup).bind()
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("o,i", [(8, 8), (8, 4096), (4104, 8), (2056, 1032), (128, 6152), (6152, 136), (1000, 120)])
+@pytest.mark.parametrize("r", [16, 64, 96])
+def test_shapes_bf16(o, i, r):
+    """One to four K slices on either side, widths that end inside a column block."""
+    print(o, i, r, flush=True)
+    c = Case(130, [(o, i)], 6, r, BF, seed=o + i).bind()
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("o,i", [(1, 1), (3, 5), (129, 257), (1000, 77)])
+def test_shapes_f32(o, i):
+    print(o, i, flush=True)
+    c = Case(41, [(o, i)], 3, 5, F32, seed=o + i).bind()
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype,r", [(BF, 16), (BF, 96), (F32, 6)])
+def test_groups(dtype, r):
+    """Seven projections of a layer's shapes (scaled down), one segmentation, dg over all of them."""
+    shapes = [(256, 256)] * 4 + [(688, 256)] * 2 + [(256, 688)]
+    c = Case(150, shapes, 8, r, dtype, seed=3).bind()
+    c.run()
+    c.check()
+
+
+def test_many_rows():
+    """Past the segmentation's one-launch limit, one expert chosen by most rows."""
+    print("rows 9000", flush=True)
+    c = Case(9000, [(64, 72)], 8, 8, BF, seed=4)
+    c.idx[:7000, 0] = 5
+    c.idx[:7000, 1] = torch.where(c.idx[:7000, 1] == 5, 6, c.idx[:7000, 1].long()).int()
+    c.bind()
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_without_experts(dtype):
+    """No row has a set: zero bank gradients, dx untouched, dg zero."""
+    c = Case(40, [(64, 64)], 4, 8, dtype)
+    c.idx[:] = -1
+    c.bind()
+    c.run()
+    c.check()
+    assert (c.dA[0] == 0).all() and (c.dB[0] == 0).all() and (c.dg == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_what_empty_rows_hold_does_not_matter(dtype):
+    """Infinities and NaN in rows without a set, and in rows behind T, reach nothing."""
+    c = Case(50, [(136, 128)], 4, 16, dtype, rows=64).bind()
+    none = (c.idx < 0).all(1)
+    assert none.any()
+    for t, d in ((c.x[0], c.dev[0][0]), (c.dy[0], c.ddy[0])):
+        t[:50][none] = float("nan")
+        t[50:] = float("inf")
+        d.copy_(t)
+        t[:50][none] = 0  # the plain form leaves these rows out by index, not by value
+    c.run(T=50)
+    c.check()
+
+
+def test_infinities_stay_with_their_expert():
+    """One row's infinite dy: only its experts' gradients and its own dx lose their values."""
+    c = Case(100, [(64, 64)], 8, 16, BF, empty=0.0, both=0.0).bind()
+    e = set(c.idx[17].tolist())
+    c.ddy[0][17, 3] = float("inf")
+    c.run()
+    for k in range(8):
+        assert torch.isfinite(c.dA[0][k]).all() == (k not in e)
+        assert torch.isfinite(c.dB[0][k]).all() == (k not in e)
+    fin = torch.isfinite(c.ddx[0]).all(1).cpu()
+    assert not fin[17] and fin[torch.arange(100) != 17].all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_accumulate(dtype):
+    c = Case(90, [(72, 136), (64, 64)], 5, 12, dtype).bind()
+    for t in c.dA + c.dB:
+        t.fill_(2.0)
+    c.run(accumulate=True)
+    c.check(base=2.0)
+
+
+def test_shared_dx_and_unwanted_dx():
+    """q, k, v of one x: the shares of one dx add up, each rounded once; a None entry is left out."""
+    gen = torch.Generator().manual_seed(1)
+    c = Case(80, [(64, 128), (32, 128), (64, 128), (128, 64)], 4, 16, BF)
+    c.x[1] = c.x[2] = c.x[0]
+    dx = _rnd((80, 128), BF, 1.0, gen)
+    dev = dx.cuda()
+    c.bind(dx=[dev, dev, dev, None])
+    c.run()
+    refs = c.refs()
+    want, tol = dx.double(), 0.0
+    for (o, i), (out, mag) in list(zip(c.shapes, refs))[:3]:
+        want = want + out[0]
+        tol = tol + (gamma(o + 4 * 16 + 8) + SPLIT) * mag[0] + 2.0 ** -8 * want.abs()
+    assert ((dev.cpu().double() - want).abs() <= tol * (1 + 3 * 2.0 ** -8)).all()
+    c.ddx = [None] * 4
+    c.check()
+
+
+def test_rows_behind_the_last_sequence():
+    """T smaller than the buffers: rows from T on are read and written nowhere."""
+    c = Case(33, [(64, 72)], 4, 16, BF, rows=70).bind()
+    c.run(T=33)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", ["index", "negative", "gate"])
+def test_rejected_sets_change_nothing(dtype, bad):
+    c = Case(60, [(64, 64)], 4, 8, dtype, empty=0.0, both=0.0).bind()
+    good_idx, good_g = c.idx.clone(), c.g.clone()
+    if bad == "index":
+        c.idx[7, 1] = 4
+    elif bad == "negative":
+        c.idx[7, 0] = -2
+    else:
+        c.g[7, 0] = float("nan")
+    ws = c.run()
+    assert dlm.sgmm_status(ws) == dlm.DLM_EDEVICE
+    assert (c.dA[0] == 9).all() and (c.dB[0] == 9).all() and (c.dg == 9).all()
+    assert torch.equal(c.ddx[0].cpu(), c.dx0[0])
+    c.idx, c.g = good_idx, good_g
+    ws = c.run()
+    assert dlm.sgmm_status(ws) == dlm.DLM_OK
+    c.check()
+
+
+def test_no_rows():
+    c = Case(16, [(64, 64)], 4, 8, BF).bind()
+    e = torch.empty((0, 2), device="cuda")
+    c.grp.backward(e.int(), e, accumulate=True)
+    torch.cuda.synchronize()
+    assert (c.dA[0] == 9).all()
+    c.grp.backward(e.int(), e)
+    torch.cuda.synchronize()
+    assert (c.dA[0] == 0).all() and (c.dB[0] == 0).all() and torch.equal(c.ddx[0].cpu(), c.dx0[0])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_same_bits_every_time_on_any_stream_and_replayed(dtype):
+    """Eager, on another stream, and replayed from a graph with eager work between the replays."""
+    c = Case(500, [(256, 136), (72, 2056)], 8, 16, dtype).bind()
+    idx, g = c.idx.cuda(), c.g.cuda()
+    ws = c.grp.backward_workspace(c.T)
+    outs = c.ddx + c.dA + c.dB + [c.dg]
+    c.grp.backward(idx, g, c.dg, workspace=ws)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+
+    def reset():
+        for t, d in zip(c.ddx, c.dx0):
+            t.copy_(d)
+        for t in c.dA + c.dB + [c.dg]:
+            t.fill_(float("nan"))
+        ws.fill_(0x5A)
+        torch.cuda.synchronize()
+
+    reset()
+    s = torch.cuda.Stream()
+    c.grp.backward(idx, g, c.dg, workspace=ws, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.grp.backward(idx, g, c.dg, workspace=ws)
+    for _ in range(3):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_reads_the_banks_as_they_are():
+    """Banks changed in place between calls (as an optimiser does): no repack is needed for the gradients."""
+    c = Case(70, [(64, 72)], 4, 16, BF).bind()
+    c.run()
+    for t, (x, A, B, y) in zip(range(1), c.dev):
+        A.mul_(-2.0)
+        B.add_(0.5)
+        c.A[0], c.B[0] = A.cpu(), B.cpu()
+    for t, d in zip(c.ddx, c.dx0):
+        t.copy_(d)
+    c.run()
+    c.check()
+
+
+def test_gradients_against_differences():
+    """Directional differences of the product in binary64 against the kernels' fp32 gradients: the
+    product is linear in x, g, A and B each, so a central difference has no truncation error, and
+    what is left is the gradients' own bound."""
+    c = Case(12, [(24, 40)], 3, 4, F32, seed=2).bind()
+    for t in c.ddx:
+        t.zero_()
+    c.run()
+    gen = torch.Generator().manual_seed(0)
+    x, A, B, g, dy = c.x[0].double(), c.A[0].double(), c.B[0].double(), c.g.double(), c.dy[0].double()
+    for which, grad in (("x", c.ddx[0]), ("A", c.dA[0]), ("B", c.dB[0]), ("g", c.dg)):
+        v = torch.randn(grad.shape, generator=gen).double()
+        f = lambda s: (ref.forward(x + s * v if which == "x" else x, c.idx, g + s * v if which == "g" else g,  # noqa: E731
+                                   A + s * v if which == "A" else A, B + s * v if which == "B" else B, c.scale) * dy).sum()
+        want = (f(0.5) - f(-0.5)).item()
+        got = (grad.cpu().double() * v).sum().item()
+        mag = (grad.cpu().double() * v).abs().sum().item()
+        assert abs(got - want) <= 2.0 ** -16 * mag
+
+
+def test_refusals_of_the_binding():
+    c = Case(16, [(64, 64), (64, 64)], 4, 8, BF).bind()
+    idx, g = c.idx.cuda(), c.g.cuda()
+    fresh = dlm.SgmmGroup(c.dev, 4, 8, 1.0)
+    with pytest.raises(dlm.DLMError):
+        fresh.backward(idx, g, workspace=c.grp.backward_workspace(16))
+    with pytest.raises(ValueError):
+        fresh.bind_grads(c.ddy[:1], c.ddx, c.dA, c.dB)
+    with pytest.raises(ValueError):
+        fresh.bind_grads(c.ddy, c.ddx, [t.bfloat16() for t in c.dA], c.dB)
+    with pytest.raises(ValueError):
+        fresh.bind_grads([t[:8] for t in c.ddy], c.ddx, c.dA, c.dB)
+    with pytest.raises(dlm.DLMError):
+        c.grp.backward(idx, g, workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        c.grp.backward(idx, g, T=17)
+    with pytest.raises(ValueError):
+        c.grp.backward(idx, g, torch.empty((15, 2), device="cuda"))
+    # a written buffer that is also read, or written twice
+    for bad in (dict(dys=c.ddy, dxs=[c.dev[0][0], None], dAs=c.dA, dBs=c.dB),
+                dict(dys=c.ddy, dxs=[c.ddy[0], None], dAs=c.dA, dBs=c.dB),
+                dict(dys=c.ddy, dxs=c.ddx, dAs=[c.dA[0], c.dA[0]], dBs=c.dB)):
+        fresh.bind_grads(**bad)
+        with pytest.raises(dlm.DLMError):
+            fresh.backward(idx, g, workspace=c.grp.backward_workspace(16))
