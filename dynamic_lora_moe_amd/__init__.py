@@ -82,7 +82,7 @@ def load(path: str = LIB_PATH):
         "dlm_pregate_centroid": ([P, P, I64, I64, I32, I32, I32, P, P, P], C.c_int),
         "dlm_route": ([P, I64, P, I64, I32, I32, P, P, P, P, P], C.c_int),
         "dlm_route_backward": ([P, I64, P, P, I64, I32, I32, P, P, I64, P], C.c_int),
-        "dlm_sgmm_backward_workspace_size": ([I64, I64, I32, I32, I32, P], C.c_int),
+        "dlm_sgmm_group_backward_workspace_size": ([P, I64, P], C.c_int),
         "dlm_sgmm_group_bind_grads": ([P, P, P, P, P], C.c_int),
         "dlm_sgmm_group_backward": ([P, P, P, P, I64, I32, P, C.c_size_t, P], C.c_int),
         "dlm_adamw_create": ([P, I32, I32, I32, I32, I64, C.c_uint32, P], C.c_int),
@@ -573,10 +573,10 @@ class SgmmGroup:
         self._grads = (dys, dxs, dAs, dBs)
 
     def backward_workspace(self, T: int):
-        d_max = max(max(x.shape[1], y.shape[1]) for x, _, _, y in self._keep)
+        """A workspace of backward() for T rows (once the buffers are bound)."""
         b = C.c_size_t(0)
-        _check(load().dlm_sgmm_backward_workspace_size(T, d_max, self.E, self.r, self.n, C.byref(b)),
-               "dlm_sgmm_backward_workspace_size")
+        _check(load().dlm_sgmm_group_backward_workspace_size(self._h, T, C.byref(b)),
+               "dlm_sgmm_group_backward_workspace_size")
         return torch.empty(b.value, dtype=torch.uint8, device=self.device)
 
     def backward(self, idx, g, dg=None, accumulate: bool = False, T: int | None = None, workspace=None, stream=None):

@@ -167,8 +167,6 @@ struct dlm_sgmm_group {
     struct Grads {
         char* d_tab = nullptr;   // device block: every table below
         char* d_pack = nullptr;  // the banks' transposes
-        const SgDesc* descs = nullptr;    // 2n shrink problems: (x, A), then (dy, B^T)
-        const SgDesc* ks_desc = nullptr;
         struct Wave {            // expands that run in one launch: no dx twice
             const SgDesc* descs;
             const SgDesc* cb_desc;
@@ -176,17 +174,27 @@ struct dlm_sgmm_group {
             int64_t total_cb, d_max;
             int32_t w_max;
         };
-        std::vector<Wave> waves;
-        const SgGrad* probs = nullptr;
+        // the tables that go by the shrink's K slice width: one set for
+        // kSgmmKSlice, one for kSgmmKSliceFew
+        struct Slices {
+            int32_t width = 0;
+            int64_t total_ks = 0;
+            const SgDesc* descs = nullptr;    // 2n shrink problems: (x, A), then (dy, B^T)
+            const SgDesc* ks_desc = nullptr;
+            std::vector<Wave> waves;
+            const SgGrad* probs = nullptr;
+        } slices[2];
         const SgOuter* outers = nullptr;
         const int32_t* unit_outer = nullptr;
         int32_t n_units = 0;
-        int64_t pk_total = 0, total_ks = 0, d_max = 0;
+        int64_t pk_total = 0;
         std::vector<const void*> dy;
         std::vector<void*> dx;
         std::vector<float*> dA, dB;
         int64_t checked_T = -1;
         bool bound = false;
+        // fp32 has one slice per side, whatever its width
+        const Slices& for_rows(int64_t T) const { return slices[slices[0].total_ks * ((T + 31) / 32) < kSgmmFewItems ? 1 : 0]; }
     } grads;
 };
 
@@ -686,6 +694,7 @@ int run_sgmm(const SgDesc* d_descs, const SgDesc* ks_desc, const SgDesc* cb_desc
              int32_t* status_out = nullptr) {
     SgmmArgs a;
     a.w_max = w_max;
+    a.kslice = kSgmmKSlice;
     a.status_out = status_out;
     a.inline_seg = 0;  // launch_sgmm decides
     a.descs = d_descs;
@@ -981,13 +990,20 @@ int dlm_sgmm_group_run(dlm_sgmm_group* h, const int32_t* idx, const float* g, in
 
 // ------------------------------------------------------- SGMM gradients ----
 
-int dlm_sgmm_backward_workspace_size(int64_t T, int64_t d_max, int32_t E, int32_t r, int32_t n_problems, size_t* bytes) {
-    if (!bytes) return fail(DLM_EINVAL, "sgmm_backward_workspace_size: bytes is null");
-    if (T < 0 || T > ((int64_t)1 << 29) || d_max < 1 || d_max > kMaxDim || E < 1 || E > DLM_MAX_EXPERTS || r < 1 ||
-        r > DLM_MAX_RANK || n_problems < 1 || n_problems > 65535)
-        return fail(DLM_ESHAPE, "sgmm_backward_workspace_size: T=%lld d_max=%lld E=%d r=%d n=%d", (long long)T,
-                    (long long)d_max, E, r, n_problems);
-    *bytes = sgmm_grad_layout(T, d_max, E, r, n_problems).total;
+static SgGradLayout grad_layout(const dlm_sgmm_group* h, int64_t T) {
+    const auto& G = h->grads;
+    return sgmm_grad_layout(T, G.for_rows(T).total_ks, h->E, h->r, h->n, G.n_units, h->dtype);
+}
+
+int dlm_sgmm_group_backward_workspace_size(const dlm_sgmm_group* h, int64_t T, size_t* bytes) {
+    if (!h || !bytes) return fail(DLM_EINVAL, "sgmm_group_backward_workspace_size: null argument");
+    if (!h->grads.bound) return fail(DLM_EINVAL, "sgmm_group_backward_workspace_size: no gradients are bound");
+    if (T < 0 || T > ((int64_t)1 << 29))
+        return fail(DLM_ESHAPE, "sgmm_group_backward_workspace_size: T=%lld", (long long)T);
+    // enough for fewer rows too: those that take the narrower K slices have more of them
+    const int64_t few = 32 * ((kSgmmFewItems - 1) / h->grads.slices[0].total_ks);
+    *bytes = grad_layout(h, T).total;
+    if (few > 0 && few < T) *bytes = std::max(*bytes, grad_layout(h, few).total);
     return ok();
 }
 
@@ -998,158 +1014,176 @@ int dlm_sgmm_group_bind_grads(dlm_sgmm_group* h, const void* const* dy, void* co
     const int n = h->n, E = h->E, r = h->r;
     const bool bf = h->dtype == DLM_BF16;
     const size_t es = esize(h->dtype);
+    if (n > 32767) return fail(DLM_ESHAPE, "sgmm_group_bind_grads: %d problems (at most 32767)", n);
     for (int i = 0; i < n; ++i) {
         if (!dy[i] || !dA[i] || !dB[i]) return fail(DLM_EINVAL, "sgmm_group_bind_grads: problem %d has a null pointer", i);
         const uintptr_t m = bf ? 15 : 3;
         if (((uintptr_t)dy[i] & m) || (dx && ((uintptr_t)dx[i] & m)) || ((uintptr_t)dA[i] & m) || ((uintptr_t)dB[i] & m))
             return fail(DLM_EALIGN, "sgmm_group_bind_grads: problem %d pointer not %d-byte aligned", i, (int)m + 1);
-        // a dx may be shared by problems of the same width; with any other d_in it would be another layout
-        for (int k = 0; dx && dx[i] && k < i; ++k)
-            if (dx[k] == dx[i] && h->h_descs[k].d_in != h->h_descs[i].d_in)
-                return fail(DLM_EINVAL, "sgmm_group_bind_grads: problems %d and %d share a dx but not their d_in", k, i);
     }
     dlm_sgmm_group::Grads G;
-    std::vector<char> tab;
-    size_t pack_bytes = 0;
+    hipError_t e = hipSuccess;
     try {
-        std::vector<SgDesc> descs(2 * (size_t)n);
-        std::vector<SgGrad> probs(n);
-        std::vector<SgOuter> outers(2 * (size_t)n);
-        std::vector<int> wave(n, -1);
-        std::map<void*, int> uses;
-        int n_waves = 0;
         auto a256 = [](size_t v) { return (v + 255) & ~(size_t)255; };
-        int64_t ks = 0, units = 0;
+        // per problem: the place of its dx in the order of the problems that share
+        // it, and its transposes' offsets
+        std::vector<int> wave(n, -1);
+        std::map<void*, std::pair<int, int>> uses;  // dx -> (d_in, problems so far)
+        int n_waves = 0;
+        std::vector<size_t> o_at(n), o_bt(n);
+        size_t pack_bytes = 0;
+        for (int i = 0; i < n; ++i) {
+            const SgDesc& p = h->h_descs[i];
+            o_at[i] = pack_bytes;
+            pack_bytes += a256((size_t)E * r * p.d_in * es);
+            o_bt[i] = pack_bytes;
+            pack_bytes += a256((size_t)E * r * p.d_out * es);
+            if (!dx || !dx[i]) continue;
+            auto it = uses.emplace(dx[i], std::make_pair(p.d_in, 0)).first;
+            if (it->second.first != p.d_in)  // with another width it would be another layout
+                return fail(DLM_EINVAL, "sgmm_group_bind_grads: problem %d shares a dx with one of another d_in", i);
+            wave[i] = it->second.second++;
+            n_waves = std::max(n_waves, wave[i] + 1);
+        }
+        // outer products: side 0 has x's columns, side 1 dy's
+        std::vector<SgOuter> outers(2 * (size_t)n);
+        int64_t units = 0;
+        const int cols = grad_cols(r, h->dtype);
         for (int i = 0; i < 2 * n; ++i) {
             const SgDesc& p = h->h_descs[i % n];
-            SgDesc& d = descs[i];
-            d = SgDesc{};
-            d.x = i < n ? p.x : dy[i - n];
-            d.d_in = i < n ? p.d_in : p.d_out;
-            d.n_ks = (d.d_in + kSgmmKSlice - 1) / kSgmmKSlice;
-            d.ks0 = ks;
-            ks += d.n_ks;
-            if (d.d_in > G.d_max) G.d_max = d.d_in;
-            // outer products: side 0 has x's columns, side 1 dy's
             SgOuter& o = outers[i];
             o = SgOuter{};
-            o.act = d.x;
+            o.act = i < n ? p.x : dy[i - n];
             o.out = i < n ? dA[i] : dB[i - n];
-            o.d = d.d_in;
+            o.d = i < n ? p.d_in : p.d_out;
             o.side = i < n ? 0 : 1;
             o.prob = i % n;
             o.unit0 = (int32_t)units;
-            units += (d.d_in + kGradCols - 1) / kGradCols;
+            units += (o.d + cols - 1) / cols;
+            if (units > ((int64_t)1 << 24)) return fail(DLM_ESHAPE, "sgmm_group_bind_grads: too many columns");
         }
-        if (units > ((int64_t)1 << 30)) return fail(DLM_ESHAPE, "sgmm_group_bind_grads: too many columns");
-        for (int i = 0; i < n; ++i) {
-            const SgDesc& p = h->h_descs[i];
-            SgGrad& q = probs[i];
-            q = SgGrad{};
-            q.A = p.A;
-            q.B = p.B;
-            q.Ap = const_cast<void*>(p.Ap);
-            q.At = (void*)pack_bytes;  // offsets until the block is allocated
-            pack_bytes += a256((size_t)E * r * p.d_in * es);
-            q.Bt = (void*)pack_bytes;
-            pack_bytes += a256((size_t)E * r * p.d_out * es);
-            q.d_in = p.d_in;
-            q.d_out = p.d_out;
-            q.pk0 = G.pk_total;
-            G.pk_total += (int64_t)E * r * (bf ? p.d_in / 8 + p.d_out / 8 : p.d_in + p.d_out);
-            q.ks_u = descs[i].ks0;
-            q.ks_w = descs[n + i].ks0;
-            // above kSgmmFoldRank the K-slice sum launch has added the slices; fp32 has one
-            const bool one = !bf || (r + 15) / 16 * 16 > kSgmmFoldRank;
-            q.n_ks_u = one ? 1 : descs[i].n_ks;
-            q.n_ks_w = one ? 1 : descs[n + i].n_ks;
-            if (dx && dx[i]) {
-                wave[i] = uses[dx[i]]++;
-                if (wave[i] + 1 > n_waves) n_waves = wave[i] + 1;
-            }
-        }
-        G.total_ks = ks;
         G.n_units = (int32_t)units;
-        hipError_t e = hipDeviceSynchronize();  // launches in flight read the current tables
-        if (e == hipSuccess) e = hipMalloc((void**)&G.d_pack, pack_bytes);
-        if (e != hipSuccess) return hip_fail(e, "sgmm_group_bind_grads");
-        for (int i = 0; i < n; ++i) {
-            probs[i].At = G.d_pack + (size_t)probs[i].At;
-            probs[i].Bt = G.d_pack + (size_t)probs[i].Bt;
-            descs[i].A = h->h_descs[i].A;
-            descs[i].Ap = h->h_descs[i].Ap;
-            descs[n + i].A = probs[i].Bt;
-            descs[n + i].Ap = probs[i].Bt;
-        }
-        size_t at = 0;
-        auto put = [&](const void* src, size_t bytes) {
-            const size_t o = at;
-            at = a256(at + bytes);
-            tab.resize(at);
-            std::memcpy(tab.data() + o, src, bytes);
-            return o;
-        };
-        auto owners = [](const std::vector<SgDesc>& v, bool cols) {
-            std::vector<SgDesc> o;
-            for (const SgDesc& d : v) o.insert(o.end(), cols ? d.n_cb : d.n_ks, d);
-            return o;
-        };
-        std::vector<SgDesc> own = owners(descs, false);
-        const size_t o_descs = put(descs.data(), sizeof(SgDesc) * descs.size());
-        const size_t o_ks = put(own.data(), sizeof(SgDesc) * own.size());
-        const size_t o_probs = put(probs.data(), sizeof(SgGrad) * n);
-        const size_t o_outers = put(outers.data(), sizeof(SgOuter) * outers.size());
-        std::vector<int32_t> uo(units);
+        std::vector<int32_t> unit_outer(units);
         for (int i = 0; i < 2 * n; ++i)
-            std::fill(uo.begin() + outers[i].unit0, i + 1 < 2 * n ? uo.begin() + outers[i + 1].unit0 : uo.end(), i);
-        const size_t o_units = put(uo.data(), sizeof(int32_t) * uo.size());
-        std::vector<std::pair<size_t, size_t>> o_waves;
-        for (int w = 0; w < n_waves; ++w) {
-            std::vector<SgDesc> v;
-            dlm_sgmm_group::Grads::Wave W{};
-            for (int i = 0; i < n; ++i) {
-                if (wave[i] != w) continue;
-                SgDesc d = descs[n + i];  // its K slices: w = B^T dy
-                d.B = probs[i].At;
-                d.y = dx[i];
-                d.d_out = h->h_descs[i].d_in;
-                d.n_cb = (d.d_out + kSgmmExpandCols - 1) / kSgmmExpandCols;
-                d.unit0 = W.total_cb;
-                W.total_cb += d.n_cb;
-                W.d_max = std::max<int64_t>(W.d_max, d.d_out);
-                W.w_max = std::max(W.w_max, d.n_ks + d.n_cb);
-                v.push_back(d);
-            }
-            W.n = (int32_t)v.size();
-            const std::vector<SgDesc> cb = owners(v, true);
-            o_waves.push_back({put(v.data(), sizeof(SgDesc) * v.size()), put(cb.data(), sizeof(SgDesc) * cb.size())});
-            G.waves.push_back(W);
-        }
-        e = hipMalloc((void**)&G.d_tab, tab.size());
-        if (e == hipSuccess) e = hipMemcpy(G.d_tab, tab.data(), tab.size(), hipMemcpyHostToDevice);
-        if (e != hipSuccess) {
-            if (G.d_tab) (void)hipFree(G.d_tab);
-            (void)hipFree(G.d_pack);
-            return hip_fail(e, "sgmm_group_bind_grads");
-        }
-        G.descs = (const SgDesc*)(G.d_tab + o_descs);
-        G.ks_desc = (const SgDesc*)(G.d_tab + o_ks);
-        G.probs = (const SgGrad*)(G.d_tab + o_probs);
-        G.outers = (const SgOuter*)(G.d_tab + o_outers);
-        G.unit_outer = (const int32_t*)(G.d_tab + o_units);
-        for (int w = 0; w < n_waves; ++w) {
-            G.waves[w].descs = (const SgDesc*)(G.d_tab + o_waves[w].first);
-            G.waves[w].cb_desc = (const SgDesc*)(G.d_tab + o_waves[w].second);
-        }
+            std::fill(unit_outer.begin() + outers[i].unit0,
+                      i + 1 < 2 * n ? unit_outer.begin() + outers[i + 1].unit0 : unit_outer.end(), i);
         G.dy.assign(dy, dy + n);
         G.dx.assign(n, nullptr);
         if (dx) G.dx.assign(dx, dx + n);
         G.dA.assign(dA, dA + n);
         G.dB.assign(dB, dB + n);
+
+        e = hipDeviceSynchronize();  // launches in flight read the current tables
+        if (e == hipSuccess) e = hipMalloc((void**)&G.d_pack, pack_bytes);
+        std::vector<char> tab;
+        auto put = [&](const void* src, size_t bytes) {
+            const size_t o = tab.size();
+            tab.resize(a256(o + bytes));
+            std::memcpy(tab.data() + o, src, bytes);
+            return o;
+        };
+        auto owners = [](const std::vector<SgDesc>& v, bool cb) {
+            std::vector<SgDesc> o;
+            for (const SgDesc& d : v) o.insert(o.end(), cb ? d.n_cb : d.n_ks, d);
+            return o;
+        };
+        const size_t o_outers = put(outers.data(), sizeof(SgOuter) * outers.size());
+        const size_t o_units = put(unit_outer.data(), sizeof(int32_t) * unit_outer.size());
+        size_t o_descs[2], o_ks[2], o_probs[2];
+        std::vector<std::pair<size_t, size_t>> o_waves[2];
+        for (int w2 = 0; w2 < 2 && e == hipSuccess; ++w2) {
+            auto& S = G.slices[w2];
+            S.width = w2 ? kSgmmKSliceFew : kSgmmKSlice;
+            std::vector<SgDesc> descs(2 * (size_t)n);
+            for (int i = 0; i < 2 * n; ++i) {
+                const SgDesc& p = h->h_descs[i % n];
+                SgDesc& d = descs[i];
+                d = SgDesc{};
+                d.x = i < n ? p.x : dy[i - n];
+                d.A = i < n ? p.A : G.d_pack + o_bt[i - n];
+                d.Ap = i < n ? p.Ap : G.d_pack + o_bt[i - n];
+                d.d_in = i < n ? p.d_in : p.d_out;
+                d.n_ks = bf ? (d.d_in + S.width - 1) / S.width : 1;
+                d.ks0 = S.total_ks;
+                S.total_ks += d.n_ks;
+            }
+            std::vector<SgGrad> probs(n);
+            int64_t pk = 0;
+            for (int i = 0; i < n; ++i) {
+                const SgDesc& p = h->h_descs[i];
+                SgGrad& q = probs[i];
+                q = SgGrad{};
+                q.A = p.A;
+                q.B = p.B;
+                q.x = p.x;
+                q.dy = dy[i];
+                q.Ap = const_cast<void*>(p.Ap);
+                q.At = G.d_pack + o_at[i];
+                q.Bt = G.d_pack + o_bt[i];
+                q.d_in = p.d_in;
+                q.d_out = p.d_out;
+                q.pk0 = pk;
+                pk += (int64_t)E * r * (bf ? p.d_in / 8 + p.d_out / 8 : p.d_in + p.d_out);
+                q.ks_u = descs[i].ks0;
+                q.ks_w = descs[n + i].ks0;
+                // above kSgmmFoldRank the K-slice sum launch has added the slices
+                const bool summed = (r + 15) / 16 * 16 > kSgmmFoldRank;
+                q.n_ks_u = summed ? 1 : descs[i].n_ks;
+                q.n_ks_w = summed ? 1 : descs[n + i].n_ks;
+            }
+            G.pk_total = pk;
+            const std::vector<SgDesc> ks = owners(descs, false);
+            o_descs[w2] = put(descs.data(), sizeof(SgDesc) * descs.size());
+            o_ks[w2] = put(ks.data(), sizeof(SgDesc) * ks.size());
+            o_probs[w2] = put(probs.data(), sizeof(SgGrad) * n);
+            for (int w = 0; w < n_waves; ++w) {
+                std::vector<SgDesc> v;
+                dlm_sgmm_group::Grads::Wave W{};
+                for (int i = 0; i < n; ++i) {
+                    if (wave[i] != w) continue;
+                    SgDesc d = descs[n + i];  // its K slices: w = B^T dy
+                    d.B = probs[i].At;
+                    d.y = dx[i];
+                    d.d_out = h->h_descs[i].d_in;
+                    d.n_cb = (d.d_out + kSgmmExpandCols - 1) / kSgmmExpandCols;
+                    d.unit0 = W.total_cb;
+                    W.total_cb += d.n_cb;
+                    W.d_max = std::max<int64_t>(W.d_max, d.d_out);
+                    W.w_max = std::max(W.w_max, d.n_ks + d.n_cb);
+                    v.push_back(d);
+                }
+                W.n = (int32_t)v.size();
+                const std::vector<SgDesc> cb = owners(v, true);
+                const size_t ow = put(v.data(), sizeof(SgDesc) * v.size());
+                o_waves[w2].push_back({ow, put(cb.data(), sizeof(SgDesc) * cb.size())});
+                S.waves.push_back(W);
+            }
+        }
+        if (e == hipSuccess) e = hipMalloc((void**)&G.d_tab, tab.size());
+        if (e == hipSuccess) e = hipMemcpy(G.d_tab, tab.data(), tab.size(), hipMemcpyHostToDevice);
+        if (e == hipSuccess) {
+            G.outers = (const SgOuter*)(G.d_tab + o_outers);
+            G.unit_outer = (const int32_t*)(G.d_tab + o_units);
+            for (int w2 = 0; w2 < 2; ++w2) {
+                auto& S = G.slices[w2];
+                S.descs = (const SgDesc*)(G.d_tab + o_descs[w2]);
+                S.ks_desc = (const SgDesc*)(G.d_tab + o_ks[w2]);
+                S.probs = (const SgGrad*)(G.d_tab + o_probs[w2]);
+                for (size_t w = 0; w < S.waves.size(); ++w) {
+                    S.waves[w].descs = (const SgDesc*)(G.d_tab + o_waves[w2][w].first);
+                    S.waves[w].cb_desc = (const SgDesc*)(G.d_tab + o_waves[w2][w].second);
+                }
+            }
+        }
     } catch (const std::bad_alloc&) {
         if (G.d_tab) (void)hipFree(G.d_tab);
         if (G.d_pack) (void)hipFree(G.d_pack);
         return fail(DLM_ENOMEM, "sgmm_group_bind_grads: host allocation failed");
+    }
+    if (e != hipSuccess) {
+        if (G.d_tab) (void)hipFree(G.d_tab);
+        if (G.d_pack) (void)hipFree(G.d_pack);
+        return hip_fail(e, "sgmm_group_bind_grads");
     }
     if (h->grads.d_tab) (void)hipFree(h->grads.d_tab);
     if (h->grads.d_pack) (void)hipFree(h->grads.d_pack);
@@ -1165,8 +1199,10 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
     if (!G.bound) return fail(DLM_EINVAL, "sgmm_group_backward: no gradients are bound");
     if (T < 0 || T > ((int64_t)1 << 29)) return fail(DLM_ESHAPE, "sgmm_group_backward: T=%lld", (long long)T);
     hipStream_t s = (hipStream_t)stream;
+    const auto& S = G.for_rows(T);
+    const bool bf = h->dtype == DLM_BF16;
     SgGradArgs b{};
-    b.probs = G.probs;
+    b.probs = S.probs;
     b.outers = G.outers;
     b.unit_outer = G.unit_outer;
     b.n_prob = h->n;
@@ -1178,13 +1214,13 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
     b.accumulate = accumulate ? 1 : 0;
     if (T == 0) {
         if (accumulate) return ok();
-        const hipError_t e = launch_grad_zero(b, s);
+        const hipError_t e = launch_grad_zero(b, h->dtype, s);
         return e == hipSuccess ? ok() : hip_fail(e, "sgmm_group_backward");
     }
     if (!idx || !g) return fail(DLM_EINVAL, "sgmm_group_backward: idx or g is null");
     if (!workspace) return fail(DLM_EWORKSPACE, "sgmm_group_backward: workspace is null");
     if (((uintptr_t)workspace & 255u) != 0) return fail(DLM_EALIGN, "sgmm_group_backward: workspace not 256-byte aligned");
-    const SgGradLayout L = sgmm_grad_layout(T, G.d_max, h->E, h->r, h->n);
+    const SgGradLayout L = grad_layout(h, T);
     if (ws_bytes < L.total)
         return fail(DLM_EWORKSPACE, "sgmm_group_backward: workspace %zu bytes < %zu needed", ws_bytes, L.total);
     try {
@@ -1193,6 +1229,7 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
         const size_t es = esize(h->dtype);
         const int64_t Tc = T > G.checked_T ? T : G.checked_T;
         std::vector<Span> v;
+        std::map<void*, int> seen;
         for (int i = 0; i < h->n; ++i) {
             const SgDesc& d = h->h_descs[i];
             const size_t na = (size_t)h->E * h->r * d.d_in, nb = (size_t)h->E * h->r * d.d_out;
@@ -1202,7 +1239,7 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
             v.push_back(span(d.B, nb * es, false, "problem B", i));
             v.push_back(span(G.dA[i], na * 4, true, "problem dA", i));
             v.push_back(span(G.dB[i], nb * 4, true, "problem dB", i));
-            if (G.dx[i] && std::find(G.dx.begin(), G.dx.begin() + i, G.dx[i]) == G.dx.begin() + i)
+            if (G.dx[i] && seen.emplace(G.dx[i], i).second)
                 v.push_back(span(G.dx[i], (size_t)Tc * d.d_in * es, true, "problem dx", i));
         }
         if (T > G.checked_T) {
@@ -1222,11 +1259,12 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
         return fail(DLM_ENOMEM, "sgmm_group_backward: host allocation failed");
     }
     SgmmArgs a{};
-    a.descs = G.descs;
-    a.ks_desc = G.ks_desc;
-    a.packed = h->dtype == DLM_BF16 ? 1 : 0;
+    a.descs = S.descs;
+    a.ks_desc = S.ks_desc;
+    a.packed = bf ? 1 : 0;
     a.n_prob = 2 * h->n;
-    a.total_ks = G.total_ks;
+    a.total_ks = S.total_ks;
+    a.kslice = S.width;
     a.idx = idx;
     a.g = g;
     a.T = T;
@@ -1240,34 +1278,27 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
     b.ws = (char*)workspace;
     b.G = L;
     b.dg = dg;
-    std::vector<SgmmArgs> ex;
-    try {
-        for (const auto& w : G.waves) {
-            SgmmArgs x = a;
-            x.descs = w.descs;
-            x.cb_desc = w.cb_desc;
-            x.ks_desc = nullptr;
-            x.n_prob = w.n;
-            x.total_cb = w.total_cb;
-            x.n_expand_units = L.L.tiles_max * w.total_cb;
-            x.d_out_max = w.d_max;
-            x.w_max = w.w_max;
-            x.total_ks = 0;
-            ex.push_back(x);
-        }
-    } catch (const std::bad_alloc&) {
-        return fail(DLM_ENOMEM, "sgmm_group_backward: host allocation failed");
-    }
+    auto expand_args = [&](const dlm_sgmm_group::Grads::Wave& w) {
+        SgmmArgs x = a;
+        x.descs = w.descs;
+        x.cb_desc = w.cb_desc;
+        x.ks_desc = nullptr;
+        x.n_prob = w.n;
+        x.total_cb = w.total_cb;
+        x.n_expand_units = L.L.tiles_max * w.total_cb;
+        x.d_out_max = w.d_max;
+        x.w_max = w.w_max;
+        x.total_ks = 0;
+        return x;
+    };
     bool fits = sgmm_grad_fits(b, h->dtype) && sgmm_launches_fit(a, h->dtype);
-    for (const SgmmArgs& x : ex) fits = fits && sgmm_launches_fit(x, h->dtype);
+    for (const auto& w : S.waves) fits = fits && sgmm_launches_fit(expand_args(w), h->dtype);
     if (!fits) return hip_fail(hipErrorInvalidConfiguration, "sgmm_group_backward");
-    hipError_t e = launch_grad_pack(b, h->dtype, s);
-    if (e == hipSuccess) e = launch_sgmm_segment(a, s);
-    if (e == hipSuccess) e = launch_sgmm_shrink(a, h->dtype, s);
-    if (e == hipSuccess) e = launch_grad_lists(b, s);
+    hipError_t e = launch_grad_prep(b, g, h->dtype, s);
+    if (e == hipSuccess) e = bf ? launch_sgmm_shrink(a, s) : launch_grad_shrink_f32(b, s);
     if (e == hipSuccess) e = launch_grad_coefs(b, h->dtype, s);
-    for (const SgmmArgs& x : ex)
-        if (e == hipSuccess) e = launch_sgmm_expand(x, h->dtype, s);
+    for (const auto& w : S.waves)
+        if (e == hipSuccess) e = launch_sgmm_expand(expand_args(w), h->dtype, s);
     if (e == hipSuccess) e = launch_grad_outer(b, h->dtype, s);
     if (e != hipSuccess) return hip_fail(e, "sgmm_group_backward");
     return ok();

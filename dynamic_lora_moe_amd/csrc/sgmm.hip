@@ -248,12 +248,69 @@ __global__ __launch_bounds__(kSegThreads) void sgmm_seg_count(const int32_t* __r
     if (tid == 0) cerr[chunk] = s_err;
 }
 
-__global__ __launch_bounds__(kSegThreads) void sgmm_seg_place(const int32_t* __restrict__ idx,
-                                                              const float* __restrict__ g, int64_t T, int E,
-                                                              char* ws, SgLayout L, int32_t* status_out,
-                                                              const SgDesc* __restrict__ descs, SgDesc single,
-                                                              int32_t n_prob, int64_t total_ks, int64_t total_cb,
-                                                              int32_t fused) {
+// The gradients' lists, from the keys' totals (all threads of a placing
+// workgroup): an expert's list runs over its keys in ascending order -- (x, e)
+// for x <= e, then (e, y) -- so a key's rows start at the sum of the totals
+// before it: oa / ob for its smaller / larger expert (a key (e, e) holds two
+// slots a row).  The first workgroup writes the starts and the chunks.
+__device__ __forceinline__ void lists_place(const int* s_tot, int* s_oa, int* s_ob, int* s_off, int* s_num, int E,
+                                            bool first, const SgLists& lists) {
+    const int tid = threadIdx.x;
+    if (tid < E) {
+        const int e = tid;
+        int n = 0;
+        for (int x = -1; x < e; ++x) {
+            const int k = (x + 1) * (E + 1) + e + 1;
+            s_ob[k] = n;
+            n += s_tot[k];
+        }
+        for (int y = e; y < E; ++y) {
+            const int k = (e + 1) * (E + 1) + y + 1;
+            s_oa[k] = n;
+            n += y == e ? 2 * s_tot[k] : s_tot[k];
+        }
+        s_num[e] = n;
+    }
+    __syncthreads();
+    if (tid < E) {
+        int off = 0, c0 = 0;
+        for (int x = 0; x < tid; ++x) {
+            const int tiles = (s_num[x] + kGradTile - 1) / kGradTile;
+            off += tiles * kGradTile;
+            c0 += tiles > 0 ? (tiles + lists.chunk_tiles - 1) / lists.chunk_tiles : 1;
+        }
+        s_off[tid] = off;
+        if (first) {
+            const int t0 = off / kGradTile, tiles = (s_num[tid] + kGradTile - 1) / kGradTile;
+            const int nc = tiles > 0 ? (tiles + lists.chunk_tiles - 1) / lists.chunk_tiles : 1;
+            gst(lists.eoff + tid, off);
+            gst(lists.echunk + tid, c0);
+            // the tiles are shared out evenly
+            for (int c = 0; c < nc; ++c) {
+                SgChunk q;
+                q.e = tid;
+                q.t0 = t0 + (int)((int64_t)tiles * c / nc);
+                q.t1 = t0 + (int)((int64_t)tiles * (c + 1) / nc);
+                q.alone = nc == 1;
+                lists.chunk[c0 + c] = q;
+            }
+            if (tid == E - 1) {
+                gst(lists.eoff + E, off + tiles * kGradTile);
+                gst(lists.echunk + E, c0 + nc);
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// One placing workgroup (chunk of n_chunks).  LISTS: also writes every expert's
+// slot list for the gradients (see SgLists).
+template <bool LISTS>
+__device__ __forceinline__ void seg_place(const int32_t* __restrict__ idx, const float* __restrict__ g, int64_t T, int E,
+                                          char* ws, const SgLayout& L, int32_t* status_out,
+                                          const SgDesc* __restrict__ descs, const SgDesc& single, int32_t n_prob,
+                                          int64_t total_ks, int64_t total_cb, int32_t fused, int64_t chunk,
+                                          int64_t n_chunks, const SgLists& lists) {
     int32_t* hdr = (int32_t*)(ws + L.hdr);
     int32_t* perm = (int32_t*)(ws + L.perm);
     uint32_t* epk = (uint32_t*)(ws + L.epk);
@@ -265,10 +322,13 @@ __global__ __launch_bounds__(kSegThreads) void sgmm_seg_place(const int32_t* __r
     __shared__ int s_base[kMaxKeys];   // the key's first position, then this chunk's first
     __shared__ uint16_t s_wc[kSegWaves][kMaxKeys];  // per-wave counts, then their prefix over waves
     __shared__ int s_sum[kSegWaves];
+    // LISTS: each key's rows in earlier chunks, its rows' first places in the
+    // lists of its smaller and larger expert, every list's start and length
+    constexpr int kLK = LISTS ? kMaxKeys : 1;
+    __shared__ int s_rel[kLK], s_oa[kLK], s_ob[kLK], s_off[32], s_num[32];
     const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
     const int nk = (E + 1) * (E + 1);
     const int nbits = 32 - __builtin_clz((unsigned)(nk - 1));
-    const int64_t chunk = blockIdx.x, n_chunks = gridDim.x;
     const int64_t t = chunk * kSegThreads + tid;
     const SegRaw raw = seg_load(idx, g, t, T);  // first needed when the row is placed
     if (tid == 0) s_err = 0;
@@ -340,10 +400,16 @@ __global__ __launch_bounds__(kSegThreads) void sgmm_seg_place(const int32_t* __r
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const int k = tid * kPer + j;
-        if (k < nk) s_base[k] += start;
+        if (k < nk) {
+            if constexpr (LISTS) s_rel[k] = s_base[k];
+            s_base[k] += start;
+        }
         start += cnt[j];
     }
     if (err) n_pos = 0;
+    if constexpr (LISTS) {
+        if (!err) lists_place(s_tot, s_oa, s_ob, s_off, s_num, E, chunk == 0, lists);
+    }
 
     if (!err) {
         const SegRow cur = seg_row(raw, t < T, E);
@@ -369,6 +435,23 @@ __global__ __launch_bounds__(kSegThreads) void sgmm_seg_place(const int32_t* __r
             epk[p] = ((uint32_t)cur.e0 & 0xffffu) | ((uint32_t)cur.e1 << 16);
             gpk[2 * p] = cur.e0 >= 0 ? cur.g0 : 0.f;
             gpk[2 * p + 1] = cur.e1 >= 0 ? cur.g1 : 0.f;
+            if constexpr (LISTS) {
+                const int rel = s_rel[k] + s_wc[w][k] + rk;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int e = j ? cur.e1 : cur.e0, o = j ? cur.e0 : cur.e1;
+                    if (e < 0) continue;
+                    const int at = e == o ? s_oa[k] + 2 * rel + j : (e < o ? s_oa[k] : s_ob[k]) + rel;
+                    gst(lists.slot + s_off[e] + at, (int32_t)(2 * p + j));
+                    gst(lists.srow + s_off[e] + at, (int32_t)t);
+                    if (at == s_num[e] - 1) {  // the list's last slot fills up its last tile
+                        for (int q = at + 1; q % kGradTile != 0; ++q) {
+                            gst(lists.slot + s_off[e] + q, -1);
+                            gst(lists.srow + s_off[e] + q, (int32_t)t);
+                        }
+                    }
+                }
+            }
         }
     }
     // positions past the live rows, split over the workgroups
@@ -386,6 +469,78 @@ __global__ __launch_bounds__(kSegThreads) void sgmm_seg_place(const int32_t* __r
     }
     if (fused && chunk == 0) sgmm_fused_ranges(ws, L, descs, single, n_prob, total_ks, total_cb,
                                                err ? 0 : (n_pos + 31) / 32);
+}
+
+__global__ __launch_bounds__(kSegThreads) void sgmm_seg_place(const int32_t* __restrict__ idx,
+                                                              const float* __restrict__ g, int64_t T, int E,
+                                                              char* ws, SgLayout L, int32_t* status_out,
+                                                              const SgDesc* __restrict__ descs, SgDesc single,
+                                                              int32_t n_prob, int64_t total_ks, int64_t total_cb,
+                                                              int32_t fused) {
+    seg_place<false>(idx, g, T, E, ws, L, status_out, descs, single, n_prob, total_ks, total_cb, fused, blockIdx.x,
+                     gridDim.x, SgLists{});
+}
+
+// The gradients' first launch: the segmentation with the lists (the first
+// workgroups), and the banks' transposes (the rest), which need none of it.
+template <bool BF>
+__global__ __launch_bounds__(kSegThreads) void grad_prep(SgGradArgs a, const float* __restrict__ g, int64_t n_chunks) {
+    if (blockIdx.x < n_chunks) {
+        SgLists l;
+        l.eoff = (int32_t*)(a.ws + a.G.eoff);
+        l.slot = (int32_t*)(a.ws + a.G.slot);
+        l.srow = (int32_t*)(a.ws + a.G.srow);
+        l.chunk = (SgChunk*)(a.ws + a.G.chunk);
+        l.echunk = (int32_t*)(a.ws + a.G.echunk);
+        l.chunk_tiles = a.G.chunk_tiles;
+        seg_place<true>(a.idx, g, a.T, a.E, a.ws, a.G.L, nullptr, nullptr, SgDesc{}, 0, 0, 0, 0, blockIdx.x, n_chunks, l);
+        return;
+    }
+    const int64_t q = (int64_t)(blockIdx.x - n_chunks) * kSegThreads + threadIdx.x;
+    if (q >= a.pk_total) return;
+    int p = 0;
+    for (int lo = 0, hi = a.n_prob - 1; lo <= hi;) {  // the last projection that starts at or before q
+        const int mid = (lo + hi) / 2;
+        if (a.probs[mid].pk0 <= q) p = mid, lo = mid + 1;
+        else hi = mid - 1;
+    }
+    const SgGrad P = a.probs[p];
+    const int r = a.r;
+    if constexpr (BF) {
+        // one thread per eight elements of A (then of B).  A: eight columns of one
+        // rank row, written as the packed group the shrink reads and as eight
+        // elements of the transpose; B: element [e][o][rho] of eight consecutive o.
+        const int64_t i = q - P.pk0, na = (int64_t)a.E * r * (P.d_in / 8);
+        if (i < na) {
+            const int64_t nq = P.d_in / 8, rho = i % r, kq = (i / r) % nq, e = i / (r * nq);
+            const u32x4 v = ld128((const uint16_t*)P.A + ((e * r + rho) * nq + kq) * 8);
+            st128((uint16_t*)P.Ap + 8 * i, v);
+            uint16_t* t = (uint16_t*)P.At + (e * P.d_in + 8 * kq) * r + rho;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                gst(t + (2 * j) * r, (uint16_t)(v[j] & 0xffffu));
+                gst(t + (2 * j + 1) * r, (uint16_t)(v[j] >> 16));
+            }
+        } else {
+            const int64_t b = i - na, nq = P.d_out / 8, rho = b % r, kq = (b / r) % nq, e = b / (r * nq);
+            const uint16_t* src = (const uint16_t*)P.B + (e * P.d_out + 8 * kq) * r + rho;
+            u32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = (uint32_t)gld(src + (2 * j) * r) | ((uint32_t)gld(src + (2 * j + 1) * r) << 16);
+            st128((uint16_t*)P.Bt + 8 * b, v);
+        }
+    } else {
+        // one thread per element; At [E][d_in][r], Bt [E][r][d_out]
+        const int64_t i = q - P.pk0, na = (int64_t)a.E * r * P.d_in;
+        if (i < na) {
+            const int64_t rho = i % r, j = (i / r) % P.d_in, e = i / ((int64_t)r * P.d_in);
+            gst((float*)P.At + i, gld((const float*)P.A + (e * r + rho) * P.d_in + j));
+        } else {
+            const int64_t b = i - na, o = b % P.d_out, rho = (b / P.d_out) % r, e = b / ((int64_t)r * P.d_out);
+            gst((float*)P.Bt + b, gld((const float*)P.B + (e * P.d_out + o) * r + rho));
+        }
+    }
 }
 
 // With at most kWave rows the shrink and expand workgroups order the rows
@@ -449,11 +604,11 @@ __device__ __forceinline__ int mask_list(uint32_t m, int* out) {
 constexpr int kXRows = 32;
 // K is staged through LDS in kShrinkStep-wide steps: 64-wide K chunks of one
 // step, and 16-byte chunks of one x row of a step.  A work item covers one
-// kSgmmKSlice-wide slice, i.e. kShrinkSteps steps, with its accumulators held
-// in registers across them.
+// slice of a.kslice (kSgmmKSlice; kSgmmKSliceFew for the gradients of few
+// rows), a whole number of steps, with its accumulators held in registers
+// across them.
 constexpr int kShrinkStep = 512;
-constexpr int kShrinkSteps = kSgmmKSlice / kShrinkStep;
-static_assert(kSgmmKSlice % kShrinkStep == 0, "a slice is a whole number of steps");
+static_assert(kSgmmKSlice % kShrinkStep == 0 && kSgmmKSliceFew % kShrinkStep == 0, "a slice is a whole number of steps");
 constexpr int kKC = kShrinkStep / 64;
 constexpr int kXC = kShrinkStep / 8;
 // A chunks in flight per wave in the shrink's K loop.  The shrink runs at 4
@@ -511,7 +666,7 @@ __device__ __forceinline__ void shrink_item(const SgmmArgs& a, int64_t gks, int 
                                             int32_t* dep = nullptr) {
     constexpr int RPAD = R16 * 16;
     const SgDesc D = a.descs ? a.ks_desc[gks] : a.single;
-    const int k0 = (int)(gks - D.ks0) * kSgmmKSlice;
+    const int k0 = (int)(gks - D.ks0) * a.kslice;
     const int32_t* perm = (const int32_t*)(a.ws + a.L.perm);
     const uint32_t* epk = (const uint32_t*)(a.ws + a.L.epk);
     float* v = (float*)(a.ws + a.L.v) + gks * a.L.T_pad * 2 * RPAD;
@@ -546,8 +701,8 @@ __device__ __forceinline__ void shrink_item(const SgmmArgs& a, int64_t gks, int 
     const uint16_t* __restrict__ x = (const uint16_t*)D.x;
     const uint16_t* __restrict__ A = (const uint16_t*)(PK ? D.Ap : D.A);
     // steps of this slice inside d_in (the same for every wave)
-    const int n_steps = (d_in - k0 + kShrinkStep - 1) / kShrinkStep < kShrinkSteps
-                            ? (d_in - k0 + kShrinkStep - 1) / kShrinkStep : kShrinkSteps;
+    const int n_left = (d_in - k0 + kShrinkStep - 1) / kShrinkStep, n_full = a.kslice / kShrinkStep;
+    const int n_steps = n_left < n_full ? n_left : n_full;
 
     // x step: thread tid reads chunk tid % kXC of rows tid / kXC + kXR j
     constexpr int kXR = 256 / kXC;           // rows per load instruction
@@ -1729,13 +1884,23 @@ hipError_t launch_sgmm(const SgmmArgs& a, int dtype, hipStream_t s) {
     return launch_expand_generic(a, s);
 }
 
-hipError_t launch_sgmm_segment(const SgmmArgs& a, hipStream_t s) {
-    if (!grid_fits(a.L.n_chunks, kSegThreads)) return hipErrorInvalidConfiguration;
-    return launch_segment(a, 0, s);
+bool grad_prep_fits(const SgGradArgs& a) {
+    return grid_fits(a.G.L.n_chunks + (a.pk_total + kSegThreads - 1) / kSegThreads, kSegThreads);
 }
-hipError_t launch_sgmm_shrink(const SgmmArgs& a, int dtype, hipStream_t s) {
-    return dtype == 1 ? launch_mfma_r(a, s, true, false) : launch_shrink_generic(a, s);
+hipError_t launch_grad_prep(const SgGradArgs& a, const float* g, int dtype, hipStream_t s) {
+    const int64_t n_chunks = a.G.L.n_chunks;
+    if (n_chunks > kSegFewChunks) {
+        hipLaunchKernelGGL(sgmm_seg_count, dim3((unsigned)n_chunks), dim3(kSegThreads), 0, s, a.idx, g, a.T, a.E, a.ws,
+                           a.G.L);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const dim3 n((unsigned)(n_chunks + (a.pk_total + kSegThreads - 1) / kSegThreads));
+    if (dtype == 1) hipLaunchKernelGGL(grad_prep<true>, n, dim3(kSegThreads), 0, s, a, g, n_chunks);
+    else hipLaunchKernelGGL(grad_prep<false>, n, dim3(kSegThreads), 0, s, a, g, n_chunks);
+    return hipGetLastError();
 }
+hipError_t launch_sgmm_shrink(const SgmmArgs& a, hipStream_t s) { return launch_mfma_r(a, s, true, false); }
 hipError_t launch_sgmm_expand(const SgmmArgs& a, int dtype, hipStream_t s) {
     return dtype == 1 ? launch_mfma_r(a, s, false, true) : launch_expand_generic(a, s);
 }

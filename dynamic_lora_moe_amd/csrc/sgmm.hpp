@@ -38,6 +38,11 @@ struct SgLayout {
 // Width of one shrink K slice (one work item; its fp32 partial v is summed
 // with the other slices' afterwards).
 constexpr int kSgmmKSlice = 2048;
+// The gradients take narrower slices while kSgmmKSlice would leave fewer than
+// kSgmmFewItems shrink items, one per CU: 256 rows of a 4096 x 4096 projection
+// make 32 items of 18 us, or 128 of 7.
+constexpr int kSgmmKSliceFew = 512;
+constexpr int kSgmmFewItems = 256;
 // Up to this rank the expand adds a tile's K-slice partials itself; above it a
 // K-slice sum launch runs between the shrink and the expand.
 constexpr int kSgmmFoldRank = 64;
@@ -102,36 +107,53 @@ struct SgmmArgs {
     int32_t* status_out;   // device word that also receives the set-validity flag, or nullptr
     int32_t inline_seg;    // 1: the shrink and expand order the rows themselves (launch_sgmm sets it)
     int32_t w_max;         // largest K slices + column groups of one problem
+    int32_t kslice;        // K slice width of the shrink (the owners' n_ks goes by it)
 };
 
 hipError_t launch_sgmm(const SgmmArgs& a, int dtype, hipStream_t s);
 // Ap[e][k / 8][rho][0..8) = A[e][rho][k..k+8) for k = 0, 8, ..., d_in - 8 (bf16).
 hipError_t launch_sgmm_pack_a(const void* A, void* Ap, int E, int r, int64_t d_in, hipStream_t s);
 
-// The steps of an SGMM one by one (the gradients run other work between them):
-// the segmentation into the workspace, the shrink of every problem of a
-// segmented batch (with its K-slice sum above kSgmmFoldRank), and the expand of
-// a set of problems, whose v (ks0, n_ks) a shrink has left in the workspace.
-hipError_t launch_sgmm_segment(const SgmmArgs& a, hipStream_t s);
-hipError_t launch_sgmm_shrink(const SgmmArgs& a, int dtype, hipStream_t s);
+// The shrink of every problem of a segmented batch (bf16; with its K-slice sum
+// above kSgmmFoldRank), and the expand of a set of problems whose v (ks0, n_ks)
+// a shrink has left in the workspace: the gradients run other work between them.
+hipError_t launch_sgmm_shrink(const SgmmArgs& a, hipStream_t s);
 hipError_t launch_sgmm_expand(const SgmmArgs& a, int dtype, hipStream_t s);
 bool sgmm_launches_fit(const SgmmArgs& a, int dtype);
 
 // ---- gradients ----------------------------------------------------------------
 
-// Columns of one item of the banks' gradients, slots of one list tile.
-constexpr int kGradCols = 128;
+// Slots of one list tile.
 constexpr int kGradTile = 32;
+
+// A run of one expert's list tiles: what one workgroup of the outer products sums.
+struct SgChunk {
+    int32_t e, t0, t1;  // tiles [t0, t1)
+    int32_t alone;      // the expert's only chunk
+};
+// The experts' slot lists as the segmentation writes them: every expert's slots
+// in sorted-position order, padded to whole tiles (a padding slot repeats a row
+// of its expert), the lists one after another, and their chunks.
+struct SgLists {
+    int32_t* eoff;    // [E + 1] first list position
+    int32_t* slot;    // 2 * position + k, or -1 (padding)
+    int32_t* srow;    // the slot's row
+    SgChunk* chunk;
+    int32_t* echunk;  // [E + 1] first chunk
+    int32_t chunk_tiles;  // most tiles of a chunk
+};
 
 // One projection and its gradients in the device table.
 struct SgGrad {
     const void* A;   // [E][r][d_in]
     const void* B;   // [E][d_out][r]
+    const void* x;   // [T][d_in]
+    const void* dy;  // [T][d_out]
     void* Ap;        // A packed for the shrink (bf16), else unused
     void* At;        // [E][d_in][r]: A transposed, the dx expand's up matrix
     void* Bt;        // B transposed: [E][d_out / 8][r][8] (bf16) or [E][r][d_out] (fp32)
     int32_t d_in, d_out;
-    int64_t pk0;     // first 8-element group of this projection's banks (prefix sum over A and B)
+    int64_t pk0;     // first group (bf16: 8 elements, fp32: one) of its banks (prefix sum)
     int64_t ks_u, ks_w;      // first K slice of u = A x and of w = B^T dy in the workspace's v
     int32_t n_ks_u, n_ks_w;  // and how many there are to add
 };
@@ -144,20 +166,22 @@ struct SgOuter {
     int32_t prob;
     int32_t unit0;    // first column block (prefix sum)
 };
+// Columns of one column block of the outer products.
+int grad_cols(int r, int dtype);
 
-// Workspace of a backward call: the SGMM's for twice the problems, then these.
+// Workspace of a backward call.
 struct SgGradLayout {
-    SgLayout L;
-    size_t eoff;   // [E + 1] first list position of every expert (multiples of kGradTile)
-    size_t slot;   // [cap] 2 * position + k, or -1 (padding)
-    size_t srow;   // [cap] the row
-    size_t coef;   // [prob][side][hi, lo][cap / kGradTile][rc_pad][kGradTile] bf16
-    size_t dgp;    // [prob][T][2] fp32
+    SgLayout L;     // a segmented SGMM's, its v for every K slice of both sides
+    size_t eoff, slot, srow, chunk, echunk;  // the lists (SgLists)
+    size_t coef;    // coefficients: bf16 [prob][side][3 terms][list tile][rc_pad][kGradTile], fp32 [prob][side][list tile][r_pad][kGradTile]
+    size_t part;    // [unit][rank chunk][chunk] partial sums of experts with several chunks (bf16)
+    size_t dgp;     // [prob][T][2] fp32
     size_t total;
-    int64_t cap;   // list positions at most
-    int rc_pad;    // ranks of a coefficient tile
+    int64_t cap;    // list positions at most
+    int chunk_tiles, max_chunks;
+    int rc_pad;     // ranks of a coefficient tile (bf16)
 };
-SgGradLayout sgmm_grad_layout(int64_t T, int64_t d_max, int E, int r, int n_prob);
+SgGradLayout sgmm_grad_layout(int64_t T, int64_t total_ks, int E, int r, int n_prob, int n_units, int dtype);
 
 struct SgGradArgs {
     const SgGrad* probs;
@@ -175,10 +199,13 @@ struct SgGradArgs {
     int32_t accumulate;  // add to dA and dB instead of writing them
 };
 // T = 0: the gradients of no rows.
-hipError_t launch_grad_zero(const SgGradArgs& a, hipStream_t s);
-hipError_t launch_grad_pack(const SgGradArgs& a, int dtype, hipStream_t s);
-hipError_t launch_grad_lists(const SgGradArgs& a, hipStream_t s);
+hipError_t launch_grad_zero(const SgGradArgs& a, int dtype, hipStream_t s);
+// Segmentation, lists and the banks' transposes.
+bool grad_prep_fits(const SgGradArgs& a);
+hipError_t launch_grad_prep(const SgGradArgs& a, const float* g, int dtype, hipStream_t s);
+hipError_t launch_grad_shrink_f32(const SgGradArgs& a, hipStream_t s);
 hipError_t launch_grad_coefs(const SgGradArgs& a, int dtype, hipStream_t s);
+// dA, dB and dg.
 hipError_t launch_grad_outer(const SgGradArgs& a, int dtype, hipStream_t s);
 bool sgmm_grad_fits(const SgGradArgs& a, int dtype);
 

@@ -5,207 +5,149 @@
 // (sums over the slots (t, k) that chose e).
 //
 // dx is itself an SGMM, of dy through the banks' transposes, so it runs the
-// SGMM's own kernels: one segmentation, one shrink launch over the projections'
-// (x, A) and (dy, B^T) together, which leaves u and w in the workspace, and the
-// expand of w through A^T into dx.  The rest is here:
-//   pack   the banks' transposes (and A as the shrink reads it), every call:
-//          the banks change with every training step.
-//   lists  every expert's slots in sorted-position order, padded to whole
-//          tiles of 32 (a padding slot repeats a row of its expert with
-//          coefficients 0, so it brings in no row's infinities that are not
-//          the expert's own); one workgroup per expert.
+// SGMM's own kernels: one shrink launch over the projections' (x, A) and
+// (dy, B^T) together, which leaves u and w in the workspace, and the expand of w
+// through A^T into dx.  Launches:
+//   prep   (in sgmm.hip) the segmentation; every expert's slot list, whose
+//          places follow from the segmentation's counts; and in the other
+//          workgroups the banks' transposes (and A as the shrink reads it),
+//          every call: the banks change with every training step.
+//   shrink the SGMM's.
 //   coefs  per (32-slot tile, projection): u and w (their K slices added in
-//          order), s u . w for dg, and the products' coefficients s g w and
-//          s g u, each as two bf16 terms (hi + lo hold 16 bits of it, as the
-//          expand's do: one bf16 alone would cost 2^-9), transposed so that
-//          eight slots of one rank are one 16-byte operand.
-//   outer  dA and dB: per (projection, side, 128 columns, expert) a product
-//          with M = ranks, N = columns and K = the expert's slots, bf16 MFMA
-//          16x16x32 with fp32 sums.  A lane reads eight columns of eight rows
-//          (16 bytes each; a quarter wave reads 256 contiguous bytes of a row)
-//          and transposes the 8x8 block in registers, one v_perm per two
-//          values: x and dy go from memory to the matrix cores without LDS.
-//          The four waves take every fourth tile and add up through LDS in a
-//          fixed order.  Every gradient element has one owner: no atomics,
-//          bitwise reproducible.
-// The x and dy rows are read by the shrink and, once per chosen slot, by the
-// outer product: the experts of one column block run next to each other on one
-// XCD so that the second slot's read finds the row in L2 or the memory-side cache.
+//          order), s u . w for dg, and the coefficients s g w and s g u, each as
+//          three bf16 terms (8 + 8 + 8 bits: fp32 whole), transposed so
+//          that eight slots of one rank are one 16-byte operand.  With two terms
+//          the gradients lose a factor of three to fp32 sums; the third costs
+//          matrix instructions where memory is the bound.
+//   expand the SGMM's.
+//   outer  dA and dB: per (projection, side, column block, chunk of an expert's
+//          list) a product with M = ranks, N = columns and K = slots, bf16 MFMA
+//          16x16x32 with fp32 sums.  A lane reads CPL columns of eight rows and
+//          transposes the block in registers, one v_perm per two values: x and dy
+//          go from memory to the matrix cores without LDS.  The four waves take
+//          every fourth tile and add up through LDS in a fixed order.
+//   sum    experts with several chunks: their partial sums in chunk order; dg.
+// Every gradient element has one owner per launch: no atomics, bitwise
+// reproducible.
+//
+// Chunks.  Routing is skewed (Zipf 1.1 over 8 experts: the first is in 60% of the
+// rows), and one workgroup per (block, expert) would wait for the longest list.
+// An expert's list is cut into chunks of at most chunk_tiles tiles, chosen so
+// that a call has about kTargetItems chunks, several rounds of what the chip
+// holds; only experts with more than one chunk pay for partial sums.
+#include <type_traits>
+
 #include "gfx950.hpp"
 #include "internal.hpp"
 #include "sgmm.hpp"
 
 namespace dlm {
 
-static size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
+namespace {
 
-SgGradLayout sgmm_grad_layout(int64_t T, int64_t d_max, int E, int r, int n_prob) {
+size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+constexpr int kTargetItems = 4096;
+constexpr int kMinChunkTiles = 16;  // four per wave: fewer would be mostly the sum at its end
+constexpr int kCoefTerms = 3;
+
+// Rank blocks (of 16) and columns per lane of the outer products.  From 48
+// ranks on a lane takes four columns instead of eight: accumulators, rows and
+// coefficients together then leave room for three waves per SIMD (one at 64
+// ranks x 8 columns).
+constexpr int outer_cpl(int r16) { return r16 <= 2 ? 8 : 4; }
+
+int rank_chunks(const SgLayout& L) { return (L.r_pad + 63) / 64; }
+int outer_r16(const SgLayout& L) { return L.r_pad <= 64 ? L.r_pad / 16 : 4; }
+
+}  // namespace
+
+int grad_cols(int r, int dtype) {
+    const int r16 = (r + 15) / 16;
+    return dtype == 1 ? 16 * outer_cpl(r16 < 4 ? r16 : 4) : 64;
+}
+
+SgGradLayout sgmm_grad_layout(int64_t T, int64_t total_ks, int E, int r, int n_prob, int n_units, int dtype) {
     SgGradLayout G;
-    G.L = sgmm_layout(T, d_max, E, r, 2 * n_prob);
+    G.L = sgmm_layout(T, 1, E, r, (int)total_ks);  // one slice each of total_ks problems
     G.cap = (2 * T + (int64_t)E * (kGradTile - 1) + kGradTile - 1) / kGradTile * kGradTile;
-    G.rc_pad = G.L.r_pad <= 64 ? G.L.r_pad : (G.L.r_pad + 63) / 64 * 64;
+    G.rc_pad = rank_chunks(G.L) * 16 * outer_r16(G.L);
+    const int64_t tiles = G.cap / kGradTile, items = (int64_t)n_units * rank_chunks(G.L) * tiles;
+    int64_t ct = (items + kTargetItems - 1) / kTargetItems;
+    ct = ct < kMinChunkTiles ? kMinChunkTiles : ct;
+    G.chunk_tiles = (int)(dtype == 1 ? (ct < (1 << 30) ? ct : 1 << 30) : 1 << 30);
+    // full chunks (the bounds, not the count, so that it does not fall as T grows), and one more per expert
+    const int64_t by_tiles = tiles / kMinChunkTiles, by_items = kTargetItems / ((int64_t)n_units * rank_chunks(G.L));
+    G.max_chunks = (int)(dtype == 1 ? (by_tiles < by_items ? by_tiles : by_items) + E : E);
     size_t o = G.L.total;
-    G.eoff = o;  o += a256((size_t)(E + 1) * 4);
-    G.slot = o;  o += a256((size_t)G.cap * 4);
-    G.srow = o;  o += a256((size_t)G.cap * 4);
-    G.coef = o;  o += a256((size_t)n_prob * 4 * G.cap * G.rc_pad * 2);
-    G.dgp = o;   o += a256((size_t)n_prob * T * 8);
+    G.eoff = o;    o += a256((size_t)(E + 1) * 4);
+    G.slot = o;    o += a256((size_t)G.cap * 4);
+    G.srow = o;    o += a256((size_t)G.cap * 4);
+    G.chunk = o;   o += a256((size_t)G.max_chunks * sizeof(SgChunk));
+    G.echunk = o;  o += a256((size_t)(E + 1) * 4);
+    G.coef = o;
+    o += a256(dtype == 1 ? (size_t)n_prob * 2 * kCoefTerms * G.cap * G.rc_pad * 2 : (size_t)n_prob * 2 * G.cap * G.L.r_pad * 4);
+    G.part = o;
+    if (dtype == 1)
+        o += (size_t)n_units * rank_chunks(G.L) * G.max_chunks * (16 * outer_r16(G.L)) * grad_cols(r, dtype) * 4;
+    G.dgp = o;     o += a256((size_t)n_prob * T * 8);
     G.total = o;
     return G;
 }
 
 namespace {
 
-// ---- banks' transposes ----------------------------------------------------------
+__device__ __forceinline__ bool rejected(const SgGradArgs& a) { return gld((const int32_t*)(a.ws + a.G.L.hdr) + SG_ERR) != 0; }
 
-// One thread per eight elements of a projection's A (then of its B).  A: eight
-// columns of one rank row, written as the packed group the shrink reads and as
-// eight elements of the transpose; B: element [e][o][rho] of eight consecutive o.
-// Groups are numbered so that neighbouring threads read and write neighbours.
-__global__ __launch_bounds__(256) void grad_pack_bf16(SgGradArgs a) {
-    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (q >= a.pk_total) return;
-    int p = 0;
-    for (int lo = 0, hi = a.n_prob - 1; lo <= hi;) {  // the last projection that starts at or before q
-        const int mid = (lo + hi) / 2;
-        if (a.probs[mid].pk0 <= q) p = mid, lo = mid + 1;
-        else hi = mid - 1;
-    }
-    const SgGrad P = a.probs[p];
-    const int r = a.r;
-    const int64_t i = q - P.pk0, na = (int64_t)a.E * r * (P.d_in / 8);
-    if (i < na) {
-        const int64_t nq = P.d_in / 8, rho = i % r, kq = (i / r) % nq, e = i / (r * nq);
-        const u32x4 v = ld128((const uint16_t*)P.A + ((e * r + rho) * nq + kq) * 8);
-        st128((uint16_t*)P.Ap + 8 * i, v);
-        uint16_t* t = (uint16_t*)P.At + (e * P.d_in + 8 * kq) * r + rho;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            gst(t + (2 * j) * r, (uint16_t)(v[j] & 0xffffu));
-            gst(t + (2 * j + 1) * r, (uint16_t)(v[j] >> 16));
-        }
-    } else {
-        const int64_t b = i - na, nq = P.d_out / 8, rho = b % r, kq = (b / r) % nq, e = b / (r * nq);
-        const uint16_t* src = (const uint16_t*)P.B + (e * P.d_out + 8 * kq) * r + rho;
-        u32x4 v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = (uint32_t)gld(src + (2 * j) * r) | ((uint32_t)gld(src + (2 * j + 1) * r) << 16);
-        st128((uint16_t*)P.Bt + 8 * b, v);
-    }
-}
+// ---- u, w in fp32 -------------------------------------------------------------------
 
-// fp32: one thread per element; At [E][d_in][r], Bt [E][r][d_out].
-__global__ __launch_bounds__(256) void grad_pack_f32(SgGradArgs a) {
-    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (q >= a.pk_total) return;
-    int p = 0;
-    for (int lo = 0, hi = a.n_prob - 1; lo <= hi;) {
-        const int mid = (lo + hi) / 2;
-        if (a.probs[mid].pk0 <= q) p = mid, lo = mid + 1;
-        else hi = mid - 1;
-    }
-    const SgGrad P = a.probs[p];
-    const int r = a.r;
-    const int64_t i = q - P.pk0, na = (int64_t)a.E * r * P.d_in;
-    if (i < na) {
-        const int64_t rho = i % r, j = (i / r) % P.d_in, e = i / ((int64_t)r * P.d_in);
-        gst((float*)P.At + i, gld((const float*)P.A + (e * r + rho) * P.d_in + j));
-    } else {
-        const int64_t b = i - na, o = b % P.d_out, rho = (b / P.d_out) % r, e = b / ((int64_t)r * P.d_out);
-        gst((float*)P.Bt + b, gld((const float*)P.B + (e * P.d_out + o) * r + rho));
-    }
-}
-
-// ---- the experts' slot lists ------------------------------------------------------
-
-constexpr int kListThreads = 1024;
-constexpr int kListWaves = kListThreads / kWave;
-
-// Workgroup e: counts every expert's slots (its list starts behind the earlier
-// experts' padded lists), then writes its own list in position order.
-__global__ __launch_bounds__(kListThreads) void grad_lists(SgGradArgs a) {
+// One wave per (projection side, position, slot): eight ranks' products at a
+// time over the row, lanes along it, then a butterfly sum.
+__global__ __launch_bounds__(256) void grad_shrink_f32(SgGradArgs a) {
     const SgLayout& L = a.G.L;
-    const int32_t* hdr = (const int32_t*)(a.ws + L.hdr);
-    const int32_t* perm = (const int32_t*)(a.ws + L.perm);
-    const uint32_t* epk = (const uint32_t*)(a.ws + L.epk);
-    int32_t* eoff = (int32_t*)(a.ws + a.G.eoff);
-    int32_t* slot = (int32_t*)(a.ws + a.G.slot);
-    int32_t* srow = (int32_t*)(a.ws + a.G.srow);
-    if (gld(hdr + SG_ERR)) return;
-    const int n_pos = gld(hdr + SG_NPOS);
-    const int e = blockIdx.x, E = a.E, tid = threadIdx.x, lane = lane_id(), w = wave_id();
-    __shared__ int s_cnt[32], s_wave[kListWaves], s_last;
-    if (tid < 32) s_cnt[tid] = 0;
-    if (tid == 0) s_last = -1;
-    __syncthreads();
-    for (int p0 = 0; p0 < n_pos; p0 += kListThreads) {
-        const int p = p0 + tid;
-        const uint32_t ep = p < n_pos ? gld(epk + p) : 0xffffffffu;
-        const int e0 = (int16_t)(ep & 0xffffu), e1 = (int16_t)(ep >> 16);
-        for (int x = 0; x < E; ++x) {
-            const int n = (int)(__popcll(__ballot(e0 == x)) + __popcll(__ballot(e1 == x)));
-            if (lane == 0 && n) atomicAdd(&s_cnt[x], n);
-        }
-    }
-    __syncthreads();
-    int off = 0;
-    for (int x = 0; x < E; ++x) {
-        if (e == 0 && tid == 0) gst(eoff + x, off);
-        if (x < e || e == 0) off += (s_cnt[x] + kGradTile - 1) / kGradTile * kGradTile;
-    }
-    if (e == 0) {
-        if (tid == 0) gst(eoff + E, off);
-        off = 0;
-    }
-    const int cnt = s_cnt[e];
-    int done = 0;
-    for (int p0 = 0; p0 < n_pos; p0 += kListThreads) {
-        const int p = p0 + tid;
-        const uint32_t ep = p < n_pos ? gld(epk + p) : 0xffffffffu;
-        const bool k0 = (int16_t)(ep & 0xffffu) == e, k1 = (int16_t)(ep >> 16) == e;
-        const uint64_t b0 = __ballot(k0), b1 = __ballot(k1), lt = (1ull << lane) - 1ull;
-        if (lane == 0) s_wave[w] = (int)(__popcll(b0) + __popcll(b1));
-        __syncthreads();
-        int at = done, all = 0;
-        for (int i = 0; i < kListWaves; ++i) {
-            at += i < w ? s_wave[i] : 0;
-            all += s_wave[i];
-        }
-        at += (int)(__popcll(b0 & lt) + __popcll(b1 & lt));
-        if (k0 || k1) {
-            const int row = gld(perm + p);
-            if (k0) {
-                gst(slot + off + at, 2 * p);
-                gst(srow + off + at, row);
+    if (rejected(a)) return;
+    const int64_t q = (int64_t)blockIdx.x * 4 + wave_id();  // 2 * position + k
+    if (q >= 2 * (int64_t)gld((const int32_t*)(a.ws + L.hdr) + SG_NPOS)) return;
+    const uint32_t ep = gld((const uint32_t*)(a.ws + L.epk) + q / 2);
+    const int e = uniform((q & 1) ? (int16_t)(ep >> 16) : (int16_t)(ep & 0xffffu));
+    if (e < 0) return;
+    const int64_t row = uniform(gld((const int32_t*)(a.ws + L.perm) + q / 2));
+    const int side = blockIdx.y & 1, lane = lane_id(), r = a.r;
+    const SgGrad P = a.probs[blockIdx.y / 2];
+    const int d = side ? P.d_out : P.d_in;
+    const float* act = (const float*)(side ? P.dy : P.x) + row * d;
+    const float* bank = (const float*)(side ? P.Bt : P.A) + (int64_t)e * r * d;
+    float* v = (float*)(a.ws + L.v) + (side ? P.ks_w : P.ks_u) * L.T_pad * 2 * L.r_pad + q * L.r_pad;
+    for (int r0 = 0; r0 < r; r0 += 8) {
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int j = lane; j < d; j += kWave) {
+            const float x = gld(act + j);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int rho = r0 + i < r ? r0 + i : r - 1;
+                acc[i] = fmaf(x, gld(bank + (int64_t)rho * d + j), acc[i]);
             }
-            if (k1) {
-                gst(slot + off + at + (k0 ? 1 : 0), 2 * p + 1);
-                gst(srow + off + at + (k0 ? 1 : 0), row);
-            }
-            if (at + (k0 && k1 ? 2 : 1) == cnt) s_last = row;
         }
-        done += all;
-        __syncthreads();
-    }
-    const int pad = (cnt + kGradTile - 1) / kGradTile * kGradTile;
-    if (tid < pad - cnt) {
-        gst(slot + off + cnt + tid, -1);
-        gst(srow + off + cnt + tid, s_last);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float s = acc[i];
+#pragma unroll
+            for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, kWave);
+            if (lane == i && r0 + i < r) gst(v + r0 + i, s);
+        }
     }
 }
 
 // ---- coefficients -------------------------------------------------------------------
 
-// Eight threads per slot, kRank ranks at a time.  Padding ranks and slots get 0
+// Eight threads per slot, 16 ranks at a time.  Padding ranks and slots get 0
 // (their v was never written: selected away, not multiplied).
 template <bool BF>
 __global__ __launch_bounds__(256) void grad_coefs(SgGradArgs a) {
     const SgLayout& L = a.G.L;
-    const int32_t* hdr = (const int32_t*)(a.ws + L.hdr);
-    if (gld(hdr + SG_ERR)) return;
-    const int32_t* eoff = (const int32_t*)(a.ws + a.G.eoff);
+    if (rejected(a)) return;
     const int64_t tile = blockIdx.x;
-    if (tile * kGradTile >= gld(eoff + a.E)) return;
+    if (tile * kGradTile >= gld((const int32_t*)(a.ws + a.G.eoff) + a.E)) return;
     const int prob = blockIdx.y;
     const SgGrad P = a.probs[prob];
     const int tid = threadIdx.x, s = tid / 8, j = tid % 8, RPAD = L.r_pad, r = a.r;
@@ -217,15 +159,17 @@ __global__ __launch_bounds__(256) void grad_coefs(SgGradArgs a) {
     const int64_t stride = L.T_pad * 2 * RPAD;  // floats per K slice
     const float* vu = (const float*)(a.ws + L.v) + P.ks_u * stride + q * RPAD;
     const float* vw = (const float*)(a.ws + L.v) + P.ks_w * stride + q * RPAD;
-    __shared__ __attribute__((aligned(16))) uint16_t s_c[4][16][kGradTile];  // side x (hi, lo), 16 ranks
+    constexpr int kParts = BF ? 2 * kCoefTerms : 2;
+    typedef typename std::conditional<BF, uint16_t, float>::type C;
+    __shared__ __attribute__((aligned(16))) C s_c[kParts][16][kGradTile];
     float dot = 0.f;
     const int rc = BF ? a.G.rc_pad : RPAD;
-    uint16_t* coef = (uint16_t*)(a.ws + a.G.coef);
+    C* coef = (C*)(a.ws + a.G.coef);
     const int64_t part = a.G.cap * rc;  // elements of one (prob, side, term)
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
     for (int r0 = 0; r0 < rc; r0 += 16) {
         const int rho = r0 + 2 * j;
         float u[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
-        typedef float f32x2_t __attribute__((ext_vector_type(2)));
         if (live && rho < r) {
             for (int k = 0; k < P.n_ks_u; ++k) {
                 const f32x2_t v = gld((const f32x2_t*)(vu + k * stride + rho));
@@ -241,22 +185,30 @@ __global__ __launch_bounds__(256) void grad_coefs(SgGradArgs a) {
         }
         dot = fmaf(u[0], w[0], dot);
         dot = fmaf(u[1], w[1], dot);
-        if constexpr (BF) {
-            __syncthreads();
+        __syncthreads();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float x = c * w[k], y = c * u[k];
-                const uint16_t xh = f_to_bf(x), yh = f_to_bf(y);
-                s_c[0][2 * j + k][s] = xh;
-                s_c[1][2 * j + k][s] = f_to_bf(x - bf_to_f(xh));
-                s_c[2][2 * j + k][s] = yh;
-                s_c[3][2 * j + k][s] = f_to_bf(y - bf_to_f(yh));
+        for (int k = 0; k < 2; ++k) {
+            float x = c * w[k], y = c * u[k];
+            if constexpr (BF) {
+#pragma unroll
+                for (int m = 0; m < kCoefTerms; ++m) {
+                    const uint16_t xm = f_to_bf(x), ym = f_to_bf(y);
+                    s_c[m][2 * j + k][s] = xm;
+                    s_c[kCoefTerms + m][2 * j + k][s] = ym;
+                    x -= bf_to_f(xm);
+                    y -= bf_to_f(ym);
+                }
+            } else {
+                s_c[0][2 * j + k][s] = x;
+                s_c[1][2 * j + k][s] = y;
             }
-            __syncthreads();
-            // 4 parts x 16 ranks x 64 bytes: one 16-byte store per thread
-            const int part_i = tid / 64, rr = (tid / 4) % 16, o = 8 * (tid % 4);
-            st128(coef + ((int64_t)prob * 4 + part_i) * part + (tile * rc + r0 + rr) * kGradTile + o,
-                  *(const u32x4*)&s_c[part_i][rr][o]);
+        }
+        __syncthreads();
+        constexpr int W = 16 / (int)sizeof(C), kRow = kGradTile / W;  // 16-byte stores per rank row
+        for (int i = tid; i < kParts * 16 * kRow; i += 256) {
+            const int m = i / (16 * kRow), rr = i / kRow % 16, o = W * (i % kRow);
+            st128(coef + ((int64_t)prob * kParts + m) * part + (tile * rc + r0 + rr) * kGradTile + o,
+                  *(const u32x4*)&s_c[m][rr][o]);
         }
     }
     // the slot's eight partial sums, in a fixed order
@@ -270,9 +222,7 @@ __global__ __launch_bounds__(256) void grad_coefs(SgGradArgs a) {
 }
 
 // dg[t][k] = the projections' parts, added in order; 0 for an empty slot.
-__global__ __launch_bounds__(256) void grad_dg(SgGradArgs a) {
-    if (gld((const int32_t*)(a.ws + a.G.L.hdr) + SG_ERR)) return;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__device__ __forceinline__ void write_dg(const SgGradArgs& a, int64_t i) {
     if (i >= 2 * a.T) return;
     const float* p = (const float*)(a.ws + a.G.dgp) + i;
     float v = 0.f;
@@ -290,46 +240,84 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
                                                    0, 0);
 }
 
-// Column c of the 8x8 bf16 block whose row i is v[i]: one v_perm per two values.
-__device__ __forceinline__ u32x4 column(const u32x4 (&v)[8], int c) {
-    u32x4 o;
+typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+template <int CPL> struct RowRegs;
+template <> struct RowRegs<8> { typedef u32x4 type; };
+template <> struct RowRegs<4> { typedef u32x2v type; };
+
+// The outer product's gradient element(s) of accumulators acc[b][j] (rank block
+// b, column j of the lane): written or added to.
+template <int R16, int CPL>
+__device__ __forceinline__ void store_block(const SgGradArgs& a, const SgOuter& O, int e, int r0, int col, int kg, int b,
+                                            const f32x4 (&acc)[CPL]) {
+    const int r = a.r, d = O.d, rho = r0 + 16 * b + 4 * kg;  // this lane's four ranks
+    if (col >= d) return;
+    if (O.side == 0) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        o[q] = __builtin_amdgcn_perm(v[2 * q + 1][c / 2], v[2 * q][c / 2], (c & 1) ? 0x07060302u : 0x05040100u);
-    return o;
+        for (int i = 0; i < 4; ++i) {
+            if (rho + i >= r) continue;
+            f32x4* p = (f32x4*)(O.out + ((int64_t)e * r + rho + i) * d + col);
+#pragma unroll
+            for (int h = 0; h < CPL / 4; ++h) {
+                f32x4 o = {acc[4 * h][i], acc[4 * h + 1][i], acc[4 * h + 2][i], acc[4 * h + 3][i]};
+                if (a.accumulate) o += gld(p + h);
+                gst(p + h, o);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            float* p = O.out + ((int64_t)e * d + col + j) * r + rho;
+            if ((r & 3) == 0) {
+                if (rho >= r) continue;
+                f32x4 o = acc[j];
+                if (a.accumulate) o += gld((const f32x4*)p);
+                gst((f32x4*)p, o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (rho + i < r) gst(p + i, a.accumulate ? gld(p + i) + acc[j][i] : acc[j][i]);
+            }
+        }
+    }
+}
+
+// Partial sums of item (unit, rank chunk, chunk): [b][j][lane] f32x4.
+template <int R16, int CPL> __device__ __forceinline__ f32x4* part_of(const SgGradArgs& a, int64_t unit, int n_ch, int ch, int c) {
+    return (f32x4*)(a.ws + a.G.part) + ((unit * n_ch + ch) * a.G.max_chunks + c) * (R16 * CPL * kWave);
 }
 
 template <int R16>
-__global__ __launch_bounds__(256) void grad_outer_bf16(SgGradArgs a, int rank_chunks) {
-    const SgLayout& L = a.G.L;
-    const int32_t* hdr = (const int32_t*)(a.ws + L.hdr);
-    if (gld(hdr + SG_ERR)) return;
-    // XCD b % 8 takes every eighth column block, its experts (and rank chunks) one after another
-    const int per_unit = a.E * rank_chunks;
+__global__ __launch_bounds__(256) void grad_outer_bf16(SgGradArgs a, int n_ch) {
+    constexpr int CPL = outer_cpl(R16);
+    typedef typename RowRegs<CPL>::type Row;
+    if (rejected(a)) return;
+    // XCD b % 8 takes every eighth column block, its chunks (and rank chunks) one after another
+    const int per_unit = a.G.max_chunks * n_ch;
     const int64_t jj = blockIdx.x / 8;
     const int64_t unit = jj / per_unit * 8 + blockIdx.x % 8;
     if (unit >= a.n_units) return;
-    const int sub = (int)(jj % per_unit), e = sub % a.E, ch = sub / a.E;
+    const int sub = (int)(jj % per_unit), c = sub % a.G.max_chunks, ch = sub / a.G.max_chunks;
+    if (c >= gld((const int32_t*)(a.ws + a.G.echunk) + a.E)) return;
+    const SgChunk K = ((const SgChunk*)(a.ws + a.G.chunk))[c];
     const SgOuter O = a.outers[a.unit_outer[unit]];
-    const int c0 = (int)(unit - O.unit0) * kGradCols;
-    const int32_t* eoff = (const int32_t*)(a.ws + a.G.eoff);
     const int32_t* srow = (const int32_t*)(a.ws + a.G.srow);
-    const int t0 = uniform(gld(eoff + e)) / kGradTile, t1 = uniform(gld(eoff + e + 1)) / kGradTile;
     const int lane = lane_id(), w = wave_id(), n = lane & 15, kg = lane >> 4;
-    const int d = uniform(O.d), rc = a.G.rc_pad, r0 = ch * 64;
-    const uint16_t* __restrict__ act = (const uint16_t*)O.act;
-    const int64_t part = a.G.cap * rc;
-    const uint16_t* __restrict__ hi = (const uint16_t*)(a.ws + a.G.coef) + ((int64_t)O.prob * 4 + 2 * O.side) * part;
-    const uint16_t* __restrict__ lo = hi + part;
-    const int col = c0 + 8 * n;
+    const int d = uniform(O.d), rc = a.G.rc_pad, r0 = ch * 64, t1 = K.t1;
+    const int col = (int)(unit - O.unit0) * (16 * CPL) + CPL * n;
     const int lcol = col < d ? col : 0;  // columns past the end read the first ones and are not stored
+    const uint16_t* __restrict__ act = (const uint16_t*)O.act + lcol;
+    const int64_t part = a.G.cap * rc;
+    const uint16_t* __restrict__ coef = (const uint16_t*)(a.ws + a.G.coef) +
+                                        ((int64_t)O.prob * 2 + O.side) * kCoefTerms * part +
+                                        (r0 + n) * kGradTile + 8 * kg;
 
-    f32x4 acc[R16][8];
+    f32x4 acc[R16][CPL];
 #pragma unroll
     for (int b = 0; b < R16; ++b)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[b][j] = f32x4{};
-    u32x4 v[8], ch_[R16], cl_[R16];
+        for (int j = 0; j < CPL; ++j) acc[b][j] = f32x4{};
+    Row v[8];
     int rows[8];
     auto load_rows = [&](int t) {
         const u32x4 a0 = ld128(srow + t * kGradTile + 8 * kg), a1 = ld128(srow + t * kGradTile + 8 * kg + 4);
@@ -339,180 +327,204 @@ __global__ __launch_bounds__(256) void grad_outer_bf16(SgGradArgs a, int rank_ch
             rows[4 + i] = (int)a1[i];
         }
     };
-    auto load_tile = [&](int t) {
+    auto load_x = [&]() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = ld128(act + (int64_t)rows[i] * d + lcol);
-#pragma unroll
-        for (int b = 0; b < R16; ++b) {
-            const int64_t o = ((int64_t)t * rc + r0 + 16 * b + n) * kGradTile + 8 * kg;
-            ch_[b] = ld128(hi + o);
-            cl_[b] = ld128(lo + o);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = gld((const Row*)(act + (int64_t)rows[i] * d));
     };
-    int t = t0 + w;
+    int t = K.t0 + w;
     if (t < t1) {
         load_rows(t);
-        load_tile(t);
+        load_x();
         if (t + 4 < t1) load_rows(t + 4);
     }
 #pragma unroll 1
     for (; t < t1; t += 4) {
-        u32x4 x[8], h[R16], l[R16];
+        // this tile's coefficients go out before the next tile's rows, so
+        // waiting for them does not wait for those
+        u32x4 h[R16][kCoefTerms];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = v[i];
+        for (int b = 0; b < R16; ++b)
 #pragma unroll
-        for (int b = 0; b < R16; ++b) {
-            h[b] = ch_[b];
-            l[b] = cl_[b];
-        }
+            for (int m = 0; m < kCoefTerms; ++m)
+                h[b][m] = ld128(coef + m * part + ((int64_t)t * rc + 16 * b) * kGradTile);
+        // column j of the 8 x CPL block: one v_perm per two values
+        u32x4 x[CPL];
+#pragma unroll
+        for (int j = 0; j < CPL; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                x[j][q] = __builtin_amdgcn_perm(v[2 * q + 1][j / 2], v[2 * q][j / 2], (j & 1) ? 0x07060302u : 0x05040100u);
         if (t + 4 < t1) {
-            load_tile(t + 4);
+            load_x();
             if (t + 8 < t1) load_rows(t + 8);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const u32x4 bx = column(x, j);
+        for (int b = 0; b < R16; ++b)
 #pragma unroll
-            for (int b = 0; b < R16; ++b) {
-                acc[b][j] = mfma16(h[b], bx, acc[b][j]);
-                acc[b][j] = mfma16(l[b], bx, acc[b][j]);
-            }
-        }
+            for (int m = 0; m < kCoefTerms; ++m)
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) acc[b][j] = mfma16(h[b][m], x[j], acc[b][j]);
     }
     // the four waves' sums: (0 + 2) + (1 + 3)
-    __shared__ f32x4 s_red[2][R16 * 8][kWave];
+    __shared__ f32x4 s_red[2][R16 * CPL][kWave];
     if (w >= 2) {
 #pragma unroll
         for (int b = 0; b < R16; ++b)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s_red[w - 2][b * 8 + j][lane] = acc[b][j];
+            for (int j = 0; j < CPL; ++j) s_red[w - 2][b * CPL + j][lane] = acc[b][j];
     }
     __syncthreads();
     if (w < 2) {
 #pragma unroll
         for (int b = 0; b < R16; ++b)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[b][j] += s_red[w][b * 8 + j][lane];
+            for (int j = 0; j < CPL; ++j) acc[b][j] += s_red[w][b * CPL + j][lane];
     }
     __syncthreads();
     if (w == 1) {
 #pragma unroll
         for (int b = 0; b < R16; ++b)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s_red[0][b * 8 + j][lane] = acc[b][j];
+            for (int j = 0; j < CPL; ++j) s_red[0][b * CPL + j][lane] = acc[b][j];
     }
     __syncthreads();
-    if (w != 0 || col >= d) return;
-    const int r = a.r;
+    if (w != 0) return;
 #pragma unroll
     for (int b = 0; b < R16; ++b) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[b][j] += s_red[0][b * 8 + j][lane];
-        const int rho = r0 + 16 * b + 4 * kg;  // this lane's four ranks
-        if (O.side == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (rho + i >= r) continue;
-                float* p = O.out + ((int64_t)e * r + rho + i) * d + col;
-                f32x4 o0 = {acc[b][0][i], acc[b][1][i], acc[b][2][i], acc[b][3][i]};
-                f32x4 o1 = {acc[b][4][i], acc[b][5][i], acc[b][6][i], acc[b][7][i]};
-                if (a.accumulate) {
-                    o0 += gld((const f32x4*)p);
-                    o1 += gld((const f32x4*)p + 1);
-                }
-                gst((f32x4*)p, o0);
-                gst((f32x4*)p + 1, o1);
-            }
+        for (int j = 0; j < CPL; ++j) acc[b][j] += s_red[0][b * CPL + j][lane];
+        if (K.alone) {
+            store_block<R16, CPL>(a, O, K.e, r0, col, kg, b, acc[b]);
         } else {
+            f32x4* p = part_of<R16, CPL>(a, unit, n_ch, ch, c) + b * CPL * kWave + lane;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float* p = O.out + ((int64_t)e * d + col + j) * r + rho;
-                if ((r & 3) == 0) {
-                    if (rho >= r) continue;
-                    f32x4 o = acc[b][j];
-                    if (a.accumulate) o += gld((const f32x4*)p);
-                    gst((f32x4*)p, o);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (rho + i < r) gst(p + i, a.accumulate ? gld(p + i) + acc[b][j][i] : acc[b][j][i]);
-                }
-            }
+            for (int j = 0; j < CPL; ++j) gst(p + j * kWave, acc[b][j]);
         }
     }
 }
 
-// fp32: one thread per column, eight ranks at a time over the expert's slots in list order.
-__global__ __launch_bounds__(kGradCols) void grad_outer_f32(SgGradArgs a) {
-    const SgLayout& L = a.G.L;
-    if (gld((const int32_t*)(a.ws + L.hdr) + SG_ERR)) return;
-    const int unit = blockIdx.x, e = blockIdx.y, r = a.r, RPAD = L.r_pad;
+// Item (unit, rank chunk, expert): an expert with several chunks gets the sum of
+// their partials in chunk order, one rank block per wave and turn.  The
+// workgroups past the items write dg.
+template <int R16>
+__global__ __launch_bounds__(256) void grad_sum_bf16(SgGradArgs a, int n_ch, int64_t n_items) {
+    constexpr int CPL = outer_cpl(R16);
+    if (rejected(a)) return;
+    if (blockIdx.x >= n_items) {
+        write_dg(a, (blockIdx.x - n_items) * 256 + threadIdx.x);
+        return;
+    }
+    const int e = blockIdx.x % a.E, ch = blockIdx.x / a.E % n_ch;
+    const int64_t unit = blockIdx.x / a.E / n_ch;
+    const int32_t* echunk = (const int32_t*)(a.ws + a.G.echunk);
+    const int c0 = uniform(gld(echunk + e)), c1 = uniform(gld(echunk + e + 1));
+    if (c1 - c0 < 2) return;
     const SgOuter O = a.outers[a.unit_outer[unit]];
-    const SgGrad P = a.probs[O.prob];
-    const int col = (unit - O.unit0) * kGradCols + threadIdx.x;
-    if (col >= O.d) return;
-    const int32_t* eoff = (const int32_t*)(a.ws + a.G.eoff);
-    const int32_t* slot = (const int32_t*)(a.ws + a.G.slot);
-    const int32_t* srow = (const int32_t*)(a.ws + a.G.srow);
-    const float* gpk = (const float*)(a.ws + L.gpk);
-    const float* v = (const float*)(a.ws + L.v) + (O.side == 0 ? P.ks_w : P.ks_u) * L.T_pad * 2 * RPAD;
-    const float* act = (const float*)O.act;
-    const int s0 = gld(eoff + e), s1 = gld(eoff + e + 1);
-    for (int r0 = 0; r0 < r; r0 += 8) {
-        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int s = s0; s < s1; ++s) {
-            const int q = gld(slot + s);
-            if (q < 0) break;
-            const float x = gld(act + (int64_t)gld(srow + s) * O.d + col), c = a.scale * gld(gpk + q);
+    const int lane = lane_id(), n = lane & 15, kg = lane >> 4;
+    const int col = (int)(unit - O.unit0) * (16 * CPL) + CPL * n;
+    for (int b = wave_id(); b < R16; b += 4) {
+        f32x4 acc[CPL];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (r0 + i < r) acc[i] = fmaf(c * gld(v + (int64_t)q * RPAD + r0 + i), x, acc[i]);
-        }
+        for (int j = 0; j < CPL; ++j) acc[j] = f32x4{};
+        for (int c = c0; c < c1; ++c) {
+            const f32x4* p = part_of<R16, CPL>(a, unit, n_ch, ch, c) + b * CPL * kWave + lane;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (r0 + i >= r) break;
-            float* p = O.side == 0 ? O.out + ((int64_t)e * r + r0 + i) * O.d + col
-                                   : O.out + ((int64_t)e * O.d + col) * r + r0 + i;
-            gst(p, a.accumulate ? gld(p) + acc[i] : acc[i]);
+            for (int j = 0; j < CPL; ++j) acc[j] += gld(p + j * kWave);
         }
+        store_block<R16, CPL>(a, O, e, ch * 64, col, kg, b, acc);
     }
 }
 
-__global__ __launch_bounds__(kGradCols) void grad_zero(SgGradArgs a) {
+// fp32: 64 columns per workgroup and eight ranks (blockIdx.z), the four waves
+// taking every fourth list tile; the coefficients of a wave's slots are the
+// same for its lanes.  The last grid row writes dg.
+__global__ __launch_bounds__(256) void grad_outer_f32(SgGradArgs a, int n_units) {
+    if (rejected(a)) return;
+    if ((int)blockIdx.x >= n_units) {
+        if (blockIdx.y == 0 && blockIdx.z == 0) write_dg(a, (int64_t)(blockIdx.x - n_units) * 256 + threadIdx.x);
+        return;
+    }
+    const int unit = blockIdx.x, e = blockIdx.y, r0 = 8 * blockIdx.z, r = a.r, RPAD = a.G.L.r_pad;
+    const SgOuter O = a.outers[a.unit_outer[unit]];
+    const int lane = lane_id(), w = wave_id();
+    const int col = (unit - O.unit0) * 64 + lane, lcol = col < O.d ? col : 0;
+    const int32_t* eoff = (const int32_t*)(a.ws + a.G.eoff);
+    const int32_t* srow = (const int32_t*)(a.ws + a.G.srow);
+    const float* __restrict__ coef = (const float*)(a.ws + a.G.coef) + ((int64_t)O.prob * 2 + O.side) * a.G.cap * RPAD;
+    const float* __restrict__ act = (const float*)O.act + lcol;
+    const int t0 = uniform(gld(eoff + e)) / kGradTile, t1 = uniform(gld(eoff + e + 1)) / kGradTile;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int t = t0 + w; t < t1; t += 4) {
+        const float* ct = coef + ((int64_t)t * RPAD + r0) * kGradTile;
+#pragma unroll 1
+        for (int s = 0; s < kGradTile; s += 8) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = gld(act + (int64_t)uniform(gld(srow + t * kGradTile + s + i)) * O.d);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[k] = fmaf(ct[k * kGradTile + s + i], x[i], acc[k]);
+        }
+    }
+    __shared__ float s_red[4][8][kWave];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s_red[w][k][lane] = acc[k];
+    __syncthreads();
+    // wave w sums and stores ranks w and w + 4
+    if (col >= O.d) return;
+    for (int k = w; k < 8; k += 4) {
+        if (r0 + k >= r) break;
+        const float v = (s_red[0][k][lane] + s_red[1][k][lane]) + (s_red[2][k][lane] + s_red[3][k][lane]);
+        float* p = O.side == 0 ? O.out + ((int64_t)e * r + r0 + k) * O.d + col : O.out + ((int64_t)e * O.d + col) * r + r0 + k;
+        gst(p, a.accumulate ? gld(p) + v : v);
+    }
+}
+
+__global__ __launch_bounds__(kWave) void grad_zero(SgGradArgs a, int cols) {
     const int unit = blockIdx.x, e = blockIdx.y;
     const SgOuter O = a.outers[a.unit_outer[unit]];
-    const int col = (unit - O.unit0) * kGradCols + threadIdx.x;
-    if (col >= O.d) return;
-    for (int rho = 0; rho < a.r; ++rho)
-        gst(O.side == 0 ? O.out + ((int64_t)e * a.r + rho) * O.d + col : O.out + ((int64_t)e * O.d + col) * a.r + rho, 0.f);
+    for (int c = threadIdx.x; c < cols; c += kWave) {
+        const int col = (unit - O.unit0) * cols + c;
+        if (col >= O.d) return;
+        for (int rho = 0; rho < a.r; ++rho)
+            gst(O.side == 0 ? O.out + ((int64_t)e * a.r + rho) * O.d + col : O.out + ((int64_t)e * O.d + col) * a.r + rho, 0.f);
+    }
 }
 
+int64_t dg_blocks(const SgGradArgs& a) { return a.dg ? (2 * a.T + 255) / 256 : 0; }
 int64_t outer_blocks(const SgGradArgs& a) {
-    const int chunks = (a.G.L.r_pad + 63) / 64;
-    return 8ll * a.E * chunks * ((a.n_units + 7) / 8);
+    return 8ll * a.G.max_chunks * rank_chunks(a.G.L) * ((a.n_units + 7) / 8);
+}
+int64_t sum_items(const SgGradArgs& a) { return (int64_t)a.n_units * rank_chunks(a.G.L) * a.E; }
+
+template <int R16> hipError_t launch_outer(const SgGradArgs& a, hipStream_t s) {
+    const int n_ch = rank_chunks(a.G.L);
+    hipLaunchKernelGGL(grad_outer_bf16<R16>, dim3((unsigned)outer_blocks(a)), dim3(256), 0, s, a, n_ch);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    // no expert can have a second chunk while a chunk holds every tile
+    const int64_t items = a.G.max_chunks > a.E ? sum_items(a) : 0;
+    if (items + dg_blocks(a) == 0) return hipSuccess;
+    hipLaunchKernelGGL(grad_sum_bf16<R16>, dim3((unsigned)(items + dg_blocks(a))), dim3(256), 0, s, a, n_ch, items);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 bool sgmm_grad_fits(const SgGradArgs& a, int dtype) {
-    return grid_fits((a.pk_total + 255) / 256, 256) && grid_fits(a.G.cap / kGradTile, 256) &&
-           grid_fits((2 * a.T + 255) / 256, 256) && grid_fits(a.n_units, kGradCols) && (dtype == 0 || grid_fits(outer_blocks(a), 256));
+    return grad_prep_fits(a) && grid_fits(a.G.cap / kGradTile, 256) && grid_fits((a.T + 1) / 2, 256) &&
+           grid_fits(a.n_units + dg_blocks(a), 256) &&
+           (dtype == 0 || (grid_fits(outer_blocks(a), 256) && grid_fits(sum_items(a) + dg_blocks(a), 256)));
 }
 
-hipError_t launch_grad_zero(const SgGradArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(grad_zero, dim3((unsigned)a.n_units, (unsigned)a.E), dim3(kGradCols), 0, s, a);
+hipError_t launch_grad_zero(const SgGradArgs& a, int dtype, hipStream_t s) {
+    hipLaunchKernelGGL(grad_zero, dim3((unsigned)a.n_units, (unsigned)a.E), dim3(kWave), 0, s, a, grad_cols(a.r, dtype));
     return hipGetLastError();
 }
 
-hipError_t launch_grad_pack(const SgGradArgs& a, int dtype, hipStream_t s) {
-    const dim3 g((unsigned)((a.pk_total + 255) / 256));
-    if (dtype == 1) hipLaunchKernelGGL(grad_pack_bf16, g, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(grad_pack_f32, g, dim3(256), 0, s, a);
-    return hipGetLastError();
-}
-
-hipError_t launch_grad_lists(const SgGradArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(grad_lists, dim3((unsigned)a.E), dim3(kListThreads), 0, s, a);
+hipError_t launch_grad_shrink_f32(const SgGradArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(grad_shrink_f32, dim3((unsigned)((a.T + 1) / 2), (unsigned)(2 * a.n_prob)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -520,26 +532,21 @@ hipError_t launch_grad_coefs(const SgGradArgs& a, int dtype, hipStream_t s) {
     const dim3 g((unsigned)(a.G.cap / kGradTile), (unsigned)a.n_prob);
     if (dtype == 1) hipLaunchKernelGGL(grad_coefs<true>, g, dim3(256), 0, s, a);
     else hipLaunchKernelGGL(grad_coefs<false>, g, dim3(256), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.dg) return e;
-    hipLaunchKernelGGL(grad_dg, dim3((unsigned)((2 * a.T + 255) / 256)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_grad_outer(const SgGradArgs& a, int dtype, hipStream_t s) {
     if (dtype == 0) {
-        hipLaunchKernelGGL(grad_outer_f32, dim3((unsigned)a.n_units, (unsigned)a.E), dim3(kGradCols), 0, s, a);
+        hipLaunchKernelGGL(grad_outer_f32, dim3((unsigned)(a.n_units + dg_blocks(a)), (unsigned)a.E, (unsigned)((a.r + 7) / 8)),
+                           dim3(256), 0, s, a, a.n_units);
         return hipGetLastError();
     }
-    const int chunks = (a.G.L.r_pad + 63) / 64;
-    const dim3 g((unsigned)outer_blocks(a));
-    switch (a.G.L.r_pad <= 64 ? a.G.L.r_pad / 16 : 4) {
-        case 1: hipLaunchKernelGGL(grad_outer_bf16<1>, g, dim3(256), 0, s, a, chunks); break;
-        case 2: hipLaunchKernelGGL(grad_outer_bf16<2>, g, dim3(256), 0, s, a, chunks); break;
-        case 3: hipLaunchKernelGGL(grad_outer_bf16<3>, g, dim3(256), 0, s, a, chunks); break;
-        default: hipLaunchKernelGGL(grad_outer_bf16<4>, g, dim3(256), 0, s, a, chunks); break;
+    switch (outer_r16(a.G.L)) {
+        case 1: return launch_outer<1>(a, s);
+        case 2: return launch_outer<2>(a, s);
+        case 3: return launch_outer<3>(a, s);
+        default: return launch_outer<4>(a, s);
     }
-    return hipGetLastError();
 }
 
 }  // namespace dlm

@@ -449,13 +449,13 @@ int dlm_sgmm_group_bind_grads(dlm_sgmm_group* h, const void* const* dy, void* co
  * bitwise reproducible.  A set the forward call would reject leaves all of
  * them unchanged and sets the workspace status word (dlm_sgmm_status).  T = 0
  * writes zeros to dA and dB unless accumulate, and looks at nothing else.
- * workspace: >= dlm_sgmm_backward_workspace_size(T, the largest d_in or d_out,
- * E, r, n_problems) bytes, 256-byte aligned.  No allocation; 7 launches (bf16
- * up to rank 64: transposes, segmentation, shrink, lists, coefficients, expand,
- * outer products) and one more each for dg, for T > 8192, for the K-slice sum
- * above rank 64, and for every further problem that shares the same dx.
+ * workspace: >= dlm_sgmm_group_backward_workspace_size(h, T) bytes (asked once
+ * the buffers are bound; it serves any smaller T too), 256-byte aligned.  No allocation.  Launches: segmentation with the banks'
+ * transposes, shrink, coefficients, expand, outer products, and the sum of their
+ * parts with dg; one more each for T > 8192, for the K-slice sum above rank 64,
+ * and for every further problem that shares the same dx.
  */
-int dlm_sgmm_backward_workspace_size(int64_t T, int64_t d_max, int32_t E, int32_t r, int32_t n_problems, size_t* bytes);
+int dlm_sgmm_group_backward_workspace_size(const dlm_sgmm_group* h, int64_t T, size_t* bytes);
 int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* g, float* dg, int64_t T,
                             int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
 

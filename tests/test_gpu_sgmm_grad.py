@@ -269,6 +269,26 @@ def test_rejected_sets_change_nothing(dtype, bad):
     c.check()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_workspace_serves_fewer_rows(dtype):
+    """A workspace for the largest batch, used for smaller ones (which cut K and the lists otherwise)."""
+    c = Case(3000, [(2056, 264)], 8, 16, dtype).bind()
+    ws = c.grp.backward_workspace(3000)
+    full = c.idx.clone()
+    for T in (3000, 1024, 300, 64, 7, 1):
+        assert c.grp.backward_workspace(T).numel() <= ws.numel()
+        for t, d in zip(c.ddx, c.dx0):
+            t.copy_(d)
+        ws.fill_(0x7F)
+        c.T, c.idx = T, full[:T]
+        gate = c.g
+        c.g = gate[:T]
+        c.dg = torch.empty((T, 2), device="cuda")
+        c.run(workspace=ws)
+        c.check()
+        c.g = gate
+
+
 def test_no_rows():
     c = Case(16, [(64, 64)], 4, 8, BF).bind()
     e = torch.empty((0, 2), device="cuda")
