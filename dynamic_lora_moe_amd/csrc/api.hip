@@ -1048,7 +1048,7 @@ int dlm_sgmm_group_bind_grads(dlm_sgmm_group* h, const void* const* dy, void* co
         // outer products: side 0 has x's columns, side 1 dy's
         std::vector<SgOuter> outers(2 * (size_t)n);
         int64_t units = 0;
-        const int cols = grad_cols(r, h->dtype);
+        const int cols = grad_cols(h->dtype);
         for (int i = 0; i < 2 * n; ++i) {
             const SgDesc& p = h->h_descs[i % n];
             SgOuter& o = outers[i];

@@ -253,54 +253,98 @@ __global__ __launch_bounds__(kSegThreads) void sgmm_seg_count(const int32_t* __r
 // for x <= e, then (e, y) -- so a key's rows start at the sum of the totals
 // before it: oa / ob for its smaller / larger expert (a key (e, e) holds two
 // slots a row).  The first workgroup writes the starts and the chunks.
+constexpr int kSortChunks = 256;
+__device__ __forceinline__ int pair_key(int e, int p, int E) {  // the key of experts e and p (p = -1: e alone)
+    return p < e ? (p + 1) * (E + 1) + e + 1 : (e + 1) * (E + 1) + p + 1;
+}
 __device__ __forceinline__ void lists_place(const int* s_tot, int* s_oa, int* s_ob, int* s_off, int* s_num, int E,
                                             bool first, const SgLists& lists) {
+    static_assert(32 <= kWave / 2, "one wave scans the experts");
     const int tid = threadIdx.x;
-    if (tid < E) {
-        const int e = tid;
+    __shared__ int s_c0[33];
+    if (tid < kWave) {
+        const int e = tid < E ? tid : E - 1;
         int n = 0;
-        for (int x = -1; x < e; ++x) {
-            const int k = (x + 1) * (E + 1) + e + 1;
-            s_ob[k] = n;
-            n += s_tot[k];
+#pragma unroll 4
+        for (int p = -1; p < E; ++p) {
+            const int k = pair_key(e, p, E), c = s_tot[k];
+            if (tid < E) (p < e ? s_ob : s_oa)[k] = n;
+            n += p == e ? 2 * c : c;
         }
-        for (int y = e; y < E; ++y) {
-            const int k = (e + 1) * (E + 1) + y + 1;
-            s_oa[k] = n;
-            n += y == e ? 2 * s_tot[k] : s_tot[k];
-        }
-        s_num[e] = n;
-    }
-    __syncthreads();
-    if (tid < E) {
-        int off = 0, c0 = 0;
-        for (int x = 0; x < tid; ++x) {
-            const int tiles = (s_num[x] + kGradTile - 1) / kGradTile;
-            off += tiles * kGradTile;
-            c0 += tiles > 0 ? (tiles + lists.chunk_tiles - 1) / lists.chunk_tiles : 1;
-        }
-        s_off[tid] = off;
-        if (first) {
-            const int t0 = off / kGradTile, tiles = (s_num[tid] + kGradTile - 1) / kGradTile;
-            const int nc = tiles > 0 ? (tiles + lists.chunk_tiles - 1) / lists.chunk_tiles : 1;
-            gst(lists.eoff + tid, off);
-            gst(lists.echunk + tid, c0);
-            // the tiles are shared out evenly
-            for (int c = 0; c < nc; ++c) {
-                SgChunk q;
-                q.e = tid;
-                q.t0 = t0 + (int)((int64_t)tiles * c / nc);
-                q.t1 = t0 + (int)((int64_t)tiles * (c + 1) / nc);
-                q.alone = nc == 1;
-                lists.chunk[c0 + c] = q;
+        const int tiles = tid < E ? (n + kGradTile - 1) / kGradTile : 0;
+        const int nc = tid >= E ? 0 : tiles > 0 ? (tiles + lists.chunk_tiles - 1) / lists.chunk_tiles : 1;
+        int ot = tiles, oc = nc;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int yt = __shfl_up(ot, o, kWave), yc = __shfl_up(oc, o, kWave);
+            if (tid >= o) {
+                ot += yt;
+                oc += yc;
             }
-            if (tid == E - 1) {
-                gst(lists.eoff + E, off + tiles * kGradTile);
-                gst(lists.echunk + E, c0 + nc);
+        }
+        if (tid < E) {
+            s_num[tid] = n;
+            s_off[tid] = (ot - tiles) * kGradTile;
+            s_c0[tid] = oc - nc;
+            if (tid == E - 1) s_c0[E] = oc;
+            if (first) {
+                gst(lists.eoff + tid, (ot - tiles) * kGradTile);
+                gst(lists.echunk + tid, oc - nc);
+                if (tid == E - 1) {
+                    gst(lists.eoff + E, ot * kGradTile);
+                    gst(lists.echunk + E, oc);
+                }
             }
         }
     }
     __syncthreads();
+    if (!first) return;
+    // the chunks: an expert's tiles shared out evenly; run in the order of the
+    // sorted positions they start at, so that the two chunks that hold a row --
+    // one of either expert of its pair -- run at about the same time, and the
+    // second finds the row in a cache.  (Very many chunks stay expert-major.)
+    __shared__ int s_pos[kSortChunks];
+    const int total = s_c0[E];
+    const bool sort = total <= kSortChunks;
+    auto make = [&](int c) {
+        int e = 0;
+        while (s_c0[e + 1] <= c) ++e;
+        const int nc = s_c0[e + 1] - s_c0[e], i = c - s_c0[e];
+        const int tiles = (s_num[e] + kGradTile - 1) / kGradTile;
+        SgChunk q;
+        q.e = e;
+        q.t0 = s_off[e] / kGradTile + (int)((int64_t)tiles * i / nc);
+        q.t1 = s_off[e] / kGradTile + (int)((int64_t)tiles * (i + 1) / nc);
+        q.part = nc == 1 ? -1 : c;
+        return q;
+    };
+    if (!sort) {
+        for (int c = tid; c < total; c += kSegThreads) lists.chunk[c] = make(c);
+        return;
+    }
+    SgChunk q;
+    if (tid < total) {
+        q = make(tid);
+        const int e = q.e, at = q.t0 * kGradTile - s_off[e];  // the chunk's first slot in its list
+        // its key, and an order that follows the positions: the key and the place inside it
+        int key = 0, rest = 0;
+        for (int p = -1; p < E; ++p) {
+            const int k = pair_key(e, p, E), o = (p < e ? s_ob : s_oa)[k];
+            if (o <= at && s_tot[k] > 0) {
+                key = k;
+                rest = at - o;
+            }
+        }
+        // (places inside a key beyond 2^20 rows order as equal)
+        s_pos[tid] = (key << 20) | (rest < (1 << 20) ? rest : (1 << 20) - 1);
+    }
+    __syncthreads();
+    if (tid < total) {
+        const int mine = s_pos[tid];
+        int at = 0;
+        for (int c = 0; c < total; ++c) at += s_pos[c] < mine || (s_pos[c] == mine && c < tid) ? 1 : 0;
+        lists.chunk[at] = q;
+    }
 }
 
 // One placing workgroup (chunk of n_chunks).  LISTS: also writes every expert's

@@ -129,7 +129,7 @@ constexpr int kGradTile = 32;
 // A run of one expert's list tiles: what one workgroup of the outer products sums.
 struct SgChunk {
     int32_t e, t0, t1;  // tiles [t0, t1)
-    int32_t alone;      // the expert's only chunk
+    int32_t part;       // its partial sums' place (expert-major), or -1: the expert's only chunk
 };
 // The experts' slot lists as the segmentation writes them: every expert's slots
 // in sorted-position order, padded to whole tiles (a padding slot repeats a row
@@ -138,8 +138,8 @@ struct SgLists {
     int32_t* eoff;    // [E + 1] first list position
     int32_t* slot;    // 2 * position + k, or -1 (padding)
     int32_t* srow;    // the slot's row
-    SgChunk* chunk;
-    int32_t* echunk;  // [E + 1] first chunk
+    SgChunk* chunk;   // in the order they run
+    int32_t* echunk;  // [E + 1] first chunk, expert-major
     int32_t chunk_tiles;  // most tiles of a chunk
 };
 
@@ -167,19 +167,20 @@ struct SgOuter {
     int32_t unit0;    // first column block (prefix sum)
 };
 // Columns of one column block of the outer products.
-int grad_cols(int r, int dtype);
+int grad_cols(int dtype);
 
 // Workspace of a backward call.
 struct SgGradLayout {
     SgLayout L;     // a segmented SGMM's, its v for every K slice of both sides
     size_t eoff, slot, srow, chunk, echunk;  // the lists (SgLists)
-    size_t coef;    // coefficients: bf16 [prob][side][3 terms][list tile][rc_pad][kGradTile], fp32 [prob][side][list tile][r_pad][kGradTile]
-    size_t part;    // [unit][rank chunk][chunk] partial sums of experts with several chunks (bf16)
+    // coefficients: bf16 [prob][side][list tile][rank block][3 terms][16 ranks][kGradTile],
+    // fp32 [prob][side][list tile][r_pad][kGradTile]
+    size_t coef;
+    size_t part;    // bf16: partial sums of experts with several chunks, [unit][rank chunk][chunk][ranks][columns] (dB: [columns][ranks])
     size_t dgp;     // [prob][T][2] fp32
     size_t total;
     int64_t cap;    // list positions at most
     int chunk_tiles, max_chunks;
-    int rc_pad;     // ranks of a coefficient tile (bf16)
 };
 SgGradLayout sgmm_grad_layout(int64_t T, int64_t total_ks, int E, int r, int n_prob, int n_units, int dtype);
 

@@ -20,12 +20,16 @@
 //          the gradients lose a factor of three to fp32 sums; the third costs
 //          matrix instructions where memory is the bound.
 //   expand the SGMM's.
-//   outer  dA and dB: per (projection, side, column block, chunk of an expert's
-//          list) a product with M = ranks, N = columns and K = slots, bf16 MFMA
-//          16x16x32 with fp32 sums.  A lane reads CPL columns of eight rows and
-//          transposes the block in registers, one v_perm per two values: x and dy
-//          go from memory to the matrix cores without LDS.  The four waves take
-//          every fourth tile and add up through LDS in a fixed order.
+//   outer  dA and dB: per (projection, side, 512-column block, chunk of an
+//          expert's list) a product with M = ranks (64 at most), N = columns and
+//          K = slots, bf16 MFMA 16x16x32 with fp32 sums.  The four waves take 128
+//          columns each and share a tile's coefficients through LDS (global to
+//          LDS directly, two tiles in turn): read by every wave on its own they
+//          were as much L2 traffic as the rows at rank 64 (134 us against 77 for
+//          4096 rows of 8192 columns on either side, 16 experts).  A lane reads
+//          eight columns of eight rows and transposes the block in registers, one
+//          v_perm per two values: x and dy go from memory to the matrix cores
+//          without LDS.
 //   sum    experts with several chunks: their partial sums in chunk order; dg.
 // Every gradient element has one owner per launch: no atomics, bitwise
 // reproducible.
@@ -33,8 +37,13 @@
 // Chunks.  Routing is skewed (Zipf 1.1 over 8 experts: the first is in 60% of the
 // rows), and one workgroup per (block, expert) would wait for the longest list.
 // An expert's list is cut into chunks of at most chunk_tiles tiles, chosen so
-// that a call has about kTargetItems chunks, several rounds of what the chip
-// holds; only experts with more than one chunk pay for partial sums.
+// that a call has about kTargetItems of them, several rounds of what the chip
+// holds, but none so short that its partial sums (4 bytes a rank, column and
+// chunk, written and read back) outweigh the 2 bytes a slot and column that it reads.
+// A row is read once for each of its experts.  (Reading it once, with the sums of
+// all 8 experts of rank 16 in a workgroup's registers, was tried: half the bytes
+// at a third of the bytes in flight, 235 us against 190 for a layer's seven
+// projections at 4096 rows.)
 #include <type_traits>
 
 #include "gfx950.hpp"
@@ -47,49 +56,42 @@ namespace {
 
 size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-constexpr int kTargetItems = 4096;
-constexpr int kMinChunkTiles = 16;  // four per wave: fewer would be mostly the sum at its end
+constexpr int kTargetItems = 2048;
 constexpr int kCoefTerms = 3;
+constexpr int kKB = 512;  // elements of one coefficient block: 16 ranks x kGradTile slots, 1 KB
 
-// Rank blocks (of 16) and columns per lane of the outer products.  From 48
-// ranks on a lane takes four columns instead of eight: accumulators, rows and
-// coefficients together then leave room for three waves per SIMD (one at 64
-// ranks x 8 columns).
-constexpr int outer_cpl(int r16) { return r16 <= 2 ? 8 : 4; }
+constexpr int kCPL = 8;                // columns per lane of the outer products
+constexpr int kOuterCols = 64 * kCPL;  // per workgroup
+constexpr int kSumPer = 4;             // gradient quads per thread of the sum
 
 int rank_chunks(const SgLayout& L) { return (L.r_pad + 63) / 64; }
 int outer_r16(const SgLayout& L) { return L.r_pad <= 64 ? L.r_pad / 16 : 4; }
 
 }  // namespace
 
-int grad_cols(int r, int dtype) {
-    const int r16 = (r + 15) / 16;
-    return dtype == 1 ? 16 * outer_cpl(r16 < 4 ? r16 : 4) : 64;
-}
+int grad_cols(int dtype) { return dtype == 1 ? kOuterCols : 64; }
 
 SgGradLayout sgmm_grad_layout(int64_t T, int64_t total_ks, int E, int r, int n_prob, int n_units, int dtype) {
     SgGradLayout G;
     G.L = sgmm_layout(T, 1, E, r, (int)total_ks);  // one slice each of total_ks problems
     G.cap = (2 * T + (int64_t)E * (kGradTile - 1) + kGradTile - 1) / kGradTile * kGradTile;
-    G.rc_pad = rank_chunks(G.L) * 16 * outer_r16(G.L);
-    const int64_t tiles = G.cap / kGradTile, items = (int64_t)n_units * rank_chunks(G.L) * tiles;
-    int64_t ct = (items + kTargetItems - 1) / kTargetItems;
-    ct = ct < kMinChunkTiles ? kMinChunkTiles : ct;
-    G.chunk_tiles = (int)(dtype == 1 ? (ct < (1 << 30) ? ct : 1 << 30) : 1 << 30);
-    // full chunks (the bounds, not the count, so that it does not fall as T grows), and one more per expert
-    const int64_t by_tiles = tiles / kMinChunkTiles, by_items = kTargetItems / ((int64_t)n_units * rank_chunks(G.L));
-    G.max_chunks = (int)(dtype == 1 ? (by_tiles < by_items ? by_tiles : by_items) + E : E);
+    const int64_t tiles = G.cap / kGradTile, units = (int64_t)n_units * rank_chunks(G.L);
+    const int64_t least = 4 * outer_r16(G.L), even = (units * tiles + kTargetItems - 1) / kTargetItems;
+    G.chunk_tiles = (int)(even > least ? even : least);
+    // full chunks (by bounds that do not fall as T grows) and one more per expert
+    const int64_t by_tiles = tiles / least, by_items = kTargetItems / units;
+    G.max_chunks = (int)(by_tiles < by_items ? by_tiles : by_items) + E;
     size_t o = G.L.total;
     G.eoff = o;    o += a256((size_t)(E + 1) * 4);
     G.slot = o;    o += a256((size_t)G.cap * 4);
     G.srow = o;    o += a256((size_t)G.cap * 4);
-    G.chunk = o;   o += a256((size_t)G.max_chunks * sizeof(SgChunk));
+    G.chunk = o;   o += a256((size_t)(tiles / G.chunk_tiles + E) * sizeof(SgChunk));
     G.echunk = o;  o += a256((size_t)(E + 1) * 4);
     G.coef = o;
-    o += a256(dtype == 1 ? (size_t)n_prob * 2 * kCoefTerms * G.cap * G.rc_pad * 2 : (size_t)n_prob * 2 * G.cap * G.L.r_pad * 4);
+    if (dtype == 0) o += a256((size_t)n_prob * 2 * G.cap * G.L.r_pad * 4);
+    else o += (size_t)n_prob * 2 * tiles * (G.L.r_pad / 16) * kCoefTerms * kKB * 2;
     G.part = o;
-    if (dtype == 1)
-        o += (size_t)n_units * rank_chunks(G.L) * G.max_chunks * (16 * outer_r16(G.L)) * grad_cols(r, dtype) * 4;
+    if (dtype == 1) o += (size_t)units * G.max_chunks * (16 * outer_r16(G.L)) * kOuterCols * 4;
     G.dgp = o;     o += a256((size_t)n_prob * T * 8);
     G.total = o;
     return G;
@@ -140,8 +142,34 @@ __global__ __launch_bounds__(256) void grad_shrink_f32(SgGradArgs a) {
 
 // ---- coefficients -------------------------------------------------------------------
 
-// Eight threads per slot, 16 ranks at a time.  Padding ranks and slots get 0
-// (their v was never written: selected away, not multiplied).
+// Two neighbouring ranks' K slices, eight loads in flight, added in order.
+__device__ __forceinline__ void slice_sum(const float* p, int64_t stride, int n, float (&o)[2]) {
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    for (int k0 = 0; k0 < n; k0 += 8) {
+        f32x2_t v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = gld((const f32x2_t*)(p + (k0 + k < n ? k0 + k : n - 1) * stride));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k0 + k >= n) break;
+            o[0] = k0 + k ? o[0] + v[k].x : v[k].x;
+            o[1] = k0 + k ? o[1] + v[k].y : v[k].y;
+        }
+    }
+}
+
+// x as three bf16 terms (hi, the rest's hi, ...), one to each array's [rank][slot].
+__device__ __forceinline__ void put_terms(uint16_t (*s_c)[16][kGradTile], int rank, int slot, float x) {
+#pragma unroll
+    for (int m = 0; m < kCoefTerms; ++m) {
+        const uint16_t t = f_to_bf(x);
+        s_c[m][rank][slot] = t;
+        x -= bf_to_f(t);
+    }
+}
+
+// Eight threads per slot, 16 ranks at a time.  Padding ranks and
+// slots get 0 (their v was never written: selected away, not multiplied).
 template <bool BF>
 __global__ __launch_bounds__(256) void grad_coefs(SgGradArgs a) {
     const SgLayout& L = a.G.L;
@@ -159,28 +187,18 @@ __global__ __launch_bounds__(256) void grad_coefs(SgGradArgs a) {
     const int64_t stride = L.T_pad * 2 * RPAD;  // floats per K slice
     const float* vu = (const float*)(a.ws + L.v) + P.ks_u * stride + q * RPAD;
     const float* vw = (const float*)(a.ws + L.v) + P.ks_w * stride + q * RPAD;
-    constexpr int kParts = BF ? 2 * kCoefTerms : 2;
     typedef typename std::conditional<BF, uint16_t, float>::type C;
-    __shared__ __attribute__((aligned(16))) C s_c[kParts][16][kGradTile];
+    constexpr int kTerms = BF ? kCoefTerms : 1;
+    __shared__ __attribute__((aligned(16))) C s_c[2 * kTerms][16][kGradTile];
     float dot = 0.f;
-    const int rc = BF ? a.G.rc_pad : RPAD;
     C* coef = (C*)(a.ws + a.G.coef);
-    const int64_t part = a.G.cap * rc;  // elements of one (prob, side, term)
-    typedef float f32x2_t __attribute__((ext_vector_type(2)));
-    for (int r0 = 0; r0 < rc; r0 += 16) {
-        const int rho = r0 + 2 * j;
+    const int64_t list_tiles = a.G.cap / kGradTile, nb = RPAD / 16;
+    for (int b = 0; b < nb; ++b) {
+        const int rho = 16 * b + 2 * j;
         float u[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
         if (live && rho < r) {
-            for (int k = 0; k < P.n_ks_u; ++k) {
-                const f32x2_t v = gld((const f32x2_t*)(vu + k * stride + rho));
-                u[0] = k ? u[0] + v.x : v.x;
-                u[1] = k ? u[1] + v.y : v.y;
-            }
-            for (int k = 0; k < P.n_ks_w; ++k) {
-                const f32x2_t v = gld((const f32x2_t*)(vw + k * stride + rho));
-                w[0] = k ? w[0] + v.x : v.x;
-                w[1] = k ? w[1] + v.y : v.y;
-            }
+            slice_sum(vu + rho, stride, P.n_ks_u, u);
+            slice_sum(vw + rho, stride, P.n_ks_w, w);
             if (rho + 1 >= r) u[1] = w[1] = 0.f;
         }
         dot = fmaf(u[0], w[0], dot);
@@ -188,27 +206,20 @@ __global__ __launch_bounds__(256) void grad_coefs(SgGradArgs a) {
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float x = c * w[k], y = c * u[k];
             if constexpr (BF) {
-#pragma unroll
-                for (int m = 0; m < kCoefTerms; ++m) {
-                    const uint16_t xm = f_to_bf(x), ym = f_to_bf(y);
-                    s_c[m][2 * j + k][s] = xm;
-                    s_c[kCoefTerms + m][2 * j + k][s] = ym;
-                    x -= bf_to_f(xm);
-                    y -= bf_to_f(ym);
-                }
+                put_terms(s_c, 2 * j + k, s, c * w[k]);
+                put_terms(s_c + kTerms, 2 * j + k, s, c * u[k]);
             } else {
-                s_c[0][2 * j + k][s] = x;
-                s_c[1][2 * j + k][s] = y;
+                s_c[0][2 * j + k][s] = c * w[k];
+                s_c[1][2 * j + k][s] = c * u[k];
             }
         }
         __syncthreads();
         constexpr int W = 16 / (int)sizeof(C), kRow = kGradTile / W;  // 16-byte stores per rank row
-        for (int i = tid; i < kParts * 16 * kRow; i += 256) {
-            const int m = i / (16 * kRow), rr = i / kRow % 16, o = W * (i % kRow);
-            st128(coef + ((int64_t)prob * kParts + m) * part + (tile * rc + r0 + rr) * kGradTile + o,
-                  *(const u32x4*)&s_c[m][rr][o]);
+        for (int i = tid; i < 2 * kTerms * 16 * kRow; i += 256) {
+            const int m = i / (16 * kRow), rr = i / kRow % 16, o = W * (i % kRow), side = m / kTerms;
+            const int64_t at = ((((int64_t)prob * 2 + side) * list_tiles + tile) * nb + b) * kTerms + m % kTerms;
+            st128(coef + at * kKB + rr * kGradTile + o, *(const u32x4*)&s_c[m][rr][o]);
         }
     }
     // the slot's eight partial sums, in a fixed order
@@ -240,16 +251,10 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
                                                    0, 0);
 }
 
-typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
-template <int CPL> struct RowRegs;
-template <> struct RowRegs<8> { typedef u32x4 type; };
-template <> struct RowRegs<4> { typedef u32x2v type; };
-
-// The outer product's gradient element(s) of accumulators acc[b][j] (rank block
-// b, column j of the lane): written or added to.
-template <int R16, int CPL>
-__device__ __forceinline__ void store_block(const SgGradArgs& a, const SgOuter& O, int e, int r0, int col, int kg, int b,
-                                            const f32x4 (&acc)[CPL]) {
+// Stores (or adds) columns 4h .. 4h + 3 of a lane's eight, rank block b: acc[j]
+// holds four ranks of column 4h + j.
+__device__ __forceinline__ void store_quad(const SgGradArgs& a, const SgOuter& O, int e, int r0, int col, int kg, int b,
+                                           const f32x4 (&acc)[4]) {
     const int r = a.r, d = O.d, rho = r0 + 16 * b + 4 * kg;  // this lane's four ranks
     if (col >= d) return;
     if (O.side == 0) {
@@ -257,16 +262,13 @@ __device__ __forceinline__ void store_block(const SgGradArgs& a, const SgOuter& 
         for (int i = 0; i < 4; ++i) {
             if (rho + i >= r) continue;
             f32x4* p = (f32x4*)(O.out + ((int64_t)e * r + rho + i) * d + col);
-#pragma unroll
-            for (int h = 0; h < CPL / 4; ++h) {
-                f32x4 o = {acc[4 * h][i], acc[4 * h + 1][i], acc[4 * h + 2][i], acc[4 * h + 3][i]};
-                if (a.accumulate) o += gld(p + h);
-                gst(p + h, o);
-            }
+            f32x4 o = {acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+            if (a.accumulate) o += gld(p);
+            gst(p, o);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) {
+        for (int j = 0; j < 4; ++j) {
             float* p = O.out + ((int64_t)e * d + col + j) * r + rho;
             if ((r & 3) == 0) {
                 if (rho >= r) continue;
@@ -282,15 +284,32 @@ __device__ __forceinline__ void store_block(const SgGradArgs& a, const SgOuter& 
     }
 }
 
-// Partial sums of item (unit, rank chunk, chunk): [b][j][lane] f32x4.
-template <int R16, int CPL> __device__ __forceinline__ f32x4* part_of(const SgGradArgs& a, int64_t unit, int n_ch, int ch, int c) {
-    return (f32x4*)(a.ws + a.G.part) + ((unit * n_ch + ch) * a.G.max_chunks + c) * (R16 * CPL * kWave);
+// The same into a partial tile of NR ranks and NC columns: [rank][column] for
+// dA, [column][rank] for dB (lc: the quad's first column in the tile).
+__device__ __forceinline__ void store_part(float* part, int side, int NR, int NC, int lc, int rho, const f32x4 (&acc)[4]) {
+    if (side == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            gst((f32x4*)(part + (int64_t)(rho + i) * NC + lc), f32x4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]});
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) gst((f32x4*)(part + (int64_t)(lc + j) * NR + rho), acc[j]);
+    }
+}
+
+// Column j of the 8x8 block whose row i is v[i]: one v_perm per two values.
+__device__ __forceinline__ u32x4 column(const u32x4 (&v)[8], int j) {
+    u32x4 o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        o[q] = __builtin_amdgcn_perm(v[2 * q + 1][j / 2], v[2 * q][j / 2], (j & 1) ? 0x07060302u : 0x05040100u);
+    return o;
 }
 
 template <int R16>
-__global__ __launch_bounds__(256) void grad_outer_bf16(SgGradArgs a, int n_ch) {
-    constexpr int CPL = outer_cpl(R16);
-    typedef typename RowRegs<CPL>::type Row;
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(R16 == 1 ? 3 : 2)))
+void grad_outer_bf16(SgGradArgs a, int n_ch) {
+    constexpr int CPL = kCPL, kCols = kOuterCols, NR = 16 * R16;
     if (rejected(a)) return;
     // XCD b % 8 takes every eighth column block, its chunks (and rank chunks) one after another
     const int per_unit = a.G.max_chunks * n_ch;
@@ -303,21 +322,22 @@ __global__ __launch_bounds__(256) void grad_outer_bf16(SgGradArgs a, int n_ch) {
     const SgOuter O = a.outers[a.unit_outer[unit]];
     const int32_t* srow = (const int32_t*)(a.ws + a.G.srow);
     const int lane = lane_id(), w = wave_id(), n = lane & 15, kg = lane >> 4;
-    const int d = uniform(O.d), rc = a.G.rc_pad, r0 = ch * 64, t1 = K.t1;
-    const int col = (int)(unit - O.unit0) * (16 * CPL) + CPL * n;
-    const int lcol = col < d ? col : 0;  // columns past the end read the first ones and are not stored
+    const int d = uniform(O.d), t0 = uniform(K.t0), t1 = uniform(K.t1);
+    const int lc = w * 16 * CPL + CPL * n, col = (int)(unit - O.unit0) * kCols + lc;
+    const int lcol = col < d ? col : 0;          // columns past the end read the first ones and are not stored
+    const bool mine = col - CPL * n < d;         // this wave has columns (else it only helps with the coefficients)
     const uint16_t* __restrict__ act = (const uint16_t*)O.act + lcol;
-    const int64_t part = a.G.cap * rc;
+    const int nb = a.G.L.r_pad / 16, b0 = ch * 4, my_b = nb - b0 < R16 ? nb - b0 : R16;
     const uint16_t* __restrict__ coef = (const uint16_t*)(a.ws + a.G.coef) +
-                                        ((int64_t)O.prob * 2 + O.side) * kCoefTerms * part +
-                                        (r0 + n) * kGradTile + 8 * kg;
+                                        ((int64_t)O.prob * 2 + O.side) * (a.G.cap / kGradTile) * nb * kCoefTerms * kKB;
 
+    __shared__ __attribute__((aligned(16))) uint16_t s_c[2][R16 * kCoefTerms * kKB];
     f32x4 acc[R16][CPL];
 #pragma unroll
     for (int b = 0; b < R16; ++b)
 #pragma unroll
         for (int j = 0; j < CPL; ++j) acc[b][j] = f32x4{};
-    Row v[8];
+    u32x4 v[8];
     int rows[8];
     auto load_rows = [&](int t) {
         const u32x4 a0 = ld128(srow + t * kGradTile + 8 * kg), a1 = ld128(srow + t * kGradTile + 8 * kg + 4);
@@ -329,109 +349,128 @@ __global__ __launch_bounds__(256) void grad_outer_bf16(SgGradArgs a, int n_ch) {
     };
     auto load_x = [&]() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = gld((const Row*)(act + (int64_t)rows[i] * d));
+        for (int i = 0; i < 8; ++i) v[i] = ld128(act + (int64_t)rows[i] * d);
     };
-    int t = K.t0 + w;
-    if (t < t1) {
-        load_rows(t);
-        load_x();
-        if (t + 4 < t1) load_rows(t + 4);
+    auto copy_coefs = [&](int t) {
+        const uint16_t* src = coef + ((int64_t)t * nb + b0) * kCoefTerms * kKB + 8 * lane;
+#pragma unroll
+        for (int i = 0; i < (R16 * kCoefTerms + 3) / 4; ++i) {
+            const int k = w + 4 * i;
+            if (k < my_b * kCoefTerms) copy16_to_lds(src + k * kKB, s_c[t & 1] + k * kKB);
+        }
+    };
+    if (t0 < t1) {
+        load_rows(t0);
+        copy_coefs(t0);
+        if (mine) load_x();
+        if (t0 + 1 < t1) load_rows(t0 + 1);
     }
 #pragma unroll 1
-    for (; t < t1; t += 4) {
-        // this tile's coefficients go out before the next tile's rows, so
-        // waiting for them does not wait for those
-        u32x4 h[R16][kCoefTerms];
-#pragma unroll
-        for (int b = 0; b < R16; ++b)
-#pragma unroll
-            for (int m = 0; m < kCoefTerms; ++m)
-                h[b][m] = ld128(coef + m * part + ((int64_t)t * rc + 16 * b) * kGradTile);
-        // column j of the 8 x CPL block: one v_perm per two values
+    for (int t = t0; t < t1; ++t) {
+        // everything loaded for this tile has landed, in every wave, and every
+        // wave is done with the tile before, whose half of s_c is free again
+        wait_vmcnt<0>();
+        __syncthreads();
         u32x4 x[CPL];
 #pragma unroll
-        for (int j = 0; j < CPL; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                x[j][q] = __builtin_amdgcn_perm(v[2 * q + 1][j / 2], v[2 * q][j / 2], (j & 1) ? 0x07060302u : 0x05040100u);
-        if (t + 4 < t1) {
-            load_x();
-            if (t + 8 < t1) load_rows(t + 8);
+        for (int j = 0; j < CPL; ++j) x[j] = column(v, j);
+        if (t + 1 < t1) {
+            copy_coefs(t + 1);
+            if (mine) load_x();
+            if (t + 2 < t1) load_rows(t + 2);
         }
+        if (mine) {
+            const uint16_t* s = s_c[t & 1] + n * kGradTile + 8 * kg;
 #pragma unroll
-        for (int b = 0; b < R16; ++b)
+            for (int b = 0; b < R16; ++b) {
+                if (R16 == 4 && b >= my_b) break;  // the last rank chunk may have fewer blocks
 #pragma unroll
-            for (int m = 0; m < kCoefTerms; ++m)
+                for (int m = 0; m < kCoefTerms; ++m) {
+                    const u32x4 h = *(const u32x4*)(s + (b * kCoefTerms + m) * kKB);
 #pragma unroll
-                for (int j = 0; j < CPL; ++j) acc[b][j] = mfma16(h[b][m], x[j], acc[b][j]);
-    }
-    // the four waves' sums: (0 + 2) + (1 + 3)
-    __shared__ f32x4 s_red[2][R16 * CPL][kWave];
-    if (w >= 2) {
-#pragma unroll
-        for (int b = 0; b < R16; ++b)
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) s_red[w - 2][b * CPL + j][lane] = acc[b][j];
-    }
-    __syncthreads();
-    if (w < 2) {
-#pragma unroll
-        for (int b = 0; b < R16; ++b)
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) acc[b][j] += s_red[w][b * CPL + j][lane];
-    }
-    __syncthreads();
-    if (w == 1) {
-#pragma unroll
-        for (int b = 0; b < R16; ++b)
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) s_red[0][b * CPL + j][lane] = acc[b][j];
-    }
-    __syncthreads();
-    if (w != 0) return;
-#pragma unroll
-    for (int b = 0; b < R16; ++b) {
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) acc[b][j] += s_red[0][b * CPL + j][lane];
-        if (K.alone) {
-            store_block<R16, CPL>(a, O, K.e, r0, col, kg, b, acc[b]);
-        } else {
-            f32x4* p = part_of<R16, CPL>(a, unit, n_ch, ch, c) + b * CPL * kWave + lane;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) gst(p + j * kWave, acc[b][j]);
+                    for (int j = 0; j < CPL; ++j) acc[b][j] = mfma16(h, x[j], acc[b][j]);
+                }
+            }
         }
     }
+    if (!mine) return;
+    float* part = (float*)(a.ws + a.G.part) + ((unit * n_ch + ch) * a.G.max_chunks + (K.part < 0 ? 0 : K.part)) * (int64_t)(NR * kCols);
+#pragma unroll
+    for (int b = 0; b < R16; ++b)
+#pragma unroll
+        for (int h = 0; h < CPL / 4; ++h) {
+            const f32x4 q[4] = {acc[b][4 * h], acc[b][4 * h + 1], acc[b][4 * h + 2], acc[b][4 * h + 3]};
+            if (K.part < 0) store_quad(a, O, K.e, ch * 64, col + 4 * h, kg, b, q);
+            else store_part(part, O.side, NR, kCols, lc + 4 * h, 16 * b + 4 * kg, q);
+        }
 }
 
-// Item (unit, rank chunk, expert): an expert with several chunks gets the sum of
-// their partials in chunk order, one rank block per wave and turn.  The
-// workgroups past the items write dg.
-template <int R16>
-__global__ __launch_bounds__(256) void grad_sum_bf16(SgGradArgs a, int n_ch, int64_t n_items) {
-    constexpr int CPL = outer_cpl(R16);
+// ---- partial sums
+
+// Four gradient elements (a quad) at a time of (unit, rank chunk, expert): the
+// expert's partial tiles added in chunk order, kSumPer quads per thread, whose
+// loads go out together.  The workgroups past the items write dg.
+__global__ __launch_bounds__(256) void grad_sum_bf16(SgGradArgs a, int n_ch, int64_t n_items, int per_item) {
     if (rejected(a)) return;
-    if (blockIdx.x >= n_items) {
-        write_dg(a, (blockIdx.x - n_items) * 256 + threadIdx.x);
+    if (blockIdx.x >= n_items * per_item) {
+        write_dg(a, (blockIdx.x - n_items * per_item) * 256 + threadIdx.x);
         return;
     }
-    const int e = blockIdx.x % a.E, ch = blockIdx.x / a.E % n_ch;
-    const int64_t unit = blockIdx.x / a.E / n_ch;
+    const int64_t item = blockIdx.x / per_item;
+    const int e = (int)(item % a.E), ch = (int)(item / a.E) % n_ch;
+    const int64_t unit = item / a.E / n_ch;
     const int32_t* echunk = (const int32_t*)(a.ws + a.G.echunk);
-    const int c0 = uniform(gld(echunk + e)), c1 = uniform(gld(echunk + e + 1));
-    if (c1 - c0 < 2) return;
+    const int c0 = uniform(gld(echunk + e)), nc = uniform(gld(echunk + e + 1)) - c0;
+    if (nc < 2) return;
+    constexpr int cols = kOuterCols;
+    const int r = a.r, nb = a.G.L.r_pad / 16, NR = 16 * (nb < 4 ? nb : 4);  // ranks of a partial tile
     const SgOuter O = a.outers[a.unit_outer[unit]];
-    const int lane = lane_id(), n = lane & 15, kg = lane >> 4;
-    const int col = (int)(unit - O.unit0) * (16 * CPL) + CPL * n;
-    for (int b = wave_id(); b < R16; b += 4) {
-        f32x4 acc[CPL];
+    const int64_t step = (int64_t)NR * cols;
+    const float* p = (const float*)(a.ws + a.G.part) + ((unit * n_ch + ch) * a.G.max_chunks + c0) * step;
+    const int u0 = (int)(unit - O.unit0) * cols;  // the tile's first column
+    f32x4 acc[kSumPer];
+    int i[kSumPer];
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) acc[j] = f32x4{};
-        for (int c = c0; c < c1; ++c) {
-            const f32x4* p = part_of<R16, CPL>(a, unit, n_ch, ch, c) + b * CPL * kWave + lane;
+    for (int q = 0; q < kSumPer; ++q) {
+        i[q] = ((int)(blockIdx.x % per_item) * kSumPer + q) * 256 + threadIdx.x;
+        if (i[q] >= NR * cols / 4) i[q] = -1;
+        acc[q] = gld((const f32x4*)p + (i[q] < 0 ? 0 : i[q]));
+    }
+    for (int c = 1; c < nc; c += 2) {
+        f32x4 y[kSumPer], z[kSumPer];
 #pragma unroll
-            for (int j = 0; j < CPL; ++j) acc[j] += gld(p + j * kWave);
+        for (int q = 0; q < kSumPer; ++q) {
+            const int at = i[q] < 0 ? 0 : i[q];
+            y[q] = gld((const f32x4*)(p + c * step) + at);
+            z[q] = gld((const f32x4*)(p + (c + 1 < nc ? c + 1 : c) * step) + at);
         }
-        store_block<R16, CPL>(a, O, e, ch * 64, col, kg, b, acc);
+#pragma unroll
+        for (int q = 0; q < kSumPer; ++q) {
+            acc[q] += y[q];
+            if (c + 1 < nc) acc[q] += z[q];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kSumPer; ++q) {
+        // the quad's place: four columns of a rank (dA), four ranks of a column (dB)
+        const int rho = 64 * ch + (O.side == 0 ? i[q] / (cols / 4) : 4 * (i[q] % (NR / 4)));
+        const int col = u0 + (O.side == 0 ? 4 * (i[q] % (cols / 4)) : i[q] / (NR / 4));
+        if (i[q] < 0 || rho >= r || col >= O.d) continue;
+        if (O.side == 0) {
+            f32x4* o = (f32x4*)(O.out + ((int64_t)e * r + rho) * O.d + col);
+            if (a.accumulate) acc[q] += gld(o);
+            gst(o, acc[q]);
+        } else {
+            float* o = O.out + ((int64_t)e * O.d + col) * r + rho;
+            if ((r & 3) == 0) {
+                if (a.accumulate) acc[q] += gld((const f32x4*)o);
+                gst((f32x4*)o, acc[q]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (rho + k < r) gst(o + k, a.accumulate ? gld(o + k) + acc[q][k] : acc[q][k]);
+            }
+        }
     }
 }
 
@@ -496,30 +535,24 @@ int64_t dg_blocks(const SgGradArgs& a) { return a.dg ? (2 * a.T + 255) / 256 : 0
 int64_t outer_blocks(const SgGradArgs& a) {
     return 8ll * a.G.max_chunks * rank_chunks(a.G.L) * ((a.n_units + 7) / 8);
 }
-int64_t sum_items(const SgGradArgs& a) { return (int64_t)a.n_units * rank_chunks(a.G.L) * a.E; }
-
-template <int R16> hipError_t launch_outer(const SgGradArgs& a, hipStream_t s) {
-    const int n_ch = rank_chunks(a.G.L);
-    hipLaunchKernelGGL(grad_outer_bf16<R16>, dim3((unsigned)outer_blocks(a)), dim3(256), 0, s, a, n_ch);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    // no expert can have a second chunk while a chunk holds every tile
-    const int64_t items = a.G.max_chunks > a.E ? sum_items(a) : 0;
-    if (items + dg_blocks(a) == 0) return hipSuccess;
-    hipLaunchKernelGGL(grad_sum_bf16<R16>, dim3((unsigned)(items + dg_blocks(a))), dim3(256), 0, s, a, n_ch, items);
-    return hipGetLastError();
+// Items of the sum (none where no expert can have a second chunk) and workgroups per item.
+int64_t sum_items(const SgGradArgs& a) {
+    if (a.G.max_chunks <= a.E) return 0;
+    return (int64_t)a.n_units * rank_chunks(a.G.L) * a.E;
 }
+int sum_blocks(const SgGradArgs& a) { return (16 * outer_r16(a.G.L) * kOuterCols / 4 + 256 * kSumPer - 1) / (256 * kSumPer); }
 
 }  // namespace
 
 bool sgmm_grad_fits(const SgGradArgs& a, int dtype) {
     return grad_prep_fits(a) && grid_fits(a.G.cap / kGradTile, 256) && grid_fits((a.T + 1) / 2, 256) &&
            grid_fits(a.n_units + dg_blocks(a), 256) &&
-           (dtype == 0 || (grid_fits(outer_blocks(a), 256) && grid_fits(sum_items(a) + dg_blocks(a), 256)));
+           (dtype == 0 || (grid_fits(outer_blocks(a), 256) && grid_fits(sum_items(a) * sum_blocks(a) + dg_blocks(a), 256)));
 }
 
 hipError_t launch_grad_zero(const SgGradArgs& a, int dtype, hipStream_t s) {
-    hipLaunchKernelGGL(grad_zero, dim3((unsigned)a.n_units, (unsigned)a.E), dim3(kWave), 0, s, a, grad_cols(a.r, dtype));
+    hipLaunchKernelGGL(grad_zero, dim3((unsigned)a.n_units, (unsigned)a.E), dim3(kWave), 0, s, a,
+                       grad_cols(dtype));
     return hipGetLastError();
 }
 
@@ -541,12 +574,20 @@ hipError_t launch_grad_outer(const SgGradArgs& a, int dtype, hipStream_t s) {
                            dim3(256), 0, s, a, a.n_units);
         return hipGetLastError();
     }
+    const int n_ch = rank_chunks(a.G.L);
+    const dim3 g((unsigned)outer_blocks(a));
     switch (outer_r16(a.G.L)) {
-        case 1: return launch_outer<1>(a, s);
-        case 2: return launch_outer<2>(a, s);
-        case 3: return launch_outer<3>(a, s);
-        default: return launch_outer<4>(a, s);
+        case 1: hipLaunchKernelGGL(grad_outer_bf16<1>, g, dim3(256), 0, s, a, n_ch); break;
+        case 2: hipLaunchKernelGGL(grad_outer_bf16<2>, g, dim3(256), 0, s, a, n_ch); break;
+        case 3: hipLaunchKernelGGL(grad_outer_bf16<3>, g, dim3(256), 0, s, a, n_ch); break;
+        default: hipLaunchKernelGGL(grad_outer_bf16<4>, g, dim3(256), 0, s, a, n_ch); break;
     }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t blocks = sum_items(a) * sum_blocks(a) + dg_blocks(a);
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(grad_sum_bf16, dim3((unsigned)blocks), dim3(256), 0, s, a, n_ch, sum_items(a), sum_blocks(a));
+    return hipGetLastError();
 }
 
 }  // namespace dlm
