@@ -15,6 +15,7 @@ fallback: if the library is missing or fails to load, importing the ops raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import re
 
@@ -225,13 +226,17 @@ def _rows(t: torch.Tensor, name: str):
     return T, E, ld
 
 
-def _here(t: torch.Tensor, stream, name: str):
-    """The library launches on the current device: tensors and stream belong to it."""
-    dev = torch.cuda.current_device()
+def _here(t: torch.Tensor, stream, name: str) -> int:
+    """The library launches on the current device: tensors and stream belong to
+    it.  Returns the stream's handle."""
+    dev = torch._C._cuda_getDevice()
     if t.device.index != dev:
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
-    if stream is not None and stream.device.index != dev:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
         raise ValueError(f"the stream belongs to {stream.device}, but the current device is cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _fresh(stream, *tensors):
@@ -243,10 +248,16 @@ def _fresh(stream, *tensors):
                 t.record_stream(stream)
 
 
+@functools.lru_cache(maxsize=64)
 def _route_cfg(k, score, n_groups, keep_groups, group_top, renorm, scale):
     if score not in _SCORES:
         raise ValueError(f"score is one of {sorted(_SCORES)}, got {score!r}")
-    return dlm_route_cfg(k, _SCORES[score], n_groups, keep_groups, group_top, 1 if renorm else 0, scale)
+    return C.byref(dlm_route_cfg(k, _SCORES[score], n_groups, keep_groups, group_top, 1 if renorm else 0, scale))
+
+
+def _ptr(t):
+    """A tensor's address as ctypes takes it, None for None."""
+    return None if t is None else t.data_ptr()
 
 
 def route(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, n_groups: int = 1, keep_groups: int = 1,
@@ -257,20 +268,22 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, n_gro
     the chosen or not -> idx [T][k] int32, g [T][k] fp32 (device).  -inf marks an
     expert the row may not use; counts [E] int32 is added to."""
     T, E, ld = _rows(logits, "logits")
-    _here(logits, stream, "logits")
+    handle = _here(logits, stream, "logits")
     if bias is not None:
         _like(bias, "bias", (E,), torch.float32, logits.device)
     if counts is not None:
         _like(counts, "counts", (E,), torch.int32, logits.device)
     if idx is None:
         idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    else:
+        _like(idx, "route idx", (T, k), torch.int32, logits.device)
     if g is None:
         g = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    _like(idx, "route idx", (T, k), torch.int32, logits.device)
-    _like(g, "route g", (T, k), torch.float32, logits.device)
-    cfg = _route_cfg(k, score, n_groups, keep_groups, group_top, renorm, scale)
-    _check(load().dlm_route(_p(logits), ld, _p(bias), T, E, _dt(logits), C.byref(cfg), _p(idx), _p(g), _p(counts),
-                            _stream(stream)), "dlm_route")
+    else:
+        _like(g, "route g", (T, k), torch.float32, logits.device)
+    cfg = _route_cfg(k, score, n_groups, keep_groups, group_top, bool(renorm), float(scale))
+    _check(load().dlm_route(logits.data_ptr(), ld, _ptr(bias), T, E, _dt(logits), cfg, idx.data_ptr(), g.data_ptr(),
+                            _ptr(counts), handle), "dlm_route")
     _fresh(stream, idx, g)
     return idx, g
 
@@ -280,20 +293,21 @@ def route_backward(logits: torch.Tensor, idx: torch.Tensor, dg: torch.Tensor, sc
     """dLoss/dlogits [T][E] (logits' dtype; returned) from dg [T][k] = dLoss/dg of
     route()'s weights for its choice idx [T][k]."""
     T, E, ld = _rows(logits, "logits")
-    _here(logits, stream, "logits")
+    handle = _here(logits, stream, "logits")
     if idx.dim() != 2:
         raise ValueError("idx must be [T][k]")
     k = idx.shape[1]
     _like(idx, "idx", (T, k), torch.int32, logits.device)
     _like(dg, "dg", (T, k), torch.float32, logits.device)
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    Td, Ed, ldd = _rows(dlogits, "dlogits")
-    if (Td, Ed) != (T, E) or dlogits.dtype != logits.dtype or dlogits.device != logits.device:
-        raise ValueError("dlogits must have logits' shape, dtype and device")
-    cfg = _route_cfg(k, score, 1, 1, 1, renorm, scale)
-    _check(load().dlm_route_backward(_p(logits), ld, _p(idx), _p(dg), T, E, _dt(logits), C.byref(cfg), _p(dlogits), ldd,
-                                     _stream(stream)), "dlm_route_backward")
+        dlogits, ldd = torch.empty((T, E), dtype=logits.dtype, device=logits.device), max(E, 1)
+    else:
+        Td, Ed, ldd = _rows(dlogits, "dlogits")
+        if (Td, Ed) != (T, E) or dlogits.dtype != logits.dtype or dlogits.device != logits.device:
+            raise ValueError("dlogits must have logits' shape, dtype and device")
+    cfg = _route_cfg(k, score, 1, 1, 1, bool(renorm), float(scale))
+    _check(load().dlm_route_backward(logits.data_ptr(), ld, idx.data_ptr(), dg.data_ptr(), T, E, _dt(logits), cfg,
+                                     dlogits.data_ptr(), ldd, handle), "dlm_route_backward")
     _fresh(stream, dlogits)
     return dlogits
 
@@ -585,7 +599,7 @@ class SgmmGroup:
         fp32, if given, is the gradient of g.  Returns the workspace, whose status
         word sgmm_status() reads (a rejected set leaves every buffer unchanged)."""
         _need(idx, "idx")
-        _here(idx, stream, "idx")
+        handle = _here(idx, stream, "idx")
         T = idx.shape[0] if T is None else T
         if not 0 <= T <= self.rows:
             raise ValueError(f"T={T} rows, but the group's problems hold {self.rows}")
@@ -596,8 +610,8 @@ class SgmmGroup:
         own = workspace is None
         if own:
             workspace = self.backward_workspace(T)
-        _check(load().dlm_sgmm_group_backward(self._h, _p(idx), _p(g), _p(dg), T, 1 if accumulate else 0, _p(workspace),
-                                              _ws_bytes(workspace), _stream(stream)), "dlm_sgmm_group_backward")
+        _check(load().dlm_sgmm_group_backward(self._h, _ptr(idx), _ptr(g), _ptr(dg), T, 1 if accumulate else 0,
+                                              _ptr(workspace), _ws_bytes(workspace), handle), "dlm_sgmm_group_backward")
         if own:
             _fresh(stream, workspace)
         return workspace
@@ -684,13 +698,12 @@ class AdamW:
     def step(self, lr: float, lr_scale=None, grad_scale=None, stream=None):
         """One step.  lr_scale / grad_scale: optional fp32 [1] device tensors that
         multiply lr / the gradients, read when the step runs."""
-        _here(self.params[0], stream, "parameter 0")
+        handle = _here(self.params[0], stream, "parameter 0")
         for t, name in ((lr_scale, "lr_scale"), (grad_scale, "grad_scale")):
             if t is not None:
                 _like(t, name, (1,), torch.float32, self.device)
         cfg = dlm_adamw_cfg(float(lr), self.beta1, self.beta2, self.eps)
-        _check(load().dlm_adamw_step(self._h, C.byref(cfg), _p(lr_scale), _p(grad_scale), _stream(stream)),
-               "dlm_adamw_step")
+        _check(load().dlm_adamw_step(self._h, C.byref(cfg), _ptr(lr_scale), _ptr(grad_scale), handle), "dlm_adamw_step")
 
     def status(self, stream=None):
         """(steps taken, DLM_OK or DLM_EDEVICE: some gradient was not finite); clears the error."""
@@ -726,12 +739,12 @@ def adamw_read_state(m, v, m_scale, v_scale, m_out=None, v_out=None, stream=None
     _like(v, "v", (n,), torch.uint8, m.device)
     _like(m_scale, "m_scale", (nb,), torch.float32, m.device)
     _like(v_scale, "v_scale", (nb,), torch.float32, m.device)
-    _here(m, stream, "m")
+    handle = _here(m, stream, "m")
     m_out = torch.empty(n, device=m.device) if m_out is None else m_out
     v_out = torch.empty(n, device=m.device) if v_out is None else v_out
     _like(m_out, "m_out", (n,), torch.float32, m.device)
     _like(v_out, "v_out", (n,), torch.float32, m.device)
-    _check(load().dlm_adamw_read_state(_p(m), _p(v), _p(m_scale), _p(v_scale), n, _p(m_out), _p(v_out), _stream(stream)),
+    _check(load().dlm_adamw_read_state(_p(m), _p(v), _p(m_scale), _p(v_scale), n, _p(m_out), _p(v_out), handle),
            "dlm_adamw_read_state")
     _fresh(stream, m_out, v_out)
     return m_out, v_out

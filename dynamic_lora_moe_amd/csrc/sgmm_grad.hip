@@ -56,7 +56,7 @@ namespace {
 
 size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-constexpr int kTargetItems = 2048;
+constexpr int kTargetItems = 1536;
 constexpr int kCoefTerms = 3;
 constexpr int kKB = 512;  // elements of one coefficient block: 16 ranks x kGradTile slots, 1 KB
 
@@ -76,7 +76,7 @@ SgGradLayout sgmm_grad_layout(int64_t T, int64_t total_ks, int E, int r, int n_p
     G.L = sgmm_layout(T, 1, E, r, (int)total_ks);  // one slice each of total_ks problems
     G.cap = (2 * T + (int64_t)E * (kGradTile - 1) + kGradTile - 1) / kGradTile * kGradTile;
     const int64_t tiles = G.cap / kGradTile, units = (int64_t)n_units * rank_chunks(G.L);
-    const int64_t least = 4 * outer_r16(G.L), even = (units * tiles + kTargetItems - 1) / kTargetItems;
+    const int64_t least = 8 * outer_r16(G.L), even = (units * tiles + kTargetItems - 1) / kTargetItems;
     G.chunk_tiles = (int)(even > least ? even : least);
     // full chunks (by bounds that do not fall as T grows) and one more per expert
     const int64_t by_tiles = tiles / least, by_items = kTargetItems / units;
