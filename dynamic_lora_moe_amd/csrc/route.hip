@@ -13,15 +13,19 @@
 //
 // L lanes hold one token's row, V experts each (L x V >= E), so a wave holds
 // 64 / L tokens and a reduction over a token takes log2(L) DPP steps for all of
-// them at once.  Few lanes with many experts each are the cheaper split: a
-// round of the top-k costs V compares and log2(L) steps per wave, 64 / L tokens.
+// them at once.  The kernels are bound by instruction issue (binary64 scores of
+// every expert, then the selection), so few lanes with many experts each are the
+// cheaper split.
 //
 // A key carries its expert in its nine lowest mantissa bits (the complement
 // for a positive key), so one binary64 maximum is an argmax with ties to the
-// lower index, all keys differ, and the next round's candidates are the keys
-// below the last winner: nothing is removed or marked.  Logits leave those
-// bits empty (24 significant bits of 53); of a score plus bias they cut what
-// lies 2^-43 below it.
+// lower index, and all keys differ.  Logits leave those bits empty (24
+// significant bits of 53); of a score plus bias they cut what lies 2^-43 below
+// it.  The k largest: each lane sorts its keys in lists of 4, 8 or 16 (k rounded
+// up; Batcher's odd-even network) and merges them, then the lanes' lists merge
+// pairwise; of two descending lists the largest are max(a[i], b[N - 1 - i]).
+#include <type_traits>
+
 #include "gfx950.hpp"
 #include "internal.hpp"
 #include "route.hpp"
@@ -34,27 +38,113 @@ constexpr int kIdxBits = 9;
 constexpr int kIdxMask = (1 << kIdxBits) - 1;
 static_assert(kRouteMaxExperts <= kIdxMask + 1, "an expert fits the key's index bits");
 
-template <int CTRL> __device__ __forceinline__ double dpp_f64(double v) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xf, 0xf, true);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf, true);
-    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+// No operand is ever a NaN here (checked where keys are made).  As instructions
+// of their own: the compiler's fmax first quiets both operands, an instruction each.
+__device__ __forceinline__ double max2(double a, double b) {
+    double d;
+    asm("v_max_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+    return d;
 }
+__device__ __forceinline__ double min2(double a, double b) {
+    double d;
+    asm("v_min_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+    return d;
+}
+
+// A double from another lane of the row.  A DPP operand must have been written
+// two wait states before; the compiler does not see that those above write one,
+// so the wait is here.
+#define DLM_DPP_F64(NAME, CTRL)                                                             \
+    __device__ __forceinline__ double NAME(double v) {                                      \
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);                                 \
+        uint32_t lo, hi;                                                                    \
+        asm("s_nop 1\n\tv_mov_b32_dpp %0, %2 " CTRL " row_mask:0xf bank_mask:0xf\n\t"        \
+            "v_mov_b32_dpp %1, %3 " CTRL " row_mask:0xf bank_mask:0xf"                      \
+            : "=&v"(lo), "=&v"(hi)                                                          \
+            : "v"((uint32_t)b), "v"((uint32_t)(b >> 32)));                                  \
+        return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);                       \
+    }
+DLM_DPP_F64(dpp_xor1, "quad_perm:[1,0,3,2]")
+DLM_DPP_F64(dpp_xor2, "quad_perm:[2,3,0,1]")
+DLM_DPP_F64(dpp_half_mirror, "row_half_mirror")
+DLM_DPP_F64(dpp_mirror, "row_mirror")
+#undef DLM_DPP_F64
 
 // The other operand of step STEP of a reduction over a row of lanes: within a
 // quad, between quads (half-row mirror), between half rows (row mirror) and
 // between rows.  Every lane ends with the same bits (the operands of a step
 // are the same two partial results in either order).
 template <int STEP> __device__ __forceinline__ double peer(double v) {
-    if constexpr (STEP == 1) return dpp_f64<0xB1>(v);
-    else if constexpr (STEP == 2) return dpp_f64<0x4E>(v);
-    else if constexpr (STEP == 4) return dpp_f64<0x141>(v);
-    else if constexpr (STEP == 8) return dpp_f64<0x140>(v);
+    if constexpr (STEP == 1) return dpp_xor1(v);
+    else if constexpr (STEP == 2) return dpp_xor2(v);
+    else if constexpr (STEP == 4) return dpp_half_mirror(v);
+    else if constexpr (STEP == 8) return dpp_mirror(v);
     else return __shfl_xor(v, STEP, kWave);
 }
 
-// No operand is ever a NaN here (checked where keys are made).
-__device__ __forceinline__ double max2(double a, double b) { return __builtin_fmax(a, b); }
+// Comparators of Batcher's odd-even merge sort of N = 4, 8 or 16 values.
+template <int N> struct Network {
+    int n = 0;
+    int8_t lo[64] = {}, hi[64] = {};
+    constexpr Network() {
+        for (int p = 1; p < N; p *= 2)
+            for (int k = p; k >= 1; k /= 2)
+                for (int j = k % p; j <= N - 1 - k; j += 2 * k)
+                    for (int i = 0; i < k && i < N - j - k; ++i)
+                        if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                            lo[n] = (int8_t)(i + j);
+                            hi[n] = (int8_t)(i + j + k);
+                            ++n;
+                        }
+    }
+};
+template <int N> __device__ __forceinline__ void sort_descending(double* k) {
+    constexpr Network<N> net;
+#pragma unroll
+    for (int c = 0; c < net.n; ++c) {
+        const double a = k[net.lo[c]], b = k[net.hi[c]];
+        k[net.lo[c]] = max2(a, b);
+        k[net.hi[c]] = min2(a, b);
+    }
+}
+// a <- the largest N of two descending lists of N, descending: the larger of
+// a[i] and b[N - 1 - i] are those N as a bitonic sequence, which log2(N) steps sort.
+template <int N> __device__ __forceinline__ void merge_top(double* a, const double (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = max2(a[i], b[N - 1 - i]);
+#pragma unroll
+    for (int h = N / 2; h >= 1; h /= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if ((i & h) == 0) {
+                const double x = a[i], y = a[i + h];
+                a[i] = max2(x, y);
+                a[i + h] = min2(x, y);
+            }
+}
+template <int N, int STEP> __device__ __forceinline__ void merge_peer(double* a) {
+    double b[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] = peer<STEP>(a[i]);
+    merge_top<N>(a, b);
+}
+// The largest D keys of a token, descending, in key[0 .. D) of each of its lanes.
+template <int L, int V, int D> __device__ __forceinline__ void top_keys(double (&key)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += D) sort_descending<D>(key + i);
+#pragma unroll
+    for (int i = D; i < V; i += D) {
+        double b[D];
+#pragma unroll
+        for (int j = 0; j < D; ++j) b[j] = key[i + j];
+        merge_top<D>(key, b);
+    }
+    if constexpr (L > 1) merge_peer<D, 1>(key);
+    if constexpr (L > 2) merge_peer<D, 2>(key);
+    if constexpr (L > 4) merge_peer<D, 4>(key);
+    if constexpr (L > 8) merge_peer<D, 8>(key);
+    if constexpr (L > 16) merge_peer<D, 16>(key);
+}
 
 template <int L> __device__ __forceinline__ double row_max(double v) {
     if constexpr (L > 1) v = max2(v, peer<1>(v));
@@ -75,16 +165,35 @@ template <int L> __device__ __forceinline__ double row_sum(double v) {
 
 constexpr double kNone = -__builtin_huge_val();
 
-// A key with its index in the low bits.  -inf (not available) stays as it is.
-__device__ __forceinline__ double with_index(double k, int e) {
-    if (!(k > kNone)) return kNone;  // also a NaN
-    k = k < 1.7976931348623157e308 ? k + 0.0 : 1.7976931348623157e308;  // -0 -> +0, +inf -> largest
-    const uint64_t b = __builtin_bit_cast(uint64_t, k) & ~(uint64_t)kIdxMask;
-    return __builtin_bit_cast(double, b | (uint64_t)(k < 0.0 ? e : kIdxMask - e));
+// A key with its index in the low bits.  -inf or NaN (not available) gives
+// -inf.  Straight-line code: the key is made either way and then selected.
+__device__ __forceinline__ double with_index(double k, int e, bool on = true) {
+    const double f = min2(k, 1.7976931348623157e308);  // +inf -> largest
+    const uint64_t b = __builtin_bit_cast(uint64_t, f);
+    const uint32_t lo = ((uint32_t)b & ~(uint32_t)kIdxMask) | (uint32_t)(f < 0.0 ? e : kIdxMask - e);
+    const double r = __builtin_bit_cast(double, (b & 0xffffffff00000000ull) | lo);
+    return on && k > kNone ? r : kNone;
 }
 __device__ __forceinline__ int index_of(double k) {
     const int b = (int)(__builtin_bit_cast(uint64_t, k) & kIdxMask);
     return k < 0.0 ? b : kIdxMask - b;
+}
+
+__device__ __forceinline__ double without_index(double k) {
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~(uint64_t)kIdxMask);
+}
+// A group's key from its best two: the best, or the sum of both (without their index bits).
+__device__ __forceinline__ double group_key(double b1, double b2, int top, int g) {
+    if (!(b1 > kNone)) return kNone;
+    double k = without_index(b1);
+    if (top == 2 && b2 > kNone) k += without_index(b2);
+    return with_index(k + 0.0, g);
+}
+// (b1 >= b2) <- the best two of this lane's pair and the peer's, of other keys.
+template <int STEP> __device__ __forceinline__ void merge_pair(double& b1, double& b2) {
+    const double p1 = peer<STEP>(b1), p2 = peer<STEP>(b2);
+    b2 = max2(min2(b1, p1), max2(b2, p2));
+    b1 = max2(b1, p1);
 }
 
 template <typename T> __device__ __forceinline__ float logit_of(T v);
@@ -92,13 +201,64 @@ template <> __device__ __forceinline__ float logit_of<float>(float v) { return v
 template <> __device__ __forceinline__ float logit_of<uint16_t>(uint16_t v) { return bf_to_f(v); }
 
 // A logit as the routing sees it: +inf counts as the largest finite value, a
-// NaN as not available (-inf).
+// NaN as not available (-inf): the median instruction answers with the minimum
+// of three where one is a NaN.  (The builtin of it is folded to a minimum of two.)
 __device__ __forceinline__ float clean(float l) {
-    l = l == l ? l : -__builtin_huge_valf();
-    return l > 3.402823466e38f ? 3.402823466e38f : l;
+    float r;
+    asm("v_med3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(l), "v"(-__builtin_huge_valf()), "v"(3.402823466e38f));
+    return r;
 }
 
-__device__ __forceinline__ double sigmoid(double l) { return 1.0 / (1.0 + exp(-l)); }
+// a b + c with c a constant: one instruction with c in scalar registers.  (Left
+// to itself the compiler moves c into a vector register first, two more each.)
+__device__ __forceinline__ double fma_c(double a, double b, double c) {
+    double d;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+    return d;
+}
+// e^x for |x| <= 750 (0 and infinity past binary64's range): x = n ln 2 + r, the
+// Taylor series of e^r to r^13 (|r| <= 0.347: the rest is below 5e-18 of it), times 2^n.
+__device__ __forceinline__ double exp_small(double x) {
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    double r = __builtin_fma(n, -0.69314718036912381649, x);  // ln 2's upper 32 bits, then the rest
+    r = __builtin_fma(n, -1.9082149292705877000e-10, r);
+    double p = fma_c(r, 1.0 / 6227020800.0, 1.0 / 479001600.0);
+    p = fma_c(p, r, 1.0 / 39916800.0);
+    p = fma_c(p, r, 1.0 / 3628800.0);
+    p = fma_c(p, r, 1.0 / 362880.0);
+    p = fma_c(p, r, 1.0 / 40320.0);
+    p = fma_c(p, r, 1.0 / 5040.0);
+    p = fma_c(p, r, 1.0 / 720.0);
+    p = fma_c(p, r, 1.0 / 120.0);
+    p = fma_c(p, r, 1.0 / 24.0);
+    p = fma_c(p, r, 1.0 / 6.0);
+    p = __builtin_fma(p, r, 0.5);
+    p = __builtin_fma(p, r, 1.0);
+    p = __builtin_fma(p, r, 1.0);
+    return __builtin_amdgcn_ldexp(p, (int)n);
+}
+// 1 / x for normal x: the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double recip(double x) {
+    double y = __builtin_amdgcn_rcp(x);
+    y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+    return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+}
+// The softmax's numerator: 0 for -inf.
+__device__ __forceinline__ double exp_of(float l, double mx) {
+    const double d = (double)l - mx;
+    return exp_small(d > -750.0 ? d : -750.0);
+}
+// e^-700 for anything below, which every use takes for 0 (keys: next to nothing;
+// weights: weight_of).
+__device__ __forceinline__ double sigmoid(float l) {
+    return recip(1.0 + exp_small(-(double)__builtin_amdgcn_fmed3f(l, -700.f, 700.f)));
+}
+// A chosen expert's score.
+__device__ __forceinline__ double weight_of(bool soft, float l, double mx, double inv) {
+    if (soft) return exp_of(l, mx) * inv;
+    const double s = sigmoid(l);
+    return l < -700.f ? 0.0 : s;
+}
 
 // Lane `lane` of a token's L lanes holds experts W * (L * c + lane) + j of its
 // 16-byte chunks c: a chunk of the L lanes is one contiguous run.
@@ -140,9 +300,9 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
 
 // One workgroup: NT / L tokens.  Dynamic LDS: the chosen experts [tokens][k]
 // and their scores, then (with groups) keys, group keys and the kept flags.
-template <typename T, int L, int V, int NT>
+template <typename T, int L, int V, int NT, int SCORE>
 __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
-    constexpr int TPB = NT / L;
+    constexpr int TPB = NT / L, W = 16 / (int)sizeof(T);
     extern __shared__ char smem[];
     const int tid = threadIdx.x, tl = tid / L, lane = tid % L;
     const int E = a.E, k = a.k, G = a.n_groups, gs = a.group_size;
@@ -159,7 +319,7 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
     // softmax: the largest logit (0 for a row with none), and with it the
     // denominator where the weights or the keys need it
     double mx = 0.0, inv = 1.0;
-    if (a.score == kRouteSoftmax) {
+    if constexpr (SCORE == kRouteSoftmax) {
         float m = l[0];
 #pragma unroll
         for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
@@ -168,35 +328,78 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
     }
     double key[V];
     if (a.need_scores) {
-        if (a.score == kRouteSoftmax) {
+        if constexpr (SCORE == kRouteSoftmax) {
             double sum = 0.0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                key[v] = l[v] > -__builtin_huge_valf() ? exp((double)l[v] - mx) : 0.0;
+                key[v] = exp_of(l[v], mx);
                 sum += key[v];
             }
             sum = row_sum<L>(sum);
             inv = sum > 0.0 ? 1.0 / sum : 0.0;
         }
         if (a.scores_order) {
+            float bias[V] = {};
+            if (a.bias) {
+#pragma unroll
+                for (int c = 0; c < V / W; ++c) {
+                    const int e0 = expert_of<T, L>(c * W, lane);
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        if (a.vec ? e0 < E : e0 + j < E) bias[c * W + j] = gld(a.bias + e0 + j);
+                }
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int e = expert_of<T, L>(v, lane);
-                const double s = a.score == kRouteSoftmax ? key[v] * inv : sigmoid((double)l[v]);
-                const double b = a.bias && e < E ? (double)gld(a.bias + e) : 0.0;
-                key[v] = l[v] > -__builtin_huge_valf() ? with_index(s + b, e) : kNone;
+                const double s = SCORE == kRouteSoftmax ? key[v] * inv : sigmoid(l[v]);
+                key[v] = with_index(s + (double)bias[v], expert_of<T, L>(v, lane), l[v] > -__builtin_huge_valf());
             }
         }
     }
     if (!a.scores_order) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = with_index((double)l[v], expert_of<T, L>(v, lane));
+        for (int v = 0; v < V; ++v) key[v] = with_index((double)l[v] + 0.0, expert_of<T, L>(v, lane));  // -0 -> +0
     }
 
     if (a.counts) {
         for (int e = tid; e < E; e += NT) s_cnt[e] = 0;
     }
-    if (G > 1) {
+    if (G > 1 && a.group_lanes) {
+        // a group is group_lanes neighbouring lanes' part of one chunk: its best two
+        // keys by merging sorted pairs over those lanes
+        constexpr int C = V / W;
+        const int gl = a.group_lanes;
+        double gk[C];
+        int above[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            double b1 = kNone, b2 = kNone;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const double x = key[c * W + j];
+                b2 = max2(b2, min2(b1, x));
+                b1 = max2(b1, x);
+            }
+            if (L > 1 && gl > 1) merge_pair<1>(b1, b2);
+            if (L > 2 && gl > 2) merge_pair<2>(b1, b2);
+            if (L > 4 && gl > 4) merge_pair<4>(b1, b2);
+            if (L > 8 && gl > 8) merge_pair<8>(b1, b2);
+            if (L > 16 && gl > 16) merge_pair<16>(b1, b2);
+            gk[c] = group_key(b1, b2, a.group_top, c * (L / gl) + lane / gl);
+            above[c] = 0;
+        }
+        for (int o = 0; o < L; o += gl) {  // this run of lanes, then the token's others
+#pragma unroll
+            for (int q = 0; q < C; ++q) {
+                const double x = o ? __shfl_xor(gk[q], o, kWave) : gk[q];
+#pragma unroll
+                for (int c = 0; c < C; ++c) above[c] += x > gk[c] ? 1 : 0;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (above[v / W] >= a.keep_groups) key[v] = kNone;
+    } else if (G > 1) {
         const int S = G * (gs + 1);  // a token's keys, a gap behind each group (LDS banks)
         double* s_key = (double*)(smem + a.lds_groups);
         double* s_gk = s_key + TPB * S;
@@ -213,18 +416,10 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
             double b1 = kNone, b2 = kNone;
             for (int j = 0; j < gs; ++j) {
                 const double x = kp[j];
-                b2 = max2(b2, x < b1 ? x : b1);
+                b2 = max2(b2, min2(b1, x));
                 b1 = max2(b1, x);
             }
-            // the sum is of the keys without their index bits
-            if (a.group_top == 2 && b2 > kNone) {
-                const uint64_t m = ~(uint64_t)kIdxMask;
-                b1 = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, b1) & m) +
-                     __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, b2) & m);
-            } else if (b1 > kNone) {
-                b1 = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, b1) & ~(uint64_t)kIdxMask);
-            }
-            s_gk[q] = with_index(b1, gi);
+            s_gk[q] = group_key(b1, b2, a.group_top, gi);
         }
         __syncthreads();
         for (int q = tid; q < TPB * G; q += NT) {
@@ -243,16 +438,17 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
         }
     }
 
-    // k rounds of an argmax over the keys below the last winner
-    double last = __builtin_huge_val();
-    for (int s = 0; s < k; ++s) {
-        double m = kNone;
+    // the k largest keys: lists of 4, 8 or 16 merged
+    auto choose = [&](auto depth) {
+        constexpr int D = decltype(depth)::value;
+        top_keys<L, V, D>(key);
 #pragma unroll
-        for (int v = 0; v < V; ++v) m = max2(m, key[v] < last ? key[v] : kNone);
-        m = row_max<L>(m);
-        if (lane == s % L) s_idx[tl * k + s] = m > kNone ? index_of(m) : -1;
-        last = m;
-    }
+        for (int q = 0; q < D; ++q)
+            if (q < k && lane == q % L) s_idx[tl * k + q] = key[q] > kNone ? index_of(key[q]) : -1;
+    };
+    if (k <= 4) choose(std::integral_constant<int, 4>());
+    else if (k <= 8) choose(std::integral_constant<int, 8>());
+    else choose(std::integral_constant<int, V>());
     __syncthreads();
 
     // the chosen experts' scores, one slot per lane
@@ -260,8 +456,8 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
         const int e = s_idx[tl * k + s];
         double w = 0.0;
         if (e >= 0 && live) {
-            const double le = (double)clean(logit_of<T>(gld(row + e)));
-            w = a.score == kRouteSoftmax ? exp(le - mx) * inv : sigmoid(le);
+            const float le = clean(logit_of<T>(gld(row + e)));
+            w = weight_of(SCORE == kRouteSoftmax, le, mx, inv);
         }
         s_w[tl * k + s] = w;
     }
@@ -328,7 +524,7 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteArgs a) {
         double sum = 0.0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            p[v] = l[v] > -__builtin_huge_valf() ? exp((double)l[v] - mx) : 0.0;
+            p[v] = exp_of(l[v], mx);
             sum += p[v];
         }
         sum = row_sum<L>(sum);
@@ -343,7 +539,7 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteArgs a) {
         if (e >= 0) {
             const float lf = clean(logit_of<T>(gld(row + e)));
             if (lf > -__builtin_huge_valf()) {
-                w = soft ? exp((double)lf - mx) * inv : sigmoid((double)lf);
+                w = weight_of(soft, lf, mx, inv);
                 d = (double)a.scale * (double)gld(a.dg + t * k + s);
             } else {
                 e = -1;
@@ -379,8 +575,8 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteArgs a) {
                 d *= w;
             } else {
                 // s (1 - s) without the cancellation of 1 - s
-                const double z = exp(-fabs((double)clean(logit_of<T>(gld(row + e)))));
-                d *= z / ((1.0 + z) * (1.0 + z));
+                const double z = exp_of(-fabsf(clean(logit_of<T>(gld(row + e)))), 0.0);
+                d *= z * recip((1.0 + z) * (1.0 + z));
             }
         }
         s_row[tl * EP + e] = d;
@@ -437,12 +633,18 @@ hipError_t launch_one(RouteArgs a, bool grad, hipStream_t s) {
         hipLaunchKernelGGL((route_grad_kernel<T, L, V, NT>), dim3((unsigned)blocks), dim3(NT), lds, s, a);
     } else {
         size_t lds = (size_t)TPB * a.k * 12 + (a.counts ? (size_t)a.E * 4 : 0);
-        if (a.n_groups > 1) {
+        // groups that are whole runs of 2^i lanes of a chunk need no LDS
+        constexpr int W = 16 / (int)sizeof(T);
+        const int gl = a.group_size / W;
+        a.group_lanes = a.n_groups > 1 && a.group_size % W == 0 && (gl & (gl - 1)) == 0 && gl <= L ? gl : 0;
+        if (a.n_groups > 1 && !a.group_lanes) {
             lds = (lds + 15) & ~(size_t)15;
             a.lds_groups = (int)lds;
             lds += (size_t)TPB * (a.n_groups * (a.group_size + 1) * 8 + a.n_groups * 9);
         }
-        hipLaunchKernelGGL((route_kernel<T, L, V, NT>), dim3((unsigned)blocks), dim3(NT), lds, s, a);
+        const dim3 g((unsigned)blocks), n(NT);
+        if (a.score == kRouteSoftmax) hipLaunchKernelGGL((route_kernel<T, L, V, NT, kRouteSoftmax>), g, n, lds, s, a);
+        else hipLaunchKernelGGL((route_kernel<T, L, V, NT, kRouteSigmoid>), g, n, lds, s, a);
     }
     return hipGetLastError();
 }

@@ -23,6 +23,7 @@ struct RouteArgs {
     int32_t vec, vec_out;  // rows of logits / dlogits take 16-byte accesses
     int32_t need_scores;   // every expert's score is needed, not only the chosen ones'
     int32_t scores_order;  // keys are scores plus bias; else the logits order the experts
+    int32_t group_lanes;   // lanes a group spans when groups are whole runs of them, else 0 (the launcher sets it)
     int32_t lds_groups;    // byte offset of the groups' part of the dynamic LDS
     int32_t* idx;          // [T][k] out
     float* g;              // [T][k] out

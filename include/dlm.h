@@ -132,7 +132,7 @@ int dlm_pregate_centroid(const void* x, const void* C, int64_t T, int64_t d, int
  * Equal keys go to the lower index.  Without a bias (and with group_top 1) the
  * logits themselves are compared, exactly; otherwise keys are binary64 values
  * and two within 2^-43 of their size may count as equal.  Scores and sums are
- * binary64; g is rounded to fp32 once.
+ * binary64; g is rounded to fp32 once.  (A sigmoid below e^-700 counts as 0.)
  * A logit of -inf or NaN marks an expert that is not available to the row: its
  * score is 0 and it is never chosen; +inf counts as the largest fp32 value.  A
  * row with fewer than k available experts in its kept groups ends in empty
