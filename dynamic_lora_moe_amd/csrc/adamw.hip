@@ -44,6 +44,7 @@ namespace {
 
 constexpr int kNT = 256;
 constexpr int kPer = kAdamChunk / (kNT * 4);  // rounds of four elements per thread
+constexpr int kReadPer = 4;  // quads per thread of the read-back
 static_assert(kAdamBlock == 4 * kWave, "a wave's four elements per lane are one block");
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -78,10 +79,10 @@ __device__ __forceinline__ float load1(const uint16_t* p) { return bf_to_f(gld(p
 __device__ __forceinline__ void store1(float* p, float f) { gst(p, f); }
 __device__ __forceinline__ void store1(uint16_t* p, float f) { gst(p, f_to_bf(f)); }
 
-// Four elements i .. i+3 of an array of n: one access where vec allows it, else
-// element by element, 0 past the end.
-template <typename T> __device__ __forceinline__ void get4(const T* p, int64_t i, int64_t n, bool vec, float (&f)[4]) {
-    if (vec && i + 4 <= n) {
+// Four elements i .. i+3 of an array of n: one access (FULL: the workgroup's
+// whole chunk is inside and aligned), else element by element, 0 past the end.
+template <bool FULL, typename T> __device__ __forceinline__ void get4(const T* p, int64_t i, int64_t n, float (&f)[4]) {
+    if constexpr (FULL) {
         Raw4<T> r;
         load4(r, p + i);
         widen(r, f);
@@ -90,9 +91,9 @@ template <typename T> __device__ __forceinline__ void get4(const T* p, int64_t i
         for (int j = 0; j < 4; ++j) f[j] = i + j < n ? load1(p + i + j) : 0.f;
     }
 }
-template <typename T>
-__device__ __forceinline__ void put4(T* p, int64_t i, int64_t n, bool vec, const float (&f)[4]) {
-    if (vec && i + 4 <= n) {
+template <bool FULL, typename T>
+__device__ __forceinline__ void put4(T* p, int64_t i, int64_t n, const float (&f)[4]) {
+    if constexpr (FULL) {
         store4(p + i, f);
     } else {
 #pragma unroll
@@ -100,16 +101,16 @@ __device__ __forceinline__ void put4(T* p, int64_t i, int64_t n, bool vec, const
             if (i + j < n) store1(p + i + j, f[j]);
     }
 }
-__device__ __forceinline__ uint32_t get4b(const uint8_t* p, int64_t i, int64_t n, bool vec) {
-    if (vec && i + 4 <= n) return gld((const uint32_t*)(p + i));
+template <bool FULL> __device__ __forceinline__ uint32_t get4b(const uint8_t* p, int64_t i, int64_t n) {
+    if constexpr (FULL) return gld((const uint32_t*)(p + i));
     uint32_t w = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         if (i + j < n) w |= (uint32_t)gld(p + i + j) << (8 * j);
     return w;
 }
-__device__ __forceinline__ void put4b(uint8_t* p, int64_t i, int64_t n, bool vec, uint32_t w) {
-    if (vec && i + 4 <= n) {
+template <bool FULL> __device__ __forceinline__ void put4b(uint8_t* p, int64_t i, int64_t n, uint32_t w) {
+    if constexpr (FULL) {
         gst((uint32_t*)(p + i), w);
     } else {
 #pragma unroll
@@ -126,33 +127,31 @@ __global__ void adamw_begin(AdamArgs a) {
     w.gs = a.grad_scale ? *a.grad_scale : 1.f;
     w.lr = a.lr_scale ? a.lr * *a.lr_scale : a.lr;
     w.ic1 = (float)(-1.0 / expm1((double)w.t * a.lb1));
-    w.ic2 = (float)(-1.0 / expm1((double)w.t * a.lb2));
+    w.rc2 = (float)sqrt(-1.0 / expm1((double)w.t * a.lb2));
     *a.words = w;
 }
 
 struct Step {
     uint32_t t;
-    float gs, lr, keep, ic1, ic2;  // keep = 1 - lr wd
+    float gs, lr, keep, ic1, rc2;  // keep = 1 - lr wd
 };
 __device__ __forceinline__ Step step_of(const AdamArgs& a, float wd) {
     const AdWords w = *a.words;
-    return Step{(uint32_t)w.t, w.gs, w.lr, (float)(1.0 - (double)w.lr * (double)wd), w.ic1, w.ic2};
+    return Step{(uint32_t)w.t, w.gs, w.lr, (float)(1.0 - (double)w.lr * (double)wd), w.ic1, w.rc2};
 }
 
 __device__ __forceinline__ float updated(float w, float m, float v, const Step& s, float eps) {
-    const float step = (m * s.ic1) / (sqrtf(v * s.ic2) + eps);
+    const float step = (m * s.ic1) / (sqrtf(v) * s.rc2 + eps);
     return w * s.keep - s.lr * step;
 }
 
 // ---- fp32 moments --------------------------------------------------------------
 
-template <typename P, typename G>
-__global__ __launch_bounds__(kNT) void adamw_f32(AdamArgs a) {
-    const AdDesc D = a.descs[a.chunk_tensor[blockIdx.x]];
+template <bool FULL, typename P, typename G>
+__device__ __forceinline__ void step_f32(const AdamArgs& a, const AdDesc& D) {
     const Step s = step_of(a, D.wd);
     const float b1 = (float)a.beta1, b2 = (float)a.beta2, r1 = (float)(1.0 - a.beta1), r2 = (float)(1.0 - a.beta2);
     const int64_t base = ((int64_t)blockIdx.x - D.chunk0) * kAdamChunk + 4 * threadIdx.x;
-    const bool vec = D.vec;
     P* __restrict__ p = (P*)D.p;
     const G* __restrict__ gp = (const G*)D.g;
     float* __restrict__ mp = (float*)D.m;
@@ -162,11 +161,11 @@ __global__ __launch_bounds__(kNT) void adamw_f32(AdamArgs a) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int64_t i = base + k * kNT * 4;
-        get4(gp, i, D.n, vec, g[k]);
-        get4(mp, i, D.n, vec, m[k]);
-        get4(vp, i, D.n, vec, v[k]);
-        if (D.master) get4(D.master, i, D.n, vec, w[k]);
-        else get4(p, i, D.n, vec, w[k]);
+        get4<FULL>(gp, i, D.n, g[k]);
+        get4<FULL>((const float*)mp, i, D.n, m[k]);
+        get4<FULL>((const float*)vp, i, D.n, v[k]);
+        if (D.master) get4<FULL>((const float*)D.master, i, D.n, w[k]);
+        else get4<FULL>((const P*)p, i, D.n, w[k]);
     }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
@@ -184,12 +183,23 @@ __global__ __launch_bounds__(kNT) void adamw_f32(AdamArgs a) {
                 w[k][j] = updated(w[k][j], mj, vj, s, a.eps);
             }
         }
-        put4(mp, i, D.n, vec, m[k]);
-        put4(vp, i, D.n, vec, v[k]);
-        if (D.master) put4(D.master, i, D.n, vec, w[k]);
-        put4(p, i, D.n, vec, w[k]);
+        put4<FULL>(mp, i, D.n, m[k]);
+        put4<FULL>(vp, i, D.n, v[k]);
+        if (D.master) put4<FULL>(D.master, i, D.n, w[k]);
+        put4<FULL>(p, i, D.n, w[k]);
     }
     if (bad) gst(&a.words->err, 1);
+}
+
+// A chunk that lies whole in its tensor, with pointers for four elements at a time.
+__device__ __forceinline__ bool whole(const AdDesc& D) {
+    return D.vec && ((int64_t)blockIdx.x - D.chunk0 + 1) * kAdamChunk <= D.n;
+}
+
+template <typename P, typename G> __global__ __launch_bounds__(kNT) void adamw_f32(AdamArgs a) {
+    const AdDesc D = a.descs[a.chunk_tensor[blockIdx.x]];
+    if (whole(D)) step_f32<true, P, G>(a, D);
+    else step_f32<false, P, G>(a, D);
 }
 
 // ---- 8-bit moments -------------------------------------------------------------
@@ -203,60 +213,64 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 
 constexpr double kM2 = 127.0 * 127.0, kV4 = 255.0 * 255.0 * 255.0 * 255.0;
 
-__device__ __forceinline__ double m_value(int q, double unit) { return unit * (double)(q * (q < 0 ? -q : q)); }
-__device__ __forceinline__ double v_value(uint32_t c, double unit) { return unit * (double)((c * c) * (c * c)); }
-
-// The code of x = (|m| / ms) 127^2: floor(sqrt x), or one more where x lies
-// further up its step of 2c + 1 than the noise (2h + 1) / 2^17.  The fp32 root
-// may miss the floor by one next to a square; it is put right exactly.
-__device__ __forceinline__ int m_code(double x, uint32_t h) {
-    int c = (int)sqrtf((float)x);
-    double d = x - (double)(c * c);
-    if (d < 0.0) {
-        --c;
-        d = x - (double)(c * c);
-    } else if (d >= (double)(2 * c + 1)) {
-        ++c;
-        d = x - (double)(c * c);
+// The codes' values over their block's scale: sign(q) (q / 127)^2 and (c / 255)^4,
+// 1 exactly at the top (a block's largest moment goes on as it was stored: its
+// decayed value often lies next to the middle of two fp32 scales, and the last
+// bit of binary64 decides).  A table of each in LDS, looked up by code.
+__device__ __forceinline__ void value_tables(double* s_m, double* s_v) {
+    for (int i = threadIdx.x; i < 256; i += blockDim.x) {
+        const int q = (int8_t)i;
+        s_m[i] = (double)(q * (q < 0 ? -q : q)) / kM2;
+        s_v[i] = (double)((uint32_t)(i * i) * (uint32_t)(i * i)) / kV4;
     }
-    return c + (d * 131072.0 > (double)((2 * (int)h + 1) * (2 * c + 1)) ? 1 : 0);
+    __syncthreads();
 }
-// The same for v with steps between fourth powers.
-__device__ __forceinline__ double pow4(int c) {
+
+// The code of x = (|m| / ms) 127^2: with c = floor(sqrt x), c, or c + 1 where x
+// lies further up its step of 2c + 1 than the noise u = (2h + 1) / 2^17.  So it
+// is the first n with x <= border(n) = n^2 + u (2n + 1), borders and x times 2^17
+// being whole numbers below 2^32 (x rounded up, which changes no comparison).
+// The fp32 root, made a little smaller, starts at c or c - 1: two comparisons.
+__device__ __forceinline__ uint32_t m_code(double x, uint32_t h) {
+    const uint32_t xi = (uint32_t)__builtin_ceil(x * 131072.0);
+    const uint32_t c = (uint32_t)(__builtin_amdgcn_sqrtf((float)x) * 0.9999997f);
+    const uint32_t u = 2 * h + 1;
+    const uint32_t b0 = ((c * c) << 17) + u * (2 * c + 1), b1 = (((c + 1) * (c + 1)) << 17) + u * (2 * c + 3);
+    return c + (xi > b0 ? 1u : 0u) + (xi > b1 ? 1u : 0u);
+}
+// The same for v with steps between fourth powers; root = sqrt x.
+__device__ __forceinline__ double pow4(uint32_t c) {
     const double s = (double)(c * c);
     return s * s;
 }
-__device__ __forceinline__ uint32_t v_code(double x, uint32_t h, bool positive) {
-    int c = (int)sqrtf(sqrtf((float)x));
-    double lo = pow4(c), hi = pow4(c + 1);
-    if (x < lo) {
-        --c;
-        hi = lo;
-        lo = pow4(c);
-    } else if (x >= hi) {
-        ++c;
-        lo = hi;
-        hi = pow4(c + 1);
-    }
-    c += (x - lo) * 131072.0 > (double)(2 * (int)h + 1) * (hi - lo) ? 1 : 0;
-    return (uint32_t)(positive && c < 1 ? 1 : c);
+__device__ __forceinline__ uint32_t v_code(double x, float root, uint32_t h) {
+    const uint32_t c = (uint32_t)(__builtin_amdgcn_sqrtf(root) * 0.9999997f);
+    const double u = (double)(2 * h + 1) * (1.0 / 131072.0);
+    const double p0 = pow4(c), p1 = pow4(c + 1), p2 = pow4(c + 2);
+    return c + (x > __builtin_fma(u, p1 - p0, p0) ? 1u : 0u) + (x > __builtin_fma(u, p2 - p1, p1) ? 1u : 0u);
 }
 
+// The largest of the wave's values (none a NaN), as a scalar.
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-    return v;
+    int x = __float_as_int(v);
+#define DLM_STEP(CTRL, ROWS) \
+    x = __float_as_int(fmaxf(__int_as_float(x), __int_as_float(__builtin_amdgcn_update_dpp(x, x, CTRL, ROWS, 0xf, false))))
+    DLM_STEP(0xB1, 0xf);   // quad_perm: within pairs
+    DLM_STEP(0x4E, 0xf);   // between pairs
+    DLM_STEP(0x141, 0xf);  // half rows mirrored
+    DLM_STEP(0x140, 0xf);  // rows mirrored
+    DLM_STEP(0x142, 0xa);  // row 0 to 1, 2 to 3
+    DLM_STEP(0x143, 0xc);  // rows 0..1 to 2..3
+#undef DLM_STEP
+    return __int_as_float(__builtin_amdgcn_readlane(x, kWave - 1));
 }
 
-template <typename P, typename G>
-__global__ __launch_bounds__(kNT) void adamw_q8(AdamArgs a) {
-    const int tensor = a.chunk_tensor[blockIdx.x];
-    const AdDesc D = a.descs[tensor];
+template <bool FULL, typename P, typename G>
+__device__ __forceinline__ void step_q8(const AdamArgs& a, const AdDesc& D, int tensor, const double* s_m, const double* s_v) {
     const Step s = step_of(a, D.wd);
     constexpr int kBlocks = kAdamChunk / kAdamBlock / (kNT / kWave);  // blocks per wave
     const int lane = lane_id();
     const int64_t blk0 = ((int64_t)blockIdx.x - D.chunk0) * (kAdamChunk / kAdamBlock) + wave_id() * kBlocks;
-    const bool vec = D.vec;
     P* __restrict__ p = (P*)D.p;
     const G* __restrict__ gp = (const G*)D.g;
     const double r1 = 1.0 - a.beta1, r2 = 1.0 - a.beta2;
@@ -266,32 +280,33 @@ __global__ __launch_bounds__(kNT) void adamw_q8(AdamArgs a) {
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
         const int64_t blk = blk0 + b, i = blk * kAdamBlock + 4 * lane;
-        const bool in = blk * kAdamBlock < D.n;
-        get4(gp, i, D.n, vec, g[b]);
-        q[b] = get4b((const uint8_t*)D.m, i, D.n, vec);
-        c[b] = get4b((const uint8_t*)D.v, i, D.n, vec);
+        const bool in = FULL || blk * kAdamBlock < D.n;
+        get4<FULL>(gp, i, D.n, g[b]);
+        q[b] = get4b<FULL>((const uint8_t*)D.m, i, D.n);
+        c[b] = get4b<FULL>((const uint8_t*)D.v, i, D.n);
         ms[b] = in ? gld(D.ms + blk) : 0.f;
         vs[b] = in ? gld(D.vs + blk) : 0.f;
-        if (D.master) get4(D.master, i, D.n, vec, w[b]);
-        else get4(p, i, D.n, vec, w[b]);
+        if (D.master) get4<FULL>((const float*)D.master, i, D.n, w[b]);
+        else get4<FULL>((const P*)p, i, D.n, w[b]);
     }
     const uint32_t key_t = mix(mix(a.seed + s.t * 0x9E3779B1u) + (uint32_t)tensor * 0x85EBCA77u);
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
         const int64_t blk = blk0 + b, i = blk * kAdamBlock + 4 * lane;
-        if (blk * kAdamBlock >= D.n) break;  // the same for the whole wave
-        const double mu = (double)ms[b] / kM2, vu = (double)vs[b] / kV4;
+        if (!FULL && blk * kAdamBlock >= D.n) break;  // the same for the whole wave
         double m[4], v[4];
         float mm = 0.f, vm = 0.f;
         bool fin = true;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const double gj = (double)(g[b][j] * s.gs);
-            m[j] = a.beta1 * m_value((int)(int8_t)(q[b] >> (8 * j)), mu) + r1 * gj;
-            v[j] = a.beta2 * v_value((c[b] >> (8 * j)) & 255u, vu) + r2 * (gj * gj);
+            const double mo = (double)ms[b] * s_m[(q[b] >> (8 * j)) & 255u], vo = (double)vs[b] * s_v[(c[b] >> (8 * j)) & 255u];
+            m[j] = a.beta1 * mo + r1 * gj;
+            v[j] = a.beta2 * vo + r2 * (gj * gj);
+            const float vj = (float)v[j];
             mm = fmaxf(mm, fabsf((float)m[j]));
-            vm = fmaxf(vm, (float)v[j]);
-            fin = fin && __builtin_isfinite((float)v[j]);
+            vm = fmaxf(vm, vj);
+            fin = fin && vj < __builtin_huge_valf();  // false for a NaN too
         }
         if (__ballot(!fin)) {  // a NaN does not reach the maxima: the ballot decides
             bad = true;
@@ -300,47 +315,75 @@ __global__ __launch_bounds__(kNT) void adamw_q8(AdamArgs a) {
         mm = wave_max(mm);
         vm = wave_max(vm);
         const double mi = mm > 0.f ? kM2 / (double)mm : 0.0, vi = vm > 0.f ? kV4 / (double)vm : 0.0;
+        // sqrt(v / (1 - b2^t)) from the root of v's place in the block
+        const float vroot = sqrtf(vm) * s.rc2 * (1.f / (255.f * 255.f));
         const uint32_t key = mix(key_t + (uint32_t)blk * 0xC2B2AE3Du);
+        const uint32_t least = vm > 0.f ? 1u : 0u;
         uint32_t nq = 0, nc = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t h = mix(key + (uint32_t)(4 * lane + j) * 0x9E3779B1u);
             const double xm = fabs(m[j]) * mi, xv = v[j] * vi;
-            int k = m_code(xm < kM2 ? xm : kM2, h & 0xffffu);
-            k = m[j] < 0.0 ? -k : k;
-            nq |= ((uint32_t)k & 255u) << (8 * j);
-            nc |= v_code(xv < kV4 ? xv : kV4, h >> 16, v[j] > 0.0 && vm > 0.f) << (8 * j);
-            w[b][j] = updated(w[b][j], (float)m[j], (float)v[j], s, a.eps);
+            const uint32_t k = m_code(xm < kM2 ? xm : kM2, h & 0xffffu);
+            nq |= ((m[j] < 0.0 ? 0u - k : k) & 255u) << (8 * j);
+            const double xc = xv < kV4 ? xv : kV4;
+            const float root = __builtin_amdgcn_sqrtf((float)xc);
+            uint32_t cv = v_code(xc, root, h >> 16);
+            cv = cv < least && v[j] > 0.0 ? least : cv;
+            nc |= cv << (8 * j);
+            // the quotient by the reciprocal's estimate (1 ulp): the step is lr of a weight
+            const float step = ((float)m[j] * s.ic1) * __builtin_amdgcn_rcpf(root * vroot + a.eps);
+            w[b][j] = w[b][j] * s.keep - s.lr * step;
         }
-        put4b((uint8_t*)D.m, i, D.n, vec, nq);
-        put4b((uint8_t*)D.v, i, D.n, vec, nc);
+        put4b<FULL>((uint8_t*)D.m, i, D.n, nq);
+        put4b<FULL>((uint8_t*)D.v, i, D.n, nc);
         if (lane == 0) {
             gst(D.ms + blk, mm);
             gst(D.vs + blk, vm);
         }
-        if (D.master) put4(D.master, i, D.n, vec, w[b]);
-        put4(p, i, D.n, vec, w[b]);
+        if (D.master) put4<FULL>(D.master, i, D.n, w[b]);
+        put4<FULL>(p, i, D.n, w[b]);
     }
     if (bad) gst(&a.words->err, 1);
 }
 
+template <typename P, typename G> __global__ __launch_bounds__(kNT) void adamw_q8(AdamArgs a) {
+    const int tensor = a.chunk_tensor[blockIdx.x];
+    const AdDesc D = a.descs[tensor];
+    __shared__ double s_m[256], s_v[256];
+    value_tables(s_m, s_v);
+    if (whole(D)) step_q8<true, P, G>(a, D, tensor, s_m, s_v);
+    else step_q8<false, P, G>(a, D, tensor, s_m, s_v);
+}
+
 // The moments that the codes stand for.
-__global__ __launch_bounds__(kNT) void adamw_read(const int8_t* __restrict__ m, const uint8_t* __restrict__ v,
-                                                  const float* __restrict__ ms, const float* __restrict__ vs, int64_t n,
-                                                  int vec, float* __restrict__ m_out, float* __restrict__ v_out) {
-    const int64_t i = ((int64_t)blockIdx.x * kNT + threadIdx.x) * 4;
-    if (i >= n) return;
+template <bool FULL>
+__device__ __forceinline__ void read_state(const int8_t* m, const uint8_t* v, const float* ms, const float* vs, int64_t i,
+                                           int64_t n, float* m_out, float* v_out, const double* s_m, const double* s_v) {
     const int64_t blk = i / kAdamBlock;
-    const uint32_t q = get4b((const uint8_t*)m, i, n, vec), c = get4b(v, i, n, vec);
-    const double mu = (double)gld(ms + blk) / kM2, vu = (double)gld(vs + blk) / kV4;
+    const uint32_t q = get4b<FULL>((const uint8_t*)m, i, n), c = get4b<FULL>(v, i, n);
+    const double mu = (double)gld(ms + blk), vu = (double)gld(vs + blk);
     float mo[4], vo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        mo[j] = (float)m_value((int)(int8_t)(q >> (8 * j)), mu);
-        vo[j] = (float)v_value((c >> (8 * j)) & 255u, vu);
+        mo[j] = (float)(mu * s_m[(q >> (8 * j)) & 255u]);
+        vo[j] = (float)(vu * s_v[(c >> (8 * j)) & 255u]);
     }
-    put4(m_out, i, n, vec, mo);
-    put4(v_out, i, n, vec, vo);
+    put4<FULL>(m_out, i, n, mo);
+    put4<FULL>(v_out, i, n, vo);
+}
+__global__ __launch_bounds__(kNT) void adamw_read(const int8_t* __restrict__ m, const uint8_t* __restrict__ v,
+                                                  const float* __restrict__ ms, const float* __restrict__ vs, int64_t n,
+                                                  int vec, float* __restrict__ m_out, float* __restrict__ v_out) {
+    __shared__ double s_m[256], s_v[256];
+    value_tables(s_m, s_v);
+#pragma unroll
+    for (int k = 0; k < kReadPer; ++k) {
+        const int64_t i = (((int64_t)blockIdx.x * kReadPer + k) * kNT + threadIdx.x) * 4;
+        if (i >= n) return;
+        if (vec && i + 4 <= n) read_state<true>(m, v, ms, vs, i, n, m_out, v_out, s_m, s_v);
+        else read_state<false>(m, v, ms, vs, i, n, m_out, v_out, s_m, s_v);
+    }
 }
 
 template <typename P, typename G> hipError_t launch_pg(const AdamArgs& a, int bits, hipStream_t s) {
@@ -362,7 +405,7 @@ hipError_t launch_adamw(const AdamArgs& a, int p_dtype, int g_dtype, int bits, h
 
 hipError_t launch_adamw_read_state(const int8_t* m, const uint8_t* v, const float* ms, const float* vs, int64_t n,
                                    float* m_out, float* v_out, hipStream_t s) {
-    const int64_t blocks = (n + 4 * kNT - 1) / (4 * kNT);
+    const int64_t blocks = (n + 4 * kNT * kReadPer - 1) / (4 * kNT * kReadPer);
     if (!grid_fits(blocks, kNT)) return hipErrorInvalidConfiguration;
     const uintptr_t all = (uintptr_t)m_out | (uintptr_t)v_out, codes = (uintptr_t)m | (uintptr_t)v;
     const int vec = (all & 15) == 0 && (codes & 3) == 0;

@@ -31,7 +31,7 @@ struct AdWords {
     int32_t err;   // a gradient was not finite
     // the running step's
     float gs, lr;    // gradient scale, rate
-    float ic1, ic2;  // 1 / (1 - b1^t), 1 / (1 - b2^t)
+    float ic1, rc2;  // 1 / (1 - b1^t), sqrt(1 / (1 - b2^t))
 };
 
 struct AdamArgs {
