@@ -8,12 +8,12 @@
 // kAdamChunk-element chunk of one tensor, found through a table of chunks, so
 // tensors of any sizes share a launch.
 //
-// The step count t lives on the device (a captured step counts on replay): a
-// one-thread launch moves it and works out the bias corrections, and the step
-// reads them with ordinary cached loads.  Counting in the step itself, by a
-// ticket that the last workgroup to end finds complete, took 8.0 ms where this
-// takes 1.8 (322 million weights, 78 thousand workgroups): every workgroup's
-// atomics on one address go past the XCD's L2 and queue up.
+// The step count t lives on the device, so that a captured step counts on
+// replay, and once per chunk: a workgroup reads, uses and moves its own, and none
+// waits for another.  (One count moved by the last workgroup to end, found by a
+// ticket, took 8.0 ms where this takes 1.8 -- 322 million weights, 78 thousand
+// workgroups whose atomics on one address queue up past their XCD's L2; moved by
+// a one-thread launch before the step it took the same time and a second launch.)
 //
 // 8-bit moments.  Blocks of 256 consecutive elements share an fp32 scale, the
 // block's largest |m| and largest v:
@@ -119,25 +119,26 @@ template <bool FULL> __device__ __forceinline__ void put4b(uint8_t* p, int64_t i
     }
 }
 
-// A step's first launch, one thread: counts the step and works out what its
-// elements share.
-__global__ void adamw_begin(AdamArgs a) {
-    AdWords w = *a.words;
-    w.t += 1;
-    w.gs = a.grad_scale ? *a.grad_scale : 1.f;
-    w.lr = a.lr_scale ? a.lr * *a.lr_scale : a.lr;
-    w.ic1 = (float)(-1.0 / expm1((double)w.t * a.lb1));
-    w.rc2 = (float)sqrt(-1.0 / expm1((double)w.t * a.lb2));
-    *a.words = w;
-}
-
 struct Step {
     uint32_t t;
-    float gs, lr, keep, ic1, rc2;  // keep = 1 - lr wd
+    float gs, lr, keep, ic1, rc2;  // gradient scale, rate, 1 - lr wd, 1 / (1 - b1^t), sqrt(1 / (1 - b2^t))
 };
-__device__ __forceinline__ Step step_of(const AdamArgs& a, float wd) {
-    const AdWords w = *a.words;
-    return Step{(uint32_t)w.t, w.gs, w.lr, (float)(1.0 - (double)w.lr * (double)wd), w.ic1, w.rc2};
+// Counts the chunk's step and shares what its elements need (called by the whole
+// workgroup, once its loads are out: one thread works, the others wait).
+__device__ __forceinline__ Step begin_step(const AdamArgs& a, float wd, Step* s_step) {
+    if (threadIdx.x == 0) {
+        Step s;
+        s.t = (uint32_t)gld(a.steps + blockIdx.x) + 1u;
+        gst(a.steps + blockIdx.x, (int32_t)s.t);
+        s.gs = a.grad_scale ? gld(a.grad_scale) : 1.f;
+        s.lr = a.lr_scale ? a.lr * gld(a.lr_scale) : a.lr;
+        s.keep = (float)(1.0 - (double)s.lr * (double)wd);
+        s.ic1 = (float)(-1.0 / expm1((double)s.t * a.lb1));
+        s.rc2 = (float)sqrt(-1.0 / expm1((double)s.t * a.lb2));
+        *s_step = s;
+    }
+    __syncthreads();
+    return *s_step;
 }
 
 __device__ __forceinline__ float updated(float w, float m, float v, const Step& s, float eps) {
@@ -148,8 +149,7 @@ __device__ __forceinline__ float updated(float w, float m, float v, const Step& 
 // ---- fp32 moments --------------------------------------------------------------
 
 template <bool FULL, typename P, typename G>
-__device__ __forceinline__ void step_f32(const AdamArgs& a, const AdDesc& D) {
-    const Step s = step_of(a, D.wd);
+__device__ __forceinline__ void step_f32(const AdamArgs& a, const AdDesc& D, Step* s_step) {
     const float b1 = (float)a.beta1, b2 = (float)a.beta2, r1 = (float)(1.0 - a.beta1), r2 = (float)(1.0 - a.beta2);
     const int64_t base = ((int64_t)blockIdx.x - D.chunk0) * kAdamChunk + 4 * threadIdx.x;
     P* __restrict__ p = (P*)D.p;
@@ -167,6 +167,7 @@ __device__ __forceinline__ void step_f32(const AdamArgs& a, const AdDesc& D) {
         if (D.master) get4<FULL>((const float*)D.master, i, D.n, w[k]);
         else get4<FULL>((const P*)p, i, D.n, w[k]);
     }
+    const Step s = begin_step(a, D.wd, s_step);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int64_t i = base + k * kNT * 4;
@@ -188,7 +189,7 @@ __device__ __forceinline__ void step_f32(const AdamArgs& a, const AdDesc& D) {
         if (D.master) put4<FULL>(D.master, i, D.n, w[k]);
         put4<FULL>(p, i, D.n, w[k]);
     }
-    if (bad) gst(&a.words->err, 1);
+    if (bad) gst(a.err, 1);
 }
 
 // A chunk that lies whole in its tensor, with pointers for four elements at a time.
@@ -198,8 +199,9 @@ __device__ __forceinline__ bool whole(const AdDesc& D) {
 
 template <typename P, typename G> __global__ __launch_bounds__(kNT) void adamw_f32(AdamArgs a) {
     const AdDesc D = a.descs[a.chunk_tensor[blockIdx.x]];
-    if (whole(D)) step_f32<true, P, G>(a, D);
-    else step_f32<false, P, G>(a, D);
+    __shared__ Step s_step;
+    if (whole(D)) step_f32<true, P, G>(a, D, &s_step);
+    else step_f32<false, P, G>(a, D, &s_step);
 }
 
 // ---- 8-bit moments -------------------------------------------------------------
@@ -266,8 +268,7 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 
 template <bool FULL, typename P, typename G>
-__device__ __forceinline__ void step_q8(const AdamArgs& a, const AdDesc& D, int tensor, const double* s_m, const double* s_v) {
-    const Step s = step_of(a, D.wd);
+__device__ __forceinline__ void step_q8(const AdamArgs& a, const AdDesc& D, int tensor, double* s_m, double* s_v, Step* s_step) {
     constexpr int kBlocks = kAdamChunk / kAdamBlock / (kNT / kWave);  // blocks per wave
     const int lane = lane_id();
     const int64_t blk0 = ((int64_t)blockIdx.x - D.chunk0) * (kAdamChunk / kAdamBlock) + wave_id() * kBlocks;
@@ -289,6 +290,8 @@ __device__ __forceinline__ void step_q8(const AdamArgs& a, const AdDesc& D, int 
         if (D.master) get4<FULL>((const float*)D.master, i, D.n, w[b]);
         else get4<FULL>((const P*)p, i, D.n, w[b]);
     }
+    value_tables(s_m, s_v);
+    const Step s = begin_step(a, D.wd, s_step);
     const uint32_t key_t = mix(mix(a.seed + s.t * 0x9E3779B1u) + (uint32_t)tensor * 0x85EBCA77u);
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
@@ -344,16 +347,16 @@ __device__ __forceinline__ void step_q8(const AdamArgs& a, const AdDesc& D, int 
         if (D.master) put4<FULL>(D.master, i, D.n, w[b]);
         put4<FULL>(p, i, D.n, w[b]);
     }
-    if (bad) gst(&a.words->err, 1);
+    if (bad) gst(a.err, 1);
 }
 
 template <typename P, typename G> __global__ __launch_bounds__(kNT) void adamw_q8(AdamArgs a) {
     const int tensor = a.chunk_tensor[blockIdx.x];
     const AdDesc D = a.descs[tensor];
     __shared__ double s_m[256], s_v[256];
-    value_tables(s_m, s_v);
-    if (whole(D)) step_q8<true, P, G>(a, D, tensor, s_m, s_v);
-    else step_q8<false, P, G>(a, D, tensor, s_m, s_v);
+    __shared__ Step s_step;
+    if (whole(D)) step_q8<true, P, G>(a, D, tensor, s_m, s_v, &s_step);
+    else step_q8<false, P, G>(a, D, tensor, s_m, s_v, &s_step);
 }
 
 // The moments that the codes stand for.
@@ -396,9 +399,6 @@ template <typename P, typename G> hipError_t launch_pg(const AdamArgs& a, int bi
 
 hipError_t launch_adamw(const AdamArgs& a, int p_dtype, int g_dtype, int bits, hipStream_t s) {
     if (!grid_fits(a.n_chunks, kNT)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(adamw_begin, dim3(1), dim3(1), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
     if (p_dtype == 0) return g_dtype == 0 ? launch_pg<float, float>(a, bits, s) : launch_pg<float, uint16_t>(a, bits, s);
     return g_dtype == 0 ? launch_pg<uint16_t, float>(a, bits, s) : launch_pg<uint16_t, uint16_t>(a, bits, s);
 }

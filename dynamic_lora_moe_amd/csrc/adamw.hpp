@@ -25,19 +25,11 @@ struct AdDesc {
     int32_t vec;     // every pointer allows four elements per access
 };
 
-// Device words of a handle.
-struct AdWords {
-    int64_t t;     // steps taken, the running one included
-    int32_t err;   // a gradient was not finite
-    // the running step's
-    float gs, lr;    // gradient scale, rate
-    float ic1, rc2;  // 1 / (1 - b1^t), sqrt(1 / (1 - b2^t))
-};
-
 struct AdamArgs {
     const AdDesc* descs;
     const int32_t* chunk_tensor;  // the tensor of every chunk
-    AdWords* words;
+    int32_t* steps;               // steps taken, one count per chunk
+    int32_t* err;                 // set where a gradient is not finite
     int64_t n_chunks;
     double beta1, beta2, lb1, lb2;  // and their natural logarithms
     float lr, eps;

@@ -199,9 +199,11 @@ struct dlm_sgmm_group {
 };
 
 struct dlm_adamw {
-    AdDesc* d_descs = nullptr;  // device block: descriptors, then the tensor of every chunk
+    AdDesc* d_descs = nullptr;  // device block: descriptors, the tensor of every chunk, every chunk's step count, the error word
     const int32_t* d_chunk_tensor = nullptr;
-    AdWords* d_words = nullptr;
+    int32_t* d_steps = nullptr;
+    int32_t* d_err = nullptr;
+    int64_t step0 = 0;
     int64_t n_chunks = 0;
     int32_t p_dtype = 0, g_dtype = 0, bits = 32;
     uint32_t seed = 0;
@@ -1396,30 +1398,30 @@ int dlm_adamw_create(const dlm_adamw_param* params, int32_t n, int32_t p_dtype, 
         Span a, b;
         if (write_conflict(std::move(v), &a, &b)) return conflict_fail("adamw_create", a, b);
         desc_bytes = (sizeof(AdDesc) * n + 255) & ~(size_t)255;
-        blob.resize(desc_bytes + sizeof(int32_t) * (size_t)chunks + 256);
+        blob.resize(desc_bytes + sizeof(int32_t) * (2 * (size_t)chunks + 1));
         std::memcpy(blob.data(), descs.data(), sizeof(AdDesc) * n);
         int32_t* map = (int32_t*)(blob.data() + desc_bytes);
         for (int i = 0; i < n; ++i) {
             const int64_t end = i + 1 < n ? descs[i + 1].chunk0 : chunks;
             for (int64_t c = descs[i].chunk0; c < end; ++c) map[c] = i;
         }
+        std::fill(map + chunks, map + 2 * chunks, (int32_t)step);
+        map[2 * chunks] = 0;
         h = new dlm_adamw();
     } catch (const std::bad_alloc&) {
         return fail(DLM_ENOMEM, "adamw_create: host allocation failed");
     }
-    AdWords w{};
-    w.t = step;
     hipError_t e = hipMalloc((void**)&h->d_descs, blob.size());
     if (e == hipSuccess) e = hipMemcpy(h->d_descs, blob.data(), blob.size(), hipMemcpyHostToDevice);
-    if (e == hipSuccess) e = hipMalloc((void**)&h->d_words, 256);
-    if (e == hipSuccess) e = hipMemcpy(h->d_words, &w, sizeof w, hipMemcpyHostToDevice);
     if (e != hipSuccess) {
         if (h->d_descs) (void)hipFree(h->d_descs);
-        if (h->d_words) (void)hipFree(h->d_words);
         delete h;
         return hip_fail(e, "adamw_create");
     }
     h->d_chunk_tensor = (const int32_t*)((const char*)h->d_descs + desc_bytes);
+    h->d_steps = const_cast<int32_t*>(h->d_chunk_tensor) + chunks;
+    h->d_err = h->d_steps + chunks;
+    h->step0 = step;
     h->n_chunks = chunks;
     h->p_dtype = p_dtype;
     h->g_dtype = g_dtype;
@@ -1433,7 +1435,6 @@ int dlm_adamw_destroy(dlm_adamw* h) {
     if (!h) return fail(DLM_EINVAL, "adamw_destroy: null handle");
     const hipError_t e = hipDeviceSynchronize();
     (void)hipFree(h->d_descs);
-    (void)hipFree(h->d_words);
     delete h;
     if (e != hipSuccess) return hip_fail(e, "adamw_destroy");
     return ok();
@@ -1449,7 +1450,8 @@ int dlm_adamw_step(dlm_adamw* h, const dlm_adamw_cfg* c, const float* lr_scale, 
     AdamArgs a{};
     a.descs = h->d_descs;
     a.chunk_tensor = h->d_chunk_tensor;
-    a.words = h->d_words;
+    a.steps = h->d_steps;
+    a.err = h->d_err;
     a.n_chunks = h->n_chunks;
     a.beta1 = c->beta1;
     a.beta2 = c->beta2;
@@ -1467,13 +1469,14 @@ int dlm_adamw_step(dlm_adamw* h, const dlm_adamw_cfg* c, const float* lr_scale, 
 
 int dlm_adamw_status(dlm_adamw* h, int64_t* step, int32_t* code, void* stream) {
     if (!h || !step || !code) return fail(DLM_EINVAL, "adamw_status: null argument");
-    AdWords w{};
+    int32_t t = (int32_t)h->step0, err = 0;  // a handle of empty tensors counts nothing
     hipError_t e = hipStreamSynchronize((hipStream_t)stream);
-    if (e == hipSuccess) e = hipMemcpy(&w, h->d_words, sizeof w, hipMemcpyDeviceToHost);
-    if (e == hipSuccess && w.err) e = hipMemset(&h->d_words->err, 0, sizeof w.err);
+    if (e == hipSuccess && h->n_chunks > 0) e = hipMemcpy(&t, h->d_steps, sizeof t, hipMemcpyDeviceToHost);
+    if (e == hipSuccess) e = hipMemcpy(&err, h->d_err, sizeof err, hipMemcpyDeviceToHost);
+    if (e == hipSuccess && err) e = hipMemset(h->d_err, 0, sizeof err);
     if (e != hipSuccess) return hip_fail(e, "adamw_status");
-    *step = w.t;
-    *code = w.err ? DLM_EDEVICE : DLM_OK;
+    *step = t;
+    *code = err ? DLM_EDEVICE : DLM_OK;
     return ok();
 }
 

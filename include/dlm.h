@@ -530,7 +530,7 @@ int dlm_adamw_create(const dlm_adamw_param* params, int32_t n, int32_t p_dtype, 
 int dlm_adamw_destroy(dlm_adamw* h);
 
 /*
- * One step over every tensor, two launches (a one-thread count, the step), no allocation:
+ * One step over every tensor, one launch, no allocation:
  *   t <- t + 1,  g' = grad_scale g,  m <- b1 m + (1 - b1) g',  v <- b2 v + (1 - b2) g'^2
  *   w <- w (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
  * w = the master where there is one, else the parameter; lr = cfg's times
