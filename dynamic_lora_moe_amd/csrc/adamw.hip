@@ -49,13 +49,15 @@ static_assert(kAdamBlock == 4 * kWave, "a wave's four elements per lane are one 
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// Four consecutive elements as loaded.
+// Four consecutive elements as loaded.  Loads and stores are nontemporal: every
+// array is touched once, and kept out of the caches it leaves them to whatever
+// comes next (322 million weights 1.69 ms against 1.79, one layer's 54 us against 63).
 template <typename T> struct Raw4;
 template <> struct Raw4<float> { u32x4 r; };
 template <> struct Raw4<uint16_t> { u32x2 r; };
 
-__device__ __forceinline__ void load4(Raw4<float>& o, const float* p) { o.r = *(gcptr<u32x4>)p; }
-__device__ __forceinline__ void load4(Raw4<uint16_t>& o, const uint16_t* p) { o.r = *(gcptr<u32x2>)p; }
+__device__ __forceinline__ void load4(Raw4<float>& o, const float* p) { o.r = __builtin_nontemporal_load((gcptr<u32x4>)p); }
+__device__ __forceinline__ void load4(Raw4<uint16_t>& o, const uint16_t* p) { o.r = __builtin_nontemporal_load((gcptr<u32x2>)p); }
 __device__ __forceinline__ void widen(const Raw4<float>& o, float (&f)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(o.r[j]);
@@ -68,10 +70,12 @@ __device__ __forceinline__ void widen(const Raw4<uint16_t>& o, float (&f)[4]) {
     }
 }
 __device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
-    *(gptr<u32x4>)p = u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+    const u32x4 o = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+    __builtin_nontemporal_store(o, (gptr<u32x4>)p);
 }
 __device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
-    *(gptr<u32x2>)p = u32x2{pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3])};
+    const u32x2 o = {pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3])};
+    __builtin_nontemporal_store(o, (gptr<u32x2>)p);
 }
 // One element (tensors whose pointers or end do not allow four).
 __device__ __forceinline__ float load1(const float* p) { return gld(p); }
