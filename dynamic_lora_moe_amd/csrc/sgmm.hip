@@ -648,7 +648,7 @@ __device__ __forceinline__ int mask_list(uint32_t m, int* out) {
 constexpr int kXRows = 32;
 // K is staged through LDS in kShrinkStep-wide steps: 64-wide K chunks of one
 // step, and 16-byte chunks of one x row of a step.  A work item covers one
-// slice of a.kslice (kSgmmKSlice; kSgmmKSliceFew for the gradients of few
+// slice of kslice columns (kSgmmKSlice; kSgmmKSliceFew for the gradients of few
 // rows), a whole number of steps, with its accumulators held in registers
 // across them.
 constexpr int kShrinkStep = 512;
@@ -707,10 +707,10 @@ struct ShrinkLds {
 template <int R16, bool PK>
 __device__ __forceinline__ void shrink_item(const SgmmArgs& a, int64_t gks, int tile0, int n_tiles,
                                             const int32_t* i_perm, const uint32_t* i_ep, ShrinkLds& sm,
-                                            int32_t* dep = nullptr) {
+                                            int32_t* dep = nullptr, int kslice = kSgmmKSlice) {
     constexpr int RPAD = R16 * 16;
     const SgDesc D = a.descs ? a.ks_desc[gks] : a.single;
-    const int k0 = (int)(gks - D.ks0) * a.kslice;
+    const int k0 = (int)(gks - D.ks0) * kslice;
     const int32_t* perm = (const int32_t*)(a.ws + a.L.perm);
     const uint32_t* epk = (const uint32_t*)(a.ws + a.L.epk);
     float* v = (float*)(a.ws + a.L.v) + gks * a.L.T_pad * 2 * RPAD;
@@ -745,7 +745,7 @@ __device__ __forceinline__ void shrink_item(const SgmmArgs& a, int64_t gks, int 
     const uint16_t* __restrict__ x = (const uint16_t*)D.x;
     const uint16_t* __restrict__ A = (const uint16_t*)(PK ? D.Ap : D.A);
     // steps of this slice inside d_in (the same for every wave)
-    const int n_left = (d_in - k0 + kShrinkStep - 1) / kShrinkStep, n_full = a.kslice / kShrinkStep;
+    const int n_left = (d_in - k0 + kShrinkStep - 1) / kShrinkStep, n_full = kslice / kShrinkStep;
     const int n_steps = n_left < n_full ? n_left : n_full;
 
     // x step: thread tid reads chunk tid % kXC of rows tid / kXC + kXR j
@@ -966,7 +966,7 @@ void sgmm_shrink_bf16(SgmmArgs a) {
     const int64_t gks = t / n_tiles;  // slice index over all problems
     __shared__ ShrinkLds sm;
     shrink_item<R16, PK>(a, gks, (int)(t - gks * n_tiles), n_tiles, a.inline_seg ? s_iperm : nullptr,
-                         a.inline_seg ? s_iep : nullptr, sm);
+                         a.inline_seg ? s_iep : nullptr, sm, nullptr, a.kslice);
 }
 
 // ---- expand (bf16, MFMA) -----------------------------------------------------
