@@ -570,6 +570,7 @@ class SgmmGroup:
         """Bind the buffers of backward(): per problem dy [T][d_out] and dx [T][d_in]
         (the problems' dtype; dxs or an entry of it may be None, and problems that
         share an x may share a dx), dA [E][r][d_in] and dB [E][d_out][r] fp32."""
+        _here(self._keep[0][0], None, "problem 0 x")
         n = self.n
         dys, dAs, dBs = list(dys), list(dAs), list(dBs)
         dxs = [None] * n if dxs is None else list(dxs)
@@ -636,7 +637,8 @@ ADAMW_BLOCK = 256  # elements that share a scale of the 8-bit moments
 class AdamW:
     """AdamW over many tensors at once (params updated in place).
 
-    params / grads: device tensors of one dtype each (fp32 or bf16), any shapes.
+    params / grads: device tensors of one dtype each (fp32 or bf16), any shapes.  A
+    step reads the gradients from these buffers.
     masters: per parameter an fp32 copy that the step updates (a bf16 parameter
     then becomes its rounding), or None.  state_bits 32: moments fp32; 8: codes
     with a scale per 256 elements.  states: per parameter (m, v), or with 8 bits

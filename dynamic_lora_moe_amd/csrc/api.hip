@@ -97,6 +97,18 @@ bool write_conflict(std::vector<Span> v, Span* a, Span* b) {
     return false;
 }
 
+// The same for the few spans of one call, pair by pair: it allocates nothing.
+template <int N> bool pair_conflict(const Span (&v)[N], Span* a, Span* b) {
+    for (int i = 0; i < N; ++i)
+        for (int k = 0; k < i; ++k)
+            if (v[k].hi > v[i].lo && v[i].hi > v[k].lo && (v[k].write || v[i].write)) {
+                *a = v[k];
+                *b = v[i];
+                return true;
+            }
+    return false;
+}
+
 int conflict_fail(const char* call, const Span& a, const Span& b) {
     return fail(DLM_EINVAL, "%s: %s %d overlaps %s %d, and one of them is written in place", call, a.what, a.who,
                 b.what, b.who);
@@ -306,12 +318,12 @@ int dlm_route(const void* logits, int64_t ld, const float* bias, int64_t T, int3
     if (rc != DLM_OK) return rc;
     if (T == 0) return ok();
     if (!logits || !idx || !g) return fail(DLM_EINVAL, "route: null pointer");
-    std::vector<Span> v = {span(logits, rows_bytes(T, ld, E, esize(dtype)), false, "logits", 0),
-                           span(idx, (size_t)T * a.k * 4, true, "idx", 0), span(g, (size_t)T * a.k * 4, true, "g", 0)};
-    if (bias) v.push_back(span(bias, (size_t)E * 4, false, "bias", 0));
-    if (counts) v.push_back(span(counts, (size_t)E * 4, true, "counts", 0));
+    const Span v[] = {span(logits, rows_bytes(T, ld, E, esize(dtype)), false, "logits", 0),
+                      span(idx, (size_t)T * a.k * 4, true, "idx", 0), span(g, (size_t)T * a.k * 4, true, "g", 0),
+                      span(bias, bias ? (size_t)E * 4 : 0, false, "bias", 0),
+                      span(counts, counts ? (size_t)E * 4 : 0, true, "counts", 0)};
     Span p, q;
-    if (write_conflict(std::move(v), &p, &q)) return conflict_fail("route", p, q);
+    if (pair_conflict(v, &p, &q)) return conflict_fail("route", p, q);
     a.bias = bias;
     a.scores_order = bias || (a.n_groups > 1 && a.group_top == 2) ? 1 : 0;
     a.need_scores = a.scores_order || (a.score == kRouteSoftmax && !a.renorm) ? 1 : 0;
@@ -334,11 +346,10 @@ int dlm_route_backward(const void* logits, int64_t ld, const int32_t* idx, const
     if (!logits || !idx || !dg || !dlogits) return fail(DLM_EINVAL, "route_backward: null pointer");
     const size_t es = esize(dtype);
     Span p, q;
-    if (write_conflict({span(logits, rows_bytes(T, ld, E, es), false, "logits", 0),
-                        span(dlogits, rows_bytes(T, ldd, E, es), true, "dlogits", 0),
-                        span(idx, (size_t)T * a.k * 4, false, "idx", 0), span(dg, (size_t)T * a.k * 4, false, "dg", 0)},
-                       &p, &q))
-        return conflict_fail("route_backward", p, q);
+    const Span v[] = {span(logits, rows_bytes(T, ld, E, es), false, "logits", 0),
+                      span(dlogits, rows_bytes(T, ldd, E, es), true, "dlogits", 0),
+                      span(idx, (size_t)T * a.k * 4, false, "idx", 0), span(dg, (size_t)T * a.k * 4, false, "dg", 0)};
+    if (pair_conflict(v, &p, &q)) return conflict_fail("route_backward", p, q);
     a.in_idx = idx;
     a.dg = dg;
     a.dlogits = dlogits;
@@ -1487,10 +1498,10 @@ int dlm_adamw_read_state(const int8_t* m, const uint8_t* v, const float* m_scale
     if (!m || !v || !m_scale || !v_scale || !m_out || !v_out) return fail(DLM_EINVAL, "adamw_read_state: null pointer");
     const size_t nb = (size_t)(n + kAdamBlock - 1) / kAdamBlock * 4;
     Span a, b;
-    if (write_conflict({span(m, n, false, "m", 0), span(v, n, false, "v", 0), span(m_scale, nb, false, "m_scale", 0),
-                        span(v_scale, nb, false, "v_scale", 0), span(m_out, (size_t)n * 4, true, "m_out", 0),
-                        span(v_out, (size_t)n * 4, true, "v_out", 0)}, &a, &b))
-        return conflict_fail("adamw_read_state", a, b);
+    const Span v8[] = {span(m, n, false, "m", 0), span(v, n, false, "v", 0), span(m_scale, nb, false, "m_scale", 0),
+                       span(v_scale, nb, false, "v_scale", 0), span(m_out, (size_t)n * 4, true, "m_out", 0),
+                       span(v_out, (size_t)n * 4, true, "v_out", 0)};
+    if (pair_conflict(v8, &a, &b)) return conflict_fail("adamw_read_state", a, b);
     const hipError_t e = launch_adamw_read_state(m, v, m_scale, v_scale, n, m_out, v_out, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "adamw_read_state launch");
     return ok();
