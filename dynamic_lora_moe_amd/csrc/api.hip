@@ -705,7 +705,7 @@ int run_sgmm(const SgDesc* d_descs, const SgDesc* ks_desc, const SgDesc* cb_desc
              int64_t total_ks, int64_t d_out_max, int32_t w_max, const int32_t* idx, const float* g, int64_t T,
              int E, int r, float scale, int dtype, int packed, void* ws, const SgLayout& L, hipStream_t s,
              int32_t* status_out = nullptr) {
-    SgmmArgs a;
+    SgmmArgs a{};
     a.w_max = w_max;
     a.kslice = kSgmmKSlice;
     a.status_out = status_out;
@@ -1048,7 +1048,7 @@ int dlm_sgmm_group_bind_grads(dlm_sgmm_group* h, const void* const* dy, void* co
         for (int i = 0; i < n; ++i) {
             const SgDesc& p = h->h_descs[i];
             o_at[i] = pack_bytes;
-            pack_bytes += a256((size_t)E * r * p.d_in * es);
+            pack_bytes += a256((size_t)E * (bf ? (r + 15) / 16 * 16 : r) * p.d_in * es);
             o_bt[i] = pack_bytes;
             pack_bytes += a256((size_t)E * r * p.d_out * es);
             if (!dx || !dx[i]) continue;
@@ -1088,6 +1088,8 @@ int dlm_sgmm_group_bind_grads(dlm_sgmm_group* h, const void* const* dy, void* co
 
         e = hipDeviceSynchronize();  // launches in flight read the current tables
         if (e == hipSuccess) e = hipMalloc((void**)&G.d_pack, pack_bytes);
+        // the transposes' padding ranks, which no call writes
+        if (e == hipSuccess && bf && r % 16 != 0) e = hipMemset(G.d_pack, 0, pack_bytes);
         std::vector<char> tab;
         auto put = [&](const void* src, size_t bytes) {
             const size_t o = tab.size();
@@ -1293,6 +1295,7 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
     b.dg = dg;
     auto expand_args = [&](const dlm_sgmm_group::Grads::Wave& w) {
         SgmmArgs x = a;
+        x.packed_b = bf ? 1 : 0;
         x.descs = w.descs;
         x.cb_desc = w.cb_desc;
         x.ks_desc = nullptr;

@@ -559,11 +559,11 @@ __global__ __launch_bounds__(kSegThreads) void grad_prep(SgGradArgs a, const flo
             const int64_t nq = P.d_in / 8, rho = i % r, kq = (i / r) % nq, e = i / (r * nq);
             const u32x4 v = ld128((const uint16_t*)P.A + ((e * r + rho) * nq + kq) * 8);
             st128((uint16_t*)P.Ap + 8 * i, v);
-            uint16_t* t = (uint16_t*)P.At + (e * P.d_in + 8 * kq) * r + rho;
+            uint16_t* t = (uint16_t*)P.At + ((e * ((r + 15) / 16) + rho / 16) * P.d_in + 8 * kq) * 16 + rho % 16;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                gst(t + (2 * j) * r, (uint16_t)(v[j] & 0xffffu));
-                gst(t + (2 * j + 1) * r, (uint16_t)(v[j] >> 16));
+                gst(t + 32 * j, (uint16_t)(v[j] & 0xffffu));
+                gst(t + 32 * j + 16, (uint16_t)(v[j] >> 16));
             }
         } else {
             const int64_t b = i - na, nq = P.d_out / 8, rho = b % r, kq = (b / r) % nq, e = b / (r * nq);
@@ -1010,7 +1010,11 @@ struct ExpandLds {
 constexpr int kDepSpinMax = 1 << 20;
 
 // dep: the one-launch form's shrink counts (see shrink_item), or nullptr.
-template <int R16, bool RVEC>
+// BV: the layout of B. 0: [E][d_out][r]; 1: the same with r % 8 == 0; 2: packed
+// [E][R16][d_out][16], padding ranks 0 (the gradients' transposes, whose layout is
+// theirs to choose): one load then covers 1 KB in a row, where at rank 64 it
+// touches 32 bytes of every second cache line.
+template <int R16, int BV>
 __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int tile, int half,
                                             const int32_t* i_perm, const uint32_t* i_ep, const f32x2* i_g,
                                             ExpandLds& sm, const int32_t* dep = nullptr) {
@@ -1109,6 +1113,11 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
     const int nq = nU * R16;
     const bool shared_u = nq <= kQLds;
     float* s_v = shared_u ? (float*)&s_y[0][0] : (float*)&s_u[0][0][0];
+    // in LDS the 16-byte chunk c of row n is at chunk c ^ (n & kVX) of the row, so
+    // that the rows' reads of one chunk fall on different banks (kVX + 1 divides a
+    // row's kVC chunks; in the one-launch form it would spill at some ranks)
+    constexpr int kVC = 2 * RPAD / 4, kVX = BV != 2 ? 0 : R16 % 2 ? 7 : 15;
+    static_assert(kVC % (kVX + 1) == 0, "a chunk stays in its row");
     if constexpr (FOLD) {
         // the tile's v block (32 rows x 2 slots x RPAD floats, contiguous in
         // each slice) with the problem's K slices added in slice order; it
@@ -1138,11 +1147,15 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
                             acc[k][c] = __float_as_uint(__uint_as_float(acc[k][c]) + __uint_as_float(p[j][k][c]));
         }
 #pragma unroll
-        for (int k = 0; k < R16; ++k) *(u32x4*)(s_v + 4 * threadIdx.x + 1024 * k) = acc[k];
+        for (int k = 0; k < R16; ++k) {
+            const int c = threadIdx.x + 256 * k;  // the block's 16-byte chunk c, moved inside its row
+            *(u32x4*)(s_v + 4 * (c ^ ((c / kVC) & kVX))) = acc[k];
+        }
         __syncthreads();
     }
     const float* v0 = FOLD ? s_v + n * 2 * RPAD : v + ((int64_t)(tile * 32 + n) * 2) * RPAD;
     const float* v1 = v0 + RPAD;
+    auto v_lds = [&](int rank) { return *(const u32x4*)(v0 + 4 * ((rank / 4) ^ (n & kVX))); };
     // row-side operand of (expert U[q / R16], ranks 16(q % R16) + 8h + [0,8)):
     // u = s*g*v as hi + lo bf16 (v = the K slices' sum).  v of a slot that is not this expert, or of a
     // padding rank, is never written: it is selected away, not multiplied by 0.
@@ -1152,10 +1165,10 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
         const bool m0 = (e0 == e), m1 = (e1 == e);
         u32x4 p0, p1, q0, q1;
         if constexpr (FOLD) {
-            p0 = *(const u32x4*)(v0 + rho0);
-            p1 = *(const u32x4*)(v0 + rho0 + 4);
-            q0 = *(const u32x4*)(v1 + rho0);
-            q1 = *(const u32x4*)(v1 + rho0 + 4);
+            p0 = v_lds(rho0);
+            p1 = v_lds(rho0 + 4);
+            q0 = v_lds(RPAD + rho0);
+            q1 = v_lds(RPAD + rho0 + 4);
         } else {
             p0 = ld128(v0 + rho0);
             p1 = ld128(v0 + rho0 + 4);
@@ -1189,15 +1202,17 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
         blo = u32x4{lw[0], lw[1], lw[2], lw[3]};
     };
     // column-side operand: B[e][col][16(q % R16) + 8h .. +8]; padding columns
-    // read column 0 and are never stored.  With r % 8 == 0 (RVEC) the load is
+    // read column 0 and are never stored.  With r % 8 == 0 (BV 1) the load is
     // one unguarded 16-byte access (a rank chunk past r reads rank 0 and is
     // replaced by zero), so the loads of consecutive q stay in flight together.
     auto load_bop = [&](int q, int col) {
         const int e = s_U[q / R16];
         const int rho0 = (q % R16) * 16 + 8 * h;
+        if constexpr (BV == 2)
+            return ld128(B + ((int64_t)(e * R16 + q % R16) * d_out + (col < d_out ? col : 0)) * 16 + 8 * h);
         const uint16_t* bp = B + ((int64_t)e * d_out + (col < d_out ? col : 0)) * r + rho0;
         u32x4 ao = {0u, 0u, 0u, 0u};
-        if constexpr (RVEC) {
+        if constexpr (BV == 1) {
             const u32x4 t = ld128(bp - (rho0 < r ? 0 : rho0));
             ao = rho0 < r ? t : ao;
         } else {
@@ -1296,7 +1311,7 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
 // (kECols / 2 columns), dispatched last: a launch drains for about one item's
 // duration while its last items finish, and half items halve that.  Every
 // column is computed the same way in either form.
-template <int R16, bool RVEC>
+template <int R16, int BV>
 __global__ __launch_bounds__(256) void sgmm_expand_bf16(SgmmArgs a) {
     const int32_t* hdr = (const int32_t*)(a.ws + a.L.hdr);
     __shared__ int32_t s_iperm[kWave];
@@ -1332,7 +1347,7 @@ __global__ __launch_bounds__(256) void sgmm_expand_bf16(SgmmArgs a) {
     if (t >= n_live) return;
     const int64_t cgg = t / n_tiles;
     __shared__ ExpandLds sm;
-    expand_item<R16, RVEC>(a, cgg, (int)(t - cgg * n_tiles), half, a.inline_seg ? s_iperm : nullptr,
+    expand_item<R16, BV>(a, cgg, (int)(t - cgg * n_tiles), half, a.inline_seg ? s_iperm : nullptr,
                            a.inline_seg ? s_iep : nullptr, a.inline_seg ? s_ig : nullptr, sm);
 }
 
@@ -1406,7 +1421,7 @@ void sgmm_fused_bf16(SgmmArgs a) {
             c = e[15] + u / e[3];
             t = u % e[3];
         }
-        expand_item<R16, RVEC>(a, c, t, -1, nullptr, nullptr, nullptr, lds.e, dep);
+        expand_item<R16, RVEC ? 1 : 0>(a, c, t, -1, nullptr, nullptr, nullptr, lds.e, dep);
     }
 }
 
@@ -1787,10 +1802,12 @@ template <int R16>
 hipError_t launch_expand(const SgmmArgs& a, hipStream_t s) {
     const int64_t per_max = (a.n_expand_units + 7) / 8;
     const dim3 ge((unsigned)(8 * (per_max + (per_max < kExpandSplit ? per_max : kExpandSplit))));
-    if (a.r % 8 == 0)
-        hipLaunchKernelGGL((sgmm_expand_bf16<R16, true>), ge, dim3(256), 0, s, a);
+    if (a.packed_b)
+        hipLaunchKernelGGL((sgmm_expand_bf16<R16, 2>), ge, dim3(256), 0, s, a);
+    else if (a.r % 8 == 0)
+        hipLaunchKernelGGL((sgmm_expand_bf16<R16, 1>), ge, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((sgmm_expand_bf16<R16, false>), ge, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((sgmm_expand_bf16<R16, 0>), ge, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

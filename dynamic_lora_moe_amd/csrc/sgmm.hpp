@@ -107,6 +107,7 @@ struct SgmmArgs {
     int32_t* status_out;   // device word that also receives the set-validity flag, or nullptr
     int32_t inline_seg;    // 1: the shrink and expand order the rows themselves (launch_sgmm sets it)
     int32_t w_max;         // largest K slices + column groups of one problem
+    int32_t packed_b;      // 1: the expand reads every problem's B packed, [E][rank chunk of 16][d_out][16] (bf16)
     int32_t kslice;        // K slice width of the shrink (the owners' n_ks goes by it)
 };
 
@@ -150,7 +151,9 @@ struct SgGrad {
     const void* x;   // [T][d_in]
     const void* dy;  // [T][d_out]
     void* Ap;        // A packed for the shrink (bf16), else unused
-    void* At;        // [E][d_in][r]: A transposed, the dx expand's up matrix
+    // A transposed, the dx expand's up matrix: [E][rank chunk of 16][d_in][16], the
+    // last chunk's padding ranks 0 (bf16), or [E][d_in][r] (fp32)
+    void* At;
     void* Bt;        // B transposed: [E][d_out / 8][r][8] (bf16) or [E][r][d_out] (fp32)
     int32_t d_in, d_out;
     int64_t pk0;     // first group (bf16: 8 elements, fp32: one) of its banks (prefix sum)
