@@ -1220,6 +1220,9 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
     b.probs = S.probs;
     b.outers = G.outers;
     b.unit_outer = G.unit_outer;
+    b.ks_desc = S.ks_desc;
+    b.total_ks = S.total_ks;
+    b.kslice = S.width;
     b.n_prob = h->n;
     b.n_units = G.n_units;
     b.pk_total = G.pk_total;
@@ -1311,7 +1314,12 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
     for (const auto& w : S.waves) fits = fits && sgmm_launches_fit(expand_args(w), h->dtype);
     if (!fits) return hip_fail(hipErrorInvalidConfiguration, "sgmm_group_backward");
     hipError_t e = launch_grad_prep(b, g, h->dtype, s);
-    if (e == hipSuccess) e = bf ? launch_sgmm_shrink(a, s) : launch_grad_shrink_f32(b, s);
+    if (bf && h->r >= kGradListRank) {
+        if (e == hipSuccess) e = launch_grad_shrink(b, s);
+        if (e == hipSuccess) e = launch_sgmm_vsum(a, s);
+    } else if (e == hipSuccess) {
+        e = bf ? launch_sgmm_shrink(a, s) : launch_grad_shrink_f32(b, s);
+    }
     if (e == hipSuccess) e = launch_grad_coefs(b, h->dtype, s);
     for (const auto& w : S.waves)
         if (e == hipSuccess) e = launch_sgmm_expand(expand_args(w), h->dtype, s);

@@ -1780,6 +1780,12 @@ __global__ __launch_bounds__(256) void sgmm_pack_a_kernel(const uint16_t* __rest
 // Grid for at most max_items work items (a multiple of 8: one share per XCD).
 inline int64_t item_grid(int64_t max_items) { return 8 * ((max_items + 7) / 8); }
 
+hipError_t launch_vsum(const SgmmArgs& a, hipStream_t s) {
+    const dim3 gs((unsigned)((a.L.T_pad * 2 * a.L.r_pad / 4 + 255) / 256), (unsigned)a.n_prob);
+    hipLaunchKernelGGL(sgmm_vsum_kernel, gs, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 // The shrink, and above kSgmmFoldRank the K-slice sum.
 template <int R16>
 hipError_t launch_shrink(const SgmmArgs& a, hipStream_t s) {
@@ -1790,11 +1796,7 @@ hipError_t launch_shrink(const SgmmArgs& a, hipStream_t s) {
         hipLaunchKernelGGL((sgmm_shrink_bf16<R16, false>), gs, dim3(256), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (R16 > kExpandFoldR16 && a.total_ks > a.n_prob) {  // K slices the expand does not add itself
-        const dim3 gs((unsigned)((a.L.T_pad * 2 * a.L.r_pad / 4 + 255) / 256), (unsigned)a.n_prob);
-        hipLaunchKernelGGL(sgmm_vsum_kernel, gs, dim3(256), 0, s, a);
-        e = hipGetLastError();
-    }
+    if (R16 > kExpandFoldR16 && a.total_ks > a.n_prob) e = launch_vsum(a, s);  // K slices the expand does not add itself
     return e;
 }
 
@@ -1962,6 +1964,9 @@ hipError_t launch_grad_prep(const SgGradArgs& a, const float* g, int dtype, hipS
     return hipGetLastError();
 }
 hipError_t launch_sgmm_shrink(const SgmmArgs& a, hipStream_t s) { return launch_mfma_r(a, s, true, false); }
+hipError_t launch_sgmm_vsum(const SgmmArgs& a, hipStream_t s) {
+    return a.L.r_pad > kSgmmFoldRank && a.total_ks > a.n_prob ? launch_vsum(a, s) : hipSuccess;
+}
 hipError_t launch_sgmm_expand(const SgmmArgs& a, int dtype, hipStream_t s) {
     return dtype == 1 ? launch_mfma_r(a, s, false, true) : launch_expand_generic(a, s);
 }

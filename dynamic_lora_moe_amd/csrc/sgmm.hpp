@@ -119,11 +119,14 @@ hipError_t launch_sgmm_pack_a(const void* A, void* Ap, int E, int r, int64_t d_i
 // above kSgmmFoldRank), and the expand of a set of problems whose v (ks0, n_ks)
 // a shrink has left in the workspace: the gradients run other work between them.
 hipError_t launch_sgmm_shrink(const SgmmArgs& a, hipStream_t s);
+hipError_t launch_sgmm_vsum(const SgmmArgs& a, hipStream_t s);  // the K-slice sum alone
 hipError_t launch_sgmm_expand(const SgmmArgs& a, int dtype, hipStream_t s);
 bool sgmm_launches_fit(const SgmmArgs& a, int dtype);
 
 // ---- gradients ----------------------------------------------------------------
 
+// From this rank on the gradients' shrink goes by the experts' slot lists.
+constexpr int kGradListRank = 33;
 // Slots of one list tile.
 constexpr int kGradTile = 32;
 
@@ -191,6 +194,9 @@ struct SgGradArgs {
     const SgGrad* probs;
     const SgOuter* outers;       // 2 * n_prob
     const int32_t* unit_outer;   // the owning entry of every column block
+    const SgDesc* ks_desc;       // the shrink problem (x, A or dy, B^T) of every K slice
+    int64_t total_ks;
+    int32_t kslice;
     int32_t n_prob, n_units;
     int64_t pk_total;
     const int32_t* idx;
@@ -207,6 +213,8 @@ hipError_t launch_grad_zero(const SgGradArgs& a, int dtype, hipStream_t s);
 // Segmentation, lists and the banks' transposes.
 bool grad_prep_fits(const SgGradArgs& a);
 hipError_t launch_grad_prep(const SgGradArgs& a, const float* g, int dtype, hipStream_t s);
+// u and w over the experts' slot lists (bf16).
+hipError_t launch_grad_shrink(const SgGradArgs& a, hipStream_t s);
 hipError_t launch_grad_shrink_f32(const SgGradArgs& a, hipStream_t s);
 hipError_t launch_grad_coefs(const SgGradArgs& a, int dtype, hipStream_t s);
 // dA, dB and dg.

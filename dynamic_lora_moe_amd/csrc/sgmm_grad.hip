@@ -101,6 +101,132 @@ namespace {
 
 __device__ __forceinline__ bool rejected(const SgGradArgs& a) { return gld((const int32_t*)(a.ws + a.G.L.hdr) + SG_ERR) != 0; }
 
+// ---- u, w over the lists (bf16) -----------------------------------------------------
+
+// D = A(16x32) B(32x16) + C: lane l supplies row (l % 16) of A and column
+// (l % 16) of B, k = 8 (l / 16) + [0, 8); register i holds D[4 (l / 16) + i][l % 16].
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+// One work item = (K slice, rank chunk, kListSlots slots of one expert's list): a
+// product with M = ranks, N = slots, K = columns.  The waves take 32 slots each and
+// share the bank's rows.  Both come through LDS, copied directly, two steps in turn:
+// a lane that loads its operand's 16 bytes of a row by itself makes one cache access
+// of them, and those accesses were the bound.
+constexpr int kListSlots = 128;
+constexpr int kListK = 64;  // columns per step
+
+template <int R16>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
+void grad_shrink_list(SgGradArgs a, int n_ch) {
+    constexpr int NR = 16 * R16;
+    const SgLayout& L = a.G.L;
+    if (rejected(a)) return;
+    const int lane = lane_id(), w = wave_id(), n = lane & 15, kg = lane >> 4, r = a.r, E = a.E;
+    // the experts' groups of kListSlots slots: lane e holds expert e's
+    const int32_t* eoff = (const int32_t*)(a.ws + a.G.eoff);
+    const int e_l = lane < E ? lane : E - 1;
+    const int my0 = gld(eoff + e_l), my1 = gld(eoff + e_l + 1);
+    const int ng = lane < E ? (my1 - my0 + kListSlots - 1) / kListSlots : 0;
+    int incl = ng;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up(incl, o, kWave);
+        if (lane >= o) incl += y;
+    }
+    const int n_groups = __shfl(incl, E - 1, kWave);
+    // XCD b % 8 takes a contiguous share, the groups of one slice next to each other
+    const int64_t n_live = a.total_ks * n_ch * n_groups, per = (n_live + 7) / 8;
+    const int64_t j = blockIdx.x >> 3, item = (int64_t)(blockIdx.x & 7) * per + j;
+    if (j >= per || item >= n_live) return;
+    const int group = uniform((int)(item % n_groups));
+    const int ch = uniform((int)(item / n_groups % n_ch));
+    const int64_t gks = item / n_groups / n_ch;
+    const int e = __popcll(__ballot(lane < E && incl <= group));
+    const int p0 = uniform(__shfl(my0, e, kWave) + (group - __shfl(incl - ng, e, kWave)) * kListSlots + 32 * w);
+    const int p1 = uniform(__shfl(my1, e, kWave));
+    const bool mine = p0 < p1;  // (else this wave only helps with the bank)
+
+    const SgDesc D = a.ks_desc[gks];
+    const int d = uniform(D.d_in), nq = d / 8, k0 = (int)(gks - D.ks0) * a.kslice;
+    const int n_steps = ((d - k0 < a.kslice ? d - k0 : a.kslice) + kListK - 1) / kListK;
+    const uint16_t* bank = (const uint16_t*)D.Ap + (int64_t)e * nq * r * 8;
+    int entry[2];  // of the slots whose sums this lane holds
+    const uint16_t* row[4];  // of the slots whose rows it copies
+    const int32_t* srow = (const int32_t*)(a.ws + a.G.srow);
+    auto place = [&](int i) { return mine ? (p0 + i < p1 ? p0 + i : p1 - 1) : 0; };
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+        entry[m] = mine && p0 + 16 * m + n < p1 ? gld((const int32_t*)(a.ws + a.G.slot) + place(16 * m + n)) : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row[i] = (const uint16_t*)D.x + (int64_t)gld(srow + place(8 * i + lane / 8)) * d;
+    __shared__ __attribute__((aligned(16))) uint16_t s_a[2][kListK / 8][NR][8];
+    // 16-byte piece c of slot n is at piece c ^ (n & 7): the reads of a piece of
+    // eight slots fall on different banks
+    __shared__ __attribute__((aligned(16))) uint16_t s_x[2][4][32][kListK];
+    const int xc = 8 * ((lane % 8) ^ (lane / 8));  // the column of a step that this lane copies
+    auto copy = [&](int s) {
+        const int kb = k0 + s * kListK;
+        if (mine) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) copy16_to_lds(row[i] + (kb + xc < d ? kb + xc : 0), s_x[s & 1][w][8 * i]);
+        }
+        // the bank's packed rows: 16-byte pieces (k group, rank); ranks and groups
+        // past the end repeat the last
+#pragma unroll
+        for (int i = 0; i < (2 * R16 + 3) / 4; ++i) {
+            const int c = w + 4 * i, piece = c * kWave + lane, kq = kb / 8 + piece / NR, rho = 64 * ch + piece % NR;
+            if (c < 2 * R16)
+                copy16_to_lds(bank + ((int64_t)(kq < nq ? kq : nq - 1) * r + (rho < r ? rho : r - 1)) * 8,
+                              &s_a[s & 1][0][0][0] + c * kWave * 8);
+        }
+    };
+    f32x4 acc[R16][2];
+#pragma unroll
+    for (int b = 0; b < R16; ++b) acc[b][0] = acc[b][1] = f32x4{};
+    copy(0);
+#pragma unroll 1
+    for (int s = 0; s < n_steps; ++s) {
+        // this step's rows and bank have landed, in every wave, and every wave is
+        // done with the step before, whose half of the buffers is free again
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (s + 1 < n_steps) copy(s + 1);
+        if (!mine) continue;
+        const int kb = k0 + s * kListK;
+        const bool full = kb + kListK <= d;
+#pragma unroll
+        for (int i = 0; i < kListK / 32; ++i) {
+            const bool in = full || kb + 32 * i + 8 * kg < d;
+            u32x4 x[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                x[m] = *(const u32x4*)&s_x[s & 1][w][16 * m + n][8 * ((4 * i + kg) ^ (n & 7))];
+                if (!in) x[m] = u32x4{};
+            }
+#pragma unroll
+            for (int b = 0; b < R16; ++b) {
+                u32x4 h = *(const u32x4*)s_a[s & 1][4 * i + kg][16 * b + n];
+                if (!in) h = u32x4{};  // the repeated group may hold an infinity
+#pragma unroll
+                for (int m = 0; m < 2; ++m) acc[b][m] = mfma16(h, x[m], acc[b][m]);
+            }
+        }
+    }
+    if (!mine) return;
+    // register i of block b: rank 16 b + 4 kg + i of slot n (ranks r .. r_pad - 1 are not read)
+    float* v = (float*)(a.ws + L.v) + gks * L.T_pad * 2 * L.r_pad + 64 * ch + 4 * kg;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        if (entry[m] < 0) continue;
+#pragma unroll
+        for (int b = 0; b < R16; ++b)
+            if (64 * ch + 16 * b < L.r_pad) gst((f32x4*)(v + (int64_t)entry[m] * L.r_pad + 16 * b), acc[b][m]);
+    }
+}
+
 // ---- u, w in fp32 -------------------------------------------------------------------
 
 // One wave per (projection side, position, slot): eight ranks' products at a
@@ -243,13 +369,6 @@ __device__ __forceinline__ void write_dg(const SgGradArgs& a, int64_t i) {
 }
 
 // ---- dA, dB -------------------------------------------------------------------------
-
-// D = A(16x32) B(32x16) + C: lane l supplies row (l % 16) of A and column
-// (l % 16) of B, k = 8 (l / 16) + [0, 8); register i holds D[4 (l / 16) + i][l % 16].
-__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-}
 
 // Stores (or adds) columns 4h .. 4h + 3 of a lane's eight, rank block b: acc[j]
 // holds four ranks of column 4h + j.
@@ -531,6 +650,11 @@ __global__ __launch_bounds__(kWave) void grad_zero(SgGradArgs a, int cols) {
     }
 }
 
+// Work items of grad_shrink_list at most, a multiple of 8.
+int64_t list_blocks(const SgGradArgs& a) {
+    const int64_t items = a.total_ks * rank_chunks(a.G.L) * (a.G.cap / kListSlots + a.E);
+    return (items + 7) / 8 * 8;
+}
 int64_t dg_blocks(const SgGradArgs& a) { return a.dg ? (2 * a.T + 255) / 256 : 0; }
 int64_t outer_blocks(const SgGradArgs& a) {
     return 8ll * a.G.max_chunks * rank_chunks(a.G.L) * ((a.n_units + 7) / 8);
@@ -547,12 +671,24 @@ int sum_blocks(const SgGradArgs& a) { return (16 * outer_r16(a.G.L) * kOuterCols
 bool sgmm_grad_fits(const SgGradArgs& a, int dtype) {
     return grad_prep_fits(a) && grid_fits(a.G.cap / kGradTile, 256) && grid_fits((a.T + 1) / 2, 256) &&
            grid_fits(a.n_units + dg_blocks(a), 256) &&
-           (dtype == 0 || (grid_fits(outer_blocks(a), 256) && grid_fits(sum_items(a) * sum_blocks(a) + dg_blocks(a), 256)));
+           (dtype == 0 || (grid_fits(list_blocks(a), 256) && grid_fits(outer_blocks(a), 256) && grid_fits(sum_items(a) * sum_blocks(a) + dg_blocks(a), 256)));
 }
 
 hipError_t launch_grad_zero(const SgGradArgs& a, int dtype, hipStream_t s) {
     hipLaunchKernelGGL(grad_zero, dim3((unsigned)a.n_units, (unsigned)a.E), dim3(kWave), 0, s, a,
                        grad_cols(dtype));
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_shrink(const SgGradArgs& a, hipStream_t s) {
+    const int n_ch = rank_chunks(a.G.L);
+    const dim3 g((unsigned)list_blocks(a));
+    switch (outer_r16(a.G.L)) {
+        case 1: hipLaunchKernelGGL(grad_shrink_list<1>, g, dim3(256), 0, s, a, n_ch); break;
+        case 2: hipLaunchKernelGGL(grad_shrink_list<2>, g, dim3(256), 0, s, a, n_ch); break;
+        case 3: hipLaunchKernelGGL(grad_shrink_list<3>, g, dim3(256), 0, s, a, n_ch); break;
+        default: hipLaunchKernelGGL(grad_shrink_list<4>, g, dim3(256), 0, s, a, n_ch); break;
+    }
     return hipGetLastError();
 }
 
