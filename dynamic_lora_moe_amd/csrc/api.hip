@@ -1298,7 +1298,6 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
     b.dg = dg;
     auto expand_args = [&](const dlm_sgmm_group::Grads::Wave& w) {
         SgmmArgs x = a;
-        x.packed_b = bf ? 1 : 0;
         x.descs = w.descs;
         x.cb_desc = w.cb_desc;
         x.ks_desc = nullptr;
@@ -1311,7 +1310,7 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
         return x;
     };
     bool fits = sgmm_grad_fits(b, h->dtype) && sgmm_launches_fit(a, h->dtype);
-    for (const auto& w : S.waves) fits = fits && sgmm_launches_fit(expand_args(w), h->dtype);
+    for (const auto& w : S.waves) fits = fits && grad_expand_fits(b, expand_args(w), h->dtype);
     if (!fits) return hip_fail(hipErrorInvalidConfiguration, "sgmm_group_backward");
     hipError_t e = launch_grad_prep(b, g, h->dtype, s);
     if (bf && h->r >= kGradListRank) {
@@ -1320,9 +1319,9 @@ int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* 
     } else if (e == hipSuccess) {
         e = bf ? launch_sgmm_shrink(a, s) : launch_grad_shrink_f32(b, s);
     }
-    if (e == hipSuccess) e = launch_grad_coefs(b, h->dtype, s);
-    for (const auto& w : S.waves)
-        if (e == hipSuccess) e = launch_sgmm_expand(expand_args(w), h->dtype, s);
+    if (e == hipSuccess && S.waves.empty()) e = launch_grad_coefs(b, h->dtype, s);
+    for (const auto& w : S.waves)  // the first also writes the coefficients
+        if (e == hipSuccess) e = launch_grad_expand(b, expand_args(w), &w == &S.waves[0], h->dtype, s);
     if (e == hipSuccess) e = launch_grad_outer(b, h->dtype, s);
     if (e != hipSuccess) return hip_fail(e, "sgmm_group_backward");
     return ok();

@@ -36,6 +36,7 @@
 #include "gfx950.hpp"
 #include "internal.hpp"
 #include "sgmm.hpp"
+#include "sgmm_coefs.hpp"
 
 namespace dlm {
 
@@ -1311,6 +1312,22 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
 // (kECols / 2 columns), dispatched last: a launch drains for about one item's
 // duration while its last items finish, and half items halve that.  Every
 // column is computed the same way in either form.
+// The item of expand workgroup bid (-1: none) and its half (-1: the whole).
+__device__ __forceinline__ int64_t expand_place(const SgmmArgs& a, int64_t bid, int n_tiles, int& half) {
+    const int64_t n_live = a.total_cb * n_tiles, per = (n_live + 7) / 8;
+    const int64_t m = per < kExpandSplit ? per : kExpandSplit;
+    const int64_t j = bid >> 3;
+    half = -1;
+    if (j >= per + m) return -1;
+    int64_t jj = j;
+    if (j >= per - m) {
+        const int64_t k = j - (per - m);
+        jj = per - m + (k >> 1);
+        half = (int)(k & 1);
+    }
+    const int64_t t = (bid & 7) * per + jj;
+    return t < n_live ? t : -1;
+}
 template <int R16, int BV>
 __global__ __launch_bounds__(256) void sgmm_expand_bf16(SgmmArgs a) {
     const int32_t* hdr = (const int32_t*)(a.ws + a.L.hdr);
@@ -1332,23 +1349,33 @@ __global__ __launch_bounds__(256) void sgmm_expand_bf16(SgmmArgs a) {
         n_tiles = uniform(gld(hdr + SG_NTILES));
         if (gld(hdr + SG_ERR)) return;
     }
-    const int64_t n_live = a.total_cb * n_tiles, per = (n_live + 7) / 8;
-    const int64_t m = per < kExpandSplit ? per : kExpandSplit;
-    const int64_t bid = blockIdx.x, j = bid >> 3;
-    if (j >= per + m) return;
-    int64_t jj = j;
-    int half = -1;
-    if (j >= per - m) {
-        const int64_t k = j - (per - m);
-        jj = per - m + (k >> 1);
-        half = (int)(k & 1);
-    }
-    const int64_t t = (bid & 7) * per + jj;
-    if (t >= n_live) return;
-    const int64_t cgg = t / n_tiles;
     __shared__ ExpandLds sm;
+    int half;
+    const int64_t t = expand_place(a, blockIdx.x, n_tiles, half);
+    if (t < 0) return;
+    const int64_t cgg = t / n_tiles;
     expand_item<R16, BV>(a, cgg, (int)(t - cgg * n_tiles), half, a.inline_seg ? s_iperm : nullptr,
                            a.inline_seg ? s_iep : nullptr, a.inline_seg ? s_ig : nullptr, sm);
+}
+
+// The gradients' expand, and the outer products' coefficients in the first
+// n_coef8 workgroups (n_coef, rounded up to 8): neither needs the other.
+template <int R16>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
+void grad_expand(SgGradArgs b, SgmmArgs a, int64_t n_coef, int64_t n_coef8) {
+    __shared__ ExpandLds sm;
+    static_assert(sizeof(CoefLds<true>) <= sizeof(ExpandLds), "one workgroup's LDS");
+    if (rejected(b)) return;
+    if (blockIdx.x < n_coef8) {
+        if (blockIdx.x < n_coef) coefs_tile<true>(b, blockIdx.x / b.n_prob, (int)(blockIdx.x % b.n_prob), *(CoefLds<true>*)&sm);
+        return;
+    }
+    const int n_tiles = uniform(gld((const int32_t*)(a.ws + a.L.hdr) + SG_NTILES));
+    int half;
+    const int64_t t = expand_place(a, blockIdx.x - n_coef8, n_tiles, half);
+    if (t < 0) return;
+    const int64_t cgg = t / n_tiles;
+    expand_item<R16, 2>(a, cgg, (int)(t - cgg * n_tiles), half, nullptr, nullptr, nullptr, sm);
 }
 
 // ---- one launch: shrink then expand ---------------------------------------------
@@ -1699,13 +1726,11 @@ __global__ __launch_bounds__(256) void sgmm_shrink_generic(SgmmArgs a) {
 
 // y[row][o] += c0 * (v0 . B[e0][o]) + c1 * (v1 . B[e1][o]), one thread each.
 template <typename T>
-__global__ __launch_bounds__(256) void sgmm_expand_generic(SgmmArgs a) {
+__device__ __forceinline__ void expand_generic(const SgmmArgs& a, int64_t block, int prob) {
     const int32_t* hdr = (const int32_t*)(a.ws + a.L.hdr);
-    if (hdr[SG_ERR]) return;
-    const int prob = blockIdx.y;
     const SgDesc D = a.descs ? a.descs[prob] : a.single;
     const int RPAD = a.L.r_pad;
-    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t q = block * 256 + threadIdx.x;
     const int64_t n_pos = hdr[SG_NPOS];
     if (q >= n_pos * D.d_out) return;
     const int64_t pos = q / D.d_out;
@@ -1726,6 +1751,20 @@ __global__ __launch_bounds__(256) void sgmm_expand_generic(SgmmArgs a) {
     T* y = (T*)D.y;
     const int64_t i = (int64_t)row * D.d_out + o;
     stf(y, i, ldf(y, i) + (part[0] + part[1]));
+}
+template <typename T>
+__global__ __launch_bounds__(256) void sgmm_expand_generic(SgmmArgs a) {
+    if (((const int32_t*)(a.ws + a.L.hdr))[SG_ERR]) return;
+    expand_generic<T>(a, blockIdx.x, blockIdx.y);
+}
+
+// fp32: the gradients' coefficients (the first n_coef workgroups of a grid row per
+// projection) and their expand.
+__global__ __launch_bounds__(256) void grad_expand_f32(SgGradArgs b, SgmmArgs a, int64_t n_coef) {
+    __shared__ CoefLds<false> sm;
+    if (rejected(b)) return;
+    if (blockIdx.x < n_coef) coefs_tile<false>(b, blockIdx.x, blockIdx.y, sm);
+    else if ((int)blockIdx.y < a.n_prob) expand_generic<float>(a, blockIdx.x - n_coef, blockIdx.y);
 }
 
 // ---- K-slice sum ---------------------------------------------------------------
@@ -1780,6 +1819,11 @@ __global__ __launch_bounds__(256) void sgmm_pack_a_kernel(const uint16_t* __rest
 // Grid for at most max_items work items (a multiple of 8: one share per XCD).
 inline int64_t item_grid(int64_t max_items) { return 8 * ((max_items + 7) / 8); }
 
+int64_t expand_blocks(const SgmmArgs& a) {
+    const int64_t per_max = (a.n_expand_units + 7) / 8;
+    return 8 * (per_max + (per_max < kExpandSplit ? per_max : kExpandSplit));
+}
+
 hipError_t launch_vsum(const SgmmArgs& a, hipStream_t s) {
     const dim3 gs((unsigned)((a.L.T_pad * 2 * a.L.r_pad / 4 + 255) / 256), (unsigned)a.n_prob);
     hipLaunchKernelGGL(sgmm_vsum_kernel, gs, dim3(256), 0, s, a);
@@ -1802,11 +1846,8 @@ hipError_t launch_shrink(const SgmmArgs& a, hipStream_t s) {
 
 template <int R16>
 hipError_t launch_expand(const SgmmArgs& a, hipStream_t s) {
-    const int64_t per_max = (a.n_expand_units + 7) / 8;
-    const dim3 ge((unsigned)(8 * (per_max + (per_max < kExpandSplit ? per_max : kExpandSplit))));
-    if (a.packed_b)
-        hipLaunchKernelGGL((sgmm_expand_bf16<R16, 2>), ge, dim3(256), 0, s, a);
-    else if (a.r % 8 == 0)
+    const dim3 ge((unsigned)expand_blocks(a));
+    if (a.r % 8 == 0)
         hipLaunchKernelGGL((sgmm_expand_bf16<R16, 1>), ge, dim3(256), 0, s, a);
     else
         hipLaunchKernelGGL((sgmm_expand_bf16<R16, 0>), ge, dim3(256), 0, s, a);
@@ -1836,24 +1877,22 @@ hipError_t launch_fused_r(const SgmmArgs& a, hipStream_t s) {
     }
 }
 
-// The MFMA launches for the workspace's padded rank: the shrink, the expand or both.
+// The MFMA launches for the workspace's padded rank: the shrink, and the expand if asked.
 template <int R16>
-hipError_t launch_mfma(const SgmmArgs& a, bool shrink, bool expand, hipStream_t s) {
-    hipError_t e = hipSuccess;
-    if (shrink) e = launch_shrink<R16>(a, s);
-    if (expand && e == hipSuccess) e = launch_expand<R16>(a, s);
-    return e;
+hipError_t launch_mfma(const SgmmArgs& a, bool expand, hipStream_t s) {
+    const hipError_t e = launch_shrink<R16>(a, s);
+    return expand && e == hipSuccess ? launch_expand<R16>(a, s) : e;
 }
-hipError_t launch_mfma_r(const SgmmArgs& a, hipStream_t s, bool shrink = true, bool expand = true) {
+hipError_t launch_mfma_r(const SgmmArgs& a, hipStream_t s, bool expand = true) {
     switch (a.L.r_pad / 16) {
-        case 1: return launch_mfma<1>(a, shrink, expand, s);
-        case 2: return launch_mfma<2>(a, shrink, expand, s);
-        case 3: return launch_mfma<3>(a, shrink, expand, s);
-        case 4: return launch_mfma<4>(a, shrink, expand, s);
-        case 5: return launch_mfma<5>(a, shrink, expand, s);
-        case 6: return launch_mfma<6>(a, shrink, expand, s);
-        case 7: return launch_mfma<7>(a, shrink, expand, s);
-        case 8: return launch_mfma<8>(a, shrink, expand, s);
+        case 1: return launch_mfma<1>(a, expand, s);
+        case 2: return launch_mfma<2>(a, expand, s);
+        case 3: return launch_mfma<3>(a, expand, s);
+        case 4: return launch_mfma<4>(a, expand, s);
+        case 5: return launch_mfma<5>(a, expand, s);
+        case 6: return launch_mfma<6>(a, expand, s);
+        case 7: return launch_mfma<7>(a, expand, s);
+        case 8: return launch_mfma<8>(a, expand, s);
         default: return hipErrorInvalidValue;
     }
 }
@@ -1899,10 +1938,9 @@ hipError_t launch_sgmm_pack_a(const void* A, void* Ap, int E, int r, int64_t d_i
 static bool sgmm_grids_fit(const SgmmArgs& a, int dtype) {
     if (!grid_fits(a.L.n_chunks, kSegThreads)) return false;
     if (dtype == 1) {
-        const int64_t per_max = (a.n_expand_units + 7) / 8;
         return grid_fits((a.L.T_pad * 2 * a.L.r_pad / 4 + 255) / 256, 256) &&
                grid_fits(item_grid(a.total_ks * a.L.tiles_max), 256) && grid_fits(8 * fused_per_xcd(a), 256) &&
-               grid_fits(8 * (per_max + (per_max < kExpandSplit ? per_max : kExpandSplit)), 256);
+               grid_fits(expand_blocks(a), 256);
     }
     return grid_fits((a.L.T_pad * 2 * a.r + 255) / 256, 256) &&
            grid_fits((a.L.T_pad * a.d_out_max + 255) / 256, 256);
@@ -1963,12 +2001,36 @@ hipError_t launch_grad_prep(const SgGradArgs& a, const float* g, int dtype, hipS
     else hipLaunchKernelGGL(grad_prep<false>, n, dim3(kSegThreads), 0, s, a, g, n_chunks);
     return hipGetLastError();
 }
-hipError_t launch_sgmm_shrink(const SgmmArgs& a, hipStream_t s) { return launch_mfma_r(a, s, true, false); }
+hipError_t launch_sgmm_shrink(const SgmmArgs& a, hipStream_t s) { return launch_mfma_r(a, s, false); }
 hipError_t launch_sgmm_vsum(const SgmmArgs& a, hipStream_t s) {
     return a.L.r_pad > kSgmmFoldRank && a.total_ks > a.n_prob ? launch_vsum(a, s) : hipSuccess;
 }
-hipError_t launch_sgmm_expand(const SgmmArgs& a, int dtype, hipStream_t s) {
-    return dtype == 1 ? launch_mfma_r(a, s, false, true) : launch_expand_generic(a, s);
+bool grad_expand_fits(const SgGradArgs& b, const SgmmArgs& a, int dtype) {
+    const int64_t tiles = b.G.cap / kGradTile;
+    return dtype == 1 ? grid_fits(tiles * b.n_prob + 8 + expand_blocks(a), 256)
+                      : grid_fits(tiles + (a.L.T_pad * a.d_out_max + 255) / 256, 256);
+}
+hipError_t launch_grad_expand(const SgGradArgs& b, const SgmmArgs& a, bool coefs, int dtype, hipStream_t s) {
+    const int64_t tiles = coefs ? b.G.cap / kGradTile : 0;
+    if (dtype == 0) {
+        const dim3 g((unsigned)(tiles + (a.L.T_pad * a.d_out_max + 255) / 256), (unsigned)(coefs ? b.n_prob : a.n_prob));
+        hipLaunchKernelGGL(grad_expand_f32, g, dim3(256), 0, s, b, a, tiles);
+        return hipGetLastError();
+    }
+    const int64_t n = tiles * b.n_prob, n8 = (n + 7) / 8 * 8;
+    const dim3 g((unsigned)(n8 + expand_blocks(a)));
+    switch (a.L.r_pad / 16) {
+        case 1: hipLaunchKernelGGL(grad_expand<1>, g, dim3(256), 0, s, b, a, n, n8); break;
+        case 2: hipLaunchKernelGGL(grad_expand<2>, g, dim3(256), 0, s, b, a, n, n8); break;
+        case 3: hipLaunchKernelGGL(grad_expand<3>, g, dim3(256), 0, s, b, a, n, n8); break;
+        case 4: hipLaunchKernelGGL(grad_expand<4>, g, dim3(256), 0, s, b, a, n, n8); break;
+        case 5: hipLaunchKernelGGL(grad_expand<5>, g, dim3(256), 0, s, b, a, n, n8); break;
+        case 6: hipLaunchKernelGGL(grad_expand<6>, g, dim3(256), 0, s, b, a, n, n8); break;
+        case 7: hipLaunchKernelGGL(grad_expand<7>, g, dim3(256), 0, s, b, a, n, n8); break;
+        case 8: hipLaunchKernelGGL(grad_expand<8>, g, dim3(256), 0, s, b, a, n, n8); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
 }
 bool sgmm_launches_fit(const SgmmArgs& a, int dtype) { return sgmm_grids_fit(a, dtype); }
 

@@ -107,7 +107,6 @@ struct SgmmArgs {
     int32_t* status_out;   // device word that also receives the set-validity flag, or nullptr
     int32_t inline_seg;    // 1: the shrink and expand order the rows themselves (launch_sgmm sets it)
     int32_t w_max;         // largest K slices + column groups of one problem
-    int32_t packed_b;      // 1: the expand reads every problem's B packed, [E][rank chunk of 16][d_out][16] (bf16)
     int32_t kslice;        // K slice width of the shrink (the owners' n_ks goes by it)
 };
 
@@ -116,11 +115,9 @@ hipError_t launch_sgmm(const SgmmArgs& a, int dtype, hipStream_t s);
 hipError_t launch_sgmm_pack_a(const void* A, void* Ap, int E, int r, int64_t d_in, hipStream_t s);
 
 // The shrink of every problem of a segmented batch (bf16; with its K-slice sum
-// above kSgmmFoldRank), and the expand of a set of problems whose v (ks0, n_ks)
-// a shrink has left in the workspace: the gradients run other work between them.
+// above kSgmmFoldRank).
 hipError_t launch_sgmm_shrink(const SgmmArgs& a, hipStream_t s);
 hipError_t launch_sgmm_vsum(const SgmmArgs& a, hipStream_t s);  // the K-slice sum alone
-hipError_t launch_sgmm_expand(const SgmmArgs& a, int dtype, hipStream_t s);
 bool sgmm_launches_fit(const SgmmArgs& a, int dtype);
 
 // ---- gradients ----------------------------------------------------------------
@@ -216,6 +213,12 @@ hipError_t launch_grad_prep(const SgGradArgs& a, const float* g, int dtype, hipS
 // u and w over the experts' slot lists (bf16).
 hipError_t launch_grad_shrink(const SgGradArgs& a, hipStream_t s);
 hipError_t launch_grad_shrink_f32(const SgGradArgs& a, hipStream_t s);
+// The expand of a set of problems whose v (ks0, n_ks) the shrink has left in the
+// workspace and whose B is packed as SgGrad::At, with the coefficients of all
+// projections in the same launch if asked.
+bool grad_expand_fits(const SgGradArgs& b, const SgmmArgs& a, int dtype);
+hipError_t launch_grad_expand(const SgGradArgs& b, const SgmmArgs& a, bool coefs, int dtype, hipStream_t s);
+// The coefficients alone.
 hipError_t launch_grad_coefs(const SgGradArgs& a, int dtype, hipStream_t s);
 // dA, dB and dg.
 hipError_t launch_grad_outer(const SgGradArgs& a, int dtype, hipStream_t s);
