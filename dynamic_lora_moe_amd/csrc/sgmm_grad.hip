@@ -44,6 +44,8 @@
 // all 8 experts of rank 16 in a workgroup's registers, was tried: half the bytes
 // at a third of the bytes in flight, 235 us against 190 for a layer's seven
 // projections at 4096 rows.)
+#include <algorithm>
+
 #include "gfx950.hpp"
 #include "internal.hpp"
 #include "sgmm.hpp"
@@ -73,7 +75,7 @@ SgGradLayout sgmm_grad_layout(int64_t T, int64_t total_ks, int E, int r, int n_p
     G.L = sgmm_layout(T, 1, E, r, (int)total_ks);  // one slice each of total_ks problems
     G.cap = (2 * T + (int64_t)E * (kGradTile - 1) + kGradTile - 1) / kGradTile * kGradTile;
     const int64_t tiles = G.cap / kGradTile, units = (int64_t)n_units * rank_chunks(G.L);
-    const int64_t least = 8 * outer_r16(G.L), even = (units * tiles + kTargetItems - 1) / kTargetItems;
+    const int64_t least = 8 * outer_r16(G.L), even = std::min((units * tiles + kTargetItems - 1) / kTargetItems, tiles);
     G.chunk_tiles = (int)(even > least ? even : least);
     // full chunks (by bounds that do not fall as T grows) and one more per expert
     const int64_t by_tiles = tiles / least, by_items = kTargetItems / units;

@@ -213,6 +213,46 @@ def test_infinities_stay_with_their_expert():
     assert not fin[17] and fin[torch.arange(100) != 17].all()
 
 
+@pytest.mark.parametrize("T,E,r,dup", [(1, 2, 64, 0.0), (5, 32, 40, 1.0), (129, 2, 64, 0.5), (700, 2, 48, 0.0),
+                                       (700, 32, 64, 1.0), (1300, 6, 128, 0.2), (1300, 16, 33, 0.0), (9000, 3, 64, 0.0)])
+def test_ranks_above_32(T, E, r, dup):
+    """Sums over the experts' slot lists: groups of slots that end inside one, a single slot, one expert twice in a row."""
+    print(T, E, r, flush=True)
+    c = Case(T, [(200, 136), (72, 2056)] if T < 2000 else [(72, 136)], E, r, BF, seed=T + r, dup=dup).bind()
+    c.run()
+    c.check()
+
+
+def test_rows_without_experts_at_rank_64():
+    c = Case(40, [(64, 72)], 4, 64, BF)
+    c.idx[:] = -1
+    c.bind()
+    c.run()
+    c.check()
+    assert (c.dA[0] == 0).all() and (c.dB[0] == 0).all() and (c.dg == 0).all()
+
+
+@pytest.mark.parametrize("i", [64, 72])
+def test_infinities_stay_with_their_row_and_rank(i):
+    """Rank 64, widths that end inside a step: one row's infinite x, and one infinity at the end of a bank's row."""
+    c = Case(100, [(i, i)], 8, 64, BF, empty=0.0, both=0.0).bind()
+    e = set(c.idx[17].tolist())
+    c.dev[0][0][17, i - 1] = float("inf")
+    c.run()
+    fin = torch.isfinite(c.dg).all(1).cpu()
+    assert not fin[17] and fin[torch.arange(100) != 17].all()
+    for k in range(8):
+        assert torch.isfinite(c.dA[0][k]).all() == (k not in e)
+        assert torch.isfinite(c.dB[0][k]).all() == (k not in e)
+    c = Case(100, [(i, i)], 8, 64, BF, empty=0.0, both=0.0).bind()
+    c.dev[0][1][3, 5, i - 1] = float("inf")  # A of expert 3, rank 5: only that rank's u, so only dB[3][:, 5]
+    c.run()
+    assert torch.isfinite(c.dA[0]).all()
+    want = torch.ones((8, 64), dtype=torch.bool)
+    want[3, 5] = False
+    assert torch.equal(torch.isfinite(c.dB[0]).all(1).cpu(), want)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_accumulate(dtype):
     c = Case(90, [(72, 136), (64, 64)], 5, 12, dtype).bind()
