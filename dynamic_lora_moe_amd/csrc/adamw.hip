@@ -34,7 +34,7 @@
 // Measured: 322 million bf16 weights with fp32 masters and moments in 448 tensors,
 // 1.69 ms, 5.7 TB/s (a large copy reaches 4.7); one layer's 10 million 54 us; with
 // 8-bit moments 47 us, where the binary64 codes and hashes bound it as much as the
-// memory; 82 million fp32 weights with 8-bit moments 317 us, 4.0 TB/s.
+// memory; 80 million fp32 weights with 8-bit moments 317 us, 4.0 TB/s.
 //
 // An element whose new v is not finite in fp32 (a gradient that is infinite,
 // NaN, or past 1.8e19) is left as it was, with 8-bit moments its whole block,

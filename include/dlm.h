@@ -3,7 +3,7 @@
  * dynamic LoRA adapters (AdaFuse: "Accelerating Dynamic Adapter Inference via
  * Token-Level Pre-Gating and Fused Kernel Optimization").
  *
- * Three operations:
+ * Three operations, and below them what trains their adapters:
  *   dlm_pregate  one top-2 routing decision per token, made once and reused by
  *                every adapted layer (AdaFuse digest, section 2-ga "token-level
  *                pre-gating"; English abstract, "decide-once, apply-everywhere").
@@ -16,6 +16,12 @@
  *                y += sum_k g_k (x A_k^T) B_k^T, segmenting rows by their set
  *                (digest section 2-na names the SGMM, "segmented gather matrix
  *                multiplication", kernel).
+ *   dlm_route    routing from logits (top k of up to 512 experts, biased, in
+ *                groups) and dlm_route_backward, the gradient of its weights;
+ *   dlm_sgmm_group_backward  the gradients of the grouped SGMM: its inputs',
+ *                its banks' and its gates';
+ *   dlm_adamw_*  AdamW over many tensors in one launch, with fp32 or 8-bit
+ *                moments.
  *
  * Conventions (all calls):
  *   - Pointers are DEVICE pointers unless marked (host).  The caller owns every
@@ -444,16 +450,18 @@ int dlm_sgmm_group_bind_grads(dlm_sgmm_group* h, const void* const* dy, void* co
  *   dg[t][k] = s sum_problems u . w   ([T][2] fp32 or NULL; 0 for an empty slot)
  *   dA_e = s sum g w x[t]^T,  dB_e = s sum g dy[t] u^T   (over the slots with e;
  *          written whole, 0 for an expert no row chose, or with accumulate != 0 added to)
- * bf16: bf16 operands, fp32 sums; s g u and s g w enter as two bf16 terms.
- * Reads the banks as they are (nothing is packed ahead).  Every result is
- * bitwise reproducible.  A set the forward call would reject leaves all of
+ * bf16: bf16 operands, fp32 sums; s g u and s g w enter dA and dB as three bf16
+ * terms (24 bits), s g w enters dx as two.  An infinity among them becomes NaN.
+ * Reads the banks as they are, and refreshes the packed A copies that the
+ * forward call reads on the way.  Every result is bitwise reproducible.  A set the forward call would reject leaves all of
  * them unchanged and sets the workspace status word (dlm_sgmm_status).  T = 0
  * writes zeros to dA and dB unless accumulate, and looks at nothing else.
  * workspace: >= dlm_sgmm_group_backward_workspace_size(h, T) bytes (asked once
- * the buffers are bound; it serves any smaller T too), 256-byte aligned.  No allocation.  Launches: segmentation with the banks'
- * transposes, shrink, coefficients, expand, outer products, and the sum of their
- * parts with dg; one more each for T > 8192, for the K-slice sum above rank 64,
- * and for every further problem that shares the same dx.
+ * the buffers are bound; it serves any smaller T too), 256-byte aligned.  No
+ * allocation.  Launches: segmentation with the banks' transposes, shrink, expand
+ * (with the outer products' coefficients), outer products, and for bf16 the sum of
+ * their parts with dg; one more each for T > 8192, for the K-slice sum above rank
+ * 64, and for every further problem that shares the same dx.
  */
 int dlm_sgmm_group_backward_workspace_size(const dlm_sgmm_group* h, int64_t T, size_t* bytes);
 int dlm_sgmm_group_backward(dlm_sgmm_group* h, const int32_t* idx, const float* g, float* dg, int64_t T,
