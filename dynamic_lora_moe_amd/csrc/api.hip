@@ -325,6 +325,7 @@ int dlm_route(const void* logits, int64_t ld, const float* bias, int64_t T, int3
     Span p, q;
     if (pair_conflict(v, &p, &q)) return conflict_fail("route", p, q);
     a.bias = bias;
+    a.vec_bias = bias && aligned16(bias) && E % 4 == 0;
     a.scores_order = bias || (a.n_groups > 1 && a.group_top == 2) ? 1 : 0;
     a.need_scores = a.scores_order || (a.score == kRouteSoftmax && !a.renorm) ? 1 : 0;
     a.idx = idx;

@@ -134,8 +134,8 @@ template <int N, int STEP> __device__ __forceinline__ void merge_peer(double* a)
     for (int i = 0; i < N; ++i) b[i] = peer<STEP>(a[i]);
     merge_top<N>(a, b);
 }
-// The largest D keys of a token, descending, in key[0 .. D) of each of its lanes.
-template <int L, int V, int D> __device__ __forceinline__ void top_keys(double (&key)[V]) {
+// A lane's largest D keys, descending, in key[0 .. D).
+template <int V, int D> __device__ __forceinline__ void lane_keys(double (&key)[V]) {
 #pragma unroll
     for (int i = 0; i < V; i += D) sort_descending<D>(key + i);
 #pragma unroll
@@ -145,6 +145,9 @@ template <int L, int V, int D> __device__ __forceinline__ void top_keys(double (
         for (int j = 0; j < D; ++j) b[j] = key[i + j];
         merge_top<D>(key, b);
     }
+}
+// From those, the token's in each of its lanes.
+template <int L, int V, int D> __device__ __forceinline__ void row_keys(double (&key)[V]) {
     if constexpr (L > 1) merge_peer<D, 1>(key);
     if constexpr (L > 2) merge_peer<D, 2>(key);
     if constexpr (L > 4) merge_peer<D, 4>(key);
@@ -267,13 +270,14 @@ __device__ __forceinline__ double weight_of(bool soft, float l, double mx, doubl
 }
 
 // Lane `lane` of a token's L lanes holds experts W * (L * c + lane) + j of its
-// 16-byte chunks c: a chunk of the L lanes is one contiguous run.
-template <typename T, int L> __device__ __forceinline__ int expert_of(int v, int lane) {
+// 16-byte chunks c: a chunk of the L lanes is one contiguous run.  RUN: V
+// neighbouring experts, so that a group of V or more is a run of whole lanes.
+template <typename T, int L, int V, bool RUN = false> __device__ __forceinline__ int expert_of(int v, int lane) {
     constexpr int W = 16 / (int)sizeof(T);
-    return (v / W) * (W * L) + lane * W + v % W;
+    return RUN ? lane * V + v : (v / W) * (W * L) + lane * W + v % W;
 }
 
-template <typename T, int L, int V>
+template <typename T, int L, int V, bool RUN = false>
 __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int lane, bool live, bool vec, float (&l)[V]) {
     constexpr int W = 16 / (int)sizeof(T);
     static_assert(V % W == 0, "whole chunks");
@@ -281,12 +285,12 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
         u32x4 c[V / W];
 #pragma unroll
         for (int i = 0; i < V / W; ++i) {
-            const int e = expert_of<T, L>(i * W, lane);
+            const int e = expert_of<T, L, V, RUN>(i * W, lane);
             c[i] = live && e < E ? ld128(row + e) : u32x4{0u, 0u, 0u, 0u};
         }
 #pragma unroll
         for (int i = 0; i < V / W; ++i) {
-            const bool in = live && expert_of<T, L>(i * W, lane) < E;
+            const bool in = live && expert_of<T, L, V, RUN>(i * W, lane) < E;
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 float f;
@@ -298,7 +302,7 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
     } else {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = expert_of<T, L>(v, lane);
+            const int e = expert_of<T, L, V, RUN>(v, lane);
             l[v] = live && e < E ? clean(logit_of<T>(gld(row + e))) : -__builtin_huge_valf();
         }
     }
@@ -306,7 +310,7 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
 
 // One workgroup: NT / L tokens.  Dynamic LDS: the chosen experts [tokens][k]
 // and their scores, then (with groups) keys, group keys and the kept flags.
-template <typename T, int L, int V, int NT, int SCORE>
+template <typename T, int L, int V, int NT, int SCORE, bool RUN>
 __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
     constexpr int TPB = NT / L, W = 16 / (int)sizeof(T);
     extern __shared__ char smem[];
@@ -320,7 +324,7 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
 
     const T* row = (const T*)a.logits + (live ? t : 0) * a.ld;
     float l[V];
-    load_row<T, L, V>(row, E, lane, live, a.vec, l);
+    load_row<T, L, V, RUN>(row, E, lane, live, a.vec, l);
 
     // softmax: the largest logit (0 for a row with none), and with it the
     // denominator where the weights or the keys need it
@@ -346,10 +350,18 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
         }
         if (a.scores_order) {
             float bias[V] = {};
-            if (a.bias) {
+            if (RUN && a.vec_bias) {
+#pragma unroll
+                for (int v = 0; v < V; v += 4) {
+                    const int e = expert_of<T, L, V, RUN>(v, lane);
+                    const u32x4 q = ld128(a.bias + (e < E ? e : 0));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) bias[v + j] = __uint_as_float(q[j]);
+                }
+            } else if (a.bias) {
 #pragma unroll
                 for (int c = 0; c < V / W; ++c) {
-                    const int e0 = expert_of<T, L>(c * W, lane);
+                    const int e0 = expert_of<T, L, V, RUN>(c * W, lane);
 #pragma unroll
                     for (int j = 0; j < W; ++j)
                         if (a.vec ? e0 < E : e0 + j < E) bias[c * W + j] = gld(a.bias + e0 + j);
@@ -358,19 +370,19 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const double s = SCORE == kRouteSoftmax ? key[v] * inv : sigmoid(l[v]);
-                key[v] = with_index(s + (double)bias[v], expert_of<T, L>(v, lane), l[v] > -__builtin_huge_valf());
+                key[v] = with_index(s + (double)bias[v], expert_of<T, L, V, RUN>(v, lane), l[v] > -__builtin_huge_valf());
             }
         }
     }
     if (!a.scores_order) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = with_index((double)l[v] + 0.0, expert_of<T, L>(v, lane));  // -0 -> +0
+        for (int v = 0; v < V; ++v) key[v] = with_index((double)l[v] + 0.0, expert_of<T, L, V, RUN>(v, lane));  // -0 -> +0
     }
 
     if (a.counts) {
         for (int e = tid; e < E; e += NT) s_cnt[e] = 0;
     }
-    if (G > 1 && a.group_lanes) {
+    if (!RUN && G > 1 && a.group_lanes) {
         // a group is group_lanes neighbouring lanes' part of one chunk: its best two
         // keys by merging sorted pairs over those lanes
         constexpr int C = V / W;
@@ -405,14 +417,14 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (above[v / W] >= a.keep_groups) key[v] = kNone;
-    } else if (G > 1) {
+    } else if (!RUN && G > 1) {
         const int S = G * (gs + 1);  // a token's keys, a gap behind each group (LDS banks)
         double* s_key = (double*)(smem + a.lds_groups);
         double* s_gk = s_key + TPB * S;
         uint8_t* s_keep = (uint8_t*)(s_gk + TPB * G);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = expert_of<T, L>(v, lane);
+            const int e = expert_of<T, L, V, RUN>(v, lane);
             if (e < E) s_key[tl * S + e + (int)(((uint32_t)e * a.gs_magic) >> 20)] = key[v];
         }
         __syncthreads();
@@ -438,7 +450,7 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
         __syncthreads();
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = expert_of<T, L>(v, lane);
+            const int e = expert_of<T, L, V, RUN>(v, lane);
             const int gi = (int)(((uint32_t)e * a.gs_magic) >> 20);
             if (e < E && !s_keep[tl * G + gi]) key[v] = kNone;
         }
@@ -447,7 +459,23 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
     // the k largest keys: lists of 4, 8 or 16 merged
     auto choose = [&](auto depth) {
         constexpr int D = decltype(depth)::value;
-        top_keys<L, V, D>(key);
+        lane_keys<V, D>(key);
+        if constexpr (RUN) {
+            // a group is group_lanes lanes, whose lists begin with their best two
+            double b1 = key[0], b2 = key[1];
+            const int gl = a.group_lanes;
+            if (L > 1 && gl > 1) merge_pair<1>(b1, b2);
+            if (L > 2 && gl > 2) merge_pair<2>(b1, b2);
+            if (L > 4 && gl > 4) merge_pair<4>(b1, b2);
+            if (L > 8 && gl > 8) merge_pair<8>(b1, b2);
+            const double gk = group_key(b1, b2, a.group_top, lane / gl);
+            int above = 0;
+            for (int o = gl; o < L; o += gl) above += __shfl_xor(gk, o, kWave) > gk ? 1 : 0;
+#pragma unroll
+            for (int q = 0; q < D; ++q)
+                if (above >= a.keep_groups) key[q] = kNone;
+        }
+        row_keys<L, V, D>(key);
 #pragma unroll
         for (int q = 0; q < D; ++q)
             if (q < k && lane == q % L) s_idx[tl * k + q] = key[q] > kNone ? index_of(key[q]) : -1;
@@ -593,7 +621,7 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteArgs a) {
     constexpr int W = 16 / (int)sizeof(T);
 #pragma unroll
     for (int c = 0; c < V / W; ++c) {
-        const int e0 = expert_of<T, L>(c * W, lane);
+        const int e0 = expert_of<T, L, V>(c * W, lane);
         float r[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) {
@@ -639,18 +667,31 @@ hipError_t launch_one(RouteArgs a, bool grad, hipStream_t s) {
         hipLaunchKernelGGL((route_grad_kernel<T, L, V, NT>), dim3((unsigned)blocks), dim3(NT), lds, s, a);
     } else {
         size_t lds = (size_t)TPB * a.k * 12 + (a.counts ? (size_t)a.E * 4 : 0);
-        // groups that are whole runs of 2^i lanes of a chunk need no LDS
+        const dim3 g((unsigned)blocks), n(NT);
+        auto is_run = [](int lanes) { return lanes > 0 && (lanes & (lanes - 1)) == 0 && lanes <= L; };
+        if constexpr (L > 1) {
+            // groups that are whole runs of 2^i lanes: V neighbouring experts a lane
+            if (a.n_groups > 1 && a.group_size % V == 0 && is_run(a.group_size / V)) {
+                a.group_lanes = a.group_size / V;
+                if (a.score == kRouteSoftmax)
+                    hipLaunchKernelGGL((route_kernel<T, L, V, NT, kRouteSoftmax, true>), g, n, lds, s, a);
+                else
+                    hipLaunchKernelGGL((route_kernel<T, L, V, NT, kRouteSigmoid, true>), g, n, lds, s, a);
+                return hipGetLastError();
+            }
+        }
+        // smaller ones that are whole runs of 2^i lanes of a chunk need no LDS either
         constexpr int W = 16 / (int)sizeof(T);
-        const int gl = a.group_size / W;
-        a.group_lanes = a.n_groups > 1 && a.group_size % W == 0 && (gl & (gl - 1)) == 0 && gl <= L ? gl : 0;
+        a.group_lanes = a.n_groups > 1 && a.group_size % W == 0 && is_run(a.group_size / W) ? a.group_size / W : 0;
         if (a.n_groups > 1 && !a.group_lanes) {
             lds = (lds + 15) & ~(size_t)15;
             a.lds_groups = (int)lds;
             lds += (size_t)TPB * (a.n_groups * (a.group_size + 1) * 8 + a.n_groups * 9);
         }
-        const dim3 g((unsigned)blocks), n(NT);
-        if (a.score == kRouteSoftmax) hipLaunchKernelGGL((route_kernel<T, L, V, NT, kRouteSoftmax>), g, n, lds, s, a);
-        else hipLaunchKernelGGL((route_kernel<T, L, V, NT, kRouteSigmoid>), g, n, lds, s, a);
+        if (a.score == kRouteSoftmax)
+            hipLaunchKernelGGL((route_kernel<T, L, V, NT, kRouteSoftmax, false>), g, n, lds, s, a);
+        else
+            hipLaunchKernelGGL((route_kernel<T, L, V, NT, kRouteSigmoid, false>), g, n, lds, s, a);
     }
     return hipGetLastError();
 }

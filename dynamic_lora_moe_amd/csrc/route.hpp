@@ -21,6 +21,7 @@ struct RouteArgs {
     int32_t n_groups, group_size, keep_groups, group_top;
     uint32_t gs_magic;     // e / group_size = (e * gs_magic) >> 20 for e < 512
     int32_t vec, vec_out;  // rows of logits / dlogits take 16-byte accesses
+    int32_t vec_bias;      // so does the bias, and E is a multiple of 4
     int32_t need_scores;   // every expert's score is needed, not only the chosen ones'
     int32_t scores_order;  // keys are scores plus bias; else the logits order the experts
     int32_t group_lanes;   // lanes a group spans when groups are whole runs of them, else 0 (the launcher sets it)

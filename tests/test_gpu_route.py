@@ -83,6 +83,29 @@ def test_groups(E, groups, keep, top, score, biased):
     _check(l, dev, k, bias=bias, score=score, n_groups=groups, keep_groups=keep, group_top=top, scale=2.5)
 
 
+@pytest.mark.parametrize("E,groups,keep,top", [(512, 4, 2, 2), (512, 32, 7, 2), (128, 8, 3, 1), (48, 3, 2, 2), (96, 2, 1, 2),
+                                               (32, 2, 1, 1), (320, 20, 6, 2), (192, 3, 2, 2)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("k", [3, 8, 13])
+def test_groups_of_whole_lanes(E, groups, keep, top, dtype, k):
+    """Groups of 16 experts and more, whose lanes' lists rank them; the bias at an odd address."""
+    l, dev = _logits(70, E, dtype, E + groups + k)
+    l[3, : E // groups] = -float("inf")
+    l[4] = -float("inf")
+    dev.copy_(l)
+    k = min(keep * (E // groups), k)
+    bias = torch.randn(E, generator=torch.Generator().manual_seed(k)) * 0.3
+    for b in (None, bias):
+        for score in ("softmax", "sigmoid"):
+            _check(l, dev, k, bias=b, score=score, n_groups=groups, keep_groups=keep, group_top=top, scale=2.5)
+    odd = torch.zeros(E + 1).cuda()
+    odd[1:] = bias
+    kw = dict(score="sigmoid", n_groups=groups, keep_groups=keep, group_top=top)
+    i1, g1 = dlm.route(dev, k, bias=odd[1:], **kw)
+    i2, g2 = dlm.route(dev, k, bias=bias.cuda(), **kw)
+    assert torch.equal(i1, i2) and torch.equal(g1, g2)
+
+
 @pytest.mark.parametrize("masked", [0.3, 0.9, 1.0])
 @pytest.mark.parametrize("E,groups,keep", [(8, 1, 1), (60, 4, 2), (256, 8, 2)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
