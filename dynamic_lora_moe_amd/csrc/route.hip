@@ -27,9 +27,12 @@
 //
 // Measured: 64 tokens of 8 experts, top 2: 2.8 us.  4099 tokens of 60 experts, bf16,
 // softmax, top 6: 6.6 us, the gradient 8.8 (few workgroups: latency).  32768 tokens
-// of 256 experts, fp32, sigmoid with bias, 4 of 8 groups, top 8: 30 us, 1.2 TB/s,
-// four times what reading the logits takes; 16384 of them in bf16 19 us and their
-// gradient, which needs the sigmoid of the chosen only, 7.8 us (2.2 TB/s).
+// of 256 experts, fp32, sigmoid with bias, 4 of 8 groups, top 8: 26 us, 1.4 TB/s,
+// three and a half times what reading the logits takes (softmax without bias and
+// groups: 16 us); 16384 of them in bf16 16 us and their gradient, which needs the
+// sigmoid of the chosen only, 7.8 us (2.2 TB/s).  The former on 8 lanes with 32
+// experts each, which merges less across lanes: 28 us, and 4096 rows without groups
+// 6.9 against 5.7, as fewer waves hide less.
 #include <type_traits>
 
 #include "gfx950.hpp"
@@ -591,6 +594,11 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteArgs a) {
         sw += w;
         sdw += s_d[tl * k + j] * w;
     }
+    if (a.renorm) {
+        __syncthreads();  // the sums are read
+        for (int s = lane; s < k; s += L) s_d[tl * k + s] = sw > 0.0 ? (s_d[tl * k + s] - sdw / sw) / sw : 0.0;
+        __syncthreads();
+    }
     for (int s = lane; s < k; s += L) {
         const int e = s_idx[tl * k + s];
         bool first = e >= 0;
@@ -598,9 +606,7 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteArgs a) {
         for (int j = 0; j < k; ++j) {
             if (s_idx[tl * k + j] != e) continue;
             if (j < s) first = false;
-            double dj = s_d[tl * k + j];
-            if (a.renorm) dj = sw > 0.0 ? (dj - sdw / sw) / sw : 0.0;
-            d += dj;
+            d += s_d[tl * k + j];
         }
         if (!first) continue;
         if (!full) {
@@ -670,7 +676,9 @@ hipError_t launch_one(RouteArgs a, bool grad, hipStream_t s) {
         const dim3 g((unsigned)blocks), n(NT);
         auto is_run = [](int lanes) { return lanes > 0 && (lanes & (lanes - 1)) == 0 && lanes <= L; };
         if constexpr (L > 1) {
-            // groups that are whole runs of 2^i lanes: V neighbouring experts a lane
+            // groups that are whole runs of 2^i lanes: V neighbouring experts a lane,
+            // ranked by the heads of its sorted list (32768 rows of 256 experts in 8
+            // groups: 26 us, where ranking chunk by chunk before the sort took 31)
             if (a.n_groups > 1 && a.group_size % V == 0 && is_run(a.group_size / V)) {
                 a.group_lanes = a.group_size / V;
                 if (a.score == kRouteSoftmax)
