@@ -29,8 +29,8 @@
 // softmax, top 6: 6.6 us, the gradient 8.8 (few workgroups: latency).  32768 tokens
 // of 256 experts, fp32, sigmoid with bias, 4 of 8 groups, top 8: 26 us, 1.4 TB/s,
 // three and a half times what reading the logits takes (softmax without bias and
-// groups: 16 us); 16384 of them in bf16 16 us and their gradient, which needs the
-// sigmoid of the chosen only, 7.8 us (2.2 TB/s).  The former on 8 lanes with 32
+// groups: 16 us); 16384 of them in bf16 15 us and their gradient, which needs the
+// sigmoid of the chosen only, 7 us (2.4 TB/s).  The former on 8 lanes with 32
 // experts each, which merges less across lanes: 28 us, and 4096 rows without groups
 // 6.9 against 5.7, as fewer waves hide less.
 #include <type_traits>

@@ -438,7 +438,8 @@ int dlm_sgmm_group_run(dlm_sgmm_group* h, const int32_t* idx, const float* g, in
  *      fp32
  * bf16: all 16-byte aligned.  The handle allocates memory for the banks'
  * transposes (the banks' size); the device is synchronised first.  The buffers
- * stay owned by the caller.  Binding again replaces them.
+ * stay owned by the caller.  Binding again replaces them (calls captured into
+ * graphs before then read freed tables: capture them again).
  */
 int dlm_sgmm_group_bind_grads(dlm_sgmm_group* h, const void* const* dy, void* const* dx, float* const* dA,
                               float* const* dB);

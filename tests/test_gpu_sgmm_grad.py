@@ -340,10 +340,10 @@ def test_no_rows():
     assert (c.dA[0] == 0).all() and (c.dB[0] == 0).all() and torch.equal(c.ddx[0].cpu(), c.dx0[0])
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
-def test_same_bits_every_time_on_any_stream_and_replayed(dtype):
+@pytest.mark.parametrize("dtype,r", [(BF, 16), (F32, 16), (BF, 64), (BF, 128)])
+def test_same_bits_every_time_on_any_stream_and_replayed(dtype, r):
     """Eager, on another stream, and replayed from a graph with eager work between the replays."""
-    c = Case(500, [(256, 136), (72, 2056)], 8, 16, dtype).bind()
+    c = Case(500, [(256, 136), (72, 2056)], 8, r, dtype).bind()
     idx, g = c.idx.cuda(), c.g.cuda()
     ws = c.grp.backward_workspace(c.T)
     outs = c.ddx + c.dA + c.dB + [c.dg]
@@ -372,6 +372,19 @@ def test_same_bits_every_time_on_any_stream_and_replayed(dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_two_groups_at_once():
+    """Two handles with workspaces of their own, on two streams without an order between them."""
+    cs = [Case(900, [(264, 136), (72, 2056)], 8, r, BF, seed=r).bind() for r in (16, 64)]
+    args = [(c.idx.cuda(), c.g.cuda(), c.grp.backward_workspace(c.T)) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for (idx, g, ws), c, s in zip(args, cs, streams):
+        c.grp.backward(idx, g, c.dg, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for c in cs:
+        c.check()
 
 
 def test_reads_the_banks_as_they_are():
