@@ -31,10 +31,11 @@
 //          eight columns of eight rows and transposes the block in registers, one
 //          v_perm per two values: x and dy go from memory to the matrix cores
 //          without LDS.
-//   sum    experts with several chunks: their partial sums in chunk order; dg.
+//          Its last workgroups write dg.
+//   sum    experts with several chunks: their partial sums in chunk order.
 //
 // Measured (us)                            prep  shrink  expand  outer  sum
-//   256 rows, 4096 x 4096, 8 x rank 16        9       9       9      9    2   latency
+//   256 rows, 4096 x 4096, 8 x rank 16        9       9       9      9    -   latency
 //   4096 rows, a 7B-shaped layer, 8 x 16     21     146     147    190   23
 //   4096 rows, 8192 x 8192, 16 x rank 64     26      53      80     84   11
 // The layer's shrink reads x and dy at 4.4 TB/s, its expand reads and writes dx at
@@ -91,11 +92,18 @@ SgGradLayout sgmm_grad_layout(int64_t T, int64_t total_ks, int E, int r, int n_p
     // full chunks (by bounds that do not fall as T grows) and one more per expert
     const int64_t by_tiles = tiles / least, by_items = kTargetItems / units;
     G.max_chunks = (int)(by_tiles < by_items ? by_tiles : by_items) + E;
+    // few rows, whose longest list makes two short chunks at most: one chunk an
+    // expert, and no launch to add them (256 rows of 4096 x 4096: 39.7 us to 37.3)
+    const int64_t longest = (2 * T + kGradTile - 1) / kGradTile;
+    if (longest <= 2 * least) {
+        G.chunk_tiles = (int)std::max<int64_t>(longest, least);
+        G.max_chunks = E;
+    }
     size_t o = G.L.total;
     G.eoff = o;    o += a256((size_t)(E + 1) * 4);
     G.slot = o;    o += a256((size_t)G.cap * 4);
     G.srow = o;    o += a256((size_t)G.cap * 4);
-    G.chunk = o;   o += a256((size_t)(tiles / G.chunk_tiles + E) * sizeof(SgChunk));
+    G.chunk = o;   o += a256((size_t)(tiles / least + 2 * E + 2) * sizeof(SgChunk));
     G.echunk = o;  o += a256((size_t)(E + 1) * 4);
     G.coef = o;
     if (dtype == 0) o += a256((size_t)n_prob * 2 * G.cap * G.L.r_pad * 4);
@@ -350,9 +358,13 @@ __device__ __forceinline__ u32x4 column(const u32x4 (&v)[8], int j) {
 
 template <int R16>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(R16 == 1 ? 3 : 2)))
-void grad_outer_bf16(SgGradArgs a, int n_ch) {
+void grad_outer_bf16(SgGradArgs a, int n_ch, int64_t n_blocks) {
     constexpr int CPL = kCPL, kCols = kOuterCols, NR = 16 * R16;
     if (rejected(a)) return;
+    if (blockIdx.x >= n_blocks) {
+        write_dg(a, (blockIdx.x - n_blocks) * 256 + threadIdx.x);
+        return;
+    }
     // XCD b % 8 takes every eighth column block, its chunks (and rank chunks) one after another
     const int per_unit = a.G.max_chunks * n_ch;
     const int64_t jj = blockIdx.x / 8;
@@ -451,13 +463,9 @@ void grad_outer_bf16(SgGradArgs a, int n_ch) {
 
 // Four gradient elements (a quad) at a time of (unit, rank chunk, expert): the
 // expert's partial tiles added in chunk order, kSumPer quads per thread, whose
-// loads go out together.  The workgroups past the items write dg.
-__global__ __launch_bounds__(256) void grad_sum_bf16(SgGradArgs a, int n_ch, int64_t n_items, int per_item) {
+// loads go out together.
+__global__ __launch_bounds__(256) void grad_sum_bf16(SgGradArgs a, int n_ch, int per_item) {
     if (rejected(a)) return;
-    if (blockIdx.x >= n_items * per_item) {
-        write_dg(a, (blockIdx.x - n_items * per_item) * 256 + threadIdx.x);
-        return;
-    }
     const int64_t item = blockIdx.x / per_item;
     const int e = (int)(item % a.E), ch = (int)(item / a.E) % n_ch;
     const int64_t unit = item / a.E / n_ch;
@@ -594,7 +602,8 @@ int sum_blocks(const SgGradArgs& a) { return (16 * outer_r16(a.G.L) * kOuterCols
 bool sgmm_grad_fits(const SgGradArgs& a, int dtype) {
     return grad_prep_fits(a) && grid_fits(a.G.cap / kGradTile, 256) && grid_fits((a.T + 1) / 2, 256) &&
            grid_fits(a.n_units + dg_blocks(a), 256) &&
-           (dtype == 0 || (grid_fits(list_blocks(a), 256) && grid_fits(outer_blocks(a), 256) && grid_fits(sum_items(a) * sum_blocks(a) + dg_blocks(a), 256)));
+           (dtype == 0 || (grid_fits(list_blocks(a), 256) && grid_fits(outer_blocks(a) + dg_blocks(a), 256) &&
+                           grid_fits(sum_items(a) * sum_blocks(a), 256)));
 }
 
 hipError_t launch_grad_zero(const SgGradArgs& a, int dtype, hipStream_t s) {
@@ -634,18 +643,19 @@ hipError_t launch_grad_outer(const SgGradArgs& a, int dtype, hipStream_t s) {
         return hipGetLastError();
     }
     const int n_ch = rank_chunks(a.G.L);
-    const dim3 g((unsigned)outer_blocks(a));
+    const int64_t n = outer_blocks(a);
+    const dim3 g((unsigned)(n + dg_blocks(a)));
     switch (outer_r16(a.G.L)) {
-        case 1: hipLaunchKernelGGL(grad_outer_bf16<1>, g, dim3(256), 0, s, a, n_ch); break;
-        case 2: hipLaunchKernelGGL(grad_outer_bf16<2>, g, dim3(256), 0, s, a, n_ch); break;
-        case 3: hipLaunchKernelGGL(grad_outer_bf16<3>, g, dim3(256), 0, s, a, n_ch); break;
-        default: hipLaunchKernelGGL(grad_outer_bf16<4>, g, dim3(256), 0, s, a, n_ch); break;
+        case 1: hipLaunchKernelGGL(grad_outer_bf16<1>, g, dim3(256), 0, s, a, n_ch, n); break;
+        case 2: hipLaunchKernelGGL(grad_outer_bf16<2>, g, dim3(256), 0, s, a, n_ch, n); break;
+        case 3: hipLaunchKernelGGL(grad_outer_bf16<3>, g, dim3(256), 0, s, a, n_ch, n); break;
+        default: hipLaunchKernelGGL(grad_outer_bf16<4>, g, dim3(256), 0, s, a, n_ch, n); break;
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t blocks = sum_items(a) * sum_blocks(a) + dg_blocks(a);
+    const int64_t blocks = sum_items(a) * sum_blocks(a);
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL(grad_sum_bf16, dim3((unsigned)blocks), dim3(256), 0, s, a, n_ch, sum_items(a), sum_blocks(a));
+    hipLaunchKernelGGL(grad_sum_bf16, dim3((unsigned)blocks), dim3(256), 0, s, a, n_ch, sum_blocks(a));
     return hipGetLastError();
 }
 

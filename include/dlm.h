@@ -460,8 +460,8 @@ int dlm_sgmm_group_bind_grads(dlm_sgmm_group* h, const void* const* dy, void* co
  * workspace: >= dlm_sgmm_group_backward_workspace_size(h, T) bytes (asked once
  * the buffers are bound; it serves any smaller T too), 256-byte aligned.  No
  * allocation.  Launches: segmentation with the banks' transposes, shrink, expand
- * (with the outer products' coefficients), outer products, and for bf16 the sum of
- * their parts with dg; one more each for T > 8192, for the K-slice sum above rank
+ * (with the outer products' coefficients), outer products with dg, and for bf16 and
+ * more than a few hundred rows the sum of their parts; one more each for T > 8192, for the K-slice sum above rank
  * 64, and for every further problem that shares the same dx.
  */
 int dlm_sgmm_group_backward_workspace_size(const dlm_sgmm_group* h, int64_t T, size_t* bytes);
