@@ -329,6 +329,51 @@ def test_one_workspace_serves_fewer_rows(dtype):
         c.g = gate
 
 
+@pytest.mark.parametrize("r", [16, 64, 128])
+def test_a_workspace_serves_every_smaller_batch(r):
+    c = Case(8, [(2056, 264), (64, 8200)], 8, r, BF).bind()
+    sizes = [c.grp.backward_workspace(T).numel() for T in (*range(1, 600), *range(600, 20000, 97))]
+    assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("r", [16, 64])
+def test_no_dx_at_all(r):
+    """Nothing asks for dx: the coefficients are a launch of their own."""
+    c = Case(300, [(72, 136), (64, 64)], 6, r, BF).bind(dx=[None, None])
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("r", [16, 64])
+def test_tied_banks_and_shared_dx(r):
+    """Two problems of one A, B and x with one dx: every gradient buffer has its own problem's share."""
+    c = Case(200, [(64, 128), (64, 128)], 4, r, BF)
+    c.x[1], c.A[1], c.B[1] = c.x[0], c.A[0], c.B[0]
+    c.bind()
+    x, A, B, _ = c.dev[0]
+    c.dev = [(x, A, B, c.dev[0][3]), (x, A, B, c.dev[1][3])]
+    dx = c.dx0[0].cuda()
+    c.grp = dlm.SgmmGroup(c.dev, c.E, r, c.scale)
+    c.grp.bind_grads(c.ddy, [dx, dx], c.dA, c.dB)
+    c.run()
+    want, tol = c.dx0[0].double(), 0.0
+    for (o, i), (out, mag) in zip(c.shapes, c.refs()):
+        want = want + out[0]
+        tol = tol + (gamma(o + 4 * r + 8) + SPLIT) * mag[0] + 2.0 ** -8 * want.abs()
+    assert ((dx.cpu().double() - want).abs() <= tol * (1 + 3 * 2.0 ** -8)).all()
+    c.ddx = [None, None]
+    c.check()
+
+
+def test_a_rejected_set_changes_nothing_at_rank_64():
+    c = Case(300, [(64, 72)], 4, 64, BF, empty=0.0, both=0.0).bind()
+    c.idx[7, 1] = 4
+    before = [t.clone() for t in c.ddx + c.dA + c.dB + [c.dg]]
+    ws = c.run()
+    assert dlm.sgmm_status(ws) == dlm.DLM_EDEVICE
+    assert all(torch.equal(x, y) for x, y in zip(before, c.ddx + c.dA + c.dB + [c.dg]))
+
+
 def test_no_rows():
     c = Case(16, [(64, 64)], 4, 8, BF).bind()
     e = torch.empty((0, 2), device="cuda")
