@@ -1358,21 +1358,24 @@ __global__ __launch_bounds__(256) void sgmm_expand_bf16(SgmmArgs a) {
                            a.inline_seg ? s_iep : nullptr, a.inline_seg ? s_ig : nullptr, sm);
 }
 
-// The gradients' expand, and the outer products' coefficients in the first
-// n_coef8 workgroups (n_coef, rounded up to 8): neither needs the other.
+// The gradients' expand, and the outer products' coefficients in the last n_coef
+// workgroups, where they fill the expand's drain: neither needs the other.  (First,
+// they held the expand's places: up to 1% of a call more.)
 template <int R16>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
-void grad_expand(SgGradArgs b, SgmmArgs a, int64_t n_coef, int64_t n_coef8) {
+void grad_expand(SgGradArgs b, SgmmArgs a, int64_t n_coef) {
     __shared__ ExpandLds sm;
     static_assert(sizeof(CoefLds<true>) <= sizeof(ExpandLds), "one workgroup's LDS");
     if (rejected(b)) return;
-    if (blockIdx.x < n_coef8) {
-        if (blockIdx.x < n_coef) coefs_tile<true>(b, blockIdx.x / b.n_prob, (int)(blockIdx.x % b.n_prob), *(CoefLds<true>*)&sm);
+    const int64_t n_exp = gridDim.x - n_coef, bid = blockIdx.x;
+    if (bid >= n_exp) {
+        const uint32_t c = (uint32_t)(bid - n_exp), n = b.n_prob;
+        coefs_tile<true>(b, c / n, (int)(c % n), *(CoefLds<true>*)&sm);
         return;
     }
     const int n_tiles = uniform(gld((const int32_t*)(a.ws + a.L.hdr) + SG_NTILES));
     int half;
-    const int64_t t = expand_place(a, blockIdx.x - n_coef8, n_tiles, half);
+    const int64_t t = expand_place(a, bid, n_tiles, half);
     if (t < 0) return;
     const int64_t cgg = t / n_tiles;
     expand_item<R16, 2>(a, cgg, (int)(t - cgg * n_tiles), half, nullptr, nullptr, nullptr, sm);
@@ -2007,7 +2010,7 @@ hipError_t launch_sgmm_vsum(const SgmmArgs& a, hipStream_t s) {
 }
 bool grad_expand_fits(const SgGradArgs& b, const SgmmArgs& a, int dtype) {
     const int64_t tiles = b.G.cap / kGradTile;
-    return dtype == 1 ? grid_fits(tiles * b.n_prob + 8 + expand_blocks(a), 256)
+    return dtype == 1 ? grid_fits(tiles * b.n_prob + expand_blocks(a), 256)
                       : grid_fits(tiles + (a.L.T_pad * a.d_out_max + 255) / 256, 256);
 }
 hipError_t launch_grad_expand(const SgGradArgs& b, const SgmmArgs& a, bool coefs, int dtype, hipStream_t s) {
@@ -2017,17 +2020,17 @@ hipError_t launch_grad_expand(const SgGradArgs& b, const SgmmArgs& a, bool coefs
         hipLaunchKernelGGL(grad_expand_f32, g, dim3(256), 0, s, b, a, tiles);
         return hipGetLastError();
     }
-    const int64_t n = tiles * b.n_prob, n8 = (n + 7) / 8 * 8;
-    const dim3 g((unsigned)(n8 + expand_blocks(a)));
+    const int64_t n = tiles * b.n_prob;
+    const dim3 g((unsigned)(n + expand_blocks(a)));
     switch (a.L.r_pad / 16) {
-        case 1: hipLaunchKernelGGL(grad_expand<1>, g, dim3(256), 0, s, b, a, n, n8); break;
-        case 2: hipLaunchKernelGGL(grad_expand<2>, g, dim3(256), 0, s, b, a, n, n8); break;
-        case 3: hipLaunchKernelGGL(grad_expand<3>, g, dim3(256), 0, s, b, a, n, n8); break;
-        case 4: hipLaunchKernelGGL(grad_expand<4>, g, dim3(256), 0, s, b, a, n, n8); break;
-        case 5: hipLaunchKernelGGL(grad_expand<5>, g, dim3(256), 0, s, b, a, n, n8); break;
-        case 6: hipLaunchKernelGGL(grad_expand<6>, g, dim3(256), 0, s, b, a, n, n8); break;
-        case 7: hipLaunchKernelGGL(grad_expand<7>, g, dim3(256), 0, s, b, a, n, n8); break;
-        case 8: hipLaunchKernelGGL(grad_expand<8>, g, dim3(256), 0, s, b, a, n, n8); break;
+        case 1: hipLaunchKernelGGL(grad_expand<1>, g, dim3(256), 0, s, b, a, n); break;
+        case 2: hipLaunchKernelGGL(grad_expand<2>, g, dim3(256), 0, s, b, a, n); break;
+        case 3: hipLaunchKernelGGL(grad_expand<3>, g, dim3(256), 0, s, b, a, n); break;
+        case 4: hipLaunchKernelGGL(grad_expand<4>, g, dim3(256), 0, s, b, a, n); break;
+        case 5: hipLaunchKernelGGL(grad_expand<5>, g, dim3(256), 0, s, b, a, n); break;
+        case 6: hipLaunchKernelGGL(grad_expand<6>, g, dim3(256), 0, s, b, a, n); break;
+        case 7: hipLaunchKernelGGL(grad_expand<7>, g, dim3(256), 0, s, b, a, n); break;
+        case 8: hipLaunchKernelGGL(grad_expand<8>, g, dim3(256), 0, s, b, a, n); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
