@@ -26,13 +26,12 @@
 // pairwise; of two descending lists the largest are max(a[i], b[N - 1 - i]).
 //
 // Measured: 64 tokens of 8 experts, top 2: 2.8 us.  4099 tokens of 60 experts, bf16,
-// softmax, top 6: 6.6 us, the gradient 8.8 (few workgroups: latency).  32768 tokens
+// softmax, top 6: 5.2 us, the gradient 6.1 (few workgroups: latency).  32768 tokens
 // of 256 experts, fp32, sigmoid with bias, 4 of 8 groups, top 8: 26 us, 1.4 TB/s,
 // three and a half times what reading the logits takes (softmax without bias and
 // groups: 16 us); 16384 of them in bf16 15 us and their gradient, which needs the
 // sigmoid of the chosen only, 7 us (2.4 TB/s).  The former on 8 lanes with 32
-// experts each, which merges less across lanes: 28 us, and 4096 rows without groups
-// 6.9 against 5.7, as fewer waves hide less.
+// experts each, which merges less across lanes: 28 us, as fewer waves hide less.
 #include <type_traits>
 
 #include "gfx950.hpp"
@@ -485,7 +484,7 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs a) {
     };
     if (k <= 4) choose(std::integral_constant<int, 4>());
     else if (k <= 8) choose(std::integral_constant<int, 8>());
-    else choose(std::integral_constant<int, V>());
+    else if constexpr (V >= 16) choose(std::integral_constant<int, V>());  // (8 a lane: k <= 8)
     __syncthreads();
 
     // the chosen experts' scores, one slot per lane
@@ -704,14 +703,23 @@ hipError_t launch_one(RouteArgs a, bool grad, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Lanes and experts per lane by E.
+// Lanes and experts per lane by E: 16 a lane, the cheaper split, or 8 on twice the
+// lanes, whose chains are shorter, while that makes at most two waves per SIMD: 512
+// rows of 60 experts 6.0 us against 8.8 (sigmoid, bias), of 256 experts 6.5 against
+// 8.6, but 65536 of 256 58 against 53.  Lists of more than 8 need 16.  The gradients
+// of up to 64 experts always take 8, for the rows' smaller share of a workgroup's LDS:
+// 65536 rows of 60 experts 11.5 us against 16.2.
+constexpr int64_t kRouteFewLanes = 2 * 1024 * kWave;
 template <typename T> hipError_t launch_t(const RouteArgs& a, bool grad, hipStream_t s) {
+    const auto eight = [&](int lanes) {
+        return grad ? a.E <= 64 || a.T * lanes <= kRouteFewLanes : a.k <= 8 && a.T * lanes <= kRouteFewLanes;
+    };
     if (a.E <= 8) return launch_one<T, 1, 8, 64>(a, grad, s);
     if (a.E <= 16) return launch_one<T, 1, 16, 64>(a, grad, s);
-    if (a.E <= 32) return launch_one<T, 2, 16, 128>(a, grad, s);
-    if (a.E <= 64) return launch_one<T, 4, 16, 128>(a, grad, s);
-    if (a.E <= 128) return launch_one<T, 8, 16, 256>(a, grad, s);
-    if (a.E <= 256) return launch_one<T, 16, 16, 256>(a, grad, s);
+    if (a.E <= 32) return eight(4) ? launch_one<T, 4, 8, 128>(a, grad, s) : launch_one<T, 2, 16, 128>(a, grad, s);
+    if (a.E <= 64) return eight(8) ? launch_one<T, 8, 8, 128>(a, grad, s) : launch_one<T, 4, 16, 128>(a, grad, s);
+    if (a.E <= 128) return eight(16) ? launch_one<T, 16, 8, 256>(a, grad, s) : launch_one<T, 8, 16, 256>(a, grad, s);
+    if (a.E <= 256) return eight(32) ? launch_one<T, 32, 8, 256>(a, grad, s) : launch_one<T, 16, 16, 256>(a, grad, s);
     return launch_one<T, 32, 16, 256>(a, grad, s);
 }
 

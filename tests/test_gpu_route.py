@@ -83,6 +83,18 @@ def test_groups(E, groups, keep, top, score, biased):
     _check(l, dev, k, bias=bias, score=score, n_groups=groups, keep_groups=keep, group_top=top, scale=2.5)
 
 
+@pytest.mark.parametrize("T,E,groups,keep", [(33000, 32, 1, 1), (33000, 32, 4, 2), (17000, 60, 1, 1), (17000, 64, 4, 2),
+                                             (17000, 60, 10, 3), (8300, 128, 1, 1), (8300, 128, 4, 2), (8300, 100, 4, 1),
+                                             (4200, 256, 1, 1), (4200, 256, 8, 4), (4200, 256, 32, 9)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_rows(T, E, groups, keep, dtype):
+    """Enough rows that a lane holds 16 experts."""
+    l, dev = _logits(T, E, dtype, T)
+    bias = torch.randn(E, generator=torch.Generator().manual_seed(5)) * 0.2
+    for b, score, k in ((None, "softmax", 2), (bias, "sigmoid", 6)):
+        _check(l, dev, k, bias=b, score=score, n_groups=groups, keep_groups=keep, group_top=2, renorm=k == 6)
+
+
 @pytest.mark.parametrize("E,groups,keep,top", [(512, 4, 2, 2), (512, 32, 7, 2), (128, 8, 3, 1), (48, 3, 2, 2), (96, 2, 1, 2),
                                                (32, 2, 1, 1), (320, 20, 6, 2), (192, 3, 2, 2)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
