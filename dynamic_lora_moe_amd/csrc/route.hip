@@ -212,11 +212,14 @@ template <> __device__ __forceinline__ float logit_of<float>(float v) { return v
 template <> __device__ __forceinline__ float logit_of<uint16_t>(uint16_t v) { return bf_to_f(v); }
 
 // A logit as the routing sees it: +inf counts as the largest finite value, a
-// NaN as not available (-inf): the median instruction answers with the minimum
-// of three where one is a NaN.  (The builtin of it is folded to a minimum of two.)
+// NaN as not available (-inf).  Where an operand is a NaN the median instruction
+// answers min(min(a, b), c): a quiet one drops out of the inner minimum, of a
+// signalling one that makes a quiet NaN, which drops out of the outer.  With -inf
+// as the last operand the answer is -inf for both.  (The builtin of it is folded to
+// a minimum of two.)
 __device__ __forceinline__ float clean(float l) {
     float r;
-    asm("v_med3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(l), "v"(-__builtin_huge_valf()), "v"(3.402823466e38f));
+    asm("v_med3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(l), "v"(3.402823466e38f), "v"(-__builtin_huge_valf()));
     return r;
 }
 

@@ -171,6 +171,36 @@ def test_extreme_logits():
             assert torch.isfinite(g).all()
 
 
+NANS = {torch.bfloat16: [0x7F81, 0xFF81, 0x7FBF, 0xFFBF, 0x7FC0, 0xFFFF],
+        torch.float32: [0x7F800001, 0xFF800001, 0x7FBFFFFF, 0xFFBFFFFF, 0x7FC00000, 0xFFFFFFFF]}
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E,pitch", [(8, 0), (60, 61), (256, 0)])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_every_kind_of_nan(dtype, E, pitch, score, renorm):
+    """Quiet and signalling NaN of either sign, copied as bits, in aligned and unaligned rows: not available."""
+    l, _ = _logits(24, E, dtype, 5)
+    width = 8 * l.element_size()
+    ints = l.view(torch.int16 if width == 16 else torch.int32)
+    for n, t in enumerate(range(1, 24)):
+        for j in range(3):
+            p = NANS[dtype][(3 * n + j) % 6]
+            ints[t, (7 * t + 3 * j) % E] = p - (1 << width) if p >> (width - 1) else p
+    wide = torch.zeros((24, pitch or E), dtype=ints.dtype, device="cuda")
+    wide[:, :E] = ints.cuda()
+    idx, _ = _check(l, wide.view(dtype)[:, :E], 4, score=score, renorm=renorm)
+    took = l.gather(1, idx.cpu().clamp(min=0).long())
+    assert not took[idx.cpu() >= 0].isnan().any()
+
+
+def test_every_bf16_logit():
+    """All 65536 bit patterns as logits, 256 neighbouring ones a row."""
+    ints = torch.arange(-(1 << 15), 1 << 15, dtype=torch.int32).to(torch.int16).view(256, 256)
+    for score in ("softmax", "sigmoid"):
+        _check(ints.view(torch.bfloat16), ints.cuda().view(torch.bfloat16), 8, score=score, renorm=False)
+
+
 def test_bias_that_excludes():
     """-inf and NaN in the bias make an expert unavailable to be chosen, +inf puts it first; the weights do not know the bias."""
     l, dev = _logits(40, 16, torch.float32, 4)
