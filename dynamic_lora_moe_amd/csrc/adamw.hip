@@ -36,9 +36,9 @@
 // 8-bit moments 47 us, where the binary64 codes and hashes bound it as much as the
 // memory; 80 million fp32 weights with 8-bit moments 317 us, 4.0 TB/s.
 //
-// An element whose new v is not finite in fp32 (a gradient that is infinite,
-// NaN, or past 1.8e19) is left as it was, with 8-bit moments its whole block,
-// and the handle's error word is set.
+// An element whose new v is not finite in fp32 (a gradient that is infinite, NaN,
+// or past 1.8e19 / sqrt(1 - b2)) is left as it was, with 8-bit moments its whole
+// block, and the handle's error word is set.
 #include "adamw.hpp"
 #include "gfx950.hpp"
 #include "internal.hpp"
@@ -183,7 +183,9 @@ __device__ __forceinline__ void step_f32(const AdamArgs& a, const AdDesc& D, Ste
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float gj = g[k][j] * s.gs;
-            const float mj = fmaf(b1, m[k][j], r1 * gj), vj = fmaf(b2, v[k][j], r2 * (gj * gj));
+            // g'^2 may pass fp32 where v's share of it does not
+            const float g2 = gj * gj, inc = __builtin_isfinite(g2) ? r2 * g2 : (r2 * gj) * gj;
+            const float mj = fmaf(b1, m[k][j], r1 * gj), vj = fmaf(b2, v[k][j], inc);
             const bool fin = __builtin_isfinite(vj);
             if (!fin) {
                 bad = true;

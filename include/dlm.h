@@ -547,9 +547,9 @@ int dlm_adamw_destroy(dlm_adamw* h);
  * step reads them, and t, on every replay.
  * fp32 throughout (8-bit moments: binary64 between their codes); m and v of
  * this step enter w before they are rounded to codes.
- * An element whose new v is not finite in fp32 (a gradient infinite, NaN or
- * past 1.8e19) is left unchanged, with 8-bit states its whole block of 256, and
- * the error word is set.
+ * An element whose new v is not finite in fp32 (a g' infinite, NaN, or past about
+ * 1.8e19 / sqrt(1 - b2), which is 5.8e20 for b2 = 0.999) is left unchanged, with
+ * 8-bit states its whole block of 256, and the error word is set.
  */
 int dlm_adamw_step(dlm_adamw* h, const dlm_adamw_cfg* cfg, const float* lr_scale, const float* grad_scale, void* stream);
 

@@ -258,6 +258,33 @@ def test_gradients_that_are_not_finite(bits, value):
     assert opt.status() == (2, dlm.DLM_OK)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("value,taken", [(1e19, True), (-1e20, True), (5.8e20, True), (5.9e20, False), (-1e21, False)])
+def test_the_largest_gradients(bits, value, taken):
+    """Both widths take a gradient as long as the new v is finite in fp32, here up to 5.83e20."""
+    ps, gs, ws, st, _, _ = _make([1000, 300], torch.float32, torch.float32, False, bits, 7)
+    gs[0][600] = value
+    opt = dlm.AdamW(ps, gs, state_bits=bits, states=st, weight_decay=0.0, seed=5)
+    p0, s0 = ps[0].clone(), tuple(x.clone() for x in st[0])
+    opt.step(1e-3)
+    torch.cuda.synchronize()
+    assert opt.status() == (1, dlm.DLM_OK if taken else dlm.DLM_EDEVICE)
+    if not taken:
+        assert ps[0][600] == p0[600] and all(x[600] == y[600] for x, y in zip(st[0][:2], s0))
+        return
+    m0, v0 = (_f64(s0[0]), _f64(s0[1])) if bits == 32 else ref.decode(*[x.cpu().numpy() for x in s0])
+    m, v = ref.moments(_f64(gs[0]), m0, v0, B1, B2)
+    if bits == 8:
+        for x, y in zip(st[0], ref.encode(m, v, 5, 1, 0)):
+            assert np.array_equal(x.cpu().numpy(), y)
+    else:  # (two products and a sum for v, r2 rounded: 4 u; the old moments are nothing beside it)
+        assert abs(float(st[0][0][600]) - m[600]) <= 4 * U * abs(m[600])
+        assert abs(float(st[0][1][600]) - v[600]) <= 4 * U * v[600]
+    new, s = ref.update(_f64(p0), m, v, 1, 1e-3, B1, B2, EPS, 0.0)
+    # the step's sixteen roundings and what 4 u of m and of v (a root of it) make of it
+    assert abs(float(ps[0][600]) - new[600]) <= 4 * U * abs(float(p0[600])) + 1e-3 * (16 + 4 + 2) * U * abs(s[600])
+
+
 def test_scales_on_the_device():
     """lr_scale and grad_scale multiply as the arguments would."""
     n = 3000
