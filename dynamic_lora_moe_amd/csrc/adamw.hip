@@ -251,13 +251,14 @@ __device__ __forceinline__ uint32_t m_code(double x, uint32_t h) {
     const uint32_t b0 = ((c * c) << 17) + u * (2 * c + 1), b1 = (((c + 1) * (c + 1)) << 17) + u * (2 * c + 3);
     return c + (xi > b0 ? 1u : 0u) + (xi > b1 ? 1u : 0u);
 }
-// The same for v with steps between fourth powers; root = sqrt x.
+// The same for v with steps between fourth powers; root = sqrt x over shrink^2 (a
+// power of two, times the little).
 __device__ __forceinline__ double pow4(uint32_t c) {
     const double s = (double)(c * c);
     return s * s;
 }
-__device__ __forceinline__ uint32_t v_code(double x, float root, uint32_t h) {
-    const uint32_t c = (uint32_t)(__builtin_amdgcn_sqrtf(root) * 0.9999997f);
+__device__ __forceinline__ uint32_t v_code(double x, float root, float shrink, uint32_t h) {
+    const uint32_t c = (uint32_t)(__builtin_amdgcn_sqrtf(root) * shrink);
     const double u = (double)(2 * h + 1) * (1.0 / 131072.0);
     const double p0 = pow4(c), p1 = pow4(c + 1), p2 = pow4(c + 2);
     return c + (x > __builtin_fma(u, p1 - p0, p0) ? 1u : 0u) + (x > __builtin_fma(u, p2 - p1, p1) ? 1u : 0u);
@@ -329,8 +330,13 @@ __device__ __forceinline__ void step_q8(const AdamArgs& a, const AdDesc& D, int 
         mm = wave_max(mm);
         vm = wave_max(vm);
         const double mi = mm > 0.f ? kM2 / (double)mm : 0.0, vi = vm > 0.f ? kV4 / (double)vm : 0.0;
-        // sqrt(v / (1 - b2^t)) from the root of v's place in the block
-        const float vroot = sqrtf(vm) * s.rc2 * (1.f / (255.f * 255.f));
+        // sqrt(v / (1 - b2^t)) from the root of v's place in the block.  Beside a large
+        // vm the place of a v that counts may lie below fp32's normal numbers: its
+        // root is taken 2^46 times as large (vm <= 1: such a v is 0 in fp32 too)
+        const bool high = vm > 1.f;
+        const double up = high ? 0x1p92 : 1.0;
+        const float shrink = high ? 0.9999997f * 0x1p-23f : 0.9999997f;
+        const float vroot = sqrtf(vm) * s.rc2 * (1.f / (255.f * 255.f)) * (high ? 0x1p-46f : 1.f);
         const uint32_t key = mix(key_t + (uint32_t)blk * 0xC2B2AE3Du);
         const uint32_t least = vm > 0.f ? 1u : 0u;
         uint32_t nq = 0, nc = 0;
@@ -341,8 +347,8 @@ __device__ __forceinline__ void step_q8(const AdamArgs& a, const AdDesc& D, int 
             const uint32_t k = m_code(xm < kM2 ? xm : kM2, h & 0xffffu);
             nq |= ((m[j] < 0.0 ? 0u - k : k) & 255u) << (8 * j);
             const double xc = xv < kV4 ? xv : kV4;
-            const float root = __builtin_amdgcn_sqrtf((float)xc);
-            uint32_t cv = v_code(xc, root, h >> 16);
+            const float root = __builtin_amdgcn_sqrtf((float)(xc * up));
+            uint32_t cv = v_code(xc, root, shrink, h >> 16);
             cv = cv < least && v[j] > 0.0 ? least : cv;
             nc |= cv << (8 * j);
             // the quotient by the reciprocal's estimate (1 ulp): the step is lr of a weight

@@ -285,6 +285,21 @@ def test_the_largest_gradients(bits, value, taken):
     assert abs(float(ps[0][600]) - new[600]) <= 4 * U * abs(float(p0[600])) + 1e-3 * (16 + 4 + 2) * U * abs(s[600])
 
 
+@pytest.mark.parametrize("value", [1e15, 1e20, 5e20])
+def test_8bit_neighbours_of_a_huge_gradient(value):
+    """One huge gradient in a block: the others' codes go to the bottom of its range, their steps do not."""
+    ps, gs, ws, st, _, _ = _make([1000], torch.float32, torch.float32, False, 8, 7)
+    st[0][1][512:768] = 0
+    gs[0][512:600] = torch.logspace(-3, -18, 88)
+    gs[0][600] = value
+    opt = dlm.AdamW(ps, gs, state_bits=8, states=st, weight_decay=0.0, seed=5)
+    p0, s0 = ps[0].clone(), tuple(x.clone() for x in st[0])
+    opt.step(1e-3)
+    torch.cuda.synchronize()
+    assert opt.status() == (1, dlm.DLM_OK)
+    _compare(0, (p0, None, s0), ps[0], gs[0], None, st[0], 8, 1, 1e-3, 0.0)
+
+
 def test_scales_on_the_device():
     """lr_scale and grad_scale multiply as the arguments would."""
     n = 3000
