@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1468,6 +1469,8 @@ int dlm_adamw_step(dlm_adamw* h, const dlm_adamw_cfg* c, const float* lr_scale, 
     if (!(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0))
         return fail(DLM_EINVAL, "adamw_step: beta1=%g, beta2=%g not in [0, 1)", c->beta1, c->beta2);
     if (!(c->eps > 0.f) || !std::isfinite(c->eps)) return fail(DLM_EINVAL, "adamw_step: eps=%g is not positive", c->eps);
+    if (h->bits == 8 && c->eps < FLT_MIN)  // the kernel's reciprocal of such a number is infinite
+        return fail(DLM_EINVAL, "adamw_step: eps=%g is below 2^-126, the least with 8-bit moments", c->eps);
     if (h->n_chunks == 0) return ok();
     AdamArgs a{};
     a.descs = h->d_descs;

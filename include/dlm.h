@@ -512,7 +512,7 @@ typedef struct {
 typedef struct {
     float lr;
     double beta1, beta2; /* in [0, 1) */
-    float eps;           /* > 0 */
+    float eps;           /* > 0, with 8-bit states at least 2^-126 */
 } dlm_adamw_cfg;
 
 typedef struct dlm_adamw dlm_adamw;

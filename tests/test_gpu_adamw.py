@@ -300,6 +300,24 @@ def test_8bit_neighbours_of_a_huge_gradient(value):
     _compare(0, (p0, None, s0), ps[0], gs[0], None, st[0], 8, 1, 1e-3, 0.0)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 2.0 ** -126, 1e-30])
+def test_the_least_eps(bits, eps):
+    """Elements without a gradient stay where they are at any eps that is taken; the 8-bit step refuses those below 2^-126."""
+    p = torch.full((600,), 0.5, device="cuda")
+    g = torch.zeros(600, device="cuda")
+    g[:100] = 1e-3
+    opt = dlm.AdamW([p], [g], state_bits=bits, eps=eps, weight_decay=0.0)
+    if bits == 8 and eps < 2.0 ** -126:
+        with pytest.raises(dlm.DLMError, match="eps"):
+            opt.step(1e-3)
+        assert opt.status() == (0, dlm.DLM_OK)
+        return
+    opt.step(1e-3)
+    torch.cuda.synchronize()
+    assert (p[100:] == 0.5).all() and (p[:100] < 0.5).all() and torch.isfinite(p).all()
+
+
 def test_scales_on_the_device():
     """lr_scale and grad_scale multiply as the arguments would."""
     n = 3000
