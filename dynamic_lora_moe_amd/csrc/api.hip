@@ -1494,7 +1494,8 @@ int dlm_adamw_step(dlm_adamw* h, const dlm_adamw_cfg* c, const float* lr_scale, 
 
 int dlm_adamw_status(dlm_adamw* h, int64_t* step, int32_t* code, void* stream) {
     if (!h || !step || !code) return fail(DLM_EINVAL, "adamw_status: null argument");
-    int32_t t = (int32_t)h->step0, err = 0;  // a handle of empty tensors counts nothing
+    uint32_t t = (uint32_t)h->step0;  // a handle of empty tensors counts nothing
+    int32_t err = 0;
     hipError_t e = hipStreamSynchronize((hipStream_t)stream);
     if (e == hipSuccess && h->n_chunks > 0) e = hipMemcpy(&t, h->d_steps, sizeof t, hipMemcpyDeviceToHost);
     if (e == hipSuccess) e = hipMemcpy(&err, h->d_err, sizeof err, hipMemcpyDeviceToHost);

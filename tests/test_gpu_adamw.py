@@ -318,6 +318,14 @@ def test_the_least_eps(bits, eps):
     assert (p[100:] == 0.5).all() and (p[:100] < 0.5).all() and torch.isfinite(p).all()
 
 
+def test_the_count_goes_on_past_31_bits():
+    p, g = torch.zeros(10, device="cuda"), torch.ones(10, device="cuda")
+    opt = dlm.AdamW([p], [g], step=(1 << 31) - 1)
+    for k in range(3):
+        opt.step(1e-3)
+        assert opt.status() == ((1 << 31) + k, dlm.DLM_OK)
+
+
 def test_scales_on_the_device():
     """lr_scale and grad_scale multiply as the arguments would."""
     n = 3000
