@@ -709,8 +709,9 @@ class AdamW:
 
     def status(self, stream=None):
         """(steps taken, DLM_OK or DLM_EDEVICE: some gradient was not finite); clears the error."""
+        handle = _here(self.params[0], stream, "parameter 0")
         step, code = C.c_int64(0), C.c_int32(0)
-        _check(load().dlm_adamw_status(self._h, C.byref(step), C.byref(code), _stream(stream)), "dlm_adamw_status")
+        _check(load().dlm_adamw_status(self._h, C.byref(step), C.byref(code), handle), "dlm_adamw_status")
         return step.value, code.value
 
     def read_state(self, k: int, stream=None):

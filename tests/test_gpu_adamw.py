@@ -379,6 +379,17 @@ def test_other_stream_and_many_tensors():
     assert all(torch.equal(a, b) for a, b in zip(*out))
 
 
+def test_calls_with_another_device_current(monkeypatch):
+    """A stream of another device orders nothing here: step() and status() refuse the call."""
+    opt = dlm.AdamW([torch.zeros(10, device="cuda")], [torch.ones(10, device="cuda")])
+    with monkeypatch.context() as m:
+        m.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+        for call in (lambda: opt.step(1e-3), opt.status):
+            with pytest.raises(ValueError, match="current device"):
+                call()
+    assert opt.status() == (0, dlm.DLM_OK)
+
+
 def test_refusals_of_the_binding():
     p, g = torch.zeros(10, device="cuda"), torch.zeros(10, device="cuda")
     with pytest.raises(ValueError):
