@@ -170,15 +170,34 @@ def _like(t: torch.Tensor, name: str, shape, dtype, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _sets_out(idx, g, T: int, device, what: str):
-    """Per-row expert sets: idx [T][2] int32 and g [T][2] fp32 (allocated when None)."""
-    if idx is None:
-        idx = torch.empty((T, 2), dtype=torch.int32, device=device)
-    if g is None:
-        g = torch.empty((T, 2), dtype=torch.float32, device=device)
-    _like(idx, f"{what} idx", (T, 2), torch.int32, device)
-    _like(g, f"{what} g", (T, 2), torch.float32, device)
+def _sets_out(idx, g, T: int, k: int, device, what: str, stream):
+    """Per-row expert sets: idx [T][k] int32 and g [T][k] fp32 (allocated when None)."""
+    own_idx, own_g = idx is None, g is None
+    if own_idx:
+        idx = torch.empty((T, k), dtype=torch.int32, device=device)
+    else:
+        _like(idx, f"{what} idx", (T, k), torch.int32, device)
+    if own_g:
+        g = torch.empty((T, k), dtype=torch.float32, device=device)
+    else:
+        _like(g, f"{what} g", (T, k), torch.float32, device)
+    if stream is not None:
+        _fresh(stream, idx if own_idx else None, g if own_g else None)
     return idx, g
+
+
+def _fresh(stream, *tensors):
+    """Before a launch on `stream` into tensors made here on the current stream (a None
+    was not): what the current stream still runs may use the memory they were given, so
+    `stream` waits for it, and the allocator keeps them until the launch has ended."""
+    made = [t for t in tensors if t is not None]
+    if stream is None or not made:
+        return
+    current = torch.cuda.current_stream(made[0].device)
+    if stream != current:
+        stream.wait_stream(current)
+        for t in made:
+            t.record_stream(stream)
 
 
 # ---- router -------------------------------------------------------------------
@@ -190,7 +209,7 @@ def pregate(x: torch.Tensor, Wr: torch.Tensor, idx=None, g=None, stream=None):
     T, d = x.shape
     E = Wr.shape[1]
     _like(Wr, "Wr", (d, E), x.dtype, x.device)
-    idx, g = _sets_out(idx, g, T, x.device, "pregate")
+    idx, g = _sets_out(idx, g, T, 2, x.device, "pregate", stream)
     _check(load().dlm_pregate(_p(x), _p(Wr), T, d, E, _dt(x), _p(idx), _p(g), _stream(stream)),
            "dlm_pregate")
     return idx, g
@@ -204,7 +223,7 @@ def pregate_centroid(x: torch.Tensor, C: torch.Tensor, idx=None, g=None, stream=
     T, d = x.shape
     E, J, d2 = C.shape
     _like(C, "C", (E, J, d), x.dtype, x.device)
-    idx, g = _sets_out(idx, g, T, x.device, "pregate_centroid")
+    idx, g = _sets_out(idx, g, T, 2, x.device, "pregate_centroid", stream)
     _check(load().dlm_pregate_centroid(_p(x), _p(C), T, d, E, J, _dt(x), _p(idx), _p(g), _stream(stream)),
            "dlm_pregate_centroid")
     return idx, g
@@ -239,15 +258,6 @@ def _here(t: torch.Tensor, stream, name: str) -> int:
     return stream.cuda_stream
 
 
-def _fresh(stream, *tensors):
-    """Tensors made here on the current stream and used on `stream`: the
-    allocator keeps them until that work has ended."""
-    if stream is not None and stream != torch.cuda.current_stream():
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-
-
 @functools.lru_cache(maxsize=64)
 def _route_cfg(k, score, n_groups, keep_groups, group_top, renorm, scale):
     if score not in _SCORES:
@@ -273,18 +283,10 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, n_gro
         _like(bias, "bias", (E,), torch.float32, logits.device)
     if counts is not None:
         _like(counts, "counts", (E,), torch.int32, logits.device)
-    if idx is None:
-        idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    else:
-        _like(idx, "route idx", (T, k), torch.int32, logits.device)
-    if g is None:
-        g = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    else:
-        _like(g, "route g", (T, k), torch.float32, logits.device)
+    idx, g = _sets_out(idx, g, T, k, logits.device, "route", stream)
     cfg = _route_cfg(k, score, n_groups, keep_groups, group_top, bool(renorm), float(scale))
     _check(load().dlm_route(logits.data_ptr(), ld, _ptr(bias), T, E, _dt(logits), cfg, idx.data_ptr(), g.data_ptr(),
                             _ptr(counts), handle), "dlm_route")
-    _fresh(stream, idx, g)
     return idx, g
 
 
@@ -301,6 +303,7 @@ def route_backward(logits: torch.Tensor, idx: torch.Tensor, dg: torch.Tensor, sc
     _like(dg, "dg", (T, k), torch.float32, logits.device)
     if dlogits is None:
         dlogits, ldd = torch.empty((T, E), dtype=logits.dtype, device=logits.device), max(E, 1)
+        _fresh(stream, dlogits)
     else:
         Td, Ed, ldd = _rows(dlogits, "dlogits")
         if (Td, Ed) != (T, E) or dlogits.dtype != logits.dtype or dlogits.device != logits.device:
@@ -308,7 +311,6 @@ def route_backward(logits: torch.Tensor, idx: torch.Tensor, dg: torch.Tensor, sc
     cfg = _route_cfg(k, score, 1, 1, 1, bool(renorm), float(scale))
     _check(load().dlm_route_backward(logits.data_ptr(), ld, idx.data_ptr(), dg.data_ptr(), T, E, _dt(logits), cfg,
                                      dlogits.data_ptr(), ldd, handle), "dlm_route_backward")
-    _fresh(stream, dlogits)
     return dlogits
 
 
@@ -457,6 +459,7 @@ def sgmm(x, idx, g, A, B, y, scale: float, workspace=None, stream=None):
     own = workspace is None
     if own:
         workspace = sgmm_workspace(T, d_in, E, r, 1, x.device)
+        _fresh(stream, workspace)
     _check(load().dlm_sgmm(_p(x), _p(idx), _p(g), _p(A), _p(B), _p(y), T, d_in, d_out, E, r,
                            float(scale), _dt(x), _p(workspace), _ws_bytes(workspace), _stream(stream)),
            "dlm_sgmm")
@@ -555,15 +558,11 @@ class SgmmGroup:
             raise ValueError(f"T={T} rows, but the group's problems hold {self.rows}")
         _like(idx[:T], "idx", (T, 2), torch.int32, self.device)
         _like(g[:T], "g", (T, 2), torch.float32, self.device)
-        own = workspace is None
-        if own:
+        if workspace is None:
             workspace = self.workspace(T, idx.device)
+            _fresh(stream, workspace)
         _check(load().dlm_sgmm_group_run(self._h, _p(idx), _p(g), T, _p(workspace),
                                          _ws_bytes(workspace), _stream(stream)), "dlm_sgmm_group_run")
-        if own and stream is not None and stream != torch.cuda.current_stream():
-            # a workspace made here on the current stream is used on `stream`:
-            # keep the allocator from handing it out again before those launches end
-            workspace.record_stream(stream)
         return workspace
 
     def bind_grads(self, dys, dxs, dAs, dBs):
@@ -608,13 +607,11 @@ class SgmmGroup:
         _like(g[:T], "g", (T, 2), torch.float32, self.device)
         if dg is not None:
             _like(dg[:T], "dg", (T, 2), torch.float32, self.device)
-        own = workspace is None
-        if own:
+        if workspace is None:
             workspace = self.backward_workspace(T)
+            _fresh(stream, workspace)
         _check(load().dlm_sgmm_group_backward(self._h, _ptr(idx), _ptr(g), _ptr(dg), T, 1 if accumulate else 0,
                                               _ptr(workspace), _ws_bytes(workspace), handle), "dlm_sgmm_group_backward")
-        if own:
-            _fresh(stream, workspace)
         return workspace
 
     def close(self):
@@ -743,11 +740,12 @@ def adamw_read_state(m, v, m_scale, v_scale, m_out=None, v_out=None, stream=None
     _like(m_scale, "m_scale", (nb,), torch.float32, m.device)
     _like(v_scale, "v_scale", (nb,), torch.float32, m.device)
     handle = _here(m, stream, "m")
-    m_out = torch.empty(n, device=m.device) if m_out is None else m_out
-    v_out = torch.empty(n, device=m.device) if v_out is None else v_out
+    own_m, own_v = m_out is None, v_out is None
+    m_out = torch.empty(n, device=m.device) if own_m else m_out
+    v_out = torch.empty(n, device=m.device) if own_v else v_out
     _like(m_out, "m_out", (n,), torch.float32, m.device)
     _like(v_out, "v_out", (n,), torch.float32, m.device)
+    _fresh(stream, m_out if own_m else None, v_out if own_v else None)
     _check(load().dlm_adamw_read_state(_p(m), _p(v), _p(m_scale), _p(v_scale), n, _p(m_out), _p(v_out), handle),
            "dlm_adamw_read_state")
-    _fresh(stream, m_out, v_out)
     return m_out, v_out
