@@ -654,6 +654,8 @@ class AdamW:
             raise ValueError("state_bits is 32 or 8")
         if states is None:
             states = [self._zeros(p, state_bits) for p in self.params]
+            if self.params[0].is_cuda:  # steps may run on any stream
+                torch.cuda.current_stream(self.params[0].device).synchronize()
         self.states = [tuple(st) for st in states]
         if not len(self.masters) == len(wd) == len(self.states) == n:
             raise ValueError("one master (or None), weight decay and state per parameter")

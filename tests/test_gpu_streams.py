@@ -78,3 +78,21 @@ def test_a_workspace_waits_for_its_memory(name):
         assert not done.query()
         torch.cuda.synchronize()
         assert dlm.sgmm_status(workspace) == dlm.DLM_OK
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_made_on_another_stream_than_the_steps(bits):
+    """Zero moments made behind queued work are zero before the handle's first step, on whatever stream."""
+    w, g = _rnd(100000), _rnd(100000, seed=1)
+    a, b = w.clone(), w.clone()
+    want = dlm.AdamW([a], [g], state_bits=bits)
+    want.step(1e-3)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(one):
+        torch.cuda._sleep(100_000_000)
+        opt = dlm.AdamW([b], [g], state_bits=bits)
+    opt.step(1e-3, stream=two)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    assert all(torch.equal(x, y) for x, y in zip(opt.states[0], want.states[0]))
