@@ -433,6 +433,12 @@ def sgmm_workspace(T: int, d_in_max: int, E: int, r: int, n_problems: int = 1,
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _clean(workspace):
+    """The workspace with its status word cleared, for who may read it before a launch has written it."""
+    workspace[:256].zero_()
+    return workspace
+
+
 def _ws_bytes(workspace) -> int:
     _need(workspace, "workspace")
     return workspace.numel() * workspace.element_size()
@@ -559,7 +565,7 @@ class SgmmGroup:
         _like(idx[:T], "idx", (T, 2), torch.int32, self.device)
         _like(g[:T], "g", (T, 2), torch.float32, self.device)
         if workspace is None:
-            workspace = self.workspace(T, idx.device)
+            workspace = self.workspace(T, idx.device) if T else _clean(self.workspace(T, idx.device))
             _fresh(stream, workspace)
         _check(load().dlm_sgmm_group_run(self._h, _p(idx), _p(g), T, _p(workspace),
                                          _ws_bytes(workspace), _stream(stream)), "dlm_sgmm_group_run")
@@ -608,7 +614,7 @@ class SgmmGroup:
         if dg is not None:
             _like(dg[:T], "dg", (T, 2), torch.float32, self.device)
         if workspace is None:
-            workspace = self.backward_workspace(T)
+            workspace = self.backward_workspace(T) if T else _clean(self.backward_workspace(T))
             _fresh(stream, workspace)
         _check(load().dlm_sgmm_group_backward(self._h, _ptr(idx), _ptr(g), _ptr(dg), T, 1 if accumulate else 0,
                                               _ptr(workspace), _ws_bytes(workspace), handle), "dlm_sgmm_group_backward")

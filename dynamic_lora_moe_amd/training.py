@@ -21,7 +21,7 @@ from __future__ import annotations
 
 import torch
 
-from . import DLM_OK, AdamW, SgmmGroup, route, route_backward, sgmm_status
+from . import DLM_OK, AdamW, SgmmGroup, _clean, route, route_backward, sgmm_status
 
 
 class AdapterTraining:
@@ -52,8 +52,9 @@ class AdapterTraining:
         self.logits = torch.empty((T, E), device=dev)
         self.idx = torch.empty((T, 2), dtype=torch.int32, device=dev)
         self.g, self.dg = torch.empty((T, 2), device=dev), torch.empty((T, 2), device=dev)
-        self.ws_forward = self.group.workspace(T, dev)
-        self.ws_backward = self.group.backward_workspace(T)
+        # status() may be asked before the first backward()
+        self.ws_forward = _clean(self.group.workspace(T, dev))
+        self.ws_backward = _clean(self.group.backward_workspace(T))
         params = [t for _, A, B, _ in self.projections for t in (A, B)] + [self.W_r]
         grads = [t for pair in zip(self.dA, self.dB) for t in pair] + [self.dW_r]
         keep = masters and self.W_r.dtype != torch.float32

@@ -162,3 +162,38 @@ def test_a_whole_step_replayed_from_a_graph():
         assert opt.status() == (4, dlm.DLM_OK)
         res.append([A, B, y, dx, dA, dB, dg, dl])
     assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
+@pytest.fixture
+def dirty_workspaces(monkeypatch):
+    """Byte tensors that torch.empty makes hold garbage."""
+    real = torch.empty
+
+    def empty(*a, **k):
+        t = real(*a, **k)
+        return t.fill_(0x5A) if t.dtype == torch.uint8 else t
+
+    monkeypatch.setattr(torch, "empty", empty)
+
+
+def test_status_before_anything_ran(dirty_workspaces):
+    """The status is that of the calls so far, whatever the workspaces' memory held."""
+    T, E, r, d = 8, 4, 8, 64
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    tr = AdapterTraining([(z(T, d), z(E, r, d), z(E, d, r), z(T, d))], (z(T, d), z(d, E)), [z(T, d)], [z(T, d)], E, r, 1.0)
+    assert tr.status() == dlm.DLM_OK
+    tr.forward()
+    assert tr.status() == dlm.DLM_OK
+    tr.backward()
+    tr.step(1e-3)
+    assert tr.status() == dlm.DLM_OK
+
+
+def test_status_of_calls_without_rows(dirty_workspaces):
+    E, r, d = 4, 8, 64
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    grp = dlm.SgmmGroup([(z(8, d), z(E, r, d), z(E, d, r), z(8, d))], E, r, 1.0)
+    grp.bind_grads([z(8, d)], [z(8, d)], [torch.empty((E, r, d), device="cuda")], [torch.empty((E, d, r), device="cuda")])
+    idx, g = torch.zeros((8, 2), dtype=torch.int32, device="cuda"), torch.zeros((8, 2), device="cuda")
+    for call in (grp.run, grp.backward):
+        assert dlm.sgmm_status(call(idx, g, T=0)) == dlm.DLM_OK
