@@ -1227,6 +1227,55 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
         return ao;
     };
 
+    // The results in ys of the 64 columns from c0b on that are not finite, again from
+    // the row's own experts: one at a time, a lane to an element.  (BV 2.)
+    auto own_terms = [&](int c0b) {
+        const int64_t row = gld(perm + tile * 32 + n);
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {
+            const int chunk = 4 * (i >> 4) + 2 * h + (i >> 3 & 1), col = c0b + 8 * chunk + (i & 7);
+            uint16_t* at = ys + y_off(n, chunk) + (i & 7);
+            if (row < 0 || col >= d_out || __builtin_isfinite(bf_to_f(*at))) continue;
+            float sum = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < nU; ++k) {
+                const int e = s_U[k];
+                if (e0 != e && e1 != e) continue;
+#pragma unroll 1
+                for (int c = 0; c < 2 * R16; ++c) {  // eight ranks
+                    const int q = k * R16 + c / 2;
+                    const u32x4 bo = ld128(B + ((int64_t)(e * R16 + c / 2) * d_out + col) * 16 + 8 * (c & 1));
+                    if (shared_u) {
+                        const u32x4 uh = s_u[q][0][n + 32 * (c & 1)], ul = s_u[q][1][n + 32 * (c & 1)];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            sum = fmaf(bf_lo(bo[j]), bf_lo(uh[j]) + bf_lo(ul[j]), sum);
+                            sum = fmaf(bf_hi(bo[j]), bf_hi(uh[j]) + bf_hi(ul[j]), sum);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int j = 0; j < 8; ++j) {
+                            const int rank = 8 * c + j;
+                            if (rank >= r) break;
+                            float a0, a1;
+                            if constexpr (FOLD) {
+                                a0 = v0[4 * ((rank / 4) ^ (n & kVX)) + rank % 4];
+                                a1 = v0[4 * (((RPAD + rank) / 4) ^ (n & kVX)) + rank % 4];
+                            } else {
+                                a0 = gld(v0 + rank);
+                                a1 = gld(v1 + rank);
+                            }
+                            const float u = fmaf(c1, e1 == e ? a1 : 0.f, c0 * (e0 == e ? a0 : 0.f));
+                            const uint32_t word = j < 4 ? (j < 2 ? bo[0] : bo[1]) : (j < 6 ? bo[2] : bo[3]);
+                            sum = fmaf(j & 1 ? bf_hi(word) : bf_lo(word), u, sum);
+                        }
+                    }
+                }
+            }
+            *at = f_to_bf(bf_to_f(gld(y + row * d_out + col)) + sum);
+        }
+    };
+
     if (shared_u) {
         for (int q = w; q < nq; q += 4) make_u(q, s_u[q][0][lane], s_u[q][1][lane]);
     }
@@ -1294,6 +1343,17 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
                 }
                 *(u32x4*)(ys + y_off(n, 4 * b + 2 * h + q)) = u32x4{ow[0], ow[1], ow[2], ow[3]};
             }
+        if constexpr (BV == 2) {
+            // A bank's infinity or NaN times the 0 of a row without that expert is a NaN:
+            // where a sum is not finite, the row's own experts alone decide.
+            float bad[4] = {0.f, 0.f, 0.f, 0.f};  // 0, or NaN
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) bad[2 * b + (i & 1)] = fmaf(acc[b][i], 0.f, bad[2 * b + (i & 1)]);
+            const float any = (bad[0] + bad[1]) + (bad[2] + bad[3]);
+            if (__ballot(any != any)) own_terms(c0b);
+        }
         const int col = c0b + 8 * lc;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -253,6 +253,37 @@ def test_infinities_stay_with_their_row_and_rank(i):
     assert torch.equal(torch.isfinite(c.dB[0]).all(1).cpu(), want)
 
 
+@pytest.mark.parametrize("dtype,E,r,T,shape", [(BF, 8, 16, 100, (64, 64)), (BF, 8, 64, 100, (72, 200)), (BF, 8, 128, 100, (64, 72)),
+                                               (BF, 32, 16, 300, (64, 136)), (BF, 32, 64, 300, (64, 64)), (BF, 32, 5, 300, (64, 2056)),
+                                               (BF, 12, 100, 200, (64, 72)), (F32, 8, 6, 100, (40, 33))])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_bank_that_is_not_finite_stays_with_its_rows(dtype, E, r, T, shape, value):
+    """One element of one expert's A (every matrix tile of its rows holds others' too): dx of the rows that
+    choose it is lost in that column, everything else is as if that expert's terms were elsewhere."""
+    o, i = shape
+    col, rank = i - 3, r - 1
+    c = Case(T, [shape], E, r, dtype, empty=0.1, both=0.0).bind()
+    c.dev[0][1][3, rank, col] = value
+    c.run()
+    mine = (c.idx == 3).any(1) & (c.g[torch.arange(T)[:, None], torch.arange(2)] != 0).any(1)
+    assert mine.any() and (~mine).any()
+    got = c.ddx[0].cpu()
+    assert not torch.isfinite(got[mine, col]).any()
+    # what the value cannot reach, against the plain form of the banks as they were
+    out, mag = c.refs()[0]
+    want = c.dx0[0].double() + out[0]
+    bf = dtype == BF
+    u = 2.0 ** -8 if bf else 2.0 ** -24
+    tol = (gamma(o + 4 * r + 8) + (SPLIT if bf else 0.0)) * (mag[0] + c.dx0[0].double().abs() * (1 - bf)) + u * want.abs()
+    free = torch.ones_like(got, dtype=torch.bool)
+    free[mine, col] = False
+    err = (got.double() - want).abs()
+    assert (err[free] <= (tol + u * tol)[free]).all()
+    other = (c.idx != 3).all(1)
+    dg, dgm = out[3], mag[3]
+    assert ((c.dg.cpu().double() - dg).abs()[other] <= gamma(o + i + 2 * r + 9) * dgm[other]).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_accumulate(dtype):
     c = Case(90, [(72, 136), (64, 64)], 5, 12, dtype).bind()
