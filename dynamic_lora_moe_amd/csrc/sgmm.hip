@@ -1228,9 +1228,9 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
     };
 
     // The results in ys of the 64 columns from c0b on that are not finite, again from
-    // the row's own experts: one at a time, a lane to an element.  (BV 2.)
+    // the row's own experts: one at a time, a lane to an element.
     auto own_terms = [&](int c0b) {
-        const int64_t row = gld(perm + tile * 32 + n);
+        const int64_t row = i_perm ? i_perm[tile * 32 + n] : gld(perm + tile * 32 + n);
 #pragma unroll 1
         for (int i = 0; i < 32; ++i) {
             const int chunk = 4 * (i >> 4) + 2 * h + (i >> 3 & 1), col = c0b + 8 * chunk + (i & 7);
@@ -1244,7 +1244,23 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
 #pragma unroll 1
                 for (int c = 0; c < 2 * R16; ++c) {  // eight ranks
                     const int q = k * R16 + c / 2;
-                    const u32x4 bo = ld128(B + ((int64_t)(e * R16 + c / 2) * d_out + col) * 16 + 8 * (c & 1));
+                    if (8 * c >= r) break;
+                    u32x4 bo = {0u, 0u, 0u, 0u};
+                    if constexpr (BV == 2) {
+                        bo = ld128(B + ((int64_t)(e * R16 + c / 2) * d_out + col) * 16 + 8 * (c & 1));
+                    } else {
+                        const uint16_t* bp = B + ((int64_t)e * d_out + col) * r + 8 * c;
+                        if constexpr (BV == 1) {
+                            bo = ld128(bp);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t lo = 8 * c + 2 * j < r ? gld(bp + 2 * j) : 0u;
+                                const uint32_t hi = 8 * c + 2 * j + 1 < r ? gld(bp + 2 * j + 1) : 0u;
+                                bo[j] = lo | (hi << 16);
+                            }
+                        }
+                    }
                     if (shared_u) {
                         const u32x4 uh = s_u[q][0][n + 32 * (c & 1)], ul = s_u[q][1][n + 32 * (c & 1)];
 #pragma unroll
@@ -1343,17 +1359,15 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
                 }
                 *(u32x4*)(ys + y_off(n, 4 * b + 2 * h + q)) = u32x4{ow[0], ow[1], ow[2], ow[3]};
             }
-        if constexpr (BV == 2) {
-            // A bank's infinity or NaN times the 0 of a row without that expert is a NaN:
-            // where a sum is not finite, the row's own experts alone decide.
-            float bad[4] = {0.f, 0.f, 0.f, 0.f};  // 0, or NaN
+        // A bank's infinity or NaN times the 0 of a row without that expert is a NaN:
+        // where a sum is not finite, the row's own experts alone decide.
+        float bad[4] = {0.f, 0.f, 0.f, 0.f};  // 0, or NaN
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 16; ++i)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) bad[2 * b + (i & 1)] = fmaf(acc[b][i], 0.f, bad[2 * b + (i & 1)]);
-            const float any = (bad[0] + bad[1]) + (bad[2] + bad[3]);
-            if (__ballot(any != any)) own_terms(c0b);
-        }
+            for (int b = 0; b < 2; ++b) bad[2 * b + (i & 1)] = fmaf(acc[b][i], 0.f, bad[2 * b + (i & 1)]);
+        const float any = (bad[0] + bad[1]) + (bad[2] + bad[3]);
+        if (__ballot(any != any)) own_terms(c0b);
         const int col = c0b + 8 * lc;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1389,7 +1403,10 @@ __device__ __forceinline__ int64_t expand_place(const SgmmArgs& a, int64_t bid, 
     return t < n_live ? t : -1;
 }
 template <int R16, int BV>
-__global__ __launch_bounds__(256) void sgmm_expand_bf16(SgmmArgs a) {
+// (Three waves per SIMD at r % 8 == 0, which the compiler would give up for four
+// registers; the guarded loads of other ranks have always taken two.)
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BV == 1 ? 3 : 2)))
+void sgmm_expand_bf16(SgmmArgs a) {
     const int32_t* hdr = (const int32_t*)(a.ws + a.L.hdr);
     __shared__ int32_t s_iperm[kWave];
     __shared__ uint32_t s_iep[kWave];

@@ -345,6 +345,7 @@ int dlm_sgmm_workspace_size(int64_t T, int64_t d_in_max, int32_t E, int32_t r,
  * results are those of the segmented launches bit for bit.  Results are
  * bitwise reproducible run to run.
  * Rows whose two slots are empty are not touched.
+ * What is not finite in a bank reaches the rows that choose its expert, no others.
  * A row with an index outside [-1, E) or a non-finite gate on a used slot makes
  * the whole call a no-op on y and sets the workspace status word (read it with
  * dlm_sgmm_status).

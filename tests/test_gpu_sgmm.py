@@ -346,3 +346,46 @@ def test_inline_row_order_equals_the_segmentation(T, d_in, d_out, E, r, seed):
     assert torch.equal(ya, yb[:T]), "inline order differs from the segmentation"
     assert torch.equal(yb[T:], y0[T:]), "a released row was written"
     _check(x[:T], idx[:T], g[:T], A, B, y0[:T].cpu(), ya, 1.0, f"inline order T={T}")
+
+
+@pytest.mark.parametrize("n,T,E,r", [(1, 3, 8, 16), (1, 40, 8, 16), (1, 64, 32, 12), (1, 100, 8, 16), (26, 300, 8, 16),
+                                     (26, 300, 8, 12), (26, 300, 32, 64), (1, 300, 32, 40), (1, 100, 8, 100), (1, 300, 32, 128)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_bank_that_is_not_finite_stays_with_its_rows(n, T, E, r, value):
+    """One element of one expert's B, in every launch form (few rows, rows ordered in the kernels, one
+    launch, two): y of the rows that choose it is lost in that column; all else has the bits of a bank
+    without it, and that column those of a product summed in another order, within two bf16 ulp or the
+    fp32 sums' bound on both sides."""
+    d_in, d_out, col = 72, 136, 77
+    gen = torch.Generator().manual_seed(T + r)
+    rnd = lambda std, *s: (torch.randn(s, generator=gen) * std).bfloat16().cuda()  # noqa: E731
+    idx = torch.stack([torch.randperm(E, generator=gen)[:2] for _ in range(T)]).int()
+    idx[0] = torch.tensor([3, 1], dtype=torch.int32)
+    g = torch.rand((T, 2), generator=gen) + 0.1
+    probs = [(rnd(1.0, T, d_in), rnd(0.1, E, r, d_in), rnd(0.3, E, d_out, r), rnd(1.0, T, d_out)) for _ in range(n)]
+    grp = dlm.SgmmGroup(probs, E, r, 1.0)
+    y0 = [p[3].clone() for p in probs]
+    grp.run(idx.cuda(), g.cuda())
+    torch.cuda.synchronize()
+    want = [p[3].clone() for p in probs]
+    at = n - 1
+    x, A, B, y = probs[at]
+    B[3, col, r - 1] = value
+    for p, t in zip(probs, y0):
+        p[3].copy_(t)
+    grp.run(idx.cuda(), g.cuda())
+    torch.cuda.synchronize()
+    for k in range(n - 1):
+        assert torch.equal(probs[k][3], want[k])
+    mine = (idx == 3).any(1).cuda()
+    assert not torch.isfinite(y[mine, col]).any()
+    rest = torch.arange(d_out) != col
+    assert torch.equal(y[:, rest], want[at][:, rest])
+    a, b = y[~mine, col].double(), want[at][~mine, col].double()
+    # the sum of magnitudes of a row's terms, and both sides' fp32 sums over ranks (hi and lo) and columns
+    Bf = B[:, col].double().abs()
+    Bf[3] = 0
+    S = torch.stack([(x.double().abs() @ A[e].double().abs().t()) @ Bf[e] for e in range(E)], 1)
+    S = (S.gather(1, idx.cuda().long()) * g.cuda().double()).sum(1)[~mine] + y0[at][~mine, col].double().abs()
+    ulp = 2.0 ** -7 * b.abs()
+    assert ((a - b).abs() <= ulp + 2 * (d_in + 4 * r + 8) * 2.0 ** -24 * S).all()
