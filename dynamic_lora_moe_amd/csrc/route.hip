@@ -665,12 +665,12 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteArgs a) {
     }
 }
 
-template <typename T, int L, int V, int NT>
-hipError_t launch_one(RouteArgs a, bool grad, hipStream_t s) {
+template <bool GRAD, typename T, int L, int V, int NT>
+hipError_t launch_one(RouteArgs a, hipStream_t s) {
     constexpr int TPB = NT / L;
     const int64_t blocks = (a.T + TPB - 1) / TPB;
     if (!grid_fits(blocks, NT)) return hipErrorInvalidConfiguration;
-    if (grad) {
+    if constexpr (GRAD) {
         const size_t lds = (size_t)TPB * (L * V * 8 + a.k * 20);
         hipLaunchKernelGGL((route_grad_kernel<T, L, V, NT>), dim3((unsigned)blocks), dim3(NT), lds, s, a);
     } else {
@@ -713,26 +713,29 @@ hipError_t launch_one(RouteArgs a, bool grad, hipStream_t s) {
 // of up to 64 experts always take 8, for the rows' smaller share of a workgroup's LDS:
 // 65536 rows of 60 experts 11.5 us against 16.2.
 constexpr int64_t kRouteFewLanes = 2 * 1024 * kWave;
-template <typename T> hipError_t launch_t(const RouteArgs& a, bool grad, hipStream_t s) {
-    const auto eight = [&](int lanes) {
-        return grad ? a.E <= 64 || a.T * lanes <= kRouteFewLanes : a.k <= 8 && a.T * lanes <= kRouteFewLanes;
-    };
-    if (a.E <= 8) return launch_one<T, 1, 8, 64>(a, grad, s);
-    if (a.E <= 16) return launch_one<T, 1, 16, 64>(a, grad, s);
-    if (a.E <= 32) return eight(4) ? launch_one<T, 4, 8, 128>(a, grad, s) : launch_one<T, 2, 16, 128>(a, grad, s);
-    if (a.E <= 64) return eight(8) ? launch_one<T, 8, 8, 128>(a, grad, s) : launch_one<T, 4, 16, 128>(a, grad, s);
-    if (a.E <= 128) return eight(16) ? launch_one<T, 16, 8, 256>(a, grad, s) : launch_one<T, 8, 16, 256>(a, grad, s);
-    if (a.E <= 256) return eight(32) ? launch_one<T, 32, 8, 256>(a, grad, s) : launch_one<T, 16, 16, 256>(a, grad, s);
-    return launch_one<T, 32, 16, 256>(a, grad, s);
+template <bool GRAD, typename T> hipError_t launch_t(const RouteArgs& a, hipStream_t s) {
+    const auto eight = [&](int lanes) { return (GRAD || a.k <= 8) && a.T * lanes <= kRouteFewLanes; };
+    if (a.E <= 8) return launch_one<GRAD, T, 1, 8, 64>(a, s);
+    if (a.E <= 16) return launch_one<GRAD, T, 1, 16, 64>(a, s);
+    if constexpr (GRAD) {
+        if (a.E <= 32) return launch_one<GRAD, T, 4, 8, 128>(a, s);
+        if (a.E <= 64) return launch_one<GRAD, T, 8, 8, 128>(a, s);
+    } else {
+        if (a.E <= 32) return eight(4) ? launch_one<GRAD, T, 4, 8, 128>(a, s) : launch_one<GRAD, T, 2, 16, 128>(a, s);
+        if (a.E <= 64) return eight(8) ? launch_one<GRAD, T, 8, 8, 128>(a, s) : launch_one<GRAD, T, 4, 16, 128>(a, s);
+    }
+    if (a.E <= 128) return eight(16) ? launch_one<GRAD, T, 16, 8, 256>(a, s) : launch_one<GRAD, T, 8, 16, 256>(a, s);
+    if (a.E <= 256) return eight(32) ? launch_one<GRAD, T, 32, 8, 256>(a, s) : launch_one<GRAD, T, 16, 16, 256>(a, s);
+    return launch_one<GRAD, T, 32, 16, 256>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) {
-    return dtype == 0 ? launch_t<float>(a, false, s) : launch_t<uint16_t>(a, false, s);
+    return dtype == 0 ? launch_t<false, float>(a, s) : launch_t<false, uint16_t>(a, s);
 }
 hipError_t launch_route_grad(const RouteArgs& a, int dtype, hipStream_t s) {
-    return dtype == 0 ? launch_t<float>(a, true, s) : launch_t<uint16_t>(a, true, s);
+    return dtype == 0 ? launch_t<true, float>(a, s) : launch_t<true, uint16_t>(a, s);
 }
 
 }  // namespace dlm

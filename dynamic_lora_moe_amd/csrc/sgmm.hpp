@@ -116,8 +116,7 @@ hipError_t launch_sgmm(const SgmmArgs& a, int dtype, hipStream_t s);
 // Ap[e][k / 8][rho][0..8) = A[e][rho][k..k+8) for k = 0, 8, ..., d_in - 8 (bf16).
 hipError_t launch_sgmm_pack_a(const void* A, void* Ap, int E, int r, int64_t d_in, hipStream_t s);
 
-// The shrink of every problem of a segmented batch (bf16; with its K-slice sum
-// above kSgmmFoldRank).
+// The shrink of every problem of a segmented batch (bf16, ranks below kGradListRank).
 hipError_t launch_sgmm_shrink(const SgmmArgs& a, hipStream_t s);
 hipError_t launch_sgmm_vsum(const SgmmArgs& a, hipStream_t s);  // the K-slice sum alone
 bool sgmm_launches_fit(const SgmmArgs& a, int dtype);

@@ -615,12 +615,9 @@ hipError_t launch_grad_zero(const SgGradArgs& a, int dtype, hipStream_t s) {
 hipError_t launch_grad_shrink(const SgGradArgs& a, hipStream_t s) {
     const int n_ch = rank_chunks(a.G.L);
     const dim3 g((unsigned)list_blocks(a));
-    switch (outer_r16(a.G.L)) {
-        case 1: hipLaunchKernelGGL(grad_shrink_list<1>, g, dim3(256), 0, s, a, n_ch); break;
-        case 2: hipLaunchKernelGGL(grad_shrink_list<2>, g, dim3(256), 0, s, a, n_ch); break;
-        case 3: hipLaunchKernelGGL(grad_shrink_list<3>, g, dim3(256), 0, s, a, n_ch); break;
-        default: hipLaunchKernelGGL(grad_shrink_list<4>, g, dim3(256), 0, s, a, n_ch); break;
-    }
+    static_assert(kGradListRank > 32, "ranks padded to 48 at least");
+    if (outer_r16(a.G.L) == 3) hipLaunchKernelGGL(grad_shrink_list<3>, g, dim3(256), 0, s, a, n_ch);
+    else hipLaunchKernelGGL(grad_shrink_list<4>, g, dim3(256), 0, s, a, n_ch);
     return hipGetLastError();
 }
 
