@@ -253,6 +253,58 @@ def test_infinities_stay_with_their_row_and_rank(i):
     assert torch.equal(torch.isfinite(c.dB[0]).all(1).cpu(), want)
 
 
+@pytest.mark.parametrize("r", [4, 16, 24, 64, 100])
+def test_coefficients_keep_every_bit_of_fp32(r):
+    """One row an expert, x and dy a single power of two, the banks powers of two: u and w are exact, and
+    s g w and s g u are gates of 24 significant bits.  Three bf16 terms hold those whole and add up without a
+    rounding, so dA and dB are exact (two terms would be 2^-17 of an element off in most of them)."""
+    E = T = 32
+    d = 72
+    gen = torch.Generator().manual_seed(r)
+    row = torch.arange(T)
+
+    def pow2(*s):
+        return torch.exp2(torch.randint(-2, 3, s, generator=gen).float()) * (2 * torch.randint(0, 2, s, generator=gen) - 1)
+
+    x, dy = torch.zeros(T, d), torch.zeros(T, d)
+    x[row, torch.randint(0, d, (T,), generator=gen)] = pow2(T)
+    dy[row, torch.randint(0, d, (T,), generator=gen)] = pow2(T)
+    A, B = pow2(E, r, d), pow2(E, d, r)
+    idx = torch.stack([torch.randperm(E, generator=gen), torch.full((T,), -1)], 1).int()
+    g = torch.rand((T, 2), generator=gen) / 2 + 0.5
+    up = lambda t: t.bfloat16().cuda()  # noqa: E731
+    dA, dB = torch.empty((E, r, d), device="cuda"), torch.empty((E, d, r), device="cuda")
+    grp = dlm.SgmmGroup([(up(x), up(A), up(B), up(torch.zeros(T, d)))], E, r, 1.0)
+    grp.bind_grads([up(dy)], None, [dA], [dB])
+    grp.backward(idx.cuda(), g.cuda())
+    torch.cuda.synchronize()
+    _, wA, wB, _ = ref.backward(x, idx, g, A, B, dy, 1.0)[0]
+    assert torch.equal(dA.cpu().double(), wA) and torch.equal(dB.cpu().double(), wB)
+
+
+@pytest.mark.parametrize("T,r", [(300, 16), (300, 64), (600, 16)])
+def test_bank_gradients_are_nearer_than_two_terms_would_be(T, r):
+    """The norms of dA and dB against the plain form's, u and w being sums of eight products.  An element is
+    the sum of n = T / 4 slots: with 7 roundings of u or w, 2 of the coefficient and n of the sum, each 2^-24 /
+    sqrt(3) in the root mean square, fp32 leaves sqrt(n + 9) times that, at most 2^-21.1 of the norm.  A two-term
+    form worked out here leaves more than the 2^-20 that is allowed."""
+    c = Case(T, [(8, 8)], 8, r, BF, seed=T + r, empty=0.0, both=0.0).bind()
+    c.run()
+    out, _ = c.refs()[0]
+    x, A, B, dy = (t[0].double() for t in (c.x, c.A, c.B, c.dy))
+    two = [torch.zeros_like(A), torch.zeros_like(B)]
+    for t in range(T):
+        for k in (0, 1):
+            e, s = int(c.idx[t, k]), c.scale * float(c.g[t, k])
+            for grad, co, row in ((two[0], s * (dy[t] @ B[e]), x[t]), (two[1], s * (A[e] @ x[t]), dy[t])):
+                hi = co.bfloat16().double()
+                co = hi + (co - hi).bfloat16().double()
+                grad[e] += torch.outer(co, row) if grad is two[0] else torch.outer(row, co)
+    for got, want, short in ((c.dA[0], out[1], two[0]), (c.dB[0], out[2], two[1])):
+        assert (got.cpu().double() - want).norm() <= 2.0 ** -20 * want.norm()
+        assert (short - want).norm() > 2.0 ** -20 * want.norm()
+
+
 @pytest.mark.parametrize("dtype,E,r,T,shape", [(BF, 8, 16, 100, (64, 64)), (BF, 8, 64, 100, (72, 200)), (BF, 8, 128, 100, (64, 72)),
                                                (BF, 32, 16, 300, (64, 136)), (BF, 32, 64, 300, (64, 64)), (BF, 32, 5, 300, (64, 2056)),
                                                (BF, 12, 100, 200, (64, 72)), (F32, 8, 6, 100, (40, 33))])
