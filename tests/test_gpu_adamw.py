@@ -390,6 +390,39 @@ def test_calls_with_another_device_current(monkeypatch):
     assert opt.status() == (0, dlm.DLM_OK)
 
 
+@pytest.mark.parametrize("n,shift", [(1, 0), (2, 1), (255, 1), (256, 0), (1000, 0), (1001, 3), (70001, 2), (70001, 0), (70004, 0)])
+def test_read_back_of_every_element(n, shift):
+    """Codes of every kind with scales from 1e-40 to 1e20 beside one another, sizes and places that end inside
+    four elements: each value to one fp32 rounding of its own, on guarded outputs too."""
+    gen = torch.Generator().manual_seed(n + shift)
+    nb = -(-n // 256)
+    put = lambda t: _place(t, shift)[0]  # noqa: E731
+    st = (put(torch.randint(-127, 128, (n,), generator=gen).to(torch.int8)),
+          put(torch.randint(0, 256, (n,), generator=gen).to(torch.uint8)),
+          put(10.0 ** (torch.rand(nb, generator=gen) * 60 - 40)), put(10.0 ** (torch.rand(nb, generator=gen) * 60 - 40)))
+    rm, rv = ref.decode(*[x.cpu().numpy() for x in st])
+    outs = [_place(torch.zeros(n), shift) for _ in range(2)]
+    for mo, vo in (dlm.adamw_read_state(*st), dlm.adamw_read_state(*st, m_out=outs[0][0], v_out=outs[1][0])):
+        assert (np.abs(_f64(mo) - rm) <= U * np.abs(rm) + 2.0 ** -149).all()
+        assert (np.abs(_f64(vo) - rv) <= U * rv + 2.0 ** -149).all()
+    for v, buf in outs:
+        assert (buf[:16 + shift] == 3).all() and (buf[16 + shift + n:] == 3).all()
+
+
+def test_moments_read_back_after_steps_element_by_element():
+    """What steps over blocks from 1e15 down to 1e-18 leave, read back: m and v each to one rounding."""
+    n = 256 * 5 + 3
+    g = torch.cat([_rnd(256, k) * 10.0 ** e for k, e in enumerate((15, 3, 0, -8, -18))] + [torch.tensor([-1.0, 0.0, 2e-5])])
+    opt = dlm.AdamW([torch.zeros(n, device="cuda")], [g.cuda()], state_bits=8, seed=5)
+    for _ in range(3):
+        opt.step(1e-3)
+        mo, vo = opt.read_state(0)
+        rm, rv = ref.decode(*[x.cpu().numpy() for x in opt.states[0]])
+        assert (np.abs(_f64(mo) - rm) <= U * np.abs(rm) + 2.0 ** -149).all()
+        assert (np.abs(_f64(vo) - rv) <= U * rv + 2.0 ** -149).all()
+        assert (np.sign(rm) == np.sign(g.double().numpy()))[rm != 0].all() and (rm != 0).mean() > 0.9
+
+
 def test_refusals_of_the_binding():
     p, g = torch.zeros(10, device="cuda"), torch.zeros(10, device="cuda")
     with pytest.raises(ValueError):
