@@ -197,3 +197,51 @@ def test_status_of_calls_without_rows(dirty_workspaces):
     idx, g = torch.zeros((8, 2), dtype=torch.int32, device="cuda"), torch.zeros((8, 2), device="cuda")
     for call in (grp.run, grp.backward):
         assert dlm.sgmm_status(call(idx, g, T=0)) == dlm.DLM_OK
+
+
+@pytest.mark.parametrize("how", ["graph", "stream"])
+def test_the_composed_step_replayed_or_on_another_stream(how):
+    """AdapterTraining's own step, router products included: replays with eager work between them, or calls on a
+    stream of their own, equal eager calls bit for bit."""
+    T, E, r, d = 200, 8, 16, 128
+    shapes = [(64, d), (136, d), (d, 136)]
+    res = []
+    for other in (False, True):
+        gen = torch.Generator().manual_seed(7)
+        rnd = lambda std, *s: (torch.randn(s, generator=gen) * std).bfloat16().cuda()  # noqa: E731
+        proj = [(rnd(1.0, T, i), rnd(0.1, E, r, i), rnd(0.1, E, o, r), rnd(1.0, T, o)) for o, i in shapes]
+        dys, dxs = [rnd(1.0, T, o) for o, _ in shapes], [rnd(1.0, T, i) for _, i in shapes]
+        x_r, W_r, dx_r = rnd(1.0, T, d), rnd(0.3, d, E), rnd(1.0, T, d)
+        counts = torch.zeros(E, dtype=torch.int32, device="cuda")
+        tr = AdapterTraining(proj, (x_r, W_r), dys, dxs, E, r, 1.5, dx_r=dx_r, counts=counts, state_bits=8, seed=3)
+
+        def step():
+            tr.forward()
+            tr.backward()
+            tr.step(1e-2)
+
+        torch.cuda.synchronize()
+        stream = torch.cuda.Stream()
+        if other and how == "stream":
+            with torch.cuda.stream(stream):
+                for _ in range(4):
+                    step()
+        elif other:
+            with torch.cuda.stream(stream):
+                step()
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+            for _ in range(3):
+                graph.replay()
+                torch.cuda.synchronize()
+                torch.zeros(5000, device="cuda").add_(1).sum()
+                torch.cuda.synchronize()
+        else:
+            for _ in range(4):
+                step()
+        torch.cuda.synchronize()
+        assert tr.status() == dlm.DLM_OK and int(counts.sum()) == 4 * 2 * T
+        res.append([*tr.opt.params, *tr.masters, *tr.opt.grads, *(p[3] for p in proj), *dxs, dx_r, tr.dg, tr.logits])
+    assert all(torch.equal(a, b) for a, b in zip(*res))
