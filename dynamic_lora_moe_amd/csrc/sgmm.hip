@@ -1228,62 +1228,58 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
     };
 
     // The results in ys of the 64 columns from c0b on that are not finite, again from
-    // the row's own experts: one at a time, a lane to an element.
+    // the row's own experts: one at a time, a lane to an element.  The lane's number is
+    // opaque here, so that nothing of this is worked out, and held, outside it.
     auto own_terms = [&](int c0b) {
-        const int64_t row = i_perm ? i_perm[tile * 32 + n] : gld(perm + tile * 32 + n);
+        int at_lane = lane_id();
+        asm volatile("" : "+v"(at_lane));
+        const int m = at_lane & 31, g = at_lane >> 5;  // row and column half
+        const uint32_t eps = i_perm ? i_ep[tile * 32 + m] : gld(epk + tile * 32 + m);
+        const int f0 = (int16_t)(eps & 0xffffu), f1 = (int16_t)(eps >> 16);
+        const int64_t row = i_perm ? i_perm[tile * 32 + m] : gld(perm + tile * 32 + m);
 #pragma unroll 1
         for (int i = 0; i < 32; ++i) {
-            const int chunk = 4 * (i >> 4) + 2 * h + (i >> 3 & 1), col = c0b + 8 * chunk + (i & 7);
-            uint16_t* at = ys + y_off(n, chunk) + (i & 7);
+            const int chunk = 4 * (i >> 4) + 2 * g + (i >> 3 & 1), col = c0b + 8 * chunk + (i & 7);
+            uint16_t* at = ys + y_off(m, chunk) + (i & 7);
             if (row < 0 || col >= d_out || __builtin_isfinite(bf_to_f(*at))) continue;
             float sum = 0.f;
 #pragma unroll 1
             for (int k = 0; k < nU; ++k) {
                 const int e = s_U[k];
-                if (e0 != e && e1 != e) continue;
-#pragma unroll 1
-                for (int c = 0; c < 2 * R16; ++c) {  // eight ranks
-                    const int q = k * R16 + c / 2;
-                    if (8 * c >= r) break;
-                    u32x4 bo = {0u, 0u, 0u, 0u};
-                    if constexpr (BV == 2) {
-                        bo = ld128(B + ((int64_t)(e * R16 + c / 2) * d_out + col) * 16 + 8 * (c & 1));
-                    } else {
-                        const uint16_t* bp = B + ((int64_t)e * d_out + col) * r + 8 * c;
-                        if constexpr (BV == 1) {
-                            bo = ld128(bp);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t lo = 8 * c + 2 * j < r ? gld(bp + 2 * j) : 0u;
-                                const uint32_t hi = 8 * c + 2 * j + 1 < r ? gld(bp + 2 * j + 1) : 0u;
-                                bo[j] = lo | (hi << 16);
-                            }
-                        }
-                    }
+                if (f0 != e && f1 != e) continue;
+                auto u_of = [&](int rank) {
                     if (shared_u) {
-                        const u32x4 uh = s_u[q][0][n + 32 * (c & 1)], ul = s_u[q][1][n + 32 * (c & 1)];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            sum = fmaf(bf_lo(bo[j]), bf_lo(uh[j]) + bf_lo(ul[j]), sum);
-                            sum = fmaf(bf_hi(bo[j]), bf_hi(uh[j]) + bf_hi(ul[j]), sum);
-                        }
+                        const int q = k * R16 + rank / 16, l = m + 32 * (rank / 8 & 1);
+                        return bf_to_f(((const uint16_t*)&s_u[q][0][l])[rank & 7]) +
+                               bf_to_f(((const uint16_t*)&s_u[q][1][l])[rank & 7]);
+                    }
+                    float a0, a1;
+                    if constexpr (FOLD) {
+                        const float* vm = s_v + m * 2 * RPAD;
+                        a0 = vm[4 * ((rank / 4) ^ (m & kVX)) + rank % 4];
+                        a1 = vm[4 * (((RPAD + rank) / 4) ^ (m & kVX)) + rank % 4];
                     } else {
+                        a0 = gld(v + ((int64_t)(tile * 32 + m) * 2) * RPAD + rank);
+                        a1 = gld(v + ((int64_t)(tile * 32 + m) * 2 + 1) * RPAD + rank);
+                    }
+                    const float g0 = i_perm ? i_g[tile * 32 + m].x : gld(gpk + 2 * (tile * 32 + m));
+                    const float g1 = i_perm ? i_g[tile * 32 + m].y : gld(gpk + 2 * (tile * 32 + m) + 1);
+                    return fmaf(a.scale * g1, f1 == e ? a1 : 0.f, a.scale * g0 * (f0 == e ? a0 : 0.f));
+                };
+                if constexpr (BV == 0) {
+                    const uint16_t* bp = B + ((int64_t)e * d_out + col) * r;
 #pragma unroll 1
+                    for (int rank = 0; rank < r; ++rank) sum = fmaf(bf_to_f(gld(bp + rank)), u_of(rank), sum);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; 8 * c < r; ++c) {  // eight ranks
+                        const u32x4 bo = BV == 2 ? ld128(B + ((int64_t)(e * R16 + c / 2) * d_out + col) * 16 + 8 * (c & 1))
+                                                 : ld128(B + ((int64_t)e * d_out + col) * r + 8 * c);
+                        const int n_in = r - 8 * c;  // (BV 2: the last eight may have padding)
+#pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const int rank = 8 * c + j;
-                            if (rank >= r) break;
-                            float a0, a1;
-                            if constexpr (FOLD) {
-                                a0 = v0[4 * ((rank / 4) ^ (n & kVX)) + rank % 4];
-                                a1 = v0[4 * (((RPAD + rank) / 4) ^ (n & kVX)) + rank % 4];
-                            } else {
-                                a0 = gld(v0 + rank);
-                                a1 = gld(v1 + rank);
-                            }
-                            const float u = fmaf(c1, e1 == e ? a1 : 0.f, c0 * (e0 == e ? a0 : 0.f));
-                            const uint32_t word = j < 4 ? (j < 2 ? bo[0] : bo[1]) : (j < 6 ? bo[2] : bo[3]);
-                            sum = fmaf(j & 1 ? bf_hi(word) : bf_lo(word), u, sum);
+                            const float b = j & 1 ? bf_hi(bo[j / 2]) : bf_lo(bo[j / 2]);
+                            if (BV == 1 || j < n_in) sum = fmaf(b, u_of(8 * c + j), sum);
                         }
                     }
                 }
@@ -1367,7 +1363,7 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
 #pragma unroll
             for (int b = 0; b < 2; ++b) bad[2 * b + (i & 1)] = fmaf(acc[b][i], 0.f, bad[2 * b + (i & 1)]);
         const float any = (bad[0] + bad[1]) + (bad[2] + bad[3]);
-        if (__ballot(any != any)) own_terms(c0b);
+        if (__builtin_expect(__ballot(any != any) != 0, 0)) own_terms(c0b);
         const int col = c0b + 8 * lc;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1403,9 +1399,8 @@ __device__ __forceinline__ int64_t expand_place(const SgmmArgs& a, int64_t bid, 
     return t < n_live ? t : -1;
 }
 template <int R16, int BV>
-// (Three waves per SIMD at r % 8 == 0, which the compiler would give up for four
-// registers; the guarded loads of other ranks have always taken two.)
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BV == 1 ? 3 : 2)))
+// (Three waves per SIMD, which the compiler would give up for a few registers.)
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void sgmm_expand_bf16(SgmmArgs a) {
     const int32_t* hdr = (const int32_t*)(a.ws + a.L.hdr);
     __shared__ int32_t s_iperm[kWave];
@@ -1477,7 +1472,7 @@ union FusedLds {
     ExpandLds e;
 };
 
-template <int R16, bool PK, bool RVEC>
+template <int R16, bool PK>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void sgmm_fused_bf16(SgmmArgs a) {
     int32_t* hdr = (int32_t*)(a.ws + a.L.hdr);
@@ -1528,7 +1523,7 @@ void sgmm_fused_bf16(SgmmArgs a) {
             c = e[15] + u / e[3];
             t = u % e[3];
         }
-        expand_item<R16, RVEC ? 1 : 0>(a, c, t, -1, nullptr, nullptr, nullptr, lds.e, dep);
+        expand_item<R16, 1>(a, c, t, -1, nullptr, nullptr, nullptr, lds.e, dep);
     }
 }
 
@@ -1937,13 +1932,8 @@ hipError_t launch_expand(const SgmmArgs& a, hipStream_t s) {
 template <int R16>
 hipError_t launch_fused(const SgmmArgs& a, hipStream_t s) {
     const dim3 gf((unsigned)(8 * fused_per_xcd(a)));
-    if (a.packed) {
-        if (a.r % 8 == 0) hipLaunchKernelGGL((sgmm_fused_bf16<R16, true, true>), gf, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((sgmm_fused_bf16<R16, true, false>), gf, dim3(256), 0, s, a);
-    } else {
-        if (a.r % 8 == 0) hipLaunchKernelGGL((sgmm_fused_bf16<R16, false, true>), gf, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((sgmm_fused_bf16<R16, false, false>), gf, dim3(256), 0, s, a);
-    }
+    if (a.packed) hipLaunchKernelGGL((sgmm_fused_bf16<R16, true>), gf, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((sgmm_fused_bf16<R16, false>), gf, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -2045,7 +2035,7 @@ hipError_t launch_sgmm(const SgmmArgs& a, int dtype, hipStream_t s) {
     // expand workgroups order the rows themselves, no segmentation launch
     static_assert(kSgmmInlineRows <= kWave, "inline ordering: one row per lane");
     const bool fold = a.L.r_pad / 16 <= kExpandFoldR16;
-    const bool fused = dtype == 1 && fold && a.L.max_ks <= kSgmmFusedMaxKs && kSgmmFused > 0 &&
+    const bool fused = dtype == 1 && fold && a.r % 8 == 0 && a.L.max_ks <= kSgmmFusedMaxKs && kSgmmFused > 0 &&
                        (int64_t)a.n_prob * a.L.tiles_max >= kSgmmFusedMinPairs &&
                        (kSgmmFused > 1 || a.T > kSgmmInlineRows);
     const bool inl = !fused && dtype == 1 && a.T <= kSgmmInlineRows &&

@@ -75,7 +75,9 @@ enum { SG_ERR = 0, SG_NPOS = 1, SG_NTILES = 2 };
 // Words per XCD of the one-launch shrink + expand's work ranges.
 constexpr int kSgmmXcdWords = 16;
 // One-launch shrink + expand after the segmentation (bf16, ranks up to
-// kSgmmFoldRank): 0 off, 1 for segmented batches, 2 also for batches of up to
+// kSgmmFoldRank that are multiples of 8: the others' loads of B leave it no
+// registers, 4096 rows of a layer's seven projections at rank 12 477 us against
+// 421 in two launches): 0 off, 1 for segmented batches, 2 also for batches of up to
 // kSgmmInlineRows rows (segmented first instead of ordered in the kernels).
 #ifndef DLM_SGMM_FUSED
 #define DLM_SGMM_FUSED 2

@@ -166,6 +166,15 @@ def test_sgmm_launch_count(lib):
     assert dlm.sgmm_launches(64, 11008, 128) == 4
 
 
+def test_sgmm_launch_count_of_ranks_that_are_no_multiple_of_eight(lib):
+    """They keep separate shrink and expand launches at any number of pairs."""
+    f = lib.dlm_sgmm_launches
+    for r in (1, 4, 12, 20, 63):
+        assert f(8192, 4096, r, 1, dlm.DLM_BF16) == 3
+        assert f(64, 4096, r, 128, dlm.DLM_BF16) == 2
+        assert f(8193, 4096, r, 1, dlm.DLM_BF16) == 4
+
+
 def test_sgmm_workspace_size(lib):
     b = C.c_size_t(0)
     assert lib.dlm_sgmm_workspace_size(4096, 11008, 8, 16, 7, C.byref(b)) == dlm.DLM_OK

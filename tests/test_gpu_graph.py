@@ -345,3 +345,19 @@ def test_sgmm_one_launch_group_in_graph_matches_eager(T, n_prob):
         for k, (p, gy) in enumerate(zip(probs, got)):
             assert torch.equal(p[3], gy), (rep, k)
     grp.close()
+
+
+@pytest.mark.parametrize("T,n,r,want", [(8192, 1, 12, 3), (300, 26, 20, 3), (64, 128, 12, 2), (300, 26, 24, 2)])
+def test_sgmm_launch_count_by_rank_matches_captured_kernels(T, n, r, want):
+    """256 pairs and more: one launch for the shrink and expand at ranks that are multiples of 8 only."""
+    from test_gpu_sgmm import _problem, _sets as _sgmm_sets
+    probs = [_problem(T, 64, 72, 8, r, torch.bfloat16, 5300 + k) for k in range(n)]
+    idx, g = _sgmm_sets(T, 8, np.random.default_rng(5301))
+    idx, g = idx.cuda(), g.cuda()
+    assert dlm.sgmm_launches(T, 64, r, n) == want
+    grp = dlm.SgmmGroup(probs, 8, r, 1.0)
+    ws = grp.workspace(T)
+    grp.run(idx, g, workspace=ws)
+    assert _captured(lambda: grp.run(idx, g, workspace=ws)) == want
+    assert dlm.sgmm_status(ws) == dlm.DLM_OK
+    grp.close()
