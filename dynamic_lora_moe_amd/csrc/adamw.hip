@@ -33,8 +33,9 @@
 //
 // Measured: 322 million bf16 weights with fp32 masters and moments in 448 tensors,
 // 1.69 ms, 5.7 TB/s (a large copy reaches 4.7); one layer's 10 million 54 us; with
-// 8-bit moments 47 us, where the binary64 codes and hashes bound it as much as the
-// memory; 80 million fp32 weights with 8-bit moments 317 us, 4.0 TB/s.
+// 8-bit moments 48 us, where the binary64 codes and hashes bound it as much as the
+// memory; 80 million fp32 weights with 8-bit moments 306 us (420 with the read-back's
+// 114), 4.2 TB/s.
 //
 // An element whose new v is not finite in fp32 (a gradient that is infinite, NaN,
 // or past 1.8e19 / sqrt(1 - b2)) is left as it was, with 8-bit moments its whole

@@ -1228,8 +1228,10 @@ __device__ __forceinline__ void expand_item(const SgmmArgs& a, int64_t cgg, int 
     };
 
     // The results in ys of the 64 columns from c0b on that are not finite, again from
-    // the row's own experts: one at a time, a lane to an element.  The lane's number is
-    // opaque here, so that nothing of this is worked out, and held, outside it.
+    // the row's own experts: one at a time, a lane to an element (4096 rows of a layer's
+    // seven projections whose most chosen bank is all NaN: 4.0 ms a pass for 0.23).  The
+    // lane's number is opaque here, so that nothing of this is worked out, and held,
+    // outside it.
     auto own_terms = [&](int c0b) {
         int at_lane = lane_id();
         asm volatile("" : "+v"(at_lane));

@@ -127,10 +127,14 @@ bool sgmm_launches_fit(const SgmmArgs& a, int dtype);
 
 // From this rank on the gradients' shrink goes by the experts' slot lists, not by
 // tiles of expert pairs: a tile's bank rows then serve 128 slots of one expert, not 32
-// rows of two or more, and every row is read once per expert.  Rank 64, 4096 rows,
-// 8192 columns on either side, 16 experts: 53 us against 113; rank 128, 4096 columns,
-// 8 experts: 47 against 82; rank 64 and 64 rows: 10 against 24.  At rank 32 reading
-// the rows twice no longer pays: 4096 rows of 4096 columns 34 us against 25.
+// rows of two or more, and every row is read once per expert.  The shrink at rank 64,
+// 4096 rows, 8192 columns on either side, 16 experts: 53 us against 113; at rank 128,
+// 4096 columns, 8 experts: 47 against 82.  Whole calls at ranks 33, 40, 48, 56 and 64:
+// those 16 experts' 206, 201, 205, 239, 244 us against 258, 250, 257, 299, 303; 4096
+// rows of 4096 columns, 8 experts, 120, 120, 120, 139, 140 against 132, 132, 132, 146,
+// 146; 512 rows and 32 experts, and 64 rows and 8, are 13 to 25% shorter too.  At rank
+// 32 reading the rows twice no longer pays: the shrink of 4096 rows of 4096 columns 34
+// us against 25.
 constexpr int kGradListRank = 33;
 // Slots of one list tile.
 constexpr int kGradTile = 32;

@@ -36,10 +36,10 @@
 //
 // Measured (us)                            prep  shrink  expand  outer  sum
 //   256 rows, 4096 x 4096, 8 x rank 16        9       9       9      9    -   latency
-//   4096 rows, a 7B-shaped layer, 8 x 16     21     146     147    190   23
-//   4096 rows, 8192 x 8192, 16 x rank 64     26      53      80     84   11
-// The layer's shrink reads x and dy at 4.4 TB/s, its expand reads and writes dx at
-// 4.0 and its outer products read x and dy once per expert, 1.26 GB at 6.6 TB/s, of
+//   4096 rows, a 7B-shaped layer, 8 x 16     20     138     142    188   22
+//   4096 rows, 8192 x 8192, 16 x rank 64     26      53      79     83   11
+// The layer's shrink reads x and dy at 4.6 TB/s, its expand reads and writes dx at
+// 4.1 and its outer products read x and dy once per expert, 1.26 GB at 6.7 TB/s, of
 // which the L2s find almost nothing: a row's two experts come to it at different
 // times.  At rank 64 the bank rows' and coefficients' traffic through L2 and LDS
 // weighs as much as the memory's.

@@ -453,7 +453,8 @@ int dlm_sgmm_group_bind_grads(dlm_sgmm_group* h, const void* const* dy, void* co
  *   dA_e = s sum g w x[t]^T,  dB_e = s sum g dy[t] u^T   (over the slots with e;
  *          written whole, 0 for an expert no row chose, or with accumulate != 0 added to)
  * bf16: bf16 operands, fp32 sums; s g u and s g w enter dA and dB as three bf16
- * terms (24 bits), s g w enters dx as two.  An infinity among them becomes NaN.
+ * terms (24 bits), s g w enters dx as two.  An infinity among them, or in x or dy,
+ * may become NaN.
  * What is not finite in a bank reaches the rows that choose its expert, no others.
  * Reads the banks as they are, and refreshes the packed A copies that the
  * forward call reads on the way.  Every result is bitwise reproducible.  A set the forward call would reject leaves all of
