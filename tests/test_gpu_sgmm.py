@@ -389,3 +389,31 @@ def test_a_bank_that_is_not_finite_stays_with_its_rows(n, T, E, r, value):
     S = (S.gather(1, idx.cuda().long()) * g.cuda().double()).sum(1)[~mine] + y0[at][~mine, col].double().abs()
     ulp = 2.0 ** -7 * b.abs()
     assert ((a - b).abs() <= ulp + 2 * (d_in + 4 * r + 8) * 2.0 ** -24 * S).all()
+
+
+@pytest.mark.parametrize("n,T,E,r", [(1, 3, 8, 16), (1, 40, 8, 16), (1, 100, 8, 12), (26, 300, 8, 16), (26, 300, 32, 64), (1, 300, 32, 128)])
+def test_an_a_bank_that_is_not_finite_stays_with_its_rows(n, T, E, r):
+    """One element of one expert's A: every column of the rows that choose it, and the other rows' bits as before."""
+    gen = torch.Generator().manual_seed(T + r)
+    rnd = lambda std, *s: (torch.randn(s, generator=gen) * std).bfloat16().cuda()  # noqa: E731
+    idx = torch.stack([torch.randperm(E, generator=gen)[:2] for _ in range(T)]).int()
+    idx[0] = torch.tensor([3, 1], dtype=torch.int32)
+    g = torch.rand((T, 2), generator=gen) + 0.1
+    probs = [(rnd(1.0, T, 72), rnd(0.1, E, r, 72), rnd(0.3, E, 136, r), rnd(1.0, T, 136)) for _ in range(n)]
+    grp = dlm.SgmmGroup(probs, E, r, 1.0)
+    y0 = [p[3].clone() for p in probs]
+    grp.run(idx.cuda(), g.cuda())
+    torch.cuda.synchronize()
+    want = [p[3].clone() for p in probs]
+    probs[-1][1][3, r - 1, 70] = float("nan")
+    grp.repack()
+    for p, t in zip(probs, y0):
+        p[3].copy_(t)
+    grp.run(idx.cuda(), g.cuda())
+    torch.cuda.synchronize()
+    mine = (idx == 3).any(1).cuda()
+    for p, t in zip(probs[:-1], want):
+        assert torch.equal(p[3], t)
+    y = probs[-1][3]
+    assert not torch.isfinite(y[mine]).any()
+    assert torch.equal(y[~mine], want[-1][~mine])
