@@ -60,6 +60,10 @@ class dlm_adamw_param(C.Structure):
                 ("m_scale", C.c_void_p), ("v_scale", C.c_void_p), ("n", C.c_int64), ("weight_decay", C.c_float)]
 
 
+class dlm_balance_cfg(C.Structure):
+    _fields_ = [("k", C.c_int32), ("score", C.c_int32), ("alpha", C.c_float), ("zeta", C.c_float)]
+
+
 class dlm_adamw_cfg(C.Structure):
     _fields_ = [("lr", C.c_float), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_float)]
 
@@ -83,6 +87,9 @@ def load(path: str = LIB_PATH):
         "dlm_pregate_centroid": ([P, P, I64, I64, I32, I32, I32, P, P, P], C.c_int),
         "dlm_route": ([P, I64, P, I64, I32, I32, P, P, P, P, P], C.c_int),
         "dlm_route_backward": ([P, I64, P, P, I64, I32, I32, P, P, I64, P], C.c_int),
+        "dlm_balance_workspace_size": ([I64, I32, I32, P], C.c_int),
+        "dlm_balance": ([P, I64, P, P, I32, I64, I32, I32, P, P, P, P, P, P, C.c_size_t, P], C.c_int),
+        "dlm_balance_backward": ([P, I64, P, P, P, I32, I64, I32, I32, P, P, I32, P, I64, P], C.c_int),
         "dlm_sgmm_group_backward_workspace_size": ([P, I64, P], C.c_int),
         "dlm_sgmm_group_bind_grads": ([P, P, P, P, P], C.c_int),
         "dlm_sgmm_group_backward": ([P, P, P, P, I64, I32, P, C.c_size_t, P], C.c_int),
@@ -311,6 +318,99 @@ def route_backward(logits: torch.Tensor, idx: torch.Tensor, dg: torch.Tensor, sc
     cfg = _route_cfg(k, score, 1, 1, 1, bool(renorm), float(scale))
     _check(load().dlm_route_backward(logits.data_ptr(), ld, idx.data_ptr(), dg.data_ptr(), T, E, _dt(logits), cfg,
                                      dlogits.data_ptr(), ldd, handle), "dlm_route_backward")
+    return dlogits
+
+
+@functools.lru_cache(maxsize=64)
+def _balance_cfg(k, score, alpha, zeta):
+    if score not in _SCORES:
+        raise ValueError(f"score is one of {sorted(_SCORES)}, got {score!r}")
+    return C.byref(dlm_balance_cfg(k, _SCORES[score], alpha, zeta))
+
+
+def _sequences(offsets, device) -> int:
+    """Sequences that offsets [S + 1] int32 cut the rows into (None: one)."""
+    if offsets is None:
+        return 1
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be [sequences + 1], of at least one sequence")
+    _like(offsets, "offsets", offsets.shape, torch.int32, device)
+    return offsets.shape[0] - 1
+
+
+@functools.lru_cache(maxsize=64)
+def balance_workspace_size(T: int, E: int, n_seq: int = 1) -> int:
+    b = C.c_size_t(0)
+    _check(load().dlm_balance_workspace_size(T, E, n_seq, C.byref(b)), "dlm_balance_workspace_size")
+    return b.value
+
+
+def balance(logits: torch.Tensor, idx: torch.Tensor, score: str = "softmax", alpha: float = 1.0, zeta: float = 0.0,
+            offsets=None, loss=None, counts=None, rows=None, probs=None, workspace=None, stream=None):
+    """The balance loss of a routing: logits [T][E] (any row pitch), idx [T][k] route()'s
+    choice, offsets [S + 1] int32 the packed sequences' borders (None: one sequence) ->
+    loss [2] fp32 (alpha times the balance term, zeta times the squared log sums, both
+    means over the sequences), counts [S][E] int32 and rows [S] int32 (what
+    balance_backward() takes), probs [S][E] fp32 the mean scores (device)."""
+    T, E, ld = _rows(logits, "logits")
+    handle = _here(logits, stream, "logits")
+    dev = logits.device
+    if idx.dim() != 2:
+        raise ValueError("idx must be [T][k]")
+    k = idx.shape[1]
+    _like(idx, "idx", (T, k), torch.int32, dev)
+    S = _sequences(offsets, dev)
+    cfg = _balance_cfg(k, score, float(alpha), float(zeta))
+    made = []
+
+    def out(t, name, shape, dtype):
+        if t is None:
+            made.append(t := torch.empty(shape, dtype=dtype, device=dev))
+        else:
+            _like(t, name, shape, dtype, dev)
+        return t
+
+    loss = out(loss, "loss", (2,), torch.float32)
+    counts, rows = out(counts, "counts", (S, E), torch.int32), out(rows, "rows", (S,), torch.int32)
+    probs = out(probs, "probs", (S, E), torch.float32)
+    if workspace is None:
+        made.append(workspace := torch.empty(balance_workspace_size(T, E, S), dtype=torch.uint8, device=dev))
+    _fresh(stream, *made)
+    _check(load().dlm_balance(logits.data_ptr(), ld, idx.data_ptr(), _ptr(offsets), S, T, E, _dt(logits), cfg,
+                              loss.data_ptr(), counts.data_ptr(), rows.data_ptr(), probs.data_ptr(), workspace.data_ptr(),
+                              _ws_bytes(workspace), handle), "dlm_balance")
+    return loss, counts, rows, probs
+
+
+def balance_backward(logits: torch.Tensor, counts: torch.Tensor, rows: torch.Tensor, k: int, score: str = "softmax",
+                     alpha: float = 1.0, zeta: float = 0.0, offsets=None, dloss=None, dlogits=None,
+                     accumulate: bool = False, stream=None):
+    """dLoss/dlogits [T][E] (logits' dtype; returned) of balance()'s loss, weighted by
+    dloss [2] fp32 (None: 1, 1), from its counts [S][E] and rows [S] for a choice of k
+    experts a row.  accumulate adds to dlogits, as to route_backward()'s; rows of no
+    sequence are left as they are (0 in a dlogits made here)."""
+    T, E, ld = _rows(logits, "logits")
+    handle = _here(logits, stream, "logits")
+    dev = logits.device
+    S = _sequences(offsets, dev)
+    _like(counts, "counts", (S, E), torch.int32, dev)
+    _like(rows, "rows", (S,), torch.int32, dev)
+    if dloss is not None:
+        _like(dloss, "dloss", (2,), torch.float32, dev)
+    if dlogits is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dlogits to add to")
+        make = torch.empty if offsets is None else torch.zeros
+        dlogits, ldd = make((T, E), dtype=logits.dtype, device=dev), max(E, 1)
+        _fresh(stream, dlogits)
+    else:
+        Td, Ed, ldd = _rows(dlogits, "dlogits")
+        if (Td, Ed) != (T, E) or dlogits.dtype != logits.dtype or dlogits.device != dev:
+            raise ValueError("dlogits must have logits' shape, dtype and device")
+    cfg = _balance_cfg(k, score, float(alpha), float(zeta))
+    _check(load().dlm_balance_backward(logits.data_ptr(), ld, counts.data_ptr(), rows.data_ptr(), _ptr(offsets), S, T, E,
+                                       _dt(logits), cfg, _ptr(dloss), 1 if accumulate else 0, dlogits.data_ptr(), ldd,
+                                       handle), "dlm_balance_backward")
     return dlogits
 
 

@@ -176,6 +176,52 @@ int dlm_route(const void* logits, int64_t ld, const float* bias, int64_t T, int3
 int dlm_route_backward(const void* logits, int64_t ld, const int32_t* idx, const float* dg, int64_t T, int32_t E,
                        int32_t dtype, const dlm_route_cfg* cfg, void* dlogits, int64_t ldd, void* stream);
 
+/*
+ * The router's balance loss over packed sequences, with the counts it steers by.
+ * Rows offsets[q] .. offsets[q + 1] - 1 are sequence q (offsets [n_seq + 1] int32 on
+ * the device, not decreasing, within [0, T]; NULL: all T rows are one sequence).
+ *   p      softmax(l) over the available experts of the row, or sigmoid(l) over its
+ *          sum there; a logit of -inf or NaN marks an expert that is not available,
+ *          as for dlm_route, and a row without any (padding) belongs to nothing
+ *   and per sequence, over its n rows that have an expert:
+ *   counts [n_seq][E] int32: the slots of idx [T][k] that name expert e (entries
+ *          outside [0, E), or that name an expert not available, are empty)
+ *   rows   [n_seq] int32: n
+ *   probs  [n_seq][E] fp32: the mean of p_e
+ *   loss   [2] fp32: alpha * mean over the sequences of sum_e f_e probs_e with
+ *          f_e = E counts_e / (k n), which is alpha for a balanced router, and
+ *          zeta * mean over the sequences of the mean of (log sum_e exp l_e)^2
+ * A sequence without rows counts as 0 in both means.  zeta must be 0 for sigmoid
+ * scores.  Everything is written, not added to; also for T = 0.  p is fp32, its sums
+ * binary64; bitwise reproducible.  Two launches, no allocation.
+ * workspace: >= dlm_balance_workspace_size(T, E, n_seq) bytes, 256-byte aligned, of
+ * any content.
+ */
+#define DLM_MAX_BALANCE_SEQS 65536
+typedef struct {
+    int32_t k;     /* slots of a row of idx: 1 .. DLM_MAX_ROUTE_K */
+    int32_t score; /* dlm_score */
+    float alpha, zeta;
+} dlm_balance_cfg;
+int dlm_balance_workspace_size(int64_t T, int32_t E, int32_t n_seq, size_t* bytes);
+int dlm_balance(const void* logits, int64_t ld, const int32_t* idx, const int32_t* offsets, int32_t n_seq, int64_t T,
+                int32_t E, int32_t dtype, const dlm_balance_cfg* cfg, float* loss, int32_t* counts, int32_t* rows,
+                float* probs, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The gradient of loss[0] dloss[0] + loss[1] dloss[1] (dloss [2] fp32 on the device,
+ * NULL = 1, 1) with the counts held constant: dlogits [T] rows of E (dtype, ldd
+ * elements apart) are written, or with accumulate != 0 added to (it joins
+ * dlm_route_backward's), rounded once.  Rows of no sequence are left as they are;
+ * padding rows and experts not available get 0.  counts and rows are dlm_balance's,
+ * or their sums over several processes' batches (the loss is then that of the joint
+ * batch, and the processes' gradients add up to its).  One launch, no allocation.
+ * T = 0 enqueues nothing.
+ */
+int dlm_balance_backward(const void* logits, int64_t ld, const int32_t* counts, const int32_t* rows, const int32_t* offsets,
+                         int32_t n_seq, int64_t T, int32_t E, int32_t dtype, const dlm_balance_cfg* cfg, const float* dloss,
+                         int32_t accumulate, void* dlogits, int64_t ldd, void* stream);
+
 /* ------------------------------------------------------------ fused switch */
 
 /* One adapted weight and its expert bank. */
