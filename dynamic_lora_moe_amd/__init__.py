@@ -68,6 +68,19 @@ class dlm_adamw_cfg(C.Structure):
     _fields_ = [("lr", C.c_float), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_float)]
 
 
+class dlm_muon_param(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("master", C.c_void_p), ("m", C.c_void_p), ("count", C.c_int64),
+                ("rows", C.c_int64), ("cols", C.c_int64), ("weight_decay", C.c_float), ("scale", C.c_float)]
+
+
+MAX_MUON_STEPS = 10
+
+
+class dlm_muon_cfg(C.Structure):
+    _fields_ = [("lr", C.c_float), ("momentum", C.c_double), ("nesterov", C.c_int32), ("eps", C.c_float), ("steps", C.c_int32),
+                ("coefs", C.c_double * 3 * MAX_MUON_STEPS)]
+
+
 _lib = None
 
 
@@ -98,6 +111,10 @@ def load(path: str = LIB_PATH):
         "dlm_adamw_step": ([P, P, P, P, P], C.c_int),
         "dlm_adamw_status": ([P, P, P, P], C.c_int),
         "dlm_adamw_read_state": ([P, P, P, P, I64, P, P, P], C.c_int),
+        "dlm_muon_create": ([P, I32, I32, I32, P], C.c_int),
+        "dlm_muon_destroy": ([P], C.c_int),
+        "dlm_muon_step": ([P, P, P, P, P], C.c_int),
+        "dlm_muon_status": ([P, P, P], C.c_int),
         "dlm_layers_create": ([P, I32, I32, I32, F, I32, P], C.c_int),
         "dlm_layers_destroy": ([P], C.c_int),
         "dlm_switch": ([P, P, P, P, P, P], C.c_int),
@@ -857,3 +874,104 @@ def adamw_read_state(m, v, m_scale, v_scale, m_out=None, v_out=None, stream=None
     _check(load().dlm_adamw_read_state(_p(m), _p(v), _p(m_scale), _p(v_scale), n, _p(m_out), _p(v_out), handle),
            "dlm_adamw_read_state")
     return m_out, v_out
+
+
+# ---- Muon -------------------------------------------------------------------------
+
+class Muon:
+    """Momentum orthogonalised by Newton-Schulz products, over the matrices of many
+    tensors at once (params updated in place).
+
+    params / grads: device tensors of one dtype each (fp32 or bf16) of two or more
+    dimensions; the last two are a matrix, what is before them counts matrices (a bank
+    [E][r][d] holds one per expert).  The smaller side is at most 512.
+    masters: per parameter an fp32 copy that the step updates (a bf16 parameter then
+    becomes its rounding), or None.  states: per parameter its momentum, fp32 of the
+    parameter's shape; zeros are made when None.
+    steps, coefs: the products X <- a X + (b A + c A^2) X, (a, b, c) for all or one triple
+    per step.  scale: the update's factor: "shape" = sqrt(max(1, rows / cols)), "rms" =
+    0.2 sqrt(max(rows, cols)) (an entry's size then is about AdamW's), a number, or one
+    per parameter.  weight_decay: one value, or one per parameter."""
+
+    def __init__(self, params, grads, masters=None, states=None, momentum: float = 0.95, nesterov: bool = True,
+                 weight_decay=0.0, eps: float = 1e-7, steps: int = 5, coefs=(3.4445, -4.7750, 2.0315), scale="shape"):
+        self.params, self.grads = list(params), list(grads)
+        n = len(self.params)
+        if not n or len(self.grads) != n:
+            raise ValueError("one gradient per parameter, at least one parameter")
+        self.masters = [None] * n if masters is None else list(masters)
+        each = lambda v: list(v) if isinstance(v, (list, tuple)) else [v] * n  # noqa: E731
+        wd, scales = each(weight_decay), each(scale)
+        if states is None:
+            states = [torch.zeros(p.shape, device=p.device) for p in self.params]
+            if self.params[0].is_cuda:  # steps may run on any stream
+                torch.cuda.current_stream(self.params[0].device).synchronize()
+        self.states = list(states)
+        if not len(self.masters) == len(wd) == len(scales) == len(self.states) == n:
+            raise ValueError("one master (or None), weight decay, scale and state per parameter")
+        if not 1 <= int(steps) <= MAX_MUON_STEPS:
+            raise ValueError(f"steps is 1 to {MAX_MUON_STEPS}, got {steps}")
+        triples = [coefs] * int(steps) if not isinstance(coefs[0], (list, tuple)) else list(coefs)
+        if len(triples) != steps or any(len(t) != 3 for t in triples):
+            raise ValueError("coefs is one (a, b, c), or one for each step")
+        p0, g0 = self.params[0], self.grads[0]
+        arr = (dlm_muon_param * n)()
+        for k, (p, g, w, m) in enumerate(zip(self.params, self.grads, self.masters, self.states)):
+            if p.dim() < 2:
+                raise ValueError(f"parameter {k} is no matrix: it has {p.dim()} dimension(s)")
+            _like(p, f"parameter {k}", p.shape, p0.dtype, p0.device)
+            _like(g, f"gradient {k}", p.shape, g0.dtype, p0.device)
+            _like(m, f"state {k}", p.shape, torch.float32, p0.device)
+            if w is not None:
+                _like(w, f"master {k}", p.shape, torch.float32, p0.device)
+            rows, cols = p.shape[-2:]
+            count = p.numel() // (rows * cols) if p.numel() else 0
+            arr[k] = dlm_muon_param(p.data_ptr(), g.data_ptr(), None if w is None else w.data_ptr(), m.data_ptr(), count,
+                                    rows, cols, float(wd[k]), self._scale(scales[k], rows, cols))
+        _here(p0, None, "parameter 0")
+        h = C.c_void_p()
+        _check(load().dlm_muon_create(arr, n, _dt(p0), _dt(g0), C.byref(h)), "dlm_muon_create")
+        self._h = h
+        self.device = p0.device
+        self._cfg = dlm_muon_cfg(0.0, float(momentum), 1 if nesterov else 0, float(eps), int(steps))
+        for k, t in enumerate(triples):
+            for j in range(3):
+                self._cfg.coefs[k][j] = float(t[j])
+
+    @staticmethod
+    def _scale(scale, rows, cols) -> float:
+        if scale == "shape":
+            return max(1.0, rows / max(cols, 1)) ** 0.5
+        if scale == "rms":
+            return 0.2 * max(rows, cols) ** 0.5
+        if isinstance(scale, str):
+            raise ValueError(f"scale is 'shape', 'rms' or a number, got {scale!r}")
+        return float(scale)
+
+    def step(self, lr: float, lr_scale=None, grad_scale=None, stream=None):
+        """One step.  lr_scale / grad_scale: optional fp32 [1] device tensors that
+        multiply lr / the gradients, read when the step runs."""
+        handle = _here(self.params[0], stream, "parameter 0")
+        for t, name in ((lr_scale, "lr_scale"), (grad_scale, "grad_scale")):
+            if t is not None:
+                _like(t, name, (1,), torch.float32, self.device)
+        self._cfg.lr = float(lr)
+        _check(load().dlm_muon_step(self._h, C.byref(self._cfg), _ptr(lr_scale), _ptr(grad_scale), handle), "dlm_muon_step")
+
+    def status(self, stream=None) -> int:
+        """DLM_OK, or DLM_EDEVICE if some matrix was not finite (and was left unchanged); clears the error."""
+        handle = _here(self.params[0], stream, "parameter 0")
+        code = C.c_int32(0)
+        _check(load().dlm_muon_status(self._h, C.byref(code), handle), "dlm_muon_status")
+        return code.value
+
+    def close(self):
+        if getattr(self, "_h", None):
+            _check(load().dlm_muon_destroy(self._h), "dlm_muon_destroy")
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001
+            pass

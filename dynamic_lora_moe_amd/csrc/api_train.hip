@@ -1,15 +1,35 @@
-// Host side of the C ABI, continued: the balance loss.
+// Host side of the C ABI, continued: the balance loss and the orthogonalised momentum step.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <cstring>
+#include <new>
+#include <utility>
 #include <vector>
 
 #include "api.hpp"
 #include "balance.hpp"
 #include "dlm.h"
+#include "muon.hpp"
 #include "route.hpp"
 
 using namespace dlm;
+
+// --------------------------------------------------------------- handles ----
+
+struct dlm_muon {
+    void* d_tables = nullptr;  // descriptors, work tables, error word
+    void* d_work = nullptr;    // scratch of a step
+    int32_t* d_err = nullptr;
+    int32_t p_dtype = 0, g_dtype = 0;
+    struct Class {
+        int nb;
+        MuonArgs args;
+    };
+    std::vector<Class> classes;
+    MuonArgs big{};
+    int64_t big_elems = 0;  // of the largest tensor with big matrices
+};
 
 extern "C" {
 
@@ -130,6 +150,313 @@ int dlm_balance_backward(const void* logits, int64_t ld, const int32_t* counts, 
     a.vec_out = aligned16(dlogits) && ldd % w == 0 && E % w == 0;
     const hipError_t e = launch_balance_grad(a, dtype, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "balance_backward launch");
+    return ok();
+}
+
+// -------------------------------------------------------------------- muon ----
+
+int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, int32_t g_dtype, dlm_muon** out) {
+    static_assert(kMuonMaxSide == DLM_MAX_MUON_SIDE && kMuonMaxSteps == DLM_MAX_MUON_STEPS, "muon limits");
+    if (!out) return fail(DLM_EINVAL, "muon_create: out is null");
+    *out = nullptr;
+    if (!params || n < 1 || n > (1 << 20)) return fail(DLM_EINVAL, "muon_create: bad tensor list (n=%d)", n);
+    if (!valid_dtype(p_dtype) || !valid_dtype(g_dtype))
+        return fail(DLM_EDTYPE, "muon_create: unknown dtype (p %d, g %d)", p_dtype, g_dtype);
+    const size_t ps = esize(p_dtype), gs = esize(g_dtype);
+    dlm_muon* h = nullptr;
+    std::vector<char> blob;
+    size_t work = 0;
+    // where a class's or the big matrices' tables and scratch lie: offsets until the memory is there
+    struct Slot {
+        size_t items, mats, part, pm, bad;
+    };
+    std::vector<Slot> slots;
+    size_t descs_at = 0, err_at = 0, big_at = 0, big_items = 0, big_pair = 0, big_sum = 0, big_sump = 0, big_mul = 0, big_mula = 0,
+           big_out = 0, big_outa = 0, big_part = 0, big_sq = 0, big_meta = 0, big_bad = 0;
+    std::vector<size_t> u_at;
+    try {
+        h = new dlm_muon();
+        std::vector<MuDesc> descs(n);
+        std::vector<Span> v;
+        std::vector<int> nbs(n);
+        u_at.assign(n, 0);
+        for (int i = 0; i < n; ++i) {
+            const dlm_muon_param& q = params[i];
+            MuDesc& d = descs[i];
+            const auto bad = [&](int rc) {
+                delete h;
+                return rc;
+            };
+            if (q.rows < 1 || q.cols < 1 || q.count < 0 || q.rows > kMaxDim || q.cols > kMaxDim || q.count > kMaxDim ||
+                (double)q.rows * (double)q.cols * (double)q.count > (double)((int64_t)1 << 40))
+                return bad(fail(DLM_ESHAPE, "muon_create: tensor %d: %lld matrices of %lld x %lld", i, (long long)q.count,
+                                (long long)q.rows, (long long)q.cols));
+            const bool wide = q.rows <= q.cols;
+            const int64_t side = wide ? q.rows : q.cols, elems = q.count * q.rows * q.cols;
+            if (side > kMuonMaxSide)
+                return bad(fail(DLM_ESHAPE, "muon_create: tensor %d: the smaller side of %lld x %lld is above %d", i,
+                                (long long)q.rows, (long long)q.cols, kMuonMaxSide));
+            if (elems > 0 && (!q.p || !q.g || !q.m)) return bad(fail(DLM_EINVAL, "muon_create: tensor %d: null pointer", i));
+            if (q.master && p_dtype == DLM_F32)
+                return bad(fail(DLM_EINVAL, "muon_create: tensor %d: an fp32 parameter has no master", i));
+            if (!std::isfinite(q.weight_decay) || !std::isfinite(q.scale))
+                return bad(fail(DLM_EINVAL, "muon_create: tensor %d: weight_decay or scale is not finite", i));
+            if ((uintptr_t)q.p % ps || (uintptr_t)q.g % gs || (uintptr_t)q.m % 4 || (uintptr_t)q.master % 4)
+                return bad(fail(DLM_EALIGN, "muon_create: tensor %d: a pointer is not a multiple of its element's size", i));
+            d = MuDesc{};
+            d.p = q.p;
+            d.g = q.g;
+            d.master = q.master;
+            d.m = q.m;
+            d.d = wide ? q.cols : q.rows;
+            d.n = (int32_t)side;
+            d.wide = wide ? 1 : 0;
+            d.count = q.count;
+            d.vec = q.cols % 4 == 0 && (uintptr_t)q.p % (4 * ps) == 0 && (uintptr_t)q.g % (4 * gs) == 0 &&
+                    (uintptr_t)q.m % 16 == 0 && (uintptr_t)q.master % 16 == 0;
+            d.wd = q.weight_decay;
+            d.scale = q.scale;
+            nbs[i] = side <= 16 ? 1 : side <= 32 ? 2 : side <= kMuonTileSide ? 4 : 0;
+            const int chunk = muon_chunk(nbs[i] ? nbs[i] : 4);
+            if ((d.d + chunk - 1) / chunk > (1 << 30)) return bad(fail(DLM_ESHAPE, "muon_create: tensor %d: too long", i));
+            d.chunks = (int32_t)((d.d + chunk - 1) / chunk);
+            v.push_back(span(q.p, elems * ps, true, "p", i));
+            v.push_back(span(q.g, elems * gs, false, "g", i));
+            v.push_back(span(q.m, (size_t)elems * 4, true, "m", i));
+            if (q.master) v.push_back(span(q.master, (size_t)elems * 4, true, "master", i));
+        }
+        Span a, b;
+        if (write_conflict(std::move(v), &a, &b)) {
+            delete h;
+            return conflict_fail("muon_create", a, b);
+        }
+        const auto table = [&](size_t bytes) {
+            const size_t at = blob.size();
+            blob.resize((at + bytes + 255) & ~(size_t)255);
+            return at;
+        };
+        const auto put32 = [&](const std::vector<int32_t>& t) {
+            const size_t at = table(t.size() * 4 + 4);
+            if (!t.empty()) std::memcpy(blob.data() + at, t.data(), t.size() * 4);
+            return at;
+        };
+        const auto scratch = [&](size_t bytes) {
+            const size_t at = work;
+            work = (at + bytes + 255) & ~(size_t)255;
+            return at;
+        };
+        err_at = table(4);
+        // tensors by their small side: one set of launches each, one after the other, on the same scratch
+        size_t shared = 0;
+        for (int nb : {1, 2, 4}) {
+            int64_t items = 0, mats = 0;
+            std::vector<int32_t> item_desc, mat_desc;
+            for (int i = 0; i < n; ++i) {
+                MuDesc& d = descs[i];
+                if (nbs[i] != nb || d.count == 0) continue;
+                d.item0 = items;
+                d.mat0 = mats;
+                items += d.count * d.chunks;
+                mats += d.count;
+                if (!grid_fits(items, 256) || !grid_fits(mats, nb * nb * 64)) {
+                    delete h;
+                    return fail(DLM_ESHAPE, "muon_create: the sizes need a launch grid of more than 2^32 - 1 work-items");
+                }
+                item_desc.insert(item_desc.end(), (size_t)(d.count * d.chunks), i);
+                mat_desc.insert(mat_desc.end(), (size_t)d.count, i);
+            }
+            if (!mats) continue;
+            dlm_muon::Class c{nb, MuonArgs{}};
+            c.args.items = items;
+            c.args.mats = mats;
+            Slot s;
+            s.items = put32(item_desc);
+            s.mats = put32(mat_desc);
+            work = 0;
+            s.part = scratch((size_t)items * muon_part(nb) * 8);
+            s.pm = scratch((size_t)mats * nb * nb * 256 * 8);
+            s.bad = scratch((size_t)mats * 4);
+            shared = std::max(shared, work);
+            h->classes.push_back(c);
+            slots.push_back(s);
+        }
+        std::vector<MuBig> bigs;
+        std::vector<int32_t> ti, tp, ts, tsp, tm, tma, to, toa;
+        int64_t off = 0;
+        work = 0;
+        for (int i = 0; i < n; ++i) {
+            MuDesc& d = descs[i];
+            if (nbs[i] || d.count == 0) continue;
+            ti.push_back(i);
+            if (ti.size() > 65535) {
+                delete h;
+                return fail(DLM_ESHAPE, "muon_create: more than 65535 tensors of a smaller side above %d", kMuonTileSide);
+            }
+            const int nb = (d.n + 63) / 64 * 4, groups = nb / 4, pairs = groups * (groups + 1) / 2;
+            if (!grid_fits((int64_t)tp.size() + d.count * d.chunks * pairs, 256)) {
+                delete h;
+                return fail(DLM_ESHAPE, "muon_create: the sizes need a launch grid of more than 2^32 - 1 work-items");
+            }
+            h->big_elems = std::max(h->big_elems, d.count * d.n * d.d);
+            for (int64_t m = 0; m < d.count; ++m) {
+                const int32_t at = (int32_t)bigs.size();
+                bigs.push_back(MuBig{i, nb, m, (int64_t)tp.size(), off});
+                off += (int64_t)nb * nb * 256;
+                tp.insert(tp.end(), (size_t)d.chunks * pairs, at);
+                for (int p = 0; p < pairs; ++p) {
+                    ts.push_back(at);
+                    tsp.push_back(p);
+                }
+                for (int blk = 0; blk < nb * nb; blk += 4) {
+                    tm.push_back(at);
+                    tma.push_back(blk);
+                }
+                for (int o = 0; o < d.chunks * groups; ++o) {
+                    to.push_back(at);
+                    toa.push_back(o);
+                }
+            }
+        }
+        if (!bigs.empty()) {
+            MuonArgs& g = h->big;
+            g.n_big = (int64_t)bigs.size();
+            g.items = (int64_t)ti.size();
+            g.n_pair = (int64_t)tp.size();
+            g.n_sum = (int64_t)ts.size();
+            g.n_mul = (int64_t)tm.size();
+            g.n_out = (int64_t)to.size();
+            g.sq = off;
+            big_at = table(bigs.size() * sizeof(MuBig));
+            std::memcpy(blob.data() + big_at, bigs.data(), bigs.size() * sizeof(MuBig));
+            big_items = put32(ti);
+            big_pair = put32(tp);
+            big_sum = put32(ts);
+            big_sump = put32(tsp);
+            big_mul = put32(tm);
+            big_mula = put32(tma);
+            big_out = put32(to);
+            big_outa = put32(toa);
+            big_part = scratch((size_t)g.n_pair * kMuonBigPart * 8);
+            big_sq = scratch((size_t)off * 6 * 8);
+            big_meta = scratch((size_t)g.n_big * 16);
+            big_bad = scratch((size_t)g.n_big * 4);
+            for (int i : ti) u_at[i] = scratch((size_t)(descs[i].count * descs[i].n * descs[i].d) * 4);
+        }
+        work = std::max(work, shared);
+        descs_at = table(sizeof(MuDesc) * n);
+        hipError_t e = hipSuccess;
+        if (work) e = hipMalloc(&h->d_work, work);
+        if (e == hipSuccess) e = hipMalloc(&h->d_tables, blob.size());
+        for (int i = 0; i < n; ++i)
+            if (!nbs[i] && descs[i].count) descs[i].u = (float*)((char*)h->d_work + u_at[i]);
+        std::memcpy(blob.data() + descs_at, descs.data(), sizeof(MuDesc) * n);
+        if (e == hipSuccess) e = hipMemcpy(h->d_tables, blob.data(), blob.size(), hipMemcpyHostToDevice);
+        if (e == hipSuccess) e = prepare_muon();
+        if (e != hipSuccess) {
+            if (h->d_work) (void)hipFree(h->d_work);
+            if (h->d_tables) (void)hipFree(h->d_tables);
+            delete h;
+            return hip_fail(e, "muon_create");
+        }
+    } catch (const std::bad_alloc&) {
+        if (h) {
+            if (h->d_work) (void)hipFree(h->d_work);
+            if (h->d_tables) (void)hipFree(h->d_tables);
+            delete h;
+        }
+        return fail(DLM_ENOMEM, "muon_create: host allocation failed");
+    }
+    const auto t32 = [&](size_t at) { return (int32_t*)((char*)h->d_tables + at); };
+    const auto w = [&](size_t at) { return (char*)h->d_work + at; };
+    h->p_dtype = p_dtype;
+    h->g_dtype = g_dtype;
+    h->d_err = t32(err_at);
+    for (size_t k = 0; k < slots.size(); ++k) {
+        MuonArgs& a = h->classes[k].args;
+        a.descs = (const MuDesc*)t32(descs_at);
+        a.item_desc = t32(slots[k].items);
+        a.mat_desc = t32(slots[k].mats);
+        a.part = (double*)w(slots[k].part);
+        a.pm = (double*)w(slots[k].pm);
+        a.bad = (int32_t*)w(slots[k].bad);
+        a.err = h->d_err;
+    }
+    if (h->big.n_big) {
+        MuonArgs& a = h->big;
+        a.descs = (const MuDesc*)t32(descs_at);
+        a.big = (const MuBig*)t32(big_at);
+        a.item_desc = t32(big_items);
+        a.pair_big = t32(big_pair);
+        a.sum_big = t32(big_sum);
+        a.sum_pair = t32(big_sump);
+        a.mul_big = t32(big_mul);
+        a.mul_at = t32(big_mula);
+        a.out_big = t32(big_out);
+        a.out_at = t32(big_outa);
+        a.part = (double*)w(big_part);
+        a.square = (double*)w(big_sq);
+        a.meta = (double*)w(big_meta);
+        a.bad = (int32_t*)w(big_bad);
+        a.err = h->d_err;
+    }
+    *out = h;
+    return ok();
+}
+
+int dlm_muon_destroy(dlm_muon* h) {
+    if (!h) return fail(DLM_EINVAL, "muon_destroy: null handle");
+    const hipError_t e = hipDeviceSynchronize();
+    if (h->d_work) (void)hipFree(h->d_work);
+    (void)hipFree(h->d_tables);
+    delete h;
+    if (e != hipSuccess) return hip_fail(e, "muon_destroy");
+    return ok();
+}
+
+int dlm_muon_step(dlm_muon* h, const dlm_muon_cfg* c, const float* lr_scale, const float* grad_scale, void* stream) {
+    if (!h || !c) return fail(DLM_EINVAL, "muon_step: null argument");
+    if (!std::isfinite(c->lr)) return fail(DLM_EINVAL, "muon_step: lr is not finite");
+    if (!(c->momentum >= 0.0 && c->momentum < 1.0)) return fail(DLM_EINVAL, "muon_step: momentum=%g not in [0, 1)", c->momentum);
+    if (!(c->eps > 0.f) || !std::isfinite(c->eps)) return fail(DLM_EINVAL, "muon_step: eps=%g is not positive", c->eps);
+    if (c->steps < 1 || c->steps > DLM_MAX_MUON_STEPS)
+        return fail(DLM_EINVAL, "muon_step: steps=%d not in [1, %d]", c->steps, DLM_MAX_MUON_STEPS);
+    for (int k = 0; k < c->steps; ++k)
+        for (int j = 0; j < 3; ++j)
+            if (!std::isfinite(c->coefs[k][j])) return fail(DLM_EINVAL, "muon_step: coefficient %d of step %d is not finite", j, k);
+    if ((uintptr_t)lr_scale % 4 || (uintptr_t)grad_scale % 4) return fail(DLM_EALIGN, "muon_step: a pointer is not a multiple of 4");
+    const auto set = [&](MuonArgs& a) {
+        a.beta = c->momentum;
+        a.lr = c->lr;
+        a.eps = c->eps;
+        a.nesterov = c->nesterov ? 1 : 0;
+        a.steps = c->steps;
+        std::memcpy(a.coefs, c->coefs, sizeof a.coefs);
+        a.lr_scale = lr_scale;
+        a.grad_scale = grad_scale;
+    };
+    for (const dlm_muon::Class& k : h->classes) {
+        MuonArgs a = k.args;
+        set(a);
+        const hipError_t e = launch_muon(a, k.nb, h->p_dtype, h->g_dtype, (hipStream_t)stream);
+        if (e != hipSuccess) return hip_fail(e, "muon_step launch");
+    }
+    if (h->big.n_big) {
+        MuonArgs a = h->big;
+        set(a);
+        const hipError_t e = launch_muon_big(a, h->big_elems, h->p_dtype, h->g_dtype, (hipStream_t)stream);
+        if (e != hipSuccess) return hip_fail(e, "muon_step launch");
+    }
+    return ok();
+}
+
+int dlm_muon_status(dlm_muon* h, int32_t* code, void* stream) {
+    if (!h || !code) return fail(DLM_EINVAL, "muon_status: null argument");
+    int32_t err = 0;
+    hipError_t e = hipStreamSynchronize((hipStream_t)stream);
+    if (e == hipSuccess) e = hipMemcpy(&err, h->d_err, sizeof err, hipMemcpyDeviceToHost);
+    if (e == hipSuccess && err) e = hipMemset(h->d_err, 0, sizeof err);
+    if (e != hipSuccess) return hip_fail(e, "muon_status");
+    *code = err ? DLM_EDEVICE : DLM_OK;
     return ok();
 }
 

@@ -1,0 +1,703 @@
+// One step of momentum orthogonalised by Newton-Schulz products, over many matrices:
+//   m <- b m + (1 - b) g,  u = b m + (1 - b) g (or m)
+//   X = u / (|u| + eps), K times X <- a X + (b A + c A^2) X with A = X X^T
+//   w <- w (1 - lr wd) - lr s X
+//
+// Every factor of the K products is a polynomial of one Gram matrix, G = u u^T over
+// the small side n of a matrix n x d (u^T u for the other way round: the same X): with
+//   Q = a + b G + c G^2,  P <- Q P,  G <- Q G Q     X = P u / (|u| + eps)
+// u is read twice, not 2 K times, and what lies between is n x n.  Squaring u loses
+// its weak directions in fp32 (a direction 10^-4 of the strongest is 10^-8 of G, and
+// each of the K steps makes it, and its error, a^2 = 12 times larger): G, P and the
+// sums are binary64, on the binary64 matrix instructions, whose products of fp32
+// values are exact.  At rank 16 they cost a tenth of the memory's time.
+//
+// Launches per class of matrices (small sides up to 16, 32, 64): the Gram matrices of
+// pieces of the long side, the n x n steps (a workgroup per matrix, a wave per 16 x 16
+// block), and the product with the update.  A symmetric block's accumulators are its
+// operands of the next product: entry (4 v + l / 16, l % 16) in register v of lane l is
+// also what an operand wants there.  The product takes four neighbouring elements of u
+// per lane and access, with the order of rows or columns within a tile (which the
+// sum does not see) chosen so that each lane's results are the elements it loaded.
+//
+// Small sides from 65 to 512 (routers of many experts): the same with 64 x 64 tiles, u
+// in scratch memory, and a launch per n x n product.
+//
+// A matrix whose u is not finite is left as it was, momentum too, and the handle's
+// error word is set.
+#include <utility>
+
+#include "gfx950.hpp"
+#include "internal.hpp"
+#include "muon.hpp"
+
+namespace dlm {
+
+namespace {
+
+constexpr int kNT = 256;
+constexpr int kWaves = kNT / kWave;
+
+typedef double d4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ d4 mfma(double a, double b, d4 c) { return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0); }
+
+__device__ __forceinline__ float load1(const float* p) { return gld(p); }
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf_to_f(gld(p)); }
+__device__ __forceinline__ void store1(float* p, float f) { gst(p, f); }
+__device__ __forceinline__ void store1(uint16_t* p, float f) { gst(p, f_to_bf(f)); }
+
+__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
+    const u32x4 r = ld128(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(r[j]);
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float (&f)[4]) {
+    const u32x2 r = gld((const u32x2*)p);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        f[2 * j] = bf_lo(r[j]);
+        f[2 * j + 1] = bf_hi(r[j]);
+    }
+}
+__device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
+    st128(p, u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])});
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
+    gst((u32x2*)p, u32x2{pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3])});
+}
+// Four neighbours of which nv are inside (vec: all or none), 0 for the others.
+template <typename T> __device__ __forceinline__ void read4(const T* p, int64_t i, int nv, bool vec, float (&f)[4]) {
+    if (vec && nv >= 4) {
+        load4(p + i, f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = !vec && j < nv ? load1(p + i + j) : 0.f;
+    }
+}
+template <typename T> __device__ __forceinline__ void write4(T* p, int64_t i, int nv, bool vec, const float (&f)[4]) {
+    if (vec && nv >= 4) {
+        store4(p + i, f);
+    } else if (!vec) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < nv) store1(p + i + j, f[j]);
+    }
+}
+
+// The momentum's step: fp32, as it is stored.
+struct Mom {
+    float b, r, gs;
+    bool nesterov;
+    __device__ __forceinline__ explicit Mom(const MuonArgs& a)
+        : b((float)a.beta), r((float)(1.0 - a.beta)), gs(a.grad_scale ? gld(a.grad_scale) : 1.f), nesterov(a.nesterov != 0) {}
+    __device__ __forceinline__ float m(float m0, float g) const { return fmaf(b, m0, r * (g * gs)); }
+    __device__ __forceinline__ float u(float m1, float g) const { return nesterov ? fmaf(b, m1, r * (g * gs)) : m1; }
+};
+
+// Where an element of the matrix at `base` lies.
+struct Place {
+    int64_t base, d;
+    int n;
+    bool wide, vec;
+    __device__ __forceinline__ Place(const MuDesc& D, int64_t mat) : base(mat * D.n * D.d), d(D.d), n(D.n), wide(D.wide != 0), vec(D.vec != 0) {}
+    __device__ __forceinline__ int64_t at(int i, int64_t j) const { return wide ? base + i * d + j : base + j * n + i; }
+};
+
+// ---- u --------------------------------------------------------------------------------
+
+// From the gradient and the momentum,
+template <typename G> struct FromState {
+    const G* g;
+    const float* m;
+    Mom mom;
+    __device__ __forceinline__ void get4(int64_t i, int nv, bool vec, float (&u)[4]) const {
+        float gv[4], mv[4];
+        read4(g, i, nv, vec, gv);
+        read4(m, i, nv, vec, mv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = mom.u(mom.m(mv[j], gv[j]), gv[j]);
+    }
+    __device__ __forceinline__ float get1(int64_t i, bool in) const {
+        const float gv = in ? load1(g + i) : 0.f, mv = in ? gld(m + i) : 0.f;
+        return mom.u(mom.m(mv, gv), gv);
+    }
+};
+// or from the scratch where a launch has left it.
+struct FromScratch {
+    const float* u;
+    __device__ __forceinline__ void get4(int64_t i, int nv, bool vec, float (&f)[4]) const { read4(u, i, nv, vec, f); }
+    __device__ __forceinline__ float get1(int64_t i, bool in) const { return in ? gld(u + i) : 0.f; }
+};
+
+// ---- Gram matrices of pieces ------------------------------------------------------------
+
+// Operands of one wave's share of columns [lo, hi) of the long side, for NB blocks of the
+// small side from i0 on, handed to `use(a)` four columns at a time.  Wide: a lane loads
+// four neighbours of its row; tall: the small side is contiguous, and a wave's lanes are.
+template <int NB, int S, typename SRC, typename F>
+__device__ __forceinline__ void long_side(const SRC& src, const Place& q, const int (&i0)[NB], int64_t lo, int64_t hi, F use) {
+    const int lane = lane_id();
+    if (q.wide) {
+        const int row = lane % 16, sub = 4 * (lane / 16);
+        for (int64_t j0 = lo + wave_id() * 16 * S; j0 < hi; j0 += kWaves * 16 * S) {
+            float u[NB][S][4];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const int64_t j = j0 + 16 * s + sub;
+                    const int i = i0[b] + row;
+                    const int64_t left = hi - j;
+                    const int nv = i < q.n && left > 0 ? (left < 4 ? (int)left : 4) : 0;
+                    src.get4(q.at(i, j), nv, q.vec, u[b][s]);
+                }
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    double a[NB];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) a[b] = (double)u[b][s][c];
+                    use(a);
+                }
+        }
+    } else {
+        const int col = lane % 16, sub = lane / 16;
+        for (int64_t j0 = lo + wave_id() * 16 * S; j0 < hi; j0 += kWaves * 16 * S) {
+            float u[NB][4 * S];
+#pragma unroll
+            for (int k = 0; k < 4 * S; ++k)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const int64_t j = j0 + 4 * k + sub;
+                    const int i = i0[b] + col;
+                    u[b][k] = src.get1(q.at(i, j), i < q.n && j < hi);
+                }
+#pragma unroll
+            for (int k = 0; k < 4 * S; ++k) {
+                double a[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) a[b] = (double)u[b][k];
+                use(a);
+            }
+        }
+    }
+}
+
+// Adds the waves' tiles, in their order, and stores them: tile t, register v, lane l at
+// out[256 t + 64 v + l].
+template <int N> __device__ __forceinline__ void store_tiles(const d4 (&acc)[N], double* s, double* out) {
+    const int lane = lane_id(), w = wave_id();
+#pragma unroll
+    for (int k = 1; k < kWaves; ++k) {
+        if (w == k) {
+#pragma unroll
+            for (int t = 0; t < N; ++t)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    double* p = s + 256 * t + 64 * v + lane;
+                    *p = k == 1 ? acc[t][v] : *p + acc[t][v];
+                }
+        }
+        __syncthreads();
+    }
+    if (w == 0) {
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) gst(out + 256 * t + 64 * v + lane, acc[t][v] + s[256 * t + 64 * v + lane]);
+    }
+}
+
+// One workgroup: one piece of one matrix; its blocks on and above the diagonal.
+template <int NB, typename G> __global__ __launch_bounds__(kNT) void muon_gram(MuonArgs a) {
+    constexpr int T = NB * (NB + 1) / 2, S = NB == 1 ? 4 : NB == 2 ? 2 : 1;
+    __shared__ double s_sum[T * 256];
+    const MuDesc D = a.descs[gld(a.item_desc + blockIdx.x)];
+    const int64_t local = (int64_t)blockIdx.x - D.item0;
+    const Place q(D, local / D.chunks);
+    const int64_t lo = local % D.chunks * muon_chunk(NB), end = lo + muon_chunk(NB), hi = end < q.d ? end : q.d;
+    const FromState<G> src{(const G*)D.g, D.m, Mom(a)};
+    int i0[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) i0[b] = 16 * b;
+    d4 acc[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[t] = d4{0.0, 0.0, 0.0, 0.0};
+    long_side<NB, S>(src, q, i0, lo, hi, [&](const double (&u)[NB]) {
+        int t = 0;
+#pragma unroll
+        for (int bi = 0; bi < NB; ++bi)
+#pragma unroll
+            for (int bj = bi; bj < NB; ++bj, ++t) acc[t] = mfma(u[bi], u[bj], acc[t]);
+    });
+    store_tiles(acc, s_sum, a.part + (int64_t)blockIdx.x * muon_part(NB));
+}
+
+// ---- the n x n steps ----------------------------------------------------------------------
+
+// Of block (bi, bj), element (row, col) as register v of lane l: (4 v + l / 16, l % 16).
+__device__ __forceinline__ bool on_diagonal(int v, int lane) { return 4 * v + lane / 16 == lane % 16; }
+// The place of that element's mirror image in block (bj, bi).
+__device__ __forceinline__ int mirrored(int v, int lane) { return lane % 16 / 4 * 64 + lane % 16 % 4 * 16 + 4 * v + lane / 16; }
+
+// One workgroup per matrix, wave (bi, bj) with that block of every square matrix in
+// registers; the operands of products lie in LDS, block after block as they are in
+// registers (one block alone is its own operand).
+template <int NB> __global__ __launch_bounds__(NB* NB* kWave) void muon_steps(MuonArgs a) {
+    constexpr int SQ = NB * NB * 256;
+    extern __shared__ double smem[];
+    double *LG = smem, *LQ = smem + SQ, *LP = smem + 2 * SQ, *s_tr = smem + (NB > 1 ? 3 * SQ : 0);
+    const int lane = lane_id(), w = wave_id(), bi = w / NB, bj = w % NB;
+    const int64_t mat = blockIdx.x;
+    const MuDesc D = a.descs[gld(a.mat_desc + mat)];
+    // the pieces' sums, in their order
+    d4 g = {0.0, 0.0, 0.0, 0.0};
+    {
+        const int lo = bi < bj ? bi : bj, hi = bi < bj ? bj : bi;
+        const int tile = lo * NB - lo * (lo - 1) / 2 + (hi - lo);
+        const double* part = a.part + (D.item0 + (mat - D.mat0) * D.chunks) * muon_part(NB) + tile * 256;
+#pragma unroll 4
+        for (int c = 0; c < D.chunks; ++c, part += muon_part(NB))
+#pragma unroll
+            for (int v = 0; v < 4; ++v) g[v] += gld(part + (bi <= bj ? 64 * v + lane : mirrored(v, lane)));
+    }
+    // |u|^2 is the trace
+    double tr = 0.0;
+    if (bi == bj) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) tr += on_diagonal(v, lane) ? g[v] : 0.0;
+        tr = wave_sum(tr);
+    }
+    if (lane == 0 && bi == bj) s_tr[bi] = tr;
+    __syncthreads();
+    tr = 0.0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) tr += s_tr[b];
+    const double inv = 1.0 / (sqrt(tr) + (double)a.eps);
+    g *= inv * inv;
+
+    d4 eye;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) eye[v] = bi == bj && on_diagonal(v, lane) ? 1.0 : 0.0;
+    const auto put = [&](double* L, const d4& x) {
+        if constexpr (NB > 1) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) L[w * 256 + 64 * v + lane] = x[v];
+        }
+    };
+    // X Y of symmetric X, Y (all are polynomials of G): an operand's block (bi, bk) is read as (bk, bi)
+    const auto mul = [&](const double* LX, const d4& x, const double* LY, const d4& y) {
+        d4 r = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+        for (int bk = 0; bk < NB; ++bk)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                if constexpr (NB > 1)
+                    r = mfma(LX[(bk * NB + bi) * 256 + 64 * v + lane], LY[(bk * NB + bj) * 256 + 64 * v + lane], r);
+                else
+                    r = mfma(x[v], y[v], r);
+            }
+        return r;
+    };
+    const auto sync = [] {
+        if constexpr (NB > 1) __syncthreads();
+    };
+    d4 p = eye;
+    put(LG, g);
+    sync();
+    for (int k = 0; k < a.steps; ++k) {
+        const d4 s = mul(LG, g, LG, g);
+        const d4 q = a.coefs[k][0] * eye + a.coefs[k][1] * g + a.coefs[k][2] * s;
+        put(LQ, q);
+        sync();
+        p = k == 0 ? q : mul(LP, p, LQ, q);
+        if (k + 1 == a.steps) break;
+        const d4 r = mul(LG, g, LQ, q);
+        sync();  // G and P are read
+        put(LG, r);
+        put(LP, p);
+        sync();
+        g = mul(LG, r, LQ, q);
+        sync();
+        put(LG, g);
+        sync();
+    }
+    p *= inv;
+    bool fin = true;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        fin = fin && __builtin_isfinite(p[v]);
+        gst(a.pm + mat * SQ + w * 256 + 64 * v + lane, p[v]);
+    }
+    const bool ok = __syncthreads_and(fin && __builtin_isfinite(tr));
+    if (threadIdx.x == 0) {
+        gst(a.bad + mat, ok ? 0 : 1);
+        if (!ok) gst(a.err, 1);
+    }
+}
+
+// ---- the product and the update ---------------------------------------------------------
+
+// A lane's tile of 64 of the long side (16 NB of the small): wide, rows 16 b + 4 v + l / 16
+// of four columns 4 (l % 16) + c; tall, four of the small side 16 b + 4 (l / 16) + c of
+// columns 16 x + l % 16.
+struct Rate {
+    float lr, keep;
+    __device__ __forceinline__ Rate(const MuonArgs& a, const MuDesc& D) {
+        const float l = a.lr_scale ? a.lr * gld(a.lr_scale) : a.lr;
+        keep = (float)(1.0 - (double)l * (double)D.wd);
+        lr = l * D.scale;
+    }
+};
+// Four neighbours' weights from their four products.
+template <typename P>
+__device__ __forceinline__ void update4(const MuDesc& D, const Rate& r, int64_t at, int nv, bool vec, const double (&x)[4]) {
+    if (nv <= 0) return;
+    float w[4];
+    if (D.master) read4((const float*)D.master, at, nv, vec, w);
+    else read4((const P*)D.p, at, nv, vec, w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = w[j] * r.keep - r.lr * (float)x[j];
+    if (D.master) write4(D.master, at, nv, vec, w);
+    write4((P*)D.p, at, nv, vec, w);
+}
+// The lane's place of its v-th (wide) or x-th (tall) group of four in block b.
+__device__ __forceinline__ int group_at(const Place& q, int b, int k, int64_t j0, int64_t hi, int lane, int64_t* at) {
+    const int i = q.wide ? 16 * b + 4 * k + lane / 16 : 16 * b + 4 * (lane / 16);
+    const int64_t j = q.wide ? j0 + 4 * (lane % 16) : j0 + 16 * k + lane % 16;
+    *at = q.at(i, j);
+    if (i >= q.n || j >= hi) return 0;
+    const int64_t left = q.wide ? hi - j : q.n - i;
+    return left < 4 ? (int)left : 4;
+}
+// Entry of a square matrix's block that a tall product's first operand wants: row
+// sigma(l % 16), column 4 (l / 16) + k, of a symmetric block pair.
+__device__ __forceinline__ int tall_entry(int k, int lane) {
+    return lane / 16 * 64 + k * 16 + 4 * (lane % 4) + lane % 16 / 4;
+}
+
+// One workgroup: one piece of one matrix, the last first (the pieces that the Gram launch
+// read last are the likeliest to be in a cache still).
+template <int NB, typename P, typename G> __global__ __launch_bounds__(kNT) void muon_apply(MuonArgs a) {
+    __shared__ double s_p[NB > 1 ? NB * NB * 256 : 1];
+    const int64_t item = (int64_t)gridDim.x - 1 - blockIdx.x;
+    const MuDesc D = a.descs[gld(a.item_desc + item)];
+    const int64_t local = item - D.item0, index = local / D.chunks, mat = D.mat0 + index;
+    if (gld(a.bad + mat)) return;
+    const Place q(D, index);
+    const int64_t lo = local % D.chunks * muon_chunk(NB), end = lo + muon_chunk(NB), hi = end < q.d ? end : q.d;
+    const int lane = lane_id();
+    const double* pm = a.pm + mat * NB * NB * 256;
+    double own[4];
+    if constexpr (NB > 1) {
+        for (int i = threadIdx.x; i < NB * NB * 256; i += kNT) s_p[i] = gld(pm + i);
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) own[k] = gld(pm + (q.wide ? 64 * k + lane : tall_entry(k, lane)));
+    }
+    const Mom mom(a);
+    const Rate rate(a, D);
+    for (int64_t j0 = lo + wave_id() * 64; j0 < hi; j0 += kWaves * 64) {
+        float u[NB][4][4];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float g[4][4], m[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                int64_t at;
+                const int nv = group_at(q, b, k, j0, hi, lane, &at);
+                read4((const G*)D.g, at, nv, q.vec, g[k]);
+                read4((const float*)D.m, at, nv, q.vec, m[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                int64_t at;
+                const int nv = group_at(q, b, k, j0, hi, lane, &at);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    m[k][c] = mom.m(m[k][c], g[k][c]);
+                    u[b][k][c] = mom.u(m[k][c], g[k][c]);
+                }
+                write4(D.m, at, nv, q.vec, m[k]);
+            }
+        }
+#pragma unroll
+        for (int ib = 0; ib < NB; ++ib) {
+            d4 acc[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[c] = d4{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    double x;
+                    if constexpr (NB > 1) x = s_p[(kb * NB + ib) * 256 + (q.wide ? 64 * k + lane : tall_entry(k, lane))];
+                    else x = own[k];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[c] = mfma(x, (double)(q.wide ? u[kb][k][c] : u[kb][c][k]), acc[c]);
+                }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                int64_t at;
+                const int nv = group_at(q, ib, k, j0, hi, lane, &at);
+                const double x[4] = {q.wide ? acc[0][k] : acc[k][0], q.wide ? acc[1][k] : acc[k][1],
+                                     q.wide ? acc[2][k] : acc[k][2], q.wide ? acc[3][k] : acc[k][3]};
+                update4<P>(D, rate, at, nv, q.vec, x);
+            }
+        }
+    }
+}
+
+// ---- small sides above 64 -----------------------------------------------------------------
+
+// u of the big matrices' tensors, element by element.
+template <typename G> __global__ __launch_bounds__(kNT) void muon_big_u(MuonArgs a) {
+    const MuDesc D = a.descs[gld(a.item_desc + blockIdx.y)];
+    const Mom mom(a);
+    const int64_t n = D.count * D.n * D.d;
+    for (int64_t i = ((int64_t)blockIdx.x * kNT + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * kNT * 4) {
+        const int nv = n - i < 4 ? (int)(n - i) : 4;
+        float g[4], m[4], u[4];
+        read4((const G*)D.g, i, nv, D.vec != 0, g);
+        read4((const float*)D.m, i, nv, D.vec != 0, m);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = mom.u(mom.m(m[j], g[j]), g[j]);
+        write4(D.u, i, nv, D.vec != 0, u);
+    }
+}
+
+// One workgroup: one 64 x 64 of one piece's Gram matrix (rows 64 bi .., columns 64 bj .., bi <= bj).
+__device__ __forceinline__ void pair_of(int t, int groups, int* bi, int* bj) {
+    int i = 0;
+    while (t >= groups - i) t -= groups - i++;
+    *bi = i;
+    *bj = i + t;
+}
+__global__ __launch_bounds__(kNT) void muon_big_gram(MuonArgs a) {
+    __shared__ double s_sum[kMuonBigPart];
+    const MuBig B = a.big[gld(a.pair_big + blockIdx.x)];
+    const MuDesc D = a.descs[B.desc];
+    const int groups = B.nb / 4, pairs = groups * (groups + 1) / 2;
+    const int64_t local = (int64_t)blockIdx.x - B.part0;
+    int bi, bj;
+    pair_of((int)(local % pairs), groups, &bi, &bj);
+    const Place q(D, B.index);
+    const int64_t lo = local / pairs * muon_chunk(4), end = lo + muon_chunk(4), hi = end < q.d ? end : q.d;
+    const FromScratch src{D.u};
+    int i0[8];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        i0[b] = 64 * bi + 16 * b;
+        i0[4 + b] = 64 * bj + 16 * b;
+    }
+    d4 acc[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) acc[t] = d4{0.0, 0.0, 0.0, 0.0};
+    long_side<8, 1>(src, q, i0, lo, hi, [&](const double (&u)[8]) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t) acc[t] = mfma(u[t / 4], u[4 + t % 4], acc[t]);
+    });
+    store_tiles(acc, s_sum, a.part + (int64_t)blockIdx.x * kMuonBigPart);
+}
+
+// The pieces' sums of one 64 x 64, in their order, into G and its mirror image.
+__global__ __launch_bounds__(kNT) void muon_big_sum(MuonArgs a) {
+    const MuBig B = a.big[gld(a.sum_big + blockIdx.x)];
+    const MuDesc D = a.descs[B.desc];
+    const int groups = B.nb / 4, pairs = groups * (groups + 1) / 2, pair = gld(a.sum_pair + blockIdx.x);
+    int bi, bj;
+    pair_of(pair, groups, &bi, &bj);
+    double* G = a.square + B.off;
+    for (int e = threadIdx.x; e < kMuonBigPart; e += kNT) {
+        const double* part = a.part + (B.part0 + pair) * kMuonBigPart + e;
+        double s = 0.0;
+#pragma unroll 8
+        for (int c = 0; c < D.chunks; ++c, part += (int64_t)pairs * kMuonBigPart) s += gld(part);
+        const int t = e / 256, v = e / 64 % 4, lane = e % 64;
+        const int r = 4 * bi + t / 4, k = 4 * bj + t % 4;
+        gst(G + ((int64_t)r * B.nb + k) * 256 + e % 256, s);
+        if (bi != bj) gst(G + ((int64_t)k * B.nb + r) * 256 + mirrored(v, lane), s);
+    }
+}
+
+// The trace and what follows from it.
+__global__ __launch_bounds__(kNT) void muon_big_norm(MuonArgs a) {
+    __shared__ double s_tr[kWaves];
+    const MuBig B = a.big[blockIdx.x];
+    const double* G = a.square + B.off;
+    double tr = 0.0;
+    for (int i = threadIdx.x; i < 16 * B.nb; i += kNT) {
+        const int b = i / 16, r = i % 16;  // entry (r, r): register r / 4 of lane 16 (r % 4) + r
+        tr += gld(G + ((int64_t)b * B.nb + b) * 256 + r / 4 * 64 + r % 4 * 16 + r);
+    }
+    tr = wave_sum(tr);
+    if (lane_id() == 0) s_tr[wave_id()] = tr;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    tr = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) tr += s_tr[w];
+    const double inv = 1.0 / (sqrt(tr) + (double)a.eps);
+    gst(a.meta + 2 * blockIdx.x, inv);
+    gst(a.meta + 2 * blockIdx.x + 1, inv * inv);
+    const bool ok = __builtin_isfinite(tr);
+    gst(a.bad + blockIdx.x, ok ? 0 : 1);
+    if (!ok) gst(a.err, 1);
+}
+
+// Products of the square matrices, a wave per 16 x 16 block of the result.  G's factor
+// 1 / norm^2 is applied in the first step, P's 1 / norm too.
+//   MUL_S  S = G G        MUL_RP  R = G Q, and (blockIdx.y 1, or alone in the last step) P' = P Q
+//   MUL_G  G' = R Q       with Q = a + b G + c S of this step's G and S
+enum { MUL_S = 0, MUL_RP = 1, MUL_G = 2 };
+struct BigMats {
+    double *G, *S, *R, *P, *G2, *P2;
+};
+template <int MODE> __global__ __launch_bounds__(kNT) void muon_big_mul(MuonArgs a, BigMats M, int step, int only_p) {
+    const int bigi = gld(a.mul_big + blockIdx.x);
+    const MuBig B = a.big[bigi];
+    const int nb = B.nb, lane = lane_id(), block = gld(a.mul_at + blockIdx.x) + wave_id(), bi = block / nb, bj = block % nb;
+    const double f = step == 0 ? gld(a.meta + 2 * bigi + 1) : 1.0;  // G is f times what is stored
+    const double ca = a.coefs[step][0], cb = a.coefs[step][1] * f, cc = a.coefs[step][2] * f * f;
+    const auto frag = [&](const double* X, int r, int c, int v) { return gld(X + B.off + ((int64_t)r * nb + c) * 256 + 64 * v + lane); };
+    const auto q = [&](int r, int c, int v) {
+        const double d = r == c && on_diagonal(v, lane) ? ca : 0.0;
+        return d + cb * frag(M.G, r, c, v) + cc * frag(M.S, r, c, v);
+    };
+    const bool want_p = MODE == MUL_RP && (only_p || blockIdx.y == 1);
+    d4 r = {0.0, 0.0, 0.0, 0.0};
+    double* out = MODE == MUL_S ? M.S : MODE == MUL_G ? M.G2 : want_p ? M.P2 : M.R;
+    if (want_p && step == 0) {
+        const double inv = gld(a.meta + 2 * bigi);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) r[v] = inv * q(bi, bj, v);
+    } else {
+        const double* X = MODE == MUL_G ? M.R : want_p ? M.P : M.G;
+        for (int bk = 0; bk < nb; ++bk) {
+            double x[4], y[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                x[v] = frag(X, bk, bi, v);
+                y[v] = MODE == MUL_S ? frag(M.G, bk, bj, v) : q(bk, bj, v);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) r = mfma(x[v], y[v], r);
+        }
+        // (R and S keep the stored G's scale; G' takes it from R)
+        if (MODE == MUL_G) r *= f;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) gst(out + B.off + (int64_t)block * 256 + 64 * v + lane, r[v]);
+}
+
+// One workgroup: one piece's long side, 64 of the small side.
+template <typename P, typename G> __global__ __launch_bounds__(kNT) void muon_big_apply(MuonArgs a, const double* PM) {
+    const int bigi = gld(a.out_big + blockIdx.x);
+    if (gld(a.bad + bigi)) return;
+    const MuBig B = a.big[bigi];
+    const MuDesc D = a.descs[B.desc];
+    const int groups = B.nb / 4, at0 = gld(a.out_at + blockIdx.x), ob = at0 % groups, lane = lane_id();
+    const Place q(D, B.index);
+    const int64_t lo = (int64_t)(at0 / groups) * muon_chunk(4), end = lo + muon_chunk(4), hi = end < q.d ? end : q.d;
+    const Mom mom(a);
+    const Rate rate(a, D);
+    for (int64_t j0 = lo + wave_id() * 64; j0 < hi; j0 += kWaves * 64) {
+        d4 acc[4][4];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) acc[t / 4][t % 4] = d4{0.0, 0.0, 0.0, 0.0};
+        for (int kb = 0; kb < B.nb; ++kb) {
+            float u[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                int64_t at;
+                const int nv = group_at(q, kb, k, j0, hi, lane, &at);
+                read4((const float*)D.u, at, nv, q.vec, u[k]);
+            }
+#pragma unroll
+            for (int ib = 0; ib < 4; ++ib) {
+                const double* pm = PM + B.off + ((int64_t)kb * B.nb + 4 * ob + ib) * 256;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const double x = gld(pm + (q.wide ? 64 * k + lane : tall_entry(k, lane)));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[ib][c] = mfma(x, (double)(q.wide ? u[k][c] : u[c][k]), acc[ib][c]);
+                }
+            }
+        }
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                int64_t at;
+                const int nv = group_at(q, 4 * ob + ib, k, j0, hi, lane, &at);
+                float g[4], m[4];
+                read4((const G*)D.g, at, nv, q.vec, g);
+                read4((const float*)D.m, at, nv, q.vec, m);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) m[c] = mom.m(m[c], g[c]);
+                write4(D.m, at, nv, q.vec, m);
+                const double x[4] = {q.wide ? acc[ib][0][k] : acc[ib][k][0], q.wide ? acc[ib][1][k] : acc[ib][k][1],
+                                     q.wide ? acc[ib][2][k] : acc[ib][k][2], q.wide ? acc[ib][3][k] : acc[ib][k][3]};
+                update4<P>(D, rate, at, nv, q.vec, x);
+            }
+    }
+}
+
+// ---- launches ---------------------------------------------------------------------------
+
+constexpr size_t steps_lds(int nb) { return nb > 1 ? (size_t)(3 * nb * nb * 256 + nb) * 8 : 64; }
+
+template <int NB, typename P, typename G> hipError_t launch_class(const MuonArgs& a, hipStream_t s) {
+    const dim3 items((unsigned)a.items), n(kNT);
+    hipLaunchKernelGGL((muon_gram<NB, G>), items, n, 0, s, a);
+    hipLaunchKernelGGL((muon_steps<NB>), dim3((unsigned)a.mats), dim3(NB * NB * kWave), steps_lds(NB), s, a);
+    hipLaunchKernelGGL((muon_apply<NB, P, G>), items, n, 0, s, a);
+    return hipGetLastError();
+}
+template <typename P, typename G> hipError_t launch_pg(const MuonArgs& a, int nb, hipStream_t s) {
+    return nb == 1 ? launch_class<1, P, G>(a, s) : nb == 2 ? launch_class<2, P, G>(a, s) : launch_class<4, P, G>(a, s);
+}
+template <typename P, typename G> hipError_t launch_big_pg(const MuonArgs& a, int64_t u_elems, hipStream_t s) {
+    const dim3 n(kNT);
+    const int64_t ublocks = (u_elems + 4 * kNT - 1) / (4 * kNT);
+    hipLaunchKernelGGL((muon_big_u<G>), dim3((unsigned)(ublocks < 4096 ? ublocks : 4096), (unsigned)a.items), n, 0, s, a);
+    hipLaunchKernelGGL(muon_big_gram, dim3((unsigned)a.n_pair), n, 0, s, a);
+    hipLaunchKernelGGL(muon_big_sum, dim3((unsigned)a.n_sum), n, 0, s, a);
+    hipLaunchKernelGGL(muon_big_norm, dim3((unsigned)a.n_big), n, 0, s, a);
+    double* at = a.square;
+    BigMats M{at, at + a.sq, at + 2 * a.sq, at + 3 * a.sq, at + 4 * a.sq, at + 5 * a.sq};
+    const unsigned mul = (unsigned)a.n_mul;
+    for (int k = 0; k < a.steps; ++k) {
+        const bool last = k + 1 == a.steps;
+        hipLaunchKernelGGL((muon_big_mul<MUL_S>), dim3(mul), n, 0, s, a, M, k, 0);
+        hipLaunchKernelGGL((muon_big_mul<MUL_RP>), dim3(mul, last ? 1 : 2), n, 0, s, a, M, k, last ? 1 : 0);
+        if (!last) hipLaunchKernelGGL((muon_big_mul<MUL_G>), dim3(mul), n, 0, s, a, M, k, 0);
+        std::swap(M.P, M.P2);
+        std::swap(M.G, M.G2);
+    }
+    hipLaunchKernelGGL((muon_big_apply<P, G>), dim3((unsigned)a.n_out), n, 0, s, a, (const double*)M.P);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t prepare_muon() {
+    return hipFuncSetAttribute((const void*)muon_steps<4>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)steps_lds(4));
+}
+
+hipError_t launch_muon(const MuonArgs& a, int nb, int p_dtype, int g_dtype, hipStream_t s) {
+    if (!grid_fits(a.items, kNT) || !grid_fits(a.mats, nb * nb * kWave)) return hipErrorInvalidConfiguration;
+    if (p_dtype == 0) return g_dtype == 0 ? launch_pg<float, float>(a, nb, s) : launch_pg<float, uint16_t>(a, nb, s);
+    return g_dtype == 0 ? launch_pg<uint16_t, float>(a, nb, s) : launch_pg<uint16_t, uint16_t>(a, nb, s);
+}
+hipError_t launch_muon_big(const MuonArgs& a, int64_t u_elems, int p_dtype, int g_dtype, hipStream_t s) {
+    if (!grid_fits(a.n_pair, kNT) || !grid_fits(a.n_mul, kNT) || !grid_fits(a.n_out, kNT)) return hipErrorInvalidConfiguration;
+    if (p_dtype == 0) return g_dtype == 0 ? launch_big_pg<float, float>(a, u_elems, s) : launch_big_pg<float, uint16_t>(a, u_elems, s);
+    return g_dtype == 0 ? launch_big_pg<uint16_t, float>(a, u_elems, s) : launch_big_pg<uint16_t, uint16_t>(a, u_elems, s);
+}
+
+}  // namespace dlm

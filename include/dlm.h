@@ -615,6 +615,70 @@ int dlm_adamw_status(dlm_adamw* h, int64_t* step, int32_t* code, void* stream);
 int dlm_adamw_read_state(const int8_t* m, const uint8_t* v, const float* m_scale, const float* v_scale, int64_t n,
                          float* m_out, float* v_out, void* stream);
 
+/* ------------------------------------------------------------------- muon */
+
+/* One tensor of a muon step: `count` matrices, one behind the other. */
+typedef struct {
+    void* p;           /* [count][rows][cols] parameter (p_dtype), updated in place */
+    const void* g;     /* gradient (g_dtype), of the same shape */
+    float* master;     /* fp32 copy of a bf16 parameter, updated in place (the
+                          parameter becomes its rounding), or NULL */
+    float* m;          /* momentum, fp32 */
+    int64_t count, rows, cols;
+    float weight_decay;
+    float scale;       /* of the orthogonalised update */
+} dlm_muon_param;
+
+#define DLM_MAX_MUON_SIDE 512
+#define DLM_MAX_MUON_STEPS 10
+typedef struct {
+    float lr;
+    double momentum;   /* in [0, 1) */
+    int32_t nesterov;  /* 0 or 1 */
+    float eps;         /* > 0 */
+    int32_t steps;     /* 1 .. DLM_MAX_MUON_STEPS */
+    double coefs[DLM_MAX_MUON_STEPS][3]; /* a, b, c of every step */
+} dlm_muon_cfg;
+
+typedef struct dlm_muon dlm_muon;
+
+/*
+ * Register n tensors of matrices (every expert's A and B is one, a router's weight
+ * another) that one step of orthogonalised momentum updates together.  Copies the
+ * descriptors to the device and allocates a step's scratch memory; the buffers stay
+ * owned by the caller, must outlive the handle, and no written one may overlap
+ * another.  The smaller side of a matrix is at most DLM_MAX_MUON_SIDE, the other at
+ * most 2^30, and a tensor has at most 2^40 elements.  Any sizes and
+ * alignments of their element (cols a multiple of 4 and tensors aligned to four
+ * elements are faster).
+ */
+int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, int32_t g_dtype, dlm_muon** out);
+
+/* Free the handle's device memory (synchronises the device first). */
+int dlm_muon_destroy(dlm_muon* h);
+
+/*
+ * One step over every matrix of every tensor, no allocation:
+ *   g' = grad_scale g,  m <- beta m + (1 - beta) g',  u = nesterov ? beta m + (1 - beta) g' : m
+ *   X = u / (|u| + eps),  then `steps` times  X <- a X + (b A + c A^2) X,  A = X X^T
+ *   w <- w (1 - lr wd) - lr scale X
+ * with |u| the Frobenius norm, w = the master where there is one, else the parameter;
+ * lr = cfg's times *lr_scale.  lr_scale and grad_scale are DEVICE floats or NULL (1): a
+ * captured step reads them on every replay.  m and u are fp32; the products are formed
+ * on the smaller side in binary64 and X is rounded to fp32 once.
+ * A matrix whose u, or whose iterated factor, is not finite is left unchanged, momentum
+ * too, and the error word is set.  Bitwise reproducible.
+ * Launches: three for the matrices with a smaller side up to 16, three up to 32, three
+ * up to 64, and 4 + 3 steps for those above.
+ */
+int dlm_muon_step(dlm_muon* h, const dlm_muon_cfg* cfg, const float* lr_scale, const float* grad_scale, void* stream);
+
+/*
+ * Synchronise `stream`, then read and clear the error word: *code (host) = DLM_OK or
+ * DLM_EDEVICE (some matrix was not finite).
+ */
+int dlm_muon_status(dlm_muon* h, int32_t* code, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -100,3 +100,56 @@ def test_balance_by_hand():
     assert torch.allclose(probs, torch.tensor([[0.375, 0.625]], dtype=torch.float64))
     assert abs(float(loss[0]) - 1.0) < 1e-6  # f = (1, 1)
     assert abs(float(loss[1]) - (torch.log(torch.tensor(4.0)) ** 2 + torch.log(torch.tensor(2.0)) ** 2) / 2) < 1e-6
+
+
+def _muon_params(*ps):
+    arr = (dlm.dlm_muon_param * len(ps))()
+    for i, p in enumerate(ps):
+        arr[i] = dlm.dlm_muon_param(*p)
+    return arr
+
+
+@built
+def test_muon_validation():
+    lib = dlm.load()
+    h = C.c_void_p()
+    a = [FAKE + k * MB for k in range(8)]
+    fine = (a[0], a[1], None, a[2], 2, 5, 10, 0.01, 1.0)
+
+    def create(ps, n=1, pd=0, gd=0, out=True):
+        return lib.dlm_muon_create(ps, n, pd, gd, C.byref(h) if out else None)
+
+    def put(**kw):
+        names = ("p", "g", "master", "m", "count", "rows", "cols", "wd", "scale")
+        return _muon_params(tuple(kw.get(k, v) for k, v in zip(names, fine)))
+
+    assert create(None) == dlm.DLM_EINVAL and create(put(), 0) == dlm.DLM_EINVAL and create(put(), out=False) == dlm.DLM_EINVAL
+    assert create(put(), pd=3) == dlm.DLM_EDTYPE and create(put(), gd=-1) == dlm.DLM_EDTYPE
+    for k in ("p", "g", "m"):
+        assert create(put(**{k: None})) == dlm.DLM_EINVAL
+    for k, v in (("rows", 0), ("cols", 0), ("count", -1), ("rows", 1 << 31), ("cols", -5)):
+        assert create(put(**{k: v})) == dlm.DLM_ESHAPE
+    assert create(put(rows=513, cols=600)) == dlm.DLM_ESHAPE
+    assert create(put(count=1 << 29, rows=512, cols=1 << 29)) == dlm.DLM_ESHAPE
+    assert create(put(wd=float("nan"))) == dlm.DLM_EINVAL and create(put(scale=float("inf"))) == dlm.DLM_EINVAL
+    assert create(put(master=a[3])) == dlm.DLM_EINVAL  # an fp32 parameter has none
+    assert create(put(p=a[0] + 2)) == dlm.DLM_EALIGN and create(put(p=a[0] + 1), pd=1) == dlm.DLM_EALIGN
+    assert create(put(m=a[2] + 1)) == dlm.DLM_EALIGN
+    assert create(put(g=a[0])) == dlm.DLM_EINVAL and create(put(m=a[1])) == dlm.DLM_EINVAL
+    other = (a[4], a[1] + 100, None, a[2] + 396, 1, 5, 10, 0.0, 1.0)
+    assert create(_muon_params(fine, other), 2) == dlm.DLM_EINVAL and "1" in lib.dlm_last_error().decode()
+    assert h.value is None
+    cfg = dlm.dlm_muon_cfg(1e-3, 0.95, 1, 1e-7, 5)
+    assert lib.dlm_muon_step(None, C.byref(cfg), None, None, None) == dlm.DLM_EINVAL
+    assert lib.dlm_muon_destroy(None) == dlm.DLM_EINVAL and lib.dlm_muon_status(None, None, None) == dlm.DLM_EINVAL
+
+
+@pytest.mark.parametrize("shape", [(3, 8), (8, 3), (5, 5)])
+def test_muon_by_values_is_muon_by_products(shape):
+    import muon_ref
+    import numpy as np
+
+    u = np.random.default_rng(0).standard_normal(shape)
+    c = [muon_ref.COEFS] * 5
+    assert np.abs(muon_ref.by_values(u, 1e-7, c) - muon_ref.by_products(u, 1e-7, c)).max() < 1e-12
+    assert np.abs(muon_ref.by_products(u, 1e-7, c) - muon_ref.by_products(u.T, 1e-7, c).T).max() < 1e-12
