@@ -68,6 +68,11 @@ class dlm_adamw_cfg(C.Structure):
     _fields_ = [("lr", C.c_float), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_float)]
 
 
+class dlm_i8_problem(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("W", C.c_void_p), ("w_scale", C.c_void_p), ("y", C.c_void_p), ("d_in", C.c_int64),
+                ("d_out", C.c_int64)]
+
+
 class dlm_muon_param(C.Structure):
     _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("master", C.c_void_p), ("m", C.c_void_p), ("count", C.c_int64),
                 ("rows", C.c_int64), ("cols", C.c_int64), ("weight_decay", C.c_float), ("scale", C.c_float)]
@@ -111,6 +116,14 @@ def load(path: str = LIB_PATH):
         "dlm_adamw_step": ([P, P, P, P, P], C.c_int),
         "dlm_adamw_status": ([P, P, P, P], C.c_int),
         "dlm_adamw_read_state": ([P, P, P, P, I64, P, P, P], C.c_int),
+        "dlm_i8_quantize": ([P, I64, I64, I32, P, P, P], C.c_int),
+        "dlm_i8_group_create": ([P, I32, I32, P], C.c_int),
+        "dlm_i8_group_destroy": ([P], C.c_int),
+        "dlm_i8_group_workspace_size": ([P, I64, P], C.c_int),
+        "dlm_i8_group_run": ([P, I64, P, C.c_size_t, P], C.c_int),
+        "dlm_i8_group_bind_grads": ([P, P, P], C.c_int),
+        "dlm_i8_group_backward_workspace_size": ([P, I64, P], C.c_int),
+        "dlm_i8_group_backward": ([P, I64, I32, P, C.c_size_t, P], C.c_int),
         "dlm_muon_create": ([P, I32, I32, I32, P], C.c_int),
         "dlm_muon_destroy": ([P], C.c_int),
         "dlm_muon_step": ([P, P, P, P, P], C.c_int),
@@ -740,6 +753,131 @@ class SgmmGroup:
     def close(self):
         if getattr(self, "_h", None):
             _check(load().dlm_sgmm_group_destroy(self._h), "dlm_sgmm_group_destroy")
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001
+            pass
+
+
+# ---- 8-bit products -----------------------------------------------------------------
+
+def quantize_rows(x: torch.Tensor, q=None, scale=None, stream=None):
+    """Rows [T][d] as 8-bit codes and a scale each: (q [T][d] int8, scale [T] fp32), 127
+    for a row's largest magnitude.  A weight [d_out][d_in] so becomes what Int8Group takes."""
+    _need(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [T][d]")
+    handle = _here(x, stream, "x")
+    T, d = x.shape
+    own_q, own_s = q is None, scale is None
+    q = torch.empty((T, d), dtype=torch.int8, device=x.device) if own_q else q
+    scale = torch.empty(T, device=x.device) if own_s else scale
+    _like(q, "q", (T, d), torch.int8, x.device)
+    _like(scale, "scale", (T,), torch.float32, x.device)
+    _fresh(stream, q if own_q else None, scale if own_s else None)
+    _check(load().dlm_i8_quantize(_p(x), T, d, _dt(x), _p(q), _p(scale), handle), "dlm_i8_quantize")
+    return q, scale
+
+
+class Int8Group:
+    """A frozen base's products in 8 bits, many at once: y = s_x w_scale (codes of x) W^T.
+
+    problems: [(x [T][d_in], W [d_out][d_in] int8, w_scale [d_out] fp32, y [T][d_out])], x
+    and y fixed buffers of one dtype (bf16 or fp32).  W and w_scale are copied here; x is
+    coded at every run, once where problems share it.  Run it before the SgmmGroup of the
+    same problems, which adds the adapters to y."""
+
+    def __init__(self, problems):
+        problems = list(problems)
+        n = len(problems)
+        if not n:
+            raise ValueError("at least one problem")
+        x0 = problems[0][0]
+        _need(x0, "problem 0 x")
+        arr = (dlm_i8_problem * n)()
+        for k, (x, W, w_scale, y) in enumerate(problems):
+            if x.dim() != 2 or W.dim() != 2:
+                raise ValueError(f"problem {k}: x must be [T][d_in] and W [d_out][d_in]")
+            T, d_in = x.shape
+            d_out = W.shape[0]
+            _like(x, f"problem {k} x", (T, d_in), x0.dtype, x0.device)
+            _like(W, f"problem {k} W", (d_out, d_in), torch.int8, x0.device)
+            _like(w_scale, f"problem {k} w_scale", (d_out,), torch.float32, x0.device)
+            _like(y, f"problem {k} y", (T, d_out), x0.dtype, x0.device)
+            arr[k] = dlm_i8_problem(x.data_ptr(), W.data_ptr(), w_scale.data_ptr(), y.data_ptr(), d_in, d_out)
+        dt = _dt(x0)
+        _here(x0, None, "problem 0 x")
+        torch.cuda.current_stream(x0.device).synchronize()  # W is read on another stream
+        h = C.c_void_p()
+        _check(load().dlm_i8_group_create(arr, n, dt, C.byref(h)), "dlm_i8_group_create")
+        self._h = h
+        self._keep = [(x, y) for x, _, _, y in problems]
+        self.n, self.device = n, x0.device
+        self.rows = min(x.shape[0] for x, _ in self._keep)  # rows every problem holds
+        self._sizes = {}
+
+    def _size(self, T: int, what: str) -> int:
+        if (T, what) not in self._sizes:
+            b = C.c_size_t(0)
+            _check(getattr(load(), what)(self._h, T, C.byref(b)), what)
+            self._sizes[T, what] = b.value
+        return self._sizes[T, what]
+
+    def workspace(self, T: int):
+        """A workspace of run() for T rows."""
+        return torch.empty(self._size(T, "dlm_i8_group_workspace_size"), dtype=torch.uint8, device=self.device)
+
+    def backward_workspace(self, T: int):
+        """A workspace of backward() for T rows (once the buffers are bound)."""
+        return torch.empty(self._size(T, "dlm_i8_group_backward_workspace_size"), dtype=torch.uint8, device=self.device)
+
+    def _call(self, T, workspace, stream, make):
+        handle = _here(self._keep[0][0], stream, "problem 0 x")
+        T = self.rows if T is None else T
+        if not 0 <= T <= self.rows:
+            raise ValueError(f"T={T} rows, but the group's problems hold {self.rows}")
+        if workspace is None:
+            workspace = make(T)
+            _fresh(stream, workspace)
+        return handle, T, workspace
+
+    def run(self, T: int | None = None, workspace=None, stream=None):
+        """Write rows [0, T) of every y (None: every row)."""
+        handle, T, workspace = self._call(T, workspace, stream, self.workspace)
+        _check(load().dlm_i8_group_run(self._h, T, _ptr(workspace), _ws_bytes(workspace), handle), "dlm_i8_group_run")
+        return workspace
+
+    def bind_grads(self, dys, dxs):
+        """Bind the buffers of backward(): per problem dy [T][d_out] and dx [T][d_in] (the
+        problems' dtype; a None dx, or dy with it, is not wanted).  Problems that share an
+        input share its dx, which is then their sum."""
+        _here(self._keep[0][0], None, "problem 0 x")
+        dys, dxs = list(dys), list(dxs)
+        if not len(dys) == len(dxs) == self.n:
+            raise ValueError("one dy and dx (or None) per problem")
+        for k, ((x, y), dy, dx) in enumerate(zip(self._keep, dys, dxs)):
+            if dy is not None:
+                _like(dy, f"dy {k}", y.shape, x.dtype, x.device)
+            if dx is not None:
+                _like(dx, f"dx {k}", x.shape, x.dtype, x.device)
+        ptrs = lambda ts: (C.c_void_p * self.n)(*[None if t is None else t.data_ptr() for t in ts])  # noqa: E731
+        _check(load().dlm_i8_group_bind_grads(self._h, ptrs(dys), ptrs(dxs)), "dlm_i8_group_bind_grads")
+        self._grads = (dys, dxs)
+        self._sizes.clear()
+
+    def backward(self, accumulate: bool = False, T: int | None = None, workspace=None, stream=None):
+        """dx of rows [0, T) from the bound dy: written, or with accumulate added to."""
+        handle, T, workspace = self._call(T, workspace, stream, self.backward_workspace)
+        _check(load().dlm_i8_group_backward(self._h, T, 1 if accumulate else 0, _ptr(workspace), _ws_bytes(workspace), handle),
+               "dlm_i8_group_backward")
+        return workspace
+
+    def close(self):
+        if getattr(self, "_h", None):
+            _check(load().dlm_i8_group_destroy(self._h), "dlm_i8_group_destroy")
             self._h = None
 
     def __del__(self):

@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdlm.so")
 SOURCES = ["api.hip", "pregate.hip", "route.hip", "switch.hip", "sgmm.hip", "sgmm_grad.hip",
-           "adamw.hip", "api_train.hip", "balance.hip", "muon.hip"]
+           "adamw.hip", "api_train.hip", "balance.hip", "int8.hip", "muon.hip"]
 ARCH = "gfx950"
 
 FLAGS = [
@@ -29,7 +29,7 @@ def hipcc() -> str:
     return p
 
 
-def build(verbose: bool = False, jobs: int = 9) -> str:
+def build(verbose: bool = False, jobs: int = 10) -> str:
     """Compile every source to an object (in parallel) and link libdlm.so."""
     bdir = os.path.join(HERE, "_build")
     os.makedirs(bdir, exist_ok=True)

@@ -1,15 +1,18 @@
-// Host side of the C ABI, continued: the balance loss and the orthogonalised momentum step.
+// Host side of the C ABI, continued: the balance loss, the orthogonalised
+// momentum step and the 8-bit products.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 #include <cstring>
 #include <new>
+#include <set>
 #include <utility>
 #include <vector>
 
 #include "api.hpp"
 #include "balance.hpp"
 #include "dlm.h"
+#include "int8.hpp"
 #include "muon.hpp"
 #include "route.hpp"
 
@@ -29,6 +32,25 @@ struct dlm_muon {
     std::vector<Class> classes;
     MuonArgs big{};
     int64_t big_elems = 0;  // of the largest tensor with big matrices
+};
+
+// One direction of the 8-bit products: its tables on the device.
+struct I8Tables {
+    void* d = nullptr;
+    I8Args args{};
+};
+
+struct dlm_i8_group {
+    std::vector<dlm_i8_problem> probs;
+    int32_t dtype = 0;
+    char* d_w = nullptr;              // packed weights, then their scales
+    std::vector<size_t> w_at, s_at;   // of every problem
+    I8Tables fwd, bwd;
+    char* d_wt = nullptr;             // packed transposes
+    std::vector<const void*> dy;      // bound buffers
+    std::vector<void*> dx;
+    bool bound = false;
+    int64_t checked_fwd = 0, checked_bwd = 0;  // rows up to which the buffers are known not to overlap
 };
 
 extern "C" {
@@ -458,6 +480,330 @@ int dlm_muon_status(dlm_muon* h, int32_t* code, void* stream) {
     if (e != hipSuccess) return hip_fail(e, "muon_status");
     *code = err ? DLM_EDEVICE : DLM_OK;
     return ok();
+}
+
+// -------------------------------------------------------------------- int8 ----
+
+static int i8_pieces(int64_t d) { return (int)((d + 127) / 128 * 2); }
+
+int dlm_i8_quantize(const void* x, int64_t T, int64_t d, int32_t dtype, int8_t* q, float* scale, void* stream) {
+    if (T < 0 || T >= ((int64_t)1 << 31)) return fail(DLM_ESHAPE, "i8_quantize: T=%lld out of range", (long long)T);
+    if (d < 1 || d > kMaxDim) return fail(DLM_ESHAPE, "i8_quantize: d=%lld out of range", (long long)d);
+    if (!valid_dtype(dtype)) return fail(DLM_EDTYPE, "i8_quantize: unknown dtype %d", dtype);
+    if (T == 0) return ok();
+    if (!x || !q || !scale) return fail(DLM_EINVAL, "i8_quantize: null pointer");
+    if ((uintptr_t)x % esize(dtype) || (uintptr_t)scale % 4)
+        return fail(DLM_EALIGN, "i8_quantize: a pointer is not a multiple of its element's size");
+    const Span v[] = {span(x, (size_t)T * d * esize(dtype), false, "x", 0), span(q, (size_t)T * d, true, "q", 0),
+                      span(scale, (size_t)T * 4, true, "scale", 0)};
+    Span a, b;
+    if (pair_conflict(v, &a, &b)) return conflict_fail("i8_quantize", a, b);
+    const hipError_t e = launch_i8_quantize(x, T, d, dtype, q, scale, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "i8_quantize launch");
+    return ok();
+}
+
+// Copies a direction's tables to the device and fills in its arguments.
+static hipError_t i8_upload(const std::vector<I8Seg>& segs, const std::vector<I8Rows>& rows, std::vector<I8Prod>& prods, I8Tables* t) {
+    // the longest sums first: what is left at the end of a launch is short
+    std::stable_sort(prods.begin(), prods.end(), [](const I8Prod& x, const I8Prod& y) { return x.pieces > y.pieces; });
+    I8Args& a = t->args;
+    a = I8Args{};
+    a.n_rows = (int32_t)rows.size();
+    a.n_prods = (int32_t)prods.size();
+    for (I8Prod& p : prods) {
+        p.tile_big = a.tiles_big;
+        p.tile_mid = a.tiles_mid;
+        p.tile_few = a.tiles_few;
+        a.tiles_big += (int32_t)((p.d + kI8BigD - 1) / kI8BigD);
+        a.tiles_mid += (int32_t)((p.d + kI8MidD - 1) / kI8MidD);
+        a.tiles_few += (int32_t)((p.d + kI8FewD - 1) / kI8FewD);
+    }
+    for (const I8Rows& r : rows) a.pieces += r.pieces;
+    const size_t b0 = (segs.size() * sizeof(I8Seg) + 255) & ~(size_t)255, b1 = b0 + ((rows.size() * sizeof(I8Rows) + 255) & ~(size_t)255);
+    std::vector<char> blob(b1 + prods.size() * sizeof(I8Prod));
+    std::memcpy(blob.data(), segs.data(), segs.size() * sizeof(I8Seg));
+    std::memcpy(blob.data() + b0, rows.data(), rows.size() * sizeof(I8Rows));
+    std::memcpy(blob.data() + b1, prods.data(), prods.size() * sizeof(I8Prod));
+    hipError_t e = hipMalloc(&t->d, blob.size());
+    if (e == hipSuccess) e = hipMemcpy(t->d, blob.data(), blob.size(), hipMemcpyHostToDevice);
+    a.segs = (const I8Seg*)t->d;
+    a.rows = (const I8Rows*)((char*)t->d + b0);
+    a.prods = (const I8Prod*)((char*)t->d + b1);
+    return e;
+}
+
+static size_t i8_workspace(const I8Args& a, int64_t T, size_t* scale_at) {
+    const size_t t16 = (size_t)(T + 15) / 16, q = t16 * a.pieces * kI8Piece;
+    if (scale_at) *scale_at = q;
+    return (q + t16 * 16 * 4 * a.n_rows + 255) & ~(size_t)255;
+}
+
+int dlm_i8_group_create(const dlm_i8_problem* probs, int32_t n, int32_t dtype, dlm_i8_group** out) {
+    if (!out) return fail(DLM_EINVAL, "i8_group_create: out is null");
+    *out = nullptr;
+    if (!probs || n < 1 || n > 65535) return fail(DLM_EINVAL, "i8_group_create: bad problem list (n=%d)", n);
+    if (!valid_dtype(dtype)) return fail(DLM_EDTYPE, "i8_group_create: unknown dtype %d", dtype);
+    const size_t es = esize(dtype);
+    int64_t tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        const dlm_i8_problem& q = probs[i];
+        if (!q.x || !q.W || !q.w_scale || !q.y) return fail(DLM_EINVAL, "i8_group_create: problem %d: null pointer", i);
+        if (q.d_in < 1 || q.d_in > kI8MaxK)
+            return fail(DLM_ESHAPE, "i8_group_create: problem %d: d_in=%lld not in [1, %lld]", i, (long long)q.d_in, (long long)kI8MaxK);
+        if (q.d_out < 1 || q.d_out > kMaxDim)
+            return fail(DLM_ESHAPE, "i8_group_create: problem %d: d_out=%lld out of range", i, (long long)q.d_out);
+        if ((uintptr_t)q.x % es || (uintptr_t)q.y % es || (uintptr_t)q.w_scale % 4)
+            return fail(DLM_EALIGN, "i8_group_create: problem %d: a pointer is not a multiple of its element's size", i);
+        tiles += (q.d_out + kI8FewD - 1) / kI8FewD;
+    }
+    if (!grid_fits(tiles, 512))
+        return fail(DLM_ESHAPE, "i8_group_create: the sizes need a launch grid of more than 2^32 - 1 work-items");
+    dlm_i8_group* h = nullptr;
+    hipError_t e = hipSuccess;
+    try {
+        h = new dlm_i8_group();
+        h->probs.assign(probs, probs + n);
+        h->dtype = dtype;
+        size_t bytes = 0;
+        for (const dlm_i8_problem& q : h->probs) {
+            h->w_at.push_back(bytes);
+            bytes += (size_t)(q.d_out + 15) / 16 * i8_pieces(q.d_in) * kI8Piece;
+        }
+        for (const dlm_i8_problem& q : h->probs) {
+            h->s_at.push_back(bytes);
+            bytes += (size_t)(q.d_out + 15) / 16 * 64;
+        }
+        std::vector<I8Seg> segs;
+        std::vector<I8Rows> rows;
+        std::vector<I8Prod> prods;
+        int64_t q0 = 0;
+        e = hipMalloc((void**)&h->d_w, bytes);
+        for (int i = 0; i < n && e == hipSuccess; ++i) {
+            const dlm_i8_problem& q = h->probs[i];
+            const int pieces = i8_pieces(q.d_in);
+            // problems that read one x share its codes
+            int r = 0;
+            while (r < (int)rows.size() && !(segs[r].x == q.x && segs[r].d == q.d_in)) ++r;
+            if (r == (int)rows.size()) {
+                segs.push_back(I8Seg{q.x, nullptr, q.d_in, 0, aligned16(q.x) && q.d_in % (16 / (int64_t)es) == 0});
+                rows.push_back(I8Rows{r, r + 1, pieces, 0, q0, r});
+                q0 += pieces;
+            }
+            I8Prod p{};
+            p.w = (const int8_t*)h->d_w + h->w_at[i];
+            p.w_scale = (const float*)(h->d_w + h->s_at[i]);
+            p.out = q.y;
+            p.d = q.d_out;
+            p.pieces = pieces;
+            p.vec = q.d_out % 4 == 0 && (uintptr_t)q.y % (4 * es) == 0;
+            p.q0 = rows[r].q0;
+            p.rows = r;
+            prods.push_back(p);
+            e = launch_i8_pack(q.W, q.d_out, q.d_in, pieces, (int8_t*)h->d_w + h->w_at[i], nullptr);
+            if (e == hipSuccess) e = hipMemcpy(h->d_w + h->s_at[i], q.w_scale, (size_t)q.d_out * 4, hipMemcpyDeviceToDevice);
+        }
+        if (e == hipSuccess) e = i8_upload(segs, rows, prods, &h->fwd);
+        if (e == hipSuccess) e = prepare_i8();
+        if (e == hipSuccess) e = hipDeviceSynchronize();
+    } catch (const std::bad_alloc&) {
+        e = hipErrorOutOfMemory;
+    }
+    if (e != hipSuccess) {
+        if (h) {
+            if (h->d_w) (void)hipFree(h->d_w);
+            if (h->fwd.d) (void)hipFree(h->fwd.d);
+            delete h;
+        }
+        return e == hipErrorOutOfMemory ? fail(DLM_ENOMEM, "i8_group_create: an allocation failed") : hip_fail(e, "i8_group_create");
+    }
+    *out = h;
+    return ok();
+}
+
+int dlm_i8_group_destroy(dlm_i8_group* h) {
+    if (!h) return fail(DLM_EINVAL, "i8_group_destroy: null handle");
+    const hipError_t e = hipDeviceSynchronize();
+    for (void* p : {(void*)h->d_w, h->fwd.d, (void*)h->d_wt, h->bwd.d})
+        if (p) (void)hipFree(p);
+    delete h;
+    if (e != hipSuccess) return hip_fail(e, "i8_group_destroy");
+    return ok();
+}
+
+int dlm_i8_group_workspace_size(const dlm_i8_group* h, int64_t T, size_t* bytes) {
+    if (!h || !bytes) return fail(DLM_EINVAL, "i8_group_workspace_size: null argument");
+    if (T < 0 || T >= ((int64_t)1 << 31)) return fail(DLM_ESHAPE, "i8_group_workspace_size: T=%lld out of range", (long long)T);
+    *bytes = i8_workspace(h->fwd.args, T, nullptr);
+    return ok();
+}
+
+// Refuses a call whose written buffers overlap others: looked up when it has more rows than any before.
+static int i8_overlap(const char* call, dlm_i8_group* h, bool back, int64_t T, const void* ws, size_t ws_bytes) {
+    const size_t es = esize(h->dtype);
+    const int n = (int)h->probs.size();
+    const auto in = [&](int i) { return back ? span(h->dy[i], (size_t)T * h->probs[i].d_out * es, false, "dy", i)
+                                             : span(h->probs[i].x, (size_t)T * h->probs[i].d_in * es, false, "x", i); };
+    const auto out = [&](int i) { return back ? span(h->dx[i], (size_t)T * h->probs[i].d_in * es, true, "dx", i)
+                                              : span(h->probs[i].y, (size_t)T * h->probs[i].d_out * es, true, "y", i); };
+    const Span w = span(ws, ws_bytes, true, "workspace", 0);
+    for (int i = 0; i < n; ++i) {
+        if (back && !h->dx[i]) continue;
+        for (const Span& s : {in(i), out(i)})
+            if (s.hi > w.lo && w.hi > s.lo) return conflict_fail(call, w, s);
+    }
+    int64_t& checked = back ? h->checked_bwd : h->checked_fwd;
+    if (T <= checked) return DLM_OK;
+    try {
+        std::vector<Span> v;
+        std::set<const void*> shared;  // a dx that several problems share is one buffer
+        for (int i = 0; i < n; ++i) {
+            if (back && !h->dx[i]) continue;
+            v.push_back(in(i));
+            if (!back || shared.insert(h->dx[i]).second) v.push_back(out(i));
+        }
+        Span a, b;
+        if (write_conflict(std::move(v), &a, &b)) return conflict_fail(call, a, b);
+    } catch (const std::bad_alloc&) {
+        return fail(DLM_ENOMEM, "%s: host allocation failed", call);
+    }
+    checked = T;
+    return DLM_OK;
+}
+
+static int i8_launch(const char* call, dlm_i8_group* h, bool back, int64_t T, int32_t accumulate, void* workspace, size_t ws_bytes, void* stream) {
+    if (T < 0 || T >= ((int64_t)1 << 31)) return fail(DLM_ESHAPE, "%s: T=%lld out of range", call, (long long)T);
+    I8Args a = back ? h->bwd.args : h->fwd.args;
+    if (T == 0 || a.n_prods == 0) return ok();
+    size_t scale_at;
+    const size_t need = i8_workspace(a, T, &scale_at);
+    if (!workspace || ws_bytes < need)
+        return fail(DLM_EWORKSPACE, "%s: workspace of %zu bytes, %zu needed", call, workspace ? ws_bytes : (size_t)0, need);
+    if ((uintptr_t)workspace % 256) return fail(DLM_EALIGN, "%s: workspace is not 256-byte aligned", call);
+    const int rc = i8_overlap(call, h, back, T, workspace, need);
+    if (rc != DLM_OK) return rc;
+    a.T = T;
+    a.T16 = (T + 15) / 16;
+    a.q = (int8_t*)workspace;
+    a.scale = (float*)((char*)workspace + scale_at);
+    a.accumulate = accumulate ? 1 : 0;
+    hipError_t e = launch_i8_rows(a, h->dtype, (hipStream_t)stream);
+    if (e == hipSuccess) e = launch_i8_products(a, h->dtype, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, call);
+    return ok();
+}
+
+int dlm_i8_group_run(dlm_i8_group* h, int64_t T, void* workspace, size_t ws_bytes, void* stream) {
+    if (!h) return fail(DLM_EINVAL, "i8_group_run: null handle");
+    return i8_launch("i8_group_run", h, false, T, 0, workspace, ws_bytes, stream);
+}
+
+int dlm_i8_group_bind_grads(dlm_i8_group* h, const void* const* dy, void* const* dx) {
+    if (!h || !dy || !dx) return fail(DLM_EINVAL, "i8_group_bind_grads: null argument");
+    const int n = (int)h->probs.size();
+    const size_t es = esize(h->dtype);
+    for (int i = 0; i < n; ++i) {
+        if (!dx[i]) continue;
+        if (!dy[i]) return fail(DLM_EINVAL, "i8_group_bind_grads: problem %d: dx without dy", i);
+        if ((uintptr_t)dy[i] % es || (uintptr_t)dx[i] % es)
+            return fail(DLM_EALIGN, "i8_group_bind_grads: problem %d: a pointer is not a multiple of its element's size", i);
+        for (int j = 0; j < i; ++j)
+            if (dx[j] == dx[i] && h->probs[j].d_in != h->probs[i].d_in)
+                return fail(DLM_EINVAL, "i8_group_bind_grads: problems %d and %d share a dx and differ in d_in", j, i);
+    }
+    I8Tables t;
+    char* wt = nullptr;
+    hipError_t e = hipDeviceSynchronize();
+    std::vector<const void*> new_dy;
+    std::vector<void*> new_dx;
+    try {
+        new_dy.assign(dy, dy + n);
+        new_dx.assign(dx, dx + n);
+        std::vector<I8Seg> segs;
+        std::vector<I8Rows> rows;
+        std::vector<I8Prod> prods;
+        std::vector<size_t> at;
+        std::vector<std::vector<int>> of;
+        size_t bytes = 0;
+        int64_t q0 = 0;
+        for (int i = 0; i < n; ++i) {
+            if (!dx[i]) continue;
+            bool first = true;
+            for (int j = 0; j < i; ++j) first = first && dx[j] != dx[i];
+            if (!first) continue;
+            const int64_t d_in = h->probs[i].d_in;
+            const int seg0 = (int)segs.size();
+            int k0 = 0;
+            of.emplace_back();
+            for (int j = i; j < n; ++j) {
+                if (dx[j] != dx[i]) continue;
+                const int64_t d = h->probs[j].d_out;
+                if (((int64_t)k0 + (d + 63) / 64) * 64 > kI8MaxK)
+                    return fail(DLM_ESHAPE, "i8_group_bind_grads: problem %d: more than %lld output channels share its dx", j,
+                                (long long)kI8MaxK);
+                segs.push_back(I8Seg{dy[j], (const float*)(h->d_w + h->s_at[j]), d, k0,
+                                     aligned16(dy[j]) && d % (16 / (int64_t)es) == 0});
+                k0 += (int)((d + 63) / 64);
+                of.back().push_back(j);
+            }
+            const int pieces = (k0 + 1) / 2 * 2, r = (int)rows.size();
+            rows.push_back(I8Rows{seg0, (int)segs.size(), pieces, 0, q0, r});
+            I8Prod p{};
+            p.out = dx[i];
+            p.d = d_in;
+            p.pieces = pieces;
+            p.vec = d_in % 4 == 0 && (uintptr_t)dx[i] % (4 * es) == 0;
+            p.q0 = q0;
+            p.rows = r;
+            prods.push_back(p);
+            at.push_back(bytes);
+            q0 += pieces;
+            bytes += (size_t)(d_in + 15) / 16 * pieces * kI8Piece;
+        }
+        if (e == hipSuccess && bytes) e = hipMalloc((void**)&wt, bytes);
+        if (e == hipSuccess && bytes) e = hipMemset(wt, 0, bytes);
+        for (size_t r = 0; r < rows.size() && e == hipSuccess; ++r) {
+            prods[r].w = (const int8_t*)wt + at[r];
+            for (size_t s = 0; s < of[r].size() && e == hipSuccess; ++s) {
+                const dlm_i8_problem& q = h->probs[of[r][s]];
+                e = launch_i8_transpose((const int8_t*)h->d_w + h->w_at[of[r][s]], q.d_out, q.d_in, i8_pieces(q.d_in), (int8_t*)wt + at[r],
+                                        rows[r].pieces, segs[rows[r].seg0 + s].k0, nullptr);
+            }
+        }
+        if (e == hipSuccess) e = i8_upload(segs, rows, prods, &t);
+        if (e == hipSuccess) e = hipDeviceSynchronize();
+    } catch (const std::bad_alloc&) {
+        e = hipErrorOutOfMemory;
+    }
+    if (e != hipSuccess) {
+        if (wt) (void)hipFree(wt);
+        if (t.d) (void)hipFree(t.d);
+        return e == hipErrorOutOfMemory ? fail(DLM_ENOMEM, "i8_group_bind_grads: an allocation failed") : hip_fail(e, "i8_group_bind_grads");
+    }
+    if (h->d_wt) (void)hipFree(h->d_wt);
+    if (h->bwd.d) (void)hipFree(h->bwd.d);
+    h->d_wt = wt;
+    h->bwd = t;
+    h->dy.swap(new_dy);
+    h->dx.swap(new_dx);
+    h->bound = true;
+    h->checked_bwd = 0;
+    return ok();
+}
+
+int dlm_i8_group_backward_workspace_size(const dlm_i8_group* h, int64_t T, size_t* bytes) {
+    if (!h || !bytes) return fail(DLM_EINVAL, "i8_group_backward_workspace_size: null argument");
+    if (!h->bound) return fail(DLM_EINVAL, "i8_group_backward_workspace_size: no gradients are bound");
+    if (T < 0 || T >= ((int64_t)1 << 31))
+        return fail(DLM_ESHAPE, "i8_group_backward_workspace_size: T=%lld out of range", (long long)T);
+    *bytes = i8_workspace(h->bwd.args, T, nullptr);
+    return ok();
+}
+
+int dlm_i8_group_backward(dlm_i8_group* h, int64_t T, int32_t accumulate, void* workspace, size_t ws_bytes, void* stream) {
+    if (!h) return fail(DLM_EINVAL, "i8_group_backward: null handle");
+    if (!h->bound) return fail(DLM_EINVAL, "i8_group_backward: no gradients are bound");
+    return i8_launch("i8_group_backward", h, true, T, accumulate, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,511 @@
+// Products in 8-bit integers with a scale per row (token) and per column (channel).
+//
+//   codes   q = 127 x / max|x| of the row, to the nearest whole number (a half goes
+//           towards 0), s = max|x| / 127; weights come as codes and scales
+//   out     s_t w_o sum_k q_tk w_ok     sums exact in 32 bits, then three fp32 roundings
+//
+// The rounding is decided on the exact quotient: x 127 / max is one binary64 fma onto
+// 1.5 * 2^52, whose low byte is the code (127 / max is taken a hair low, 2^-51, so that
+// the only exact halves, which binary64 could put on either side, go one way).
+//
+// The input gradient is the same product: codes of dy w_scale, whose runs from all the
+// products of one input stand side by side in one row with one scale, against the
+// transposed codes of W.
+//
+// Codes and weights are kept in 1 KB pieces that are the matrix instruction's operands
+// (16 x 16 x 64): a wave copies a piece with one instruction, lane after lane, to
+// registers or LDS, and reads it from there without bank conflicts.  W is the first
+// operand, so a lane's four results are neighbouring columns of out.
+#include "gfx950.hpp"
+#include "int8.hpp"
+#include "internal.hpp"
+
+namespace dlm {
+
+namespace {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ i32x4 mfma(u32x4 a, u32x4 b, i32x4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// ---- codes of rows ---------------------------------------------------------------------
+
+constexpr int kQT = 256;   // threads of a row
+constexpr int kKeep = 4;   // groups of 16 values that a thread keeps in registers
+
+__device__ __forceinline__ float value(float v) { return v; }
+__device__ __forceinline__ float value(uint16_t v) { return bf_to_f(v); }
+
+// 16 neighbours i .. i + 15 of a row of d, 0 past its end.
+template <typename T> __device__ __forceinline__ void load16(const T* row, int64_t i, int64_t d, bool vec, float (&f)[16]) {
+    constexpr int W = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int c = 0; c < 16 / W; ++c) {
+        if (vec) {  // d a multiple of W: all in or all out
+            const u32x4 r = i + c * W < d ? ld128(row + i + c * W) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                if constexpr (sizeof(T) == 4) f[c * W + j] = __uint_as_float(r[j]);
+                else f[c * W + j] = j & 1 ? bf_hi(r[j / 2]) : bf_lo(r[j / 2]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) f[c * W + j] = i + c * W + j < d ? value(gld(row + i + c * W + j)) : 0.f;
+        }
+    }
+}
+__device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
+
+// The codes' factor and the scale of a row from the largest magnitude; 0 and NaN for one
+// that is not finite (its codes are 0, its results NaN), 0 and 0 for zeros.
+__device__ __forceinline__ void row_scale(double top, double* by, float* scale) {
+    const bool fin = top <= 1.7976931348623157e308;
+    *by = fin && top > 0.0 ? 127.0 / top * (1.0 - 0x1p-51) : 0.0;
+    *scale = fin ? (float)(top / 127.0) : __builtin_nanf("");
+}
+__device__ __forceinline__ uint32_t code(double x, double by) {
+    return (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(x, by, 0x1.8p52)) & 255u;
+}
+__device__ __forceinline__ u32x4 codes16(const float (&f)[16], const float* sc, int64_t i, int64_t d, double by) {
+    u32x4 o;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t b = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            double x = (double)f[4 * w + j];
+            if (sc) x *= i + 4 * w + j < d ? (double)gld(sc + i + 4 * w + j) : 0.0;
+            b |= code(by > 0.0 ? x : 0.0, by) << (8 * j);
+        }
+        o[w] = b;
+    }
+    return o;
+}
+// The largest |x| of 16 values, each times its scale: bits of an fp32 without one
+// (infinities and NaN are the largest), a binary64 with one.
+__device__ __forceinline__ double top16(const float (&f)[16], const float* sc, int64_t i, int64_t d) {
+    if (!sc) {
+        uint32_t b = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) b = b > abs_bits(f[j]) ? b : abs_bits(f[j]);
+        return b >= 0x7f800000u ? __builtin_huge_val() : (double)__uint_as_float(b);
+    }
+    double m = 0.0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const double x = fabs((double)f[j] * (i + j < d ? (double)gld(sc + i + j) : 0.0));
+        m = x <= m ? m : x == x ? x : __builtin_huge_val();
+    }
+    return m;
+}
+
+__device__ __forceinline__ double block_max(double v, double* s) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+        const double p = __shfl_xor(v, o, kWave);
+        v = v > p ? v : p;
+    }
+    if (lane_id() == 0) s[wave_id()] = v;
+    __syncthreads();
+    v = s[0];
+#pragma unroll
+    for (int w = 1; w < kQT / kWave; ++w) v = v > s[w] ? v : s[w];
+    return v;
+}
+
+// Block b's row: 16 consecutive rows (whose codes share cache lines) go to one XCD.
+__device__ __forceinline__ int64_t row_of_block(int64_t b, int64_t blocks) {
+    if (blocks % 128) return b;
+    const int64_t local = b / 8;
+    return (local / 16 * 8 + b % 8) * 16 + local % 16;
+}
+
+// One workgroup: one row of one matrix of codes.
+template <typename T> __global__ __launch_bounds__(kQT) void i8_rows(I8Args a) {
+    __shared__ double s_max[kQT / kWave];
+    const I8Rows R = a.rows[blockIdx.y];
+    const int64_t t = row_of_block(blockIdx.x, gridDim.x);
+    if (t >= a.T) return;
+    const int tid = threadIdx.x;
+    // groups of 16 values, along all runs; a thread takes every kQT-th of each run
+    float keep[kKeep][16];
+    double top = 0.0;
+    const I8Seg S0 = a.segs[R.seg0];
+    const T* row0 = (const T*)S0.x + t * S0.d;
+#pragma unroll
+    for (int c = 0; c < kKeep; ++c) {
+        const int64_t i = ((int64_t)c * kQT + tid) * 16;
+        if (i < S0.d) {
+            load16(row0, i, S0.d, S0.vec, keep[c]);
+            const double m = top16(keep[c], S0.scale, i, S0.d);
+            top = top > m ? top : m;
+        }
+    }
+    for (int s = R.seg0; s < R.seg1; ++s) {
+        const I8Seg S = a.segs[s];
+        const T* row = (const T*)S.x + t * S.d;
+        for (int64_t i = ((s == R.seg0 ? (int64_t)kKeep * kQT : 0) + tid) * 16; i < S.d; i += kQT * 16) {
+            float f[16];
+            load16(row, i, S.d, S.vec, f);
+            const double m = top16(f, S.scale, i, S.d);
+            top = top > m ? top : m;
+        }
+    }
+    top = block_max(top, s_max);
+    double by;
+    float scale;
+    row_scale(top, &by, &scale);
+    if (tid == 0) gst(a.scale + R.index * a.T16 * 16 + t, scale);
+    int8_t* out = a.q + (R.q0 * a.T16 + t / 16 * R.pieces) * kI8Piece + t % 16 * 16;
+    const auto put = [&](int k0, int64_t i, u32x4 o) {
+        const int64_t g = i / 16;
+        st128(out + (k0 + g / 4) * kI8Piece + g % 4 * 256, o);
+    };
+#pragma unroll
+    for (int c = 0; c < kKeep; ++c) {
+        const int64_t i = ((int64_t)c * kQT + tid) * 16;
+        if (i < S0.d) put(S0.k0, i, codes16(keep[c], S0.scale, i, S0.d, by));
+    }
+    for (int s = R.seg0; s < R.seg1; ++s) {
+        const I8Seg S = a.segs[s];
+        const T* row = (const T*)S.x + t * S.d;
+        for (int64_t i = ((s == R.seg0 ? (int64_t)kKeep * kQT : 0) + tid) * 16; i < S.d; i += kQT * 16) {
+            float f[16];
+            load16(row, i, S.d, S.vec, f);
+            put(S.k0, i, codes16(f, S.scale, i, S.d, by));
+        }
+    }
+}
+
+// Rows to row-major codes (weights, when they are quantized).
+template <typename T> __global__ __launch_bounds__(kQT) void i8_quantize(const T* __restrict__ x, int64_t d, int vec, int8_t* q, float* scale) {
+    __shared__ double s_max[kQT / kWave];
+    const T* row = x + (int64_t)blockIdx.x * d;
+    double top = 0.0;
+    for (int64_t i = threadIdx.x * 16; i < d; i += kQT * 16) {
+        float f[16];
+        load16(row, i, d, vec, f);
+        const double m = top16(f, nullptr, i, d);
+        top = top > m ? top : m;
+    }
+    top = block_max(top, s_max);
+    double by;
+    float sc;
+    row_scale(top, &by, &sc);
+    if (threadIdx.x == 0) gst(scale + blockIdx.x, sc);
+    for (int64_t i = threadIdx.x * 16; i < d; i += kQT * 16) {
+        float f[16];
+        load16(row, i, d, vec, f);
+        const u32x4 o = codes16(f, nullptr, i, d, by);
+        int8_t* out = q + (int64_t)blockIdx.x * d + i;
+        if (i + 16 <= d && ((uintptr_t)out & 15u) == 0) {
+            st128(out, o);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (i + j < d) gst(out + j, (int8_t)(o[j / 4] >> (8 * (j % 4))));
+        }
+    }
+}
+
+// ---- weights -----------------------------------------------------------------------------
+
+__global__ __launch_bounds__(256) void i8_pack(const int8_t* __restrict__ W, int64_t d_out, int64_t d_in, int pieces, int64_t groups,
+                                               int8_t* out) {
+    for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < groups; g += (int64_t)gridDim.x * 256) {
+        const int64_t piece = g / 64, o = piece / pieces * 16 + g % 16, k = piece % pieces * 64 + g % 64 / 16 * 16;
+        u32x4 r = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const uint32_t b = o < d_out && k + j < d_in ? (uint8_t)gld(W + o * d_in + k + j) : 0u;
+            r[j / 4] |= b << (8 * (j % 4));
+        }
+        st128(out + g * 16, r);
+    }
+}
+// W's transpose: rows are W's columns, columns k0 * 64 .. its rows.
+__global__ __launch_bounds__(256) void i8_transpose(const int8_t* __restrict__ Wp, int64_t d_out, int64_t d_in, int pieces,
+                                                    int64_t groups, int own, int8_t* out, int out_pieces, int k0) {
+    for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < groups; g += (int64_t)gridDim.x * 256) {
+        const int64_t piece = g / 64, i = piece / own * 16 + g % 16;
+        const int kp = (int)(piece % own), k = kp * 64 + (int)(g % 64) / 16 * 16;
+        u32x4 r = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int64_t o = k + j;
+            uint32_t b = 0;
+            if (i < d_in && o < d_out)
+                b = (uint8_t)gld(Wp + (o / 16 * pieces + i / 64) * kI8Piece + (i % 64 / 16 * 16 + o % 16) * 16 + i % 16);
+            r[j / 4] |= b << (8 * (j % 4));
+        }
+        st128(out + ((piece / own * out_pieces + k0 + kp) * 64 + g % 64) * 16, r);
+    }
+}
+
+// ---- products ------------------------------------------------------------------------------
+
+// Four neighbouring columns o .. o + 3 of row t, their scales in w.
+template <typename T> __device__ __forceinline__ void put4(const I8Prod& P, int64_t t, int64_t o, const i32x4& acc, float s, const float (&w)[4], bool add) {
+    const int64_t left = P.d - o;
+    if (left <= 0) return;
+    T* out = (T*)P.out + t * P.d + o;
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (float)acc[j] * s * w[j];
+    if (P.vec) {
+        if constexpr (sizeof(T) == 4) {
+            if (add) {
+                const u32x4 y = ld128(out);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] += __uint_as_float(y[j]);
+            }
+            st128(out, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+        } else {
+            if (add) {
+                const u32x2 y = gld((const u32x2*)out);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] += j & 1 ? bf_hi(y[j / 2]) : bf_lo(y[j / 2]);
+            }
+            gst((u32x2*)out, u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])});
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) {
+                if (add) v[j] += value(gld(out + j));
+                if constexpr (sizeof(T) == 4) gst(out + j, v[j]);
+                else gst(out + j, f_to_bf(v[j]));
+            }
+    }
+}
+// The scales of columns o .. o + 3 (the array is padded to whole pieces).
+__device__ __forceinline__ void column_scales(const I8Prod& P, int64_t o, float (&w)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = 1.f;
+    if (P.w_scale && o < P.d) {
+        const u32x4 r = ld128(P.w_scale + o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __uint_as_float(r[j]);
+    }
+}
+
+// All waves' LDS reads so far are done, and nothing moves across (unlike __syncthreads,
+// it leaves the copies to LDS in flight).
+__device__ __forceinline__ void step_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// The product whose tiles hold tile `t` (`first`: a product's tiles of earlier ones).
+template <int32_t I8Prod::*FIRST> __device__ __forceinline__ int product_of(const I8Prod* prods, int n, int t) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (gld(&(prods[mid].*FIRST)) <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Many rows.  One workgroup: WM x WN waves of 16 MB columns of out x 16 NB rows each.
+// Pieces go from memory to LDS directly, STAGES - 1 steps of 64 columns ahead of the
+// products; a step's pieces are overwritten one barrier after all waves have read them.
+template <typename T, int MB, int NB, int WM, int WN, int32_t I8Prod::*FIRST>
+__global__ __launch_bounds__(WM* WN* kWave) void i8_many(I8Args a) {
+    constexpr int WAVES = WM * WN, PA = MB * WM, PB = NB * WN, STAGES = 4, PER = (PA + PB) / WAVES;
+    static_assert((PA + PB) % WAVES == 0, "every wave copies the same number of pieces");
+    extern __shared__ __align__(16) char smem[];
+    // consecutive workgroups go round the XCDs: each takes a run of neighbouring tiles
+    const uint32_t nt = (uint32_t)((a.T16 + PB - 1) / PB);
+    const uint32_t x = blockIdx.x % 8, each = gridDim.x / 8, more = gridDim.x % 8;
+    const uint32_t at = x * each + (x < more ? x : more) + blockIdx.x / 8;
+    const int p = uniform(product_of<FIRST>(a.prods, a.n_prods, (int)(at / nt)));
+    const I8Prod P = a.prods[p];
+    // its tiles in bands of eight rows of tiles, column after column: neighbours share both operands
+    const uint32_t local = at - (uint32_t)(P.*FIRST) * nt, mt = (uint32_t)((P.d + 16 * PA - 1) / (16 * PA));
+    const uint32_t band = local / (8 * mt), in = local % (8 * mt), height = nt - band * 8 < 8 ? nt - band * 8 : 8;
+    const int64_t tb = band * 8 + in % height, ob = in / height;
+    const int lane = lane_id(), w = wave_id(), wm = w % WM, wn = w / WM;
+    const int64_t o16 = (P.d + 15) / 16;
+    // this wave's pieces of a step: the first PA are W's, the others the rows' (blocks past the end: the last)
+    const int8_t* src[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int piece = w * PER + i;
+        int64_t b;
+        if (piece < PA) {
+            b = ob * PA + piece;
+            src[i] = P.w + (b < o16 ? b : o16 - 1) * P.pieces * kI8Piece;
+        } else {
+            b = tb * PB + piece - PA;
+            src[i] = a.q + (P.q0 * a.T16 + (b < a.T16 ? b : a.T16 - 1) * P.pieces) * kI8Piece;
+        }
+        src[i] += lane * 16;
+    }
+    const auto copy = [&](int k) {
+        char* to = smem + (k % STAGES) * (PA + PB) * kI8Piece + w * PER * kI8Piece;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) copy16_to_lds(src[i] + (int64_t)k * kI8Piece, to + i * kI8Piece);
+    };
+    i32x4 acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    const int K = P.pieces;
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k)
+        if (k < K) copy(k);
+    for (int k = 0; k < K; ++k) {
+        const int ahead = K - 1 - k < STAGES - 2 ? K - 1 - k : STAGES - 2;  // later steps in flight
+        wait_vmcnt_le<(STAGES - 2) * PER>(ahead * PER);
+        step_barrier();
+        if (k + STAGES - 1 < K) copy(k + STAGES - 1);
+        const char* st = smem + (k % STAGES) * (PA + PB) * kI8Piece + lane * 16;
+        u32x4 fa[MB], fb[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) fb[j] = *(const u32x4*)(st + (PA + wn * NB + j) * kI8Piece);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) fa[i] = *(const u32x4*)(st + (wm * MB + i) * kI8Piece);
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) acc[i][j] = mfma(fa[i], fb[j], acc[i][j]);
+    }
+    float sr[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        const int64_t t = (tb * PB + wn * NB + j) * 16 + lane % 16;
+        sr[j] = t < a.T ? gld(a.scale + P.rows * a.T16 * 16 + t) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        const int64_t o = (ob * PA + wm * MB + i) * 16 + lane / 16 * 4;
+        float sw[4];
+        column_scales(P, o, sw);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int64_t t = (tb * PB + wn * NB + j) * 16 + lane % 16;
+            if (t < a.T) put4<T>(P, t, o, acc[i][j], sr[j], sw, a.accumulate != 0);
+        }
+    }
+}
+
+// Few rows (up to 16 TB): the weights are read once, straight into operands.  One
+// workgroup: 16 columns of out, its waves every kFewWaves-th piece of the row; their sums
+// are whole numbers, joined through LDS.
+constexpr int kFewWaves = 8;
+template <typename T, int TB> __global__ __launch_bounds__(kFewWaves* kWave) void i8_few(I8Args a) {
+    constexpr int UNROLL = TB == 1 ? 8 : 4;
+    __shared__ i32x4 s_acc[kFewWaves][TB][kWave];
+    const int p = uniform(product_of<&I8Prod::tile_few>(a.prods, a.n_prods, blockIdx.x));
+    const I8Prod P = a.prods[p];
+    const int64_t ob = blockIdx.x - P.tile_few;
+    const int lane = lane_id(), w = wave_id(), K = P.pieces;
+    const int8_t* W = P.w + ob * K * kI8Piece + lane * 16;
+    const int8_t* X = a.q + P.q0 * a.T16 * kI8Piece + lane * 16;
+    bool row[TB];
+#pragma unroll
+    for (int b = 0; b < TB; ++b) row[b] = b * 16 + lane % 16 < a.T;
+    i32x4 acc[TB];
+#pragma unroll
+    for (int b = 0; b < TB; ++b) acc[b] = i32x4{0, 0, 0, 0};
+    for (int k0 = w; k0 < K; k0 += kFewWaves * UNROLL) {
+        u32x4 fw[UNROLL], fx[UNROLL][TB];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int k = k0 + u * kFewWaves;
+            fw[u] = k < K ? ld128_nt(W + (int64_t)k * kI8Piece) : u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int k = k0 + u * kFewWaves;
+#pragma unroll
+            for (int b = 0; b < TB; ++b)
+                fx[u][b] = k < K && row[b] ? ld128(X + ((int64_t)b * K + k) * kI8Piece) : u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int b = 0; b < TB; ++b) acc[b] = mfma(fw[u], fx[u][b], acc[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < TB; ++b) s_acc[w][b][lane] = acc[b];
+    __syncthreads();
+    if (w >= TB) return;
+    i32x4 sum = s_acc[0][w][lane];
+#pragma unroll
+    for (int v = 1; v < kFewWaves; ++v) sum += s_acc[v][w][lane];
+    const int64_t t = w * 16 + lane % 16;
+    float sw[4];
+    column_scales(P, ob * 16 + lane / 16 * 4, sw);
+    if (t < a.T) put4<T>(P, t, ob * 16 + lane / 16 * 4, sum, gld(a.scale + P.rows * a.T16 * 16 + t), sw, a.accumulate != 0);
+}
+
+constexpr size_t kBigLds = 4 * (16 + 16) * kI8Piece, kMidLds = 4 * (8 + 8) * kI8Piece;
+
+template <typename T> hipError_t launch_products(const I8Args& a, hipStream_t s) {
+    if (a.T <= kI8FewT) {
+        const dim3 g((unsigned)a.tiles_few), n(kFewWaves * kWave);
+        if (!grid_fits(a.tiles_few, kFewWaves * kWave)) return hipErrorInvalidConfiguration;
+        if (a.T16 == 1) hipLaunchKernelGGL((i8_few<T, 1>), g, n, 0, s, a);
+        else if (a.T16 == 2) hipLaunchKernelGGL((i8_few<T, 2>), g, n, 0, s, a);
+        else hipLaunchKernelGGL((i8_few<T, 4>), g, n, 0, s, a);
+        return hipGetLastError();
+    }
+    const int64_t big = (a.T + kI8BigT - 1) / kI8BigT * a.tiles_big, mid = (a.T + kI8MidT - 1) / kI8MidT * a.tiles_mid;
+    if (!grid_fits(mid, 512)) return hipErrorInvalidConfiguration;
+    if (big >= 192) hipLaunchKernelGGL((i8_many<T, 8, 4, 2, 4, &I8Prod::tile_big>), dim3((unsigned)big), dim3(512), kBigLds, s, a);
+    else hipLaunchKernelGGL((i8_many<T, 4, 4, 2, 2, &I8Prod::tile_mid>), dim3((unsigned)mid), dim3(256), kMidLds, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t prepare_i8() {
+    const void* big[] = {(const void*)&i8_many<float, 8, 4, 2, 4, &I8Prod::tile_big>,
+                         (const void*)&i8_many<uint16_t, 8, 4, 2, 4, &I8Prod::tile_big>};
+    for (const void* f : big) {
+        const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBigLds);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_i8_rows(const I8Args& a, int dtype, hipStream_t s) {
+    const int64_t rows = a.T >= 128 ? (a.T + 127) / 128 * 128 : a.T;
+    if (!grid_fits(rows, kQT)) return hipErrorInvalidConfiguration;
+    const dim3 g((unsigned)rows, (unsigned)a.n_rows);
+    if (dtype == 0) hipLaunchKernelGGL(i8_rows<float>, g, dim3(kQT), 0, s, a);
+    else hipLaunchKernelGGL(i8_rows<uint16_t>, g, dim3(kQT), 0, s, a);
+    return hipGetLastError();
+}
+hipError_t launch_i8_products(const I8Args& a, int dtype, hipStream_t s) {
+    return dtype == 0 ? launch_products<float>(a, s) : launch_products<uint16_t>(a, s);
+}
+hipError_t launch_i8_pack(const int8_t* W, int64_t d_out, int64_t d_in, int pieces, int8_t* out, hipStream_t s) {
+    const int64_t groups = (d_out + 15) / 16 * pieces * 64, blocks = (groups + 255) / 256;
+    hipLaunchKernelGGL(i8_pack, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, W, d_out, d_in, pieces, groups, out);
+    return hipGetLastError();
+}
+hipError_t launch_i8_transpose(const int8_t* packed, int64_t d_out, int64_t d_in, int pieces, int8_t* out, int out_pieces, int k0,
+                               hipStream_t s) {
+    const int own = (int)((d_out + 63) / 64);
+    const int64_t groups = (d_in + 15) / 16 * own * 64, blocks = (groups + 255) / 256;
+    hipLaunchKernelGGL(i8_transpose, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, packed, d_out, d_in, pieces,
+                       groups, own, out, out_pieces, k0);
+    return hipGetLastError();
+}
+hipError_t launch_i8_quantize(const void* x, int64_t T, int64_t d, int dtype, int8_t* q, float* scale, hipStream_t s) {
+    if (!grid_fits(T, kQT)) return hipErrorInvalidConfiguration;
+    const int vec = ((uintptr_t)x & 15u) == 0 && d % (dtype == 0 ? 4 : 8) == 0;
+    if (dtype == 0) hipLaunchKernelGGL(i8_quantize<float>, dim3((unsigned)T), dim3(kQT), 0, s, (const float*)x, d, vec, q, scale);
+    else hipLaunchKernelGGL(i8_quantize<uint16_t>, dim3((unsigned)T), dim3(kQT), 0, s, (const uint16_t*)x, d, vec, q, scale);
+    return hipGetLastError();
+}
+
+}  // namespace dlm

@@ -542,6 +542,77 @@ int dlm_sgmm_status(void* workspace, int32_t* code, void* stream);
  */
 int dlm_sgmm_launches(int64_t T, int64_t d_in_max, int32_t r, int32_t n_problems, int32_t dtype);
 
+/* ---------------------------------------------------------- 8-bit products */
+
+/*
+ * Rows as 8-bit codes with a scale each: x [T][d] (dtype) ->
+ *   q [T][d] int8:  127 x / max|x| of the row, to the nearest whole number (decided on
+ *                   the exact quotient; a half goes towards 0)
+ *   scale [T] fp32: max|x| / 127
+ * A row of zeros has scale 0; a row that is not finite has codes 0 and scale NaN.  The
+ * form that dlm_i8_group_create takes weights in.  One launch, no allocation.
+ */
+int dlm_i8_quantize(const void* x, int64_t T, int64_t d, int32_t dtype, int8_t* q, float* scale, void* stream);
+
+/* One product of a frozen base weight that is held in 8 bits. */
+typedef struct {
+    const void* x;        /* [T][d_in] */
+    const int8_t* W;      /* [d_out][d_in] codes */
+    const float* w_scale; /* [d_out] */
+    void* y;              /* [T][d_out], written */
+    int64_t d_in;         /* 1 .. 131072 */
+    int64_t d_out;
+} dlm_i8_problem;
+
+typedef struct dlm_i8_group dlm_i8_group;
+
+/*
+ * Register n products that run together (the base's share of the problems that a
+ * dlm_sgmm_group then adds the adapters' to).  The handle keeps a copy of every W (padded
+ * to 16 rows and 128 columns, in the layout its kernels read) and w_scale, taken here;
+ * the caller's may be freed.  x and y stay the caller's.  x, y and every pointer need
+ * their element's alignment only (16 bytes and sizes a multiple of 8 are faster).
+ * Synchronises the device.
+ */
+int dlm_i8_group_create(const dlm_i8_problem* probs, int32_t n, int32_t dtype, dlm_i8_group** out);
+
+/* Free the handle's device memory (synchronises the device first). */
+int dlm_i8_group_destroy(dlm_i8_group* h);
+
+/*
+ * y[t][o] = round( s_t w_scale[o] sum_k q[t][k] W[o][k] ) for T rows of every problem, with
+ * q and s the row's codes and scale as dlm_i8_quantize makes them.  The sum is exact; the
+ * factors are applied in fp32.  A row of x that is not finite gives NaN in its row of y,
+ * and nothing else.  Two launches (the codes, once for problems that share an x; the
+ * products), no allocation.  Up to 64 rows the weights are read once, straight into the
+ * products' operands.  T = 0 enqueues nothing.
+ * workspace: >= dlm_i8_group_workspace_size(h, T) bytes, 256-byte aligned, of any content.
+ */
+int dlm_i8_group_workspace_size(const dlm_i8_group* h, int64_t T, size_t* bytes);
+int dlm_i8_group_run(dlm_i8_group* h, int64_t T, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The gradient of the inputs, W held: dx = sum over the problems that share it of
+ * dy_i (w_scale_i W_i), with dy in 8 bits too.  Bind once:
+ *   dy (host) [n] device pointers, dy_i [T][d_out_i]; dx (host) [n] device pointers,
+ *   dx_i [T][d_in_i]; NULL entries of dx (and their dy) are not wanted.  Problems of one
+ *   d_in may share a dx (at most 131072 output channels, each problem's counted as a
+ *   multiple of 64): their products dy_i[t][o] w_scale_i[o], side by side, are one row of
+ *   codes with one scale, formed from the exact products.
+ * The handle allocates the weights' transposes (the weights' size).  Synchronises the
+ * device.  Binding again replaces the buffers (calls captured into graphs before then read
+ * freed tables: capture them again).
+ */
+int dlm_i8_group_bind_grads(dlm_i8_group* h, const void* const* dy, void* const* dx);
+
+/*
+ * dx[t][i] = round( s_t sum_o q[t][o] W[o][i] ) for T rows, written, or with accumulate != 0
+ * added to dx before the rounding.  Otherwise as dlm_i8_group_run; the workspace's size is
+ * asked once the buffers are bound.
+ */
+int dlm_i8_group_backward_workspace_size(const dlm_i8_group* h, int64_t T, size_t* bytes);
+int dlm_i8_group_backward(dlm_i8_group* h, int64_t T, int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ AdamW */
 
 /* One tensor of an AdamW step. */

@@ -153,3 +153,46 @@ def test_muon_by_values_is_muon_by_products(shape):
     c = [muon_ref.COEFS] * 5
     assert np.abs(muon_ref.by_values(u, 1e-7, c) - muon_ref.by_products(u, 1e-7, c)).max() < 1e-12
     assert np.abs(muon_ref.by_products(u, 1e-7, c) - muon_ref.by_products(u.T, 1e-7, c).T).max() < 1e-12
+
+
+@built
+def test_int8_validation():
+    lib = dlm.load()
+    h = C.c_void_p()
+    a = [FAKE + k * 64 * MB for k in range(8)]
+
+    def create(n=1, dt=0, out=True, **kw):
+        v = dict(x=a[0], W=a[1], w_scale=a[2], y=a[3], d_in=32, d_out=8) | kw
+        return lib.dlm_i8_group_create((dlm.dlm_i8_problem * 1)(dlm.dlm_i8_problem(*v.values())), n, dt, C.byref(h) if out else None)
+
+    assert lib.dlm_i8_group_create(None, 1, 0, C.byref(h)) == dlm.DLM_EINVAL
+    assert create(n=0) == dlm.DLM_EINVAL and create(n=65536) == dlm.DLM_EINVAL and create(out=False) == dlm.DLM_EINVAL
+    assert create(dt=2) == dlm.DLM_EDTYPE
+    for k in ("x", "W", "w_scale", "y"):
+        assert create(**{k: None}) == dlm.DLM_EINVAL
+    for d in (0, -1, 131073):
+        assert create(d_in=d) == dlm.DLM_ESHAPE
+    assert create(d_out=0) == dlm.DLM_ESHAPE and create(d_out=1 << 31) == dlm.DLM_ESHAPE
+    assert create(x=a[0] + 2) == dlm.DLM_EALIGN and create(y=a[3] + 1, dt=1) == dlm.DLM_EALIGN and create(w_scale=a[2] + 2) == dlm.DLM_EALIGN
+    assert h.value is None
+    b = C.c_size_t(0)
+    assert lib.dlm_i8_group_workspace_size(None, 4, C.byref(b)) == dlm.DLM_EINVAL
+    assert lib.dlm_i8_group_backward_workspace_size(None, 4, C.byref(b)) == dlm.DLM_EINVAL
+    assert lib.dlm_i8_group_run(None, 4, P(a[4]), MB, None) == dlm.DLM_EINVAL
+    assert lib.dlm_i8_group_backward(None, 4, 0, P(a[4]), MB, None) == dlm.DLM_EINVAL
+    assert lib.dlm_i8_group_bind_grads(None, None, None) == dlm.DLM_EINVAL
+    assert lib.dlm_i8_group_destroy(None) == dlm.DLM_EINVAL
+    q = lib.dlm_i8_quantize
+    assert q(P(a[0]), -1, 8, 0, P(a[1]), P(a[2]), None) == dlm.DLM_ESHAPE and q(P(a[0]), 4, 0, 0, P(a[1]), P(a[2]), None) == dlm.DLM_ESHAPE
+    assert q(P(a[0]), 4, 8, 5, P(a[1]), P(a[2]), None) == dlm.DLM_EDTYPE
+    assert q(None, 4, 8, 0, P(a[1]), P(a[2]), None) == dlm.DLM_EINVAL and q(P(a[0]), 4, 8, 0, None, P(a[2]), None) == dlm.DLM_EINVAL
+    assert q(P(a[0] + 2), 4, 8, 0, P(a[1]), P(a[2]), None) == dlm.DLM_EALIGN
+    assert q(P(a[0]), 4, 8, 0, P(a[0] + 16), P(a[2]), None) == dlm.DLM_EINVAL and q(P(a[0]), 4, 8, 0, P(a[1]), P(a[1]), None) == dlm.DLM_EINVAL
+    assert q(None, 0, 8, 0, None, None, None) == dlm.DLM_OK
+
+
+def test_int8_codes_by_hand():
+    import int8_ref
+
+    q, s = int8_ref.codes(torch.tensor([[1.0, 0.5, -0.5, 0.51, 0.0], [0.0, 0.0, 0.0, 0.0, 0.0]]))
+    assert q.tolist() == [[127, 63, -63, 65, 0], [0] * 5] and s[1] == 0 and abs(float(s[0]) * 127 - 1) < 1e-6
