@@ -519,7 +519,10 @@ static hipError_t i8_upload(const std::vector<I8Seg>& segs, const std::vector<I8
         a.tiles_mid += (int32_t)((p.d + kI8MidD - 1) / kI8MidD);
         a.tiles_few += (int32_t)((p.d + kI8FewD - 1) / kI8FewD);
     }
-    for (const I8Rows& r : rows) a.pieces += r.pieces;
+    for (const I8Rows& r : rows) {
+        a.pieces += r.pieces;
+        a.max_pieces = std::max(a.max_pieces, r.pieces);
+    }
     const size_t b0 = (segs.size() * sizeof(I8Seg) + 255) & ~(size_t)255, b1 = b0 + ((rows.size() * sizeof(I8Rows) + 255) & ~(size_t)255);
     std::vector<char> blob(b1 + prods.size() * sizeof(I8Prod));
     std::memcpy(blob.data(), segs.data(), segs.size() * sizeof(I8Seg));
@@ -579,6 +582,7 @@ int dlm_i8_group_create(const dlm_i8_problem* probs, int32_t n, int32_t dtype, d
         std::vector<I8Prod> prods;
         int64_t q0 = 0;
         e = hipMalloc((void**)&h->d_w, bytes);
+        if (e == hipSuccess) e = hipMemset(h->d_w + h->s_at[0], 0, bytes - h->s_at[0]);  // the scales' padding
         for (int i = 0; i < n && e == hipSuccess; ++i) {
             const dlm_i8_problem& q = h->probs[i];
             const int pieces = i8_pieces(q.d_in);

@@ -33,29 +33,42 @@ __device__ __forceinline__ i32x4 mfma(u32x4 a, u32x4 b, i32x4 c) {
 
 // ---- codes of rows ---------------------------------------------------------------------
 
-constexpr int kQT = 256;   // threads of a row
-constexpr int kKeep = 4;   // groups of 16 values that a thread keeps in registers
-
 __device__ __forceinline__ float value(float v) { return v; }
 __device__ __forceinline__ float value(uint16_t v) { return bf_to_f(v); }
 
-// 16 neighbours i .. i + 15 of a row of d, 0 past its end.
-template <typename T> __device__ __forceinline__ void load16(const T* row, int64_t i, int64_t d, bool vec, float (&f)[16]) {
+// 16 neighbours of a row as stored, 0 past its end.
+template <typename T> struct Raw16 {
+    u32x4 r[sizeof(T)];
+};
+template <typename T> __device__ __forceinline__ void load16(const T* row, int64_t i, int64_t d, bool vec, Raw16<T>& o) {
     constexpr int W = 16 / (int)sizeof(T);
+    if (vec) {  // d a multiple of W: all in or all out
 #pragma unroll
-    for (int c = 0; c < 16 / W; ++c) {
-        if (vec) {  // d a multiple of W: all in or all out
-            const u32x4 r = i + c * W < d ? ld128(row + i + c * W) : u32x4{0u, 0u, 0u, 0u};
+        for (int c = 0; c < (int)sizeof(T); ++c) o.r[c] = i + c * W < d ? ld128(row + i + c * W) : u32x4{0u, 0u, 0u, 0u};
+    } else {
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                if constexpr (sizeof(T) == 4) f[c * W + j] = __uint_as_float(r[j]);
-                else f[c * W + j] = j & 1 ? bf_hi(r[j / 2]) : bf_lo(r[j / 2]);
+        for (int c = 0; c < (int)sizeof(T); ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                constexpr int N = 4 / (int)sizeof(T);  // values in a register
+                uint32_t b = 0;
+#pragma unroll
+                for (int h = 0; h < N; ++h) {
+                    const int64_t at = i + c * W + j * N + h;
+                    uint32_t v = 0;
+                    if (at < d) {
+                        if constexpr (sizeof(T) == 4) v = __float_as_uint(gld(row + at));
+                        else v = gld(row + at);
+                    }
+                    b |= v << (16 * h);
+                }
+                o.r[c][j] = b;
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) f[c * W + j] = i + c * W + j < d ? value(gld(row + i + c * W + j)) : 0.f;
-        }
     }
+}
+template <typename T> __device__ __forceinline__ float value16(const Raw16<T>& o, int j) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(o.r[j / 4][j % 4]);
+    else return j & 1 ? bf_hi(o.r[j / 8][j % 8 / 2]) : bf_lo(o.r[j / 8][j % 8 / 2]);
 }
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
@@ -67,139 +80,191 @@ __device__ __forceinline__ void row_scale(double top, double* by, float* scale) 
     *scale = fin ? (float)(top / 127.0) : __builtin_nanf("");
 }
 __device__ __forceinline__ uint32_t code(double x, double by) {
-    return (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(x, by, 0x1.8p52)) & 255u;
+    return (uint32_t)__builtin_bit_cast(uint64_t, __builtin_fma(x, by, 0x1.8p52));
 }
-__device__ __forceinline__ u32x4 codes16(const float (&f)[16], const float* sc, int64_t i, int64_t d, double by) {
+// The factors of 16 neighbours (an array padded to a multiple of 16; 1 where there is none).
+struct Scale16 {
+    u32x4 r[4];
+    bool on;
+    __device__ __forceinline__ Scale16(const float* sc, int64_t i, int64_t d) : on(sc != nullptr) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) r[c] = on && i < d ? ld128(sc + i + 4 * c) : u32x4{0u, 0u, 0u, 0u};
+    }
+    __device__ __forceinline__ double at(int j) const { return (double)__uint_as_float(r[j / 4][j % 4]); }
+};
+// By value, not by address: 16 codes of one lane.
+template <typename T> __device__ __forceinline__ u32x4 codes16(const Raw16<T>& f, const Scale16& sc, double by) {
     u32x4 o;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        uint32_t b = 0;
+        uint32_t b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            double x = (double)f[4 * w + j];
-            if (sc) x *= i + 4 * w + j < d ? (double)gld(sc + i + 4 * w + j) : 0.0;
-            b |= code(by > 0.0 ? x : 0.0, by) << (8 * j);
+            double x = (double)value16(f, 4 * w + j);
+            if (sc.on) x *= sc.at(4 * w + j);
+            b[j] = code(x, by);
         }
-        o[w] = b;
+        // the four low bytes
+        const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u);
+        o[w] = by > 0.0 ? lo | hi << 16 : 0u;
     }
     return o;
 }
-// The largest |x| of 16 values, each times its scale: bits of an fp32 without one
-// (infinities and NaN are the largest), a binary64 with one.
-__device__ __forceinline__ double top16(const float (&f)[16], const float* sc, int64_t i, int64_t d) {
-    if (!sc) {
+// The largest |x| of 16 values, each times its factor (infinite for one that is not finite).
+template <typename T> __device__ __forceinline__ double top16(const Raw16<T>& f, const Scale16& sc) {
+    if (!sc.on) {
         uint32_t b = 0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) b = b > abs_bits(f[j]) ? b : abs_bits(f[j]);
+        for (int j = 0; j < 16; ++j) {
+            const uint32_t v = abs_bits(value16(f, j));
+            b = b > v ? b : v;
+        }
         return b >= 0x7f800000u ? __builtin_huge_val() : (double)__uint_as_float(b);
     }
     double m = 0.0;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-        const double x = fabs((double)f[j] * (i + j < d ? (double)gld(sc + i + j) : 0.0));
+        const double x = fabs((double)value16(f, j) * sc.at(j));
         m = x <= m ? m : x == x ? x : __builtin_huge_val();
     }
     return m;
 }
 
-__device__ __forceinline__ double block_max(double v, double* s) {
+// The largest of the workgroup's values, R at a time, in every thread.
+template <int NT, int R> __device__ __forceinline__ void block_max(double (&v)[R], double (*s)[R]) {
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-        const double p = __shfl_xor(v, o, kWave);
-        v = v > p ? v : p;
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) {
+            const double p = __shfl_xor(v[r], o, kWave);
+            v[r] = v[r] > p ? v[r] : p;
+        }
+        if (lane_id() == 0) s[wave_id()][r] = v[r];
     }
-    if (lane_id() == 0) s[wave_id()] = v;
     __syncthreads();
-    v = s[0];
 #pragma unroll
-    for (int w = 1; w < kQT / kWave; ++w) v = v > s[w] ? v : s[w];
-    return v;
+    for (int r = 0; r < R; ++r) {
+        v[r] = s[0][r];
+#pragma unroll
+        for (int w = 1; w < NT / kWave; ++w) v[r] = v[r] > s[w][r] ? v[r] : s[w][r];
+    }
 }
 
-// Block b's row: 16 consecutive rows (whose codes share cache lines) go to one XCD.
-__device__ __forceinline__ int64_t row_of_block(int64_t b, int64_t blocks) {
-    if (blocks % 128) return b;
+// Block b's rows: those that share 16-row pieces, and with them cache lines, on one XCD.
+template <int R> __device__ __forceinline__ int64_t rows_of_block(int64_t b, int64_t blocks) {
+    constexpr int per = 16 / R;
+    if (blocks % (8 * per)) return b * R;
     const int64_t local = b / 8;
-    return (local / 16 * 8 + b % 8) * 16 + local % 16;
+    return ((local / per * 8 + b % 8) * per + local % per) * R;
 }
 
-// One workgroup: one row of one matrix of codes.
-template <typename T> __global__ __launch_bounds__(kQT) void i8_rows(I8Args a) {
-    __shared__ double s_max[kQT / kWave];
-    const I8Rows R = a.rows[blockIdx.y];
-    const int64_t t = row_of_block(blockIdx.x, gridDim.x);
-    if (t >= a.T) return;
-    const int tid = threadIdx.x;
-    // groups of 16 values, along all runs; a thread takes every kQT-th of each run
-    float keep[kKeep][16];
-    double top = 0.0;
-    const I8Seg S0 = a.segs[R.seg0];
-    const T* row0 = (const T*)S0.x + t * S0.d;
-#pragma unroll
-    for (int c = 0; c < kKeep; ++c) {
-        const int64_t i = ((int64_t)c * kQT + tid) * 16;
-        if (i < S0.d) {
-            load16(row0, i, S0.d, S0.vec, keep[c]);
-            const double m = top16(keep[c], S0.scale, i, S0.d);
-            top = top > m ? top : m;
-        }
-    }
-    for (int s = R.seg0; s < R.seg1; ++s) {
+// One workgroup: R rows of one matrix of codes.  A thread takes every NT-th group of 16
+// values of the rows' runs, keeps its first KEEP groups in registers and reads what is
+// longer again; the rows share a run's factors.
+template <typename T, int R, int NT, int KEEP> __global__ __launch_bounds__(NT) void i8_rows(I8Args a) {
+    __shared__ double s_max[NT / kWave][R];
+    const I8Rows M = a.rows[blockIdx.y];
+    const int64_t t0 = rows_of_block<R>(blockIdx.x, gridDim.x);
+    if (t0 >= a.T) return;
+    const int groups = M.pieces * 4, last = a.T - t0 < R ? (int)(a.T - 1 - t0) : R - 1;
+    struct Group {
+        const T* x;       // the run's first row here
+        const float* scale;
+        int64_t i, d;     // its place in the run; past its end where the run is padded
+        bool vec;
+    };
+    const auto group = [&](int g) {
+        int s = M.seg0;
+        while (s + 1 < M.seg1 && gld(&a.segs[s + 1].k0) <= g / 4) ++s;
         const I8Seg S = a.segs[s];
-        const T* row = (const T*)S.x + t * S.d;
-        for (int64_t i = ((s == R.seg0 ? (int64_t)kKeep * kQT : 0) + tid) * 16; i < S.d; i += kQT * 16) {
-            float f[16];
-            load16(row, i, S.d, S.vec, f);
-            const double m = top16(f, S.scale, i, S.d);
-            top = top > m ? top : m;
+        return Group{(const T*)S.x + t0 * S.d, S.scale, (int64_t)(g - 4 * S.k0) * 16, S.d, S.vec != 0};
+    };
+    const auto load = [&](const Group& G, Raw16<T> (&f)[R]) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) load16(G.x + (r < last ? r : last) * G.d, G.i, G.d, G.vec, f[r]);
+    };
+    double top[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) top[r] = 0.0;
+    const auto raise = [&](const Raw16<T> (&f)[R], const Scale16& sc) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const double m = top16(f[r], sc);
+            top[r] = top[r] > m ? top[r] : m;
+        }
+    };
+    Raw16<T> keep[KEEP][R];
+#pragma unroll
+    for (int c = 0; c < KEEP; ++c) {
+        const int g = c * NT + threadIdx.x;
+        if (g < groups) load(group(g), keep[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < KEEP; ++c) {
+        const int g = c * NT + threadIdx.x;
+        if (g < groups) {
+            const Group G = group(g);
+            raise(keep[c], Scale16(G.scale, G.i, G.d));
         }
     }
-    top = block_max(top, s_max);
-    double by;
-    float scale;
-    row_scale(top, &by, &scale);
-    if (tid == 0) gst(a.scale + R.index * a.T16 * 16 + t, scale);
-    int8_t* out = a.q + (R.q0 * a.T16 + t / 16 * R.pieces) * kI8Piece + t % 16 * 16;
-    const auto put = [&](int k0, int64_t i, u32x4 o) {
-        const int64_t g = i / 16;
-        st128(out + (k0 + g / 4) * kI8Piece + g % 4 * 256, o);
+    for (int g = KEEP * NT + threadIdx.x; g < groups; g += NT) {
+        const Group G = group(g);
+        Raw16<T> f[R];
+        load(G, f);
+        raise(f, Scale16(G.scale, G.i, G.d));
+    }
+    block_max<NT, R>(top, s_max);
+    double by[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float scale;
+        row_scale(top[r], &by[r], &scale);
+        if (threadIdx.x == 0 && t0 + r < a.T) gst(a.scale + M.index * a.T16 * 16 + t0 + r, scale);
+    }
+    // (rows past the last write the place of a row that no result is read from)
+    int8_t* out = a.q + (M.q0 * a.T16 + t0 / 16 * M.pieces) * kI8Piece + t0 % 16 * 16;
+    const auto put = [&](int g, const Raw16<T> (&f)[R], const Scale16& sc) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) st128(out + (int64_t)(g / 4) * kI8Piece + g % 4 * 256 + r * 16, codes16(f[r], sc, by[r]));
     };
 #pragma unroll
-    for (int c = 0; c < kKeep; ++c) {
-        const int64_t i = ((int64_t)c * kQT + tid) * 16;
-        if (i < S0.d) put(S0.k0, i, codes16(keep[c], S0.scale, i, S0.d, by));
-    }
-    for (int s = R.seg0; s < R.seg1; ++s) {
-        const I8Seg S = a.segs[s];
-        const T* row = (const T*)S.x + t * S.d;
-        for (int64_t i = ((s == R.seg0 ? (int64_t)kKeep * kQT : 0) + tid) * 16; i < S.d; i += kQT * 16) {
-            float f[16];
-            load16(row, i, S.d, S.vec, f);
-            put(S.k0, i, codes16(f, S.scale, i, S.d, by));
+    for (int c = 0; c < KEEP; ++c) {
+        const int g = c * NT + threadIdx.x;
+        if (g < groups) {
+            const Group G = group(g);
+            put(g, keep[c], Scale16(G.scale, G.i, G.d));
         }
+    }
+    for (int g = KEEP * NT + threadIdx.x; g < groups; g += NT) {
+        const Group G = group(g);
+        Raw16<T> f[R];
+        load(G, f);
+        put(g, f, Scale16(G.scale, G.i, G.d));
     }
 }
 
 // Rows to row-major codes (weights, when they are quantized).
+constexpr int kQT = 256;
 template <typename T> __global__ __launch_bounds__(kQT) void i8_quantize(const T* __restrict__ x, int64_t d, int vec, int8_t* q, float* scale) {
-    __shared__ double s_max[kQT / kWave];
+    __shared__ double s_max[kQT / kWave][1];
     const T* row = x + (int64_t)blockIdx.x * d;
-    double top = 0.0;
+    const Scale16 one(nullptr, 0, 0);
+    double top[1] = {0.0};
     for (int64_t i = threadIdx.x * 16; i < d; i += kQT * 16) {
-        float f[16];
+        Raw16<T> f;
         load16(row, i, d, vec, f);
-        const double m = top16(f, nullptr, i, d);
-        top = top > m ? top : m;
+        const double m = top16(f, one);
+        top[0] = top[0] > m ? top[0] : m;
     }
-    top = block_max(top, s_max);
+    block_max<kQT, 1>(top, s_max);
     double by;
     float sc;
-    row_scale(top, &by, &sc);
+    row_scale(top[0], &by, &sc);
     if (threadIdx.x == 0) gst(scale + blockIdx.x, sc);
     for (int64_t i = threadIdx.x * 16; i < d; i += kQT * 16) {
-        float f[16];
+        Raw16<T> f;
         load16(row, i, d, vec, f);
-        const u32x4 o = codes16(f, nullptr, i, d, by);
+        const u32x4 o = codes16(f, one, by);
         int8_t* out = q + (int64_t)blockIdx.x * d + i;
         if (i + 16 <= d && ((uintptr_t)out & 15u) == 0) {
             st128(out, o);
@@ -295,7 +360,8 @@ __device__ __forceinline__ void column_scales(const I8Prod& P, int64_t o, float 
 // All waves' LDS reads so far are done, and nothing moves across (unlike __syncthreads,
 // it leaves the copies to LDS in flight).
 __device__ __forceinline__ void step_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), the other counters at their largest
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -319,14 +385,15 @@ __global__ __launch_bounds__(WM* WN* kWave) void i8_many(I8Args a) {
     constexpr int WAVES = WM * WN, PA = MB * WM, PB = NB * WN, STAGES = 4, PER = (PA + PB) / WAVES;
     static_assert((PA + PB) % WAVES == 0, "every wave copies the same number of pieces");
     extern __shared__ __align__(16) char smem[];
-    // consecutive workgroups go round the XCDs: each takes a run of neighbouring tiles
     const uint32_t nt = (uint32_t)((a.T16 + PB - 1) / PB);
-    const uint32_t x = blockIdx.x % 8, each = gridDim.x / 8, more = gridDim.x % 8;
-    const uint32_t at = x * each + (x < more ? x : more) + blockIdx.x / 8;
-    const int p = uniform(product_of<FIRST>(a.prods, a.n_prods, (int)(at / nt)));
+    const int p = uniform(product_of<FIRST>(a.prods, a.n_prods, (int)(blockIdx.x / nt)));
     const I8Prod P = a.prods[p];
-    // its tiles in bands of eight rows of tiles, column after column: neighbours share both operands
-    const uint32_t local = at - (uint32_t)(P.*FIRST) * nt, mt = (uint32_t)((P.d + 16 * PA - 1) / (16 * PA));
+    // Consecutive workgroups go round the XCDs: each XCD takes a run of neighbouring tiles of every
+    // product (of all products together one XCD would get the longest sums).  The tiles go in bands
+    // of eight rows of tiles, column after column: neighbours share both operands.
+    const uint32_t mt = (uint32_t)((P.d + 16 * PA - 1) / (16 * PA)), n = mt * nt;
+    const uint32_t mine = blockIdx.x - (uint32_t)(P.*FIRST) * nt, x = mine % 8;
+    const uint32_t local = x * (n / 8) + (x < n % 8 ? x : n % 8) + mine / 8;
     const uint32_t band = local / (8 * mt), in = local % (8 * mt), height = nt - band * 8 < 8 ? nt - band * 8 : 8;
     const int64_t tb = band * 8 + in % height, ob = in / height;
     const int lane = lane_id(), w = wave_id(), wm = w % WM, wn = w / WM;
@@ -356,25 +423,45 @@ __global__ __launch_bounds__(WM* WN* kWave) void i8_many(I8Args a) {
     for (int i = 0; i < MB; ++i)
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    // Step k's operands are in registers while those of step k + 1 are read from LDS between its
+    // products; one barrier a step: past it step k + 1's pieces are in LDS, and step k's, read by all
+    // waves, make room for step k + STAGES.
     const int K = P.pieces;
 #pragma unroll
-    for (int k = 0; k < STAGES - 1; ++k)
+    for (int k = 0; k < STAGES; ++k)
         if (k < K) copy(k);
-    for (int k = 0; k < K; ++k) {
-        const int ahead = K - 1 - k < STAGES - 2 ? K - 1 - k : STAGES - 2;  // later steps in flight
-        wait_vmcnt_le<(STAGES - 2) * PER>(ahead * PER);
+    u32x4 fa[2][MB], fb[2][NB];
+    const auto arrive = [&](int k) {  // step k's pieces are there
+        wait_vmcnt_le<(STAGES - 1) * PER>((K - 1 - k < STAGES - 1 ? K - 1 - k : STAGES - 1) * PER);
         step_barrier();
-        if (k + STAGES - 1 < K) copy(k + STAGES - 1);
+    };
+    const auto read = [&](int k, int to) {
         const char* st = smem + (k % STAGES) * (PA + PB) * kI8Piece + lane * 16;
-        u32x4 fa[MB], fb[NB];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) fb[j] = *(const u32x4*)(st + (PA + wn * NB + j) * kI8Piece);
+        for (int j = 0; j < NB; ++j) fb[to][j] = *(const u32x4*)(st + (PA + wn * NB + j) * kI8Piece);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) fa[i] = *(const u32x4*)(st + (wm * MB + i) * kI8Piece);
+        for (int i = 0; i < MB; ++i) fa[to][i] = *(const u32x4*)(st + (wm * MB + i) * kI8Piece);
+    };
+    const auto multiply = [&](int of) {
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j) acc[i][j] = mfma(fa[i], fb[j], acc[i][j]);
+            for (int j = 0; j < NB; ++j) acc[i][j] = mfma(fa[of][i], fb[of][j], acc[i][j]);
+    };
+    // (in flight when step k + 1 has to be there: k + 2 .. k + STAGES - 1)
+    const auto ahead = [&](int k, int to) {
+        wait_vmcnt_le<(STAGES - 2) * PER>((K - 2 - k < STAGES - 2 ? K - 2 - k : STAGES - 2) * PER);
+        step_barrier();
+        if (k + STAGES < K) copy(k + STAGES);
+        read(k + 1, to);
+    };
+    arrive(0);
+    read(0, 0);
+    for (int k = 0; k < K; k += 2) {  // K is even
+        ahead(k, 1);
+        multiply(0);
+        if (k + 2 < K) ahead(k + 1, 0);
+        multiply(1);
     }
     float sr[NB];
 #pragma unroll
@@ -477,12 +564,18 @@ hipError_t prepare_i8() {
 }
 
 hipError_t launch_i8_rows(const I8Args& a, int dtype, hipStream_t s) {
-    const int64_t rows = a.T >= 128 ? (a.T + 127) / 128 * 128 : a.T;
-    if (!grid_fits(rows, kQT)) return hipErrorInvalidConfiguration;
-    const dim3 g((unsigned)rows, (unsigned)a.n_rows);
-    if (dtype == 0) hipLaunchKernelGGL(i8_rows<float>, g, dim3(kQT), 0, s, a);
-    else hipLaunchKernelGGL(i8_rows<uint16_t>, g, dim3(kQT), 0, s, a);
-    return hipGetLastError();
+    const auto go = [&](auto kernel, int rows, int threads) {
+        // many rows: whole runs of 128, which go round the XCDs 16 at a time
+        const int64_t blocks = a.T > 128 ? (a.T + 127) / 128 * (128 / rows) : (a.T + rows - 1) / rows;
+        if (!grid_fits(blocks, threads)) return hipErrorInvalidConfiguration;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks, (unsigned)a.n_rows), dim3(threads), 0, s, a);
+        return hipGetLastError();
+    };
+    // a row's values in registers where they fit
+    const bool wide = a.max_pieces > 3 * 64;
+    if (dtype == 0) return wide ? go(i8_rows<float, 1, 512, 3>, 1, 512) : go(i8_rows<float, 1, 256, 3>, 1, 256);
+    if (a.T <= 128) return wide ? go(i8_rows<uint16_t, 1, 512, 3>, 1, 512) : go(i8_rows<uint16_t, 1, 256, 3>, 1, 256);
+    return wide ? go(i8_rows<uint16_t, 2, 512, 3>, 2, 512) : go(i8_rows<uint16_t, 2, 256, 3>, 2, 256);
 }
 hipError_t launch_i8_products(const I8Args& a, int dtype, hipStream_t s) {
     return dtype == 0 ? launch_products<float>(a, s) : launch_products<uint16_t>(a, s);

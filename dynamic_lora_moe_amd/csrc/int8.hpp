@@ -49,6 +49,7 @@ struct I8Args {
     int32_t tiles_big, tiles_mid, tiles_few;
     int64_t T, T16;       // rows, and 16-row blocks
     int64_t pieces;       // of all I8Rows together (per 16 rows)
+    int32_t max_pieces;   // of the longest row
     int8_t* q;            // codes: matrix i at q0_i * T16 pieces
     float* scale;         // [n_rows][T16 * 16]
     int32_t accumulate;
