@@ -26,6 +26,7 @@ namespace {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4a8 __attribute__((aligned(8)));  // rows of a multiple of four bf16
 
 __device__ __forceinline__ i32x4 mfma(u32x4 a, u32x4 b, i32x4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
@@ -312,14 +313,24 @@ __global__ __launch_bounds__(256) void i8_transpose(const int8_t* __restrict__ W
 
 // ---- products ------------------------------------------------------------------------------
 
+// Four results and what they join, rounded.
+__device__ __forceinline__ void scaled(const i32x4& acc, float s, const float (&w)[4], float (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (float)acc[j] * s * w[j];
+}
+template <typename T> __device__ __forceinline__ void put1(T* out, float v, bool add) {
+    if (add) v += value(gld(out));
+    if constexpr (sizeof(T) == 4) gst(out, v);
+    else gst(out, f_to_bf(v));
+}
 // Four neighbouring columns o .. o + 3 of row t, their scales in w.
-template <typename T> __device__ __forceinline__ void put4(const I8Prod& P, int64_t t, int64_t o, const i32x4& acc, float s, const float (&w)[4], bool add) {
+template <typename T>
+__device__ __forceinline__ void put4(const I8Prod& P, int64_t t, int64_t o, const i32x4& acc, float s, const float (&w)[4], bool add) {
     const int64_t left = P.d - o;
     if (left <= 0) return;
     T* out = (T*)P.out + t * P.d + o;
     float v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = (float)acc[j] * s * w[j];
+    scaled(acc, s, w, v);
     if (P.vec) {
         if constexpr (sizeof(T) == 4) {
             if (add) {
@@ -339,11 +350,47 @@ template <typename T> __device__ __forceinline__ void put4(const I8Prod& P, int6
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (j < left) {
-                if (add) v[j] += value(gld(out + j));
-                if constexpr (sizeof(T) == 4) gst(out + j, v[j]);
-                else gst(out + j, f_to_bf(v[j]));
+            if (j < left) put1(out + j, v[j], add);
+    }
+}
+// The same for bf16 and two tiles side by side (columns o0 .. o0 + 31): lanes 16 apart
+// swap halves, so that each has eight neighbours and a row's 64 bytes go out in one
+// instruction (as four's 32 bytes the writes took a fifth of the kernel).  All lanes of
+// the wave call it; t may be past the end.
+__device__ __forceinline__ void put8(const I8Prod& P, int64_t T, int64_t t, int64_t o0, const i32x4& a0, const i32x4& a1, float s,
+                                     const float (&w0)[4], const float (&w1)[4], bool add) {
+    float v0[4], v1[4];
+    scaled(a0, s, w0, v0);
+    scaled(a1, s, w1, v1);
+    const int h = lane_id() / 16;
+    if (add) {  // what is there, in the places where the results are now
+        const int64_t o = o0 + 4 * h;
+        if (t < T) {
+            const uint16_t* out = (const uint16_t*)P.out + t * P.d;
+            const u32x2 y0 = o < P.d ? gld((const u32x2*)(out + o)) : u32x2{0u, 0u};
+            const u32x2 y1 = o + 16 < P.d ? gld((const u32x2*)(out + o + 16)) : u32x2{0u, 0u};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v0[j] += j & 1 ? bf_hi(y0[j / 2]) : bf_lo(y0[j / 2]);
+                v1[j] += j & 1 ? bf_hi(y1[j / 2]) : bf_lo(y1[j / 2]);
             }
+        }
+    }
+    u32x4 q;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const auto x = __builtin_amdgcn_permlane16_swap(pack2_bf16(v0[2 * j], v0[2 * j + 1]), pack2_bf16(v1[2 * j], v1[2 * j + 1]), false, false);
+        q[j] = x[0];
+        q[2 + j] = x[1];
+    }
+    // lanes 0..15 and 32..47 hold columns 0..7 and 8..15 of the first tile, the others the second's
+    const int64_t o = o0 + 16 * (h & 1) + 8 * (h >> 1);
+    if (t >= T || o >= P.d) return;
+    uint16_t* out = (uint16_t*)P.out + t * P.d + o;
+    if (o + 8 <= P.d) {
+        *(gptr<u32x4a8>)out = q;
+    } else {
+        gst((u32x2*)out, u32x2{q[0], q[1]});  // d is a multiple of 4
     }
 }
 // The scales of columns o .. o + 3 (the array is padded to whole pieces).
@@ -366,6 +413,18 @@ __device__ __forceinline__ void step_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// The order of a step: its reads from LDS go between its products, two or three to each (all
+// at once they fill the LDS's queue, and the products wait behind them).
+template <int MB, int NB> __device__ __forceinline__ void between() {
+    constexpr int READS = MB + NB, EACH = MB * NB / READS;
+#pragma unroll
+    for (int i = 0; i < READS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read
+        __builtin_amdgcn_sched_group_barrier(0x008, EACH, 0);  // products
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, MB * NB - EACH * READS, 0);
+}
+
 // The product whose tiles hold tile `t` (`first`: a product's tiles of earlier ones).
 template <int32_t I8Prod::*FIRST> __device__ __forceinline__ int product_of(const I8Prod* prods, int n, int t) {
     int lo = 0, hi = n - 1;
@@ -377,108 +436,151 @@ template <int32_t I8Prod::*FIRST> __device__ __forceinline__ int product_of(cons
     return lo;
 }
 
-// Many rows.  One workgroup: WM x WN waves of 16 MB columns of out x 16 NB rows each.
-// Pieces go from memory to LDS directly, STAGES - 1 steps of 64 columns ahead of the
-// products; a step's pieces are overwritten one barrier after all waves have read them.
-template <typename T, int MB, int NB, int WM, int WN, int32_t I8Prod::*FIRST>
-__global__ __launch_bounds__(WM* WN* kWave) void i8_many(I8Args a) {
-    constexpr int WAVES = WM * WN, PA = MB * WM, PB = NB * WN, STAGES = 4, PER = (PA + PB) / WAVES;
+// Many rows.  A tile: WM x WN waves of 16 MB columns of out x 16 NB rows each.  A workgroup
+// takes every gridDim.x-th tile and copies the next one's first pieces while it writes a
+// tile's results.  Pieces go from memory to LDS directly, STAGES - 1 steps of 64 columns
+// ahead of the products; a step's pieces are overwritten one barrier after all waves have
+// read them.
+template <typename T, int MB, int NB, int WM, int WN, int STAGES, int32_t I8Prod::*FIRST>
+__global__ __launch_bounds__(WM* WN* kWave) void i8_many(I8Args a, uint32_t tiles) {
+    constexpr int WAVES = WM * WN, PA = MB * WM, PB = NB * WN, PER = (PA + PB) / WAVES;
     static_assert((PA + PB) % WAVES == 0, "every wave copies the same number of pieces");
     extern __shared__ __align__(16) char smem[];
-    const uint32_t nt = (uint32_t)((a.T16 + PB - 1) / PB);
-    const int p = uniform(product_of<FIRST>(a.prods, a.n_prods, (int)(blockIdx.x / nt)));
-    const I8Prod P = a.prods[p];
-    // Consecutive workgroups go round the XCDs: each XCD takes a run of neighbouring tiles of every
-    // product (of all products together one XCD would get the longest sums).  The tiles go in bands
-    // of eight rows of tiles, column after column: neighbours share both operands.
-    const uint32_t mt = (uint32_t)((P.d + 16 * PA - 1) / (16 * PA)), n = mt * nt;
-    const uint32_t mine = blockIdx.x - (uint32_t)(P.*FIRST) * nt, x = mine % 8;
-    const uint32_t local = x * (n / 8) + (x < n % 8 ? x : n % 8) + mine / 8;
-    const uint32_t band = local / (8 * mt), in = local % (8 * mt), height = nt - band * 8 < 8 ? nt - band * 8 : 8;
-    const int64_t tb = band * 8 + in % height, ob = in / height;
     const int lane = lane_id(), w = wave_id(), wm = w % WM, wn = w / WM;
-    const int64_t o16 = (P.d + 15) / 16;
-    // this wave's pieces of a step: the first PA are W's, the others the rows' (blocks past the end: the last)
-    const int8_t* src[PER];
+    const uint32_t lane16 = lane * 16;
+    const uint32_t nt = (uint32_t)((a.T16 + PB - 1) / PB);
+    struct Tile {
+        I8Prod P;
+        int64_t ob, tb;
+        const int8_t* src[PER];  // the wave's pieces
+    };
+    const auto locate = [&](uint32_t at, Tile& t) {
+        const int p = uniform(product_of<FIRST>(a.prods, a.n_prods, (int)(at / nt)));
+        t.P = a.prods[p];
+        // Consecutive tiles go round the XCDs: each XCD takes a run of neighbouring tiles of every
+        // product (of all products together one XCD would get the longest sums).  The tiles go in bands
+        // of eight rows of tiles, column after column: neighbours share both operands.
+        const uint32_t mt = (uint32_t)((t.P.d + 16 * PA - 1) / (16 * PA)), n = mt * nt;
+        const uint32_t mine = at - (uint32_t)(t.P.*FIRST) * nt, x = mine % 8;
+        const uint32_t local = x * (n / 8) + (x < n % 8 ? x : n % 8) + mine / 8;
+        const uint32_t band = local / (8 * mt), in = local % (8 * mt), height = nt - band * 8 < 8 ? nt - band * 8 : 8;
+        t.tb = band * 8 + in % height;
+        t.ob = in / height;
+        // the first PA pieces of a step are W's, the others the rows' (blocks past the end: the last)
+        const int64_t o16 = (t.P.d + 15) / 16;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int piece = w * PER + i;
-        int64_t b;
-        if (piece < PA) {
-            b = ob * PA + piece;
-            src[i] = P.w + (b < o16 ? b : o16 - 1) * P.pieces * kI8Piece;
-        } else {
-            b = tb * PB + piece - PA;
-            src[i] = a.q + (P.q0 * a.T16 + (b < a.T16 ? b : a.T16 - 1) * P.pieces) * kI8Piece;
+        for (int i = 0; i < PER; ++i) {
+            const int piece = w * PER + i;
+            int64_t b;
+            if (piece < PA) {
+                b = t.ob * PA + piece;
+                t.src[i] = t.P.w + (b < o16 ? b : o16 - 1) * t.P.pieces * kI8Piece;
+            } else {
+                b = t.tb * PB + piece - PA;
+                t.src[i] = a.q + (t.P.q0 * a.T16 + (b < a.T16 ? b : a.T16 - 1) * t.P.pieces) * kI8Piece;
+            }
         }
-        src[i] += lane * 16;
-    }
-    const auto copy = [&](int k) {
+    };
+    const auto copy = [&](const Tile& t, int k) {
         char* to = smem + (k % STAGES) * (PA + PB) * kI8Piece + w * PER * kI8Piece;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) copy16_to_lds(src[i] + (int64_t)k * kI8Piece, to + i * kI8Piece);
+        for (int i = 0; i < PER; ++i) copy16_to_lds(t.src[i] + (int64_t)k * kI8Piece + lane16, to + i * kI8Piece);
     };
-    i32x4 acc[MB][NB];
+    const auto begin = [&](uint32_t at, Tile& t) {
+        locate(at, t);
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    // Step k's operands are in registers while those of step k + 1 are read from LDS between its
-    // products; one barrier a step: past it step k + 1's pieces are in LDS, and step k's, read by all
-    // waves, make room for step k + STAGES.
-    const int K = P.pieces;
-#pragma unroll
-    for (int k = 0; k < STAGES; ++k)
-        if (k < K) copy(k);
-    u32x4 fa[2][MB], fb[2][NB];
-    const auto arrive = [&](int k) {  // step k's pieces are there
-        wait_vmcnt_le<(STAGES - 1) * PER>((K - 1 - k < STAGES - 1 ? K - 1 - k : STAGES - 1) * PER);
-        step_barrier();
+        for (int k = 0; k < STAGES; ++k)
+            if (k < t.P.pieces) copy(t, k);
     };
-    const auto read = [&](int k, int to) {
-        const char* st = smem + (k % STAGES) * (PA + PB) * kI8Piece + lane * 16;
-#pragma unroll
-        for (int j = 0; j < NB; ++j) fb[to][j] = *(const u32x4*)(st + (PA + wn * NB + j) * kI8Piece);
-#pragma unroll
-        for (int i = 0; i < MB; ++i) fa[to][i] = *(const u32x4*)(st + (wm * MB + i) * kI8Piece);
-    };
-    const auto multiply = [&](int of) {
+    Tile now;
+    uint32_t at = blockIdx.x;
+    begin(at, now);
+    while (true) {
+        i32x4 acc[MB][NB];
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j) acc[i][j] = mfma(fa[of][i], fb[of][j], acc[i][j]);
-    };
-    // (in flight when step k + 1 has to be there: k + 2 .. k + STAGES - 1)
-    const auto ahead = [&](int k, int to) {
-        wait_vmcnt_le<(STAGES - 2) * PER>((K - 2 - k < STAGES - 2 ? K - 2 - k : STAGES - 2) * PER);
+            for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+        // Step k's operands are in registers while those of step k + 1 are read from LDS between its
+        // products; one barrier a step: past it step k + 1's pieces are in LDS, and step k's, read by all
+        // waves, make room for step k + STAGES.
+        const int K = now.P.pieces;
+        u32x4 fa[2][MB], fb[2][NB];
+        const auto read = [&](int k, int to) {
+            const char* st = smem + (k % STAGES) * (PA + PB) * kI8Piece + lane * 16;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) fb[to][j] = *(const u32x4*)(st + (PA + wn * NB + j) * kI8Piece);
+#pragma unroll
+            for (int i = 0; i < MB; ++i) fa[to][i] = *(const u32x4*)(st + (wm * MB + i) * kI8Piece);
+        };
+        const auto multiply = [&](int of) {
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) acc[i][j] = mfma(fa[of][i], fb[of][j], acc[i][j]);
+        };
+        // (in flight when step k + 1 has to be there: k + 2 .. k + STAGES - 1)
+        const auto ahead = [&](int k, int to) {
+            wait_vmcnt_le<(STAGES - 2) * PER>((K - 2 - k < STAGES - 2 ? K - 2 - k : STAGES - 2) * PER);
+            step_barrier();
+            if (k + STAGES < K) copy(now, k + STAGES);
+            read(k + 1, to);
+        };
+        wait_vmcnt_le<(STAGES - 1) * PER>((K - 1 < STAGES - 1 ? K - 1 : STAGES - 1) * PER);
         step_barrier();
-        if (k + STAGES < K) copy(k + STAGES);
-        read(k + 1, to);
-    };
-    arrive(0);
-    read(0, 0);
-    for (int k = 0; k < K; k += 2) {  // K is even
+        read(0, 0);
+        int k = 0;  // K is even
+        for (; k + 2 < K; k += 2) {
+            ahead(k, 1);
+            multiply(0);
+            between<MB, NB>();
+            ahead(k + 1, 0);
+            multiply(1);
+            between<MB, NB>();
+        }
         ahead(k, 1);
         multiply(0);
-        if (k + 2 < K) ahead(k + 1, 0);
+        between<MB, NB>();
         multiply(1);
-    }
-    float sr[NB];
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        const int64_t t = (tb * PB + wn * NB + j) * 16 + lane % 16;
-        sr[j] = t < a.T ? gld(a.scale + P.rows * a.T16 * 16 + t) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-        const int64_t o = (ob * PA + wm * MB + i) * 16 + lane / 16 * 4;
-        float sw[4];
-        column_scales(P, o, sw);
+        const I8Prod P = now.P;
+        const int64_t ob = now.ob, tb = now.tb;
+        at += gridDim.x;
+        const bool more = at < tiles;
+        if (more) {
+            step_barrier();  // every wave has read its last pieces
+            begin(at, now);
+        }
+        float sr[NB];
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const int64_t t = (tb * PB + wn * NB + j) * 16 + lane % 16;
-            if (t < a.T) put4<T>(P, t, o, acc[i][j], sr[j], sw, a.accumulate != 0);
+            sr[j] = t < a.T ? gld(a.scale + P.rows * a.T16 * 16 + t) : 0.f;
         }
+        if (sizeof(T) == 2 && P.vec) {
+#pragma unroll
+            for (int i = 0; i < MB; i += 2) {
+                const int64_t o0 = (ob * PA + wm * MB + i) * 16;
+                float w0[4], w1[4];
+                column_scales(P, o0 + lane / 16 * 4, w0);
+                column_scales(P, o0 + 16 + lane / 16 * 4, w1);
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    put8(P, a.T, (tb * PB + wn * NB + j) * 16 + lane % 16, o0, acc[i][j], acc[i + 1][j], sr[j], w0, w1, a.accumulate != 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                const int64_t o = (ob * PA + wm * MB + i) * 16 + lane / 16 * 4;
+                float sw[4];
+                column_scales(P, o, sw);
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const int64_t t = (tb * PB + wn * NB + j) * 16 + lane % 16;
+                    if (t < a.T) put4<T>(P, t, o, acc[i][j], sr[j], sw, a.accumulate != 0);
+                }
+            }
+        }
+        if (!more) return;
     }
 }
 
@@ -533,6 +635,7 @@ template <typename T, int TB> __global__ __launch_bounds__(kFewWaves* kWave) voi
     if (t < a.T) put4<T>(P, t, ob * 16 + lane / 16 * 4, sum, gld(a.scale + P.rows * a.T16 * 16 + t), sw, a.accumulate != 0);
 }
 
+constexpr int64_t kCus = 256;  // a workgroup of the large tiles' takes a CU
 constexpr size_t kBigLds = 4 * (16 + 16) * kI8Piece, kMidLds = 4 * (8 + 8) * kI8Piece;
 
 template <typename T> hipError_t launch_products(const I8Args& a, hipStream_t s) {
@@ -546,16 +649,19 @@ template <typename T> hipError_t launch_products(const I8Args& a, hipStream_t s)
     }
     const int64_t big = (a.T + kI8BigT - 1) / kI8BigT * a.tiles_big, mid = (a.T + kI8MidT - 1) / kI8MidT * a.tiles_mid;
     if (!grid_fits(mid, 512)) return hipErrorInvalidConfiguration;
-    if (big >= 192) hipLaunchKernelGGL((i8_many<T, 8, 4, 2, 4, &I8Prod::tile_big>), dim3((unsigned)big), dim3(512), kBigLds, s, a);
-    else hipLaunchKernelGGL((i8_many<T, 4, 4, 2, 2, &I8Prod::tile_mid>), dim3((unsigned)mid), dim3(256), kMidLds, s, a);
+    if (big >= 192)
+        hipLaunchKernelGGL((i8_many<T, 8, 4, 2, 4, 4, &I8Prod::tile_big>), dim3((unsigned)(big < kCus ? big : kCus)), dim3(512), kBigLds, s, a,
+                           (uint32_t)big);
+    else
+        hipLaunchKernelGGL((i8_many<T, 4, 4, 2, 2, 4, &I8Prod::tile_mid>), dim3((unsigned)mid), dim3(256), kMidLds, s, a, (uint32_t)mid);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t prepare_i8() {
-    const void* big[] = {(const void*)&i8_many<float, 8, 4, 2, 4, &I8Prod::tile_big>,
-                         (const void*)&i8_many<uint16_t, 8, 4, 2, 4, &I8Prod::tile_big>};
+    const void* big[] = {(const void*)&i8_many<float, 8, 4, 2, 4, 4, &I8Prod::tile_big>,
+                         (const void*)&i8_many<uint16_t, 8, 4, 2, 4, 4, &I8Prod::tile_big>};
     for (const void* f : big) {
         const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBigLds);
         if (e != hipSuccess) return e;
