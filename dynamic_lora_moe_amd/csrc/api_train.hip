@@ -512,12 +512,10 @@ static hipError_t i8_upload(const std::vector<I8Seg>& segs, const std::vector<I8
     a.n_rows = (int32_t)rows.size();
     a.n_prods = (int32_t)prods.size();
     for (I8Prod& p : prods) {
-        p.tile_big = a.tiles_big;
-        p.tile_mid = a.tiles_mid;
-        p.tile_few = a.tiles_few;
-        a.tiles_big += (int32_t)((p.d + kI8BigD - 1) / kI8BigD);
-        a.tiles_mid += (int32_t)((p.d + kI8MidD - 1) / kI8MidD);
-        a.tiles_few += (int32_t)((p.d + kI8FewD - 1) / kI8FewD);
+        for (int k = 0; k < 6; ++k) {
+            p.tile[k] = a.tiles[k];
+            a.tiles[k] += (int32_t)((p.d + kI8Cols[k] - 1) / kI8Cols[k]);
+        }
     }
     for (const I8Rows& r : rows) {
         a.pieces += r.pieces;
@@ -558,7 +556,7 @@ int dlm_i8_group_create(const dlm_i8_problem* probs, int32_t n, int32_t dtype, d
             return fail(DLM_ESHAPE, "i8_group_create: problem %d: d_out=%lld out of range", i, (long long)q.d_out);
         if ((uintptr_t)q.x % es || (uintptr_t)q.y % es || (uintptr_t)q.w_scale % 4)
             return fail(DLM_EALIGN, "i8_group_create: problem %d: a pointer is not a multiple of its element's size", i);
-        tiles += (q.d_out + kI8FewD - 1) / kI8FewD;
+        tiles += (q.d_out + 15) / 16;
     }
     if (!grid_fits(tiles, 512))
         return fail(DLM_ESHAPE, "i8_group_create: the sizes need a launch grid of more than 2^32 - 1 work-items");

@@ -425,12 +425,12 @@ template <int MB, int NB> __device__ __forceinline__ void between() {
     __builtin_amdgcn_sched_group_barrier(0x008, MB * NB - EACH * READS, 0);
 }
 
-// The product whose tiles hold tile `t` (`first`: a product's tiles of earlier ones).
-template <int32_t I8Prod::*FIRST> __device__ __forceinline__ int product_of(const I8Prod* prods, int n, int t) {
+// The product whose tiles of a kind hold tile `t`.
+template <int KIND> __device__ __forceinline__ int product_of(const I8Prod* prods, int n, int t) {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (gld(&(prods[mid].*FIRST)) <= t) lo = mid;
+        if (gld(&prods[mid].tile[KIND]) <= t) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -441,10 +441,10 @@ template <int32_t I8Prod::*FIRST> __device__ __forceinline__ int product_of(cons
 // tile's results.  Pieces go from memory to LDS directly, STAGES - 1 steps of 64 columns
 // ahead of the products; a step's pieces are overwritten one barrier after all waves have
 // read them.
-template <typename T, int MB, int NB, int WM, int WN, int STAGES, int32_t I8Prod::*FIRST>
+template <typename T, int MB, int NB, int WM, int WN, int STAGES, int KIND>
 __global__ __launch_bounds__(WM* WN* kWave) void i8_many(I8Args a, uint32_t tiles) {
     constexpr int WAVES = WM * WN, PA = MB * WM, PB = NB * WN, PER = (PA + PB) / WAVES;
-    static_assert((PA + PB) % WAVES == 0, "every wave copies the same number of pieces");
+    static_assert(kI8Cols[KIND] == 16 * PA && (PA + PB) % WAVES == 0, "every wave copies the same number of pieces");
     extern __shared__ __align__(16) char smem[];
     const int lane = lane_id(), w = wave_id(), wm = w % WM, wn = w / WM;
     const uint32_t lane16 = lane * 16;
@@ -455,13 +455,13 @@ __global__ __launch_bounds__(WM* WN* kWave) void i8_many(I8Args a, uint32_t tile
         const int8_t* src[PER];  // the wave's pieces
     };
     const auto locate = [&](uint32_t at, Tile& t) {
-        const int p = uniform(product_of<FIRST>(a.prods, a.n_prods, (int)(at / nt)));
+        const int p = uniform(product_of<KIND>(a.prods, a.n_prods, (int)(at / nt)));
         t.P = a.prods[p];
         // Consecutive tiles go round the XCDs: each XCD takes a run of neighbouring tiles of every
         // product (of all products together one XCD would get the longest sums).  The tiles go in bands
         // of eight rows of tiles, column after column: neighbours share both operands.
         const uint32_t mt = (uint32_t)((t.P.d + 16 * PA - 1) / (16 * PA)), n = mt * nt;
-        const uint32_t mine = at - (uint32_t)(t.P.*FIRST) * nt, x = mine % 8;
+        const uint32_t mine = at - (uint32_t)t.P.tile[KIND] * nt, x = mine % 8;
         const uint32_t local = x * (n / 8) + (x < n % 8 ? x : n % 8) + mine / 8;
         const uint32_t band = local / (8 * mt), in = local % (8 * mt), height = nt - band * 8 < 8 ? nt - band * 8 : 8;
         t.tb = band * 8 + in % height;
@@ -585,30 +585,38 @@ __global__ __launch_bounds__(WM* WN* kWave) void i8_many(I8Args a, uint32_t tile
 }
 
 // Few rows (up to 16 TB): the weights are read once, straight into operands.  One
-// workgroup: 16 columns of out, its waves every kFewWaves-th piece of the row; their sums
-// are whole numbers, joined through LDS.
+// workgroup: 16 CB columns of out, its waves every kFewWaves-th piece of the row; their sums
+// are whole numbers, added up in LDS in any order.  A row's pieces are read once for
+// CB blocks of columns.
 constexpr int kFewWaves = 8;
-template <typename T, int TB> __global__ __launch_bounds__(kFewWaves* kWave) void i8_few(I8Args a) {
-    constexpr int UNROLL = TB == 1 ? 8 : 4;
-    __shared__ i32x4 s_acc[kFewWaves][TB][kWave];
-    const int p = uniform(product_of<&I8Prod::tile_few>(a.prods, a.n_prods, blockIdx.x));
+template <typename T, int TB, int CB, int KIND> __global__ __launch_bounds__(kFewWaves* kWave) void i8_few(I8Args a) {
+    constexpr int UNROLL = TB * CB >= 8 ? 2 : TB * CB >= 4 ? 4 : 8, BLOCKS = TB * CB;
+    static_assert(kI8Cols[KIND] == 16 * CB, "the kind's tiles");
+    __shared__ int s_acc[BLOCKS * 256];
+    for (int i = threadIdx.x; i < BLOCKS * 256; i += kFewWaves * kWave) s_acc[i] = 0;
+    const int p = uniform(product_of<KIND>(a.prods, a.n_prods, blockIdx.x));
     const I8Prod P = a.prods[p];
-    const int64_t ob = blockIdx.x - P.tile_few;
+    const int64_t ob = (int64_t)(blockIdx.x - P.tile[KIND]) * CB, last = (P.d + 15) / 16 - 1;
     const int lane = lane_id(), w = wave_id(), K = P.pieces;
-    const int8_t* W = P.w + ob * K * kI8Piece + lane * 16;
+    const int8_t* W[CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) W[c] = P.w + (ob + c < last ? ob + c : last) * K * kI8Piece + lane * 16;
     const int8_t* X = a.q + P.q0 * a.T16 * kI8Piece + lane * 16;
     bool row[TB];
 #pragma unroll
     for (int b = 0; b < TB; ++b) row[b] = b * 16 + lane % 16 < a.T;
-    i32x4 acc[TB];
+    i32x4 acc[CB][TB];
 #pragma unroll
-    for (int b = 0; b < TB; ++b) acc[b] = i32x4{0, 0, 0, 0};
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+        for (int b = 0; b < TB; ++b) acc[c][b] = i32x4{0, 0, 0, 0};
     for (int k0 = w; k0 < K; k0 += kFewWaves * UNROLL) {
-        u32x4 fw[UNROLL], fx[UNROLL][TB];
+        u32x4 fw[UNROLL][CB], fx[UNROLL][TB];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const int k = k0 + u * kFewWaves;
-            fw[u] = k < K ? ld128_nt(W + (int64_t)k * kI8Piece) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int c = 0; c < CB; ++c) fw[u][c] = k < K ? ld128_nt(W[c] + (int64_t)k * kI8Piece) : u32x4{0u, 0u, 0u, 0u};
         }
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
@@ -620,49 +628,62 @@ template <typename T, int TB> __global__ __launch_bounds__(kFewWaves* kWave) voi
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
-            for (int b = 0; b < TB; ++b) acc[b] = mfma(fw[u], fx[u][b], acc[b]);
+            for (int c = 0; c < CB; ++c)
+#pragma unroll
+                for (int b = 0; b < TB; ++b) acc[c][b] = mfma(fw[u][c], fx[u][b], acc[c][b]);
     }
+    __syncthreads();  // the sums are clear
 #pragma unroll
-    for (int b = 0; b < TB; ++b) s_acc[w][b][lane] = acc[b];
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) atomicAdd(&s_acc[(c * TB + b) * 256 + v * kWave + lane], acc[c][b][v]);
     __syncthreads();
-    if (w >= TB) return;
-    i32x4 sum = s_acc[0][w][lane];
+    for (int i = w; i < BLOCKS; i += kFewWaves) {
+        const int64_t t = i % TB * 16 + lane % 16, o = (ob + i / TB) * 16 + lane / 16 * 4;
+        i32x4 sum;
 #pragma unroll
-    for (int v = 1; v < kFewWaves; ++v) sum += s_acc[v][w][lane];
-    const int64_t t = w * 16 + lane % 16;
-    float sw[4];
-    column_scales(P, ob * 16 + lane / 16 * 4, sw);
-    if (t < a.T) put4<T>(P, t, ob * 16 + lane / 16 * 4, sum, gld(a.scale + P.rows * a.T16 * 16 + t), sw, a.accumulate != 0);
+        for (int v = 0; v < 4; ++v) sum[v] = s_acc[i * 256 + v * kWave + lane];
+        float sw[4];
+        column_scales(P, o, sw);
+        if (t < a.T) put4<T>(P, t, o, sum, gld(a.scale + P.rows * a.T16 * 16 + t), sw, a.accumulate != 0);
+    }
 }
 
 constexpr int64_t kCus = 256;  // a workgroup of the large tiles' takes a CU
-constexpr size_t kBigLds = 4 * (16 + 16) * kI8Piece, kMidLds = 4 * (8 + 8) * kI8Piece;
+constexpr size_t kBigLds = 4 * (16 + 16) * kI8Piece, kMidLds = 4 * (8 + 8) * kI8Piece, kSmallLds = 8 * (4 + 4) * kI8Piece;
+template <typename T> constexpr auto* kBigTile = &i8_many<T, 8, 4, 2, 4, 4, kI8Big>;
+template <typename T> constexpr auto* kMidTile = &i8_many<T, 4, 4, 2, 2, 4, kI8Mid>;
+template <typename T> constexpr auto* kSmallTile = &i8_many<T, 2, 2, 2, 2, 8, kI8Small>;
 
-template <typename T> hipError_t launch_products(const I8Args& a, hipStream_t s) {
-    if (a.T <= kI8FewT) {
-        const dim3 g((unsigned)a.tiles_few), n(kFewWaves * kWave);
-        if (!grid_fits(a.tiles_few, kFewWaves * kWave)) return hipErrorInvalidConfiguration;
-        if (a.T16 == 1) hipLaunchKernelGGL((i8_few<T, 1>), g, n, 0, s, a);
-        else if (a.T16 == 2) hipLaunchKernelGGL((i8_few<T, 2>), g, n, 0, s, a);
-        else hipLaunchKernelGGL((i8_few<T, 4>), g, n, 0, s, a);
-        return hipGetLastError();
-    }
-    const int64_t big = (a.T + kI8BigT - 1) / kI8BigT * a.tiles_big, mid = (a.T + kI8MidT - 1) / kI8MidT * a.tiles_mid;
-    if (!grid_fits(mid, 512)) return hipErrorInvalidConfiguration;
-    if (big >= 192)
-        hipLaunchKernelGGL((i8_many<T, 8, 4, 2, 4, 4, &I8Prod::tile_big>), dim3((unsigned)(big < kCus ? big : kCus)), dim3(512), kBigLds, s, a,
-                           (uint32_t)big);
+template <typename T, int TB> hipError_t launch_few(const I8Args& a, hipStream_t s) {
+    const dim3 n(kFewWaves * kWave);
+    // as many columns a workgroup as leave two for every CU
+    if (TB >= 4 && a.tiles[kI8Few4] >= 2 * kCus)
+        hipLaunchKernelGGL((i8_few<T, TB, 4, kI8Few4>), dim3((unsigned)a.tiles[kI8Few4]), n, 0, s, a);
+    else if (a.T > 4 && a.tiles[kI8Few2] >= 2 * kCus)
+        hipLaunchKernelGGL((i8_few<T, TB, 2, kI8Few2>), dim3((unsigned)a.tiles[kI8Few2]), n, 0, s, a);
     else
-        hipLaunchKernelGGL((i8_many<T, 4, 4, 2, 2, 4, &I8Prod::tile_mid>), dim3((unsigned)mid), dim3(256), kMidLds, s, a, (uint32_t)mid);
+        hipLaunchKernelGGL((i8_few<T, TB, 1, kI8Few1>), dim3((unsigned)a.tiles[kI8Few1]), n, 0, s, a);
+    return hipGetLastError();
+}
+template <typename T> hipError_t launch_products(const I8Args& a, hipStream_t s) {
+    if (!grid_fits(a.tiles[kI8Few1], kFewWaves * kWave)) return hipErrorInvalidConfiguration;
+    if (a.T <= kI8FewT) return a.T16 == 1 ? launch_few<T, 1>(a, s) : a.T16 == 2 ? launch_few<T, 2>(a, s) : launch_few<T, 4>(a, s);
+    const auto tiles = [&](int kind) { return (a.T + kI8Cols[kind] - 1) / kI8Cols[kind] * a.tiles[kind]; };  // (square tiles)
+    const int64_t big = tiles(kI8Big), mid = tiles(kI8Mid), small = tiles(kI8Small);
+    if (!grid_fits(small, 512)) return hipErrorInvalidConfiguration;
+    if (big >= 192) hipLaunchKernelGGL(kBigTile<T>, dim3((unsigned)(big < kCus ? big : kCus)), dim3(512), kBigLds, s, a, (uint32_t)big);
+    else if (mid >= 256) hipLaunchKernelGGL(kMidTile<T>, dim3((unsigned)mid), dim3(256), kMidLds, s, a, (uint32_t)mid);
+    else hipLaunchKernelGGL(kSmallTile<T>, dim3((unsigned)small), dim3(256), kSmallLds, s, a, (uint32_t)small);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t prepare_i8() {
-    const void* big[] = {(const void*)&i8_many<float, 8, 4, 2, 4, 4, &I8Prod::tile_big>,
-                         (const void*)&i8_many<uint16_t, 8, 4, 2, 4, 4, &I8Prod::tile_big>};
-    for (const void* f : big) {
+    for (const void* f : {(const void*)kBigTile<float>, (const void*)kBigTile<uint16_t>}) {
         const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBigLds);
         if (e != hipSuccess) return e;
     }

@@ -38,7 +38,7 @@ struct I8Prod {
     int32_t vec;           // rows of out take accesses of four elements
     int64_t q0;            // of its I8Rows
     int64_t rows;
-    int32_t tile_big, tile_mid, tile_few, pad;  // tiles of earlier products (per row tile)
+    int32_t tile[6], pad[2];  // tiles of earlier products (per row tile), by kind
 };
 
 struct I8Args {
@@ -46,7 +46,7 @@ struct I8Args {
     const I8Rows* rows;
     const I8Prod* prods;
     int32_t n_rows, n_prods;
-    int32_t tiles_big, tiles_mid, tiles_few;
+    int32_t tiles[6];     // of all products, by kind
     int64_t T, T16;       // rows, and 16-row blocks
     int64_t pieces;       // of all I8Rows together (per 16 rows)
     int32_t max_pieces;   // of the longest row
@@ -55,8 +55,11 @@ struct I8Args {
     int32_t accumulate;
 };
 
-// Tiles of the products: columns of out, and rows.
-constexpr int kI8BigD = 256, kI8BigT = 256, kI8MidD = 128, kI8MidT = 128, kI8FewD = 16, kI8FewT = 64;
+// Kinds of tiles, and their columns of out: many rows, in three sizes; few rows, by how
+// many 16-column blocks share a read of the rows.
+enum { kI8Big = 0, kI8Mid = 1, kI8Small = 2, kI8Few1 = 3, kI8Few2 = 4, kI8Few4 = 5 };
+constexpr int kI8Cols[6] = {256, 128, 64, 16, 32, 64};
+constexpr int kI8FewT = 64;  // rows that count as few
 
 hipError_t prepare_i8();
 hipError_t launch_i8_rows(const I8Args& a, int dtype, hipStream_t s);
