@@ -689,7 +689,13 @@ static int i8_launch(const char* call, dlm_i8_group* h, bool back, int64_t T, in
     a.q = (int8_t*)workspace;
     a.scale = (float*)((char*)workspace + scale_at);
     a.accumulate = accumulate ? 1 : 0;
-    hipError_t e = launch_i8_rows(a, h->dtype, (hipStream_t)stream);
+    a.plain = back ? 0 : 1;
+    hipError_t e;
+    if (i8_one_launch(a)) {
+        e = launch_i8_token(a, h->dtype, (hipStream_t)stream);
+        return e == hipSuccess ? ok() : hip_fail(e, call);
+    }
+    e = launch_i8_rows(a, h->dtype, (hipStream_t)stream);
     if (e == hipSuccess) e = launch_i8_products(a, h->dtype, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, call);
     return ok();

@@ -436,151 +436,150 @@ template <int KIND> __device__ __forceinline__ int product_of(const I8Prod* prod
     return lo;
 }
 
-// Many rows.  A tile: WM x WN waves of 16 MB columns of out x 16 NB rows each.  A workgroup
-// takes every gridDim.x-th tile and copies the next one's first pieces while it writes a
-// tile's results.  Pieces go from memory to LDS directly, STAGES - 1 steps of 64 columns
+// Many rows.  A workgroup's tile: WM x WN waves of 16 MB columns of out x 16 NB rows each,
+// and KG such groups of waves that take every KG-th piece of the sums (products with few
+// tiles would else wait for one another's latencies step by step; their sums are joined
+// through LDS).  Pieces go from memory to LDS directly, STAGES - 1 steps of 64 KG columns
 // ahead of the products; a step's pieces are overwritten one barrier after all waves have
 // read them.
-template <typename T, int MB, int NB, int WM, int WN, int STAGES, int KIND>
-__global__ __launch_bounds__(WM* WN* kWave) void i8_many(I8Args a, uint32_t tiles) {
-    constexpr int WAVES = WM * WN, PA = MB * WM, PB = NB * WN, PER = (PA + PB) / WAVES;
-    static_assert(kI8Cols[KIND] == 16 * PA && (PA + PB) % WAVES == 0, "every wave copies the same number of pieces");
+template <typename T, int MB, int NB, int WM, int WN, int KG, int STAGES, int KIND>
+__global__ __launch_bounds__(WM* WN* KG* kWave) void i8_many(I8Args a) {
+    constexpr int WAVES = WM * WN, PA = MB * WM, PB = NB * WN, PER = (PA + PB) / WAVES, STAGE = (PA + PB) * KG * kI8Piece;
+    static_assert(kI8Cols[KIND] == 16 * PA && (PA + PB) % WAVES == 0 && MB % 2 == 0, "every wave copies the same number of pieces");
+    static_assert(KG == 1 || WAVES * KG * MB * NB * kI8Piece <= STAGES * STAGE, "the groups' sums fit LDS");
     extern __shared__ __align__(16) char smem[];
-    const int lane = lane_id(), w = wave_id(), wm = w % WM, wn = w / WM;
+    const int lane = lane_id(), w = wave_id() % WAVES, kg = wave_id() / WAVES, wm = w % WM, wn = w / WM;
     const uint32_t lane16 = lane * 16;
     const uint32_t nt = (uint32_t)((a.T16 + PB - 1) / PB);
-    struct Tile {
-        I8Prod P;
-        int64_t ob, tb;
-        const int8_t* src[PER];  // the wave's pieces
-    };
-    const auto locate = [&](uint32_t at, Tile& t) {
-        const int p = uniform(product_of<KIND>(a.prods, a.n_prods, (int)(at / nt)));
-        t.P = a.prods[p];
-        // Consecutive tiles go round the XCDs: each XCD takes a run of neighbouring tiles of every
-        // product (of all products together one XCD would get the longest sums).  The tiles go in bands
-        // of eight rows of tiles, column after column: neighbours share both operands.
-        const uint32_t mt = (uint32_t)((t.P.d + 16 * PA - 1) / (16 * PA)), n = mt * nt;
-        const uint32_t mine = at - (uint32_t)t.P.tile[KIND] * nt, x = mine % 8;
-        const uint32_t local = x * (n / 8) + (x < n % 8 ? x : n % 8) + mine / 8;
-        const uint32_t band = local / (8 * mt), in = local % (8 * mt), height = nt - band * 8 < 8 ? nt - band * 8 : 8;
-        t.tb = band * 8 + in % height;
-        t.ob = in / height;
-        // the first PA pieces of a step are W's, the others the rows' (blocks past the end: the last)
-        const int64_t o16 = (t.P.d + 15) / 16;
+    const int p = uniform(product_of<KIND>(a.prods, a.n_prods, (int)(blockIdx.x / nt)));
+    const I8Prod P = a.prods[p];
+    // Consecutive workgroups go round the XCDs: each XCD takes a run of neighbouring tiles of every
+    // product (of all products together one XCD would get the longest sums).  The tiles go in bands
+    // of eight rows of tiles, column after column: neighbours share both operands.
+    const uint32_t mt = (uint32_t)((P.d + 16 * PA - 1) / (16 * PA)), n = mt * nt;
+    const uint32_t mine = blockIdx.x - (uint32_t)P.tile[KIND] * nt, x = mine % 8;
+    const uint32_t local = x * (n / 8) + (x < n % 8 ? x : n % 8) + mine / 8;
+    const uint32_t band = local / (8 * mt), in = local % (8 * mt), height = nt - band * 8 < 8 ? nt - band * 8 : 8;
+    const int64_t tb = band * 8 + in % height, ob = in / height;
+    // this wave's pieces of a step: the first PA are W's, the others the rows' (blocks past the end: the last)
+    const int64_t o16 = (P.d + 15) / 16;
+    const int8_t* src[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int piece = w * PER + i;
-            int64_t b;
-            if (piece < PA) {
-                b = t.ob * PA + piece;
-                t.src[i] = t.P.w + (b < o16 ? b : o16 - 1) * t.P.pieces * kI8Piece;
-            } else {
-                b = t.tb * PB + piece - PA;
-                t.src[i] = a.q + (t.P.q0 * a.T16 + (b < a.T16 ? b : a.T16 - 1) * t.P.pieces) * kI8Piece;
-            }
+    for (int i = 0; i < PER; ++i) {
+        const int piece = w * PER + i;
+        int64_t b;
+        if (piece < PA) {
+            b = ob * PA + piece;
+            src[i] = P.w + (b < o16 ? b : o16 - 1) * P.pieces * kI8Piece;
+        } else {
+            b = tb * PB + piece - PA;
+            src[i] = a.q + (P.q0 * a.T16 + (b < a.T16 ? b : a.T16 - 1) * P.pieces) * kI8Piece;
         }
-    };
-    const auto copy = [&](const Tile& t, int k) {
-        char* to = smem + (k % STAGES) * (PA + PB) * kI8Piece + w * PER * kI8Piece;
+    }
+    char* const lds = smem + kg * (PA + PB) * kI8Piece;
+    const auto copy = [&](int k) {
+        char* to = lds + (k % STAGES) * STAGE + w * PER * kI8Piece;
+        int piece = k * KG + kg;  // (past the end: the last, which is not multiplied again)
+        if (KG > 1 && piece >= P.pieces) piece = P.pieces - 1;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) copy16_to_lds(t.src[i] + (int64_t)k * kI8Piece + lane16, to + i * kI8Piece);
+        for (int i = 0; i < PER; ++i) copy16_to_lds(src[i] + (int64_t)piece * kI8Piece + lane16, to + i * kI8Piece);
     };
-    const auto begin = [&](uint32_t at, Tile& t) {
-        locate(at, t);
+    i32x4 acc[MB][NB];
 #pragma unroll
-        for (int k = 0; k < STAGES; ++k)
-            if (k < t.P.pieces) copy(t, k);
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    // Step k's operands are in registers while those of step k + 1 are read from LDS between its
+    // products; one barrier a step: past it step k + 1's pieces are in LDS, and step k's, read by all
+    // waves, make room for step k + STAGES.
+    const int K = (P.pieces + KG - 1) / KG;
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k)
+        if (k < K) copy(k);
+    u32x4 fa[2][MB], fb[2][NB];
+    const auto read = [&](int k, int to) {
+        const char* st = lds + (k % STAGES) * STAGE + lane16;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) fb[to][j] = *(const u32x4*)(st + (PA + wn * NB + j) * kI8Piece);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) fa[to][i] = *(const u32x4*)(st + (wm * MB + i) * kI8Piece);
     };
-    Tile now;
-    uint32_t at = blockIdx.x;
-    begin(at, now);
-    while (true) {
-        i32x4 acc[MB][NB];
+    const auto multiply = [&](int of) {
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-        // Step k's operands are in registers while those of step k + 1 are read from LDS between its
-        // products; one barrier a step: past it step k + 1's pieces are in LDS, and step k's, read by all
-        // waves, make room for step k + STAGES.
-        const int K = now.P.pieces;
-        u32x4 fa[2][MB], fb[2][NB];
-        const auto read = [&](int k, int to) {
-            const char* st = smem + (k % STAGES) * (PA + PB) * kI8Piece + lane * 16;
-#pragma unroll
-            for (int j = 0; j < NB; ++j) fb[to][j] = *(const u32x4*)(st + (PA + wn * NB + j) * kI8Piece);
-#pragma unroll
-            for (int i = 0; i < MB; ++i) fa[to][i] = *(const u32x4*)(st + (wm * MB + i) * kI8Piece);
-        };
-        const auto multiply = [&](int of) {
-#pragma unroll
-            for (int i = 0; i < MB; ++i)
-#pragma unroll
-                for (int j = 0; j < NB; ++j) acc[i][j] = mfma(fa[of][i], fb[of][j], acc[i][j]);
-        };
-        // (in flight when step k + 1 has to be there: k + 2 .. k + STAGES - 1)
-        const auto ahead = [&](int k, int to) {
-            wait_vmcnt_le<(STAGES - 2) * PER>((K - 2 - k < STAGES - 2 ? K - 2 - k : STAGES - 2) * PER);
-            step_barrier();
-            if (k + STAGES < K) copy(now, k + STAGES);
-            read(k + 1, to);
-        };
-        wait_vmcnt_le<(STAGES - 1) * PER>((K - 1 < STAGES - 1 ? K - 1 : STAGES - 1) * PER);
+            for (int j = 0; j < NB; ++j) acc[i][j] = mfma(fa[of][i], fb[of][j], acc[i][j]);
+    };
+    // (in flight when step k + 1 has to be there: k + 2 .. k + STAGES - 1)
+    const auto ahead = [&](int k, int to) {
+        wait_vmcnt_le<(STAGES - 2) * PER>((K - 2 - k < STAGES - 2 ? K - 2 - k : STAGES - 2) * PER);
         step_barrier();
-        read(0, 0);
-        int k = 0;  // K is even
-        for (; k + 2 < K; k += 2) {
-            ahead(k, 1);
-            multiply(0);
-            between<MB, NB>();
-            ahead(k + 1, 0);
-            multiply(1);
-            between<MB, NB>();
-        }
+        if (k + STAGES < K) copy(k + STAGES);
+        read(k + 1, to);
+    };
+    wait_vmcnt_le<(STAGES - 1) * PER>((K - 1 < STAGES - 1 ? K - 1 : STAGES - 1) * PER);
+    step_barrier();
+    read(0, 0);
+    int k = 0;
+    for (; k + 2 < K; k += 2) {
         ahead(k, 1);
         multiply(0);
         between<MB, NB>();
+        ahead(k + 1, 0);
         multiply(1);
-        const I8Prod P = now.P;
-        const int64_t ob = now.ob, tb = now.tb;
-        at += gridDim.x;
-        const bool more = at < tiles;
-        if (more) {
-            step_barrier();  // every wave has read its last pieces
-            begin(at, now);
+        between<MB, NB>();
+    }
+    const bool whole = KG == 1 || (K - 1) * KG + kg < P.pieces;  // the last step has a piece for this group
+    if (KG == 1 || k + 1 < K) {  // (KG == 1: K is even)
+        ahead(k, 1);
+        multiply(0);
+        between<MB, NB>();
+        if (whole) multiply(1);
+    } else if (whole) {
+        multiply(0);
+    }
+    if constexpr (KG > 1) {
+        step_barrier();  // every wave has read its last pieces
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) *(i32x4*)(smem + ((wave_id() * MB + i) * NB + j) * kI8Piece + lane16) = acc[i][j];
+        step_barrier();
+    }
+    // the sum of the groups' tile (i, j)
+    const auto sum = [&](int i, int j) {
+        i32x4 r = acc[i][j];
+        if constexpr (KG > 1) {
+            r = i32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int g = 0; g < KG; ++g) r += *(const i32x4*)(smem + (((g * WAVES + w) * MB + i) * NB + j) * kI8Piece + lane16);
         }
-        float sr[NB];
+        return r;
+    };
+    float sr[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        const int64_t t = (tb * PB + wn * NB + j) * 16 + lane % 16;
+        sr[j] = t < a.T ? gld(a.scale + P.rows * a.T16 * 16 + t) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < MB; i += 2) {
+        const int64_t o0 = (ob * PA + wm * MB + i) * 16;
+        float w0[4], w1[4];
+        column_scales(P, o0 + lane / 16 * 4, w0);
+        column_scales(P, o0 + 16 + lane / 16 * 4, w1);
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-            const int64_t t = (tb * PB + wn * NB + j) * 16 + lane % 16;
-            sr[j] = t < a.T ? gld(a.scale + P.rows * a.T16 * 16 + t) : 0.f;
-        }
-        if (sizeof(T) == 2 && P.vec) {
-#pragma unroll
-            for (int i = 0; i < MB; i += 2) {
-                const int64_t o0 = (ob * PA + wm * MB + i) * 16;
-                float w0[4], w1[4];
-                column_scales(P, o0 + lane / 16 * 4, w0);
-                column_scales(P, o0 + 16 + lane / 16 * 4, w1);
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    put8(P, a.T, (tb * PB + wn * NB + j) * 16 + lane % 16, o0, acc[i][j], acc[i + 1][j], sr[j], w0, w1, a.accumulate != 0);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                const int64_t o = (ob * PA + wm * MB + i) * 16 + lane / 16 * 4;
-                float sw[4];
-                column_scales(P, o, sw);
-#pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    const int64_t t = (tb * PB + wn * NB + j) * 16 + lane % 16;
-                    if (t < a.T) put4<T>(P, t, o, acc[i][j], sr[j], sw, a.accumulate != 0);
-                }
+            if (KG > 1 && (i / 2 * NB + j) % KG != kg) continue;  // another group's to write
+            const i32x4 a0 = sum(i, j), a1 = sum(i + 1, j);
+            const int64_t t = (tb * PB + wn * NB + j) * 16 + lane % 16, o = o0 + lane / 16 * 4;
+            if (sizeof(T) == 2 && P.vec) {
+                put8(P, a.T, t, o0, a0, a1, sr[j], w0, w1, a.accumulate != 0);
+            } else if (t < a.T) {
+                put4<T>(P, t, o, a0, sr[j], w0, a.accumulate != 0);
+                put4<T>(P, t, o + 16, a1, sr[j], w1, a.accumulate != 0);
             }
         }
-        if (!more) return;
     }
 }
 
@@ -590,7 +589,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void i8_many(I8Args a, uint32_t tile
 // CB blocks of columns.
 constexpr int kFewWaves = 8;
 template <typename T, int TB, int CB, int KIND> __global__ __launch_bounds__(kFewWaves* kWave) void i8_few(I8Args a) {
-    constexpr int UNROLL = TB * CB >= 8 ? 2 : TB * CB >= 4 ? 4 : 8, BLOCKS = TB * CB;
+    constexpr int UNROLL = TB * CB >= 16 ? 1 : TB * CB >= 8 ? 2 : TB * CB >= 4 ? 4 : 8, BLOCKS = TB * CB;
     static_assert(kI8Cols[KIND] == 16 * CB, "the kind's tiles");
     __shared__ int s_acc[BLOCKS * 256];
     for (int i = threadIdx.x; i < BLOCKS * 256; i += kFewWaves * kWave) s_acc[i] = 0;
@@ -651,11 +650,111 @@ template <typename T, int TB, int CB, int KIND> __global__ __launch_bounds__(kFe
     }
 }
 
+// One to four rows, codes and products in one launch: every workgroup makes the codes of its
+// product's rows itself, in LDS, while its first weights are on their way.  ROWS: 1, 2 or 4,
+// an equal number of waves for each.
+constexpr int kTokenLds = 48 << 10;  // codes, a row's pieces and 64 bytes (LDS banks) each
+template <typename T, int ROWS> __global__ __launch_bounds__(kFewWaves* kWave) void i8_token(I8Args a) {
+    constexpr int UNROLL = 8, NT = kFewWaves * kWave / ROWS, KEEP = 2;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ int s_acc[256];
+    __shared__ double s_max[kFewWaves];
+    __shared__ float s_scale[4];
+    const int tid = threadIdx.x;
+    if (tid < 256) s_acc[tid] = 0;
+    const int p = uniform(product_of<kI8Few1>(a.prods, a.n_prods, blockIdx.x));
+    const I8Prod P = a.prods[p];
+    const int64_t ob = blockIdx.x - P.tile[kI8Few1];
+    const int lane = lane_id(), w = wave_id(), K = P.pieces, pitch = K * 64 + 64;
+    const int8_t* W = P.w + ob * K * kI8Piece + lane * 16;
+    u32x4 fw[UNROLL];
+    const auto weights = [&](int k0) {
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int k = k0 + u * kFewWaves;
+            fw[u] = k < K ? ld128_nt(W + (int64_t)k * kI8Piece) : u32x4{0u, 0u, 0u, 0u};
+        }
+    };
+    weights(w);
+    {
+        const int r = tid / NT, t = tid % NT, groups = K * 4;
+        const I8Seg S = a.segs[a.rows[P.rows].seg0];
+        const bool live = r < a.T;
+        const T* x = (const T*)S.x + (live ? r : 0) * S.d;
+        const Scale16 one(nullptr, 0, 0);
+        Raw16<T> keep[KEEP];
+        double top = 0.0;
+        const auto raise = [&](const Raw16<T>& f) {
+            const double m = top16(f, one);
+            top = top > m ? top : m;
+        };
+#pragma unroll
+        for (int c = 0; c < KEEP; ++c)
+            if (c * NT + t < groups) load16(x, (int64_t)(c * NT + t) * 16, S.d, S.vec, keep[c]);
+#pragma unroll
+        for (int c = 0; c < KEEP; ++c)
+            if (c * NT + t < groups) raise(keep[c]);
+        for (int g = KEEP * NT + t; g < groups; g += NT) {
+            Raw16<T> f;
+            load16(x, (int64_t)g * 16, S.d, S.vec, f);
+            raise(f);
+        }
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) {
+            const double q = __shfl_xor(top, o, kWave);
+            top = top > q ? top : q;
+        }
+        if (lane == 0) s_max[w] = top;
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < kFewWaves / ROWS; ++v) {
+            const double q = s_max[w / (kFewWaves / ROWS) * (kFewWaves / ROWS) + v];
+            top = top > q ? top : q;
+        }
+        double by;
+        float scale;
+        row_scale(top, &by, &scale);
+        if (t == 0) s_scale[r] = scale;
+        char* out = smem + r * pitch;
+#pragma unroll
+        for (int c = 0; c < KEEP; ++c)
+            if (c * NT + t < groups) *(u32x4*)(out + (c * NT + t) * 16) = codes16(keep[c], one, by);
+        for (int g = KEEP * NT + t; g < groups; g += NT) {
+            Raw16<T> f;
+            load16(x, (int64_t)g * 16, S.d, S.vec, f);
+            *(u32x4*)(out + g * 16) = codes16(f, one, by);
+        }
+        __syncthreads();
+    }
+    const bool row = lane % 16 < a.T;
+    const char* X = smem + (row ? lane % 16 : 0) * pitch + lane / 16 * 16;
+    i32x4 acc = {0, 0, 0, 0};
+    for (int k0 = w; k0 < K; k0 += kFewWaves * UNROLL) {
+        if (k0 != w) weights(k0);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int k = k0 + u * kFewWaves;
+            const u32x4 fx = k < K && row ? *(const u32x4*)(X + k * 64) : u32x4{0u, 0u, 0u, 0u};
+            acc = mfma(fw[u], fx, acc);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) atomicAdd(&s_acc[v * kWave + lane], acc[v]);
+    __syncthreads();
+    if (w != 0 || !row) return;
+    i32x4 sum;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sum[v] = s_acc[v * kWave + lane];
+    float sw[4];
+    column_scales(P, ob * 16 + lane / 16 * 4, sw);
+    put4<T>(P, lane % 16, ob * 16 + lane / 16 * 4, sum, s_scale[lane % 16], sw, a.accumulate != 0);
+}
+
 constexpr int64_t kCus = 256;  // a workgroup of the large tiles' takes a CU
-constexpr size_t kBigLds = 4 * (16 + 16) * kI8Piece, kMidLds = 4 * (8 + 8) * kI8Piece, kSmallLds = 8 * (4 + 4) * kI8Piece;
-template <typename T> constexpr auto* kBigTile = &i8_many<T, 8, 4, 2, 4, 4, kI8Big>;
-template <typename T> constexpr auto* kMidTile = &i8_many<T, 4, 4, 2, 2, 4, kI8Mid>;
-template <typename T> constexpr auto* kSmallTile = &i8_many<T, 2, 2, 2, 2, 8, kI8Small>;
+constexpr size_t kBigLds = 4 * (16 + 16) * kI8Piece, kMidLds = 4 * 2 * (8 + 8) * kI8Piece, kSmallLds = 4 * 4 * (4 + 4) * kI8Piece;
+template <typename T> constexpr auto* kBigTile = &i8_many<T, 8, 4, 2, 4, 1, 4, kI8Big>;
+template <typename T> constexpr auto* kMidTile = &i8_many<T, 4, 4, 2, 2, 2, 4, kI8Mid>;
+template <typename T> constexpr auto* kSmallTile = &i8_many<T, 2, 2, 2, 2, 4, 4, kI8Small>;
 
 template <typename T, int TB> hipError_t launch_few(const I8Args& a, hipStream_t s) {
     const dim3 n(kFewWaves * kWave);
@@ -673,23 +772,44 @@ template <typename T> hipError_t launch_products(const I8Args& a, hipStream_t s)
     if (a.T <= kI8FewT) return a.T16 == 1 ? launch_few<T, 1>(a, s) : a.T16 == 2 ? launch_few<T, 2>(a, s) : launch_few<T, 4>(a, s);
     const auto tiles = [&](int kind) { return (a.T + kI8Cols[kind] - 1) / kI8Cols[kind] * a.tiles[kind]; };  // (square tiles)
     const int64_t big = tiles(kI8Big), mid = tiles(kI8Mid), small = tiles(kI8Small);
-    if (!grid_fits(small, 512)) return hipErrorInvalidConfiguration;
-    if (big >= 192) hipLaunchKernelGGL(kBigTile<T>, dim3((unsigned)(big < kCus ? big : kCus)), dim3(512), kBigLds, s, a, (uint32_t)big);
-    else if (mid >= 256) hipLaunchKernelGGL(kMidTile<T>, dim3((unsigned)mid), dim3(256), kMidLds, s, a, (uint32_t)mid);
-    else hipLaunchKernelGGL(kSmallTile<T>, dim3((unsigned)small), dim3(256), kSmallLds, s, a, (uint32_t)small);
+    if (!grid_fits(small, 1024)) return hipErrorInvalidConfiguration;
+    // A CU takes one tile at a time, of 256, 128 or 64 square: rounds of a tile for every CU last as 24 : 10 : 4 (54, 22
+    // and 9 us at 4096 columns summed).  512 rows of two 11008 x 4096 products: 58 us in large tiles, 67 in middle ones;
+    // 2048 rows of one 4096 x 4096: 56 in middle ones, 65 in large, 81 in small; 128 rows 13.5 in small ones, 22 in middle.
+    const auto rounds = [](int64_t n) { return (n + kCus - 1) / kCus; };
+    const int64_t tb = 24 * rounds(big), tm = 10 * rounds(mid), ts = 4 * rounds(small);
+    if (tb <= tm && tb <= ts) hipLaunchKernelGGL(kBigTile<T>, dim3((unsigned)big), dim3(512), kBigLds, s, a);
+    else if (tm <= ts) hipLaunchKernelGGL(kMidTile<T>, dim3((unsigned)mid), dim3(512), kMidLds, s, a);
+    else hipLaunchKernelGGL(kSmallTile<T>, dim3((unsigned)small), dim3(1024), kSmallLds, s, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t prepare_i8() {
-    for (const void* f : {(const void*)kBigTile<float>, (const void*)kBigTile<uint16_t>}) {
+    static_assert(kMidLds == kBigLds && kSmallLds == kBigLds, "all tiles take the same LDS");
+    for (const void* f : {(const void*)kBigTile<float>, (const void*)kBigTile<uint16_t>, (const void*)kMidTile<float>,
+                          (const void*)kMidTile<uint16_t>, (const void*)kSmallTile<float>, (const void*)kSmallTile<uint16_t>}) {
         const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBigLds);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
+bool i8_one_launch(const I8Args& a) {
+    const int rows = a.T == 1 ? 1 : a.T == 2 ? 2 : 4;
+    return a.T <= 4 && a.plain && rows * a.tiles[kI8Few1] <= 2048 && rows * (a.max_pieces * 64 + 64) <= kTokenLds;
+}
+hipError_t launch_i8_token(const I8Args& a, int dtype, hipStream_t s) {
+    const int rows = a.T == 1 ? 1 : a.T == 2 ? 2 : 4;
+    const dim3 g((unsigned)a.tiles[kI8Few1]), n(kFewWaves * kWave);
+    if (!grid_fits(a.tiles[kI8Few1], kFewWaves * kWave)) return hipErrorInvalidConfiguration;
+    const size_t lds = (size_t)rows * (a.max_pieces * 64 + 64);
+    const auto go = [&](auto k1, auto k2, auto k4) { hipLaunchKernelGGL(rows == 1 ? k1 : rows == 2 ? k2 : k4, g, n, lds, s, a); };
+    if (dtype == 0) go(i8_token<float, 1>, i8_token<float, 2>, i8_token<float, 4>);
+    else go(i8_token<uint16_t, 1>, i8_token<uint16_t, 2>, i8_token<uint16_t, 4>);
+    return hipGetLastError();
+}
 hipError_t launch_i8_rows(const I8Args& a, int dtype, hipStream_t s) {
     const auto go = [&](auto kernel, int rows, int threads) {
         // many rows: whole runs of 128, which go round the XCDs 16 at a time

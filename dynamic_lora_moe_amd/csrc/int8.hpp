@@ -50,6 +50,7 @@ struct I8Args {
     int64_t T, T16;       // rows, and 16-row blocks
     int64_t pieces;       // of all I8Rows together (per 16 rows)
     int32_t max_pieces;   // of the longest row
+    int32_t plain;        // every row of codes is one run without factors
     int8_t* q;            // codes: matrix i at q0_i * T16 pieces
     float* scale;         // [n_rows][T16 * 16]
     int32_t accumulate;
@@ -62,6 +63,9 @@ constexpr int kI8Cols[6] = {256, 128, 64, 16, 32, 64};
 constexpr int kI8FewT = 64;  // rows that count as few
 
 hipError_t prepare_i8();
+// Whether codes and products take one launch (few rows, codes that fit LDS), and that launch.
+bool i8_one_launch(const I8Args& a);
+hipError_t launch_i8_token(const I8Args& a, int dtype, hipStream_t s);
 hipError_t launch_i8_rows(const I8Args& a, int dtype, hipStream_t s);
 hipError_t launch_i8_products(const I8Args& a, int dtype, hipStream_t s);
 // Weights: row-major codes to pieces, and from pieces to their transpose's at `k0`.

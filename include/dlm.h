@@ -584,7 +584,8 @@ int dlm_i8_group_destroy(dlm_i8_group* h);
  * q and s the row's codes and scale as dlm_i8_quantize makes them.  The sum is exact; the
  * factors are applied in fp32.  A row of x that is not finite gives NaN in its row of y,
  * and nothing else.  Two launches (the codes, once for problems that share an x; the
- * products), no allocation.  Up to 64 rows the weights are read once, straight into the
+ * products), no allocation; one for up to four rows whose codes fit a workgroup's LDS (four
+ * of 11008 columns do).  Up to 64 rows the weights are read once, straight into the
  * products' operands.  T = 0 enqueues nothing.
  * workspace: >= dlm_i8_group_workspace_size(h, T) bytes, 256-byte aligned, of any content.
  */
