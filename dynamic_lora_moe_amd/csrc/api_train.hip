@@ -239,7 +239,7 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
             d.wd = q.weight_decay;
             d.scale = q.scale;
             nbs[i] = side <= 16 ? 1 : side <= 32 ? 2 : side <= kMuonTileSide ? 4 : 0;
-            const int chunk = muon_chunk(nbs[i] ? nbs[i] : 4);
+            const int chunk = nbs[i] ? muon_chunk(nbs[i]) : kMuonBigChunk;
             if ((d.d + chunk - 1) / chunk > (1 << 30)) return bad(fail(DLM_ESHAPE, "muon_create: tensor %d: too long", i));
             d.chunks = (int32_t)((d.d + chunk - 1) / chunk);
             v.push_back(span(q.p, elems * ps, true, "p", i));
@@ -329,11 +329,11 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
                     ts.push_back(at);
                     tsp.push_back(p);
                 }
-                for (int blk = 0; blk < nb * nb; blk += 4) {
+                for (int blk = 0; blk < nb * nb; ++blk) {
                     tm.push_back(at);
                     tma.push_back(blk);
                 }
-                for (int o = 0; o < d.chunks * groups; ++o) {
+                for (int o = 0; o < (d.d + 63) / 64 * groups; ++o) {
                     to.push_back(at);
                     toa.push_back(o);
                 }

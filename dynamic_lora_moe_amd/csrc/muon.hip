@@ -43,8 +43,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ d4 mfma(double a, double b, d4 c) { return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0); }
 
-__device__ __forceinline__ float load1(const float* p) { return gld(p); }
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf_to_f(gld(p)); }
+__device__ __forceinline__ float read1(const float* p) { return gld(p); }
+__device__ __forceinline__ float read1(const uint16_t* p) { return bf_to_f(gld(p)); }
 __device__ __forceinline__ void store1(float* p, float f) { gst(p, f); }
 __device__ __forceinline__ void store1(uint16_t* p, float f) { gst(p, f_to_bf(f)); }
 
@@ -61,24 +61,47 @@ __device__ __forceinline__ void load4(const uint16_t* p, float (&f)[4]) {
         f[2 * j + 1] = bf_hi(r[j]);
     }
 }
-__device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
-    st128(p, u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])});
+template <typename T> __device__ __forceinline__ void store4(T* p, const float (&f)[4]) {
+    if constexpr (sizeof(T) == 4) st128(p, u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])});
+    else gst((u32x2*)p, u32x2{pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3])});
 }
-__device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
-    gst((u32x2*)p, u32x2{pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3])});
-}
-// Four neighbours of which nv are inside (vec: all or none), 0 for the others.
-template <typename T> __device__ __forceinline__ void read4(const T* p, int64_t i, int nv, bool vec, float (&f)[4]) {
-    if (vec && nv >= 4) {
-        load4(p + i, f);
-    } else {
+// The same for what is used for the last time, past the caches (which keep what a later
+// launch reads again).
+__device__ __forceinline__ void load4_nt(const float* p, float (&f)[4]) {
+    const u32x4 r = ld128_nt(p);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = !vec && j < nv ? load1(p + i + j) : 0.f;
+    for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(r[j]);
+}
+__device__ __forceinline__ void load4_nt(const uint16_t* p, float (&f)[4]) {
+    const u32x2 r = __builtin_nontemporal_load((gcptr<u32x2>)p);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        f[2 * j] = bf_lo(r[j]);
+        f[2 * j + 1] = bf_hi(r[j]);
     }
 }
-template <typename T> __device__ __forceinline__ void write4(T* p, int64_t i, int nv, bool vec, const float (&f)[4]) {
+__device__ __forceinline__ void store4_nt(float* p, const float (&f)[4]) {
+    st128_nt(p, u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])});
+}
+__device__ __forceinline__ void store4_nt(uint16_t* p, const float (&f)[4]) {
+    __builtin_nontemporal_store(u32x2{pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3])}, (gptr<u32x2>)p);
+}
+// Four neighbours of which nv are inside (vec: all or none), 0 for the others.
+template <bool NT = false, typename T>
+__device__ __forceinline__ void read4(const T* p, int64_t i, int nv, bool vec, float (&f)[4]) {
     if (vec && nv >= 4) {
-        store4(p + i, f);
+        if constexpr (NT) load4_nt(p + i, f);
+        else load4(p + i, f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = !vec && j < nv ? read1(p + i + j) : 0.f;
+    }
+}
+template <bool NT = false, typename T>
+__device__ __forceinline__ void write4(T* p, int64_t i, int nv, bool vec, const float (&f)[4]) {
+    if (vec && nv >= 4) {
+        if constexpr (NT) store4_nt(p + i, f);
+        else store4(p + i, f);
     } else if (!vec) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -109,80 +132,83 @@ struct Place {
 
 // From the gradient and the momentum,
 template <typename G> struct FromState {
+    struct Raw {
+        float g[4], m[4];
+    };
     const G* g;
     const float* m;
     Mom mom;
-    __device__ __forceinline__ void get4(int64_t i, int nv, bool vec, float (&u)[4]) const {
-        float gv[4], mv[4];
-        read4(g, i, nv, vec, gv);
-        read4(m, i, nv, vec, mv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = mom.u(mom.m(mv[j], gv[j]), gv[j]);
+    __device__ __forceinline__ void load4(int64_t i, int nv, bool vec, Raw& r) const {
+        read4(g, i, nv, vec, r.g);
+        read4(m, i, nv, vec, r.m);
     }
-    __device__ __forceinline__ float get1(int64_t i, bool in) const {
-        const float gv = in ? load1(g + i) : 0.f, mv = in ? gld(m + i) : 0.f;
-        return mom.u(mom.m(mv, gv), gv);
+    __device__ __forceinline__ void load1(int64_t i, bool in, int c, Raw& r) const {
+        r.g[c] = in ? read1(g + i) : 0.f;
+        r.m[c] = in ? gld(m + i) : 0.f;
     }
+    __device__ __forceinline__ float u(const Raw& r, int c) const { return mom.u(mom.m(r.m[c], r.g[c]), r.g[c]); }
 };
 // or from the scratch where a launch has left it.
 struct FromScratch {
-    const float* u;
-    __device__ __forceinline__ void get4(int64_t i, int nv, bool vec, float (&f)[4]) const { read4(u, i, nv, vec, f); }
-    __device__ __forceinline__ float get1(int64_t i, bool in) const { return in ? gld(u + i) : 0.f; }
+    struct Raw {
+        float u[4];
+    };
+    const float* p;
+    __device__ __forceinline__ void load4(int64_t i, int nv, bool vec, Raw& r) const { read4(p, i, nv, vec, r.u); }
+    __device__ __forceinline__ void load1(int64_t i, bool in, int c, Raw& r) const { r.u[c] = in ? gld(p + i) : 0.f; }
+    __device__ __forceinline__ float u(const Raw& r, int c) const { return r.u[c]; }
 };
 
 // ---- Gram matrices of pieces ------------------------------------------------------------
 
 // Operands of one wave's share of columns [lo, hi) of the long side, for NB blocks of the
-// small side from i0 on, handed to `use(a)` four columns at a time.  Wide: a lane loads
+// small side from i0 on, handed to `use(a)` four columns at a time; the loads of the next 16 S
+// columns are out while these are used.  WAVES of them share the columns.  Wide: a lane loads
 // four neighbours of its row; tall: the small side is contiguous, and a wave's lanes are.
-template <int NB, int S, typename SRC, typename F>
+template <bool WIDE, int NB, int S, int WAVES, typename SRC, typename F>
 __device__ __forceinline__ void long_side(const SRC& src, const Place& q, const int (&i0)[NB], int64_t lo, int64_t hi, F use) {
     const int lane = lane_id();
-    if (q.wide) {
-        const int row = lane % 16, sub = 4 * (lane / 16);
-        for (int64_t j0 = lo + wave_id() * 16 * S; j0 < hi; j0 += kWaves * 16 * S) {
-            float u[NB][S][4];
+    constexpr int STEP = WAVES * 16 * S;
+    typename SRC::Raw raw[2][NB][S];
+    const auto load = [&](int64_t j0, typename SRC::Raw (&r)[NB][S]) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+        for (int s = 0; s < S; ++s)
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    const int64_t j = j0 + 16 * s + sub;
-                    const int i = i0[b] + row;
-                    const int64_t left = hi - j;
-                    const int nv = i < q.n && left > 0 ? (left < 4 ? (int)left : 4) : 0;
-                    src.get4(q.at(i, j), nv, q.vec, u[b][s]);
+            for (int b = 0; b < NB; ++b) {
+                if constexpr (WIDE) {
+                    const int64_t j = j0 + 16 * s + 4 * (lane / 16), left = hi - j;
+                    const int i = i0[b] + lane % 16;
+                    src.load4(q.at(i, j), i < q.n && left > 0 ? (left < 4 ? (int)left : 4) : 0, q.vec, r[b][s]);
+                } else {
+                    const int i = i0[b] + lane % 16;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int64_t j = j0 + 16 * s + 4 * c + lane / 16;
+                        src.load1(q.at(i, j), i < q.n && j < hi, c, r[b][s]);
+                    }
                 }
+            }
+    };
+    const auto spend = [&](const typename SRC::Raw (&r)[NB][S]) {
 #pragma unroll
-            for (int s = 0; s < S; ++s)
+        for (int s = 0; s < S; ++s)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    double a[NB];
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) a[b] = (double)u[b][s][c];
-                    use(a);
-                }
-        }
-    } else {
-        const int col = lane % 16, sub = lane / 16;
-        for (int64_t j0 = lo + wave_id() * 16 * S; j0 < hi; j0 += kWaves * 16 * S) {
-            float u[NB][4 * S];
-#pragma unroll
-            for (int k = 0; k < 4 * S; ++k)
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int64_t j = j0 + 4 * k + sub;
-                    const int i = i0[b] + col;
-                    u[b][k] = src.get1(q.at(i, j), i < q.n && j < hi);
-                }
-#pragma unroll
-            for (int k = 0; k < 4 * S; ++k) {
+            for (int c = 0; c < 4; ++c) {
                 double a[NB];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) a[b] = (double)u[b][k];
+                for (int b = 0; b < NB; ++b) a[b] = (double)src.u(r[b][s], c);
                 use(a);
             }
-        }
+    };
+    int64_t j0 = lo + (WAVES > 1 ? wave_id() : 0) * 16 * S;
+    if (j0 >= hi) return;
+    load(j0, raw[0]);
+    for (; j0 < hi; j0 += 2 * STEP) {
+        if (j0 + STEP < hi) load(j0 + STEP, raw[1]);
+        spend(raw[0]);
+        if (j0 + STEP >= hi) break;
+        if (j0 + 2 * STEP < hi) load(j0 + 2 * STEP, raw[0]);
+        spend(raw[1]);
     }
 }
 
@@ -211,29 +237,89 @@ template <int N> __device__ __forceinline__ void store_tiles(const d4 (&acc)[N],
     }
 }
 
-// One workgroup: one piece of one matrix; its blocks on and above the diagonal.
+// The tiles of a 64-wide matrix on and above the diagonal, shared out to four waves: tile
+// (i, j) of wave W's blocks, numbered as they are stored.
+struct Tile64 {
+    int a, b, at;  // places among the wave's blocks; the tile's number
+};
+template <int W> struct Share64;
+template <> struct Share64<0> {
+    static constexpr int N = 3, T = 3, block[3] = {0, 1, 2};
+    static constexpr Tile64 tile[3] = {{0, 0, 0}, {0, 1, 1}, {0, 2, 2}};
+};
+template <> struct Share64<1> {
+    static constexpr int N = 3, T = 3, block[3] = {0, 1, 3};
+    static constexpr Tile64 tile[3] = {{0, 2, 3}, {1, 1, 4}, {1, 2, 6}};
+};
+template <> struct Share64<2> {
+    static constexpr int N = 2, T = 2, block[2] = {1, 2};
+    static constexpr Tile64 tile[2] = {{0, 1, 5}, {1, 1, 7}};
+};
+template <> struct Share64<3> {
+    static constexpr int N = 2, T = 2, block[2] = {2, 3};
+    static constexpr Tile64 tile[2] = {{0, 1, 8}, {1, 1, 9}};
+};
+template <int W, bool WIDE, typename SRC>
+__device__ __forceinline__ void gram_share(const SRC& src, const Place& q, int64_t lo, int64_t hi, double* out) {
+    using H = Share64<W>;
+    int i0[H::N];
+    d4 acc[H::T];
+#pragma unroll
+    for (int b = 0; b < H::N; ++b) i0[b] = 16 * H::block[b];
+#pragma unroll
+    for (int t = 0; t < H::T; ++t) acc[t] = d4{0.0, 0.0, 0.0, 0.0};
+    long_side<WIDE, H::N, 1, 1>(src, q, i0, lo, hi, [&](const double (&u)[H::N]) {
+#pragma unroll
+        for (int t = 0; t < H::T; ++t) acc[t] = mfma(u[H::tile[t].a], u[H::tile[t].b], acc[t]);
+    });
+#pragma unroll
+    for (int t = 0; t < H::T; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) gst(out + 256 * H::tile[t].at + 64 * v + lane_id(), acc[t][v]);
+}
+template <bool WIDE, typename SRC>
+__device__ __forceinline__ void gram64(const SRC& src, const Place& q, int64_t lo, int64_t hi, double* out) {
+    const int w = wave_id();
+    if (w == 0) gram_share<0, WIDE>(src, q, lo, hi, out);
+    else if (w == 1) gram_share<1, WIDE>(src, q, lo, hi, out);
+    else if (w == 2) gram_share<2, WIDE>(src, q, lo, hi, out);
+    else gram_share<3, WIDE>(src, q, lo, hi, out);
+}
+
+// One workgroup: one piece of one matrix; its blocks on and above the diagonal.  Up to 32
+// wide its waves share the columns, above that the tiles (in whose registers they would
+// leave one wave a SIMD: 512 pieces of 64 x 512 took 87 us so).
 template <int NB, typename G> __global__ __launch_bounds__(kNT) void muon_gram(MuonArgs a) {
-    constexpr int T = NB * (NB + 1) / 2, S = NB == 1 ? 4 : NB == 2 ? 2 : 1;
-    __shared__ double s_sum[T * 256];
+    constexpr int T = NB * (NB + 1) / 2;
     const MuDesc D = a.descs[gld(a.item_desc + blockIdx.x)];
     const int64_t local = (int64_t)blockIdx.x - D.item0;
     const Place q(D, local / D.chunks);
     const int64_t lo = local % D.chunks * muon_chunk(NB), end = lo + muon_chunk(NB), hi = end < q.d ? end : q.d;
     const FromState<G> src{(const G*)D.g, D.m, Mom(a)};
-    int i0[NB];
+    double* out = a.part + (int64_t)blockIdx.x * muon_part(NB);
+    if constexpr (NB == 4) {
+        if (q.wide) gram64<true>(src, q, lo, hi, out);
+        else gram64<false>(src, q, lo, hi, out);
+    } else {
+        constexpr int S = NB == 1 ? 2 : 1;
+        __shared__ double s_sum[T * 256];
+        int i0[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) i0[b] = 16 * b;
-    d4 acc[T];
+        for (int b = 0; b < NB; ++b) i0[b] = 16 * b;
+        d4 acc[T];
 #pragma unroll
-    for (int t = 0; t < T; ++t) acc[t] = d4{0.0, 0.0, 0.0, 0.0};
-    long_side<NB, S>(src, q, i0, lo, hi, [&](const double (&u)[NB]) {
-        int t = 0;
+        for (int t = 0; t < T; ++t) acc[t] = d4{0.0, 0.0, 0.0, 0.0};
+        const auto add = [&](const double (&u)[NB]) {
+            int t = 0;
 #pragma unroll
-        for (int bi = 0; bi < NB; ++bi)
+            for (int bi = 0; bi < NB; ++bi)
 #pragma unroll
-            for (int bj = bi; bj < NB; ++bj, ++t) acc[t] = mfma(u[bi], u[bj], acc[t]);
-    });
-    store_tiles(acc, s_sum, a.part + (int64_t)blockIdx.x * muon_part(NB));
+                for (int bj = bi; bj < NB; ++bj, ++t) acc[t] = mfma(u[bi], u[bj], acc[t]);
+        };
+        if (q.wide) long_side<true, NB, S, kWaves>(src, q, i0, lo, hi, add);
+        else long_side<false, NB, S, kWaves>(src, q, i0, lo, hi, add);
+        store_tiles(acc, s_sum, out);
+    }
 }
 
 // ---- the n x n steps ----------------------------------------------------------------------
@@ -243,26 +329,26 @@ __device__ __forceinline__ bool on_diagonal(int v, int lane) { return 4 * v + la
 // The place of that element's mirror image in block (bj, bi).
 __device__ __forceinline__ int mirrored(int v, int lane) { return lane % 16 / 4 * 64 + lane % 16 % 4 * 16 + 4 * v + lane / 16; }
 
-// One workgroup per matrix, wave (bi, bj) with that block of every square matrix in
-// registers; the operands of products lie in LDS, block after block as they are in
-// registers (one block alone is its own operand).
-template <int NB> __global__ __launch_bounds__(NB* NB* kWave) void muon_steps(MuonArgs a) {
+// One workgroup per matrix, a wave for each block (bi, bj) on or above the diagonal, which
+// holds that block of every square matrix in registers; the operands of products lie in LDS
+// whole, block after block as they are in registers (one block alone is its own operand).
+template <int NB> __global__ __launch_bounds__(NB*(NB + 1) / 2 * kWave) void muon_steps(MuonArgs a) {
     constexpr int SQ = NB * NB * 256;
     extern __shared__ double smem[];
     double *LG = smem, *LQ = smem + SQ, *LP = smem + 2 * SQ, *s_tr = smem + (NB > 1 ? 3 * SQ : 0);
-    const int lane = lane_id(), w = wave_id(), bi = w / NB, bj = w % NB;
+    const int lane = lane_id(), w = wave_id();
+    int bi = 0, bj = w;
+    while (bj >= NB) bj -= NB - 1 - bi++;  // row after row: (0, 0 ..), (1, 1 ..), ..
     const int64_t mat = blockIdx.x;
     const MuDesc D = a.descs[gld(a.mat_desc + mat)];
     // the pieces' sums, in their order
     d4 g = {0.0, 0.0, 0.0, 0.0};
     {
-        const int lo = bi < bj ? bi : bj, hi = bi < bj ? bj : bi;
-        const int tile = lo * NB - lo * (lo - 1) / 2 + (hi - lo);
-        const double* part = a.part + (D.item0 + (mat - D.mat0) * D.chunks) * muon_part(NB) + tile * 256;
+        const double* part = a.part + (D.item0 + (mat - D.mat0) * D.chunks) * muon_part(NB) + w * 256 + lane;
 #pragma unroll 4
         for (int c = 0; c < D.chunks; ++c, part += muon_part(NB))
 #pragma unroll
-            for (int v = 0; v < 4; ++v) g[v] += gld(part + (bi <= bj ? 64 * v + lane : mirrored(v, lane)));
+            for (int v = 0; v < 4; ++v) g[v] += gld(part + 64 * v);
     }
     // |u|^2 is the trace
     double tr = 0.0;
@@ -282,10 +368,14 @@ template <int NB> __global__ __launch_bounds__(NB* NB* kWave) void muon_steps(Mu
     d4 eye;
 #pragma unroll
     for (int v = 0; v < 4; ++v) eye[v] = bi == bj && on_diagonal(v, lane) ? 1.0 : 0.0;
+    // the block and its mirror image
     const auto put = [&](double* L, const d4& x) {
         if constexpr (NB > 1) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) L[w * 256 + 64 * v + lane] = x[v];
+            for (int v = 0; v < 4; ++v) {
+                L[(bi * NB + bj) * 256 + 64 * v + lane] = x[v];
+                if (bi != bj) L[(bj * NB + bi) * 256 + mirrored(v, lane)] = x[v];
+            }
         }
     };
     // X Y of symmetric X, Y (all are polynomials of G): an operand's block (bi, bk) is read as (bk, bi)
@@ -327,10 +417,12 @@ template <int NB> __global__ __launch_bounds__(NB* NB* kWave) void muon_steps(Mu
     }
     p *= inv;
     bool fin = true;
+    double* out = a.pm + mat * SQ;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
         fin = fin && __builtin_isfinite(p[v]);
-        gst(a.pm + mat * SQ + w * 256 + 64 * v + lane, p[v]);
+        gst(out + (bi * NB + bj) * 256 + 64 * v + lane, p[v]);
+        if (bi != bj) gst(out + (bj * NB + bi) * 256 + mirrored(v, lane), p[v]);
     }
     const bool ok = __syncthreads_and(fin && __builtin_isfinite(tr));
     if (threadIdx.x == 0) {
@@ -353,24 +445,25 @@ struct Rate {
     }
 };
 // Four neighbours' weights from their four products.
-template <typename P>
+template <bool NT, typename P>
 __device__ __forceinline__ void update4(const MuDesc& D, const Rate& r, int64_t at, int nv, bool vec, const double (&x)[4]) {
     if (nv <= 0) return;
     float w[4];
-    if (D.master) read4((const float*)D.master, at, nv, vec, w);
-    else read4((const P*)D.p, at, nv, vec, w);
+    if (D.master) read4<NT>((const float*)D.master, at, nv, vec, w);
+    else read4<NT>((const P*)D.p, at, nv, vec, w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = w[j] * r.keep - r.lr * (float)x[j];
-    if (D.master) write4(D.master, at, nv, vec, w);
-    write4((P*)D.p, at, nv, vec, w);
+    if (D.master) write4<NT>(D.master, at, nv, vec, w);
+    write4<NT>((P*)D.p, at, nv, vec, w);
 }
 // The lane's place of its v-th (wide) or x-th (tall) group of four in block b.
+template <bool WIDE>
 __device__ __forceinline__ int group_at(const Place& q, int b, int k, int64_t j0, int64_t hi, int lane, int64_t* at) {
-    const int i = q.wide ? 16 * b + 4 * k + lane / 16 : 16 * b + 4 * (lane / 16);
-    const int64_t j = q.wide ? j0 + 4 * (lane % 16) : j0 + 16 * k + lane % 16;
-    *at = q.at(i, j);
+    const int i = WIDE ? 16 * b + 4 * k + lane / 16 : 16 * b + 4 * (lane / 16);
+    const int64_t j = WIDE ? j0 + 4 * (lane % 16) : j0 + 16 * k + lane % 16;
+    *at = WIDE ? q.base + i * q.d + j : q.base + j * q.n + i;
     if (i >= q.n || j >= hi) return 0;
-    const int64_t left = q.wide ? hi - j : q.n - i;
+    const int64_t left = WIDE ? hi - j : q.n - i;
     return left < 4 ? (int)left : 4;
 }
 // Entry of a square matrix's block that a tall product's first operand wants: row
@@ -379,26 +472,17 @@ __device__ __forceinline__ int tall_entry(int k, int lane) {
     return lane / 16 * 64 + k * 16 + 4 * (lane % 4) + lane % 16 / 4;
 }
 
-// One workgroup: one piece of one matrix, the last first (the pieces that the Gram launch
-// read last are the likeliest to be in a cache still).
-template <int NB, typename P, typename G> __global__ __launch_bounds__(kNT) void muon_apply(MuonArgs a) {
-    __shared__ double s_p[NB > 1 ? NB * NB * 256 : 1];
-    const int64_t item = (int64_t)gridDim.x - 1 - blockIdx.x;
-    const MuDesc D = a.descs[gld(a.item_desc + item)];
-    const int64_t local = item - D.item0, index = local / D.chunks, mat = D.mat0 + index;
-    if (gld(a.bad + mat)) return;
-    const Place q(D, index);
-    const int64_t lo = local % D.chunks * muon_chunk(NB), end = lo + muon_chunk(NB), hi = end < q.d ? end : q.d;
+// A wave's share of a piece: 64 of the long side at a time.
+template <int NB, bool WIDE, typename P, typename G>
+__device__ __forceinline__ void apply_piece(const MuonArgs& a, const MuDesc& D, const Place& q, int64_t lo, int64_t hi, const double* pm, const double* s_p) {
     const int lane = lane_id();
-    const double* pm = a.pm + mat * NB * NB * 256;
     double own[4];
-    if constexpr (NB > 1) {
-        for (int i = threadIdx.x; i < NB * NB * 256; i += kNT) s_p[i] = gld(pm + i);
-        __syncthreads();
-    } else {
+    if constexpr (NB == 1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) own[k] = gld(pm + (q.wide ? 64 * k + lane : tall_entry(k, lane)));
+        for (int k = 0; k < 4; ++k) own[k] = gld(pm + (WIDE ? 64 * k + lane : tall_entry(k, lane)));
     }
+    // an access covers whole cache lines (tall rows of more than one block take several)
+    constexpr bool LAST = WIDE || NB == 1;
     const Mom mom(a);
     const Rate rate(a, D);
     for (int64_t j0 = lo + wave_id() * 64; j0 < hi; j0 += kWaves * 64) {
@@ -409,20 +493,20 @@ template <int NB, typename P, typename G> __global__ __launch_bounds__(kNT) void
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 int64_t at;
-                const int nv = group_at(q, b, k, j0, hi, lane, &at);
-                read4((const G*)D.g, at, nv, q.vec, g[k]);
-                read4((const float*)D.m, at, nv, q.vec, m[k]);
+                const int nv = group_at<WIDE>(q, b, k, j0, hi, lane, &at);
+                read4<LAST>((const G*)D.g, at, nv, q.vec, g[k]);
+                read4<LAST>((const float*)D.m, at, nv, q.vec, m[k]);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 int64_t at;
-                const int nv = group_at(q, b, k, j0, hi, lane, &at);
+                const int nv = group_at<WIDE>(q, b, k, j0, hi, lane, &at);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     m[k][c] = mom.m(m[k][c], g[k][c]);
                     u[b][k][c] = mom.u(m[k][c], g[k][c]);
                 }
-                write4(D.m, at, nv, q.vec, m[k]);
+                write4<LAST>(D.m, at, nv, q.vec, m[k]);
             }
         }
 #pragma unroll
@@ -435,21 +519,40 @@ template <int NB, typename P, typename G> __global__ __launch_bounds__(kNT) void
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     double x;
-                    if constexpr (NB > 1) x = s_p[(kb * NB + ib) * 256 + (q.wide ? 64 * k + lane : tall_entry(k, lane))];
+                    if constexpr (NB > 1) x = s_p[(kb * NB + ib) * 256 + (WIDE ? 64 * k + lane : tall_entry(k, lane))];
                     else x = own[k];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[c] = mfma(x, (double)(q.wide ? u[kb][k][c] : u[kb][c][k]), acc[c]);
+                    for (int c = 0; c < 4; ++c) acc[c] = mfma(x, (double)(WIDE ? u[kb][k][c] : u[kb][c][k]), acc[c]);
                 }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 int64_t at;
-                const int nv = group_at(q, ib, k, j0, hi, lane, &at);
-                const double x[4] = {q.wide ? acc[0][k] : acc[k][0], q.wide ? acc[1][k] : acc[k][1],
-                                     q.wide ? acc[2][k] : acc[k][2], q.wide ? acc[3][k] : acc[k][3]};
-                update4<P>(D, rate, at, nv, q.vec, x);
+                const int nv = group_at<WIDE>(q, ib, k, j0, hi, lane, &at);
+                const double x[4] = {WIDE ? acc[0][k] : acc[k][0], WIDE ? acc[1][k] : acc[k][1], WIDE ? acc[2][k] : acc[k][2],
+                                     WIDE ? acc[3][k] : acc[k][3]};
+                update4<LAST, P>(D, rate, at, nv, q.vec, x);
             }
         }
     }
+}
+
+// One workgroup: one piece of one matrix, the last first (the pieces that the Gram launch
+// read last are the likeliest to be in a cache still).
+template <int NB, typename P, typename G> __global__ __launch_bounds__(kNT, NB == 4 ? 2 : 1) void muon_apply(MuonArgs a) {
+    __shared__ double s_p[NB > 1 ? NB * NB * 256 : 1];
+    const int64_t item = (int64_t)gridDim.x - 1 - blockIdx.x;
+    const MuDesc D = a.descs[gld(a.item_desc + item)];
+    const int64_t local = item - D.item0, index = local / D.chunks, mat = D.mat0 + index;
+    if (gld(a.bad + mat)) return;
+    const Place q(D, index);
+    const int64_t lo = local % D.chunks * muon_chunk(NB), end = lo + muon_chunk(NB), hi = end < q.d ? end : q.d;
+    const double* pm = a.pm + mat * NB * NB * 256;
+    if constexpr (NB > 1) {
+        for (int i = threadIdx.x; i < NB * NB * 256; i += kNT) s_p[i] = gld(pm + i);
+        __syncthreads();
+    }
+    if (q.wide) apply_piece<NB, true, P, G>(a, D, q, lo, hi, pm, s_p);
+    else apply_piece<NB, false, P, G>(a, D, q, lo, hi, pm, s_p);
 }
 
 // ---- small sides above 64 -----------------------------------------------------------------
@@ -470,15 +573,16 @@ template <typename G> __global__ __launch_bounds__(kNT) void muon_big_u(MuonArgs
     }
 }
 
-// One workgroup: one 64 x 64 of one piece's Gram matrix (rows 64 bi .., columns 64 bj .., bi <= bj).
+// The 64 x 64 blocks on and above the diagonal, by number: (bi, bj), bi <= bj.
 __device__ __forceinline__ void pair_of(int t, int groups, int* bi, int* bj) {
     int i = 0;
     while (t >= groups - i) t -= groups - i++;
     *bi = i;
     *bj = i + t;
 }
+// One workgroup: one 64 x 64 of one piece's Gram matrix (rows 64 bi .., columns 64 bj ..),
+// 16 rows of it a wave.
 __global__ __launch_bounds__(kNT) void muon_big_gram(MuonArgs a) {
-    __shared__ double s_sum[kMuonBigPart];
     const MuBig B = a.big[gld(a.pair_big + blockIdx.x)];
     const MuDesc D = a.descs[B.desc];
     const int groups = B.nb / 4, pairs = groups * (groups + 1) / 2;
@@ -486,52 +590,52 @@ __global__ __launch_bounds__(kNT) void muon_big_gram(MuonArgs a) {
     int bi, bj;
     pair_of((int)(local % pairs), groups, &bi, &bj);
     const Place q(D, B.index);
-    const int64_t lo = local / pairs * muon_chunk(4), end = lo + muon_chunk(4), hi = end < q.d ? end : q.d;
+    const int64_t lo = local / pairs * kMuonBigChunk, end = lo + kMuonBigChunk, hi = end < q.d ? end : q.d;
     const FromScratch src{D.u};
-    int i0[8];
+    const int w = wave_id(), lane = lane_id();
+    const int i0[5] = {64 * bi + 16 * w, 64 * bj, 64 * bj + 16, 64 * bj + 32, 64 * bj + 48};
+    d4 acc[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        i0[b] = 64 * bi + 16 * b;
-        i0[4 + b] = 64 * bj + 16 * b;
-    }
-    d4 acc[16];
+    for (int t = 0; t < 4; ++t) acc[t] = d4{0.0, 0.0, 0.0, 0.0};
+    const auto add = [&](const double (&u)[5]) {
 #pragma unroll
-    for (int t = 0; t < 16; ++t) acc[t] = d4{0.0, 0.0, 0.0, 0.0};
-    long_side<8, 1>(src, q, i0, lo, hi, [&](const double (&u)[8]) {
+        for (int t = 0; t < 4; ++t) acc[t] = mfma(u[0], u[1 + t], acc[t]);
+    };
+    if (q.wide) long_side<true, 5, 1, 1>(src, q, i0, lo, hi, add);
+    else long_side<false, 5, 1, 1>(src, q, i0, lo, hi, add);
+    double* out = a.part + (int64_t)blockIdx.x * kMuonBigPart + w * 1024;
 #pragma unroll
-        for (int t = 0; t < 16; ++t) acc[t] = mfma(u[t / 4], u[4 + t % 4], acc[t]);
-    });
-    store_tiles(acc, s_sum, a.part + (int64_t)blockIdx.x * kMuonBigPart);
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) gst(out + 256 * t + 64 * v + lane, acc[t][v]);
 }
 
-// The pieces' sums of one 64 x 64, in their order, into G and its mirror image.
+// The pieces' sums of one 16 x 16, in their order, into G and its mirror image.
 __global__ __launch_bounds__(kNT) void muon_big_sum(MuonArgs a) {
-    const MuBig B = a.big[gld(a.sum_big + blockIdx.x)];
+    const MuBig B = a.big[gld(a.sum_big + blockIdx.x / 16)];
     const MuDesc D = a.descs[B.desc];
-    const int groups = B.nb / 4, pairs = groups * (groups + 1) / 2, pair = gld(a.sum_pair + blockIdx.x);
+    const int groups = B.nb / 4, pairs = groups * (groups + 1) / 2, pair = gld(a.sum_pair + blockIdx.x / 16);
     int bi, bj;
     pair_of(pair, groups, &bi, &bj);
     double* G = a.square + B.off;
-    for (int e = threadIdx.x; e < kMuonBigPart; e += kNT) {
-        const double* part = a.part + (B.part0 + pair) * kMuonBigPart + e;
-        double s = 0.0;
-#pragma unroll 8
-        for (int c = 0; c < D.chunks; ++c, part += (int64_t)pairs * kMuonBigPart) s += gld(part);
-        const int t = e / 256, v = e / 64 % 4, lane = e % 64;
-        const int r = 4 * bi + t / 4, k = 4 * bj + t % 4;
-        gst(G + ((int64_t)r * B.nb + k) * 256 + e % 256, s);
-        if (bi != bj) gst(G + ((int64_t)k * B.nb + r) * 256 + mirrored(v, lane), s);
-    }
+    const int t = blockIdx.x % 16, e = threadIdx.x, v = e / 64, lane = e % 64;
+    const double* part = a.part + (B.part0 + pair) * kMuonBigPart + t * 256 + e;
+    double s = 0.0;
+#pragma unroll 16
+    for (int c = 0; c < D.chunks; ++c, part += (int64_t)pairs * kMuonBigPart) s += gld(part);
+    const int r = 4 * bi + t / 4, k = 4 * bj + t % 4;
+    gst(G + ((int64_t)r * B.nb + k) * 256 + e, s);
+    if (bi != bj) gst(G + ((int64_t)k * B.nb + r) * 256 + mirrored(v, lane), s);
 }
 
-// The trace and what follows from it.
-__global__ __launch_bounds__(kNT) void muon_big_norm(MuonArgs a) {
+// The trace of big matrix i and what follows from it, by one workgroup.
+__device__ __forceinline__ void big_norm(const MuonArgs& a, int i) {
     __shared__ double s_tr[kWaves];
-    const MuBig B = a.big[blockIdx.x];
+    const MuBig B = a.big[i];
     const double* G = a.square + B.off;
     double tr = 0.0;
-    for (int i = threadIdx.x; i < 16 * B.nb; i += kNT) {
-        const int b = i / 16, r = i % 16;  // entry (r, r): register r / 4 of lane 16 (r % 4) + r
+    for (int e = threadIdx.x; e < 16 * B.nb; e += kNT) {
+        const int b = e / 16, r = e % 16;  // entry (r, r): register r / 4 of lane 16 (r % 4) + r
         tr += gld(G + ((int64_t)b * B.nb + b) * 256 + r / 4 * 64 + r % 4 * 16 + r);
     }
     tr = wave_sum(tr);
@@ -542,109 +646,151 @@ __global__ __launch_bounds__(kNT) void muon_big_norm(MuonArgs a) {
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) tr += s_tr[w];
     const double inv = 1.0 / (sqrt(tr) + (double)a.eps);
-    gst(a.meta + 2 * blockIdx.x, inv);
-    gst(a.meta + 2 * blockIdx.x + 1, inv * inv);
+    gst(a.meta + 2 * i, inv);
+    gst(a.meta + 2 * i + 1, inv * inv);
     const bool ok = __builtin_isfinite(tr);
-    gst(a.bad + blockIdx.x, ok ? 0 : 1);
+    gst(a.bad + i, ok ? 0 : 1);
     if (!ok) gst(a.err, 1);
 }
 
-// Products of the square matrices, a wave per 16 x 16 block of the result.  G's factor
-// 1 / norm^2 is applied in the first step, P's 1 / norm too.
-//   MUL_S  S = G G        MUL_RP  R = G Q, and (blockIdx.y 1, or alone in the last step) P' = P Q
+// Products of the square matrices, a workgroup per 16 x 16 block of the result: its waves
+// take every fourth block of the sum and add up in their order.  G's factor 1 / norm^2 is
+// applied in the first step, P's 1 / norm too.
+//   MUL_S  S = G G  (in the first step the norms beside it, in workgroups of their own)
+//   MUL_RP  R = G Q, and (blockIdx.y 1, or alone in the last step) P' = P Q
 //   MUL_G  G' = R Q       with Q = a + b G + c S of this step's G and S
 enum { MUL_S = 0, MUL_RP = 1, MUL_G = 2 };
 struct BigMats {
     double *G, *S, *R, *P, *G2, *P2;
 };
 template <int MODE> __global__ __launch_bounds__(kNT) void muon_big_mul(MuonArgs a, BigMats M, int step, int only_p) {
+    __shared__ double s_sum[kWaves][256];
+    if (MODE == MUL_S && (int64_t)blockIdx.x >= a.n_mul) return big_norm(a, (int)(blockIdx.x - a.n_mul));
     const int bigi = gld(a.mul_big + blockIdx.x);
     const MuBig B = a.big[bigi];
-    const int nb = B.nb, lane = lane_id(), block = gld(a.mul_at + blockIdx.x) + wave_id(), bi = block / nb, bj = block % nb;
-    const double f = step == 0 ? gld(a.meta + 2 * bigi + 1) : 1.0;  // G is f times what is stored
+    const int nb = B.nb, lane = lane_id(), w = wave_id(), block = gld(a.mul_at + blockIdx.x), bi = block / nb, bj = block % nb;
+    const double f = MODE != MUL_S && step == 0 ? gld(a.meta + 2 * bigi + 1) : 1.0;  // G is f times what is stored
     const double ca = a.coefs[step][0], cb = a.coefs[step][1] * f, cc = a.coefs[step][2] * f * f;
     const auto frag = [&](const double* X, int r, int c, int v) { return gld(X + B.off + ((int64_t)r * nb + c) * 256 + 64 * v + lane); };
-    const auto q = [&](int r, int c, int v) {
-        const double d = r == c && on_diagonal(v, lane) ? ca : 0.0;
-        return d + cb * frag(M.G, r, c, v) + cc * frag(M.S, r, c, v);
-    };
     const bool want_p = MODE == MUL_RP && (only_p || blockIdx.y == 1);
-    d4 r = {0.0, 0.0, 0.0, 0.0};
-    double* out = MODE == MUL_S ? M.S : MODE == MUL_G ? M.G2 : want_p ? M.P2 : M.R;
+    double* out = (MODE == MUL_S ? M.S : MODE == MUL_G ? M.G2 : want_p ? M.P2 : M.R) + B.off + (int64_t)block * 256;
     if (want_p && step == 0) {
+        if (w != 0) return;
         const double inv = gld(a.meta + 2 * bigi);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) r[v] = inv * q(bi, bj, v);
-    } else {
-        const double* X = MODE == MUL_G ? M.R : want_p ? M.P : M.G;
-        for (int bk = 0; bk < nb; ++bk) {
-            double x[4], y[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                x[v] = frag(X, bk, bi, v);
-                y[v] = MODE == MUL_S ? frag(M.G, bk, bj, v) : q(bk, bj, v);
+        for (int v = 0; v < 4; ++v) {
+            const double q = (bi == bj && on_diagonal(v, lane) ? ca : 0.0) + cb * frag(M.G, bi, bj, v) + cc * frag(M.S, bi, bj, v);
+            gst(out + 64 * v + lane, inv * q);
+            if (a.steps == 1 && !__builtin_isfinite(inv * q)) {
+                gst(a.bad + bigi, 1);
+                gst(a.err, 1);
             }
-#pragma unroll
-            for (int v = 0; v < 4; ++v) r = mfma(x[v], y[v], r);
         }
-        // (R and S keep the stored G's scale; G' takes it from R)
-        if (MODE == MUL_G) r *= f;
+        return;
+    }
+    const double* X = MODE == MUL_G ? M.R : want_p ? M.P : M.G;
+    d4 r = {0.0, 0.0, 0.0, 0.0};
+    // two blocks of the sum's loads at a time
+    for (int b0 = w; b0 < nb; b0 += 2 * kWaves) {
+        double x[2][4], y[2][4], z[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int bk = b0 + h * kWaves;
+            if (bk < nb) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    x[h][v] = frag(X, bk, bi, v);
+                    y[h][v] = frag(M.G, bk, bj, v);
+                    z[h][v] = MODE == MUL_S ? 0.0 : frag(M.S, bk, bj, v);
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int bk = b0 + h * kWaves;
+            if (bk < nb) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    double q = y[h][v];
+                    if constexpr (MODE != MUL_S) q = (bk == bj && on_diagonal(v, lane) ? ca : 0.0) + cb * q + cc * z[h][v];
+                    r = mfma(x[h][v], q, r);
+                }
+            }
+        }
     }
 #pragma unroll
-    for (int v = 0; v < 4; ++v) gst(out + B.off + (int64_t)block * 256 + 64 * v + lane, r[v]);
+    for (int v = 0; v < 4; ++v) s_sum[w][64 * v + lane] = r[v];
+    __syncthreads();
+    double s = s_sum[0][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < kWaves; ++k) s += s_sum[k][threadIdx.x];
+    // (R and S keep the stored G's scale; G' takes it from R)
+    gst(out + threadIdx.x, MODE == MUL_G ? s * f : s);
+    if (MODE == MUL_RP && step + 1 == a.steps && !__builtin_isfinite(s)) {
+        gst(a.bad + bigi, 1);
+        gst(a.err, 1);
+    }
 }
 
-// One workgroup: one piece's long side, 64 of the small side.
+// One workgroup: 64 of the long side, 64 of the small side, 16 of them a wave.
+template <bool WIDE, typename P, typename G>
+__device__ __forceinline__ void big_apply(const MuonArgs& a, const MuDesc& D, const MuBig& B, const double* PM, int ib, int64_t j0) {
+    const int lane = lane_id();
+    const Place q(D, B.index);
+    const int64_t hi = q.d;
+    const Mom mom(a);
+    const Rate rate(a, D);
+    d4 acc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = d4{0.0, 0.0, 0.0, 0.0};
+    const auto load = [&](int kb, float (&u)[4][4], double (&x)[4]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            int64_t at;
+            const int nv = group_at<WIDE>(q, kb, k, j0, hi, lane, &at);
+            read4((const float*)D.u, at, nv, q.vec, u[k]);
+            x[k] = gld(PM + B.off + ((int64_t)kb * B.nb + ib) * 256 + (WIDE ? 64 * k + lane : tall_entry(k, lane)));
+        }
+    };
+    const auto spend = [&](const float (&u)[4][4], const double (&x)[4]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[c] = mfma(x[k], (double)(WIDE ? u[k][c] : u[c][k]), acc[c]);
+    };
+    float u[2][4][4];
+    double x[2][4];
+    load(0, u[0], x[0]);
+    for (int kb = 0; kb < B.nb; kb += 2) {  // nb is a multiple of 4
+        load(kb + 1, u[1], x[1]);
+        spend(u[0], x[0]);
+        if (kb + 2 < B.nb) load(kb + 2, u[0], x[0]);
+        spend(u[1], x[1]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        int64_t at;
+        const int nv = group_at<WIDE>(q, ib, k, j0, hi, lane, &at);
+        float g[4], m[4];
+        read4((const G*)D.g, at, nv, q.vec, g);
+        read4((const float*)D.m, at, nv, q.vec, m);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) m[c] = mom.m(m[c], g[c]);
+        write4(D.m, at, nv, q.vec, m);
+        const double y[4] = {WIDE ? acc[0][k] : acc[k][0], WIDE ? acc[1][k] : acc[k][1], WIDE ? acc[2][k] : acc[k][2],
+                             WIDE ? acc[3][k] : acc[k][3]};
+        update4<false, P>(D, rate, at, nv, q.vec, y);
+    }
+}
 template <typename P, typename G> __global__ __launch_bounds__(kNT) void muon_big_apply(MuonArgs a, const double* PM) {
     const int bigi = gld(a.out_big + blockIdx.x);
     if (gld(a.bad + bigi)) return;
     const MuBig B = a.big[bigi];
     const MuDesc D = a.descs[B.desc];
-    const int groups = B.nb / 4, at0 = gld(a.out_at + blockIdx.x), ob = at0 % groups, lane = lane_id();
-    const Place q(D, B.index);
-    const int64_t lo = (int64_t)(at0 / groups) * muon_chunk(4), end = lo + muon_chunk(4), hi = end < q.d ? end : q.d;
-    const Mom mom(a);
-    const Rate rate(a, D);
-    for (int64_t j0 = lo + wave_id() * 64; j0 < hi; j0 += kWaves * 64) {
-        d4 acc[4][4];
-#pragma unroll
-        for (int t = 0; t < 16; ++t) acc[t / 4][t % 4] = d4{0.0, 0.0, 0.0, 0.0};
-        for (int kb = 0; kb < B.nb; ++kb) {
-            float u[4][4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                int64_t at;
-                const int nv = group_at(q, kb, k, j0, hi, lane, &at);
-                read4((const float*)D.u, at, nv, q.vec, u[k]);
-            }
-#pragma unroll
-            for (int ib = 0; ib < 4; ++ib) {
-                const double* pm = PM + B.off + ((int64_t)kb * B.nb + 4 * ob + ib) * 256;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const double x = gld(pm + (q.wide ? 64 * k + lane : tall_entry(k, lane)));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[ib][c] = mfma(x, (double)(q.wide ? u[k][c] : u[c][k]), acc[ib][c]);
-                }
-            }
-        }
-#pragma unroll
-        for (int ib = 0; ib < 4; ++ib)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                int64_t at;
-                const int nv = group_at(q, 4 * ob + ib, k, j0, hi, lane, &at);
-                float g[4], m[4];
-                read4((const G*)D.g, at, nv, q.vec, g);
-                read4((const float*)D.m, at, nv, q.vec, m);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) m[c] = mom.m(m[c], g[c]);
-                write4(D.m, at, nv, q.vec, m);
-                const double x[4] = {q.wide ? acc[ib][0][k] : acc[ib][k][0], q.wide ? acc[ib][1][k] : acc[ib][k][1],
-                                     q.wide ? acc[ib][2][k] : acc[ib][k][2], q.wide ? acc[ib][3][k] : acc[ib][k][3]};
-                update4<P>(D, rate, at, nv, q.vec, x);
-            }
-    }
+    const int groups = B.nb / 4, at = gld(a.out_at + blockIdx.x), ib = at % groups * 4 + wave_id();
+    const int64_t j0 = (int64_t)(at / groups) * 64;
+    if (D.wide) big_apply<true, P, G>(a, D, B, PM, ib, j0);
+    else big_apply<false, P, G>(a, D, B, PM, ib, j0);
 }
 
 // ---- launches ---------------------------------------------------------------------------
@@ -654,7 +800,7 @@ constexpr size_t steps_lds(int nb) { return nb > 1 ? (size_t)(3 * nb * nb * 256 
 template <int NB, typename P, typename G> hipError_t launch_class(const MuonArgs& a, hipStream_t s) {
     const dim3 items((unsigned)a.items), n(kNT);
     hipLaunchKernelGGL((muon_gram<NB, G>), items, n, 0, s, a);
-    hipLaunchKernelGGL((muon_steps<NB>), dim3((unsigned)a.mats), dim3(NB * NB * kWave), steps_lds(NB), s, a);
+    hipLaunchKernelGGL((muon_steps<NB>), dim3((unsigned)a.mats), dim3(NB * (NB + 1) / 2 * kWave), steps_lds(NB), s, a);
     hipLaunchKernelGGL((muon_apply<NB, P, G>), items, n, 0, s, a);
     return hipGetLastError();
 }
@@ -666,14 +812,13 @@ template <typename P, typename G> hipError_t launch_big_pg(const MuonArgs& a, in
     const int64_t ublocks = (u_elems + 4 * kNT - 1) / (4 * kNT);
     hipLaunchKernelGGL((muon_big_u<G>), dim3((unsigned)(ublocks < 4096 ? ublocks : 4096), (unsigned)a.items), n, 0, s, a);
     hipLaunchKernelGGL(muon_big_gram, dim3((unsigned)a.n_pair), n, 0, s, a);
-    hipLaunchKernelGGL(muon_big_sum, dim3((unsigned)a.n_sum), n, 0, s, a);
-    hipLaunchKernelGGL(muon_big_norm, dim3((unsigned)a.n_big), n, 0, s, a);
+    hipLaunchKernelGGL(muon_big_sum, dim3((unsigned)(a.n_sum * 16)), n, 0, s, a);
     double* at = a.square;
     BigMats M{at, at + a.sq, at + 2 * a.sq, at + 3 * a.sq, at + 4 * a.sq, at + 5 * a.sq};
     const unsigned mul = (unsigned)a.n_mul;
     for (int k = 0; k < a.steps; ++k) {
         const bool last = k + 1 == a.steps;
-        hipLaunchKernelGGL((muon_big_mul<MUL_S>), dim3(mul), n, 0, s, a, M, k, 0);
+        hipLaunchKernelGGL((muon_big_mul<MUL_S>), dim3(k == 0 ? mul + (unsigned)a.n_big : mul), n, 0, s, a, M, k, 0);
         hipLaunchKernelGGL((muon_big_mul<MUL_RP>), dim3(mul, last ? 1 : 2), n, 0, s, a, M, k, last ? 1 : 0);
         if (!last) hipLaunchKernelGGL((muon_big_mul<MUL_G>), dim3(mul), n, 0, s, a, M, k, 0);
         std::swap(M.P, M.P2);
@@ -695,7 +840,7 @@ hipError_t launch_muon(const MuonArgs& a, int nb, int p_dtype, int g_dtype, hipS
     return g_dtype == 0 ? launch_pg<uint16_t, float>(a, nb, s) : launch_pg<uint16_t, uint16_t>(a, nb, s);
 }
 hipError_t launch_muon_big(const MuonArgs& a, int64_t u_elems, int p_dtype, int g_dtype, hipStream_t s) {
-    if (!grid_fits(a.n_pair, kNT) || !grid_fits(a.n_mul, kNT) || !grid_fits(a.n_out, kNT)) return hipErrorInvalidConfiguration;
+    if (!grid_fits(a.n_pair, kNT) || !grid_fits(a.n_mul + a.n_big, kNT) || !grid_fits(a.n_sum * 16, kNT) || !grid_fits(a.n_out, kNT)) return hipErrorInvalidConfiguration;
     if (p_dtype == 0) return g_dtype == 0 ? launch_big_pg<float, float>(a, u_elems, s) : launch_big_pg<float, uint16_t>(a, u_elems, s);
     return g_dtype == 0 ? launch_big_pg<uint16_t, float>(a, u_elems, s) : launch_big_pg<uint16_t, uint16_t>(a, u_elems, s);
 }

@@ -51,9 +51,9 @@ struct MuonArgs {
     const int32_t* pair_big;   // per (matrix, chunk, pair of 64-blocks)
     const int32_t* sum_big;    // per (matrix, pair)
     const int32_t* sum_pair;   // the pair's number within its matrix
-    const int32_t* mul_big;    // per four 16 x 16 blocks
-    const int32_t* mul_at;     // the first of them
-    const int32_t* out_big;    // per (matrix, 64 of its small side, chunk)
+    const int32_t* mul_big;    // per 16 x 16 block
+    const int32_t* mul_at;     // which of the matrix's
+    const int32_t* out_big;    // per (matrix, 64 of its long side, 64 of its small side)
     const int32_t* out_at;     // which of them
     int64_t n_big, n_pair, n_sum, n_mul, n_out, sq;  // sq: doubles of one square matrix of all
     double* square;            // six square matrices of each
@@ -71,6 +71,7 @@ constexpr int muon_chunk(int nb) { return nb == 4 ? 512 : 1024; }
 // Doubles of one piece's sums: the blocks on and above the diagonal; 64 x 64 of a big matrix.
 constexpr int muon_part(int nb) { return nb * (nb + 1) / 2 * 256; }
 constexpr int kMuonBigPart = 16 * 256;
+constexpr int kMuonBigChunk = 256;  // long-side elements of a big matrix's piece
 
 // Once per handle on its device, before its first launch.
 hipError_t prepare_muon();
