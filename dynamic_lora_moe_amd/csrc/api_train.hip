@@ -25,11 +25,7 @@ struct dlm_muon {
     void* d_work = nullptr;    // scratch of a step
     int32_t* d_err = nullptr;
     int32_t p_dtype = 0, g_dtype = 0;
-    struct Class {
-        int nb;
-        MuonArgs args;
-    };
-    std::vector<Class> classes;
+    MuonArgs small[3] = {};  // small sides up to 16, 32, 64
     MuonArgs big{};
     int64_t big_elems = 0;  // of the largest tensor with big matrices
 };
@@ -192,7 +188,7 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
     struct Slot {
         size_t items, mats, part, pm, bad;
     };
-    std::vector<Slot> slots;
+    Slot slots[3] = {};
     size_t descs_at = 0, err_at = 0, big_at = 0, big_items = 0, big_pair = 0, big_sum = 0, big_sump = 0, big_mul = 0, big_mula = 0,
            big_out = 0, big_outa = 0, big_part = 0, big_sq = 0, big_meta = 0, big_bad = 0;
     std::vector<size_t> u_at;
@@ -268,9 +264,9 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
             return at;
         };
         err_at = table(4);
-        // tensors by their small side: one set of launches each, one after the other, on the same scratch
-        size_t shared = 0;
-        for (int nb : {1, 2, 4}) {
+        // tensors by their small side
+        for (int k = 0; k < 3; ++k) {
+            const int nb = 1 << k;
             int64_t items = 0, mats = 0;
             std::vector<int32_t> item_desc, mat_desc;
             for (int i = 0; i < n; ++i) {
@@ -280,7 +276,7 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
                 d.mat0 = mats;
                 items += d.count * d.chunks;
                 mats += d.count;
-                if (!grid_fits(items, 256) || !grid_fits(mats, nb * nb * 64)) {
+                if (!grid_fits(items, 256) || !grid_fits(mats, 640)) {
                     delete h;
                     return fail(DLM_ESHAPE, "muon_create: the sizes need a launch grid of more than 2^32 - 1 work-items");
                 }
@@ -288,24 +284,18 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
                 mat_desc.insert(mat_desc.end(), (size_t)d.count, i);
             }
             if (!mats) continue;
-            dlm_muon::Class c{nb, MuonArgs{}};
-            c.args.items = items;
-            c.args.mats = mats;
-            Slot s;
+            h->small[k].items = items;
+            h->small[k].mats = mats;
+            Slot& s = slots[k];
             s.items = put32(item_desc);
             s.mats = put32(mat_desc);
-            work = 0;
             s.part = scratch((size_t)items * muon_part(nb) * 8);
             s.pm = scratch((size_t)mats * nb * nb * 256 * 8);
             s.bad = scratch((size_t)mats * 4);
-            shared = std::max(shared, work);
-            h->classes.push_back(c);
-            slots.push_back(s);
         }
         std::vector<MuBig> bigs;
         std::vector<int32_t> ti, tp, ts, tsp, tm, tma, to, toa;
         int64_t off = 0;
-        work = 0;
         for (int i = 0; i < n; ++i) {
             MuDesc& d = descs[i];
             if (nbs[i] || d.count == 0) continue;
@@ -364,7 +354,6 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
             big_bad = scratch((size_t)g.n_big * 4);
             for (int i : ti) u_at[i] = scratch((size_t)(descs[i].count * descs[i].n * descs[i].d) * 4);
         }
-        work = std::max(work, shared);
         descs_at = table(sizeof(MuDesc) * n);
         hipError_t e = hipSuccess;
         if (work) e = hipMalloc(&h->d_work, work);
@@ -393,8 +382,9 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
     h->p_dtype = p_dtype;
     h->g_dtype = g_dtype;
     h->d_err = t32(err_at);
-    for (size_t k = 0; k < slots.size(); ++k) {
-        MuonArgs& a = h->classes[k].args;
+    for (int k = 0; k < 3; ++k) {
+        MuonArgs& a = h->small[k];
+        if (!a.items) continue;
         a.descs = (const MuDesc*)t32(descs_at);
         a.item_desc = t32(slots[k].items);
         a.mat_desc = t32(slots[k].mats);
@@ -456,12 +446,13 @@ int dlm_muon_step(dlm_muon* h, const dlm_muon_cfg* c, const float* lr_scale, con
         a.lr_scale = lr_scale;
         a.grad_scale = grad_scale;
     };
-    for (const dlm_muon::Class& k : h->classes) {
-        MuonArgs a = k.args;
-        set(a);
-        const hipError_t e = launch_muon(a, k.nb, h->p_dtype, h->g_dtype, (hipStream_t)stream);
-        if (e != hipSuccess) return hip_fail(e, "muon_step launch");
+    MuonArgs small[3];
+    for (int k = 0; k < 3; ++k) {
+        small[k] = h->small[k];
+        set(small[k]);
     }
+    const hipError_t e = launch_muon(small, h->p_dtype, h->g_dtype, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "muon_step launch");
     if (h->big.n_big) {
         MuonArgs a = h->big;
         set(a);

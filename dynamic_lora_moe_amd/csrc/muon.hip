@@ -142,10 +142,6 @@ template <typename G> struct FromState {
         read4(g, i, nv, vec, r.g);
         read4(m, i, nv, vec, r.m);
     }
-    __device__ __forceinline__ void load1(int64_t i, bool in, int c, Raw& r) const {
-        r.g[c] = in ? read1(g + i) : 0.f;
-        r.m[c] = in ? gld(m + i) : 0.f;
-    }
     __device__ __forceinline__ float u(const Raw& r, int c) const { return mom.u(mom.m(r.m[c], r.g[c]), r.g[c]); }
 };
 // or from the scratch where a launch has left it.
@@ -159,16 +155,26 @@ struct FromScratch {
     __device__ __forceinline__ float u(const Raw& r, int c) const { return r.u[c]; }
 };
 
+// The lane's place of its v-th (wide) or x-th (tall) group of four in block b.
+template <bool WIDE>
+__device__ __forceinline__ int group_at(const Place& q, int b, int k, int64_t j0, int64_t hi, int lane, int64_t* at) {
+    const int i = WIDE ? 16 * b + 4 * k + lane / 16 : 16 * b + 4 * (lane / 16);
+    const int64_t j = WIDE ? j0 + 4 * (lane % 16) : j0 + 16 * k + lane % 16;
+    *at = WIDE ? q.base + i * q.d + j : q.base + j * q.n + i;
+    if (i >= q.n || j >= hi) return 0;
+    const int64_t left = WIDE ? hi - j : q.n - i;
+    return left < 4 ? (int)left : 4;
+}
 // ---- Gram matrices of pieces ------------------------------------------------------------
 
-// Operands of one wave's share of columns [lo, hi) of the long side, for NB blocks of the
+// Operands of columns [lo, hi) of the long side for one wave, for NB blocks of the
 // small side from i0 on, handed to `use(a)` four columns at a time; the loads of the next 16 S
-// columns are out while these are used.  WAVES of them share the columns.  Wide: a lane loads
+// columns are out while these are used.  Wide: a lane loads
 // four neighbours of its row; tall: the small side is contiguous, and a wave's lanes are.
-template <bool WIDE, int NB, int S, int WAVES, typename SRC, typename F>
+template <bool WIDE, int NB, int S, typename SRC, typename F>
 __device__ __forceinline__ void long_side(const SRC& src, const Place& q, const int (&i0)[NB], int64_t lo, int64_t hi, F use) {
     const int lane = lane_id();
-    constexpr int STEP = WAVES * 16 * S;
+    constexpr int STEP = 16 * S;
     typename SRC::Raw raw[2][NB][S];
     const auto load = [&](int64_t j0, typename SRC::Raw (&r)[NB][S]) {
 #pragma unroll
@@ -200,7 +206,7 @@ __device__ __forceinline__ void long_side(const SRC& src, const Place& q, const 
                 use(a);
             }
     };
-    int64_t j0 = lo + (WAVES > 1 ? wave_id() : 0) * 16 * S;
+    int64_t j0 = lo;
     if (j0 >= hi) return;
     load(j0, raw[0]);
     for (; j0 < hi; j0 += 2 * STEP) {
@@ -237,89 +243,96 @@ template <int N> __device__ __forceinline__ void store_tiles(const d4 (&acc)[N],
     }
 }
 
-// The tiles of a 64-wide matrix on and above the diagonal, shared out to four waves: tile
-// (i, j) of wave W's blocks, numbered as they are stored.
-struct Tile64 {
-    int a, b, at;  // places among the wave's blocks; the tile's number
-};
-template <int W> struct Share64;
-template <> struct Share64<0> {
-    static constexpr int N = 3, T = 3, block[3] = {0, 1, 2};
-    static constexpr Tile64 tile[3] = {{0, 0, 0}, {0, 1, 1}, {0, 2, 2}};
-};
-template <> struct Share64<1> {
-    static constexpr int N = 3, T = 3, block[3] = {0, 1, 3};
-    static constexpr Tile64 tile[3] = {{0, 2, 3}, {1, 1, 4}, {1, 2, 6}};
-};
-template <> struct Share64<2> {
-    static constexpr int N = 2, T = 2, block[2] = {1, 2};
-    static constexpr Tile64 tile[2] = {{0, 1, 5}, {1, 1, 7}};
-};
-template <> struct Share64<3> {
-    static constexpr int N = 2, T = 2, block[2] = {2, 3};
-    static constexpr Tile64 tile[2] = {{0, 1, 8}, {1, 1, 9}};
-};
-template <int W, bool WIDE, typename SRC>
-__device__ __forceinline__ void gram_share(const SRC& src, const Place& q, int64_t lo, int64_t hi, double* out) {
-    using H = Share64<W>;
-    int i0[H::N];
-    d4 acc[H::T];
-#pragma unroll
-    for (int b = 0; b < H::N; ++b) i0[b] = 16 * H::block[b];
-#pragma unroll
-    for (int t = 0; t < H::T; ++t) acc[t] = d4{0.0, 0.0, 0.0, 0.0};
-    long_side<WIDE, H::N, 1, 1>(src, q, i0, lo, hi, [&](const double (&u)[H::N]) {
-#pragma unroll
-        for (int t = 0; t < H::T; ++t) acc[t] = mfma(u[H::tile[t].a], u[H::tile[t].b], acc[t]);
-    });
-#pragma unroll
-    for (int t = 0; t < H::T; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) gst(out + 256 * H::tile[t].at + 64 * v + lane_id(), acc[t][v]);
+// One workgroup: one piece of one matrix; its blocks on and above the diagonal.  A wave
+// takes 64 UN columns of the long side at a time, loaded as the apply launch does (whole
+// cache lines: straight into operands, 64 bytes a row or 4 an element, the loads were half
+// as fast) and turned round in its own part of LDS.
+template <int NB> constexpr int gram_in_flight() { return NB == 1 ? 2 : 1; }
+template <int NB> constexpr int gram_tall_pitch() { return NB == 1 ? 16 : 16 * NB + 16; }  // floats: LDS banks
+constexpr int kGramWidePitch = 68;
+template <int NB> constexpr int gram_floats() {  // of a wave's 64 columns
+    return 64 * gram_tall_pitch<NB>() > 16 * NB * kGramWidePitch ? 64 * gram_tall_pitch<NB>() : 16 * NB * kGramWidePitch;
 }
-template <bool WIDE, typename SRC>
-__device__ __forceinline__ void gram64(const SRC& src, const Place& q, int64_t lo, int64_t hi, double* out) {
-    const int w = wave_id();
-    if (w == 0) gram_share<0, WIDE>(src, q, lo, hi, out);
-    else if (w == 1) gram_share<1, WIDE>(src, q, lo, hi, out);
-    else if (w == 2) gram_share<2, WIDE>(src, q, lo, hi, out);
-    else gram_share<3, WIDE>(src, q, lo, hi, out);
-}
+template <int NB> constexpr size_t gram_lds() { return (size_t)kWaves * gram_in_flight<NB>() * gram_floats<NB>() * 4; }
 
-// One workgroup: one piece of one matrix; its blocks on and above the diagonal.  Up to 32
-// wide its waves share the columns, above that the tiles (in whose registers they would
-// leave one wave a SIMD: 512 pieces of 64 x 512 took 87 us so).
-template <int NB, typename G> __global__ __launch_bounds__(kNT) void muon_gram(MuonArgs a) {
+template <int NB, bool WIDE, typename SRC, int T>
+__device__ __forceinline__ void gram_piece(const SRC& src, const Place& q, int64_t lo, int64_t hi, float* s_u, d4 (&acc)[T]) {
+    constexpr int UN = gram_in_flight<NB>(), F = gram_floats<NB>(), TP = gram_tall_pitch<NB>();
+    const int lane = lane_id();
+    for (int64_t j0 = lo + wave_id() * 64 * UN; j0 < hi; j0 += kWaves * 64 * UN) {
+        typename SRC::Raw raw[UN][NB][4];
+#pragma unroll
+        for (int n = 0; n < UN; ++n)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    int64_t at;
+                    const int nv = group_at<WIDE>(q, b, k, j0 + 64 * n, hi, lane, &at);
+                    src.load4(at, nv, q.vec, raw[n][b][k]);
+                }
+#pragma unroll
+        for (int n = 0; n < UN; ++n)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f32x4 u;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) u[c] = src.u(raw[n][b][k], c);
+                    const int at = WIDE ? (16 * b + 4 * k + lane / 16) * kGramWidePitch + 4 * (lane % 16)
+                                        : (16 * k + lane % 16) * TP + 16 * b + 4 * (lane / 16);
+                    *(f32x4*)(s_u + n * F + at) = u;
+                }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int n = 0; n < UN; ++n)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {  // 16 columns
+                float o[NB][4];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    if constexpr (WIDE) {
+                        const f32x4 r = *(const f32x4*)(s_u + n * F + (16 * b + lane % 16) * kGramWidePitch + 16 * s + 4 * (lane / 16));
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[b][c] = r[c];
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[b][c] = s_u[n * F + (16 * s + 4 * c + lane / 16) * TP + 16 * b + lane % 16];
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    int t = 0;
+#pragma unroll
+                    for (int bi = 0; bi < NB; ++bi)
+#pragma unroll
+                        for (int bj = bi; bj < NB; ++bj, ++t) acc[t] = mfma((double)o[bi][c], (double)o[bj][c], acc[t]);
+                }
+            }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+template <int NB, typename G> __device__ __forceinline__ void gram_item(const MuonArgs& a, int64_t item, float* s_all) {
     constexpr int T = NB * (NB + 1) / 2;
-    const MuDesc D = a.descs[gld(a.item_desc + blockIdx.x)];
-    const int64_t local = (int64_t)blockIdx.x - D.item0;
+    static_assert(gram_lds<NB>() >= T * 256 * 8, "the waves' sums fit where the columns were");
+    const MuDesc D = a.descs[gld(a.item_desc + item)];
+    const int64_t local = item - D.item0;
     const Place q(D, local / D.chunks);
     const int64_t lo = local % D.chunks * muon_chunk(NB), end = lo + muon_chunk(NB), hi = end < q.d ? end : q.d;
     const FromState<G> src{(const G*)D.g, D.m, Mom(a)};
-    double* out = a.part + (int64_t)blockIdx.x * muon_part(NB);
-    if constexpr (NB == 4) {
-        if (q.wide) gram64<true>(src, q, lo, hi, out);
-        else gram64<false>(src, q, lo, hi, out);
-    } else {
-        constexpr int S = NB == 1 ? 2 : 1;
-        __shared__ double s_sum[T * 256];
-        int i0[NB];
+    float* s_u = s_all + wave_id() * gram_in_flight<NB>() * gram_floats<NB>();
+    d4 acc[T];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) i0[b] = 16 * b;
-        d4 acc[T];
-#pragma unroll
-        for (int t = 0; t < T; ++t) acc[t] = d4{0.0, 0.0, 0.0, 0.0};
-        const auto add = [&](const double (&u)[NB]) {
-            int t = 0;
-#pragma unroll
-            for (int bi = 0; bi < NB; ++bi)
-#pragma unroll
-                for (int bj = bi; bj < NB; ++bj, ++t) acc[t] = mfma(u[bi], u[bj], acc[t]);
-        };
-        if (q.wide) long_side<true, NB, S, kWaves>(src, q, i0, lo, hi, add);
-        else long_side<false, NB, S, kWaves>(src, q, i0, lo, hi, add);
-        store_tiles(acc, s_sum, out);
-    }
+    for (int t = 0; t < T; ++t) acc[t] = d4{0.0, 0.0, 0.0, 0.0};
+    if (q.wide) gram_piece<NB, true>(src, q, lo, hi, s_u, acc);
+    else gram_piece<NB, false>(src, q, lo, hi, s_u, acc);
+    __syncthreads();
+    store_tiles(acc, (double*)s_all, a.part + item * muon_part(NB));
+}
+template <int NB, typename G> __global__ __launch_bounds__(kNT) void muon_gram(MuonArgs a) {
+    extern __shared__ __align__(16) float s_all[];
+    gram_item<NB, G>(a, blockIdx.x, s_all);
 }
 
 // ---- the n x n steps ----------------------------------------------------------------------
@@ -332,14 +345,12 @@ __device__ __forceinline__ int mirrored(int v, int lane) { return lane % 16 / 4 
 // One workgroup per matrix, a wave for each block (bi, bj) on or above the diagonal, which
 // holds that block of every square matrix in registers; the operands of products lie in LDS
 // whole, block after block as they are in registers (one block alone is its own operand).
-template <int NB> __global__ __launch_bounds__(NB*(NB + 1) / 2 * kWave) void muon_steps(MuonArgs a) {
+template <int NB> __device__ __forceinline__ void steps_matrix(const MuonArgs& a, int64_t mat, double* smem) {
     constexpr int SQ = NB * NB * 256;
-    extern __shared__ double smem[];
     double *LG = smem, *LQ = smem + SQ, *LP = smem + 2 * SQ, *s_tr = smem + (NB > 1 ? 3 * SQ : 0);
     const int lane = lane_id(), w = wave_id();
     int bi = 0, bj = w;
     while (bj >= NB) bj -= NB - 1 - bi++;  // row after row: (0, 0 ..), (1, 1 ..), ..
-    const int64_t mat = blockIdx.x;
     const MuDesc D = a.descs[gld(a.mat_desc + mat)];
     // the pieces' sums, in their order
     d4 g = {0.0, 0.0, 0.0, 0.0};
@@ -430,6 +441,10 @@ template <int NB> __global__ __launch_bounds__(NB*(NB + 1) / 2 * kWave) void muo
         if (!ok) gst(a.err, 1);
     }
 }
+template <int NB> __global__ __launch_bounds__(NB*(NB + 1) / 2 * kWave) void muon_steps(MuonArgs a) {
+    extern __shared__ double smem[];
+    steps_matrix<NB>(a, blockIdx.x, smem);
+}
 
 // ---- the product and the update ---------------------------------------------------------
 
@@ -455,16 +470,6 @@ __device__ __forceinline__ void update4(const MuDesc& D, const Rate& r, int64_t 
     for (int j = 0; j < 4; ++j) w[j] = w[j] * r.keep - r.lr * (float)x[j];
     if (D.master) write4<NT>(D.master, at, nv, vec, w);
     write4<NT>((P*)D.p, at, nv, vec, w);
-}
-// The lane's place of its v-th (wide) or x-th (tall) group of four in block b.
-template <bool WIDE>
-__device__ __forceinline__ int group_at(const Place& q, int b, int k, int64_t j0, int64_t hi, int lane, int64_t* at) {
-    const int i = WIDE ? 16 * b + 4 * k + lane / 16 : 16 * b + 4 * (lane / 16);
-    const int64_t j = WIDE ? j0 + 4 * (lane % 16) : j0 + 16 * k + lane % 16;
-    *at = WIDE ? q.base + i * q.d + j : q.base + j * q.n + i;
-    if (i >= q.n || j >= hi) return 0;
-    const int64_t left = WIDE ? hi - j : q.n - i;
-    return left < 4 ? (int)left : 4;
 }
 // Entry of a square matrix's block that a tall product's first operand wants: row
 // sigma(l % 16), column 4 (l / 16) + k, of a symmetric block pair.
@@ -536,11 +541,7 @@ __device__ __forceinline__ void apply_piece(const MuonArgs& a, const MuDesc& D, 
     }
 }
 
-// One workgroup: one piece of one matrix, the last first (the pieces that the Gram launch
-// read last are the likeliest to be in a cache still).
-template <int NB, typename P, typename G> __global__ __launch_bounds__(kNT, NB == 4 ? 2 : 1) void muon_apply(MuonArgs a) {
-    __shared__ double s_p[NB > 1 ? NB * NB * 256 : 1];
-    const int64_t item = (int64_t)gridDim.x - 1 - blockIdx.x;
+template <int NB, typename P, typename G> __device__ __forceinline__ void apply_item(const MuonArgs& a, int64_t item, double* s_p) {
     const MuDesc D = a.descs[gld(a.item_desc + item)];
     const int64_t local = item - D.item0, index = local / D.chunks, mat = D.mat0 + index;
     if (gld(a.bad + mat)) return;
@@ -553,6 +554,47 @@ template <int NB, typename P, typename G> __global__ __launch_bounds__(kNT, NB =
     }
     if (q.wide) apply_piece<NB, true, P, G>(a, D, q, lo, hi, pm, s_p);
     else apply_piece<NB, false, P, G>(a, D, q, lo, hi, pm, s_p);
+}
+// One workgroup: one piece of one matrix, the last first (the pieces that the Gram launch
+// read last are the likeliest to be in a cache still).
+template <int NB, typename P, typename G> __global__ __launch_bounds__(kNT, NB == 4 ? 2 : 1) void muon_apply(MuonArgs a) {
+    __shared__ double s_p[NB > 1 ? NB * NB * 256 : 1];
+    apply_item<NB, P, G>(a, (int64_t)gridDim.x - 1 - blockIdx.x, s_p);
+}
+
+// ---- all classes in one set of launches --------------------------------------------------
+
+// Tensors of several classes that together are few pieces: a launch each after the other
+// would wait for one another's latencies (three tensors of odd sizes 133 us, together 96).
+struct MuonAll {
+    MuonArgs a[3];  // small sides up to 16, 32, 64; a class without matrices has no items
+};
+template <typename G> __global__ __launch_bounds__(kNT) void muon_gram_all(MuonAll m) {
+    extern __shared__ __align__(16) float s_all[];
+    int64_t i = blockIdx.x;  // the widest first: they take longest
+    if (i < m.a[2].items) return gram_item<4, G>(m.a[2], i, s_all);
+    i -= m.a[2].items;
+    if (i < m.a[1].items) return gram_item<2, G>(m.a[1], i, s_all);
+    gram_item<1, G>(m.a[0], i - m.a[1].items, s_all);
+}
+__global__ __launch_bounds__(10 * kWave) void muon_steps_all(MuonAll m) {
+    extern __shared__ double smem[];
+    int64_t i = blockIdx.x;
+    if (i < m.a[2].mats) return steps_matrix<4>(m.a[2], i, smem);
+    i -= m.a[2].mats;
+    if (i < m.a[1].mats) {  // waves beyond the blocks end: barriers count those that are there
+        if (wave_id() < 3) steps_matrix<2>(m.a[1], i, smem);
+        return;
+    }
+    if (wave_id() < 1) steps_matrix<1>(m.a[0], i - m.a[1].mats, smem);
+}
+template <typename P, typename G> __global__ __launch_bounds__(kNT, 2) void muon_apply_all(MuonAll m) {
+    __shared__ double s_p[16 * 256];
+    int64_t i = blockIdx.x;
+    if (i < m.a[2].items) return apply_item<4, P, G>(m.a[2], i, s_p);
+    i -= m.a[2].items;
+    if (i < m.a[1].items) return apply_item<2, P, G>(m.a[1], i, s_p);
+    apply_item<1, P, G>(m.a[0], i - m.a[1].items, s_p);
 }
 
 // ---- small sides above 64 -----------------------------------------------------------------
@@ -601,8 +643,8 @@ __global__ __launch_bounds__(kNT) void muon_big_gram(MuonArgs a) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[t] = mfma(u[0], u[1 + t], acc[t]);
     };
-    if (q.wide) long_side<true, 5, 1, 1>(src, q, i0, lo, hi, add);
-    else long_side<false, 5, 1, 1>(src, q, i0, lo, hi, add);
+    if (q.wide) long_side<true, 5, 1>(src, q, i0, lo, hi, add);
+    else long_side<false, 5, 1>(src, q, i0, lo, hi, add);
     double* out = a.part + (int64_t)blockIdx.x * kMuonBigPart + w * 1024;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -799,13 +841,29 @@ constexpr size_t steps_lds(int nb) { return nb > 1 ? (size_t)(3 * nb * nb * 256 
 
 template <int NB, typename P, typename G> hipError_t launch_class(const MuonArgs& a, hipStream_t s) {
     const dim3 items((unsigned)a.items), n(kNT);
-    hipLaunchKernelGGL((muon_gram<NB, G>), items, n, 0, s, a);
+    hipLaunchKernelGGL((muon_gram<NB, G>), items, n, gram_lds<NB>(), s, a);
     hipLaunchKernelGGL((muon_steps<NB>), dim3((unsigned)a.mats), dim3(NB * (NB + 1) / 2 * kWave), steps_lds(NB), s, a);
     hipLaunchKernelGGL((muon_apply<NB, P, G>), items, n, 0, s, a);
     return hipGetLastError();
 }
-template <typename P, typename G> hipError_t launch_pg(const MuonArgs& a, int nb, hipStream_t s) {
-    return nb == 1 ? launch_class<1, P, G>(a, s) : nb == 2 ? launch_class<2, P, G>(a, s) : launch_class<4, P, G>(a, s);
+template <typename P, typename G> hipError_t launch_pg(const MuonArgs (&a)[3], hipStream_t s) {
+    const int64_t items = a[0].items + a[1].items + a[2].items, mats = a[0].mats + a[1].mats + a[2].mats;
+    const int classes = (a[0].items > 0) + (a[1].items > 0) + (a[2].items > 0);
+    if (classes > 1 && items <= kMuonFewItems) {
+        MuonAll m;
+        for (int k = 0; k < 3; ++k) m.a[k] = a[k];
+        const bool wide = a[2].items > 0;
+        const size_t gl = wide ? gram_lds<4>() : gram_lds<2>(), sl = wide ? steps_lds(4) : steps_lds(2);
+        hipLaunchKernelGGL((muon_gram_all<G>), dim3((unsigned)items), dim3(kNT), gl, s, m);
+        hipLaunchKernelGGL(muon_steps_all, dim3((unsigned)mats), dim3(10 * kWave), sl, s, m);
+        hipLaunchKernelGGL((muon_apply_all<P, G>), dim3((unsigned)items), dim3(kNT), 0, s, m);
+        return hipGetLastError();
+    }
+    hipError_t e = hipSuccess;
+    if (a[0].items) e = launch_class<1, P, G>(a[0], s);
+    if (a[1].items && e == hipSuccess) e = launch_class<2, P, G>(a[1], s);
+    if (a[2].items && e == hipSuccess) e = launch_class<4, P, G>(a[2], s);
+    return e;
 }
 template <typename P, typename G> hipError_t launch_big_pg(const MuonArgs& a, int64_t u_elems, hipStream_t s) {
     const dim3 n(kNT);
@@ -831,13 +889,20 @@ template <typename P, typename G> hipError_t launch_big_pg(const MuonArgs& a, in
 }  // namespace
 
 hipError_t prepare_muon() {
-    return hipFuncSetAttribute((const void*)muon_steps<4>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)steps_lds(4));
+    hipError_t e = hipSuccess;
+    for (const void* f : {(const void*)muon_steps<4>, (const void*)muon_steps_all})
+        if (e == hipSuccess) e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)steps_lds(4));
+    for (const void* f : {(const void*)muon_gram<4, float>, (const void*)muon_gram<4, uint16_t>, (const void*)muon_gram_all<float>,
+                          (const void*)muon_gram_all<uint16_t>})
+        if (e == hipSuccess) e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)gram_lds<4>());
+    return e;
 }
 
-hipError_t launch_muon(const MuonArgs& a, int nb, int p_dtype, int g_dtype, hipStream_t s) {
-    if (!grid_fits(a.items, kNT) || !grid_fits(a.mats, nb * nb * kWave)) return hipErrorInvalidConfiguration;
-    if (p_dtype == 0) return g_dtype == 0 ? launch_pg<float, float>(a, nb, s) : launch_pg<float, uint16_t>(a, nb, s);
-    return g_dtype == 0 ? launch_pg<uint16_t, float>(a, nb, s) : launch_pg<uint16_t, uint16_t>(a, nb, s);
+hipError_t launch_muon(const MuonArgs (&a)[3], int p_dtype, int g_dtype, hipStream_t s) {
+    for (int k = 0; k < 3; ++k)
+        if (!grid_fits(a[k].items, kNT) || !grid_fits(a[k].mats, 10 * kWave)) return hipErrorInvalidConfiguration;
+    if (p_dtype == 0) return g_dtype == 0 ? launch_pg<float, float>(a, s) : launch_pg<float, uint16_t>(a, s);
+    return g_dtype == 0 ? launch_pg<uint16_t, float>(a, s) : launch_pg<uint16_t, uint16_t>(a, s);
 }
 hipError_t launch_muon_big(const MuonArgs& a, int64_t u_elems, int p_dtype, int g_dtype, hipStream_t s) {
     if (!grid_fits(a.n_pair, kNT) || !grid_fits(a.n_mul + a.n_big, kNT) || !grid_fits(a.n_sum * 16, kNT) || !grid_fits(a.n_out, kNT)) return hipErrorInvalidConfiguration;

@@ -71,11 +71,13 @@ constexpr int muon_chunk(int nb) { return nb == 4 ? 512 : 1024; }
 // Doubles of one piece's sums: the blocks on and above the diagonal; 64 x 64 of a big matrix.
 constexpr int muon_part(int nb) { return nb * (nb + 1) / 2 * 256; }
 constexpr int kMuonBigPart = 16 * 256;
+constexpr int64_t kMuonFewItems = 512;  // pieces that classes share launches up to
 constexpr int kMuonBigChunk = 256;  // long-side elements of a big matrix's piece
 
 // Once per handle on its device, before its first launch.
 hipError_t prepare_muon();
-hipError_t launch_muon(const MuonArgs& a, int nb, int p_dtype, int g_dtype, hipStream_t s);
+// Matrices with a small side up to 16, 32 and 64 (no items: none).
+hipError_t launch_muon(const MuonArgs (&a)[3], int p_dtype, int g_dtype, hipStream_t s);
 hipError_t launch_muon_big(const MuonArgs& a, int64_t u_elems, int p_dtype, int g_dtype, hipStream_t s);
 
 }  // namespace dlm

@@ -741,7 +741,7 @@ int dlm_muon_destroy(dlm_muon* h);
  * A matrix whose u, or whose iterated factor, is not finite is left unchanged, momentum
  * too, and the error word is set.  Bitwise reproducible.
  * Launches: three for the matrices with a smaller side up to 16, three up to 32, three
- * up to 64, and 3 + 3 steps for those above.
+ * up to 64 (three for all of these where they are few), and 3 + 3 steps for those above.
  */
 int dlm_muon_step(dlm_muon* h, const dlm_muon_cfg* cfg, const float* lr_scale, const float* grad_scale, void* stream);
 
