@@ -235,9 +235,6 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
             d.wd = q.weight_decay;
             d.scale = q.scale;
             nbs[i] = side <= 16 ? 1 : side <= 32 ? 2 : side <= kMuonTileSide ? 4 : 0;
-            const int chunk = nbs[i] ? muon_chunk(nbs[i]) : kMuonBigChunk;
-            if ((d.d + chunk - 1) / chunk > (1 << 30)) return bad(fail(DLM_ESHAPE, "muon_create: tensor %d: too long", i));
-            d.chunks = (int32_t)((d.d + chunk - 1) / chunk);
             v.push_back(span(q.p, elems * ps, true, "p", i));
             v.push_back(span(q.g, elems * gs, false, "g", i));
             v.push_back(span(q.m, (size_t)elems * 4, true, "m", i));
@@ -268,10 +265,15 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
         for (int k = 0; k < 3; ++k) {
             const int nb = 1 << k;
             int64_t items = 0, mats = 0;
+            for (int i = 0; i < n; ++i)
+                if (nbs[i] == nb) items += descs[i].count * ((descs[i].d + muon_chunk(nb, false) - 1) / muon_chunk(nb, false));
+            const int chunk = muon_chunk(nb, items < 256);
+            items = 0;
             std::vector<int32_t> item_desc, mat_desc;
             for (int i = 0; i < n; ++i) {
                 MuDesc& d = descs[i];
                 if (nbs[i] != nb || d.count == 0) continue;
+                d.chunks = (int32_t)((d.d + chunk - 1) / chunk);
                 d.item0 = items;
                 d.mat0 = mats;
                 items += d.count * d.chunks;
@@ -285,6 +287,7 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
             }
             if (!mats) continue;
             h->small[k].items = items;
+            h->small[k].chunk = chunk;
             h->small[k].mats = mats;
             Slot& s = slots[k];
             s.items = put32(item_desc);
@@ -300,6 +303,7 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
             MuDesc& d = descs[i];
             if (nbs[i] || d.count == 0) continue;
             ti.push_back(i);
+            d.chunks = (int32_t)((d.d + kMuonBigChunk - 1) / kMuonBigChunk);
             if (ti.size() > 65535) {
                 delete h;
                 return fail(DLM_ESHAPE, "muon_create: more than 65535 tensors of a smaller side above %d", kMuonTileSide);

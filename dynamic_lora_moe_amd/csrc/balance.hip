@@ -13,6 +13,7 @@
 // binary64 from there on, and stores them as a part; the second launch adds the
 // parts in their order, and the last of its workgroups (a ticket that the first
 // launch clears) adds the sequences: no atomics on values, the same bits every time.
+// (One block of one sequence needs no second launch.)
 #include "balance.hpp"
 #include "gfx950.hpp"
 #include "internal.hpp"
@@ -24,7 +25,7 @@ namespace {
 
 constexpr int kNT = 256;
 constexpr int kV = 8;                // experts per lane
-constexpr int kPiece = 32;           // experts of one sequence that a workgroup of the second launch adds
+constexpr int kPiece = 16;           // experts of one sequence that a workgroup of the second launch adds
 constexpr float kInf = __builtin_huge_valf();
 
 __device__ __forceinline__ float from(float v) { return v; }
@@ -149,7 +150,7 @@ __device__ __forceinline__ int64_t first_row(const BalanceArgs& a, int q) {
     const int64_t t = gld(a.offsets + q);
     return t < 0 ? 0 : t > a.T ? a.T : t;
 }
-// The last sequence that begins at or before row t (0 if none does).
+// The last sequence that begins at or before row t (0 if none does): of a lane's own row,
 __device__ __forceinline__ int sequence_of(const BalanceArgs& a, int64_t t) {
     if (!a.offsets) return 0;
     int lo = 0, hi = a.S - 1;
@@ -160,22 +161,55 @@ __device__ __forceinline__ int sequence_of(const BalanceArgs& a, int64_t t) {
     }
     return lo;
 }
+// and of a row that the wave shares, 64 places at a time (all lanes there).
+__device__ __forceinline__ int sequence_of_wave(const BalanceArgs& a, int64_t t) {
+    if (!a.offsets) return 0;
+    int lo = 0, n = a.S;  // it is one of lo .. lo + n - 1
+    while (n > 1) {
+        const int step = (n + kWave - 1) / kWave, q = lo + lane_id() * step;
+        const uint64_t below = __ballot(lane_id() * step < n && gld(a.offsets + (q < a.S ? q : a.S - 1)) <= t);
+        const int i = below ? 63 - __builtin_clzll(below) : 0;
+        lo += i * step;
+        n = n - i * step < step ? n - i * step : step;
+    }
+    return uniform(lo);
+}
 
-// One workgroup: `per` rows, kNT / L at a time, sequence by sequence.
+// A row's lanes' values, added over the wave's rows (in binary64, a fixed order): every
+// lane l ends with the sum of lanes l % L.
+template <int L> __device__ __forceinline__ double rows_sum(double v) {
+#pragma unroll
+    for (int o = L; o < kWave; o *= 2) v += __shfl_xor(v, o, kWave);
+    return v;
+}
+// Sums over the workgroup, in a fixed order; the result in every thread.
+__device__ __forceinline__ double block_sum(double v, double* s) {
+    v = wave_sum(v);
+    __syncthreads();
+    if (lane_id() == 0) s[wave_id()] = v;
+    __syncthreads();
+    double sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kNT / kWave; ++w) sum += s[w];
+    return sum;
+}
+
+// One workgroup: `per` rows, kNT / L at a time, sequence by sequence.  The only one of the
+// only sequence finishes it by itself.
 template <typename T, int L, int SCORE> __global__ __launch_bounds__(kNT) void balance_parts(BalanceArgs a) {
-    constexpr int TPB = kNT / L;
-    __shared__ float s_p[TPB * L * kV];
+    constexpr int TPB = kNT / L, WAVES = kNT / kWave;
+    __shared__ double s_p[WAVES][L * kV];
     __shared__ int s_cnt[kRouteMaxExperts];
-    __shared__ double s_z[TPB];
-    __shared__ int s_n[TPB];
+    __shared__ double s_z[WAVES], s_n[WAVES];
     const int tid = threadIdx.x, tl = tid / L, lane = tid % L, e0 = lane * kV, E = a.E, k = a.k;
     const int64_t b0 = (int64_t)blockIdx.x * a.per, b1 = b0 + a.per < a.T ? b0 + a.per : a.T;
+    const bool alone = a.S == 1 && gridDim.x == 1;
     if (blockIdx.x == 0 && tid == 0) gst(a.ticket, 0u);
-    for (int q = uniform(sequence_of(a, b0)); q < a.S; ++q) {
+    for (int q = sequence_of_wave(a, b0); q < a.S; ++q) {
         const int64_t q0 = first_row(a, q), q1 = first_row(a, q + 1);
-        if (q0 >= b1) break;
+        if (q0 >= b1 && !alone) break;
         const int64_t lo = q0 > b0 ? q0 : b0, hi = q1 < b1 ? q1 : b1;
-        if (lo >= hi) continue;
+        if (lo >= hi && !alone) continue;
         for (int e = tid; e < E; e += kNT) s_cnt[e] = 0;
         __syncthreads();
         float acc[kV] = {};
@@ -196,44 +230,53 @@ template <typename T, int L, int SCORE> __global__ __launch_bounds__(kNT) void b
             if constexpr (SCORE == kRouteSoftmax) z += (double)r.lse * (double)r.lse;
         }
 #pragma unroll
-        for (int v = 0; v < kV; ++v) s_p[(tl * kV + v) * L + lane] = acc[v];
-        if (lane == 0) {
-            s_z[tl] = z;
-            s_n[tl] = n;
+        for (int v = 0; v < kV; ++v) {
+            const double sum = rows_sum<L>((double)acc[v]);
+            if (tid % kWave < L) s_p[wave_id()][e0 + v] = sum;
+        }
+        const double zw = rows_sum<L>(z), nw = rows_sum<L>((double)n);  // (whole numbers below 2^53)
+        if (tid % kWave == 0) {
+            s_z[wave_id()] = zw;
+            s_n[wave_id()] = nw;
         }
         __syncthreads();
+        double zs = 0.0, ns = 0.0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            zs += s_z[w];
+            ns += s_n[w];
+        }
         const int64_t slot = (int64_t)blockIdx.x + q;
+        double part = 0.0;
         for (int e = tid; e < E; e += kNT) {
             double sum = 0.0;
-#pragma unroll 8
-            for (int j = 0; j < TPB; ++j) sum += (double)s_p[(j * kV + e % kV) * L + e / kV];
-            gst(a.part_p + slot * E + e, sum);
-            gst(a.part_c + slot * E + e, s_cnt[e]);
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) sum += s_p[w][e];
+            if (alone) {
+                const double mean = ns > 0.0 ? sum / ns : 0.0;
+                gst(a.probs + e, (float)mean);
+                gst(a.counts + e, s_cnt[e]);
+                if (ns > 0.0) part += (double)E * s_cnt[e] / ((double)k * ns) * mean;
+            } else {
+                gst(a.part_p + slot * E + e, sum);
+                gst(a.part_c + slot * E + e, s_cnt[e]);
+            }
+        }
+        if (alone) {
+            const double bal = block_sum(part, s_z);
+            if (tid == 0) {
+                gst(a.rows, (int)ns);
+                gst(a.loss, (float)((double)a.alpha * bal));
+                gst(a.loss + 1, ns > 0.0 ? (float)((double)a.zeta * (zs / ns)) : 0.f);
+            }
+            return;
         }
         if (tid == 0) {
-            double zs = 0.0;
-            int ns = 0;
-            for (int j = 0; j < TPB; ++j) {
-                zs += s_z[j];
-                ns += s_n[j];
-            }
             gst(a.part_z + slot, zs);
-            gst(a.part_n + slot, ns);
+            gst(a.part_n + slot, (int)ns);
         }
         __syncthreads();  // the shared sums are read
     }
-}
-
-// Sums over the workgroup, in a fixed order; the result in every thread.
-__device__ __forceinline__ double block_sum(double v, double* s) {
-    v = wave_sum(v);
-    __syncthreads();
-    if (lane_id() == 0) s[wave_id()] = v;
-    __syncthreads();
-    double sum = 0.0;
-#pragma unroll
-    for (int w = 0; w < kNT / kWave; ++w) sum += s[w];
-    return sum;
 }
 
 // One workgroup: kPiece experts of one sequence, kNT / kPiece runs over its parts.
@@ -248,27 +291,27 @@ __global__ __launch_bounds__(kNT) void balance_sum(BalanceArgs a) {
     const int q = blockIdx.x / pieces, piece = blockIdx.x % pieces;
     const int64_t q0 = first_row(a, q), q1 = first_row(a, q + 1);
     const int64_t f = q0 / a.per, l = q1 > q0 ? (q1 - 1) / a.per + 1 : f;  // its blocks
-    double z = 0.0;
-    int n = 0;
-    for (int64_t b = f + tid; b < l; b += kNT) {
-        z += gld(a.part_z + b + q);
-        n += gld(a.part_n + b + q);
-    }
-    z = block_sum(z, s_w);
-    n = (int)block_sum((double)n, s_w);  // whole numbers below 2^53
     const int e = piece * kPiece + tid % kPiece, run = tid / kPiece;
     double p = 0.0;
     int c = 0;
     if (e < E) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t b = f + run; b < l; b += RUNS) {
             p += gld(a.part_p + (b + q) * E + e);
             c += gld(a.part_c + (b + q) * E + e);
         }
     }
+    double z = 0.0;
+    int n = 0;
+#pragma unroll 4
+    for (int64_t b = f + tid; b < l; b += kNT) {
+        z += gld(a.part_z + b + q);
+        n += gld(a.part_n + b + q);
+    }
     s_p[run][tid % kPiece] = p;
     s_c[run][tid % kPiece] = c;
-    __syncthreads();
+    z = block_sum(z, s_w);
+    n = (int)block_sum((double)n, s_w);  // whole numbers below 2^53
     double part = 0.0;
     if (tid < kPiece && e < E) {
 #pragma unroll
@@ -311,14 +354,18 @@ template <typename T, int L, int SCORE> __global__ __launch_bounds__(kNT) void b
     const int64_t b0 = (int64_t)blockIdx.x * a.per, b1 = b0 + a.per < a.T ? b0 + a.per : a.T;
     const double wb = (double)a.alpha * (a.dloss ? (double)gld(a.dloss) : 1.0) / a.S;
     const double wz = 2.0 * (double)a.zeta * (a.dloss ? (double)gld(a.dloss + 1) : 1.0) / a.S;
-    int q = -1;
-    int64_t q0 = 0, q1 = 0;  // the rows that u and zc hold for
+    int q = sequence_of_wave(a, b0);
+    bool fresh = true;
+    int64_t q0 = first_row(a, q), q1 = first_row(a, q + 1);  // the rows that u and zc hold for
     float u[kV] = {}, zc = 0.f;
     for (int64_t t = b0 + tl; t < b1; t += TPB) {
-        if (q < 0 || t >= q1) {
-            q = sequence_of(a, t);
-            q0 = first_row(a, q);
-            q1 = first_row(a, q + 1);
+        if (fresh || t >= q1) {
+            if (t >= q1) {
+                q = sequence_of(a, t);
+                q0 = first_row(a, q);
+                q1 = first_row(a, q + 1);
+            }
+            fresh = false;
             const int n = gld(a.in_rows + q);
             const double by = n > 0 ? 1.0 / n : 0.0;
             zc = (float)(wz * by);
@@ -404,10 +451,10 @@ int lanes_of(int E) {
 
 BalanceLayout balance_layout(int64_t T, int E, int S) {
     BalanceLayout w;
-    // two rounds of rows at least, and no more than 1024 blocks: the second launch reads every part
+    // no more than 512 blocks: the second launch reads every part
     const int64_t round = kNT / lanes_of(E);
-    w.per = 2 * round;
-    while ((T + w.per - 1) / w.per > 1024) w.per *= 2;
+    w.per = round;
+    while ((T + w.per - 1) / w.per > 512) w.per *= 2;
     w.blocks = T > 0 ? (T + w.per - 1) / w.per : 1;
     w.slots = w.blocks + S;
     const int64_t pieces = (E + kPiece - 1) / kPiece;
@@ -431,13 +478,14 @@ hipError_t launch_balance(const BalanceArgs& a, int dtype, hipStream_t s) {
     const int64_t pieces = (a.E + kPiece - 1) / kPiece;
     if (!grid_fits(a.blocks, kNT) || !grid_fits(a.S * pieces, kNT)) return hipErrorInvalidConfiguration;
     const hipError_t e = dtype == 0 ? launch_t<false, float>(a, s) : launch_t<false, uint16_t>(a, s);
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || (a.S == 1 && a.blocks == 1)) return e;
     hipLaunchKernelGGL(balance_sum, dim3((unsigned)(a.S * pieces)), dim3(kNT), 0, s, a);
     return hipGetLastError();
 }
 hipError_t launch_balance_grad(const BalanceArgs& a0, int dtype, hipStream_t s) {
     BalanceArgs a = a0;
-    a.per = 4 * (kNT / lanes_of(a.E));
+    const int64_t round = kNT / lanes_of(a.E);
+    a.per = a.T > 1024 * round ? 4 * round : round;  // what a sequence's rows share is read once
     a.blocks = (a.T + a.per - 1) / a.per;
     if (!grid_fits(a.blocks, kNT)) return hipErrorInvalidConfiguration;
     return dtype == 0 ? launch_t<true, float>(a, s) : launch_t<true, uint16_t>(a, s);

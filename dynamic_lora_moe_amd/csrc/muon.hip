@@ -319,7 +319,7 @@ template <int NB, typename G> __device__ __forceinline__ void gram_item(const Mu
     const MuDesc D = a.descs[gld(a.item_desc + item)];
     const int64_t local = item - D.item0;
     const Place q(D, local / D.chunks);
-    const int64_t lo = local % D.chunks * muon_chunk(NB), end = lo + muon_chunk(NB), hi = end < q.d ? end : q.d;
+    const int64_t lo = local % D.chunks * a.chunk, end = lo + a.chunk, hi = end < q.d ? end : q.d;
     const FromState<G> src{(const G*)D.g, D.m, Mom(a)};
     float* s_u = s_all + wave_id() * gram_in_flight<NB>() * gram_floats<NB>();
     d4 acc[T];
@@ -546,7 +546,7 @@ template <int NB, typename P, typename G> __device__ __forceinline__ void apply_
     const int64_t local = item - D.item0, index = local / D.chunks, mat = D.mat0 + index;
     if (gld(a.bad + mat)) return;
     const Place q(D, index);
-    const int64_t lo = local % D.chunks * muon_chunk(NB), end = lo + muon_chunk(NB), hi = end < q.d ? end : q.d;
+    const int64_t lo = local % D.chunks * a.chunk, end = lo + a.chunk, hi = end < q.d ? end : q.d;
     const double* pm = a.pm + mat * NB * NB * 256;
     if constexpr (NB > 1) {
         for (int i = threadIdx.x; i < NB * NB * 256; i += kNT) s_p[i] = gld(pm + i);

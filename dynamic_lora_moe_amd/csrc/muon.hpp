@@ -45,6 +45,7 @@ struct MuonArgs {
     int32_t* bad;              // [matrix] 1: not finite
     int32_t* err;
     int64_t items, mats;
+    int32_t chunk;             // long-side elements of a piece
     const int32_t* mat_desc;   // of every matrix
     // big matrices
     const MuBig* big;
@@ -66,8 +67,10 @@ struct MuonArgs {
     const float* grad_scale;  // device, or nullptr
 };
 
-// Long-side elements of one piece, for nb 16-wide blocks of the small side (1, 2 or 4).
-constexpr int muon_chunk(int nb) { return nb == 4 ? 512 : 1024; }
+// Long-side elements of one piece, for nb 16-wide blocks of the small side (1, 2 or 4): of wider ones
+// half as many where that leaves CUs without one (odd sizes 97 us against 75; 70B-shaped banks in halves
+// 363 against 351).
+constexpr int muon_chunk(int nb, bool few) { return nb == 1 || !few ? 512 : 256; }
 // Doubles of one piece's sums: the blocks on and above the diagonal; 64 x 64 of a big matrix.
 constexpr int muon_part(int nb) { return nb * (nb + 1) / 2 * 256; }
 constexpr int kMuonBigPart = 16 * 256;

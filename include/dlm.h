@@ -193,7 +193,8 @@ int dlm_route_backward(const void* logits, int64_t ld, const int32_t* idx, const
  *          zeta * mean over the sequences of the mean of (log sum_e exp l_e)^2
  * A sequence without rows counts as 0 in both means.  zeta must be 0 for sigmoid
  * scores.  Everything is written, not added to; also for T = 0.  p is fp32, its sums
- * binary64; bitwise reproducible.  Two launches, no allocation.
+ * binary64; bitwise reproducible.  Two launches (one for a single sequence of few
+ * rows), no allocation.
  * workspace: >= dlm_balance_workspace_size(T, E, n_seq) bytes, 256-byte aligned, of
  * any content.
  */
