@@ -10,6 +10,9 @@ fallback: if the library is missing or fails to load, importing the ops raises.
   Layers([(W, A, B), ...], E, r, scale).switch(old, new)   # in place, one launch
   sgmm(x, idx, g, A, B, y, scale)                          # y updated in place
   AdamW(params, grads, ...).step(lr)                       # many tensors at once
+  Muon(params, grads, ...).step(lr)                        # orthogonalised momentum
+  balance(logits, idx, ...)       -> (loss, counts, rows, probs); balance_backward
+  Int8Group([(x, W, w_scale, y), ...]).run()               # a base in 8 bits; .backward()
   SgmmGroup([(x, A, B, y), ...], E, r, scale).run(idx, g)  # .bind_grads(...).backward(idx, g, dg)
 """
 from __future__ import annotations
@@ -78,7 +81,7 @@ class dlm_muon_param(C.Structure):
                 ("rows", C.c_int64), ("cols", C.c_int64), ("weight_decay", C.c_float), ("scale", C.c_float)]
 
 
-MAX_MUON_STEPS = 10
+MAX_MUON_STEPS, MAX_BALANCE_SEQS = 10, 65536
 
 
 class dlm_muon_cfg(C.Structure):
@@ -810,7 +813,6 @@ class Int8Group:
             arr[k] = dlm_i8_problem(x.data_ptr(), W.data_ptr(), w_scale.data_ptr(), y.data_ptr(), d_in, d_out)
         dt = _dt(x0)
         _here(x0, None, "problem 0 x")
-        torch.cuda.current_stream(x0.device).synchronize()  # W is read on another stream
         h = C.c_void_p()
         _check(load().dlm_i8_group_create(arr, n, dt, C.byref(h)), "dlm_i8_group_create")
         self._h = h
@@ -1062,8 +1064,8 @@ class Muon:
             _like(m, f"state {k}", p.shape, torch.float32, p0.device)
             if w is not None:
                 _like(w, f"master {k}", p.shape, torch.float32, p0.device)
-            rows, cols = p.shape[-2:]
-            count = p.numel() // (rows * cols) if p.numel() else 0
+            rows, cols = p.shape[-2:] if p.numel() else (1, 1)
+            count = p.numel() // (rows * cols)
             arr[k] = dlm_muon_param(p.data_ptr(), g.data_ptr(), None if w is None else w.data_ptr(), m.data_ptr(), count,
                                     rows, cols, float(wd[k]), self._scale(scales[k], rows, cols))
         _here(p0, None, "parameter 0")

@@ -309,7 +309,8 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
                 return fail(DLM_ESHAPE, "muon_create: more than 65535 tensors of a smaller side above %d", kMuonTileSide);
             }
             const int nb = (d.n + 63) / 64 * 4, groups = nb / 4, pairs = groups * (groups + 1) / 2;
-            if (!grid_fits((int64_t)tp.size() + d.count * d.chunks * pairs, 256)) {
+            if (!grid_fits((int64_t)tp.size() + d.count * d.chunks * pairs, 256) ||
+                !grid_fits((int64_t)to.size() + d.count * ((d.d + 63) / 64) * groups, 256)) {
                 delete h;
                 return fail(DLM_ESHAPE, "muon_create: the sizes need a launch grid of more than 2^32 - 1 work-items");
             }
@@ -331,6 +332,11 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
                     to.push_back(at);
                     toa.push_back(o);
                 }
+            }
+            if (!grid_fits((int64_t)to.size(), 256) || !grid_fits((int64_t)tm.size() + (int64_t)bigs.size(), 256) ||
+                !grid_fits((int64_t)ts.size() * 16, 256)) {
+                delete h;
+                return fail(DLM_ESHAPE, "muon_create: the sizes need a launch grid of more than 2^32 - 1 work-items");
             }
         }
         if (!bigs.empty()) {
@@ -574,7 +580,8 @@ int dlm_i8_group_create(const dlm_i8_problem* probs, int32_t n, int32_t dtype, d
         std::vector<I8Rows> rows;
         std::vector<I8Prod> prods;
         int64_t q0 = 0;
-        e = hipMalloc((void**)&h->d_w, bytes);
+        e = hipDeviceSynchronize();  // W may still be written, on any stream
+        if (e == hipSuccess) e = hipMalloc((void**)&h->d_w, bytes);
         if (e == hipSuccess) e = hipMemset(h->d_w + h->s_at[0], 0, bytes - h->s_at[0]);  // the scales' padding
         for (int i = 0; i < n && e == hipSuccess; ++i) {
             const dlm_i8_problem& q = h->probs[i];

@@ -772,16 +772,18 @@ template <typename T> hipError_t launch_products(const I8Args& a, hipStream_t s)
     if (a.T <= kI8FewT) return a.T16 == 1 ? launch_few<T, 1>(a, s) : a.T16 == 2 ? launch_few<T, 2>(a, s) : launch_few<T, 4>(a, s);
     const auto tiles = [&](int kind) { return (a.T + kI8Cols[kind] - 1) / kI8Cols[kind] * a.tiles[kind]; };  // (square tiles)
     const int64_t big = tiles(kI8Big), mid = tiles(kI8Mid), small = tiles(kI8Small);
-    if (!grid_fits(small, 1024)) return hipErrorInvalidConfiguration;
     // A CU takes one tile at a time, of 256, 128 or 64 square: rounds of a tile for every CU last as 24 : 10 : 4 (54, 22
     // and 9 us at 4096 columns summed).  512 rows of two 11008 x 4096 products: 58 us in large tiles, 67 in middle ones;
     // 2048 rows of one 4096 x 4096: 56 in middle ones, 65 in large, 81 in small; 128 rows 13.5 in small ones, 22 in middle.
     const auto rounds = [](int64_t n) { return (n + kCus - 1) / kCus; };
     const int64_t tb = 24 * rounds(big), tm = 10 * rounds(mid), ts = 4 * rounds(small);
-    if (tb <= tm && tb <= ts) hipLaunchKernelGGL(kBigTile<T>, dim3((unsigned)big), dim3(512), kBigLds, s, a);
-    else if (tm <= ts) hipLaunchKernelGGL(kMidTile<T>, dim3((unsigned)mid), dim3(512), kMidLds, s, a);
-    else hipLaunchKernelGGL(kSmallTile<T>, dim3((unsigned)small), dim3(1024), kSmallLds, s, a);
-    return hipGetLastError();
+    const auto go = [&](auto* kernel, int64_t n, int threads, size_t lds) {
+        if (!grid_fits(n, threads)) return hipErrorInvalidConfiguration;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(threads), lds, s, a);
+        return hipGetLastError();
+    };
+    if (tb <= tm && tb <= ts) return go(kBigTile<T>, big, 512, kBigLds);
+    return tm <= ts ? go(kMidTile<T>, mid, 512, kMidLds) : go(kSmallTile<T>, small, 1024, kSmallLds);
 }
 
 }  // namespace

@@ -140,6 +140,29 @@ def test_pitch_and_alignment(dtype):
         assert (out == 5.0).all()  # nothing beside the rows
 
 
+def test_as_many_sequences_as_there_may_be():
+    T, S = 70000, dlm.MAX_BALANCE_SEQS
+    l, idx = _inputs(T, 8, 2, torch.float32, 6)
+    cut = torch.randint(0, T + 1, (S - 1,), generator=torch.Generator().manual_seed(1)).sort().values
+    off = torch.cat([torch.zeros(1, dtype=torch.long), cut, torch.tensor([T])]).int()
+    loss, counts, rows, probs = dlm.balance(l.cuda(), idx.cuda(), alpha=1.0, offsets=off.cuda())
+    n = off.diff().long()
+    seq = torch.repeat_interleave(torch.arange(S), n)
+    p = ref.scores(l.double(), "softmax")[0]
+    want = torch.zeros((S, 8), dtype=torch.float64).index_add_(0, seq, p) / n.clamp(min=1)[:, None]
+    hot = torch.zeros((T, 8), dtype=torch.float64).scatter_add_(1, idx.long(), torch.ones((T, 2), dtype=torch.float64))
+    c = torch.zeros((S, 8), dtype=torch.float64).index_add_(0, seq, hot)
+    assert torch.equal(rows.cpu().long(), n) and torch.equal(counts.cpu().double(), c)
+    assert (probs.cpu().double() - want).abs().max() < 200 * U
+    assert abs(float(loss[0]) - float((8 * c / (2 * n.clamp(min=1)[:, None]) * want).sum() / S)) < 400 * U
+    dl = dlm.balance_backward(l.cuda(), counts, rows, 2, alpha=1.0, offsets=off.cuda())
+    u = (8 / (2 * S * n.clamp(min=1).double() ** 2)[:, None] * c)[seq]
+    g = p * (u - (u * p).sum(1, keepdim=True))
+    assert ((dl.cpu().double() - g).abs() <= 300 * U * u.abs().amax(1, keepdim=True) + 2.0 ** -120).all()
+    with pytest.raises(dlm.DLMError):
+        dlm.balance(l.cuda(), idx.cuda(), offsets=torch.zeros(S + 2, dtype=torch.int32, device="cuda"))
+
+
 def test_no_rows():
     for off in (None, torch.tensor([0, 0, 0], dtype=torch.int32, device="cuda")):
         S = 1 if off is None else 2

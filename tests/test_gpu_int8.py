@@ -122,10 +122,31 @@ def test_shared_inputs(T, dtype):
     _run(T, [(100, 96), (64, 72), (33, 96), (128, 96), (72, 72)], dtype, reads=[0, 1, 0, 0, 2], accumulate=True)
 
 
-@pytest.mark.parametrize("T,shapes", [(600, [(4096, 520)]), (1025, [(2048, 264), (264, 2048)]), (513, [(8192, 136)])])
+@pytest.mark.parametrize("T,shapes", [(600, [(4096, 520)]), (1025, [(2048, 264), (264, 2048)]), (513, [(8192, 136)]),
+                                      (2100, [(8190, 200)]), (2305, [(7000, 129), (640, 65), (100, 300)]), (4200, [(4100, 72)])])
 def test_large_tiles(T, shapes):
     _run(T, shapes, torch.bfloat16)
     _run(T, shapes, torch.float32, accumulate=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1, 2, 3, 4])
+def test_up_to_four_rows(T, dtype):
+    """In one launch and in two (many columns, or codes that do not fit beside one another): each with a ragged
+    end, a row of zeros and one that is not finite."""
+    for o, i in ((300, 1000), (40000, 136), (64, 12300), (64, 70000), (33, 49000)):
+        x, (W, ws) = _x(T, i, dtype, 1), _weight(o, i, 2)
+        x[T - 1, 3] = float("nan") if T > 1 else 0.0
+        x[0] = 0.0 if T > 2 else x[0]
+        y = torch.empty((T, o), dtype=dtype, device="cuda")
+        dlm.Int8Group([(x.cuda(), W.cuda(), ws.cuda(), y)]).run()
+        _near(y, ref.forward(x, W, ws), dtype)
+        alone = torch.empty((T, o), dtype=dtype, device="cuda")  # the rows among others: the same bits
+        buf = torch.cat([x, _x(80, i, dtype, 3)]).cuda()
+        many = torch.empty((T + 80, o), dtype=dtype, device="cuda")
+        dlm.Int8Group([(buf, W.cuda(), ws.cuda(), many)]).run()
+        alone.copy_(many[:T])
+        assert torch.equal(alone.isnan(), y.isnan()) and torch.equal(alone.nan_to_num(), y.nan_to_num())
 
 
 @pytest.mark.parametrize("shift", [1, 2, 3])

@@ -112,6 +112,11 @@ def test_small_sides_above_64(p_dtype, g_dtype, master):
     _run(BIG + [(8, 40)], p_dtype, g_dtype, master, wd=0.1)
 
 
+def test_classes_of_many_pieces():
+    """Small sides of every class in more pieces than share launches."""
+    _run([(300, 16, 40), (40, 150, 30), (8, 40, 5000), (7, 6000, 60), (300, 9, 7)], torch.bfloat16, torch.float32, True, steps=1)
+
+
 @pytest.mark.parametrize("shift", [1, 2, 3])
 def test_unaligned_tensors(shift):
     """Tensors at any multiple of their element's size: the same results as aligned ones, bit for bit."""
