@@ -342,6 +342,7 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
         if (!bigs.empty()) {
             MuonArgs& g = h->big;
             g.n_big = (int64_t)bigs.size();
+            g.only = bigs[0];
             g.items = (int64_t)ti.size();
             g.n_pair = (int64_t)tp.size();
             g.n_sum = (int64_t)ts.size();

@@ -169,7 +169,8 @@ __device__ __forceinline__ int group_at(const Place& q, int b, int k, int64_t j0
 
 // Operands of columns [lo, hi) of the long side for one wave, for NB blocks of the
 // small side from i0 on, handed to `use(a)` four columns at a time; the loads of the next 16 S
-// columns are out while these are used.  Wide: a lane loads
+// columns are out while these are used (three such ahead leave a SIMD one wave: 44 us for 8192 x 256,
+// against 30).  Wide: a lane loads
 // four neighbours of its row; tall: the small side is contiguous, and a wave's lanes are.
 template <bool WIDE, int NB, int S, typename SRC, typename F>
 __device__ __forceinline__ void long_side(const SRC& src, const Place& q, const int (&i0)[NB], int64_t lo, int64_t hi, F use) {
@@ -206,10 +207,9 @@ __device__ __forceinline__ void long_side(const SRC& src, const Place& q, const 
                 use(a);
             }
     };
-    int64_t j0 = lo;
-    if (j0 >= hi) return;
-    load(j0, raw[0]);
-    for (; j0 < hi; j0 += 2 * STEP) {
+    if (lo >= hi) return;
+    load(lo, raw[0]);
+    for (int64_t j0 = lo; j0 < hi; j0 += 2 * STEP) {
         if (j0 + STEP < hi) load(j0 + STEP, raw[1]);
         spend(raw[0]);
         if (j0 + STEP >= hi) break;
@@ -330,7 +330,7 @@ template <int NB, typename G> __device__ __forceinline__ void gram_item(const Mu
     __syncthreads();
     store_tiles(acc, (double*)s_all, a.part + item * muon_part(NB));
 }
-template <int NB, typename G> __global__ __launch_bounds__(kNT) void muon_gram(MuonArgs a) {
+template <int NB, typename G> __global__ __launch_bounds__(kNT, NB == 4 ? 2 : 1) void muon_gram(MuonArgs a) {
     extern __shared__ __align__(16) float s_all[];
     gram_item<NB, G>(a, blockIdx.x, s_all);
 }
@@ -615,6 +615,10 @@ template <typename G> __global__ __launch_bounds__(kNT) void muon_big_u(MuonArgs
     }
 }
 
+// A workgroup's matrix: the only one comes with the arguments, which saves two dependent
+// loads in each of the launches.
+__device__ __forceinline__ MuBig big_of(const MuonArgs& a, const int32_t* table) { return a.n_big == 1 ? a.only : a.big[gld(table)]; }
+
 // The 64 x 64 blocks on and above the diagonal, by number: (bi, bj), bi <= bj.
 __device__ __forceinline__ void pair_of(int t, int groups, int* bi, int* bj) {
     int i = 0;
@@ -625,7 +629,7 @@ __device__ __forceinline__ void pair_of(int t, int groups, int* bi, int* bj) {
 // One workgroup: one 64 x 64 of one piece's Gram matrix (rows 64 bi .., columns 64 bj ..),
 // 16 rows of it a wave.
 __global__ __launch_bounds__(kNT) void muon_big_gram(MuonArgs a) {
-    const MuBig B = a.big[gld(a.pair_big + blockIdx.x)];
+    const MuBig B = big_of(a, a.pair_big + blockIdx.x);
     const MuDesc D = a.descs[B.desc];
     const int groups = B.nb / 4, pairs = groups * (groups + 1) / 2;
     const int64_t local = (int64_t)blockIdx.x - B.part0;
@@ -654,7 +658,7 @@ __global__ __launch_bounds__(kNT) void muon_big_gram(MuonArgs a) {
 
 // The pieces' sums of one 16 x 16, in their order, into G and its mirror image.
 __global__ __launch_bounds__(kNT) void muon_big_sum(MuonArgs a) {
-    const MuBig B = a.big[gld(a.sum_big + blockIdx.x / 16)];
+    const MuBig B = big_of(a, a.sum_big + blockIdx.x / 16);
     const MuDesc D = a.descs[B.desc];
     const int groups = B.nb / 4, pairs = groups * (groups + 1) / 2, pair = gld(a.sum_pair + blockIdx.x / 16);
     int bi, bj;
@@ -673,7 +677,7 @@ __global__ __launch_bounds__(kNT) void muon_big_sum(MuonArgs a) {
 // The trace of big matrix i and what follows from it, by one workgroup.
 __device__ __forceinline__ void big_norm(const MuonArgs& a, int i) {
     __shared__ double s_tr[kWaves];
-    const MuBig B = a.big[i];
+    const MuBig B = a.n_big == 1 ? a.only : a.big[i];
     const double* G = a.square + B.off;
     double tr = 0.0;
     for (int e = threadIdx.x; e < 16 * B.nb; e += kNT) {
@@ -708,9 +712,9 @@ struct BigMats {
 template <int MODE> __global__ __launch_bounds__(kNT) void muon_big_mul(MuonArgs a, BigMats M, int step, int only_p) {
     __shared__ double s_sum[kWaves][256];
     if (MODE == MUL_S && (int64_t)blockIdx.x >= a.n_mul) return big_norm(a, (int)(blockIdx.x - a.n_mul));
-    const int bigi = gld(a.mul_big + blockIdx.x);
-    const MuBig B = a.big[bigi];
-    const int nb = B.nb, lane = lane_id(), w = wave_id(), block = gld(a.mul_at + blockIdx.x), bi = block / nb, bj = block % nb;
+    const int bigi = a.n_big == 1 ? 0 : gld(a.mul_big + blockIdx.x);
+    const MuBig B = a.n_big == 1 ? a.only : a.big[bigi];
+    const int nb = B.nb, lane = lane_id(), w = wave_id(), block = a.n_big == 1 ? (int)blockIdx.x : gld(a.mul_at + blockIdx.x), bi = block / nb, bj = block % nb;
     const double f = MODE != MUL_S && step == 0 ? gld(a.meta + 2 * bigi + 1) : 1.0;  // G is f times what is stored
     const double ca = a.coefs[step][0], cb = a.coefs[step][1] * f, cc = a.coefs[step][2] * f * f;
     const auto frag = [&](const double* X, int r, int c, int v) { return gld(X + B.off + ((int64_t)r * nb + c) * 256 + 64 * v + lane); };
@@ -825,9 +829,9 @@ __device__ __forceinline__ void big_apply(const MuonArgs& a, const MuDesc& D, co
     }
 }
 template <typename P, typename G> __global__ __launch_bounds__(kNT) void muon_big_apply(MuonArgs a, const double* PM) {
-    const int bigi = gld(a.out_big + blockIdx.x);
+    const int bigi = a.n_big == 1 ? 0 : gld(a.out_big + blockIdx.x);
     if (gld(a.bad + bigi)) return;
-    const MuBig B = a.big[bigi];
+    const MuBig B = a.n_big == 1 ? a.only : a.big[bigi];
     const MuDesc D = a.descs[B.desc];
     const int groups = B.nb / 4, at = gld(a.out_at + blockIdx.x), ib = at % groups * 4 + wave_id();
     const int64_t j0 = (int64_t)(at / groups) * 64;

@@ -48,6 +48,7 @@ struct MuonArgs {
     int32_t chunk;             // long-side elements of a piece
     const int32_t* mat_desc;   // of every matrix
     // big matrices
+    MuBig only;                // the first
     const MuBig* big;
     const int32_t* pair_big;   // per (matrix, chunk, pair of 64-blocks)
     const int32_t* sum_big;    // per (matrix, pair)
