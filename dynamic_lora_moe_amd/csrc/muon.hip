@@ -459,13 +459,14 @@ struct Rate {
         lr = l * D.scale;
     }
 };
-// Four neighbours' weights from their four products.
+// Four neighbours' weights, and what their four products make of them.
 template <bool NT, typename P>
-__device__ __forceinline__ void update4(const MuDesc& D, const Rate& r, int64_t at, int nv, bool vec, const double (&x)[4]) {
-    if (nv <= 0) return;
-    float w[4];
+__device__ __forceinline__ void weights4(const MuDesc& D, int64_t at, int nv, bool vec, float (&w)[4]) {
     if (D.master) read4<NT>((const float*)D.master, at, nv, vec, w);
     else read4<NT>((const P*)D.p, at, nv, vec, w);
+}
+template <bool NT, typename P>
+__device__ __forceinline__ void update4(const MuDesc& D, const Rate& r, int64_t at, int nv, bool vec, const double (&x)[4], float (&w)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = w[j] * r.keep - r.lr * (float)x[j];
     if (D.master) write4<NT>(D.master, at, nv, vec, w);
@@ -477,67 +478,79 @@ __device__ __forceinline__ int tall_entry(int k, int lane) {
     return lane / 16 * 64 + k * 16 + 4 * (lane % 4) + lane % 16 / 4;
 }
 
-// A wave's share of a piece: 64 of the long side at a time.
+// A wave's share of a piece: 64 UN of the long side at a time.  Loads do not move up past
+// stores (the compiler cannot know that they differ), so all of g and m comes first (block
+// by block a 64 x 64 tile waited eight times for memory, 30 us) and a block's weights come
+// before its products, which hide them.
 template <int NB, bool WIDE, typename P, typename G>
 __device__ __forceinline__ void apply_piece(const MuonArgs& a, const MuDesc& D, const Place& q, int64_t lo, int64_t hi, const double* pm, const double* s_p) {
+    constexpr int UN = NB == 1 ? 2 : 1;
+    // an access covers whole cache lines (tall rows of more than one block take several)
+    constexpr bool LAST = WIDE || NB == 1;
     const int lane = lane_id();
     double own[4];
     if constexpr (NB == 1) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) own[k] = gld(pm + (WIDE ? 64 * k + lane : tall_entry(k, lane)));
     }
-    // an access covers whole cache lines (tall rows of more than one block take several)
-    constexpr bool LAST = WIDE || NB == 1;
     const Mom mom(a);
     const Rate rate(a, D);
-    for (int64_t j0 = lo + wave_id() * 64; j0 < hi; j0 += kWaves * 64) {
-        float u[NB][4][4];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float g[4][4], m[4][4];
+    for (int64_t j0 = lo + wave_id() * 64 * UN; j0 < hi; j0 += kWaves * 64 * UN) {
+        float u[UN][NB][4][4], m[UN][NB][4][4];
+        const auto each = [&](int n, int b, auto f) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 int64_t at;
-                const int nv = group_at<WIDE>(q, b, k, j0, hi, lane, &at);
-                read4<LAST>((const G*)D.g, at, nv, q.vec, g[k]);
-                read4<LAST>((const float*)D.m, at, nv, q.vec, m[k]);
+                const int nv = group_at<WIDE>(q, b, k, j0 + 64 * n, hi, lane, &at);
+                f(k, at, nv);
             }
+        };
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                int64_t at;
-                const int nv = group_at<WIDE>(q, b, k, j0, hi, lane, &at);
+        for (int n = 0; n < UN; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    m[k][c] = mom.m(m[k][c], g[k][c]);
-                    u[b][k][c] = mom.u(m[k][c], g[k][c]);
-                }
-                write4<LAST>(D.m, at, nv, q.vec, m[k]);
+            for (int b = 0; b < NB; ++b)
+                each(n, b, [&](int k, int64_t at, int nv) {
+                    read4<LAST>((const G*)D.g, at, nv, q.vec, u[n][b][k]);
+                    read4<LAST>((const float*)D.m, at, nv, q.vec, m[n][b][k]);
+                });
+#pragma unroll
+        for (int n = 0; n < UN; ++n)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                each(n, b, [&](int k, int64_t at, int nv) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float g = u[n][b][k][c];
+                        m[n][b][k][c] = mom.m(m[n][b][k][c], g);
+                        u[n][b][k][c] = mom.u(m[n][b][k][c], g);
+                    }
+                    write4<LAST>(D.m, at, nv, q.vec, m[n][b][k]);
+                });
+#pragma unroll
+        for (int n = 0; n < UN; ++n)
+#pragma unroll
+            for (int ib = 0; ib < NB; ++ib) {
+                float w[4][4];
+                each(n, ib, [&](int k, int64_t at, int nv) { weights4<LAST, P>(D, at, nv, q.vec, w[k]); });
+                d4 acc[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[c] = d4{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        double x;
+                        if constexpr (NB > 1) x = s_p[(kb * NB + ib) * 256 + (WIDE ? 64 * k + lane : tall_entry(k, lane))];
+                        else x = own[k];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[c] = mfma(x, (double)(WIDE ? u[n][kb][k][c] : u[n][kb][c][k]), acc[c]);
+                    }
+                each(n, ib, [&](int k, int64_t at, int nv) {
+                    const double x[4] = {WIDE ? acc[0][k] : acc[k][0], WIDE ? acc[1][k] : acc[k][1], WIDE ? acc[2][k] : acc[k][2],
+                                         WIDE ? acc[3][k] : acc[k][3]};
+                    update4<LAST, P>(D, rate, at, nv, q.vec, x, w[k]);
+                });
             }
-        }
-#pragma unroll
-        for (int ib = 0; ib < NB; ++ib) {
-            d4 acc[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[c] = d4{0.0, 0.0, 0.0, 0.0};
-#pragma unroll
-            for (int kb = 0; kb < NB; ++kb)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    double x;
-                    if constexpr (NB > 1) x = s_p[(kb * NB + ib) * 256 + (WIDE ? 64 * k + lane : tall_entry(k, lane))];
-                    else x = own[k];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[c] = mfma(x, (double)(WIDE ? u[kb][k][c] : u[kb][c][k]), acc[c]);
-                }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                int64_t at;
-                const int nv = group_at<WIDE>(q, ib, k, j0, hi, lane, &at);
-                const double x[4] = {WIDE ? acc[0][k] : acc[k][0], WIDE ? acc[1][k] : acc[k][1], WIDE ? acc[2][k] : acc[k][2],
-                                     WIDE ? acc[3][k] : acc[k][3]};
-                update4<LAST, P>(D, rate, at, nv, q.vec, x);
-            }
-        }
     }
 }
 
@@ -813,19 +826,25 @@ __device__ __forceinline__ void big_apply(const MuonArgs& a, const MuDesc& D, co
         if (kb + 2 < B.nb) load(kb + 2, u[0], x[0]);
         spend(u[1], x[1]);
     }
+    float g[4][4], m[4][4], wt[4][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         int64_t at;
         const int nv = group_at<WIDE>(q, ib, k, j0, hi, lane, &at);
-        float g[4], m[4];
-        read4((const G*)D.g, at, nv, q.vec, g);
-        read4((const float*)D.m, at, nv, q.vec, m);
+        read4((const G*)D.g, at, nv, q.vec, g[k]);
+        read4((const float*)D.m, at, nv, q.vec, m[k]);
+        weights4<false, P>(D, at, nv, q.vec, wt[k]);
+    }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) m[c] = mom.m(m[c], g[c]);
-        write4(D.m, at, nv, q.vec, m);
+    for (int k = 0; k < 4; ++k) {
+        int64_t at;
+        const int nv = group_at<WIDE>(q, ib, k, j0, hi, lane, &at);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) m[k][c] = mom.m(m[k][c], g[k][c]);
+        write4(D.m, at, nv, q.vec, m[k]);
         const double y[4] = {WIDE ? acc[0][k] : acc[k][0], WIDE ? acc[1][k] : acc[k][1], WIDE ? acc[2][k] : acc[k][2],
                              WIDE ? acc[3][k] : acc[k][3]};
-        update4<false, P>(D, rate, at, nv, q.vec, y);
+        update4<false, P>(D, rate, at, nv, q.vec, y, wt[k]);
     }
 }
 template <typename P, typename G> __global__ __launch_bounds__(kNT) void muon_big_apply(MuonArgs a, const double* PM) {
