@@ -310,7 +310,9 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
             }
             const int nb = (d.n + 63) / 64 * 4, groups = nb / 4, pairs = groups * (groups + 1) / 2;
             if (!grid_fits((int64_t)tp.size() + d.count * d.chunks * pairs, 256) ||
-                !grid_fits((int64_t)to.size() + d.count * ((d.d + 63) / 64) * groups, 256)) {
+                !grid_fits((int64_t)to.size() + d.count * ((d.d + 63) / 64) * groups, 256) ||
+                !grid_fits((int64_t)tm.size() + (int64_t)bigs.size() + d.count * (nb * nb + 1), 256) ||
+                !grid_fits(((int64_t)ts.size() + d.count * pairs) * 16, 256)) {
                 delete h;
                 return fail(DLM_ESHAPE, "muon_create: the sizes need a launch grid of more than 2^32 - 1 work-items");
             }
@@ -332,11 +334,6 @@ int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, in
                     to.push_back(at);
                     toa.push_back(o);
                 }
-            }
-            if (!grid_fits((int64_t)to.size(), 256) || !grid_fits((int64_t)tm.size() + (int64_t)bigs.size(), 256) ||
-                !grid_fits((int64_t)ts.size() * 16, 256)) {
-                delete h;
-                return fail(DLM_ESHAPE, "muon_create: the sizes need a launch grid of more than 2^32 - 1 work-items");
             }
         }
         if (!bigs.empty()) {
