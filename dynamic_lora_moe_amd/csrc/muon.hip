@@ -10,7 +10,8 @@
 // its weak directions in fp32 (a direction 10^-4 of the strongest is 10^-8 of G, and
 // each of the K steps makes it, and its error, a^2 = 12 times larger): G, P and the
 // sums are binary64, on the binary64 matrix instructions, whose products of fp32
-// values are exact.  At rank 16 they cost a tenth of the memory's time.
+// values are exact.  Their rate (66 TFLOP/s in a large product) and a copy's, 4.6 TB/s,
+// meet near a small side of 80; at rank 16 they are a fifth of the memory's time.
 //
 // Launches per class of matrices (small sides up to 16, 32, 64): the Gram matrices of
 // pieces of the long side, the n x n steps (a workgroup per matrix, a wave per 16 x 16
@@ -25,6 +26,13 @@
 //
 // A matrix whose u is not finite is left as it was, momentum too, and the handle's
 // error word is set.
+//
+// Measured: 322 million bf16 weights at rank 16, fp32 gradients and masters, 1.74 ms: the
+// Gram pass 0.47, the steps 0.025, the update 1.24; both passes move 5.5 TB/s (with u read
+// twice that is 4.05 TB/s of the bytes that a step cannot do without).  10 million: 19, 8 and
+// 45 us.  Rank 64, 16.8 million: 53, 43 and 87 us, where neither memory nor the products
+// are busy: two waves a SIMD (a tile's 64 values of u and its products' operands), each in
+// a chain of loads, products and stores.  8192 x 256: 136 us in 20 launches.
 #include <utility>
 
 #include "gfx950.hpp"
@@ -578,7 +586,8 @@ template <int NB, typename P, typename G> __global__ __launch_bounds__(kNT, NB =
 // ---- all classes in one set of launches --------------------------------------------------
 
 // Tensors of several classes that together are few pieces: a launch each after the other
-// would wait for one another's latencies (three tensors of odd sizes 133 us, together 96).
+// would wait for one another's latencies (three tensors of odd sizes 133 us
+// against 96 when they were joined; 78 now).
 struct MuonAll {
     MuonArgs a[3];  // small sides up to 16, 32, 64; a class without matrices has no items
 };

@@ -21,7 +21,13 @@
  *   dlm_sgmm_group_backward  the gradients of the grouped SGMM: its inputs',
  *                its banks' and its gates';
  *   dlm_adamw_*  AdamW over many tensors in one launch, with fp32 or 8-bit
- *                moments.
+ *                moments;
+ *   dlm_balance  the router's balance loss over packed sequences, its counts, and
+ *                dlm_balance_backward, its gradient;
+ *   dlm_muon_*   a step of momentum orthogonalised by Newton-Schulz products over
+ *                many matrices;
+ *   dlm_i8_*     the frozen base's products in 8-bit integers, and their input
+ *                gradients.
  *
  * Conventions (all calls):
  *   - Pointers are DEVICE pointers unless marked (host).  The caller owns every
