@@ -30,7 +30,7 @@
 // Measured: 322 million bf16 weights at rank 16, fp32 gradients and masters, 1.74 ms: the
 // Gram pass 0.47, the steps 0.025, the update 1.24; both passes move 5.5 TB/s (with u read
 // twice that is 4.05 TB/s of the bytes that a step cannot do without).  10 million: 19, 8 and
-// 45 us.  Rank 64, 16.8 million: 53, 43 and 87 us, where neither memory nor the products
+// 45 us.  Rank 64, 16.8 million: 53, 42 and 87 us, where neither memory nor the products
 // are busy: two waves a SIMD (a tile's 64 values of u and its products' operands), each in
 // a chain of loads, products and stores.  8192 x 256: 136 us in 20 launches.
 #include <utility>
@@ -355,7 +355,7 @@ __device__ __forceinline__ int mirrored(int v, int lane) { return lane % 16 / 4 
 // whole, block after block as they are in registers (one block alone is its own operand).
 template <int NB> __device__ __forceinline__ void steps_matrix(const MuonArgs& a, int64_t mat, double* smem) {
     constexpr int SQ = NB * NB * 256;
-    double *LG = smem, *LQ = smem + SQ, *LP = smem + 2 * SQ, *s_tr = smem + (NB > 1 ? 3 * SQ : 0);
+    double *LG = smem, *LQ = smem + SQ, *LP = smem + 2 * SQ, *LR = smem + 3 * SQ, *s_tr = smem + (NB > 1 ? 4 * SQ : 0);
     const int lane = lane_id(), w = wave_id();
     int bi = 0, bj = w;
     while (bj >= NB) bj -= NB - 1 - bi++;  // row after row: (0, 0 ..), (1, 1 ..), ..
@@ -422,15 +422,16 @@ template <int NB> __device__ __forceinline__ void steps_matrix(const MuonArgs& a
         const d4 q = a.coefs[k][0] * eye + a.coefs[k][1] * g + a.coefs[k][2] * s;
         put(LQ, q);
         sync();
-        p = k == 0 ? q : mul(LP, p, LQ, q);
-        if (k + 1 == a.steps) break;
+        if (k + 1 == a.steps) {
+            p = k == 0 ? q : mul(LP, p, LQ, q);
+            break;
+        }
         const d4 r = mul(LG, g, LQ, q);
-        sync();  // G and P are read
-        put(LG, r);
+        p = k == 0 ? q : mul(LP, p, LQ, q);
+        put(LR, r);
+        sync();  // R is there, G and P are read
         put(LP, p);
-        sync();
-        g = mul(LG, r, LQ, q);
-        sync();
+        g = mul(LR, r, LQ, q);
         put(LG, g);
         sync();
     }
@@ -587,7 +588,7 @@ template <int NB, typename P, typename G> __global__ __launch_bounds__(kNT, NB =
 
 // Tensors of several classes that together are few pieces: a launch each after the other
 // would wait for one another's latencies (three tensors of odd sizes 133 us
-// against 96 when they were joined; 78 now).
+// against 96 when they were joined; 76 now).
 struct MuonAll {
     MuonArgs a[3];  // small sides up to 16, 32, 64; a class without matrices has no items
 };
@@ -610,11 +611,16 @@ __global__ __launch_bounds__(10 * kWave) void muon_steps_all(MuonAll m) {
     }
     if (wave_id() < 1) steps_matrix<1>(m.a[0], i - m.a[1].mats, smem);
 }
-template <typename P, typename G> __global__ __launch_bounds__(kNT, 2) void muon_apply_all(MuonAll m) {
-    __shared__ double s_p[16 * 256];
+// WIDEST: some small side is above 32.  Such calls are few pieces of long chains: one wave a
+// SIMD and no spilled registers (8 x 16 x 8192, 8 x 8192 x 16, 8192 x 64 and 8 x 64 x 4096 98 us,
+// against 106 with two; without such sides two waves, 49 against 56).
+template <bool WIDEST, typename P, typename G> __global__ __launch_bounds__(kNT, WIDEST ? 1 : 2) void muon_apply_all(MuonAll m) {
+    __shared__ double s_p[WIDEST ? 16 * 256 : 4 * 256];
     int64_t i = blockIdx.x;
-    if (i < m.a[2].items) return apply_item<4, P, G>(m.a[2], i, s_p);
-    i -= m.a[2].items;
+    if constexpr (WIDEST) {
+        if (i < m.a[2].items) return apply_item<4, P, G>(m.a[2], i, s_p);
+        i -= m.a[2].items;
+    }
     if (i < m.a[1].items) return apply_item<2, P, G>(m.a[1], i, s_p);
     apply_item<1, P, G>(m.a[0], i - m.a[1].items, s_p);
 }
@@ -869,7 +875,7 @@ template <typename P, typename G> __global__ __launch_bounds__(kNT) void muon_bi
 
 // ---- launches ---------------------------------------------------------------------------
 
-constexpr size_t steps_lds(int nb) { return nb > 1 ? (size_t)(3 * nb * nb * 256 + nb) * 8 : 64; }
+constexpr size_t steps_lds(int nb) { return nb > 1 ? (size_t)(4 * nb * nb * 256 + nb) * 8 : 64; }
 
 template <int NB, typename P, typename G> hipError_t launch_class(const MuonArgs& a, hipStream_t s) {
     const dim3 items((unsigned)a.items), n(kNT);
@@ -888,7 +894,8 @@ template <typename P, typename G> hipError_t launch_pg(const MuonArgs (&a)[3], h
         const size_t gl = wide ? gram_lds<4>() : gram_lds<2>(), sl = wide ? steps_lds(4) : steps_lds(2);
         hipLaunchKernelGGL((muon_gram_all<G>), dim3((unsigned)items), dim3(kNT), gl, s, m);
         hipLaunchKernelGGL(muon_steps_all, dim3((unsigned)mats), dim3(10 * kWave), sl, s, m);
-        hipLaunchKernelGGL((muon_apply_all<P, G>), dim3((unsigned)items), dim3(kNT), 0, s, m);
+        if (wide) hipLaunchKernelGGL((muon_apply_all<true, P, G>), dim3((unsigned)items), dim3(kNT), 0, s, m);
+        else hipLaunchKernelGGL((muon_apply_all<false, P, G>), dim3((unsigned)items), dim3(kNT), 0, s, m);
         return hipGetLastError();
     }
     hipError_t e = hipSuccess;
