@@ -144,6 +144,20 @@ def test_muon_validation():
     assert lib.dlm_muon_destroy(None) == dlm.DLM_EINVAL and lib.dlm_muon_status(None, None, None) == dlm.DLM_EINVAL
 
 
+@built
+@pytest.mark.parametrize("count, rows, cols", [(1 << 30, 2, 2), (1 << 25, 16, 40), (1 << 24, 40, 33), (1 << 20, 65, 65), (300000, 512, 512),
+                                               (1 << 15, 128, 1 << 17), (1, 65, 1 << 30)])
+def test_muon_grids(count, rows, cols):
+    """More pieces, matrices or products than a launch can hold are refused, before tables are made for them."""
+    import time
+
+    h, tb = C.c_void_p(), 1 << 44
+    start = time.perf_counter()
+    rc = dlm.load().dlm_muon_create(_muon_params((tb, 2 * tb, None, 3 * tb, count, rows, cols, 0.0, 1.0)), 1, 0, 0, C.byref(h))
+    assert rc == dlm.DLM_ESHAPE and h.value is None
+    assert time.perf_counter() - start < 2
+
+
 @pytest.mark.parametrize("shape", [(3, 8), (8, 3), (5, 5)])
 def test_muon_by_values_is_muon_by_products(shape):
     import muon_ref
