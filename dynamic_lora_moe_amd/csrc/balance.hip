@@ -9,10 +9,11 @@
 //
 // The gradient needs the counts but not the means, so each direction reads the
 // logits once.  L lanes hold a row, eight experts each.  The forward launch adds p
-// over a block's rows of one sequence, in fp32 per lane (at most `per` rows) and
-// binary64 from there on, and stores them as a part; the second launch adds the
-// parts in their order, and the last of its workgroups (a ticket that the first
-// launch clears) adds the sequences: no atomics on values, the same bits every time.
+// over a block's rows of one sequence, in binary64 (a lane has per L / 256 of them, as
+// many as the batch makes it; fp32 sums cost as much), and stores the sums as a part; the
+// second launch adds the parts in their order, and the last of its workgroups (a ticket
+// that the first launch clears) adds the sequences: no atomics on values, the same bits
+// every time.
 // (One block of one sequence needs no second launch.)
 //
 // 16384 rows of 256 fp32 logits, sigmoid, 8 sequences: 14 us, 9 and 15 for the gradient that
@@ -218,7 +219,7 @@ template <typename T, int L, int SCORE> __global__ __launch_bounds__(kNT) void b
         if (lo >= hi && !alone) continue;
         for (int e = tid; e < E; e += kNT) s_cnt[e] = 0;
         __syncthreads();
-        float acc[kV] = {};
+        double acc[kV] = {};
         double z = 0.0;
         int n = 0;
         for (int64_t t = lo + tl; t < hi; t += TPB) {
@@ -231,13 +232,13 @@ template <typename T, int L, int SCORE> __global__ __launch_bounds__(kNT) void b
             }
             const Row r = row_probs<L, SCORE>(l, p, slope);
 #pragma unroll
-            for (int v = 0; v < kV; ++v) acc[v] += p[v];
+            for (int v = 0; v < kV; ++v) acc[v] += (double)p[v];
             n += r.live ? 1 : 0;
             if constexpr (SCORE == kRouteSoftmax) z += (double)r.lse * (double)r.lse;
         }
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            const double sum = rows_sum<L>((double)acc[v]);
+            const double sum = rows_sum<L>(acc[v]);
             if (tid % kWave < L) s_p[wave_id()][e0 + v] = sum;
         }
         const double zw = rows_sum<L>(z), nw = rows_sum<L>((double)n);  // (whole numbers below 2^53)

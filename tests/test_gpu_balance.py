@@ -260,6 +260,36 @@ def test_past_2_32_logits():
     assert (dl[:1000, :8].float() - 2 * 0.05 * math.log(E) / (T - 150) / E).abs().max() < 2.0 ** -8 * 2 * 0.05 * math.log(E) / (T - 150) / E
 
 
+def _repeated(T, E, k, dtype, score, offsets):
+    """T rows that are all one: (probs, loss) against that row's own scores, to their error and one rounding
+    of the mean.  A sum's rounding then falls the same way every time, so one that is kept in fp32 over the
+    batch is off by a share of its length: a hundred of 2^-24 after 500 rows."""
+    row, _ = _inputs(1, E, 1, dtype, T % 1000 + E)
+    p, _, lse, _, _ = ref.scores(row.double(), score)
+    tol = (ref.relative(row.double(), p, score) + 2 * U) * p
+    idx = torch.full((T, k), E // 3, dtype=torch.int32, device="cuda")
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    b = ref.borders(T, offsets)
+    loss, counts, rows, probs = dlm.balance(row.cuda().expand(T, E).contiguous(), idx, score=score, offsets=off)
+    lens = torch.tensor(b).diff()
+    assert torch.equal(rows.cpu().long(), lens) and torch.equal(counts[:, E // 3].cpu().long(), lens * k)
+    err = (probs.cpu().double() - p).abs()
+    assert (err <= tol)[lens > 0].all(), float((err / (U * p))[lens > 0].max())
+    # every slot of every row names one expert: f is E for it
+    share = int((lens > 0).sum()) / (len(b) - 1)
+    assert abs(float(loss[0]) - share * E * float(p[0, E // 3])) <= share * E * float(tol[0, E // 3] + 2 * U * p[0, E // 3])
+
+
+@pytest.mark.parametrize("T,E,dtype,score,offsets", [
+    (1 << 21, 512, torch.float32, "softmax", None), (1 << 21, 300, torch.bfloat16, "sigmoid", None),
+    (1 << 21, 512, torch.bfloat16, "softmax", [0, 1 << 20, 1 << 20, (1 << 20) + 5, 1 << 21]),
+    (1 << 24, 8, torch.float32, "sigmoid", [100, 1 << 23, 1 << 24])])
+def test_long_batches_of_equal_rows(T, E, dtype, score, offsets):
+    """Thousands of rows a lane, whose probabilities are no powers of two."""
+    print("balance", T, E, flush=True)
+    _repeated(T, E, 2, dtype, score, offsets)
+
+
 def test_refusals_of_the_binding():
     x, idx = torch.zeros((4, 8), device="cuda"), torch.zeros((4, 2), dtype=torch.int32, device="cuda")
     _, counts, rows, _ = dlm.balance(x, idx)
