@@ -353,16 +353,19 @@ __device__ __forceinline__ int mirrored(int v, int lane) { return lane % 16 / 4 
 // One workgroup per matrix, a wave for each block (bi, bj) on or above the diagonal, which
 // holds that block of every square matrix in registers; the operands of products lie in LDS
 // whole, block after block as they are in registers (one block alone is its own operand).
-template <int NB> __device__ __forceinline__ void steps_matrix(const MuonArgs& a, int64_t mat, double* smem) {
-    constexpr int SQ = NB * NB * 256;
+// A workgroup of more waves (WAVES, shared with wider classes): those without a block only
+// take part in the barriers, which every wave of a workgroup has to reach.
+template <int NB, int WAVES = NB * (NB + 1) / 2> __device__ __forceinline__ void steps_matrix(const MuonArgs& a, int64_t mat, double* smem) {
+    constexpr int SQ = NB * NB * 256, BLOCKS = NB * (NB + 1) / 2;
     double *LG = smem, *LQ = smem + SQ, *LP = smem + 2 * SQ, *LR = smem + 3 * SQ, *s_tr = smem + (NB > 1 ? 4 * SQ : 0);
     const int lane = lane_id(), w = wave_id();
-    int bi = 0, bj = w;
+    const bool on = WAVES == BLOCKS || w < BLOCKS;
+    int bi = 0, bj = on ? w : 0;
     while (bj >= NB) bj -= NB - 1 - bi++;  // row after row: (0, 0 ..), (1, 1 ..), ..
     const MuDesc D = a.descs[gld(a.mat_desc + mat)];
     // the pieces' sums, in their order
     d4 g = {0.0, 0.0, 0.0, 0.0};
-    {
+    if (on) {
         const double* part = a.part + (D.item0 + (mat - D.mat0) * D.chunks) * muon_part(NB) + w * 256 + lane;
 #pragma unroll 4
         for (int c = 0; c < D.chunks; ++c, part += muon_part(NB))
@@ -371,12 +374,12 @@ template <int NB> __device__ __forceinline__ void steps_matrix(const MuonArgs& a
     }
     // |u|^2 is the trace
     double tr = 0.0;
-    if (bi == bj) {
+    if (on && bi == bj) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) tr += on_diagonal(v, lane) ? g[v] : 0.0;
         tr = wave_sum(tr);
     }
-    if (lane == 0 && bi == bj) s_tr[bi] = tr;
+    if (lane == 0 && on && bi == bj) s_tr[bi] = tr;
     __syncthreads();
     tr = 0.0;
 #pragma unroll
@@ -389,7 +392,7 @@ template <int NB> __device__ __forceinline__ void steps_matrix(const MuonArgs& a
     for (int v = 0; v < 4; ++v) eye[v] = bi == bj && on_diagonal(v, lane) ? 1.0 : 0.0;
     // the block and its mirror image
     const auto put = [&](double* L, const d4& x) {
-        if constexpr (NB > 1) {
+        if (NB > 1 && on) {
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 L[(bi * NB + bj) * 256 + 64 * v + lane] = x[v];
@@ -400,6 +403,7 @@ template <int NB> __device__ __forceinline__ void steps_matrix(const MuonArgs& a
     // X Y of symmetric X, Y (all are polynomials of G): an operand's block (bi, bk) is read as (bk, bi)
     const auto mul = [&](const double* LX, const d4& x, const double* LY, const d4& y) {
         d4 r = {0.0, 0.0, 0.0, 0.0};
+        if (!on) return r;
 #pragma unroll
         for (int bk = 0; bk < NB; ++bk)
 #pragma unroll
@@ -437,12 +441,14 @@ template <int NB> __device__ __forceinline__ void steps_matrix(const MuonArgs& a
     }
     p *= inv;
     bool fin = true;
-    double* out = a.pm + mat * SQ;
+    if (on) {
+        double* out = a.pm + mat * SQ;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        fin = fin && __builtin_isfinite(p[v]);
-        gst(out + (bi * NB + bj) * 256 + 64 * v + lane, p[v]);
-        if (bi != bj) gst(out + (bj * NB + bi) * 256 + mirrored(v, lane), p[v]);
+        for (int v = 0; v < 4; ++v) {
+            fin = fin && __builtin_isfinite(p[v]);
+            gst(out + (bi * NB + bj) * 256 + 64 * v + lane, p[v]);
+            if (bi != bj) gst(out + (bj * NB + bi) * 256 + mirrored(v, lane), p[v]);
+        }
     }
     const bool ok = __syncthreads_and(fin && __builtin_isfinite(tr));
     if (threadIdx.x == 0) {
@@ -605,11 +611,8 @@ __global__ __launch_bounds__(10 * kWave) void muon_steps_all(MuonAll m) {
     int64_t i = blockIdx.x;
     if (i < m.a[2].mats) return steps_matrix<4>(m.a[2], i, smem);
     i -= m.a[2].mats;
-    if (i < m.a[1].mats) {  // waves beyond the blocks end: barriers count those that are there
-        if (wave_id() < 3) steps_matrix<2>(m.a[1], i, smem);
-        return;
-    }
-    if (wave_id() < 1) steps_matrix<1>(m.a[0], i - m.a[1].mats, smem);
+    if (i < m.a[1].mats) return steps_matrix<2, 10>(m.a[1], i, smem);
+    steps_matrix<1, 10>(m.a[0], i - m.a[1].mats, smem);
 }
 // WIDEST: some small side is above 32.  Such calls are few pieces of long chains: one wave a
 // SIMD and no spilled registers (8 x 16 x 8192, 8 x 8192 x 16, 8192 x 64 and 8 x 64 x 4096 98 us,

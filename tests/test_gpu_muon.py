@@ -314,6 +314,26 @@ def test_past_2_32_elements():
         torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("shapes", [[(5, 16, 200), (3, 100, 30)], [(5, 9, 70), (3, 64, 100)], [(3, 20, 600), (2, 300, 64)],
+                                    [(5, 16, 200), (3, 100, 30), (2, 50, 90)]])
+def test_classes_in_joint_launches(shapes):
+    """Tensors of several classes in one handle, whose launches hold waves for the widest: each class as by itself,
+    bit for bit, a matrix that is not finite among them."""
+    sides = []
+    for groups in ([list(range(len(shapes)))], [[k] for k in range(len(shapes))]):
+        ps = [_rnd(s, k, 0.02).cuda() for k, s in enumerate(shapes)]
+        gs = [_rnd(s, 9 + k, 1e-3).cuda() for k, s in enumerate(shapes)]
+        for g in gs:
+            g[1, 0, 3] = float("nan")
+        opts = [dlm.Muon([ps[k] for k in ks], [gs[k] for k in ks]) for ks in groups]
+        for o in opts:
+            o.step(0.1)
+        assert all(o.status() == dlm.DLM_EDEVICE for o in opts)
+        sides.append(ps + [m for o in opts for m in o.states])
+    assert all(torch.equal(a, b) for a, b in zip(*sides))
+    assert not torch.equal(sides[0][0][0].cpu(), _rnd(shapes[0], 0, 0.02)[0])
+
+
 def test_refusals_of_the_binding(monkeypatch):
     p, g = torch.zeros((4, 10), device="cuda"), torch.zeros((4, 10), device="cuda")
     for make in (lambda: dlm.Muon([], []), lambda: dlm.Muon([p], [g[:3]]), lambda: dlm.Muon([p], [g.cpu()]),
