@@ -617,7 +617,7 @@ int dlm_i8_group_create(const dlm_i8_problem* probs, int32_t n, int32_t dtype, d
             if (h->fwd.d) (void)hipFree(h->fwd.d);
             delete h;
         }
-        return e == hipErrorOutOfMemory ? fail(DLM_ENOMEM, "i8_group_create: an allocation failed") : hip_fail(e, "i8_group_create");
+        return hip_fail(e, "i8_group_create");
     }
     *out = h;
     return ok();
@@ -786,7 +786,7 @@ int dlm_i8_group_bind_grads(dlm_i8_group* h, const void* const* dy, void* const*
     if (e != hipSuccess) {
         if (wt) (void)hipFree(wt);
         if (t.d) (void)hipFree(t.d);
-        return e == hipErrorOutOfMemory ? fail(DLM_ENOMEM, "i8_group_bind_grads: an allocation failed") : hip_fail(e, "i8_group_bind_grads");
+        return hip_fail(e, "i8_group_bind_grads");
     }
     if (h->d_wt) (void)hipFree(h->d_wt);
     if (h->bwd.d) (void)hipFree(h->bwd.d);

@@ -11,6 +11,8 @@ Tolerances (U = 2^-24).
      entries, as errors do not conspire: 1e-8.  A u off by one rounding in a few elements moves X by
      485 2^-24 of them, below that too.  Then one fp32 rounding, and the update's two: 4 U |X|.
   w: 4 U |w| on top; bf16 parameters are the master's rounding."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
@@ -312,6 +314,22 @@ def test_past_2_32_elements():
         opt.close()
         del opt, p, g
         torch.cuda.empty_cache()
+
+
+def test_scratch_that_does_not_fit_is_refused_and_leaves_nothing_behind():
+    """More scratch memory than the device has (450 GB): the status of a failed allocation, and the next calls,
+    of the library and of others, do not find its error."""
+    at = 1 << 44
+    big = (dlm.dlm_muon_param * 1)(dlm.dlm_muon_param(at, 2 * at, None, 3 * at, 1, 512, 1 << 26, 0.0, 1.0))
+    h = C.c_void_p()
+    p, g = _rnd((16, 300), 1).cuda(), _rnd((16, 300), 2).cuda()
+    opt, q = dlm.Muon([p], [g]), p.clone()
+    torch.cuda.synchronize()
+    assert dlm.load().dlm_muon_create(big, 1, 0, 0, C.byref(h)) == dlm.DLM_ENOMEM and h.value is None
+    opt.step(0.1)
+    q.add_(1.0)
+    torch.cuda.synchronize()
+    assert opt.status() == dlm.DLM_OK and bool(p.isfinite().all())
 
 
 @pytest.mark.parametrize("shapes", [[(5, 16, 200), (3, 100, 30)], [(5, 9, 70), (3, 64, 100)], [(3, 20, 600), (2, 300, 64)],
