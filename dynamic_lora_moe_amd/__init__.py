@@ -1029,9 +1029,12 @@ class Muon:
     becomes its rounding), or None.  states: per parameter its momentum, fp32 of the
     parameter's shape; zeros are made when None.
     steps, coefs: the products X <- a X + (b A + c A^2) X, (a, b, c) for all or one triple
-    per step.  scale: the update's factor: "shape" = sqrt(max(1, rows / cols)), "rms" =
-    0.2 sqrt(max(rows, cols)) (an entry's size then is about AdamW's), a number, or one
-    per parameter.  weight_decay: one value, or one per parameter."""
+    per step.  scale: the update's factor: "shape" = sqrt(max(1, rows / cols)), which is
+    sqrt(max(1, outputs / inputs)) for matrices stored outputs first, as A [r][d_in] and
+    B [d_out][r] are (one stored inputs first, as a router's [d][E], takes the number
+    max(1, cols / rows) ** 0.5), "rms" = 0.2 sqrt(max(rows, cols)) (an entry's size then is
+    about AdamW's), a number, or one per parameter.  weight_decay: one value, or one per
+    parameter."""
 
     def __init__(self, params, grads, masters=None, states=None, momentum: float = 0.95, nesterov: bool = True,
                  weight_decay=0.0, eps: float = 1e-7, steps: int = 5, coefs=(3.4445, -4.7750, 2.0315), scale="shape"):

@@ -46,7 +46,8 @@ class AdapterTraining:
                  w_scale [d_out]): forward() then writes the base product to y, and
                  backward() its gradient to dx (written, problems that share a dx summed),
                  under the adapters' shares.
-    optimizer:   "adamw" or "muon" (momentum, muon_scale: Muon's; state_bits 32).
+    optimizer:   "adamw" or "muon" (momentum, muon_scale: Muon's, "shape" with the outputs and
+                 inputs of each map, W_r's too; state_bits 32).
     alpha, zeta, offsets: the balance loss over the sequences that offsets cut the rows
                  into (balance()'s arguments); none where both are 0.  Its value is `loss`."""
 
@@ -87,7 +88,10 @@ class AdapterTraining:
         keep = masters and self.W_r.dtype != torch.float32
         self.masters = [p.float() for p in params] if keep else None
         if optimizer == "muon":
-            self.opt = Muon(params, grads, masters=self.masters, momentum=momentum, weight_decay=weight_decay, scale=muon_scale)
+            scales = list(muon_scale) if isinstance(muon_scale, (list, tuple)) else [muon_scale] * len(params)
+            if len(scales) == len(params) and scales[-1] == "shape":  # W_r has its inputs first
+                scales[-1] = max(1.0, E / self.W_r.shape[0]) ** 0.5
+            self.opt = Muon(params, grads, masters=self.masters, momentum=momentum, weight_decay=weight_decay, scale=scales)
         else:
             self.opt = AdamW(params, grads, masters=self.masters, state_bits=state_bits, beta1=beta1, beta2=beta2, eps=eps,
                              weight_decay=weight_decay, seed=seed)

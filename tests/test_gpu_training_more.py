@@ -156,6 +156,32 @@ def test_the_composed_step_replayed_or_on_another_stream(how, optimizer):
     assert all(torch.equal(a, b) for a, b in zip(*res))
 
 
+@pytest.mark.parametrize("scale", ["shape", "rms", 0.5])
+def test_update_factors(scale):
+    """"shape" is sqrt(max(1, outputs / inputs)) of the map that a matrix is: A [r][d_in] and B [d_out][r] have their
+    outputs first, the router's weight [d][E] its inputs."""
+    tr, _ = _trainer(5, optimizer="muon", muon_scale=scale, weight_decay=0.0)
+    tr.forward()
+    tr.backward()
+    weights, grads = [w.clone() for w in tr.masters], [g.clone() for g in tr.opt.grads]
+    tr.step(1e-2)
+    torch.cuda.synchronize()
+    assert tr.status() == dlm.DLM_OK
+    maps = [m for o, i in SHAPES for m in ((R, i), (o, R))] + [(E, D)]  # (outputs, inputs)
+    for k, (w0, g, (o, i)) in enumerate(zip(weights, grads, maps)):
+        shape = (-1,) + tuple(w0.shape[-2:])
+        g = g.cpu().numpy().reshape(shape)
+        _, u = muon_ref.momentum(g, np.zeros_like(g), 0.95, True)
+        new, old = (t.cpu().double().numpy().reshape(shape) for t in (tr.masters[k], w0))
+        s = 1e-2 * {"shape": max(1.0, o / i) ** 0.5, "rms": 0.2 * max(o, i) ** 0.5}.get(scale, scale)
+        for e in range(g.shape[0]):
+            x = muon_ref.by_values(u[e].astype(np.float64), np.float64(np.float32(1e-7)), [muon_ref.COEFS] * 5)
+            # as for the steps over a base
+            tol = 4 * U * np.abs(old[e]) + s * (8 * U * np.abs(x) + 1e-8 * max(np.abs(x).max(), 1e-30))
+            assert (np.abs(new[e] - (old[e] - s * x)) <= tol).all(), (k, e)
+    tr.close()
+
+
 def test_refusals():
     x, As, Bs, dys, W, x_r, W_r = [[u.cuda() for u in t] if isinstance(t, list) else t.cuda() for t in _setup(torch.bfloat16)]
     proj = [(x[r], a, b, torch.empty_like(dy)) for r, a, b, dy in zip(READS, As, Bs, dys)]
