@@ -320,10 +320,11 @@ __global__ __launch_bounds__(256) void i8_transpose(const int8_t* __restrict__ W
 
 // ---- products ------------------------------------------------------------------------------
 
-// Four results and what they join, rounded.
+// Four results.  The channel's factor goes first: rows run up to the largest fp32 value, whose
+// scale times a sum of codes is past it, weights are small.
 __device__ __forceinline__ void scaled(const i32x4& acc, float s, const float (&w)[4], float (&v)[4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = (float)acc[j] * s * w[j];
+    for (int j = 0; j < 4; ++j) v[j] = (float)acc[j] * w[j] * s;
 }
 template <typename T> __device__ __forceinline__ void put1(T* out, float v, bool add) {
     if (add) v += value(gld(out));

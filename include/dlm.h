@@ -589,8 +589,8 @@ int dlm_i8_group_destroy(dlm_i8_group* h);
 /*
  * y[t][o] = round( s_t w_scale[o] sum_k q[t][k] W[o][k] ) for T rows of every problem, with
  * q and s the row's codes and scale as dlm_i8_quantize makes them.  The sum is exact; the
- * factors are applied in fp32.  A row of x that is not finite gives NaN in its row of y,
- * and nothing else.  Two launches (the codes, once for problems that share an x; the
+ * factors are applied in fp32, w_scale's first.  A row of x that is not finite gives NaN in
+ * its row of y, and nothing else.  Two launches (the codes, once for problems that share an x; the
  * products), no allocation; one for up to four rows whose codes fit a workgroup's LDS (four
  * of 11008 columns do).  Up to 64 rows the weights are read once, straight into the
  * products' operands.  T = 0 enqueues nothing.

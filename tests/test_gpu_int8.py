@@ -224,6 +224,23 @@ def test_codes(T, d, dtype):
     assert (buf == 9).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1, 4, 12, 64, 100, 700])
+def test_rows_at_the_edge_of_fp32(T, dtype):
+    """Rows up to the largest values of their type, with channels that bring the results back into range: finite."""
+    o, i = 520, 136
+    x, (W, ws) = _x(T, i, torch.float32, 1), _weight(o, i, 2)
+    x = x / x.abs().amax(1, keepdim=True) * 3.3e38
+    x[0, 1:], x[0, 0] = 0.0, 3.3e38
+    x = x.to(dtype)
+    ws = ws * 1e-3
+    y = torch.empty((T, o), dtype=dtype, device="cuda")
+    dlm.Int8Group([(x.cuda(), W.cuda(), ws.cuda(), y)]).run()
+    want = ref.forward(x, W, ws)
+    assert (want.abs() < 1e38).all() and (want.abs() > 1e34).any()
+    _near(y, want, dtype)
+
+
 def test_codes_of_every_half():
     """Rows whose quotients are exactly k + 1/2, and one fp32 step to either side."""
     h = torch.arange(0, 127, dtype=torch.float64) + 0.5
