@@ -769,9 +769,13 @@ template <typename T> constexpr auto* kSmallTile = &i8_many<T, 2, 2, 2, 2, 4, 4,
 template <typename T, int TB> hipError_t launch_few(const I8Args& a, hipStream_t s) {
     const dim3 n(kFewWaves * kWave);
     // as many columns a workgroup as leave two for every CU
-    if (TB >= 4 && a.tiles[kI8Few4] >= 2 * kCus)
-        hipLaunchKernelGGL((i8_few<T, TB, 4, kI8Few4>), dim3((unsigned)a.tiles[kI8Few4]), n, 0, s, a);
-    else if (a.T > 4 && a.tiles[kI8Few2] >= 2 * kCus)
+    if constexpr (TB >= 4) {
+        if (a.tiles[kI8Few4] >= 2 * kCus) {
+            hipLaunchKernelGGL((i8_few<T, TB, 4, kI8Few4>), dim3((unsigned)a.tiles[kI8Few4]), n, 0, s, a);
+            return hipGetLastError();
+        }
+    }
+    if (a.T > 4 && a.tiles[kI8Few2] >= 2 * kCus)
         hipLaunchKernelGGL((i8_few<T, TB, 2, kI8Few2>), dim3((unsigned)a.tiles[kI8Few2]), n, 0, s, a);
     else
         hipLaunchKernelGGL((i8_few<T, TB, 1, kI8Few1>), dim3((unsigned)a.tiles[kI8Few1]), n, 0, s, a);
