@@ -745,6 +745,9 @@ int dlm_muon_destroy(dlm_muon* h);
  * lr = cfg's times *lr_scale.  lr_scale and grad_scale are DEVICE floats or NULL (1): a
  * captured step reads them on every replay.  m and u are fp32; the products are formed
  * on the smaller side in binary64 and X is rounded to fp32 once.
+ * Coefficients with |a| above 1 raise weak directions, and the rounding of A in them, by
+ * a^2 a step: with five steps of (3.4445, -4.775, 2.0315) X is off by less than its own
+ * rounding, with ten by 1e-4 in directions below 1e-5 of the strongest.
  * A matrix whose u, or whose iterated factor, is not finite is left unchanged, momentum
  * too, and the error word is set.  Bitwise reproducible.
  * Launches: three for the matrices with a smaller side up to 16, three up to 32, three

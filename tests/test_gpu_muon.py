@@ -316,6 +316,29 @@ def test_past_2_32_elements():
         torch.cuda.empty_cache()
 
 
+def test_ten_of_the_default_steps():
+    """Twice the usual number of products that raise weak directions.  Directions of one size: the usual bounds.
+    (Their error, some 2^-53 / 10^-4 of themselves, grows by 1.7 a step at most once they are near 1.)  Down to
+    10^-6 of the strongest: a sum's error, d 2^-53 of |u|^2, and n 2^-53 for each of the square products, are
+    raised by a^2 a step, which the singular values of the difference are held to."""
+    coefs = [ref.COEFS] * 10
+    for shape in ((16, 300), (48, 300), (300, 40), (80, 130)):
+        g, p, m = _rnd(shape, 1).cuda(), torch.zeros(shape, device="cuda"), torch.zeros(shape, device="cuda")
+        dlm.Muon([p], [g], states=[m], scale=1.0, steps=10).step(1.0)
+        _compare(torch.zeros(shape), None, torch.zeros(shape), g, p, None, m, 1.0, 0.0, 1.0, coefs=coefs)
+        n, d = min(shape), max(shape)
+        q, _ = torch.linalg.qr(_rnd((n, n), 7).double())
+        fall = torch.logspace(0, -6, n, dtype=torch.float64)
+        h = (q @ (fall[:, None] * _rnd((n, d), 2).double())).float()
+        h = (h if shape[0] == n else h.t()).contiguous().cuda()
+        dlm.Muon([p.zero_()], [h], states=[m.zero_()], scale=1.0, steps=10).step(1.0)
+        _, u = ref.momentum(h.cpu().numpy(), np.zeros(shape, np.float32), BETA, True)
+        x = ref.by_values(u.astype(np.float64), np.float64(np.float32(EPS)), coefs)
+        err = np.linalg.norm(-_f64(p) - x, 2)
+        print(shape, err)
+        assert err <= ref.growth(coefs) ** 2 * (d + 10 * n) * 2.0 ** -53 + 4 * U * np.linalg.norm(x)
+
+
 def test_scratch_that_does_not_fit_is_refused_and_leaves_nothing_behind():
     """More scratch memory than the device has (450 GB): the status of a failed allocation, and the next calls,
     of the library and of others, do not find its error."""
