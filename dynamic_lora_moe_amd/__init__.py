@@ -777,7 +777,7 @@ def quantize_rows(x: torch.Tensor, q=None, scale=None, stream=None):
     T, d = x.shape
     own_q, own_s = q is None, scale is None
     q = torch.empty((T, d), dtype=torch.int8, device=x.device) if own_q else q
-    scale = torch.empty(T, device=x.device) if own_s else scale
+    scale = torch.empty(T, dtype=torch.float32, device=x.device) if own_s else scale
     _like(q, "q", (T, d), torch.int8, x.device)
     _like(scale, "scale", (T,), torch.float32, x.device)
     _fresh(stream, q if own_q else None, scale if own_s else None)
@@ -1006,8 +1006,8 @@ def adamw_read_state(m, v, m_scale, v_scale, m_out=None, v_out=None, stream=None
     _like(v_scale, "v_scale", (nb,), torch.float32, m.device)
     handle = _here(m, stream, "m")
     own_m, own_v = m_out is None, v_out is None
-    m_out = torch.empty(n, device=m.device) if own_m else m_out
-    v_out = torch.empty(n, device=m.device) if own_v else v_out
+    m_out = torch.empty(n, dtype=torch.float32, device=m.device) if own_m else m_out
+    v_out = torch.empty(n, dtype=torch.float32, device=m.device) if own_v else v_out
     _like(m_out, "m_out", (n,), torch.float32, m.device)
     _like(v_out, "v_out", (n,), torch.float32, m.device)
     _fresh(stream, m_out if own_m else None, v_out if own_v else None)
@@ -1046,7 +1046,7 @@ class Muon:
         each = lambda v: list(v) if isinstance(v, (list, tuple)) else [v] * n  # noqa: E731
         wd, scales = each(weight_decay), each(scale)
         if states is None:
-            states = [torch.zeros(p.shape, device=p.device) for p in self.params]
+            states = [torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
             if self.params[0].is_cuda:  # steps may run on any stream
                 torch.cuda.current_stream(self.params[0].device).synchronize()
         self.states = list(states)

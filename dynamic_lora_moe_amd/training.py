@@ -63,6 +63,7 @@ class AdapterTraining:
         self.projections = list(projections)
         self.x_r, self.W_r = router
         dev, T = self.x_r.device, self.x_r.shape[0]
+        f32 = dict(dtype=torch.float32, device=dev)
         self.score, self.renorm, self.bias, self.counts, self.dx_r = score, renorm, bias, counts, dx_r
         self.group = SgmmGroup(self.projections, E, r, scale)
         self.base = None
@@ -73,13 +74,13 @@ class AdapterTraining:
             self.base = Int8Group([(x, W, ws, y) for (x, _, _, y), (W, ws) in zip(self.projections, base)])
             self.base.bind_grads(dys, dxs)
             self.ws_base, self.ws_base_backward = self.base.workspace(T), self.base.backward_workspace(T)
-        self.dA = [torch.zeros(A.shape, device=dev) for _, A, _, _ in self.projections]
-        self.dB = [torch.zeros(B.shape, device=dev) for _, _, B, _ in self.projections]
-        self.dW_r = torch.zeros(self.W_r.shape, device=dev)
+        self.dA = [torch.zeros(A.shape, **f32) for _, A, _, _ in self.projections]
+        self.dB = [torch.zeros(B.shape, **f32) for _, _, B, _ in self.projections]
+        self.dW_r = torch.zeros(self.W_r.shape, **f32)
         self.group.bind_grads(dys, dxs, self.dA, self.dB)
-        self.logits = torch.empty((T, E), device=dev)
+        self.logits = torch.empty((T, E), **f32)
         self.idx = torch.empty((T, 2), dtype=torch.int32, device=dev)
-        self.g, self.dg = torch.empty((T, 2), device=dev), torch.empty((T, 2), device=dev)
+        self.g, self.dg = torch.empty((T, 2), **f32), torch.empty((T, 2), **f32)
         # status() may be asked before the first backward()
         self.ws_forward = _clean(self.group.workspace(T, dev))
         self.ws_backward = _clean(self.group.backward_workspace(T))
@@ -99,7 +100,7 @@ class AdapterTraining:
         if alpha or zeta:
             self.balance = dict(score=score, alpha=alpha, zeta=zeta, offsets=offsets)
             S = 1 if offsets is None else offsets.shape[0] - 1
-            self.loss, self.probs = torch.empty(2, device=dev), torch.empty((S, E), device=dev)
+            self.loss, self.probs = torch.empty(2, **f32), torch.empty((S, E), **f32)
             self.slots = torch.empty((S, E), dtype=torch.int32, device=dev)
             self.rows = torch.empty(S, dtype=torch.int32, device=dev)
             self.ws_balance = torch.empty(balance_workspace_size(T, E, S), dtype=torch.uint8, device=dev)

@@ -182,6 +182,31 @@ def test_update_factors(scale):
     tr.close()
 
 
+@pytest.mark.parametrize("default", [torch.float64, torch.bfloat16])
+def test_torchs_default_dtype_does_not_matter(default):
+    """What is made here for the caller (momentum, scales, gradients, losses) names its type."""
+    res = []
+    for kind in (torch.float32, default):
+        x, As, Bs, dys, W, x_r, W_r = [[u.cuda() for u in t] if isinstance(t, list) else t.cuda() for t in _setup(torch.bfloat16)]
+        dx, ys = [torch.empty_like(t) for t in x], [torch.empty_like(t) for t in dys]
+        p8, g8 = torch.ones(1000, device="cuda"), torch.linspace(-1, 1, 1000, device="cuda")
+        torch.set_default_dtype(kind)
+        try:
+            tr = AdapterTraining([(x[r], a, b, y) for r, a, b, y in zip(READS, As, Bs, ys)], (x_r, W_r), dys, [dx[r] for r in READS],
+                                 E, R, SCALE, base=[dlm.quantize_rows(w) for w in W], optimizer="muon", alpha=0.1, zeta=1e-3)
+            opt = dlm.AdamW([p8], [g8], state_bits=8)
+            tr.forward()
+            tr.backward()
+            tr.step(1e-2)
+            opt.step(1e-2)
+            m, v = opt.read_state(0)
+        finally:
+            torch.set_default_dtype(torch.float32)
+        assert tr.status() == dlm.DLM_OK
+        res.append([*tr.opt.params, *tr.opt.states, *ys, *dx, tr.loss, m, v])
+    assert all(a.dtype == b.dtype and torch.equal(a, b) for a, b in zip(*res))
+
+
 def test_refusals():
     x, As, Bs, dys, W, x_r, W_r = [[u.cuda() for u in t] if isinstance(t, list) else t.cuda() for t in _setup(torch.bfloat16)]
     proj = [(x[r], a, b, torch.empty_like(dy)) for r, a, b, dy in zip(READS, As, Bs, dys)]
