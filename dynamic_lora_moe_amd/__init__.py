@@ -854,10 +854,10 @@ class Int8Group:
 
     def bind_grads(self, dys, dxs):
         """Bind the buffers of backward(): per problem dy [T][d_out] and dx [T][d_in] (the
-        problems' dtype; a None dx, or dy with it, is not wanted).  Problems that share an
-        input share its dx, which is then their sum."""
+        problems' dtype; dxs or an entry of it may be None, with its dy: not wanted).
+        Problems that share an input share its dx, which is then their sum."""
         _here(self._keep[0][0], None, "problem 0 x")
-        dys, dxs = list(dys), list(dxs)
+        dys, dxs = list(dys), [None] * self.n if dxs is None else list(dxs)
         if not len(dys) == len(dxs) == self.n:
             raise ValueError("one dy and dx (or None) per problem")
         for k, ((x, y), dy, dx) in enumerate(zip(self._keep, dys, dxs)):

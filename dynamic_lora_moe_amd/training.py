@@ -34,10 +34,11 @@ class AdapterTraining:
     """The adapters of a list of projections that share one router.
 
     projections: [(x [T][d_in], A [E][r][d_in], B [E][d_out][r], y [T][d_out])],
-                 fixed buffers of one dtype (bf16 or fp32); A and B are trained.
+                 fixed buffers of one dtype (bf16 or fp32); A and B are trained.  Buffers
+                 may hold more rows than x_r: the others are left as they are.
     router:      (x_r [T][d], W_r [d][E]) in the same dtype; W_r is trained.
     dys / dxs:   per projection dLoss/dy (filled by the caller) and dLoss/dx (added
-                 to; None where it is not wanted).
+                 to; None, or an entry None, where it is not wanted).
     dx_r:        optional [T][d] buffer the router's share of dLoss/dx_r is added to.
     score, renorm, bias, counts: the routing, as dlm_route takes them.
     masters:     keep fp32 copies of bf16 banks and router weight; state_bits,
@@ -60,7 +61,8 @@ class AdapterTraining:
             raise ValueError(f"optimizer is 'adamw' or 'muon', got {optimizer!r}")
         if optimizer == "muon" and state_bits != 32:
             raise ValueError("muon's momentum has 32 bits")
-        self.projections = list(projections)
+        self.projections, dys = list(projections), list(dys)
+        dxs = None if dxs is None else list(dxs)
         self.x_r, self.W_r = router
         dev, T = self.x_r.device, self.x_r.shape[0]
         f32 = dict(dtype=torch.float32, device=dev)
@@ -114,7 +116,7 @@ class AdapterTraining:
             balance(self.logits, self.idx, loss=self.loss, counts=self.slots, rows=self.rows, probs=self.probs,
                     workspace=self.ws_balance, **self.balance)
         if self.base:
-            self.base.run(workspace=self.ws_base)
+            self.base.run(T=self.x_r.shape[0], workspace=self.ws_base)
         self.group.run(self.idx, self.g, workspace=self.ws_forward)
         return self.idx, self.g
 
@@ -122,7 +124,7 @@ class AdapterTraining:
         """Gradients of the last forward() from the dys: dxs (with a base, written) and
         dx_r added to, dA, dB and dW_r written."""
         if self.base:
-            self.base.backward(workspace=self.ws_base_backward)
+            self.base.backward(T=self.x_r.shape[0], workspace=self.ws_base_backward)
         self.group.backward(self.idx, self.g, self.dg, workspace=self.ws_backward)
         dl = route_backward(self.logits, self.idx, self.dg, score=self.score, renorm=self.renorm)
         if self.balance:

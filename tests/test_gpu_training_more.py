@@ -207,6 +207,31 @@ def test_torchs_default_dtype_does_not_matter(default):
     assert all(a.dtype == b.dtype and torch.equal(a, b) for a, b in zip(*res))
 
 
+@pytest.mark.parametrize("grads", ["none", "some", "all"])
+def test_a_base_with_longer_buffers_and_unwanted_gradients(grads):
+    """Buffers that hold more rows than the batch (x_r's), dys from an iterator, and dxs that are not wanted: the
+    same rows as from buffers of the batch's size, and nothing behind them."""
+    more, res = 13, []
+    for extra in (0, more):
+        x, As, Bs, dys, W, x_r, W_r = [[u.cuda() for u in t] if isinstance(t, list) else t.cuda() for t in _setup(torch.bfloat16)]
+        longer = lambda t: torch.cat([t, torch.full((extra, t.shape[1]), 2.0, dtype=t.dtype, device="cuda")])  # noqa: E731
+        x, dys = [longer(t) for t in x], [longer(t) for t in dys]
+        ys, dx = [torch.full_like(t, 3.0) for t in dys], [torch.full_like(t, 3.0) for t in x]
+        dxs = None if grads == "none" else [dx[r] if grads == "all" or r == 1 else None for r in READS]
+        tr = AdapterTraining([(x[r], a, b, y) for r, a, b, y in zip(READS, As, Bs, ys)], (x_r, W_r), iter(dys),
+                             dxs if dxs is None else iter(dxs), E, R, SCALE, base=[dlm.quantize_rows(w) for w in W])
+        tr.forward()
+        tr.backward()
+        tr.step(1e-2)
+        assert tr.status() == dlm.DLM_OK
+        for t in ys + dx:
+            assert (t[T:] == 3).all()
+        for r in (0, 1):
+            assert bool((dx[r] == 3).all()) == (grads == "none" or (grads == "some" and r == 0))
+        res.append([*tr.opt.params, *tr.opt.grads, *(t[:T].clone() for t in ys + dx)])
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
 def test_refusals():
     x, As, Bs, dys, W, x_r, W_r = [[u.cuda() for u in t] if isinstance(t, list) else t.cuda() for t in _setup(torch.bfloat16)]
     proj = [(x[r], a, b, torch.empty_like(dy)) for r, a, b, dy in zip(READS, As, Bs, dys)]
