@@ -24,8 +24,8 @@
 // Small sides from 65 to 512 (routers of many experts): the same with 64 x 64 tiles, u
 // in scratch memory, and a launch per n x n product.
 //
-// A matrix whose u is not finite is left as it was, momentum too, and the handle's
-// error word is set.
+// A matrix whose u is not finite, or whose X would leave fp32's range, is left as it was,
+// momentum too, and the handle's error word is set.
 //
 // Measured: 322 million bf16 weights at rank 16, fp32 gradients and masters, 1.74 ms: the
 // Gram pass 0.47, the steps 0.025, the update 1.24; both passes move 5.5 TB/s (with u read
@@ -343,6 +343,10 @@ template <int NB, typename G> __global__ __launch_bounds__(kNT, NB == 4 ? 2 : 1)
     gram_item<NB, G>(a, blockIdx.x, s_all);
 }
 
+// Whether the products P u of an entry of P, with its 1 / norm, and of others like it stay within
+// fp32: |X| is at most n max|P| |u|, and |u| 1 / norm at most 1.  (False for NaN.)
+__device__ __forceinline__ bool in_range(double p, int n, double inv) { return fabs(p) * n <= 3.402823466e38 * inv; }
+
 // ---- the n x n steps ----------------------------------------------------------------------
 
 // Of block (bi, bj), element (row, col) as register v of lane l: (4 v + l / 16, l % 16).
@@ -445,7 +449,7 @@ template <int NB, int WAVES = NB * (NB + 1) / 2> __device__ __forceinline__ void
         double* out = a.pm + mat * SQ;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            fin = fin && __builtin_isfinite(p[v]);
+            fin = fin && in_range(p[v], 16 * NB, inv);
             gst(out + (bi * NB + bj) * 256 + 64 * v + lane, p[v]);
             if (bi != bj) gst(out + (bj * NB + bi) * 256 + mirrored(v, lane), p[v]);
         }
@@ -758,7 +762,7 @@ template <int MODE> __global__ __launch_bounds__(kNT) void muon_big_mul(MuonArgs
         for (int v = 0; v < 4; ++v) {
             const double q = (bi == bj && on_diagonal(v, lane) ? ca : 0.0) + cb * frag(M.G, bi, bj, v) + cc * frag(M.S, bi, bj, v);
             gst(out + 64 * v + lane, inv * q);
-            if (a.steps == 1 && !__builtin_isfinite(inv * q)) {
+            if (a.steps == 1 && !in_range(inv * q, 16 * nb, inv)) {
                 gst(a.bad + bigi, 1);
                 gst(a.err, 1);
             }
@@ -803,7 +807,7 @@ template <int MODE> __global__ __launch_bounds__(kNT) void muon_big_mul(MuonArgs
     for (int k = 1; k < kWaves; ++k) s += s_sum[k][threadIdx.x];
     // (R and S keep the stored G's scale; G' takes it from R)
     gst(out + threadIdx.x, MODE == MUL_G ? s * f : s);
-    if (MODE == MUL_RP && step + 1 == a.steps && !__builtin_isfinite(s)) {
+    if (MODE == MUL_RP && step + 1 == a.steps && !in_range(s, 16 * nb, gld(a.meta + 2 * bigi))) {
         gst(a.bad + bigi, 1);
         gst(a.err, 1);
     }

@@ -748,8 +748,8 @@ int dlm_muon_destroy(dlm_muon* h);
  * Coefficients with |a| above 1 raise weak directions, and the rounding of A in them, by
  * a^2 a step: with five steps of (3.4445, -4.775, 2.0315) X is off by less than its own
  * rounding, with ten by 1e-4 in directions below 1e-5 of the strongest.
- * A matrix whose u, or whose iterated factor, is not finite is left unchanged, momentum
- * too, and the error word is set.  Bitwise reproducible.
+ * A matrix whose u is not finite, or whose X coefficients drive out of fp32's range, is left
+ * unchanged, momentum too, and the error word is set.  Bitwise reproducible.
  * Launches: three for the matrices with a smaller side up to 16, three up to 32, three
  * up to 64 (three for all of these where they are few), and 3 + 3 steps for those above.
  */

@@ -375,6 +375,31 @@ def test_classes_in_joint_launches(shapes):
     assert not torch.equal(sides[0][0][0].cpu(), _rnd(shapes[0], 0, 0.02)[0])
 
 
+@pytest.mark.parametrize("shapes", [[(2, 16, 100)], [(2, 100, 30)], [(2, 60, 70)], [(2, 70, 90)], [(2, 16, 100), (2, 100, 30)],
+                                    [(2, 16, 100), (2, 100, 60)]])
+@pytest.mark.parametrize("steps", [1, 3])
+def test_products_past_fp32(shapes, steps):
+    """Coefficients whose products leave fp32's range leave the matrices, and set the error; up to 10^30 they do not."""
+    for big in (False, True):
+        a = (10.0 ** (60 if big else 30)) ** (1 / steps)
+        ps = [_rnd(s, k, 0.02).cuda() for k, s in enumerate(shapes)]
+        gs = [_rnd(s, 9 + k, 1e-3).cuda() for k, s in enumerate(shapes)]
+        ms = [_rnd(s, 20 + k, 1e-3).cuda() for k, s in enumerate(shapes)]
+        old = [t.clone() for t in ps + ms]
+        opt = dlm.Muon(ps, gs, states=ms, steps=steps, coefs=(a, 0.0, 0.0), scale=1.0)
+        opt.step(1e-30)
+        assert opt.status() == (dlm.DLM_EDEVICE if big else dlm.DLM_OK)
+        if big:
+            assert all(torch.equal(x, y) for x, y in zip(old, ps + ms))
+            continue
+        for p, m, w in zip(ps, ms, old):
+            u = BETA * m.double() + 0.05 * gs[[q is p for q in ps].index(True)].double()
+            x = u / (u.flatten(1).norm(dim=1)[:, None, None] + EPS)
+            # a's and the rate's roundings beside the product's
+            ok = (p.double() - (w.double() - x)).abs() <= 16 * U * (w.double().abs() + x.abs()) + 1e-8 * x.abs().max()
+            assert bool(ok.all())
+
+
 def test_refusals_of_the_binding(monkeypatch):
     p, g = torch.zeros((4, 10), device="cuda"), torch.zeros((4, 10), device="cuda")
     for make in (lambda: dlm.Muon([], []), lambda: dlm.Muon([p], [g[:3]]), lambda: dlm.Muon([p], [g.cpu()]),
