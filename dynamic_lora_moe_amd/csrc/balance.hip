@@ -17,10 +17,10 @@
 // (One block of one sequence needs no second launch.)
 //
 // 16384 rows of 256 fp32 logits, sigmoid, 8 sequences: 14 us, 9 and 15 for the gradient that
-// joins one that is there (3.4 TB/s; the forward's 1.2 are its wait for a block's few rows,
-// the exponentials, and the rows' sums across waves).  256 rows of 8: 5.5 and 2.8, a launch
-// and a chain of loads each.  512 blocks at most: the second launch reads every block's part,
-// and more of them cost it what the first gains.
+// joins one that is there (3.4 TB/s; the forward's 1.2 are its waits: two waves a SIMD, whose
+// next row is loaded once this one's sums are done, and a slot's logit once its idx is there).
+// 256 rows of 8: 5.4 and 2.8, a launch and a chain of loads each.  512 blocks at most: the
+// second launch reads every block's part, and more of them cost it what the first gains.
 #include "balance.hpp"
 #include "gfx950.hpp"
 #include "internal.hpp"

@@ -6,7 +6,10 @@
 //
 // The rounding is decided on the exact quotient: x 127 / max is one binary64 fma onto
 // 1.5 * 2^52, whose low byte is the code (127 / max is taken a hair low, 2^-51, so that
-// the only exact halves, which binary64 could put on either side, go one way).
+// the only exact halves, which binary64 could put on either side, go one way).  A quotient of
+// 24-bit numbers that is no half is farther than that from one.  The gradient's dy w_scale
+// have up to 48 bits (32 where dy is bf16): of fp32 dy a quotient can lie closer to a half,
+// and its code then be one off.
 //
 // The input gradient is the same product: codes of dy w_scale, whose runs from all the
 // products of one input stand side by side in one row with one scale, against the
@@ -17,10 +20,12 @@
 // registers or LDS, and reads it from there without bank conflicts.  W is the first
 // operand, so a lane's four results are neighbouring columns of out.
 //
-// A 7B-shaped layer's seven products, bf16: one row 5.4 us for the codes and 30 for the
+// A 7B-shaped layer's seven products, bf16: one row 5.5 us for the codes and 30 for the
 // products (6.7 TB/s, the rate at which memory is read), 64 rows 8.5 and 46, 4096 rows 88
-// and 690 (2400 TOP/s; a loop of these instructions in registers reaches 4040 on such
-// operands, 4880 on zeros: the card's power holds it), and the gradient 200 and 640.
+// and 690-730 (2300-2400 TOP/s), and the gradient 195 and 630-645.  The matrix cores are busy
+// 54 % of those cycles (61 % in the gradient) at a clock of about 2.0 GHz; a loop of these
+// instructions in registers reaches 4010 TOP/s on such operands, 4870 on zeros: it is the
+// operands' switching that costs the rest of the clock.
 #include "gfx950.hpp"
 #include "int8.hpp"
 #include "internal.hpp"

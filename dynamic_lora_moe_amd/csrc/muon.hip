@@ -27,12 +27,15 @@
 // A matrix whose u is not finite, or whose X would leave fp32's range, is left as it was,
 // momentum too, and the handle's error word is set.
 //
-// Measured: 322 million bf16 weights at rank 16, fp32 gradients and masters, 1.74 ms: the
-// Gram pass 0.47, the steps 0.025, the update 1.24; both passes move 5.5 TB/s (with u read
-// twice that is 4.05 TB/s of the bytes that a step cannot do without).  10 million: 19, 8 and
-// 45 us.  Rank 64, 16.8 million: 53, 42 and 87 us, where neither memory nor the products
-// are busy: two waves a SIMD (a tile's 64 values of u and its products' operands), each in
-// a chain of loads, products and stores.  8192 x 256: 136 us in 20 launches.
+// Measured: 322 million bf16 weights at rank 16, fp32 gradients and masters, 1.6 to 1.74 ms:
+// the Gram pass 0.44-0.47, the steps 0.026, the update 1.12-1.21; both passes move 5.6 to 6
+// TB/s (with u read twice that is 4.05 to 4.4 TB/s of the bytes that a step cannot do
+// without).  10 million: 18, 8 and 42-45 us.  Rank 64, 16.8 million: 53, 42 and 87 us, where
+// neither memory (2.9 and 4.6 TB/s) nor the matrix cores (12 and 29 % of the cycles) are
+// busy: two waves a SIMD, each in a chain of loads, products and stores, and a 64 x 64 tile's
+// u and m beside its products' operands do not fit their registers: 29 are spilled in the
+// Gram kernel, 28 or 38 (bf16 or fp32 gradients) in the update.  8192 x 256: 145 to 160 us
+// in 18 launches.
 #include <utility>
 
 #include "gfx950.hpp"

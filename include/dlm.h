@@ -592,8 +592,9 @@ int dlm_i8_group_destroy(dlm_i8_group* h);
  * factors are applied in fp32, w_scale's first.  A row of x that is not finite gives NaN in
  * its row of y, and nothing else.  Two launches (the codes, once for problems that share an x; the
  * products), no allocation; one for up to four rows whose codes fit a workgroup's LDS (four
- * of 11008 columns do).  Up to 64 rows the weights are read once, straight into the
- * products' operands.  T = 0 enqueues nothing.
+ * of 11008 columns do), while 1, 2 or 4 (the rows, 4 for three) times the 16-channel tiles
+ * of all products are at most 2048.  Up to 64 rows the weights are read once, straight into
+ * the products' operands.  T = 0 enqueues nothing.
  * workspace: >= dlm_i8_group_workspace_size(h, T) bytes, 256-byte aligned, of any content.
  */
 int dlm_i8_group_workspace_size(const dlm_i8_group* h, int64_t T, size_t* bytes);
@@ -606,7 +607,8 @@ int dlm_i8_group_run(dlm_i8_group* h, int64_t T, void* workspace, size_t ws_byte
  *   dx_i [T][d_in_i]; NULL entries of dx (and their dy) are not wanted.  Problems of one
  *   d_in may share a dx (at most 131072 output channels, each problem's counted as a
  *   multiple of 64): their products dy_i[t][o] w_scale_i[o], side by side, are one row of
- *   codes with one scale, formed from the exact products.
+ *   codes with one scale, formed from the exact products (of fp32 dy a code can be one off
+ *   where its quotient lies within 2^-50 of a half of it).
  * The handle allocates the weights' transposes (the weights' size).  Synchronises the
  * device.  Binding again replaces the buffers (calls captured into graphs before then read
  * freed tables: capture them again).
@@ -730,6 +732,12 @@ typedef struct dlm_muon dlm_muon;
  * most 2^30, and a tensor has at most 2^40 elements.  Any sizes and
  * alignments of their element (cols a multiple of 4 and tensors aligned to four
  * elements are faster).
+ * The scratch memory, for all tensors at once, by a matrix's smaller side n and longer
+ * side d: n up to 16, 32 and 64: 2, 6 and 20 KB for every 512 of d (every 256 where n is
+ * above 16 and pieces are few), and 2, 8 and 32 KB; above, with N = n rounded up to a
+ * multiple of 64: 4 bytes an element (u), (N / 64 + 1) N bytes for each of d rounded up to
+ * a multiple of 256, and 48 N^2 bytes.  A weight of rank 16 so takes 1/4 byte, of rank 128
+ * 7, of rank 512 13.
  */
 int dlm_muon_create(const dlm_muon_param* params, int32_t n, int32_t p_dtype, int32_t g_dtype, dlm_muon** out);
 
